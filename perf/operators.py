@@ -235,7 +235,7 @@ def _own_attend(st):
     c = st["c"]
     ws = st.get("workspace")
     if ws is None:  # kept by the caller from step to step, zeroed once
-        ws = st["workspace"] = qdq.kv_attention_workspace(c["seqs"], c["seqs"] * c["queries"], c["queries"], c["hi"],
+        ws = st["workspace"] = qdq.kv_attention_workspace(c["seqs"], c["queries"], c["hi"],
                                                           c["heads"], c["kv_heads"], c["dim"])
     qdq.kv_attention(st["pages"], st["table"], st["kv_len"], st["q"], st["out"], ws, n_heads=c["heads"],
                      n_kv=c["kv_heads"], head_dim=c["dim"], page_tokens=c["page"], max_kv_len=c["hi"],
