@@ -27,6 +27,11 @@ QDQ_NOALLOC_FFN_MAX_MID = 262144
 QDQ_MAX_GEMV_BATCH = 8
 QDQ_MAX_TOPK = 64
 QDQ_MAX_GEMV_N_IN = 32768
+QDQ_MAX_NORM_N = 32768
+QDQ_KV_BLOCK = 16
+QDQ_TYPE_F32 = 0
+QDQ_TYPE_F16 = 1
+QDQ_TYPE_BF16 = 2
 QDQ_OPT_PDL = 1
 QDQ_OPT_L2_PREFETCH = 2
 QDQ_OPT_CTAS_PER_SM = 3
@@ -36,6 +41,7 @@ QDQ_OPT_XS_FLOAT_X = 6
 QDQ_OPT_BATCH1_KERNEL = 7
 
 _c_int, _c_size, _c_vp, _c_char_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
+_c_ll, _c_float = ctypes.c_longlong, ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/qdq.h
 SIGNATURES = {
@@ -72,6 +78,18 @@ SIGNATURES = {
     "qdq_q4k_gemm_batch": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_vp]),
     "qdq_q4k_swiglu_batch_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "qdq_q4k_swiglu_batch": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_vp]),
+    "qdq_rms_norm": (_c_int, [_c_vp] * 6 + [_c_int] * 3 + [_c_ll] * 4 + [_c_float, _c_vp]),
+    "qdq_kv_page_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "qdq_kv_append": (_c_int, [_c_vp] + [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_ll,
+                               _c_ll, _c_int, _c_vp]),
+    "qdq_kv_read": (_c_int, [_c_vp] + [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_ll,
+                             _c_ll, _c_int, _c_vp]),
+    "qdq_kv_attention_workspace_bytes": (_c_size, [_c_int] * 6),
+    "qdq_kv_attention": (_c_int, [_c_vp] + [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_vp] + [_c_int] * 4
+                         + [_c_vp, _c_ll, _c_vp, _c_ll, _c_vp, _c_vp, _c_float, _c_float, _c_int, _c_int, _c_vp, _c_size,
+                            _c_vp]),
+    "qdq_token_logprobs_workspace_bytes": (_c_size, [_c_int] * 3),
+    "qdq_token_logprobs": (_c_int, [_c_vp, _c_ll, _c_int, _c_vp, _c_int, _c_int, _c_int] + [_c_vp] * 5 + [_c_size, _c_vp]),
     "qdq_pipeline_timeouts": (_c_int, []),
     "qdq_noop": (_c_int, [_c_vp]),
     "qdq_check_status": (_c_int, []),
@@ -286,6 +304,162 @@ def set_option(key: int, value: int) -> int:
     if r < 0:
         raise QdqError("qdq_set_option", r)
     return r
+
+
+# ---------------------------------------------------------------- decode-step operators
+# (the element type and the row strides come from the tensors, whose first dimension is the rows)
+
+_TYPES = {"torch.float32": QDQ_TYPE_F32, "torch.float16": QDQ_TYPE_F16, "torch.bfloat16": QDQ_TYPE_BF16}
+_types = {}
+
+
+def _type(t) -> int:
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        v = _TYPES.get(str(t.dtype))
+        if v is None:
+            raise TypeError("float32, float16 or bfloat16 expected, got %s" % t.dtype) from None
+        _types[t.dtype] = v
+        return v
+
+
+def _same_type(name, t, *others):
+    for o in others:
+        if o is not None and o.dtype != t.dtype:
+            raise TypeError("%s: %s and %s do not have one element type" % (name, t.dtype, o.dtype))
+
+
+def _int32(name, *tensors):
+    for t in tensors:
+        if t is not None and (str(t.dtype) != "torch.int32" or not t.is_contiguous()):
+            raise TypeError("%s: contiguous int32 tensors expected" % name)
+
+
+def _f32(name, *tensors):
+    for t in tensors:
+        if t is not None and (str(t.dtype) != "torch.float32" or not t.is_contiguous()):
+            raise TypeError("%s: contiguous float32 tensors expected" % name)
+
+
+def _rows(name, t, width):
+    """Row stride of a tensor of rows: the first dimension, the others hold ``width`` packed elements (one dimension: one row)."""
+    if t is None:
+        return 0
+    shape, st = t.shape, t.stride()
+    if len(shape) == 1:
+        shape, st = (1, *shape), (width, *st)
+    w = 1
+    for d in range(len(shape) - 1, 0, -1):
+        if shape[d] != 1 and st[d] != w:
+            raise ValueError("%s: the elements of a row must be packed" % name)
+        w *= shape[d]
+    if w != width:
+        raise ValueError("%s: rows of %d elements expected, got shape %s" % (name, width, tuple(t.shape)))
+    return st[0] if shape[0] > 1 else width
+
+
+def rms_norm(x, weight, out, rows: int, n: int, eps: float = 1e-5, residual=None, sum_out=None, q8_out=None, stream=None):
+    """RMS norm of ``x + residual`` per row into ``out`` (x's type) and / or ``q8_out`` (a packed Q8_0 matrix).
+
+    ``sum_out`` receives ``x + residual``; it may be ``residual`` or ``x`` itself, and ``out`` may be ``x``."""
+    f = lib().qdq_rms_norm
+    _same_type("rms_norm", x, residual, sum_out, out)
+    _f32("rms_norm", weight)
+    _check("qdq_rms_norm", f(_ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(out), _ptr(q8_out), _type(x), rows, n,
+                             _rows("x", x, n), _rows("residual", residual, n), _rows("sum_out", sum_out, n),
+                             _rows("out", out, n), eps, _stream(stream)))
+
+
+def kv_page_bytes(page_tokens: int, n_kv: int, head_dim: int) -> int:
+    return int(lib().qdq_kv_page_bytes(page_tokens, n_kv, head_dim))
+
+
+def kv_pages(n_pages: int, page_tokens: int, n_kv: int, head_dim: int, device="cuda"):
+    """A pool of cache pages, zeroed: a uint8 tensor ``n_pages x kv_page_bytes``."""
+    import torch
+    b = kv_page_bytes(page_tokens, n_kv, head_dim)
+    if b == 0:
+        raise QdqError("qdq_kv_page_bytes", QDQ_ERR_UNSUPPORTED)
+    return torch.zeros(n_pages, b, dtype=torch.uint8, device=device)
+
+
+def _pool(name, pages, page_table, page_tokens, n_kv, head_dim):
+    b = lib().qdq_kv_page_bytes(page_tokens, n_kv, head_dim)
+    if not pages.is_contiguous() or (b and pages.numel() * pages.element_size() % b):
+        raise ValueError("%s: pages is not a whole number of packed pages" % name)
+    _int32(name, page_table)
+    return pages.numel() * pages.element_size() // b if b else 1
+
+
+def kv_append(pages, page_table, kv_len, k, v, n_kv: int, head_dim: int, page_tokens: int, cu_new=None, max_new: int = 1,
+              stream=None):
+    """Quantise new tokens (rows of ``k`` and ``v``) into the cache: the last tokens of each sequence's ``kv_len``."""
+    n = _pool("kv_append", pages, page_table, page_tokens, n_kv, head_dim)
+    _int32("kv_append", kv_len, cu_new)
+    _same_type("kv_append", k, v)
+    w = n_kv * head_dim
+    _check("qdq_kv_append", lib().qdq_kv_append(
+        _ptr(pages), n, page_tokens, n_kv, head_dim, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(cu_new),
+        page_table.shape[0], max_new, _ptr(k), _ptr(v), _rows("k", k, w), _rows("v", v, w), _type(k), _stream(stream)))
+
+
+def kv_read(pages, page_table, start, cu, k, v, n_kv: int, head_dim: int, page_tokens: int, max_tokens: int, stream=None):
+    """Write the values of cached tokens (``cu[s+1] - cu[s]`` of sequence s from ``start[s]``) to rows of ``k`` and ``v``."""
+    n = _pool("kv_read", pages, page_table, page_tokens, n_kv, head_dim)
+    _int32("kv_read", start, cu)
+    _same_type("kv_read", k, v)
+    w = n_kv * head_dim
+    _check("qdq_kv_read", lib().qdq_kv_read(
+        _ptr(pages), n, page_tokens, n_kv, head_dim, _ptr(page_table), page_table.shape[1], _ptr(start), _ptr(cu),
+        page_table.shape[0], max_tokens, _ptr(k), _ptr(v), _rows("k", k, w), _rows("v", v, w), _type(k), _stream(stream)))
+
+
+def kv_attention_workspace_bytes(n_seqs: int, max_q: int, max_kv_len: int, n_heads: int, n_kv: int, head_dim: int) -> int:
+    return int(lib().qdq_kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim))
+
+
+def kv_attention_workspace(n_seqs: int, max_q: int, max_kv_len: int, n_heads: int, n_kv: int, head_dim: int, device="cuda"):
+    """A zeroed workspace of :func:`kv_attention`; calls on one stream may share it."""
+    import torch
+    return torch.zeros(kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def kv_attention(pages, page_table, kv_len, q, out, workspace, n_heads: int, n_kv: int, head_dim: int, page_tokens: int,
+                 max_kv_len: int, cu_q=None, max_q: int = 1, scale: float | None = None, softcap: float = 0.0,
+                 window: int = 0, slopes=None, lse=None, stream=None):
+    """Attention of the rows of ``q`` over the cached tokens into ``out`` (``scale`` defaults to head_dim ** -0.5)."""
+    n = _pool("kv_attention", pages, page_table, page_tokens, n_kv, head_dim)
+    _int32("kv_attention", kv_len, cu_q)
+    _f32("kv_attention", slopes, lse)
+    _same_type("kv_attention", q, out)
+    w = n_heads * head_dim
+    _check("qdq_kv_attention", lib().qdq_kv_attention(
+        _ptr(pages), n, page_tokens, n_kv, head_dim, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(cu_q),
+        page_table.shape[0], max_q, max_kv_len, n_heads, _ptr(q), _rows("q", q, w), _ptr(out), _rows("out", out, w), _ptr(lse),
+        _ptr(slopes), head_dim ** -0.5 if scale is None else scale, softcap, window, _type(q), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def token_logprobs_workspace_bytes(rows: int, n: int, k: int) -> int:
+    return int(lib().qdq_token_logprobs_workspace_bytes(rows, n, k))
+
+
+def token_logprobs_workspace(rows: int, n: int, k: int, device="cuda"):
+    """A zeroed workspace of :func:`token_logprobs`; calls on one stream may share it."""
+    import torch
+    return torch.zeros(token_logprobs_workspace_bytes(rows, n, k), dtype=torch.uint8, device=device)
+
+
+def token_logprobs(logits, tokens, logprob, entropy, rows: int, n: int, workspace, k: int = 0, top_index=None,
+                   top_logprob=None, stream=None):
+    """Per row: the log probability of ``tokens[r]``, the entropy, and the k best (index, log probability) pairs."""
+    _int32("token_logprobs", tokens, top_index)
+    _f32("token_logprobs", logprob, entropy, top_logprob)
+    _check("qdq_token_logprobs", lib().qdq_token_logprobs(
+        _ptr(logits), _rows("logits", logits, n), _type(logits), _ptr(tokens), rows, n, k, _ptr(logprob), _ptr(entropy),
+        _ptr(top_index), _ptr(top_logprob), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- upload helpers

@@ -1,0 +1,201 @@
+// The paged 8-bit key/value cache: appending tokens (quantisation) and reading tokens back.
+//
+// A block is 16 consecutive tokens of one sequence and head; its keys share one f32 scale and
+// its values another:
+//   s = max(s_old, max |x| / 127)  over the new tokens x of the block (s_old: its scale before,
+//       0 when it held no token; a scale below the smallest normal f32 counts as 0),
+//   code = rint(x * (1 / s)) for new tokens,  rint(code * (s_old / s)) for those it held,
+// every quotient, product and maximum in f32.  So a scale never shrinks while a block fills,
+// and appending the same tokens twice changes nothing.  A new token that is not finite makes
+// the block's scale NaN, and with it every value of the block.
+//
+// One warp per (sequence, block, head, keys or values): the block's new elements stay in
+// registers between the maximum and the rounding, so each is read once.
+#include "qdq_types.cuh"
+
+namespace qdq {
+namespace {
+
+constexpr int kWarps = 4;
+
+struct AppendArgs {
+  KvPool c;
+  const int *kv_len, *cu;  // tokens after the append; new tokens before each sequence (NULL: one each)
+  const void *k, *v;
+  int64_t k_stride, v_stride;
+  int n_seqs, n_blocks;  // blocks per sequence that the grid covers
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const AppendArgs a) {
+  constexpr int C = D / 8;       // 4-element chunks per lane: 16 * D / 4 chunks over 32 lanes
+  constexpr int PT = D / 4;      // chunks per token
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int hw = int(unit % (2 * a.c.n_kv));
+  const int64_t sb = unit / (2 * a.c.n_kv);
+  const int s = int(sb / a.n_blocks), b = int(sb % a.n_blocks);
+  if (s >= a.n_seqs) return;
+  const int h = hw >> 1, which = hw & 1;
+  const int first = a.cu ? int(ld_u1(a.cu + s)) : s;
+  const int n_new = a.cu ? int(ld_u1(a.cu + s + 1)) - first : 1;
+  const int len = int(ld_u1(a.kv_len + s));
+  const int old = len - n_new;
+  if (n_new <= 0 || old < 0) return;
+  const int blk = old / kKvBlock + b;
+  const int p0 = blk * kKvBlock;
+  if (p0 >= len) return;
+  const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
+  const int64_t at = kv_record_of(a.c, s, blk, h, rec);
+  if (at < 0) return;  // no page for these tokens: they are dropped
+  const int t0 = p0 % a.c.page_tokens;
+  int8_t *codes = reinterpret_cast<int8_t *>(a.c.pages + at) + (int64_t(which) * a.c.page_tokens + t0) * D;
+  float *scale = reinterpret_cast<float *>(a.c.pages + at + int64_t(2) * a.c.page_tokens * D) +
+                 which * (a.c.page_tokens / kKvBlock) + t0 / kKvBlock;
+  const int held = old > p0 ? old - p0 : 0;                       // tokens the block held
+  const int end = len - p0 < kKvBlock ? len - p0 : kKvBlock;  // tokens it holds now
+  const T *x = static_cast<const T *>(which ? a.v : a.k) + int64_t(h) * D;
+  const int64_t stride = which ? a.v_stride : a.k_stride;
+  const int64_t x0 = int64_t(first) + p0 - old;  // row of the block's token 0 (negative part never read)
+
+  float4 v[C];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int ch = lane + 32 * i, t = ch / PT;
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t >= held && t < end) v[i] = load4(x + (x0 + t) * stride + 4 * (ch % PT));
+  }
+  float s_old = held ? __uint_as_float(ld_u1(scale)) : 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) m = max_abs_bits(max_abs_bits(m, max_abs_bits(v[i].x, v[i].y)), max_abs_bits(v[i].z, v[i].w));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s_new = __fdiv_rn(m, 127.f);
+  if (s_new < 1.17549435e-38f) s_new = 0.f;
+  if (!(m < __int_as_float(0x7f800000))) s_new = __int_as_float(0x7fffffff);
+  const float sc = max_abs_bits(s_old, s_new);  // NaN wins
+  const float inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
+  if (held && sc != s_old) {  // a larger scale: what the block held, rounded to it
+    const float again = sc > 0.f ? __fdiv_rn(s_old, sc) : 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int ch = lane + 32 * i, t = ch / PT;
+      if (t < held) {
+        uint32_t *p = reinterpret_cast<uint32_t *>(codes + int64_t(t) * D + 4 * (ch % PT));
+        const uint32_t w = ld_u1(p);
+        uint32_t r = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          r |= uint32_t(__float2int_rn(float(int8_t(w >> (8 * j))) * again) & 0xFF) << (8 * j);
+        *p = r;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int ch = lane + 32 * i, t = ch / PT;
+    if (t >= held && t < end) {
+      auto code = [&](float f) { return uint32_t(__float2int_rn(fminf(fmaxf(f * inv, -127.f), 127.f)) & 0xFF); };
+      *reinterpret_cast<uint32_t *>(codes + int64_t(t) * D + 4 * (ch % PT)) =
+          code(v[i].x) | (code(v[i].y) << 8) | (code(v[i].z) << 16) | (code(v[i].w) << 24);
+    }
+  }
+  if (lane == 0 && (held == 0 || sc != s_old)) *scale = sc;
+}
+
+struct ReadArgs {
+  KvPool c;
+  const int *start, *cu;  // first token of each sequence's range (NULL: 0); range sizes, summed
+  void *k, *v;
+  int64_t k_stride, v_stride;
+  int n_seqs, n_blocks;
+};
+
+// One warp per (sequence, block, head, keys or values), as above; a token without a valid page
+// reads as NaN.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) {
+  constexpr int C = D / 8, PT = D / 4;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int hw = int(unit % (2 * a.c.n_kv));
+  const int64_t sb = unit / (2 * a.c.n_kv);
+  const int s = int(sb / a.n_blocks), b = int(sb % a.n_blocks);
+  if (s >= a.n_seqs) return;
+  const int h = hw >> 1, which = hw & 1;
+  const int row0 = int(ld_u1(a.cu + s)), n = int(ld_u1(a.cu + s + 1)) - row0;
+  const int start = a.start ? int(ld_u1(a.start + s)) : 0;
+  if (n <= 0 || start < 0) return;
+  const int blk = start / kKvBlock + b, p0 = blk * kKvBlock;
+  if (int64_t(p0) >= int64_t(start) + n) return;
+  const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
+  const int64_t at = kv_record_of(a.c, s, blk, h, rec);
+  const int t0 = p0 % a.c.page_tokens;
+  const int64_t off = at < 0 ? 0 : at;
+  const uint8_t *codes = a.c.pages + off + (int64_t(which) * a.c.page_tokens + t0) * D;
+  const float *scale = reinterpret_cast<const float *>(a.c.pages + off + int64_t(2) * a.c.page_tokens * D) +
+                       which * (a.c.page_tokens / kKvBlock) + t0 / kKvBlock;
+  const float sc = at < 0 ? __int_as_float(0x7fffffff) : __uint_as_float(ld_u1(scale));
+  T *o = static_cast<T *>(which ? a.v : a.k) + int64_t(h) * D;
+  const int64_t stride = which ? a.v_stride : a.k_stride;
+#pragma unroll 8
+  for (int i = 0; i < C; ++i) {
+    const int ch = lane + 32 * i, t = ch / PT;
+    const int64_t r = int64_t(p0) + t - start;
+    if (r >= 0 && r < n) {
+      const uint32_t w = at < 0 ? 0u : ld_u1(codes + int64_t(t) * D + 4 * (ch % PT));
+      store4(o + (row0 + r) * stride + 4 * (ch % PT),
+             make_float4(float(int8_t(w)) * sc, float(int8_t(w >> 8)) * sc, float(int8_t(w >> 16)) * sc,
+                         float(int8_t(w >> 24)) * sc));
+    }
+  }
+}
+
+template <typename F>
+int with_dim(int d, F &&f) {
+  switch (d) {
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 96: return f(std::integral_constant<int, 96>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 192: return f(std::integral_constant<int, 192>{});
+    default: return f(std::integral_constant<int, 256>{});
+  }
+}
+
+// Blocks of 16 that n consecutive tokens can touch.
+int blocks_touched(int n) { return n / kKvBlock + (n % kKvBlock > 1 ? 2 : 1); }
+
+}  // namespace
+
+int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int *cu, int n_seqs, int max_new,
+                     const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s) {
+  const AppendArgs a{c, kv_len, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_new)};
+  const int64_t units = int64_t(n_seqs) * a.n_blocks * 2 * c.n_kv, grid = (units + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
+  const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
+    return with_dim(head_dim, [&](auto d) {
+      return int(launch(kv_append_kernel<decltype(t), decltype(d)::value>, dim3(unsigned(grid)), dim3(kWarps * 32), 0, s, a));
+    });
+  }));
+  return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
+}
+
+int launch_kv_read(const KvPool &c, int head_dim, const int *start, const int *cu, int n_seqs, int max_tokens, void *k,
+                   void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s) {
+  const ReadArgs a{c, start, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_tokens)};
+  const int64_t units = int64_t(n_seqs) * a.n_blocks * 2 * c.n_kv, grid = (units + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
+  const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
+    return with_dim(head_dim, [&](auto d) {
+      return int(launch(kv_read_kernel<decltype(t), decltype(d)::value>, dim3(unsigned(grid)), dim3(kWarps * 32), 0, s, a));
+    });
+  }));
+  return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
+}
+
+}  // namespace qdq

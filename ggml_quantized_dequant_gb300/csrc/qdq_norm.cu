@@ -1,0 +1,201 @@
+// Root-mean-square norm of activation rows, with the residual's addition in front and the
+// result in the input's type, as a packed Q8_0 matrix, or both.
+//
+//   h = x + r,   y = h / sqrt(mean(h^2) + eps) * w
+//   Q8_0: d = f16(max |y| / 127) over 32 consecutive y, code = rint(y * (1 / d)) within +-127
+//
+// One CTA per row.  The row is read once into registers (8 to 32 elements per thread, all
+// loads before the first use), its sum of squares is folded over the warps through shared
+// memory in a fixed order, and every output is written from the registers: x and r are read
+// once and each output written once, which is the floor.  Sums are f32.
+#include "qdq_types.cuh"
+
+namespace qdq {
+namespace {
+
+struct NormArgs {
+  const void *x, *residual;
+  const float *weight;
+  void *sum_out, *out;
+  uint8_t *q8;
+  int rows, n;
+  int64_t x_stride, residual_stride, sum_stride, out_stride;
+  float eps;
+};
+
+template <int V, typename T>
+__device__ __forceinline__ void load_v(const T *p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    const uint4 u = ld_u4(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2(w[i], T{});
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else if constexpr (V == 4) {
+    const float4 f = load4(p);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  } else {
+    v[0] = load1(p);
+  }
+}
+template <int V, typename T>
+__device__ __forceinline__ void store_v(T *p, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1], T{}), pack2(v[2], v[3], T{}), pack2(v[4], v[5], T{}),
+                                               pack2(v[6], v[7], T{}));
+  } else if constexpr (V == 4) {
+    store4(p, make_float4(v[0], v[1], v[2], v[3]));
+  } else {
+    store1(p, v[0]);
+  }
+}
+
+// V elements per load (16 or 8 bytes, or 1 element where the rows are not aligned), E elements
+// per thread; element (i * blockDim + thread) * V + j of the row is the thread's i-th group.
+template <typename T, int V, int E>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
+  constexpr int G = E / V;
+  __shared__ float part[32];
+  const int row = blockIdx.x, n = a.n;
+  pdl_launch_dependents();
+  pdl_wait();
+  const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
+  const T *r = a.residual ? static_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;
+  float h[G][V];
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+    if (e < n) {
+      load_v<V>(x + e, h[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) h[i][j] = 0.f;
+    }
+  }
+  if (r) {
+    float b[G][V];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+      if (e < n) load_v<V>(r + e, b[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+      if (e < n) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] += b[i][j];
+      }
+    }
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) s = fmaf(h[i][j], h[i][j], s);
+  s = warp_sum(s);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[warp] = s;
+  __syncthreads();
+  s = warp_sum(lane < int(blockDim.x >> 5) ? part[lane] : 0.f);
+  const float inv = rsqrtf(s / float(n) + a.eps);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+    const bool in = e < n;
+    if (in && a.sum_out) store_v<V>(static_cast<T *>(a.sum_out) + row * a.sum_stride + e, h[i]);
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = h[i][j] * inv;
+    if (in && a.weight) {
+      float w[V];
+      if constexpr (V == 8) {
+        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + e)), w1 = __ldg(reinterpret_cast<const float4 *>(a.weight + e) + 1);
+        w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+        w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
+      } else if constexpr (V == 4) {
+        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + e));
+        w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+      } else {
+        w[0] = __ldg(a.weight + e);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] *= w[j];
+    }
+    if (in && a.out) store_v<V>(static_cast<T *>(a.out) + row * a.out_stride + e, y);
+    if (a.q8) {  // n % 32 == 0: a block of 32 lies in 32 / V neighbouring lanes, all in or all past the row
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) m = max_abs_bits(m, y[j]);
+#pragma unroll
+      for (int o = 16 / V; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const __half d = __float2half_rn(__fdiv_rn(m, 127.f));
+      const float df = __half2float(d);
+      const float id = df > 0.f ? __frcp_rn(df) : 0.f;
+      if (in) {
+        int8_t q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[j] = int8_t(__float2int_rn(fminf(fmaxf(y[j] * id, -127.f), 127.f)));
+        int8_t *qp = reinterpret_cast<int8_t *>(a.q8) + int64_t(row) * n + e;
+        if constexpr (V == 8)
+          *reinterpret_cast<uint2 *>(qp) = *reinterpret_cast<const uint2 *>(q);
+        else if constexpr (V == 4)
+          *reinterpret_cast<uint32_t *>(qp) = *reinterpret_cast<const uint32_t *>(q);
+        else
+          *qp = q[0];
+        if ((e & 31) == 0)
+          reinterpret_cast<__half *>(a.q8 + int64_t(a.rows) * n)[int64_t(row) * (n / 32) + e / 32] = d;
+      }
+    }
+  }
+}
+
+template <typename T, int V, int E>
+cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
+  const int groups = (a.n + V - 1) / V, per = E / V;
+  const int threads = ((groups + per - 1) / per + 31) / 32 * 32;
+  return launch(rms_norm_kernel<T, V, E>, dim3(a.rows), dim3(threads), 0, s, a);
+}
+
+}  // namespace
+
+int launch_rms_norm(const void *x, const void *residual, const float *weight, void *sum_out, void *out, void *q8,
+                    int type, int rows, int n, int64_t x_stride, int64_t residual_stride, int64_t sum_stride,
+                    int64_t out_stride, float eps, cudaStream_t s) {
+  const NormArgs a{x, residual, weight, sum_out, out, static_cast<uint8_t *>(q8), rows, n, x_stride, residual_stride,
+                   sum_stride, out_stride, eps};
+  const int eb = type_bytes(type);
+  // vector loads where every row of every operand starts on a vector boundary
+  auto fits = [&](int v) {
+    const uintptr_t b = uintptr_t(v) * eb;
+    auto ok = [&](const void *p, int64_t st) {
+      return !p || (reinterpret_cast<uintptr_t>(p) % b == 0 && (rows == 1 || (st * eb) % int64_t(b) == 0));
+    };
+    return n % v == 0 && ok(x, x_stride) && ok(residual, residual_stride) && ok(sum_out, sum_stride) &&
+           ok(out, out_stride) && (!weight || reinterpret_cast<uintptr_t>(weight) % 16 == 0);
+  };
+  const bool few = rows <= 152;
+  const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
+    using T = decltype(t);
+    auto pick = [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      if (few && n <= 8192) return run_norm<T, V, 8>(a, s);
+      if (few && n <= 16384) return run_norm<T, V, 16>(a, s);
+      return run_norm<T, V, 32>(a, s);
+    };
+    if constexpr (sizeof(T) == 2) {
+      if (fits(8)) return int(pick(std::integral_constant<int, 8>{}));
+    }
+    if (fits(4)) return int(pick(std::integral_constant<int, 4>{}));
+    return int(pick(std::integral_constant<int, 1>{}));
+  }));
+  return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
+}
+
+}  // namespace qdq

@@ -1,0 +1,113 @@
+// Activation element types of the decode-step operators (QDQ_TYPE_* in qdq.h): coherent
+// loads of 1, 4 or 8 consecutive elements as f32, stores with one rounding, and the
+// int8 cache's page geometry.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "qdq_internal.cuh"
+
+namespace qdq {
+
+inline int type_bytes(int type) { return type == QDQ_TYPE_F32 ? 4 : 2; }
+inline bool type_ok(int type) { return type == QDQ_TYPE_F32 || type == QDQ_TYPE_F16 || type == QDQ_TYPE_BF16; }
+
+// Runs `f` with a value of the element type as its argument.
+template <typename F>
+inline int with_type(int type, F &&f) {
+  switch (type) {
+    case QDQ_TYPE_F32: return f(float{});
+    case QDQ_TYPE_F16: return f(__half{});
+    default: return f(__nv_bfloat16{});
+  }
+}
+
+// Loads of data an earlier kernel wrote: volatile, so that they stay behind griddepcontrol.wait.
+__device__ __forceinline__ uint4 ld_u4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_u2(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u1(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_h1(const void *p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {  // bf16 is the high half of an f32
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float load1(const float *p) { return __uint_as_float(ld_u1(p)); }
+__device__ __forceinline__ float load1(const __half *p) { return __half2float(__ushort_as_half(ld_h1(p))); }
+__device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __uint_as_float(uint32_t(ld_h1(p)) << 16); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void store1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Four consecutive elements (16- or 8-byte aligned).
+__device__ __forceinline__ float4 load4(const float *p) {
+  const uint4 v = ld_u4(p);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
+  const uint2 v = ld_u2(p);
+  const float2 a = unpack2(v.x, T{}), b = unpack2(v.y, T{});
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float4 v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v.x, v.y, T{}), pack2(v.z, v.w, T{}));
+}
+
+// Larger of two non-negative floats with a NaN counted as the largest (the order of their bits).
+__device__ __forceinline__ float max_abs_bits(float a, float b) {
+  const uint32_t x = __float_as_uint(a) & 0x7FFFFFFFu, y = __float_as_uint(b) & 0x7FFFFFFFu;
+  return __uint_as_float(x > y ? x : y);
+}
+
+// ---- the int8 cache (layout in qdq.h) ---------------------------------------------
+constexpr int kKvBlock = QDQ_KV_BLOCK;
+
+__host__ __device__ __forceinline__ int64_t kv_record_bytes(int page_tokens, int head_dim) {
+  return (int64_t(2) * page_tokens * head_dim + 8 * (page_tokens / kKvBlock) + 127) / 128 * 128;
+}
+
+struct KvPool {
+  uint8_t *pages;
+  const int *table;  // n_seqs rows of table_stride page ids
+  int n_pages, page_tokens, n_kv, table_stride;
+};
+
+// Byte offset in the pool of head h's record of the page that holds block `blk` (16 tokens) of
+// sequence s, or -1 when the table has no valid page for it.
+__device__ __forceinline__ int64_t kv_record_of(const KvPool &c, int s, int blk, int h, int64_t rec) {
+  const int pg = blk / (c.page_tokens / kKvBlock);
+  if (pg >= c.table_stride) return -1;
+  const int id = int(ld_u1(c.table + int64_t(s) * c.table_stride + pg));
+  if (id < 0 || id >= c.n_pages) return -1;
+  return (int64_t(id) * c.n_kv + h) * rec;
+}
+
+}  // namespace qdq

@@ -294,6 +294,111 @@ size_t qdq_q4k_swiglu_batch_workspace_bytes(int M, int n_ff, int n_embd);
 int qdq_q4k_swiglu_batch(const void *Wg, const void *Wu, const float *X, float *mid, void *workspace,
                          int n_ff, int n_embd, int M, cudaStream_t stream);
 
+/* ---- what stands between the projections of a decode step ---------------------
+ * No counterpart on the reference pages (their attention, cache and norm live in another
+ * engine): the operators that a model's layer needs between the projections above.
+ * Activations are f32, f16 or bf16 (QDQ_TYPE_*); all sums, maxima and softmax
+ * statistics are f32, and an output is rounded once to its type.  Strides count
+ * elements between consecutive rows (tokens).
+ */
+#define QDQ_TYPE_F32  0
+#define QDQ_TYPE_F16  1
+#define QDQ_TYPE_BF16 2
+
+/* ---- RMS norm with the residual's addition ------------------------------------
+ *   h = x + residual (x when residual is NULL),
+ *   y = h / sqrt(mean(h^2) + eps) * weight (weight NULL: 1),
+ * per row of n elements (1 <= n <= QDQ_MAX_NORM_N), rows >= 0 (0: nothing to do).
+ * sum_out (may be NULL): h, rounded to the type (the norm uses h unrounded).
+ * out (may be NULL): y in the type.  q8_out (may be NULL; n % 32 == 0, 16-byte aligned):
+ * y as a packed Q8_0 matrix of rows x n (qdq_q8_0_packed_bytes(rows, n) bytes, layout
+ * above): d = f16(max |y| / 127) over each 32, code = rint(y * (1 / d)) within
+ * +-127, 0 where d is 0; a block with a NaN has d = NaN.  out or q8_out is given.
+ * x, residual, sum_out and out are aligned to their elements and weight to 4 bytes (16-byte
+ * aligned rows are faster); strides are at least n.  sum_out may be exactly residual or x, and out exactly x
+ * or residual (with its stride); outputs may overlap nothing else.
+ */
+#define QDQ_MAX_NORM_N 32768
+int qdq_rms_norm(const void *x, const void *residual, const float *weight, void *sum_out, void *out, void *q8_out,
+                 int type, int rows, int n, long long x_stride, long long residual_stride, long long sum_stride,
+                 long long out_stride, float eps, cudaStream_t stream);
+
+/* ---- paged 8-bit key/value cache ------------------------------------------------
+ * A pool of n_pages pages of qdq_kv_page_bytes bytes; a page holds page_tokens tokens
+ * (a multiple of QDQ_KV_BLOCK) of one sequence.  In a page each of the n_kv
+ * heads has one record of page_bytes / n_kv bytes (a multiple of 128):
+ *   key codes page_tokens x head_dim int8, value codes page_tokens x head_dim int8,
+ *   key scales page_tokens / 16 f32, value scales page_tokens / 16 f32, zeros or anything.
+ * A block is QDQ_KV_BLOCK consecutive tokens of a page (and so of a sequence); value = code * scale.
+ * head_dim is 64, 96, 128, 192 or 256.  page_table: n_seqs rows of table_stride int32 page
+ * ids; row s, entry i is the page of tokens i * page_tokens .. of sequence s.  Entries
+ * past a sequence's tokens are not read.  kv_len (int32): tokens of each sequence,
+ * the appended or querying ones included.  pages: 128-byte aligned; the int arrays 4-byte.
+ *
+ * qdq_kv_append quantises new tokens into the cache: the last cu_new[s + 1] - cu_new[s] of
+ *   sequence s's kv_len[s] tokens are rows cu_new[s] .. of k and v (n_kv x
+ *   head_dim elements per row, rows k_stride / v_stride elements apart; cu_new NULL:
+ *   one token per sequence, row s).  max_new: an upper bound of the new tokens of a
+ *   sequence (tokens past it are not appended).  Per block, head, and keys or values:
+ *     s = max(s_old, max |x| / 127) over its new tokens (s_old: its scale, 0 if it held none),
+ *     code = rint(x * (1 / s)) for new tokens, rint(code * (s_old / s)) for those it held,
+ *   all f32; s below the smallest normal f32 counts as 0.  A new value that is
+ *   not finite makes the block's scale NaN.  Tokens whose page id is outside [0, n_pages) or
+ *   whose table entry does not exist are dropped; more new tokens than kv_len append nothing.
+ * qdq_kv_read writes cu[s + 1] - cu[s] tokens of sequence s from token start[s] (start
+ *   NULL: 0) to rows cu[s] .. of k and v; max_tokens bounds a sequence's tokens.  A
+ *   token without a valid page reads as NaN.  The caller asks for tokens it has appended.
+ * k and v are 16-byte aligned, their strides (>= n_kv * head_dim) whole 16 bytes.
+ */
+#define QDQ_KV_BLOCK 16
+size_t qdq_kv_page_bytes(int page_tokens, int n_kv, int head_dim);   /* 0 on bad arguments */
+int qdq_kv_append(void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
+                  int table_stride, const int *kv_len, const int *cu_new, int n_seqs, int max_new, const void *k,
+                  const void *v, long long k_stride, long long v_stride, int type, cudaStream_t stream);
+int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
+                int table_stride, const int *start, const int *cu, int n_seqs, int max_tokens, void *k, void *v,
+                long long k_stride, long long v_stride, int type, cudaStream_t stream);
+
+/* ---- attention over the cache -----------------------------------------------------
+ * For each query row i < n of sequence s (n = cu_q[s + 1] - cu_q[s], rows cu_q[s] .. of q;
+ * cu_q NULL: one query per sequence, row s), at position pos = kv_len[s] - n + i, and
+ * each of n_heads heads (n_heads a multiple of n_kv; head h reads cache head h / (n_heads / n_kv)):
+ *   x[j] = scale * q . k[j];  softcap > 0: x[j] = softcap * tanh(x[j] / softcap);
+ *   slopes (n_heads f32, may be NULL): x[j] -= slopes[h] * (pos - j);
+ *   visible: j <= pos, and pos - j < window when window > 0;
+ *   out = sum_j softmax(x)[j] v[j],  lse (n_heads f32 per query row, may be NULL) = log sum_j e^x[j].
+ * A row that sees no token gives zeros and lse -inf.  A sequence with kv_len outside [0,
+ * max_kv_len] or past its table row gives NaN, and so does a row that sees a token
+ * with an invalid page or a NaN scale, and a query that is not finite.
+ * max_q: an upper bound of a sequence's queries (rows past it are not written).
+ * q, out: head_dim elements per head, n_heads heads per row, rows q_stride /
+ * out_stride elements apart, 16-byte aligned (strides whole 16 bytes).  out may overlap no other argument.
+ * workspace: qdq_kv_attention_workspace_bytes(...) bytes (0 when no device can be queried), 256-byte aligned, ZEROED ONCE by
+ * the caller before its first use; a call leaves it ready for the next one on the same stream.
+ * Results do not depend on the order in which CTAs run.
+ */
+size_t qdq_kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
+int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
+                     int table_stride, const int *kv_len, const int *cu_q, int n_seqs, int max_q, int max_kv_len,
+                     int n_heads, const void *q, long long q_stride, void *out, long long out_stride, float *lse,
+                     const float *slopes, float scale, float softcap, int window, int type, void *workspace,
+                     size_t workspace_bytes, cudaStream_t stream);
+
+/* ---- log probabilities of given tokens ----------------------------------------------
+ * For each of `rows` rows (row_stride elements apart) of n logits x (1 <= n <= 2^30):
+ *   lse = log sum_i e^x[i];  logprob[r] = x[tokens[r]] - lse (NaN for a token outside [0, n));
+ *   entropy[r] = -sum_i p[i] log p[i], p = softmax(x)  (a -inf logit counts 0; may be NULL);
+ *   top_index / top_logprob [r, j] (j < k, 0 <= k <= min(n, QDQ_MAX_TOPK); ignored for k = 0):
+ *   the j-th of the order of qdq_topk_rows, and its x - lse.
+ * A row with a NaN or +inf, or without a logit above -inf, has NaN in all but top_index.
+ * tokens and logprob: both given or both NULL.  workspace as for qdq_kv_attention
+ * (qdq_token_logprobs_workspace_bytes, 256-byte aligned, zeroed once).  Outputs may overlap nothing.
+ */
+size_t qdq_token_logprobs_workspace_bytes(int rows, int n, int k);
+int qdq_token_logprobs(const void *logits, long long row_stride, int type, const int *tokens, int rows, int n, int k,
+                       float *logprob, float *entropy, int *top_index, float *top_logprob, void *workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
 /* ---- pipeline health -------------------------------------------------------
  * Every wait inside the tensor-core pipeline is bounded (2 s wall clock); a
  * wait that runs out makes its CTA stop early instead of hanging, and counts

@@ -1,0 +1,177 @@
+"""Refusals and sizes of the decode-step operators (no GPU: fake, never dereferenced addresses)."""
+import pytest
+
+GOOD = 0x10000000
+
+
+def _at(i):
+    return GOOD + (i << 28)
+
+
+@pytest.fixture(scope="module")
+def qdq():
+    from ggml_quantized_dequant_gb300 import _build
+    import ggml_quantized_dequant_gb300 as q
+    _build.build()
+    q.load()
+    return q
+
+
+def test_rms_norm_refusals(qdq):
+    f = qdq.lib().qdq_rms_norm
+    x, r, w, s, o, q8 = (_at(i) for i in range(6))
+
+    def call(x=x, r=r, w=w, s=s, o=o, q8=q8, type=0, rows=4, n=256, xs=256, rs=256, ss=256, os=256, eps=1e-5):
+        return f(x, r, w, s, o, q8, type, rows, n, xs, rs, ss, os, eps, None)
+
+    assert call(x=None) == qdq.QDQ_ERR_NULL
+    assert call(o=None, q8=None) == qdq.QDQ_ERR_NULL
+    assert call(type=3) == qdq.QDQ_ERR_DIMS
+    assert call(rows=-1) == qdq.QDQ_ERR_DIMS
+    assert call(n=0) == qdq.QDQ_ERR_DIMS
+    assert call(n=250) == qdq.QDQ_ERR_DIMS                      # Q8_0 needs whole blocks
+    assert call(xs=255) == qdq.QDQ_ERR_DIMS
+    assert call(ss=255) == qdq.QDQ_ERR_DIMS
+    assert call(eps=-1.0) == qdq.QDQ_ERR_DIMS
+    assert call(eps=float("nan")) == qdq.QDQ_ERR_DIMS
+    assert call(n=1 << 16, xs=1 << 16, rs=1 << 16, ss=1 << 16, os=1 << 16) == qdq.QDQ_ERR_UNSUPPORTED
+    assert call(x=x + 2) == qdq.QDQ_ERR_ALIGN
+    assert call(x=x + 1, type=2) == qdq.QDQ_ERR_ALIGN
+    assert call(w=w + 2) == qdq.QDQ_ERR_ALIGN
+    assert call(q8=q8 + 8) == qdq.QDQ_ERR_ALIGN
+    assert call(o=x + 16) == qdq.QDQ_ERR_ALIAS                   # not exactly x
+    assert call(o=x, os=512) == qdq.QDQ_ERR_ALIAS                # x with another stride
+    assert call(s=o) == qdq.QDQ_ERR_ALIAS
+    assert call(s=w) == qdq.QDQ_ERR_ALIAS
+    assert call(q8=x) == qdq.QDQ_ERR_ALIAS
+    assert call(rows=0) == qdq.QDQ_OK
+    assert call(rows=0, o=x, s=r) == qdq.QDQ_OK                  # in place
+
+
+def test_page_bytes(qdq):
+    assert qdq.kv_page_bytes(64, 8, 128) == 8 * 16512             # 16384 codes + 32 bytes of scales, to 128
+    assert qdq.kv_page_bytes(16, 1, 64) == 2176
+    for bad in ((15, 1, 64), (24, 1, 64), (16, 0, 64), (16, 1, 80), (0, 1, 64)):
+        assert qdq.kv_page_bytes(*bad) == 0
+
+
+def test_append_and_read_refusals(qdq):
+    lib = qdq.lib()
+    p, t, n, cu, k, v = (_at(i) for i in range(6))
+
+    def append(p=p, pages=4, page=16, heads=2, dim=64, t=t, ts=3, n=n, cu=cu, seqs=2, most=5, k=k, v=v, ks=128, vs=128, type=0):
+        return lib.qdq_kv_append(p, pages, page, heads, dim, t, ts, n, cu, seqs, most, k, v, ks, vs, type, None)
+
+    def read(p=p, pages=4, page=16, heads=2, dim=64, t=t, ts=3, start=n, cu=cu, seqs=2, most=5, k=k, v=v, ks=128, vs=128, type=0):
+        return lib.qdq_kv_read(p, pages, page, heads, dim, t, ts, start, cu, seqs, most, k, v, ks, vs, type, None)
+
+    for call in (append, read):
+        assert call(p=None) == qdq.QDQ_ERR_NULL
+        assert call(t=None) == qdq.QDQ_ERR_NULL
+        assert call(k=None) == qdq.QDQ_ERR_NULL
+        assert call(pages=0) == qdq.QDQ_ERR_DIMS
+        assert call(page=24) == qdq.QDQ_ERR_DIMS
+        assert call(heads=0) == qdq.QDQ_ERR_DIMS
+        assert call(ts=0) == qdq.QDQ_ERR_DIMS
+        assert call(seqs=-1) == qdq.QDQ_ERR_DIMS
+        assert call(most=-1) == qdq.QDQ_ERR_DIMS
+        assert call(type=7) == qdq.QDQ_ERR_DIMS
+        assert call(ks=127) == qdq.QDQ_ERR_DIMS
+        assert call(dim=80, ks=160, vs=160) == qdq.QDQ_ERR_UNSUPPORTED
+        assert call(p=p + 64) == qdq.QDQ_ERR_ALIGN
+        assert call(t=t + 2) == qdq.QDQ_ERR_ALIGN
+        assert call(v=v + 8) == qdq.QDQ_ERR_ALIGN
+        assert call(vs=130) == qdq.QDQ_ERR_ALIGN
+        assert call(ks=132, type=1) == qdq.QDQ_ERR_ALIGN
+        assert call(k=p + 128) == qdq.QDQ_ERR_ALIAS
+        assert call(seqs=0) == qdq.QDQ_OK
+        assert call(most=0) == qdq.QDQ_OK
+    assert append(cu=None) == qdq.QDQ_ERR_DIMS                    # one token each needs max_new 1
+    assert append(n=None) == qdq.QDQ_ERR_NULL
+    assert append(t=p) == qdq.QDQ_ERR_ALIAS
+    assert read(cu=None) == qdq.QDQ_ERR_NULL
+    assert read(k=v) == qdq.QDQ_ERR_ALIAS
+
+
+def test_attention_refusals(qdq):
+    f = qdq.lib().qdq_kv_attention
+    p, t, n, cu, q, o, lse, sl, ws = (_at(i) for i in range(9))
+
+    def call(p=p, pages=4, page=16, heads=2, dim=64, t=t, ts=3, n=n, cu=cu, seqs=2, most=5, kv=48, nh=4, q=q, qs=256, o=o, os=256,
+             lse=lse, sl=sl, scale=0.125, cap=0.0, win=0, type=0, ws=ws, wb=1 << 24):
+        return f(p, pages, page, heads, dim, t, ts, n, cu, seqs, most, kv, nh, q, qs, o, os, lse, sl, scale, cap, win, type, ws, wb, None)
+
+    for name in ("p", "t", "n", "q", "o", "ws"):
+        assert call(**{name: None}) == qdq.QDQ_ERR_NULL
+    assert call(nh=3) == qdq.QDQ_ERR_DIMS
+    assert call(kv=-1) == qdq.QDQ_ERR_DIMS
+    assert call(win=-1) == qdq.QDQ_ERR_DIMS
+    assert call(cap=-1.0) == qdq.QDQ_ERR_DIMS
+    assert call(scale=float("inf")) == qdq.QDQ_ERR_DIMS
+    assert call(cu=None) == qdq.QDQ_ERR_DIMS
+    assert call(qs=255) == qdq.QDQ_ERR_DIMS
+    assert call(type=-1) == qdq.QDQ_ERR_DIMS
+    assert call(dim=72, qs=288, os=288) == qdq.QDQ_ERR_UNSUPPORTED
+    assert call(kv=(1 << 30) + 1) == qdq.QDQ_ERR_UNSUPPORTED
+    assert call(q=q + 4) == qdq.QDQ_ERR_ALIGN
+    assert call(ws=ws + 16) == qdq.QDQ_ERR_ALIGN
+    assert call(os=258) == qdq.QDQ_ERR_ALIGN
+    assert call(o=q) == qdq.QDQ_ERR_ALIAS
+    assert call(o=p + 256) == qdq.QDQ_ERR_ALIAS
+    assert call(lse=o) == qdq.QDQ_ERR_ALIAS
+    assert call(ws=q) == qdq.QDQ_ERR_ALIAS
+    assert call(sl=o) == qdq.QDQ_ERR_ALIAS
+    assert call(seqs=0) == qdq.QDQ_OK
+    assert call(most=0) == qdq.QDQ_OK
+    assert qdq.kv_attention_workspace_bytes(1, 1, 100, 3, 2, 64) == 0
+    assert qdq.kv_attention_workspace_bytes(1, 1, 100, 4, 2, 72) == 0
+
+
+def test_logprobs_refusals(qdq):
+    f = qdq.lib().qdq_token_logprobs
+    x, t, lp, en, ti, tl, ws = (_at(i) for i in range(7))
+
+    def call(x=x, st=1000, type=0, t=t, rows=3, n=1000, k=5, lp=lp, en=en, ti=ti, tl=tl, ws=ws, wb=1 << 24):
+        return f(x, st, type, t, rows, n, k, lp, en, ti, tl, ws, wb, None)
+
+    assert call(x=None) == qdq.QDQ_ERR_NULL
+    assert call(t=None) == qdq.QDQ_ERR_NULL                       # a log probability needs its token
+    assert call(lp=None) == qdq.QDQ_ERR_NULL
+    assert call(ti=None) == qdq.QDQ_ERR_NULL
+    assert call(ws=None) == qdq.QDQ_ERR_NULL
+    assert call(st=999) == qdq.QDQ_ERR_DIMS
+    assert call(k=-1) == qdq.QDQ_ERR_DIMS
+    assert call(n=4, k=5) == qdq.QDQ_ERR_DIMS
+    assert call(type=9) == qdq.QDQ_ERR_DIMS
+    assert call(k=65) == qdq.QDQ_ERR_UNSUPPORTED
+    assert call(x=x + 2) == qdq.QDQ_ERR_ALIGN
+    assert call(lp=lp + 2) == qdq.QDQ_ERR_ALIGN
+    assert call(ws=ws + 128) == qdq.QDQ_ERR_ALIGN
+    assert call(lp=x + 4) == qdq.QDQ_ERR_ALIAS
+    assert call(tl=ti) == qdq.QDQ_ERR_ALIAS
+    assert call(en=t) == qdq.QDQ_ERR_ALIAS
+    assert call(rows=0) == qdq.QDQ_OK
+    assert qdq.token_logprobs_workspace_bytes(3, 1000, 65) == 0
+
+
+def test_binding_refuses_wrong_tensors(qdq):
+    import torch
+    x = torch.zeros(4, 64)
+    with pytest.raises(TypeError):
+        qdq.rms_norm(x, None, x.half(), 4, 64)
+    with pytest.raises(TypeError):
+        qdq.rms_norm(x.double(), None, x.double(), 4, 64)
+    with pytest.raises(TypeError):
+        qdq.rms_norm(x, torch.zeros(64).half(), x, 4, 64)
+    with pytest.raises(ValueError):
+        qdq.rms_norm(x, None, x, 4, 63)
+    with pytest.raises(ValueError):
+        qdq.rms_norm(x.t().contiguous().t(), None, torch.zeros(4, 64), 4, 64)
+    with pytest.raises(TypeError):
+        qdq.token_logprobs(x, torch.zeros(4, dtype=torch.int64), torch.zeros(4), None, 4, 64, torch.zeros(256, dtype=torch.uint8))
+    pages = torch.zeros(3, 2176, dtype=torch.uint8)
+    table = torch.zeros(1, 2, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        qdq.kv_append(pages, table, torch.zeros(1, dtype=torch.int32), x, x, 1, 64, 16)
+    with pytest.raises(ValueError):
+        qdq.kv_append(pages[:, 1:], table.int(), torch.zeros(1, dtype=torch.int32), x, x, 1, 64, 16)
