@@ -144,10 +144,26 @@ def _ptr(t) -> int | None:
     return int(t.data_ptr())
 
 
+def _find_current_stream() -> int:
+    """The current stream of the current device; the first call binds the cheapest way to ask for it."""
+    global _current_stream
+    import torch
+    found = int(torch.cuda.current_stream().cuda_stream)  # also initialises CUDA in torch
+    try:  # the raw handle, without a Stream object for each call (3 us of a call's 6)
+        get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        if get(device()) == found:
+            _current_stream = lambda: get(device())  # noqa: E731
+    except AttributeError:
+        _current_stream = lambda: int(torch.cuda.current_stream().cuda_stream)  # noqa: E731
+    return found
+
+
+_current_stream = _find_current_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream) or None
+        return _current_stream() or None
     if isinstance(stream, int):
         return stream or None
     return int(stream.cuda_stream) or None
@@ -309,43 +325,41 @@ def set_option(key: int, value: int) -> int:
 # ---------------------------------------------------------------- decode-step operators
 # (the element type and the row strides come from the tensors, whose first dimension is the rows)
 
-_TYPES = {"torch.float32": QDQ_TYPE_F32, "torch.float16": QDQ_TYPE_F16, "torch.bfloat16": QDQ_TYPE_BF16}
-_types = {}
+_types = {}  # torch dtype -> QDQ_TYPE_*; filled at the first use, when torch is there
 
 
 def _type(t) -> int:
-    try:
-        return _types[t.dtype]
-    except KeyError:
-        v = _TYPES.get(str(t.dtype))
-        if v is None:
-            raise TypeError("float32, float16 or bfloat16 expected, got %s" % t.dtype) from None
-        _types[t.dtype] = v
-        return v
+    if not _types:
+        import torch
+        _types.update({torch.float32: QDQ_TYPE_F32, torch.float16: QDQ_TYPE_F16, torch.bfloat16: QDQ_TYPE_BF16})
+        _of["int32"], _of["float32"] = torch.int32, torch.float32
+    v = _types.get(t.dtype)
+    if v is None:
+        raise TypeError("float32, float16 or bfloat16 expected, got %s" % t.dtype)
+    return v
 
 
-def _same_type(name, t, *others):
-    for o in others:
-        if o is not None and o.dtype != t.dtype:
-            raise TypeError("%s: %s and %s do not have one element type" % (name, t.dtype, o.dtype))
+_of = {}
 
 
-def _int32(name, *tensors):
-    for t in tensors:
-        if t is not None and (str(t.dtype) != "torch.int32" or not t.is_contiguous()):
-            raise TypeError("%s: contiguous int32 tensors expected" % name)
-
-
-def _f32(name, *tensors):
-    for t in tensors:
-        if t is not None and (str(t.dtype) != "torch.float32" or not t.is_contiguous()):
-            raise TypeError("%s: contiguous float32 tensors expected" % name)
-
-
-def _rows(name, t, width):
-    """Row stride of a tensor of rows: the first dimension, the others hold ``width`` packed elements (one dimension: one row)."""
+def _vec(name, t, kind):
+    """Address of a contiguous int32 or float32 tensor, None for None (call _type first)."""
     if t is None:
-        return 0
+        return None
+    if t.dtype is not _of[kind] or not t.is_contiguous():
+        raise TypeError("%s: a contiguous %s tensor expected" % (name, kind))
+    return t.data_ptr()
+
+
+def _rows(name, t, width, dtype):
+    """(address, row stride) of a tensor of rows: the first dimension, the others hold ``width`` packed elements
+    (one dimension: one row)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise TypeError("%s: %s expected, got %s" % (name, dtype, t.dtype))
+    if t.is_contiguous() and t.numel() == len(t) * width and t.dim() > 1:
+        return t.data_ptr(), width
     shape, st = t.shape, t.stride()
     if len(shape) == 1:
         shape, st = (1, *shape), (width, *st)
@@ -356,19 +370,22 @@ def _rows(name, t, width):
         w *= shape[d]
     if w != width:
         raise ValueError("%s: rows of %d elements expected, got shape %s" % (name, width, tuple(t.shape)))
-    return st[0] if shape[0] > 1 else width
+    return t.data_ptr(), st[0] if shape[0] > 1 else width
 
 
 def rms_norm(x, weight, out, rows: int, n: int, eps: float = 1e-5, residual=None, sum_out=None, q8_out=None, stream=None):
     """RMS norm of ``x + residual`` per row into ``out`` (x's type) and / or ``q8_out`` (a packed Q8_0 matrix).
 
     ``sum_out`` receives ``x + residual``; it may be ``residual`` or ``x`` itself, and ``out`` may be ``x``."""
-    f = lib().qdq_rms_norm
-    _same_type("rms_norm", x, residual, sum_out, out)
-    _f32("rms_norm", weight)
-    _check("qdq_rms_norm", f(_ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(out), _ptr(q8_out), _type(x), rows, n,
-                             _rows("x", x, n), _rows("residual", residual, n), _rows("sum_out", sum_out, n),
-                             _rows("out", out, n), eps, _stream(stream)))
+    ty, dt = _type(x), x.dtype
+    xp, xs = _rows("x", x, n, dt)
+    rp, rs = _rows("residual", residual, n, dt)
+    sp, ss = _rows("sum_out", sum_out, n, dt)
+    op, os_ = _rows("out", out, n, dt)
+    status = lib().qdq_rms_norm(xp, rp, _vec("weight", weight, "float32"), sp, op, _ptr(q8_out), ty, rows, n, xs, rs, ss, os_, eps,
+                                _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_rms_norm", status)
 
 
 def kv_page_bytes(page_tokens: int, n_kv: int, head_dim: int) -> int:
@@ -384,35 +401,39 @@ def kv_pages(n_pages: int, page_tokens: int, n_kv: int, head_dim: int, device="c
     return torch.zeros(n_pages, b, dtype=torch.uint8, device=device)
 
 
-def _pool(name, pages, page_table, page_tokens, n_kv, head_dim):
-    b = lib().qdq_kv_page_bytes(page_tokens, n_kv, head_dim)
-    if not pages.is_contiguous() or (b and pages.numel() * pages.element_size() % b):
-        raise ValueError("%s: pages is not a whole number of packed pages" % name)
-    _int32(name, page_table)
-    return pages.numel() * pages.element_size() // b if b else 1
+def _pool(pages, page_table, page_tokens, n_kv, head_dim):
+    """(address of the pool, its pages, address of the table, its rows, their width)."""
+    rec = (2 * page_tokens * head_dim + page_tokens // 2 + 127) // 128 * 128  # a head's record
+    n, rest = divmod(pages.nbytes, n_kv * rec or 1)
+    if rest or not pages.is_contiguous():
+        raise ValueError("pages is not a whole number of packed pages")
+    seqs, width = page_table.shape
+    return pages.data_ptr(), n, _vec("page_table", page_table, "int32"), seqs, width
 
 
 def kv_append(pages, page_table, kv_len, k, v, n_kv: int, head_dim: int, page_tokens: int, cu_new=None, max_new: int = 1,
               stream=None):
     """Quantise new tokens (rows of ``k`` and ``v``) into the cache: the last tokens of each sequence's ``kv_len``."""
-    n = _pool("kv_append", pages, page_table, page_tokens, n_kv, head_dim)
-    _int32("kv_append", kv_len, cu_new)
-    _same_type("kv_append", k, v)
-    w = n_kv * head_dim
-    _check("qdq_kv_append", lib().qdq_kv_append(
-        _ptr(pages), n, page_tokens, n_kv, head_dim, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(cu_new),
-        page_table.shape[0], max_new, _ptr(k), _ptr(v), _rows("k", k, w), _rows("v", v, w), _type(k), _stream(stream)))
+    ty, w = _type(k), n_kv * head_dim
+    pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
+    kp, ks = _rows("k", k, w, k.dtype)
+    vp, vs = _rows("v", v, w, k.dtype)
+    status = lib().qdq_kv_append(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32"),
+                                 _vec("cu_new", cu_new, "int32"), seqs, max_new, kp, vp, ks, vs, ty, _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_kv_append", status)
 
 
 def kv_read(pages, page_table, start, cu, k, v, n_kv: int, head_dim: int, page_tokens: int, max_tokens: int, stream=None):
     """Write the values of cached tokens (``cu[s+1] - cu[s]`` of sequence s from ``start[s]``) to rows of ``k`` and ``v``."""
-    n = _pool("kv_read", pages, page_table, page_tokens, n_kv, head_dim)
-    _int32("kv_read", start, cu)
-    _same_type("kv_read", k, v)
-    w = n_kv * head_dim
-    _check("qdq_kv_read", lib().qdq_kv_read(
-        _ptr(pages), n, page_tokens, n_kv, head_dim, _ptr(page_table), page_table.shape[1], _ptr(start), _ptr(cu),
-        page_table.shape[0], max_tokens, _ptr(k), _ptr(v), _rows("k", k, w), _rows("v", v, w), _type(k), _stream(stream)))
+    ty, w = _type(k), n_kv * head_dim
+    pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
+    kp, ks = _rows("k", k, w, k.dtype)
+    vp, vs = _rows("v", v, w, k.dtype)
+    status = lib().qdq_kv_read(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("start", start, "int32"),
+                               _vec("cu", cu, "int32"), seqs, max_tokens, kp, vp, ks, vs, ty, _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_kv_read", status)
 
 
 def kv_attention_workspace_bytes(n_seqs: int, max_q: int, max_kv_len: int, n_heads: int, n_kv: int, head_dim: int) -> int:
@@ -430,16 +451,17 @@ def kv_attention(pages, page_table, kv_len, q, out, workspace, n_heads: int, n_k
                  max_kv_len: int, cu_q=None, max_q: int = 1, scale: float | None = None, softcap: float = 0.0,
                  window: int = 0, slopes=None, lse=None, stream=None):
     """Attention of the rows of ``q`` over the cached tokens into ``out`` (``scale`` defaults to head_dim ** -0.5)."""
-    n = _pool("kv_attention", pages, page_table, page_tokens, n_kv, head_dim)
-    _int32("kv_attention", kv_len, cu_q)
-    _f32("kv_attention", slopes, lse)
-    _same_type("kv_attention", q, out)
-    w = n_heads * head_dim
-    _check("qdq_kv_attention", lib().qdq_kv_attention(
-        _ptr(pages), n, page_tokens, n_kv, head_dim, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(cu_q),
-        page_table.shape[0], max_q, max_kv_len, n_heads, _ptr(q), _rows("q", q, w), _ptr(out), _rows("out", out, w), _ptr(lse),
-        _ptr(slopes), head_dim ** -0.5 if scale is None else scale, softcap, window, _type(q), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    ty, w = _type(q), n_heads * head_dim
+    pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
+    qp, qs = _rows("q", q, w, q.dtype)
+    op, os_ = _rows("out", out, w, q.dtype)
+    status = lib().qdq_kv_attention(
+        pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32"), _vec("cu_q", cu_q, "int32"), seqs,
+        max_q, max_kv_len, n_heads, qp, qs, op, os_, _vec("lse", lse, "float32"), _vec("slopes", slopes, "float32"),
+        head_dim ** -0.5 if scale is None else scale, softcap, window, ty, workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_kv_attention", status)
 
 
 def token_logprobs_workspace_bytes(rows: int, n: int, k: int) -> int:
@@ -455,11 +477,14 @@ def token_logprobs_workspace(rows: int, n: int, k: int, device="cuda"):
 def token_logprobs(logits, tokens, logprob, entropy, rows: int, n: int, workspace, k: int = 0, top_index=None,
                    top_logprob=None, stream=None):
     """Per row: the log probability of ``tokens[r]``, the entropy, and the k best (index, log probability) pairs."""
-    _int32("token_logprobs", tokens, top_index)
-    _f32("token_logprobs", logprob, entropy, top_logprob)
-    _check("qdq_token_logprobs", lib().qdq_token_logprobs(
-        _ptr(logits), _rows("logits", logits, n), _type(logits), _ptr(tokens), rows, n, k, _ptr(logprob), _ptr(entropy),
-        _ptr(top_index), _ptr(top_logprob), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    ty = _type(logits)
+    xp, xs = _rows("logits", logits, n, logits.dtype)
+    status = lib().qdq_token_logprobs(
+        xp, xs, ty, _vec("tokens", tokens, "int32"), rows, n, k, _vec("logprob", logprob, "float32"),
+        _vec("entropy", entropy, "float32"), _vec("top_index", top_index, "int32"), _vec("top_logprob", top_logprob, "float32"),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_token_logprobs", status)
 
 
 # ---------------------------------------------------------------- upload helpers

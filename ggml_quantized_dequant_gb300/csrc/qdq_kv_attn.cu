@@ -5,15 +5,20 @@
 //   s[j] -= slope * (pos - j)                       when slopes are given
 //   o    = sum_j e^(s[j] - m) vc[j] vs[j / 16] / sum_j e^(s[j] - m)  over the visible j
 //
-// Rows are (query token, head of the group) pairs that share a key/value head, eight to a tile.
-// A warp walks blocks of 16 tokens: the codes go from global memory straight into the operand
-// registers of 16-bit matrix instructions (a code is exact in f16), with the next block's loads
-// in flight meanwhile.  The instruction has 16 rows: rows 0-7 hold the high f16 part of the eight
-// queries (scaled to a power of two below 2^14 per row), rows 8-15 the rest in f16, so the products are exact
-// and a score has f32 precision; probabilities are split the same way.  The running maximum,
-// the sum and the accumulators are f32.  The four warps of a CTA take every fourth block of
-// their split of the tokens and are joined through shared memory; splits of one tile are joined
-// by the CTA that finishes last, in split order.
+// Rows are (query token, head of the group) pairs that share a key/value head.  A warp walks
+// blocks of 16 tokens: their codes come through a ring of asynchronous copies in its own part of
+// shared memory (16-byte chunks exchanged by row so that the fragment loads below meet no bank
+// conflict) and become the operands of 16-row matrix instructions with 16-bit operands (a code
+// is exact in f16).  A query row is scaled by a power of two to below 2^14 first.
+//   two parts (f32 activations; a tile is 8 rows): instruction rows 0-7 hold the high f16 part
+//     of the queries, rows 8-15 the rest in f16, so the products are exact and a score has f32
+//     precision; the probabilities are split the same way.
+//   one part (16-bit activations with more than 8 rows per head; a tile is 16 rows): the queries
+//     are exact in f16 but for elements 2^-25 below the row's largest, the
+//     probabilities are rounded to f16 (2^-11 relative, as the output is).
+// The running maximum, the sum and the accumulators are f32.  The four warps of a CTA take every
+// fourth block of their split of the tokens and are joined through shared memory; splits of one
+// tile are joined by the CTA that finishes last, in split order.
 #include <cuda_fp16.h>
 
 #include "qdq_types.cuh"
@@ -22,9 +27,10 @@ namespace qdq {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRows = 8;         // rows per tile
+constexpr int kStages = 3;       // blocks in a warp's ring
+constexpr float kLazy = 1.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
 constexpr int kMaxSplitBlocks = 128;
-constexpr float kPScale = 16384.f;  // probabilities are split into f16 parts at this scale
+constexpr float kPScale = 16384.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
@@ -56,25 +62,29 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t u) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-template <int N>
-struct Words {
-  uint32_t w[N];
-};
 template <int BYTES>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
   if constexpr (BYTES == 16) {
-    const uint4 v = ld_u4(p);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
   } else if constexpr (BYTES == 8) {
-    const uint2 v = ld_u2(p);
-    w[0] = v.x;
-    w[1] = v.y;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
   } else {
-    w[0] = ld_u1(p);
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
   }
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 2^x, 0 for -inf (one instruction; a result below the normal numbers is 0)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 template <int D>
@@ -84,9 +94,29 @@ struct Shape {
   static constexpr int kKSteps = D / 16;
   static constexpr int kVB = D % 128 == 0 ? 16 : D % 64 == 0 ? 8 : 4;  // of a value row
   static constexpr int kVL = D / (8 * kVB);
-  static constexpr int kWords = 2 * D / 16;          // words per lane of a block's keys (and of its values): 2 D / 16
   static constexpr int kNT = D / 8;                  // accumulator tiles of 8 dims
+  static constexpr int kPlane = kKvBlock * D;        // bytes of a block's keys (and of its values)
+  static constexpr int kRing = kStages * 2 * kPlane;
 };
+
+// First dim of lane t's load `ld` of a key row: neighbouring lanes' loads lie kKL loads apart
+// where rows are whole 128-byte lines, so that even and odd rows meet in different banks.
+template <int D>
+__device__ __forceinline__ int key_dim(int t, int ld) {
+  constexpr int KB = Shape<D>::kKB;
+  if constexpr (D == 128 || D == 256) return (ld / 2) * 128 + (2 * t + ld % 2) * KB;
+  return (4 * ld + t) * KB;
+}
+// Byte offset of 16-byte chunk c of row r within a block's plane in shared memory.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (D == 128 || D == 256) return uint32_t(r * D + ((c ^ (r & 7)) * 16));
+  if constexpr (D == 64) {  // two rows to a 128-byte line
+    const int l = r >> 1, p = (r & 1) * 4 + c;
+    return uint32_t(l * 128 + ((p ^ ((l & 3) * 2)) * 16));
+  }
+  return uint32_t(r * D + c * 16);
+}
 
 // dim of accumulator column n (0..7) of tile j
 template <int D>
@@ -101,16 +131,40 @@ struct BlockAt {
   float lv;   // log2 of the value scale, at least -95 (a block of zeros has scale 0)
 };
 
-// One warp per block of 16 tokens at a time.
+// Four dims of one row, times inv, in the output's type.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 1) kv_attn_kernel(const AttnArgs a) {
+__device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int row, int d, float4 v, float inv) {
+  const int64_t e = int64_t(q0 + row / a.group) * a.out_stride + int64_t(h * a.group + row % a.group) * D + d;
+  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (a.type == QDQ_TYPE_F32)
+    store4(static_cast<float *>(a.out) + e, v);
+  else if (a.type == QDQ_TYPE_F16)
+    store4(static_cast<__half *>(a.out) + e, v);
+  else
+    store4(static_cast<__nv_bfloat16 *>(a.out) + e, v);
+}
+// M: the reference (log2 units), L: the sum of 2^(score - M)
+__device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int row, float M, float L) {
+  if (a.lse)
+    a.lse[int64_t(q0 + row / a.group) * a.n_heads + h * a.group + row % a.group] =
+        L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.
+template <int D, int PARTS>
+__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(const AttnArgs a) {
   using S = Shape<D>;
-  extern __shared__ uint8_t smem[];
-  uint4 *qf = reinterpret_cast<uint4 *>(smem);                           // [k step][lane] A fragments
-  float *s_acc = reinterpret_cast<float *>(smem + S::kKSteps * 512);     // [warp][row][D]
-  BlockAt *s_blk = reinterpret_cast<BlockAt *>(s_acc + kWarps * kRows * D);
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_w[kWarps][kRows], s_inv[kRows], s_qs[kRows];
+  constexpr int R = 16 / PARTS;  // rows of a tile
+  constexpr int NR = 2 / PARTS;  // rows per lane: g, and g + 8 with one part
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint4 *qf = reinterpret_cast<uint4 *>(smem);                         // [k step][lane] query fragments
+  uint8_t *ring = smem + S::kKSteps * 512;                             // [warp][stage] keys, values
+  float *s_acc = reinterpret_cast<float *>(ring);                      // at the end: [warp][row][D]
+  constexpr int kBody = kWarps * S::kRing > kWarps * R * D * 4 ? kWarps * S::kRing : kWarps * R * D * 4;
+  BlockAt *s_blk = reinterpret_cast<BlockAt *>(ring + kBody);
+  __shared__ float s_m[kWarps][R], s_l[kWarps][R], s_w[kWarps][R], s_inv[R], s_qs[R];
   __shared__ int s_last;
+  const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x % a.splits;
@@ -122,9 +176,9 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 1) kv_attn_kernel(
   const int q0 = a.cu_q ? int(ld_u1(a.cu_q + s)) : s;
   const int nq = a.cu_q ? int(ld_u1(a.cu_q + s + 1)) - q0 : 1;
   const int len = int(ld_u1(a.kv_len + s));
-  const int rows = nq * a.group, r0 = tile * kRows;
+  const int rows = nq * a.group, r0 = tile * R;
   if (r0 >= rows) return;
-  const int nr = min(kRows, rows - r0);
+  const int nr = min(R, rows - r0);
   const bool bad = len < 0 || len > a.max_kv_len || (len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
   const int pos_lo = len - nq + r0 / a.group, pos_hi = len - nq + (r0 + nr - 1) / a.group;
   const int b_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) / kKvBlock : 0;
@@ -134,24 +188,43 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 1) kv_attn_kernel(
   if (split >= nsplit) return;
   const int c0 = b_lo + split * a.split_blocks, cn = min(a.split_blocks, b_hi - c0);
 
-  // the blocks of this split: where they are and their scales
+  // where the blocks of this split are
   const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
   const int64_t vplane = int64_t(a.c.page_tokens) * D;
-  for (int i = threadIdx.x; i < cn; i += kWarps * 32) {
-    const int blk = c0 + i, t0 = blk * kKvBlock % a.c.page_tokens;
-    const int64_t at = kv_record_of(a.c, s, blk, h, rec);
-    BlockAt e;
-    e.k = at < 0 ? -1 : at + int64_t(t0) * D;
-    const uint8_t *sc = a.c.pages + (at < 0 ? 0 : at) + 2 * vplane + 4 * (t0 / kKvBlock);
-    e.ks = at < 0 ? __int_as_float(0x7fffffff) : __uint_as_float(ld_u1(sc));
-    const float vs = at < 0 ? 1.f : __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
-    e.lv = log2f(fmaxf(vs, 2.5243549e-29f));  // a NaN scale gives -95 here and stays NaN in vs
-    e.vs = vs * kPScale;
-    if (e.k < 0) e.k = 0;
-    s_blk[i] = e;
+  const int64_t at0 = kv_record_of(a.c, s, c0 + int(threadIdx.x) < b_hi ? c0 + int(threadIdx.x) : c0, h, rec);
+  const int t00 = (c0 + int(threadIdx.x)) * kKvBlock % a.c.page_tokens;
+  if (int(threadIdx.x) < cn) s_blk[threadIdx.x].k = at0 < 0 ? 0 : at0 + int64_t(t00) * D;
+  __syncthreads();
+
+  const uint32_t my_ring = smem_u32(ring) + warp * S::kRing;
+  auto fetch = [&](int i, int stage) {  // this warp's copies of block i
+    if (i < cn) {
+      const uint8_t *k = a.c.pages + s_blk[i].k;
+      const uint32_t dst = my_ring + stage * 2 * S::kPlane;
+      constexpr int CR = D / 16;  // chunks per row
+#pragma unroll
+      for (int j = 0; j < CR / 2; ++j) {  // 16 rows x CR chunks over 32 lanes
+        const int e = lane + 32 * j, r = e / CR, c = e % CR;
+        copy16(dst + chunk_at<D>(r, c), k + e * 16);
+        copy16(dst + S::kPlane + chunk_at<D>(r, c), k + vplane + e * 16);
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(warp + i * kWarps, i);
+
+  // the blocks' scales
+  if (int(threadIdx.x) < cn) {
+    const uint8_t *sc = a.c.pages + (at0 < 0 ? 0 : at0) + 2 * vplane + 4 * (t00 / kKvBlock);
+    const float ks = at0 < 0 ? qnan : __uint_as_float(ld_u1(sc));
+    const float vs = at0 < 0 ? 1.f : __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+    s_blk[threadIdx.x].ks = ks;
+    s_blk[threadIdx.x].vs = vs * kPScale;
+    s_blk[threadIdx.x].lv = log2f(fmaxf(vs, 2.5243549e-29f));  // a NaN scale gives -95 here and stays NaN in vs
   }
-  // the tile's queries: scaled by a power of two per row, then split into two f16 parts
-  for (int r = warp; r < kRows; r += kWarps) {
+  // the tile's queries: scaled by a power of two per row, then f16 parts
+  for (int r = warp; r < R; r += kWarps) {
     const int row = r0 + r;
     const bool in = r < nr;
     const int64_t base = in ? int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D : 0;
@@ -175,209 +248,263 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 1) kv_attn_kernel(
     int ex = 13 - (int(__float_as_uint(m) >> 23) - 127);
     ex = max(-120, min(120, ex));
     const float up = finite ? __uint_as_float(uint32_t(ex + 127) << 23) : 0.f;
-    if (lane == 0) s_qs[r] = finite ? __uint_as_float(uint32_t(127 - ex) << 23) : __int_as_float(0x7fffffff);
+    if (lane == 0) s_qs[r] = finite ? __uint_as_float(uint32_t(127 - ex) << 23) : qnan;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int d = lane + 32 * i;
       const float f = finite ? v[i] * up : 0.f;
-      const __half hi = __float2half_rn(f), lo = __float2half_rn(f - __half2float(hi));
-      // dim d is element (d % kKB) of lane t = d / kKB % 4 in load d / (4 kKB)
-      const int ld = d / (4 * S::kKB), tt = d / S::kKB % 4, e = d % S::kKB;
-      const int ks = ld * (S::kKB / 4) + e / 4, el = e % 4;
-      __half *f16 = reinterpret_cast<__half *>(qf + ks * 32 + r * 4 + tt);
-      f16[(el >> 1) * 4 + (el & 1)] = hi;      // registers 0, 2: rows 0-7
-      f16[(el >> 1) * 4 + 2 + (el & 1)] = lo;  // registers 1, 3: rows 8-15
+      const __half hi = __float2half_rn(f);
+      int ld, tt;  // the load and the lane that bring dim d
+      if constexpr (D == 128 || D == 256) {
+        const int c = d / 16;
+        ld = (c / 8) * 2 + (c & 1);
+        tt = (c % 8) / 2;
+      } else {
+        ld = d / (4 * S::kKB);
+        tt = d / S::kKB % 4;
+      }
+      const int e = d % S::kKB, ks = ld * (S::kKB / 4) + e / 4, el = e % 4;
+      __half *f16 = reinterpret_cast<__half *>(qf + ks * 32 + (r & 7) * 4 + tt) + (el >> 1) * 4 + (el & 1);
+      if constexpr (PARTS == 2) {
+        f16[0] = hi;                                       // registers 0, 2: rows 0-7
+        f16[2] = __float2half_rn(f - __half2float(hi));  // registers 1, 3: rows 8-15
+      } else {
+        f16[r >= 8 ? 2 : 0] = hi;
+      }
     }
   }
   __syncthreads();
 
-  const int row = r0 + g;  // this lane's row
-  const int pos = len - nq + row / a.group;
-  const float qs = s_qs[g] * a.scale;
-  const float slope = a.slopes && g < nr ? __ldg(a.slopes + h * a.group + row % a.group) * kLog2e : 0.f;
-  const int lo_pos = a.window > 0 ? pos - a.window + 1 : 0;
+  int pos[NR], lo_pos[NR];
+  float qs[NR], slope[NR], m[NR], l[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int lr = g + 8 * r, row = r0 + lr;
+    pos[r] = len - nq + row / a.group;
+    lo_pos[r] = a.window > 0 ? pos[r] - a.window + 1 : 0;
+    qs[r] = s_qs[lr] * a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
+    slope[r] = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row % a.group) * kLog2e : 0.f;
+    m[r] = ninf;
+    l[r] = 0.f;
+  }
+  // blocks in [full_lo, full_hi) are visible to every row of the tile
+  const int full_lo = a.window > 0 ? max(0, pos_hi - a.window + 1 + kKvBlock - 1) / kKvBlock : 0;
+  const int full_hi = (pos_lo + 1) / kKvBlock;
 
   float acc[S::kNT][4];
 #pragma unroll
   for (int j = 0; j < S::kNT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-  float m = -__int_as_float(0x7f800000), l = 0.f;
 
-  uint32_t kw[S::kWords], vw[S::kWords];
-  auto load_k = [&](int i) {
-    const uint8_t *p = a.c.pages + s_blk[i].k + int64_t(g) * D + t * S::kKB;
+  // fragment addresses within a stage
+  uint32_t ka[S::kKL], va[4];  // a row's 8 rows down and the other chunks are fixed distances where nothing is exchanged
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int c = 0; c < S::kKL; ++c)
-        load_words<S::kKB>(p + j * 8 * D + c * 4 * S::kKB, kw + (j * S::kKL + c) * (S::kKB / 4));
-  };
-  auto load_v = [&](int i) {
-    const uint8_t *p = a.c.pages + s_blk[i].k + vplane + int64_t(2 * t) * D + g * S::kVB;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-      for (int c = 0; c < S::kVL; ++c)
-        load_words<S::kVB>(p + ((r & 1) + 8 * (r >> 1)) * D + c * 8 * S::kVB, vw + (r * S::kVL + c) * (S::kVB / 4));
-  };
-  if (warp < cn) {
-    load_k(warp);
-    load_v(warp);
+  for (int c = 0; c < S::kKL; ++c) {
+    const int d = key_dim<D>(t, c);
+    ka[c] = my_ring + chunk_at<D>(g, d / 16) + d % 16;
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int d = g * S::kVB;
+    va[r] = my_ring + S::kPlane + chunk_at<D>(2 * t + (r & 1) + 8 * (r >> 1), d / 16) + d % 16;
+  }
+
+  int stage = 0;
   for (int i = warp; i < cn; i += kWarps) {
-    const float ks = s_blk[i].ks, vs = s_blk[i].vs, lv = s_blk[i].lv;
+    copies_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies of this block are in, and the stage refilled next is free
+    fetch(i + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    const uint32_t so = stage * 2 * S::kPlane;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     // scores: two tiles of 8 tokens
     float sc[2][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
 #pragma unroll
-      for (int k = 0; k < S::kKSteps; ++k) {
-        const uint32_t u = kw[j * S::kKSteps + k] ^ 0x80808080u;
-        mma_f16(sc[j], qf[k * 32 + lane], codes_f16<0x4140>(u), codes_f16<0x4342>(u));
+    for (int c = 0; c < S::kKL; ++c) {
+      uint32_t w[2][4];
+      lds_words<S::kKB>(ka[c] + so, w[0]);
+      lds_words<S::kKB>(ka[c] + so + 8 * D, w[1]);
+#pragma unroll
+      for (int k = 0; k < S::kKB / 4; ++k) {
+        const uint4 q = qf[(c * (S::kKB / 4) + k) * 32 + lane];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t u = w[j][k] ^ 0x80808080u;
+          mma_f16(sc[j], q, codes_f16<0x4140>(u), codes_f16<0x4342>(u));
+        }
       }
     }
-    if (i + kWarps < cn) load_k(i + kWarps);
-    float p[4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the block
-    const float f = qs * ks;
+    const float ks = s_blk[i].ks, vs = s_blk[i].vs, lv = s_blk[i].lv;
+    const int blk = c0 + i;
+    const bool whole = blk >= full_lo && blk < full_hi;
+    float p[NR][4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the block
+    float mx[NR];
+    bool grow = false;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = (sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)]) * f;
-    if (a.softcap > 0.f) {
+    for (int r = 0; r < NR; ++r) {
+      const float f = qs[r] * ks;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = a.softcap * tanhf(p[e] / a.softcap);
+      for (int e = 0; e < 4; ++e)
+        p[r][e] = (PARTS == 2 ? sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)] : sc[e >> 1][2 * r + (e & 1)]) * f;
+      if (a.softcap > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[r][e] = a.softcap * kLog2e * tanhf(p[r][e] / a.softcap);
+      }
+      const int j0 = blk * kKvBlock + 2 * t;
+      if (a.slopes) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[r][e] = fmaf(-slope[r], float(pos[r] - (j0 + (e & 1) + 8 * (e >> 1))), p[r][e]);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + (e & 1) + 8 * (e >> 1);
+          if (j > pos[r] || j < lo_pos[r]) p[r][e] = ninf;
+        }
+      }
+      mx[r] = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
     }
-    const int j0 = (c0 + i) * kKvBlock + 2 * t;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = j0 + (e & 1) + 8 * (e >> 1);
-      p[e] *= kLog2e;
-      if (a.slopes) p[e] = fmaf(-slope, float(pos - j), p[e]);
-      if (j > pos || j < lo_pos) p[e] = -__int_as_float(0x7f800000);
+    for (int r = 0; r < NR; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      // the reference is the row's largest score plus log2 of its value scale: then p * vs is at
+      // most 1 (2^kLazy while the reference is behind), so its f16 parts keep their precision
+      // however far the blocks' scales lie apart
+      mx[r] += lv;
+      grow |= mx[r] > m[r] + (m[r] == ninf ? 0.f : kLazy);
     }
-    float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // the reference is the row's largest score plus log2 of its value scale: then p * vs is at
-    // most 1, so its f16 parts keep their precision however far the blocks' scales lie apart
-    const float m_new = fmaxf(m, mx + lv);
-    const bool grow = m_new > m;
     if (__any_sync(0xffffffffu, grow)) {
-      const float corr = grow ? exp2f(m - m_new) : 1.f;  // 0 from -inf
-      l *= corr;
-      m = m_new;
+      float corr[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float m_new = fmaxf(m[r], mx[r]);
+        corr[r] = m_new > m[r] ? ex2(m[r] - m_new) : 1.f;  // 0 from -inf
+        l[r] *= corr[r];
+        m[r] = m_new;
+      }
 #pragma unroll
       for (int j = 0; j < S::kNT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] *= corr;
-    }
-    const float mref = m == -__int_as_float(0x7f800000) ? 0.f : m;
-    float pv[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool seen = p[e] != -__int_as_float(0x7f800000);
-      p[e] = exp2f(p[e] - mref);
-      l += p[e];
-      pv[e] = seen ? p[e] * vs : 0.f;  // a hidden token's scale may be NaN
+        for (int e = 0; e < 4; ++e) acc[j][e] *= corr[PARTS == 2 ? 0 : e >> 1];
     }
     uint4 pa;
     {
-      const __half2 h01 = __floats2half2_rn(pv[0], pv[1]), h23 = __floats2half2_rn(pv[2], pv[3]);
-      const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
-      const __half2 l01 = __floats2half2_rn(pv[0] - f01.x, pv[1] - f01.y), l23 = __floats2half2_rn(pv[2] - f23.x, pv[3] - f23.y);
+      float pv[NR][4];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float mref = m[r] == ninf ? 0.f : m[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = ex2(p[r][e] - mref);
+          l[r] += x;
+          pv[r][e] = x * vs;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (p[r][e] == ninf) pv[r][e] = 0.f;  // a hidden token's scale may be NaN
+        }
+      }
+      const __half2 h01 = __floats2half2_rn(pv[0][0], pv[0][1]), h23 = __floats2half2_rn(pv[0][2], pv[0][3]);
+      __half2 l01, l23;
+      if constexpr (PARTS == 2) {
+        const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+        l01 = __floats2half2_rn(pv[0][0] - f01.x, pv[0][1] - f01.y);
+        l23 = __floats2half2_rn(pv[0][2] - f23.x, pv[0][3] - f23.y);
+      } else {
+        l01 = __floats2half2_rn(pv[NR - 1][0], pv[NR - 1][1]);
+        l23 = __floats2half2_rn(pv[NR - 1][2], pv[NR - 1][3]);
+      }
       pa.x = *reinterpret_cast<const uint32_t *>(&h01);
       pa.y = *reinterpret_cast<const uint32_t *>(&l01);
       pa.z = *reinterpret_cast<const uint32_t *>(&h23);
       pa.w = *reinterpret_cast<const uint32_t *>(&l23);
     }
     // values: words of 4 dims of the four tokens, re-paired by token
-    constexpr int VW = S::kVL * (S::kVB / 4);  // words per token
 #pragma unroll
-    for (int c = 0; c < VW; ++c) {
-      const uint32_t u0 = vw[c] ^ 0x80808080u, u1 = vw[VW + c] ^ 0x80808080u;
-      const uint32_t u2 = vw[2 * VW + c] ^ 0x80808080u, u3 = vw[3 * VW + c] ^ 0x80808080u;
-      const uint32_t a01 = __byte_perm(u0, u1, 0x5140), b01 = __byte_perm(u0, u1, 0x7362);
-      const uint32_t a23 = __byte_perm(u2, u3, 0x5140), b23 = __byte_perm(u2, u3, 0x7362);
-      mma_f16(acc[4 * c + 0], pa, codes_f16<0x4140>(a01), codes_f16<0x4140>(a23));
-      mma_f16(acc[4 * c + 1], pa, codes_f16<0x4342>(a01), codes_f16<0x4342>(a23));
-      mma_f16(acc[4 * c + 2], pa, codes_f16<0x4140>(b01), codes_f16<0x4140>(b23));
-      mma_f16(acc[4 * c + 3], pa, codes_f16<0x4342>(b01), codes_f16<0x4342>(b23));
+    for (int c = 0; c < S::kVL; ++c) {
+      uint32_t w[4][S::kVB / 4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) lds_words<S::kVB>(va[r] + so + c * 8 * S::kVB, w[r]);
+#pragma unroll
+      for (int k = 0; k < S::kVB / 4; ++k) {
+        const uint32_t u0 = w[0][k] ^ 0x80808080u, u1 = w[1][k] ^ 0x80808080u;
+        const uint32_t u2 = w[2][k] ^ 0x80808080u, u3 = w[3][k] ^ 0x80808080u;
+        const uint32_t a01 = __byte_perm(u0, u1, 0x5140), b01 = __byte_perm(u0, u1, 0x7362);
+        const uint32_t a23 = __byte_perm(u2, u3, 0x5140), b23 = __byte_perm(u2, u3, 0x7362);
+        float(*o)[4] = acc + c * S::kVB + 4 * k;
+        mma_f16(o[0], pa, codes_f16<0x4140>(a01), codes_f16<0x4140>(a23));
+        mma_f16(o[1], pa, codes_f16<0x4342>(a01), codes_f16<0x4342>(a23));
+        mma_f16(o[2], pa, codes_f16<0x4140>(b01), codes_f16<0x4140>(b23));
+        mma_f16(o[3], pa, codes_f16<0x4342>(b01), codes_f16<0x4342>(b23));
+      }
     }
-    if (i + kWarps < cn) load_v(i + kWarps);
   }
+  copies_wait<0>();
+  __syncthreads();  // every warp is done with its ring, which becomes s_acc
 
   // join the four warps
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-  if (t == 0) {
-    s_m[warp][g] = m;
-    s_l[warp][g] = l;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if (t == 0) {
+      s_m[warp][g + 8 * r] = m[r];
+      s_l[warp][g + 8 * r] = l[r];
+    }
+    float *mine = s_acc + (warp * R + g + 8 * r) * D;
+#pragma unroll
+    for (int j = 0; j < S::kNT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        mine[dim_of<D>(j, 2 * t + e)] = PARTS == 2 ? acc[j][e] + acc[j][e + 2] : acc[j][2 * r + e];
   }
-  float *mine = s_acc + (warp * kRows + g) * D;
-#pragma unroll
-  for (int j = 0; j < S::kNT; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) mine[dim_of<D>(j, 2 * t + e)] = acc[j][e] + acc[j][e + 2];
   __syncthreads();
-  if (threadIdx.x < kRows) {
+  if (threadIdx.x < R) {
     const int r = threadIdx.x;
-    float M = -__int_as_float(0x7f800000), L = 0.f;
+    float M = ninf, L = 0.f;
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
-    const float ref = M == -__int_as_float(0x7f800000) ? 0.f : M;
+    const float ref = M == ninf ? 0.f : M;
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(s_m[w][r] - ref);
+      const float f = ex2(s_m[w][r] - ref);
       L = fmaf(s_l[w][r], f, L);
       s_w[w][r] = f / kPScale;
     }
-    if (bad) L = __int_as_float(0x7fffffff);
+    if (bad) L = qnan;
     s_m[0][r] = M;
     s_l[0][r] = L;
   }
   __syncthreads();
 
-  auto finish = [&](int r, int d, float4 v, float inv) {  // four dims of one row
-    const int rw = r0 + r;
-    const int64_t e = int64_t(q0 + rw / a.group) * a.out_stride + int64_t(h * a.group + rw % a.group) * D + d;
-    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-    if (a.type == QDQ_TYPE_F32)
-      store4(static_cast<float *>(a.out) + e, v);
-    else if (a.type == QDQ_TYPE_F16)
-      store4(static_cast<__half *>(a.out) + e, v);
-    else
-      store4(static_cast<__nv_bfloat16 *>(a.out) + e, v);
-  };
-  auto write_lse = [&](int r, float M, float L) {
-    const int rw = r0 + r;
-    if (a.lse)
-      a.lse[int64_t(q0 + rw / a.group) * a.n_heads + h * a.group + rw % a.group] =
-          L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
-  };
-
-  float *part = a.partial + (int64_t(unit) * a.splits + split) * (kRows * (D + 2));
+  float *part = a.partial + (int64_t(unit) * a.splits + split) * (R * (D + 2));
   for (int i = threadIdx.x; i < nr * (D / 4); i += kWarps * 32) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float4 x = *reinterpret_cast<const float4 *>(s_acc + (w * kRows + r) * D + d);
+      const float4 x = *reinterpret_cast<const float4 *>(s_acc + (w * R + r) * D + d);
       const float f = s_w[w][r];
       v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
     }
     if (nsplit == 1) {
       const float L = s_l[0][r];
-      finish(r, d, v, L == 0.f ? 0.f : 1.f / L);
+      store_out<D>(a, q0, h, r0 + r, d, v, L == 0.f ? 0.f : 1.f / L);
     } else {
       *reinterpret_cast<float4 *>(part + r * D + d) = v;
     }
   }
   if (nsplit == 1) {
-    if (threadIdx.x < nr) write_lse(threadIdx.x, s_m[0][threadIdx.x], s_l[0][threadIdx.x]);
+    if (int(threadIdx.x) < nr) store_lse(a, q0, h, r0 + threadIdx.x, s_m[0][threadIdx.x], s_l[0][threadIdx.x]);
     return;
   }
-  if (threadIdx.x < nr) {
-    part[kRows * D + threadIdx.x] = s_m[0][threadIdx.x];
-    part[kRows * D + kRows + threadIdx.x] = s_l[0][threadIdx.x];
+  if (int(threadIdx.x) < nr) {
+    part[R * D + threadIdx.x] = s_m[0][threadIdx.x];
+    part[R * D + R + threadIdx.x] = s_l[0][threadIdx.x];
   }
   // the CTA that finishes last joins the splits, in split order; the ticket wraps to 0 for the next call
   __threadfence();
@@ -386,36 +513,37 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 1) kv_attn_kernel(
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  const float *all = a.partial + int64_t(unit) * a.splits * (kRows * (D + 2));
-  const int step = kRows * (D + 2);
-  if (threadIdx.x < nr) {
+  const int step = R * (D + 2);
+  const float *all = a.partial + int64_t(unit) * a.splits * step;
+  if (int(threadIdx.x) < nr) {
     const int r = threadIdx.x;
-    float M = -__int_as_float(0x7f800000), L = 0.f;
-    for (int i = 0; i < nsplit; ++i) M = fmaxf(M, __ldcg(all + i * step + kRows * D + r));
-    const float ref = M == -__int_as_float(0x7f800000) ? 0.f : M;
+    float M = ninf, L = 0.f;
+    for (int i = 0; i < nsplit; ++i) M = fmaxf(M, __ldcg(all + i * step + R * D + r));
+    const float ref = M == ninf ? 0.f : M;
     for (int i = 0; i < nsplit; ++i)
-      L = fmaf(__ldcg(all + i * step + kRows * D + kRows + r), exp2f(__ldcg(all + i * step + kRows * D + r) - ref), L);
+      L = fmaf(__ldcg(all + i * step + R * D + R + r), ex2(__ldcg(all + i * step + R * D + r) - ref), L);
     s_m[0][r] = ref;
     s_inv[r] = L == 0.f ? 0.f : 1.f / L;
-    write_lse(r, M, L);
+    store_lse(a, q0, h, r0 + r, M, L);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < nr * (D / 4); i += kWarps * 32) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < nsplit; ++k) {
       const float4 x = __ldcg(reinterpret_cast<const float4 *>(all + k * step + r * D + d));
-      const float f = exp2f(__ldcg(all + k * step + kRows * D + r) - s_m[0][r]);
+      const float f = ex2(__ldcg(all + k * step + R * D + r) - s_m[0][r]);
       v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
     }
-    finish(r, d, v, s_inv[r]);
+    store_out<D>(a, q0, h, r0 + r, d, v, s_inv[r]);
   }
 }
 
-template <int D>
+template <int D, int PARTS>
 size_t attn_smem() {
-  return Shape<D>::kKSteps * 512 + size_t(kWarps) * kRows * D * 4 + size_t(kMaxSplitBlocks) * sizeof(BlockAt);
+  const size_t ring = size_t(kWarps) * Shape<D>::kRing, acc = size_t(kWarps) * (16 / PARTS) * D * 4;
+  return Shape<D>::kKSteps * 512 + (ring > acc ? ring : acc) + size_t(kMaxSplitBlocks) * sizeof(BlockAt);
 }
 
 template <typename F>
@@ -430,26 +558,32 @@ int with_dim(int d, F &&f) {
 }
 
 struct Plan {
-  int tiles, splits, split_blocks;
+  int parts, tiles, splits, split_blocks;
   int64_t units;
   size_t ticket_bytes, bytes;
 };
 
-Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim) {
+Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, int type) {
   Plan p{};
-  p.tiles = int((int64_t(max_q) * (n_heads / n_kv) + kRows - 1) / kRows);
+  const int64_t rows = int64_t(max_q) * (n_heads / n_kv);
+  p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
+  const int R = 16 / p.parts;
+  p.tiles = int((rows + R - 1) / R);
   p.units = int64_t(n_seqs) * n_kv * p.tiles;
   const int64_t blocks = (int64_t(max_kv_len) + kKvBlock - 1) / kKvBlock;
-  // enough CTAs for a few waves of three per SM, but no fewer than two blocks per warp and split
-  const int64_t want = int64_t(di.sm_count) * 3 * 2;
-  int64_t per = blocks * p.units / (want > 0 ? want : 1);
+  // whole waves of resident CTAs (two of them, so that sequences of different lengths even
+  // out), but no fewer than two blocks per warp and split
+  const int64_t want = int64_t(di.sm_count) * (head_dim <= 128 ? 4 : 2) * (n_seqs > 1 ? 2 : 1);
+  int64_t splits = want / (p.units > 0 ? p.units : 1);
+  if (splits < 1) splits = 1;
+  int64_t per = (blocks + splits - 1) / splits;
   if (per < 2 * kWarps) per = 2 * kWarps;
   if (per > kMaxSplitBlocks) per = kMaxSplitBlocks;
   p.split_blocks = int(per);
   p.splits = int((blocks + per - 1) / per);
   if (p.splits < 1) p.splits = 1;
   p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
-  p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * kRows * (head_dim + 2) * 4 : 0);
+  p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * R * (head_dim + 2) * 4 : 0);
   return p;
 }
 
@@ -458,7 +592,12 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
 size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return 0;
-  return plan(di, n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim).bytes;
+  size_t most = 0;  // enough for every element type
+  for (int type : {QDQ_TYPE_F32, QDQ_TYPE_BF16}) {
+    const size_t b = plan(di, n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, type).bytes;
+    if (b > most) most = b;
+  }
+  return most;
 }
 
 int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, int n_seqs, int max_q,
@@ -468,7 +607,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
-  const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim);
+  const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, type);
   if (p.units * p.splits > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
   AttnArgs a{};
   a.c = c;
@@ -495,10 +634,12 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.softcap = softcap;
   e = cudaError_t(with_dim(head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    const size_t sm = attn_smem<D>();
-    const cudaError_t r = allow_dynamic_smem(reinterpret_cast<const void *>(kv_attn_kernel<D>), int(sm));
-    if (r != cudaSuccess) return int(r);
-    return int(launch(kv_attn_kernel<D>, dim3(unsigned(p.units * p.splits)), dim3(kWarps * 32), sm, s, a));
+    auto run = [&](auto kernel, size_t sm) {
+      const cudaError_t r = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(sm));
+      if (r != cudaSuccess) return int(r);
+      return int(launch(kernel, dim3(unsigned(p.units * p.splits)), dim3(kWarps * 32), sm, s, a));
+    };
+    return p.parts == 2 ? run(kv_attn_kernel<D, 2>, attn_smem<D, 2>()) : run(kv_attn_kernel<D, 1>, attn_smem<D, 1>());
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }

@@ -10,7 +10,9 @@ Bounds (u = 2^-24, the f32 unit roundoff; e = the output type's: 2^-24, 2^-11, 2
   are off by a relative 2 d + 2^-20 before and after normalisation, and the sums over tokens by 2^-18;
   the f16 parts of a probability times its value scale end at 2^-39 of the row's largest such product
   (z = max p s, a code is at most 127, and the tokens of a sum share the row's total of p):
-  |o - o_ref| <= (2 d + 2^-17) sum p|v| + 2^-39 127 n z + e |o_ref|,  |lse - ref| <= d + 2^-18 + 2^-22 |lse|.
+  |o - o_ref| <= (2 d + 2^-17) sum p|v| + 2^-39 127 n z + e |o_ref|,  |lse - ref| <= d + 2^-18 + 2^-22 |lse|;
+  with 16-bit activations the probabilities are rounded to f16 once where a tile has more than 8
+  rows: + 2^-11 sum p|v|.
 * log probabilities: the running sum of a thread has at most n / 256 + 64 additions and an exponent
   is off by 2^-22 (|x| + 1): |lp - ref| <= t with t = (n / 256 + 64) u + 2^-21 (max |x| + 1), the entropy
   by t (4 + 2 H).
@@ -314,7 +316,7 @@ def _check_attention(c, table, lens, nq, q, out, lse, dtype, scale, softcap, win
                                       None if slopes is None else _np(slopes))
         d = 2.0 ** -18 * mag + 2.0 ** -20 * (1 + softcap)
         tiny = 2.0 ** -25 if dtype == "f16" else 0
-        _within(on[cu[s]:cu[s + 1]], o, ((2 * d + 2.0 ** -17)[..., None] * av + EPS[dtype] * np.abs(o) + tiny
+        _within(on[cu[s]:cu[s + 1]], o, ((2 * d + 2.0 ** -17 + (0 if dtype == "f32" else 2.0 ** -11))[..., None] * av + EPS[dtype] * np.abs(o) + tiny
                                              + 2.0 ** -39 * n * z[..., None]))
         with np.errstate(invalid="ignore"):
             _within(ln[cu[s]:cu[s + 1]], l, d + 2.0 ** -18 + 2.0 ** -22 * np.abs(np.where(np.isinf(l), 0, l)))
