@@ -29,6 +29,7 @@ QDQ_MAX_TOPK = 64
 QDQ_MAX_GEMV_N_IN = 32768
 QDQ_MAX_NORM_N = 32768
 QDQ_KV_BLOCK = 16
+QDQ_MAX_KV_LEN = 4194304
 QDQ_TYPE_F32 = 0
 QDQ_TYPE_F16 = 1
 QDQ_TYPE_BF16 = 2

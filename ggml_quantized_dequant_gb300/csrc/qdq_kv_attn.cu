@@ -26,10 +26,13 @@
 namespace qdq {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kStages = 3;       // blocks in a warp's ring
 constexpr float kLazy = 1.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
-constexpr int kMaxSplitBlocks = 128;
+// Splits of one tile (the joining CTA keeps their maxima and sums in shared memory), and blocks
+// of 16 tokens in one split.
+constexpr int max_splits(int warps) { return warps > 4 ? 512 : 64; }
+constexpr int max_split_blocks(int warps) { return warps > 4 ? 512 : 128; }
+static_assert(int64_t(max_splits(8)) * max_split_blocks(8) * kKvBlock == QDQ_MAX_KV_LEN, "the longest cache");
 constexpr float kPScale = 16384.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -125,11 +128,27 @@ __device__ __forceinline__ int dim_of(int j, int n) {
   return (j / VB) * 8 * VB + n * VB + j % VB;
 }
 
+// A block of the split.
 struct BlockAt {
-  int64_t k;  // byte offset of the block's first key code, -1 when it has no page
+  int64_t k;  // byte offset of its first key code
   float ks, vs;
   float lv;   // log2 of the value scale, at least -95 (a block of zeros has scale 0)
 };
+
+// Bytes of the rings, which the warps' accumulators and the join of the splits use afterwards
+// (a maximum and a sum per split and row, and a float4 per thread).
+template <int D, int PARTS, int W>
+constexpr int body_bytes() {
+  constexpr int ring = W * Shape<D>::kRing, acc = W * (16 / PARTS) * D * 4;
+  constexpr int join = 2 * max_splits(W) * (16 / PARTS) * 4 + W * 32 * 16;
+  static_assert(join <= (ring > acc ? ring : acc), "room for the join");
+  return ring > acc ? ring : acc;
+}
+
+// Place of four dims (quad c) in a row of accumulators in shared memory: exchanged so that the
+// lanes of one store, which hold dims 32 or 16 apart of rows a whole number of lines apart, meet
+// in different banks (unexchanged, a one-token call took 1.5 us longer).
+__device__ __forceinline__ int quad_at(int row, int c) { return c ^ (((c >> 3) & 3) | ((row & 1) << 2)); }
 
 // Four dims of one row, times inv, in the output's type.
 template <int D>
@@ -150,9 +169,10 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int 
         L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.
-template <int D, int PARTS>
-__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(const AttnArgs a) {
+// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.  W warps.
+template <int D, int PARTS, int W>
+__global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kernel(const AttnArgs a) {
+  constexpr int kThreads = W * 32;
   using S = Shape<D>;
   constexpr int R = 16 / PARTS;  // rows of a tile
   constexpr int NR = 2 / PARTS;  // rows per lane: g, and g + 8 with one part
@@ -160,9 +180,9 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
   uint4 *qf = reinterpret_cast<uint4 *>(smem);                         // [k step][lane] query fragments
   uint8_t *ring = smem + S::kKSteps * 512;                             // [warp][stage] keys, values
   float *s_acc = reinterpret_cast<float *>(ring);                      // at the end: [warp][row][D]
-  constexpr int kBody = kWarps * S::kRing > kWarps * R * D * 4 ? kWarps * S::kRing : kWarps * R * D * 4;
+  constexpr int kBody = body_bytes<D, PARTS, W>();
   BlockAt *s_blk = reinterpret_cast<BlockAt *>(ring + kBody);
-  __shared__ float s_m[kWarps][R], s_l[kWarps][R], s_w[kWarps][R], s_inv[R], s_qs[R];
+  __shared__ float s_m[W][R], s_l[W][R], s_w[W][R], s_inv[R], s_qs[R];
   __shared__ int s_last;
   const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
 
@@ -191,9 +211,12 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
   // where the blocks of this split are
   const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
   const int64_t vplane = int64_t(a.c.page_tokens) * D;
-  const int64_t at0 = kv_record_of(a.c, s, c0 + int(threadIdx.x) < b_hi ? c0 + int(threadIdx.x) : c0, h, rec);
-  const int t00 = (c0 + int(threadIdx.x)) * kKvBlock % a.c.page_tokens;
-  if (int(threadIdx.x) < cn) s_blk[threadIdx.x].k = at0 < 0 ? 0 : at0 + int64_t(t00) * D;
+  for (int i = threadIdx.x; i < cn; i += kThreads) {
+    const int blk = c0 + i, t0 = blk % (a.c.page_tokens / kKvBlock) * kKvBlock;
+    const int64_t at = kv_record_of(a.c, s, blk, h, rec);
+    s_blk[i].k = (at < 0 ? 0 : at) + int64_t(t0) * D;
+    s_blk[i].ks = at < 0 ? qnan : 0.f;  // without a page: any valid place, and marked
+  }
   __syncthreads();
 
   const uint32_t my_ring = smem_u32(ring) + warp * S::kRing;
@@ -212,35 +235,43 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
     copies_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(warp + i * kWarps, i);
+  for (int i = 0; i < kStages - 1; ++i) fetch(warp + i * W, i);
 
-  // the blocks' scales
-  if (int(threadIdx.x) < cn) {
-    const uint8_t *sc = a.c.pages + (at0 < 0 ? 0 : at0) + 2 * vplane + 4 * (t00 / kKvBlock);
-    const float ks = at0 < 0 ? qnan : __uint_as_float(ld_u1(sc));
-    const float vs = at0 < 0 ? 1.f : __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
-    s_blk[threadIdx.x].ks = ks;
-    s_blk[threadIdx.x].vs = vs * kPScale;
-    s_blk[threadIdx.x].lv = log2f(fmaxf(vs, 2.5243549e-29f));  // a NaN scale gives -95 here and stays NaN in vs
+  // the queries' loads, then the blocks' scales, all in flight together
+  constexpr int QR = (R + W - 1) / W;  // rows per warp
+  float qv[QR][D / 32];
+#pragma unroll
+  for (int i = 0; i < QR; ++i) {
+    const int r = warp + i * W, row = r0 + r;
+    const bool in = r < nr;
+    const int64_t base = in ? int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D + lane : 0;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      qv[i][j] = 0.f;
+      if (in)
+        qv[i][j] = a.type == QDQ_TYPE_F32   ? load1(static_cast<const float *>(a.q) + base + 32 * j)
+                   : a.type == QDQ_TYPE_F16 ? load1(static_cast<const __half *>(a.q) + base + 32 * j)
+                                            : load1(static_cast<const __nv_bfloat16 *>(a.q) + base + 32 * j);
+    }
+  }
+  for (int i = threadIdx.x; i < cn; i += kThreads) {
+    const int b = (c0 + i) % (a.c.page_tokens / kKvBlock);  // of its page
+    const uint8_t *sc = a.c.pages + (s_blk[i].k - int64_t(b) * S::kPlane + 2 * vplane + 4 * b);
+    const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+    const bool none = s_blk[i].ks != 0.f;  // no page: NaN scores
+    s_blk[i].lv = log2f(fmaxf(none ? 1.f : vs, 2.5243549e-29f));  // a NaN scale gives -95 here and stays NaN in vs
+    s_blk[i].vs = none ? 1.f : vs * kPScale;
+    if (!none) s_blk[i].ks = ks;
   }
   // the tile's queries: scaled by a power of two per row, then f16 parts
-  for (int r = warp; r < R; r += kWarps) {
-    const int row = r0 + r;
-    const bool in = r < nr;
-    const int64_t base = in ? int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D : 0;
-    float v[D / 32];
+#pragma unroll
+  for (int qi = 0; qi < QR; ++qi) {
+    const int r = warp + qi * W;
+    if (r >= R) break;
+    const float(&v)[D / 32] = qv[qi];
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      v[i] = 0.f;
-      if (in) {
-        const int64_t e = base + lane + 32 * i;
-        v[i] = a.type == QDQ_TYPE_F32   ? load1(static_cast<const float *>(a.q) + e)
-               : a.type == QDQ_TYPE_F16 ? load1(static_cast<const __half *>(a.q) + e)
-                                        : load1(static_cast<const __nv_bfloat16 *>(a.q) + e);
-      }
-      m = max_abs_bits(m, v[i]);
-    }
+    for (int i = 0; i < D / 32; ++i) m = max_abs_bits(m, v[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
     const bool finite = m < __int_as_float(0x7f800000);
@@ -311,10 +342,10 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
   }
 
   int stage = 0;
-  for (int i = warp; i < cn; i += kWarps) {
+  for (int i = warp; i < cn; i += W) {
     copies_wait<kStages - 2>();
     __syncwarp();  // every lane's copies of this block are in, and the stage refilled next is free
-    fetch(i + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    fetch(i + (kStages - 1) * W, stage == 0 ? kStages - 1 : stage - 1);
     const uint32_t so = stage * 2 * S::kPlane;
     stage = stage == kStages - 1 ? 0 : stage + 1;
     // scores: two tiles of 8 tokens
@@ -448,7 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
   copies_wait<0>();
   __syncthreads();  // every warp is done with its ring, which becomes s_acc
 
-  // join the four warps
+  // join the warps
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -457,20 +488,22 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
       s_m[warp][g + 8 * r] = m[r];
       s_l[warp][g + 8 * r] = l[r];
     }
-    float *mine = s_acc + (warp * R + g + 8 * r) * D;
+    float4 *mine = reinterpret_cast<float4 *>(s_acc + (warp * R + g + 8 * r) * D);
 #pragma unroll
-    for (int j = 0; j < S::kNT; ++j)
+    for (int j = 0; j < S::kNT; j += 4)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        mine[dim_of<D>(j, 2 * t + e)] = PARTS == 2 ? acc[j][e] + acc[j][e + 2] : acc[j][2 * r + e];
+      for (int e = 0; e < 2; ++e) {
+        auto v = [&](int i) { return PARTS == 2 ? acc[j + i][e] + acc[j + i][e + 2] : acc[j + i][2 * r + e]; };
+        mine[quad_at(g, dim_of<D>(j, 2 * t + e) / 4)] = make_float4(v(0), v(1), v(2), v(3));
+      }
   }
   __syncthreads();
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
     float M = ninf, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w][r]);
     const float ref = M == ninf ? 0.f : M;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = ex2(s_m[w][r] - ref);
       L = fmaf(s_l[w][r], f, L);
       s_w[w][r] = f / kPScale;
@@ -482,12 +515,12 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
   __syncthreads();
 
   float *part = a.partial + (int64_t(unit) * a.splits + split) * (R * (D + 2));
-  for (int i = threadIdx.x; i < nr * (D / 4); i += kWarps * 32) {
+  for (int i = threadIdx.x; i < nr * (D / 4); i += kThreads) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 x = *reinterpret_cast<const float4 *>(s_acc + (w * R + r) * D + d);
+    for (int w = 0; w < W; ++w) {
+      const float4 x = reinterpret_cast<const float4 *>(s_acc + (w * R + r) * D)[quad_at(r, d / 4)];
       const float f = s_w[w][r];
       v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
     }
@@ -513,37 +546,68 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2) kv_attn_kernel(
   __syncthreads();
   if (!s_last) return;
   __threadfence();
+  // maxima and sums into shared memory, weights from them, then the accumulators: thread
+  // (k, item) adds every KG-th split's four dims of one row, the KG sums are added in order
   const int step = R * (D + 2);
   const float *all = a.partial + int64_t(unit) * a.splits * step;
-  if (int(threadIdx.x) < nr) {
-    const int r = threadIdx.x;
-    float M = ninf, L = 0.f;
-    for (int i = 0; i < nsplit; ++i) M = fmaxf(M, __ldcg(all + i * step + R * D + r));
-    const float ref = M == ninf ? 0.f : M;
-    for (int i = 0; i < nsplit; ++i)
-      L = fmaf(__ldcg(all + i * step + R * D + R + r), ex2(__ldcg(all + i * step + R * D + r) - ref), L);
-    s_m[0][r] = ref;
-    s_inv[r] = L == 0.f ? 0.f : 1.f / L;
-    store_lse(a, q0, h, r0 + r, M, L);
+  float *w_m = s_acc, *w_l = s_acc + nsplit * R;
+  for (int i = threadIdx.x; i < nsplit * R; i += kThreads) {
+    const float *p = all + int64_t(i / R) * step + R * D + i % R;
+    w_m[i] = __ldcg(p);
+    w_l[i] = __ldcg(p + R);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nr * (D / 4); i += kWarps * 32) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
+  for (int r = warp; r < nr; r += W) {
+    float M = ninf, L = 0.f;
+    for (int i = lane; i < nsplit; i += 32) M = fmaxf(M, w_m[i * R + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == ninf ? 0.f : M;
+    for (int i = lane; i < nsplit; i += 32) {
+      const float f = ex2(w_m[i * R + r] - ref);
+      w_m[i * R + r] = f;
+      L = fmaf(w_l[i * R + r], f, L);
+    }
+    L = warp_sum(L);
+    if (lane == 0) {
+      s_inv[r] = L == 0.f ? 0.f : 1.f / L;
+      store_lse(a, q0, h, r0 + r, M, L);
+    }
+  }
+  __syncthreads();
+  float4 *s_sum = reinterpret_cast<float4 *>(s_acc + (2 * nsplit * R + 3) / 4 * 4);  // [k][item]
+  const int items = nr * (D / 4);
+  const int KG = items >= kThreads ? 1 : min(8, kThreads / items);
+  for (int i = threadIdx.x; i < items * KG; i += kThreads) {
+    const int kg = i / items, it = i % items, r = it / (D / 4), d = it % (D / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = 0; k < nsplit; ++k) {
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(all + k * step + r * D + d));
-      const float f = ex2(__ldcg(all + k * step + R * D + r) - s_m[0][r]);
+    for (int k = kg; k < nsplit; k += KG) {
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(all + int64_t(k) * step + r * D + d));
+      const float f = w_m[k * R + r];
       v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
     }
-    store_out<D>(a, q0, h, r0 + r, d, v, s_inv[r]);
+    if (KG == 1)
+      store_out<D>(a, q0, h, r0 + r, d, v, s_inv[r]);
+    else
+      s_sum[i] = v;
+  }
+  if (KG == 1) return;
+  __syncthreads();
+  for (int it = threadIdx.x; it < items; it += kThreads) {
+    float4 v = s_sum[it];
+    for (int kg = 1; kg < KG; ++kg) {
+      const float4 x = s_sum[kg * items + it];
+      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+    const int r = it / (D / 4);
+    store_out<D>(a, q0, h, r0 + r, it % (D / 4) * 4, v, s_inv[r]);
   }
 }
 
-template <int D, int PARTS>
+template <int D, int PARTS, int W>
 size_t attn_smem() {
-  const size_t ring = size_t(kWarps) * Shape<D>::kRing, acc = size_t(kWarps) * (16 / PARTS) * D * 4;
-  return Shape<D>::kKSteps * 512 + (ring > acc ? ring : acc) + size_t(kMaxSplitBlocks) * sizeof(BlockAt);
+  return Shape<D>::kKSteps * 512 + body_bytes<D, PARTS, W>() + size_t(max_split_blocks(W)) * sizeof(BlockAt);
 }
 
 template <typename F>
@@ -558,27 +622,35 @@ int with_dim(int d, F &&f) {
 }
 
 struct Plan {
-  int parts, tiles, splits, split_blocks;
+  int parts, warps, tiles, splits, split_blocks;
   int64_t units;
   size_t ticket_bytes, bytes;
 };
 
-Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, int type) {
+Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, int window,
+          int type) {
   Plan p{};
   const int64_t rows = int64_t(max_q) * (n_heads / n_kv);
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
   const int R = 16 / p.parts;
   p.tiles = int((rows + R - 1) / R);
   p.units = int64_t(n_seqs) * n_kv * p.tiles;
-  const int64_t blocks = (int64_t(max_kv_len) + kKvBlock - 1) / kKvBlock;
-  // whole waves of resident CTAs (two of them, so that sequences of different lengths even
-  // out), but no fewer than two blocks per warp and split
-  const int64_t want = int64_t(di.sm_count) * (head_dim <= 128 ? 4 : 2) * (n_seqs > 1 ? 2 : 1);
-  int64_t splits = want / (p.units > 0 ? p.units : 1);
+  // blocks a tile can see: its rows span at most R queries
+  int64_t tokens = max_kv_len;
+  if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
+  const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
+  const int resident = head_dim <= 128 ? 16 : 8;  // warps per SM
+  // Few tiles: CTAs that fill an SM, so that a tile is cut into few splits; many: small CTAs,
+  // whose starts and ends overlap with their neighbours' work.
+  p.warps = p.units <= di.sm_count || blocks > int64_t(max_splits(4)) * max_split_blocks(4) ? resident : 4;
+  const int64_t per_wave = int64_t(di.sm_count) * (resident / p.warps);
+  int64_t splits = p.warps == 4 ? 2 * per_wave / p.units : per_wave / (p.units > 0 ? p.units : 1);
   if (splits < 1) splits = 1;
+  if (splits > max_splits(p.warps)) splits = max_splits(p.warps);
+  // a split costs its join (about 3 us): not below this many blocks per warp
   int64_t per = (blocks + splits - 1) / splits;
-  if (per < 2 * kWarps) per = 2 * kWarps;
-  if (per > kMaxSplitBlocks) per = kMaxSplitBlocks;
+  if (per < 4 * p.warps) per = 4 * p.warps;
+  if (per > max_split_blocks(p.warps)) per = max_split_blocks(p.warps);
   p.split_blocks = int(per);
   p.splits = int((blocks + per - 1) / per);
   if (p.splits < 1) p.splits = 1;
@@ -594,7 +666,7 @@ size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n
   if (device_info(&di) != cudaSuccess) return 0;
   size_t most = 0;  // enough for every element type
   for (int type : {QDQ_TYPE_F32, QDQ_TYPE_BF16}) {
-    const size_t b = plan(di, n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, type).bytes;
+    const size_t b = plan(di, n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, 0, type).bytes;
     if (b > most) most = b;
   }
   return most;
@@ -607,7 +679,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
-  const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, type);
+  const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, window, type);
   if (p.units * p.splits > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
   AttnArgs a{};
   a.c = c;
@@ -634,12 +706,15 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.softcap = softcap;
   e = cudaError_t(with_dim(head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
+    constexpr int W = D <= 128 ? 16 : 8;
     auto run = [&](auto kernel, size_t sm) {
       const cudaError_t r = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(sm));
       if (r != cudaSuccess) return int(r);
-      return int(launch(kernel, dim3(unsigned(p.units * p.splits)), dim3(kWarps * 32), sm, s, a));
+      return int(launch(kernel, dim3(unsigned(p.units * p.splits)), dim3(p.warps * 32), sm, s, a));
     };
-    return p.parts == 2 ? run(kv_attn_kernel<D, 2>, attn_smem<D, 2>()) : run(kv_attn_kernel<D, 1>, attn_smem<D, 1>());
+    if (p.warps == 4)
+      return p.parts == 2 ? run(kv_attn_kernel<D, 2, 4>, attn_smem<D, 2, 4>()) : run(kv_attn_kernel<D, 1, 4>, attn_smem<D, 1, 4>());
+    return p.parts == 2 ? run(kv_attn_kernel<D, 2, W>, attn_smem<D, 2, W>()) : run(kv_attn_kernel<D, 1, W>, attn_smem<D, 1, W>());
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }

@@ -377,6 +377,7 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
  * the caller before its first use; a call leaves it ready for the next one on the same stream.
  * Results do not depend on the order in which CTAs run.
  */
+#define QDQ_MAX_KV_LEN 4194304   /* the largest max_kv_len */
 size_t qdq_kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
 int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
                      int table_stride, const int *kv_len, const int *cu_q, int n_seqs, int max_q, int max_kv_len,
