@@ -787,11 +787,16 @@ int launch_gemv_xs_qkv(const void *Wq, const void *Wk, const void *Wv, const flo
 
 QDQ_CHECK_READER(read_checks_xs)
 
+int read_attn_tc_timeouts();  // qdq_kv_attn_tc.cu
+
+// ... of this ring kernel and of the tensor-core attention
 int read_xs_timeouts() {
+  const int attn = read_attn_tc_timeouts();
+  if (attn < 0) return -1;
   unsigned int v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_xs_timeouts, sizeof(v)) != cudaSuccess) return -1;
   if (cudaMemcpyToSymbol(g_xs_timeouts, &zero, sizeof(zero)) != cudaSuccess) return -1;
-  return int(v);
+  return int(v) + attn;
 }
 
 }  // namespace qdq

@@ -133,24 +133,6 @@ int launch_q6k_pack(const void *ggml, void *packed, int n_out, int n_in, cudaStr
 int launch_q6k_dequant(const void *W, float *out, int n_out, int n_in, cudaStream_t s);
 int launch_q6k_get_rows(const void *W, const int *ids, float *out, int n_ids, int n_rows, int n_in, cudaStream_t s);
 int launch_q6k_gemv(const void *W, const float *x, float *y, int n_out, int n_in, int batch, cudaStream_t s);
-// Decode-step operators (qdq_norm.cu, qdq_kv.cu, qdq_kv_attn.cu, qdq_logprobs.cu); arguments as in qdq.h.
-struct KvPool;
-int launch_rms_norm(const void *x, const void *residual, const float *weight, void *sum_out, void *out, void *q8,
-                    int type, int rows, int n, int64_t x_stride, int64_t residual_stride, int64_t sum_stride,
-                    int64_t out_stride, float eps, cudaStream_t s);
-int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int *cu, int n_seqs, int max_new,
-                     const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s);
-int launch_kv_read(const KvPool &c, int head_dim, const int *start, const int *cu, int n_seqs, int max_tokens, void *k,
-                   void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s);
-size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
-int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, int n_seqs, int max_q,
-                        int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,
-                        float *lse, const float *slopes, float scale, float softcap, int window, int type,
-                        void *workspace, cudaStream_t s);
-size_t token_logprobs_workspace_bytes(int rows, int n, int k);
-int launch_token_logprobs(const void *logits, int64_t stride, int type, const int *tokens, int rows, int n, int k,
-                          void *workspace, float *logprob, float *entropy, int *top_index, float *top_logprob,
-                          cudaStream_t s);
 // Pipeline-timeout counters of the translation units that run bounded waits:
 // each returns its count since the last call and resets it (-1 on CUDA error).
 int read_gemm_timeouts();

@@ -19,50 +19,22 @@
 // The running maximum, the sum and the accumulators are f32.  The four warps of a CTA take every
 // fourth block of their split of the tokens and are joined through shared memory; splits of one
 // tile are joined by the CTA that finishes last, in split order.
-#include <cuda_fp16.h>
-
-#include "qdq_types.cuh"
+#include "qdq_kv_attn.cuh"
 
 namespace qdq {
 namespace {
 
 constexpr int kStages = 3;       // blocks in a warp's ring
-constexpr float kLazy = 1.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
 // Splits of one tile (the joining CTA keeps their maxima and sums in shared memory), and blocks
 // of 16 tokens in one split.
 constexpr int max_splits(int warps) { return warps > 4 ? 512 : 64; }
 constexpr int max_split_blocks(int warps) { return warps > 4 ? 512 : 128; }
 static_assert(int64_t(max_splits(8)) * max_split_blocks(8) * kKvBlock == QDQ_MAX_KV_LEN, "the longest cache");
-constexpr float kPScale = 16384.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnArgs {
-  KvPool c;
-  const int *kv_len, *cu_q;
-  const void *q;
-  void *out;
-  float *lse;
-  const float *slopes;
-  uint32_t *tickets;
-  float *partial;
-  int64_t q_stride, out_stride;
-  int n_seqs, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
-  float scale, softcap;
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-// Bytes 0, 1 (lo) or 2, 3 (hi) of four excess-128 codes as two exact f16: the byte under the
-// exponent of 1024, then 1024 + 128 taken off.
-template <int SEL>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t u) {
-  const uint32_t w = __byte_perm(u, 0x64646464u, SEL);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 template <int BYTES>
@@ -83,13 +55,6 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// 2^x, 0 for -inf (one instruction; a result below the normal numbers is 0)
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 template <int D>
 struct Shape {
   static constexpr int kKB = D % 64 == 0 ? 16 : 8;   // bytes of a key row per lane and load
@@ -128,13 +93,6 @@ __device__ __forceinline__ int dim_of(int j, int n) {
   return (j / VB) * 8 * VB + n * VB + j % VB;
 }
 
-// A block of the split.
-struct BlockAt {
-  int64_t k;  // byte offset of its first key code
-  float ks, vs;
-  float lv;   // log2 of the value scale, at least -95 (a block of zeros has scale 0)
-};
-
 // Bytes of the rings, which the warps' accumulators and the join of the splits use afterwards
 // (a maximum and a sum per split and row, and a float4 per thread).
 template <int D, int PARTS, int W>
@@ -149,25 +107,6 @@ constexpr int body_bytes() {
 // lanes of one store, which hold dims 32 or 16 apart of rows a whole number of lines apart, meet
 // in different banks (unexchanged, a one-token call took 1.5 us longer).
 __device__ __forceinline__ int quad_at(int row, int c) { return c ^ (((c >> 3) & 3) | ((row & 1) << 2)); }
-
-// Four dims of one row, times inv, in the output's type.
-template <int D>
-__device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int row, int d, float4 v, float inv) {
-  const int64_t e = int64_t(q0 + row / a.group) * a.out_stride + int64_t(h * a.group + row % a.group) * D + d;
-  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-  if (a.type == QDQ_TYPE_F32)
-    store4(static_cast<float *>(a.out) + e, v);
-  else if (a.type == QDQ_TYPE_F16)
-    store4(static_cast<__half *>(a.out) + e, v);
-  else
-    store4(static_cast<__nv_bfloat16 *>(a.out) + e, v);
-}
-// M: the reference (log2 units), L: the sum of 2^(score - M)
-__device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int row, float M, float L) {
-  if (a.lse)
-    a.lse[int64_t(q0 + row / a.group) * a.n_heads + h * a.group + row % a.group] =
-        L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
-}
 
 // PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.  W warps.
 template <int D, int PARTS, int W>
@@ -259,7 +198,7 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
     const uint8_t *sc = a.c.pages + (s_blk[i].k - int64_t(b) * S::kPlane + 2 * vplane + 4 * b);
     const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
     const bool none = s_blk[i].ks != 0.f;  // no page: NaN scores
-    s_blk[i].lv = log2f(fmaxf(none ? 1.f : vs, 2.5243549e-29f));  // a NaN scale gives -95 here and stays NaN in vs
+    s_blk[i].lv = log2f(fmaxf(none ? 1.f : vs, kMinScale));  // a NaN scale gives -95 here and stays NaN in vs
     s_blk[i].vs = none ? 1.f : vs * kPScale;
     if (!none) s_blk[i].ks = ks;
   }
@@ -621,7 +560,11 @@ int with_dim(int d, F &&f) {
   }
 }
 
+constexpr int kTcMinRows = 64;    // query rows per key/value head from which on the tensor-core kernel runs
+constexpr int kTcMinBlocks = 32;  // blocks of 16 tokens that a split of it has at least
+
 struct Plan {
+  bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
   int parts, warps, tiles, splits, split_blocks;
   int64_t units;
   size_t ticket_bytes, bytes;
@@ -631,6 +574,28 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
           int type) {
   Plan p{};
   const int64_t rows = int64_t(max_q) * (n_heads / n_kv);
+  p.parts = type == QDQ_TYPE_F32 ? 2 : 1;
+  p.tc = rows > kTcMinRows && attn_tc_supported(head_dim, p.parts);
+  if (p.tc) {
+    p.tiles = int((rows + kTcRows - 1) / kTcRows);
+    p.units = int64_t(n_seqs) * n_kv * p.tiles;
+    int64_t tokens = max_kv_len;
+    if (window > 0 && tokens > int64_t(window) + kTcRows) tokens = int64_t(window) + kTcRows;
+    const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
+    // two waves of resident CTAs where the tokens are many enough: tiles differ in length
+    const int64_t wave = int64_t(di.sm_count) * (head_dim <= 128 && p.parts == 1 ? 2 : 1);
+    int64_t splits = 2 * wave / p.units;
+    if (splits < 1) splits = 1;
+    int64_t per = ((blocks + splits - 1) / splits + 3) / 4 * 4;  // whole tiles of 64 tokens
+    if (per < kTcMinBlocks) per = kTcMinBlocks;
+    if (per > kTcSplitBlocks) per = kTcSplitBlocks;
+    p.split_blocks = int(per);
+    p.splits = int((blocks + per - 1) / per);
+    if (p.splits < 1) p.splits = 1;
+    p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
+    p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * attn_tc_part_bytes(head_dim) : 0);
+    return p;
+  }
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
   const int R = 16 / p.parts;
   p.tiles = int((rows + R - 1) / R);
@@ -704,6 +669,10 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.type = type;
   a.scale = scale;
   a.softcap = softcap;
+  if (p.tc) {
+    e = launch_attn_tc(a, head_dim, p.parts, s);
+    return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
+  }
   e = cudaError_t(with_dim(head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
     constexpr int W = D <= 128 ? 16 : 8;

@@ -1,0 +1,83 @@
+// What the two attention kernels over the paged 8-bit cache share: the arguments, the blocks of a
+// split, the codes' conversion and the outputs' stores.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "qdq_types.cuh"
+
+namespace qdq {
+
+constexpr float kLazy = 1.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
+constexpr float kPScale = 16384.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinScale = 2.5243549e-29f;  // 2^-95: a smaller value scale counts as this in the reference
+
+struct AttnArgs {
+  KvPool c;
+  const int *kv_len, *cu_q;
+  const void *q;
+  void *out;
+  float *lse;
+  const float *slopes;
+  uint32_t *tickets;
+  float *partial;
+  int64_t q_stride, out_stride;
+  int n_seqs, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
+  float scale, softcap;
+};
+
+// Bytes 0, 1 (lo) or 2, 3 (hi) of four excess-128 codes as two exact f16: the byte under the
+// exponent of 1024, then 1024 + 128 taken off.
+template <int SEL>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u) {
+  const uint32_t w = __byte_perm(u, 0x64646464u, SEL);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// 2^x, 0 for -inf (one instruction; a result below the normal numbers is 0)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A block of the split.
+struct BlockAt {
+  int64_t k;  // byte offset of its first key code
+  float ks, vs;
+  float lv;   // log2 of the value scale, at least -95 (a block of zeros has scale 0)
+};
+
+// Four dims of one row, times inv, in the output's type.
+template <int D>
+__device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int row, int d, float4 v, float inv) {
+  const int64_t e = int64_t(q0 + row / a.group) * a.out_stride + int64_t(h * a.group + row % a.group) * D + d;
+  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (a.type == QDQ_TYPE_F32)
+    store4(static_cast<float *>(a.out) + e, v);
+  else if (a.type == QDQ_TYPE_F16)
+    store4(static_cast<__half *>(a.out) + e, v);
+  else
+    store4(static_cast<__nv_bfloat16 *>(a.out) + e, v);
+}
+// M: the reference (log2 units), L: the sum of 2^(score - M)
+__device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int row, float M, float L) {
+  if (a.lse)
+    a.lse[int64_t(q0 + row / a.group) * a.n_heads + h * a.group + row % a.group] =
+        L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The tensor-core kernel (qdq_kv_attn_tc.cu): 128 rows to a tile, head dims that are whole 64s
+// (256 in two parts does not fit shared memory).
+constexpr int kTcRows = 128;
+constexpr int kTcSplitBlocks = 512;  // blocks of 16 tokens in one split, at most
+inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
+// Bytes of one split's partial result.
+inline size_t attn_tc_part_bytes(int head_dim) { return size_t(kTcRows) * (head_dim + 2) * 4; }
+// Launches a.tiles * n_kv * n_seqs * a.splits CTAs; parts: f16 parts of the queries and probabilities.
+cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, cudaStream_t s);
+int read_attn_tc_timeouts();
+
+}  // namespace qdq

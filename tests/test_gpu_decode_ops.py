@@ -336,6 +336,14 @@ ATTN = [
     ([1500], [200], 12, 4, 128, 64, "f32", 0, 0, False),
     ([1500, 90, 257], [130, 90, 1], 8, 2, 128, 16, "bf16", 0, 0, False),
     ([513, 700], [129, 260], 16, 1, 64, 32, "f32", 30.0, 200, True),
+    ([300, 90], [90, 70], 2, 1, 256, 64, "bf16", 0, 0, False),
+    ([300, 90], [90, 70], 2, 1, 256, 64, "f32", 0, 50, False),
+    ([1000, 80], [70, 80], 4, 2, 192, 48, "f32", 0, 0, True),
+    ([1000, 80], [70, 80], 4, 2, 192, 16, "f16", 30.0, 0, False),
+    ([400, 81], [100, 81], 3, 1, 96, 16, "bf16", 0, 0, False),
+    ([64, 65, 127, 128], [64, 65, 127, 128], 4, 2, 64, 16, "f32", 0, 0, False),
+    ([9000, 300], [80, 65], 2, 1, 128, 32, "bf16", 0, 0, False),
+    ([9000], [65], 2, 1, 64, 32, "f32", 0, 8000, False),
     ([6000, 100, 2100], [1] * 3, 9, 3, 64, 16, "f16", 0, 1, False),
     ([6000, 100, 2100], [1] * 3, 32, 2, 128, 16, "bf16", 15.0, 1024, True),
 ]
