@@ -565,7 +565,7 @@ constexpr int kTcMinBlocks = 32;  // blocks of 16 tokens that a split of it has 
 
 struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
-  int parts, warps, tiles, splits, split_blocks;
+  int parts, groups, warps, tiles, splits, split_blocks;
   int64_t units;
   size_t ticket_bytes, bytes;
 };
@@ -577,14 +577,15 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   p.parts = type == QDQ_TYPE_F32 ? 2 : 1;
   p.tc = rows > kTcMinRows && attn_tc_supported(head_dim, p.parts);
   if (p.tc) {
-    p.tiles = int((rows + kTcRows - 1) / kTcRows);
+    p.groups = rows > kTcRows && head_dim <= 128 ? 2 : 1;
+    const int R = kTcRows * p.groups;
+    p.tiles = int((rows + R - 1) / R);
     p.units = int64_t(n_seqs) * n_kv * p.tiles;
     int64_t tokens = max_kv_len;
-    if (window > 0 && tokens > int64_t(window) + kTcRows) tokens = int64_t(window) + kTcRows;
+    if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
     const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
-    // two waves of resident CTAs where the tokens are many enough: tiles differ in length
-    const int64_t wave = int64_t(di.sm_count) * (head_dim <= 128 && p.parts == 1 ? 2 : 1);
-    int64_t splits = 2 * wave / p.units;
+    // two waves of CTAs (one per SM) where the tokens are many enough: tiles differ in length
+    int64_t splits = 2 * int64_t(di.sm_count) / p.units;
     if (splits < 1) splits = 1;
     int64_t per = ((blocks + splits - 1) / splits + 3) / 4 * 4;  // whole tiles of 64 tokens
     if (per < kTcMinBlocks) per = kTcMinBlocks;
@@ -593,7 +594,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     p.splits = int((blocks + per - 1) / per);
     if (p.splits < 1) p.splits = 1;
     p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
-    p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * attn_tc_part_bytes(head_dim) : 0);
+    p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * attn_tc_part_bytes(head_dim, p.groups) : 0);
     return p;
   }
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
@@ -670,7 +671,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.scale = scale;
   a.softcap = softcap;
   if (p.tc) {
-    e = launch_attn_tc(a, head_dim, p.parts, s);
+    e = launch_attn_tc(a, head_dim, p.parts, p.groups, s);
     return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
   }
   e = cudaError_t(with_dim(head_dim, [&](auto d) {

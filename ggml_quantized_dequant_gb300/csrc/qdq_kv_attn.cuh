@@ -8,8 +8,8 @@
 
 namespace qdq {
 
-constexpr float kLazy = 1.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
-constexpr float kPScale = 16384.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
+constexpr float kLazy = 5.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
+constexpr float kPScale = 1024.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinScale = 2.5243549e-29f;  // 2^-95: a smaller value scale counts as this in the reference
 
@@ -69,15 +69,16 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int 
         L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// The tensor-core kernel (qdq_kv_attn_tc.cu): 128 rows to a tile, head dims that are whole 64s
+// The tensor-core kernel (qdq_kv_attn_tc.cu): one or two groups of 128 rows to a tile, head dims that are whole 64s
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
 constexpr int kTcSplitBlocks = 512;  // blocks of 16 tokens in one split, at most
 inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
 // Bytes of one split's partial result.
-inline size_t attn_tc_part_bytes(int head_dim) { return size_t(kTcRows) * (head_dim + 2) * 4; }
-// Launches a.tiles * n_kv * n_seqs * a.splits CTAs; parts: f16 parts of the queries and probabilities.
-cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, cudaStream_t s);
+inline size_t attn_tc_part_bytes(int head_dim, int groups) { return size_t(kTcRows) * groups * (head_dim + 2) * 4; }
+// Launches a.tiles * n_kv * n_seqs * a.splits CTAs; parts: f16 parts of the queries and
+// probabilities; groups: of 128 rows to a tile (2 up to head_dim 128).
+cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, int groups, cudaStream_t s);
 int read_attn_tc_timeouts();
 
 }  // namespace qdq

@@ -1,8 +1,8 @@
 // Attention of many query rows over the paged 8-bit cache on the 5th-generation tensor cores
 // (prompt chunks; the formulas are those of qdq_kv_attn.cu).
 //
-// A CTA takes 128 rows (query token, head of the group) of one key/value head and walks tiles of
-// 64 tokens of its split:
+// A CTA takes one or two groups of 128 rows (query token, head of the group) of one key/value
+// head and walks tiles of 64 tokens of its split:
 //   S = Q K^T (128 x 64, f32 in TMEM), P = 2^(S - reference) in f16 written over S in TMEM,
 //   O += P V (128 x D, f32 in TMEM).
 // Codes are exact in f16, so K and V tiles are converted in registers, without their scales, into
@@ -12,15 +12,15 @@
 //     row's largest, the probabilities are rounded to f16 (2^-11 relative, as the output is);
 //   two parts (f32): queries and probabilities in two f16 parts each, twice the products.
 //
-// Warp roles (288 threads):
-//   warps 0-3  softmax: one row per thread (a TMEM lane), so its maximum and sum need no
-//              exchange; O is rescaled only when a reference has grown by 2^kLazy;
-//   warps 4-7  convert the codes (two tiles of K and of V in shared memory, loads one tile ahead);
-//   warp 8     allocates TMEM and issues the products: S of tile i + 1 before P V of tile i, so
+// Warp roles (G groups of rows):
+//   4 G softmax warps: one row per thread (a TMEM lane), so its maximum and sum need no exchange;
+//              O is rescaled only when a reference has grown by 2^kLazy;
+//   8 warps that convert the codes, as two sets of 4 taking alternate tiles, so that the loads and
+//              the fence of one tile run beside the conversion of the other;
+//   1 warp that allocates TMEM and issues the products: S of tile i + 1 before P V of tile i, so
 //              that the tensor core works while the softmax of a tile runs.
-// With one part and D <= 128 two CTAs share an SM (256 columns of TMEM each) and fill each
-// other's waits.  Every wait is bounded; one that runs out makes the tile's rows NaN and counts in
-// qdq_pipeline_timeouts.
+// One CTA per SM.  Two groups (head dims up to 128) share each tile's conversion.  Every wait is
+// bounded; one that runs out makes the CTA's rows NaN and counts in qdq_pipeline_timeouts.
 #include "qdq_kv_attn.cuh"
 
 namespace qdq {
@@ -30,8 +30,7 @@ __device__ unsigned int g_attn_tc_timeouts = 0;
 namespace {
 
 constexpr int BN = 64;  // tokens per tile
-constexpr int kSoft = 4, kConv = 4;
-constexpr int kThreads = 32 * (kSoft + kConv + 1);
+constexpr int kSoft = 4, kConv = 8;  // softmax warps per group, converting warps
 
 // ---- tcgen05 --------------------------------------------------------------------
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -103,35 +102,40 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
 // kind::f16 with f16 operands (format 0), f32 accumulator, both K-major.
 constexpr uint32_t idesc_f16(int m, int n) { return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24); }
 
-template <int D, int PARTS>
+template <int D, int PARTS, int G>
 struct Cfg {
-  static constexpr int kSub = D / 64;                       // 64-dim sub-tiles
-  static constexpr uint32_t kQPart = kSub * kTcRows * 128;  // bytes
+  static constexpr int kSub = D / 64;                    // 64-dim sub-tiles
+  static constexpr uint32_t kQTile = kTcRows * 128;      // bytes of 128 rows of a sub-tile
+  static constexpr uint32_t kQPart = G * kSub * kQTile;  // [group][sub-tile]
   static constexpr uint32_t kK = kSub * BN * 128, kV = D * 128;
   static constexpr uint32_t kRing = PARTS * kQPart + 2 * (kK + kV);
-  static constexpr uint32_t kOCol = 2 * BN;  // S0 | S1 | O
-  static constexpr uint32_t kCols = kOCol + D <= 256 ? 256 : 512;
+  static constexpr uint32_t kOCol = 2 * BN * G;  // S of group 0 (two), of group 1 (two) | O of group 0, of group 1
+  static constexpr uint32_t kCols = kOCol + G * D <= 256 ? 256 : 512;
+  static_assert(kOCol + G * D <= 512, "TMEM");
   static constexpr uint32_t kBytes = 1024 + kRing + kTcSplitBlocks * uint32_t(sizeof(BlockAt));
-  // an SM's 512 columns of TMEM hold two CTAs at most: no third one may fit its shared memory
-  static constexpr uint32_t kSmem = kBytes > 80 * 1024 ? kBytes : 80 * 1024;
+  // more than half an SM's shared memory: one CTA per SM, as the columns of TMEM want it
+  static constexpr uint32_t kSmem = kBytes > 116 * 1024 ? kBytes : 116 * 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static constexpr int kPerSm = kCols == 256 && kSmem <= 112 * 1024 ? 2 : 1;
+  static constexpr int kThreads = 32 * (kSoft * G + kConv + 1);
 };
 
+template <int G>
 struct Bars {
-  uint64_t kfull[2], vfull[2], sfull[2], pready[2], pvdone[2], drain;
+  uint64_t kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain;
   uint32_t tmem;
   int abort, last;
 };
 
-template <int D, int PARTS>
-__global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kernel(const AttnArgs a) {
-  using C = Cfg<D, PARTS>;
+template <int D, int PARTS, int G>
+__global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(const AttnArgs a) {
+  using C = Cfg<D, PARTS, G>;
+  constexpr int R = kTcRows * G, kThreads = C::kThreads;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t *kring = smem + PARTS * C::kQPart, *vring = kring + 2 * C::kK;
   BlockAt *s_blk = reinterpret_cast<BlockAt *>(smem + C::kRing);
-  __shared__ Bars bars;
+  __shared__ Bars<G> bars;
+  __shared__ float s_qs[R];
   const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x % a.splits;
@@ -144,9 +148,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
   const int q0 = a.cu_q ? int(ld_u1(a.cu_q + s)) : s;
   const int nq = a.cu_q ? int(ld_u1(a.cu_q + s + 1)) - q0 : 1;
   const int len = int(ld_u1(a.kv_len + s));
-  const int rows = nq * a.group, r0 = tile * kTcRows;
+  const int rows = nq * a.group, r0 = tile * R;
   if (r0 >= rows) return;
-  const int nr = min(kTcRows, rows - r0);
+  const int nr = min(R, rows - r0);
   const bool bad = len < 0 || len > a.max_kv_len || (len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
   const int pos_lo = len - nq + r0 / a.group, pos_hi = len - nq + (r0 + nr - 1) / a.group;
   const int b_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) / kKvBlock : 0;
@@ -159,17 +163,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.kfull[i], kConv);
-      mbar_init(&bars.vfull[i], kConv);
-      mbar_init(&bars.sfull[i], 1);
-      mbar_init(&bars.pready[i], kSoft);
-      mbar_init(&bars.pvdone[i], 1);
+      mbar_init(&bars.kfull[i], kConv / 2);
+      mbar_init(&bars.vfull[i], kConv / 2);
+      mbar_init(&bars.kfree[i], 1);
+      for (int g = 0; g < G; ++g) {
+        mbar_init(&bars.sfull[g][i], 1);
+        mbar_init(&bars.pready[g][i], kSoft);
+        mbar_init(&bars.pvdone[g][i], 1);
+      }
     }
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kSoft + kConv) {
+  if (warp == kSoft * G + kConv) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)),
                  "r"(C::kCols)
                  : "memory");
@@ -195,62 +202,72 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
     s_blk[i] = e;
   }
 
-  // softmax threads: their row's queries, scaled by a power of two, into f16 parts
-  const int row = r0 + tid;  // tid < 128
-  float qs = 0.f;
-  if (warp < kSoft) {
-    const bool in = tid < nr;
-    const int64_t base = in ? int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D : 0;
-    auto load8 = [&](int d, float (&v)[8]) {  // dims d .. d + 7
-      if (!in) {
+  // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row
+  if (warp < kSoft * G + kConv) {
+    constexpr int LR = D / 8 == 24 ? 32 : D / 8, RW = 32 / LR;  // lanes and rows of a warp's load
+    constexpr int kWarps = kSoft * G + kConv, kBatch = 4;
+    const int sub = lane / LR, d = lane % LR * 8;
+    for (int rb = warp * RW; rb < R; rb += kWarps * RW * kBatch) {
+      uint4 raw0[kBatch], raw1[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      } else if (a.type == QDQ_TYPE_F32) {
-        const float4 x = load4(static_cast<const float *>(a.q) + base + d), y = load4(static_cast<const float *>(a.q) + base + d + 4);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-      } else {
-        const uint4 u = ld_u4(static_cast<const uint16_t *>(a.q) + base + d);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = a.type == QDQ_TYPE_F16 ? unpack2(w[i], __half{}) : unpack2(w[i], __nv_bfloat16{});
-          v[2 * i] = f.x;
-          v[2 * i + 1] = f.y;
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = rb + i * kWarps * RW + sub, row = r0 + r;
+        raw0[i] = raw1[i] = make_uint4(0, 0, 0, 0);
+        if (r < nr && d < D) {
+          const int64_t e = int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D + d;
+          if (a.type == QDQ_TYPE_F32) {
+            raw0[i] = ld_u4(static_cast<const float *>(a.q) + e);
+            raw1[i] = ld_u4(static_cast<const float *>(a.q) + e + 4);
+          } else {
+            raw0[i] = ld_u4(static_cast<const uint16_t *>(a.q) + e);
+          }
         }
       }
-    };
-    float m = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 8) {
-      float v[8];
-      load8(d, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_abs_bits(m, v[i]);
-    }
-    const bool finite = m < __int_as_float(0x7f800000);
-    int ex = 13 - (int(__float_as_uint(m) >> 23) - 127);
-    ex = max(-120, min(120, ex));
-    // the scale's sign goes into the queries, so that a larger product is a larger score
-    float up = finite ? __uint_as_float(uint32_t(ex + 127) << 23) : 0.f;
-    qs = (finite ? __uint_as_float(uint32_t(127 - ex) << 23) : qnan) * fabsf(a.scale);
-    if (a.scale < 0.f) up = -up;
-    if (!(a.softcap > 0.f)) qs *= kLog2e;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 8) {
-      float v[8];
-      load8(d, v);
-      uint32_t hi[4], lo[4];
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = rb + i * kWarps * RW + sub;
+        float v[8];
+        const uint32_t w0[4] = {raw0[i].x, raw0[i].y, raw0[i].z, raw0[i].w}, w1[4] = {raw1[i].x, raw1[i].y, raw1[i].z, raw1[i].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = finite ? v[2 * i] * up : 0.f, y = finite ? v[2 * i + 1] * up : 0.f;
-        hi[i] = pack2(x, y, __half{});
-        const float2 b = unpack2(hi[i], __half{});
-        lo[i] = pack2(x - b.x, y - b.y, __half{});
+        for (int e = 0; e < 4; ++e) {
+          if (a.type == QDQ_TYPE_F32) {
+            v[e] = __uint_as_float(w0[e]);
+            v[4 + e] = __uint_as_float(w1[e]);
+          } else {
+            const float2 f = a.type == QDQ_TYPE_F16 ? unpack2(w0[e], __half{}) : unpack2(w0[e], __nv_bfloat16{});
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+          }
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = max_abs_bits(mx, v[e]);
+#pragma unroll
+        for (int o = LR / 2; o > 0; o >>= 1) mx = max_abs_bits(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const bool finite = mx < __int_as_float(0x7f800000);
+        int ex = 13 - (int(__float_as_uint(mx) >> 23) - 127);
+        ex = max(-120, min(120, ex));
+        // the scale's sign goes into the queries, so that a larger product is a larger score
+        float up = finite ? __uint_as_float(uint32_t(ex + 127) << 23) : 0.f;
+        if (a.scale < 0.f) up = -up;
+        if (d == 0 && r < R) {
+          const float q = (finite ? __uint_as_float(uint32_t(127 - ex) << 23) : qnan) * fabsf(a.scale);
+          s_qs[r] = a.softcap > 0.f ? q : q * kLog2e;
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = finite ? v[2 * e] * up : 0.f, y = finite ? v[2 * e + 1] * up : 0.f;
+          hi[e] = pack2(x, y, __half{});
+          const float2 back = unpack2(hi[e], __half{});
+          lo[e] = pack2(x - back.x, y - back.y, __half{});
+        }
+        if (r < R && d < D) {
+          uint8_t *dst = smem + ((r / kTcRows) * C::kSub + d / 64) * C::kQTile + (r % kTcRows) * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
-      uint8_t *dst = smem + (d / 64) * (kTcRows * 128) + tid * 128 + (((d % 64 / 8) ^ (tid & 7)) << 4);
-      *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -266,18 +283,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
     return false;
   };
 
-  float m = ninf, l = 0.f;  // softmax threads: their row's reference and sum
-  if (warp < kSoft) {
+  const int grp = warp / kSoft;        // softmax warps: their group of rows
+  const int lr = tid;                  // and their thread's row of the tile
+  const int row = r0 + lr;
+  float m = ninf, l = 0.f;             // its reference and sum
+  const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+  const uint32_t otm = tmem + lanes + C::kOCol + uint32_t(grp * D);  // its O
+  if (warp < kSoft * G) {
     const int pos = len - nq + row / a.group;
     const int lo_pos = a.window > 0 ? pos - a.window + 1 : 0;
-    const float slope = a.slopes && tid < nr ? __ldg(a.slopes + h * a.group + row % a.group) * kLog2e : 0.f;
+    const float qs = s_qs[lr];
+    const float slope = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row % a.group) * kLog2e : 0.f;
     // tokens that every row of the tile sees
     const int all_lo = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0, all_hi = pos_lo + 1;
-    const uint32_t lanes = uint32_t(warp * 32) << 16;
     for (int i = 0; i < nt; ++i) {
       const int b = i & 1;
-      const uint32_t sp = tmem + lanes + uint32_t(b * BN);
-      if (!wait(&bars.sfull[b], i >> 1)) break;
+      const uint32_t sp = tmem + lanes + uint32_t((2 * grp + b) * BN);
+      if (!wait(&bars.sfull[grp][b], i >> 1)) break;
       tc_fence_after();
       uint32_t r[BN];
 #pragma unroll
@@ -290,11 +312,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
       if (whole && !(a.softcap > 0.f) && !a.slopes) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float bm = __uint_as_float(r[16 * c]);
+          float bm = fmaxf(__uint_as_float(r[16 * c]), __uint_as_float(r[16 * c + 1]));
+          float bn = fmaxf(__uint_as_float(r[16 * c + 2]), __uint_as_float(r[16 * c + 3]));
 #pragma unroll
-          for (int e = 1; e < 16; ++e) bm = fmaxf(bm, __uint_as_float(r[16 * c + e]));
+          for (int e = 4; e < 16; e += 4) {
+            bm = fmaxf(fmaxf(bm, __uint_as_float(r[16 * c + e])), __uint_as_float(r[16 * c + e + 1]));
+            bn = fmaxf(fmaxf(bn, __uint_as_float(r[16 * c + e + 2])), __uint_as_float(r[16 * c + e + 3]));
+          }
           f[c] = qs * s_blk[4 * i + c].ks;
-          mx = fmaxf(mx, fmaf(bm, f[c], s_blk[4 * i + c].lv));
+          mx = fmaxf(mx, fmaf(fmaxf(bm, bn), f[c], s_blk[4 * i + c].lv));
         }
       } else {
 #pragma unroll
@@ -323,21 +349,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
         l *= corr;
         m = m_new;
         if (i > 0) {
-          if (!wait(&bars.pvdone[(i - 1) & 1], (i - 1) >> 1)) break;
+          if (!wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1)) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
-            tmem_ld16_async(tmem + lanes + C::kOCol + c, o);
+            tmem_ld16_async(otm + c, o);
             tmem_wait_ld16(o);
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st16(tmem + lanes + C::kOCol + c, o);
+            tmem_st16(otm + c, o);
           }
         }
       }
       const float mref = m == ninf ? 0.f : m;
-      float2 l2 = f2(0.f, 0.f);
+      float2 l2 = f2(0.f, 0.f), l3 = f2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float vs = s_blk[4 * i + c].vs;
@@ -347,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
         for (int e = 0; e < 8; ++e) {
           const float2 x = __ffma2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), ff, mm);
           const float2 p = f2(ex2(x.x), ex2(x.y));
-          l2 = __fadd2_rn(l2, p);
+          if (e & 1)
+            l3 = __fadd2_rn(l3, p);
+          else
+            l2 = __fadd2_rn(l2, p);
           float2 pv = __fmul2_rn(p, vv);
           if (!whole) {  // a hidden token's scale may be NaN
             if (x.x == ninf) pv.x = 0.f;
@@ -362,46 +391,40 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
         tmem_st8(sp + 8 * c, hi);
         if (PARTS == 2) tmem_st8(sp + BN / 2 + 8 * c, lo);
       }
-      l += l2.x + l2.y;
+      l += (l2.x + l2.y) + (l3.x + l3.y);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.pready[b]);
+      if (lane == 0) mbar_arrive(&bars.pready[grp][b]);
     }
-  } else if (warp < kSoft + kConv) {
+  } else if (warp < kSoft * G + kConv) {
     // ---------------- codes to f16 tiles ----------------
-    const int w = warp - kSoft;
-    constexpr int KL = D / 32;          // 16-byte loads of keys per thread: tokens 16 w .. 16 w + 15 of the tile
+    const int set = (warp - kSoft * G) >> 2, w = (warp - kSoft * G) & 3;  // tiles set, set + 2, ...
+    constexpr int KL = D / 32;            // 16-byte loads of keys per thread: tokens 16 w .. 16 w + 15 of the tile
     constexpr int VG = (D / 32 + 3) / 4;  // groups of 32 dims of the values per warp
     uint4 kq[KL];
     uint2 vq[VG][8];
     const int ktok = lane & 7, kch = lane >> 3;  // row and 16-dim chunk of a load
     const int vtc = lane & 7, vd = lane >> 3;    // 8-token chunk, 8-dim part of the group
-    auto load_k = [&](int i) {
+    auto load = [&](int i) {
       const int64_t at = s_blk[4 * i + w].k;
       const uint8_t *p = a.c.pages + at + ktok * D + kch * 16;
 #pragma unroll
       for (int j = 0; j < KL; ++j)  // rows + 8 (j & 1), chunks + 4 (j >> 1)
         kq[j] = at < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(p + (j & 1) * 8 * D + (j >> 1) * 64);
-    };
-    auto load_v = [&](int i) {
-      const int64_t at = s_blk[4 * i + vtc / 2].k;
-      const uint8_t *p = a.c.pages + at + vplane + (vtc & 1) * 8 * D + vd * 8;
+      const int64_t av = s_blk[4 * i + vtc / 2].k;
+      const uint8_t *pv = a.c.pages + av + vplane + (vtc & 1) * 8 * D + vd * 8;
 #pragma unroll
       for (int g = 0; g < VG; ++g)
         if (w + 4 * g < D / 32) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) vq[g][t] = at < 0 ? make_uint2(0, 0) : ld_u2(p + t * D + (w + 4 * g) * 32);
+          for (int t = 0; t < 8; ++t) vq[g][t] = av < 0 ? make_uint2(0, 0) : ld_u2(pv + t * D + (w + 4 * g) * 32);
         }
     };
-    if (nt > 0) {
-      load_k(0);
-      load_v(0);
-    }
-    for (int i = 0; i < nt; ++i) {
-      const int b = i & 1;
-      if (i >= 2 && !wait(&bars.sfull[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
-      uint8_t *kt = kring + b * C::kK;
+    if (set < nt) load(set);
+    uint8_t *kt = kring + set * C::kK, *vt = vring + set * C::kV;
+    for (int i = set; i < nt; i += 2) {
+      if (i >= 2 && !wait(&bars.kfree[set], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
 #pragma unroll
       for (int j = 0; j < KL; ++j) {
         const int rr = 16 * w + 8 * (j & 1) + ktok, ch = kch + 4 * (j >> 1);
@@ -418,12 +441,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
         *reinterpret_cast<uint4 *>(dst + ((c ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      if (i + 1 < nt) load_k(i + 1);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.kfull[b]);
-      if (i >= 2 && !wait(&bars.pvdone[b], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
-      uint8_t *vt = vring + b * C::kV;
+      if (lane == 0) mbar_arrive(&bars.kfull[set]);
+      if (i >= 2 && !wait(&bars.pvdone[G - 1][set], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
 #pragma unroll
       for (int g = 0; g < VG; ++g)
         if (w + 4 * g < D / 32) {
@@ -447,31 +468,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
             put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
           }
         }
-      if (i + 1 < nt) load_v(i + 1);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.vfull[b]);
+      if (lane == 0) mbar_arrive(&bars.vfull[set]);
+      if (i + 2 < nt) load(i + 2);  // after the fences, which would wait for these loads
     }
   } else {
     // ---------------- products ----------------
     const uint32_t leader = elect_lane();
     const uint32_t q_base = smem_u32(smem), k_base = smem_u32(kring), v_base = smem_u32(vring);
-    auto scores = [&](int i) {  // S of tile i
+    auto scores = [&](int g, int i) {  // S of tile i
       const int b = i & 1;
 #pragma unroll
       for (int part = 0; part < PARTS; ++part)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(leader, tmem + uint32_t(b * BN), desc_sw128(q_base + part * C::kQPart + (k / 4) * (kTcRows * 128) + (k % 4) * 32),
+          mma_ss(leader, tmem + uint32_t((2 * g + b) * BN),
+                 desc_sw128(q_base + part * C::kQPart + (g * C::kSub + k / 4) * C::kQTile + (k % 4) * 32),
                  desc_sw128(k_base + b * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
-      mma_commit(leader, &bars.sfull[b]);
+      mma_commit(leader, &bars.sfull[g][b]);
     };
     bool ok = true;
     if (nt > 0) {
       ok = wait(&bars.kfull[0], 0);
       if (ok) {
         tc_fence_after();
-        scores(0);
+#pragma unroll
+        for (int g = 0; g < G; ++g) scores(g, 0);
+        mma_commit(leader, &bars.kfree[0]);
       }
     }
     for (int i = 0; i < nt && ok; ++i) {
@@ -479,21 +503,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
       if (i + 1 < nt) {
         ok = wait(&bars.kfull[b ^ 1], (i + 1) >> 1);
         // the other S holds the probabilities of tile i - 1 until its products are done
-        if (ok && i >= 1) ok = wait(&bars.pvdone[b ^ 1], (i - 1) >> 1);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          if (ok && i >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (i - 1) >> 1);
+          if (ok) {
+            tc_fence_after();
+            scores(g, i + 1);
+          }
+        }
+        if (!ok) break;
+        mma_commit(leader, &bars.kfree[b ^ 1]);
+      }
+      ok = wait(&bars.vfull[b], i >> 1);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (ok) ok = wait(&bars.pready[g][b], i >> 1);
         if (!ok) break;
         tc_fence_after();
-        scores(i + 1);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(leader, tmem + C::kOCol + uint32_t(g * D), tmem + uint32_t((2 * g + b) * BN + part * (BN / 2) + 8 * k),
+                   desc_sw128(v_base + b * C::kV + k * 32), idesc_f16(kTcRows, D), (i | part | k) != 0);
+        mma_commit(leader, &bars.pvdone[g][b]);
       }
-      ok = wait(&bars.pready[b], i >> 1) && wait(&bars.vfull[b], i >> 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_ts(leader, tmem + C::kOCol, tmem + uint32_t(b * BN + part * (BN / 2) + 8 * k),
-                 desc_sw128(v_base + b * C::kV + k * 32), idesc_f16(kTcRows, D), (i | part | k) != 0);
-      mma_commit(leader, &bars.pvdone[b]);
     }
     mma_commit(leader, &bars.drain);
   }
@@ -506,17 +540,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
   __syncthreads();
   const bool lost = bad || *reinterpret_cast<volatile int *>(&bars.abort) != 0;
   if (tid == 0 && bars.abort) atomicAdd(&g_attn_tc_timeouts, 1u);
-  constexpr int kPart = kTcRows * (D + 2);
+  constexpr int kPart = R * (D + 2);
   float *part = a.partial + (int64_t(unit) * a.splits + split) * kPart;  // [dim][row], maxima, sums
-  if (warp < kSoft) {
+  if (warp < kSoft * G) {
     if (lost) l = qnan;
     const float inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
-    const bool in = tid < nr;
+    const bool in = lr < nr;
 #pragma unroll 1
     for (int c = 0; c < D; c += 16) {
       uint32_t o[16];
       if (nt > 0) {
-        tmem_ld16_async(tmem + (uint32_t(warp * 32) << 16) + C::kOCol + c, o);
+        tmem_ld16_async(otm + c, o);
         tmem_wait_ld16(o);
       } else {
 #pragma unroll
@@ -533,74 +567,84 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, PARTS>::kPerSm) attn_tc_kerne
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[(c + e) * kTcRows + tid] = __uint_as_float(o[e]);
+        for (int e = 0; e < 16; ++e) part[(c + e) * R + lr] = __uint_as_float(o[e]);
       }
     }
     if (nsplit == 1) {
       if (in) store_lse(a, q0, h, row, m, l);
     } else {
-      part[D * kTcRows + tid] = m;
-      part[D * kTcRows + kTcRows + tid] = l;
+      part[D * R + lr] = m;
+      part[D * R + R + lr] = l;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoft + kConv) {
+  if (warp == kSoft * G + kConv) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
   if (nsplit == 1) return;
 
-  // the CTA that finishes last joins the splits, in split order
+  // the CTA that finishes last joins the splits, in split order: thread (row, share of the dims)
   __threadfence();
   __syncthreads();
   if (tid == 0) bars.last = atomicInc(a.tickets + unit, nsplit - 1) == uint32_t(nsplit - 1);
   __syncthreads();
   if (!bars.last) return;
   __threadfence();
-  if (tid >= 2 * kTcRows) return;
+  constexpr int kShares = kThreads / R;
   const float *all = a.partial + int64_t(unit) * a.splits * kPart;
-  const int jr = tid & (kTcRows - 1), half = tid / kTcRows;  // row, half of the dims
-  if (jr >= nr) return;
+  const int jr = tid % R, share = tid / R;
+  if (share >= kShares || jr >= nr) return;
   float M = ninf, L = 0.f;
-  for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(all + int64_t(k) * kPart + D * kTcRows + jr));
+#pragma unroll 4
+  for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(all + int64_t(k) * kPart + D * R + jr));
   const float ref = M == ninf ? 0.f : M;
+#pragma unroll 4
   for (int k = 0; k < nsplit; ++k)
-    L = fmaf(__ldcg(all + int64_t(k) * kPart + (D + 1) * kTcRows + jr), ex2(__ldcg(all + int64_t(k) * kPart + D * kTcRows + jr) - ref), L);
+    L = fmaf(__ldcg(all + int64_t(k) * kPart + (D + 1) * R + jr), ex2(__ldcg(all + int64_t(k) * kPart + D * R + jr) - ref), L);
   const float inv = L == 0.f ? 0.f : (1.f / kPScale) / L;
 #pragma unroll 1
-  for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 16) {
+  for (int d = share * 16; d < D; d += kShares * 16) {
     float v[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = 0.f;
     for (int k = 0; k < nsplit; ++k) {
-      const float f = ex2(__ldcg(all + int64_t(k) * kPart + D * kTcRows + jr) - ref);
+      const float f = ex2(__ldcg(all + int64_t(k) * kPart + D * R + jr) - ref);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = fmaf(__ldcg(all + int64_t(k) * kPart + (d + e) * kTcRows + jr), f, v[e]);
+      for (int e = 0; e < 16; ++e) v[e] = fmaf(__ldcg(all + int64_t(k) * kPart + (d + e) * R + jr), f, v[e]);
     }
 #pragma unroll
     for (int e = 0; e < 16; e += 4) store_out<D>(a, q0, h, r0 + jr, d + e, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]), inv);
   }
-  if (half == 0) store_lse(a, q0, h, r0 + jr, M, L);
+  if (share == 0) store_lse(a, q0, h, r0 + jr, M, L);
 }
 
-template <int D, int PARTS>
+template <int D, int PARTS, int G>
 cudaError_t run(const AttnArgs &a, cudaStream_t s) {
-  const auto kernel = attn_tc_kernel<D, PARTS>;
-  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(Cfg<D, PARTS>::kSmem));
+  using C = Cfg<D, PARTS, G>;
+  const auto kernel = attn_tc_kernel<D, PARTS, G>;
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(C::kSmem));
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(a.n_seqs) * a.c.n_kv * a.tiles * a.splits;
-  return launch(kernel, dim3(unsigned(grid)), dim3(kThreads), Cfg<D, PARTS>::kSmem, s, a);
+  return launch(kernel, dim3(unsigned(grid)), dim3(C::kThreads), C::kSmem, s, a);
+}
+template <int D, int PARTS>
+cudaError_t run(const AttnArgs &a, int groups, cudaStream_t s) {
+  if constexpr (D <= 128) {
+    if (groups == 2) return run<D, PARTS, 2>(a, s);
+  }
+  return run<D, PARTS, 1>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, cudaStream_t s) {
+cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, int groups, cudaStream_t s) {
   switch (head_dim) {
-    case 64: return parts == 2 ? run<64, 2>(a, s) : run<64, 1>(a, s);
-    case 128: return parts == 2 ? run<128, 2>(a, s) : run<128, 1>(a, s);
-    case 192: return parts == 2 ? run<192, 2>(a, s) : run<192, 1>(a, s);
-    default: return parts == 1 ? run<256, 1>(a, s) : cudaErrorInvalidValue;
+    case 64: return parts == 2 ? run<64, 2>(a, groups, s) : run<64, 1>(a, groups, s);
+    case 128: return parts == 2 ? run<128, 2>(a, groups, s) : run<128, 1>(a, groups, s);
+    case 192: return parts == 2 ? run<192, 2>(a, groups, s) : run<192, 1>(a, groups, s);
+    default: return parts == 1 ? run<256, 1>(a, groups, s) : cudaErrorInvalidValue;
   }
 }
 
