@@ -94,6 +94,17 @@ __device__ __forceinline__ void mma_commit(uint32_t leader, uint64_t *bar) {
       "r"(leader)
       : "memory");
 }
+// Registers per thread of the calling warps' group of four. With two groups of rows the kernel is
+// launched with 96 (17 warps): 8 softmax warps x 128 + 8 converting x 64 + 96 = 17 x 96; all have 96
+// again for the output.
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // K-major operand tile, rows of 128 bytes, 128-byte swizzle (16-byte chunk c of row r at c ^ (r % 8)).
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
   return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
@@ -290,6 +301,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
   const uint32_t otm = tmem + lanes + C::kOCol + uint32_t(grp * D);  // its O
   if (warp < kSoft * G) {
+    if constexpr (G == 2) reg_inc<128>();
     const int pos = len - nq + row / a.group;
     const int lo_pos = a.window > 0 ? pos - a.window + 1 : 0;
     const float qs = s_qs[lr];
@@ -308,8 +320,54 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       for (int c = 0; c < 4; ++c) tmem_wait_ld16(r + 16 * c);
       const int j0 = (c0 + 4 * i) * kKvBlock;
       const bool whole = j0 >= all_lo && j0 + BN <= all_hi;
-      float f[4], mx = ninf;
+      // the reference is the row's largest score plus log2 of its value scale (see qdq_kv_attn.cu)
+      auto raise = [&](float mx) {
+        const bool grow = mx > m + (m == ninf ? 0.f : kLazy);
+        if (!__any_sync(0xffffffffu, grow)) return true;
+        const float m_new = fmaxf(m, mx);
+        const float corr = m_new > m ? ex2(m - m_new) : 1.f;
+        l *= corr;
+        m = m_new;
+        if (i > 0) {
+          if (!wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16_async(otm + c, o);
+            tmem_wait_ld16(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st16(otm + c, o);
+          }
+        }
+        return true;
+      };
+      float2 l2 = f2(0.f, 0.f), l3 = f2(0.f, 0.f);
+      // a pair of probabilities (their exponents given) into the sums and, times the value scale, into f16 parts
+      auto put = [&](float2 x, float2 vv, int e, uint32_t &hi, uint32_t &lo, bool masked) {
+        const float2 p = f2(ex2(x.x), ex2(x.y));
+        if (e & 1)
+          l3 = __fadd2_rn(l3, p);
+        else
+          l2 = __fadd2_rn(l2, p);
+        float2 pv = __fmul2_rn(p, vv);
+        if (masked) {  // a hidden token's scale may be NaN
+          if (x.x == ninf) pv.x = 0.f;
+          if (x.y == ninf) pv.y = 0.f;
+        }
+        hi = pack2(pv.x, pv.y, __half{});
+        if (PARTS == 2) {
+          const float2 back = unpack2(hi, __half{});
+          lo = pack2(pv.x - back.x, pv.y - back.y, __half{});
+        }
+      };
+      auto store_p = [&](int c, const uint32_t *hi, const uint32_t *lo) {
+        tmem_st8(sp + 8 * c, hi);
+        if (PARTS == 2) tmem_st8(sp + BN / 2 + 8 * c, lo);
+      };
       if (whole && !(a.softcap > 0.f) && !a.slopes) {
+        float f[4], mx = ninf;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float bm = fmaxf(__uint_as_float(r[16 * c]), __uint_as_float(r[16 * c + 1]));
@@ -322,7 +380,20 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           f[c] = qs * s_blk[4 * i + c].ks;
           mx = fmaxf(mx, fmaf(fmaxf(bm, bn), f[c], s_blk[4 * i + c].lv));
         }
+        if (!raise(mx)) break;
+        const float mref = m == ninf ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float vs = s_blk[4 * i + c].vs;
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            put(__ffma2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(f[c], f[c]), f2(-mref, -mref)), f2(vs, vs), e,
+                hi[e], lo[e], false);
+          store_p(c, hi, lo);
+        }
       } else {
+        float mx = ninf;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float fc = qs * s_blk[4 * i + c].ks;
@@ -338,58 +409,18 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
             r[16 * c + e] = __float_as_uint(x);
           }
           mx = fmaxf(mx, bm + s_blk[4 * i + c].lv);
-          f[c] = 1.f;
         }
-      }
-      // the reference is the row's largest score plus log2 of its value scale (see qdq_kv_attn.cu)
-      const bool grow = mx > m + (m == ninf ? 0.f : kLazy);
-      if (__any_sync(0xffffffffu, grow)) {
-        const float m_new = fmaxf(m, mx);
-        const float corr = m_new > m ? ex2(m - m_new) : 1.f;
-        l *= corr;
-        m = m_new;
-        if (i > 0) {
-          if (!wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16_async(otm + c, o);
-            tmem_wait_ld16(o);
+        if (!raise(mx)) break;
+        const float mref = m == ninf ? 0.f : m;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st16(otm + c, o);
-          }
+        for (int c = 0; c < 4; ++c) {
+          const float vs = s_blk[4 * i + c].vs;
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            put(__fadd2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(-mref, -mref)), f2(vs, vs), e, hi[e], lo[e], true);
+          store_p(c, hi, lo);
         }
-      }
-      const float mref = m == ninf ? 0.f : m;
-      float2 l2 = f2(0.f, 0.f), l3 = f2(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float vs = s_blk[4 * i + c].vs;
-        const float2 ff = f2(f[c], f[c]), mm = f2(-mref, -mref), vv = f2(vs, vs);
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 x = __ffma2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), ff, mm);
-          const float2 p = f2(ex2(x.x), ex2(x.y));
-          if (e & 1)
-            l3 = __fadd2_rn(l3, p);
-          else
-            l2 = __fadd2_rn(l2, p);
-          float2 pv = __fmul2_rn(p, vv);
-          if (!whole) {  // a hidden token's scale may be NaN
-            if (x.x == ninf) pv.x = 0.f;
-            if (x.y == ninf) pv.y = 0.f;
-          }
-          hi[e] = pack2(pv.x, pv.y, __half{});
-          if (PARTS == 2) {
-            const float2 back = unpack2(hi[e], __half{});
-            lo[e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
-          }
-        }
-        tmem_st8(sp + 8 * c, hi);
-        if (PARTS == 2) tmem_st8(sp + BN / 2 + 8 * c, lo);
       }
       l += (l2.x + l2.y) + (l3.x + l3.y);
       tmem_wait_st();
@@ -397,8 +428,10 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.pready[grp][b]);
     }
+    if constexpr (G == 2) reg_dec<96>();
   } else if (warp < kSoft * G + kConv) {
     // ---------------- codes to f16 tiles ----------------
+    if constexpr (G == 2) reg_dec<64>();
     const int set = (warp - kSoft * G) >> 2, w = (warp - kSoft * G) & 3;  // tiles set, set + 2, ...
     constexpr int KL = D / 32;            // 16-byte loads of keys per thread: tokens 16 w .. 16 w + 15 of the tile
     constexpr int VG = (D / 32 + 3) / 4;  // groups of 32 dims of the values per warp
@@ -473,6 +506,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       if (lane == 0) mbar_arrive(&bars.vfull[set]);
       if (i + 2 < nt) load(i + 2);  // after the fences, which would wait for these loads
     }
+    if constexpr (G == 2) reg_inc<96>();  // waits for the softmax warps' registers
   } else {
     // ---------------- products ----------------
     const uint32_t leader = elect_lane();
