@@ -122,7 +122,9 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
 }
 
 size_t qdq_kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim) {
-  if (n_seqs < 1 || max_q < 1 || max_kv_len < 0 || max_kv_len > QDQ_MAX_KV_LEN || n_kv < 1 || n_heads < 1 || n_heads % n_kv || !dim_ok(head_dim)) return 0;
+  if (n_seqs < 1 || max_q < 1 || max_kv_len < 0 || max_kv_len > QDQ_MAX_KV_LEN || n_kv < 1 || n_heads < 1 || n_heads % n_kv || !dim_ok(head_dim) ||
+      max_q > (1 << 20) || n_heads / n_kv > 1024)
+    return 0;
   return kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim);
 }
 
@@ -137,7 +139,7 @@ int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, 
   if (!type_ok(type) || max_q < 0 || (!cu_q && max_q != 1) || max_kv_len < 0 || n_heads < 1 || n_heads % n_kv || window < 0 ||
       !std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
     return QDQ_ERR_DIMS;
-  if (max_kv_len > QDQ_MAX_KV_LEN || max_q > (1 << 24) || int64_t(max_q) * (n_heads / n_kv) > (1 << 30)) return QDQ_ERR_UNSUPPORTED;
+  if (max_kv_len > QDQ_MAX_KV_LEN || max_q > (1 << 20) || n_heads / n_kv > 1024) return QDQ_ERR_UNSUPPORTED;
   if (!aligned(kv_len, 4) || !aligned(cu_q, 4) || !aligned(lse, 4) || !aligned(slopes, 4) || !aligned(workspace, 256))
     return QDQ_ERR_ALIGN;
   const int64_t width = int64_t(n_heads) * head_dim;

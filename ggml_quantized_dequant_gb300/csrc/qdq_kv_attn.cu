@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
   for (int i = 0; i < QR; ++i) {
     const int r = warp + i * W, row = r0 + r;
     const bool in = r < nr;
-    const int64_t base = in ? int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D + lane : 0;
+    const int qi = int(a.query_of(row));
+    const int64_t base = in ? int64_t(q0 + qi) * a.q_stride + int64_t(h * a.group + row - qi * a.group) * D + lane : 0;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       qv[i][j] = 0.f;
@@ -250,10 +251,11 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     const int lr = g + 8 * r, row = r0 + lr;
-    pos[r] = len - nq + row / a.group;
+    const int qi = int(a.query_of(row));
+    pos[r] = len - nq + qi;
     lo_pos[r] = a.window > 0 ? pos[r] - a.window + 1 : 0;
     qs[r] = s_qs[lr] * a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-    slope[r] = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row % a.group) * kLog2e : 0.f;
+    slope[r] = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row - qi * a.group) * kLog2e : 0.f;
     m[r] = ninf;
     l[r] = 0.f;
   }
@@ -663,6 +665,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.max_kv_len = max_kv_len;
   a.n_heads = n_heads;
   a.group = n_heads / c.n_kv;
+  a.group_mul = ((uint64_t(1) << 40) + uint64_t(a.group) - 1) / uint64_t(a.group);
   a.tiles = p.tiles;
   a.splits = p.splits;
   a.split_blocks = p.split_blocks;

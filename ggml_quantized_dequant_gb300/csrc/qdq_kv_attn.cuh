@@ -25,6 +25,9 @@ struct AttnArgs {
   int64_t q_stride, out_stride;
   int n_seqs, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
   float scale, softcap;
+  uint64_t group_mul;  // ceil(2^40 / group)
+  // row / group, exact while row * group < 2^40 (rows are at most 2^30, the group of a row's heads below 2^10)
+  __device__ __forceinline__ uint32_t query_of(int row) const { return uint32_t((uint64_t(uint32_t(row)) * group_mul) >> 40); }
 };
 
 // Bytes 0, 1 (lo) or 2, 3 (hi) of four excess-128 codes as two exact f16: the byte under the
@@ -53,7 +56,8 @@ struct BlockAt {
 // Four dims of one row, times inv, in the output's type.
 template <int D>
 __device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int row, int d, float4 v, float inv) {
-  const int64_t e = int64_t(q0 + row / a.group) * a.out_stride + int64_t(h * a.group + row % a.group) * D + d;
+  const int qi = int(a.query_of(row));
+  const int64_t e = int64_t(q0 + qi) * a.out_stride + int64_t(h * a.group + row - qi * a.group) * D + d;
   v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
   if (a.type == QDQ_TYPE_F32)
     store4(static_cast<float *>(a.out) + e, v);
@@ -64,15 +68,16 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int 
 }
 // M: the reference (log2 units), L: the sum of 2^(score - M)
 __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int row, float M, float L) {
+  const int qi = int(a.query_of(row));
   if (a.lse)
-    a.lse[int64_t(q0 + row / a.group) * a.n_heads + h * a.group + row % a.group] =
+    a.lse[int64_t(q0 + qi) * a.n_heads + h * a.group + row - qi * a.group] =
         L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // The tensor-core kernel (qdq_kv_attn_tc.cu): one or two groups of 128 rows to a tile, head dims that are whole 64s
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
-constexpr int kTcSplitBlocks = 512;  // blocks of 16 tokens in one split, at most
+constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one split, at most
 inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
 // Bytes of one split's partial result.
 inline size_t attn_tc_part_bytes(int head_dim, int groups) { return size_t(kTcRows) * groups * (head_dim + 2) * 4; }

@@ -17,7 +17,7 @@
 //              O is rescaled only when a reference has grown by 2^kLazy;
 //   8 warps that convert the codes, as two sets of 4 taking alternate tiles, so that the loads and
 //              the fence of one tile run beside the conversion of the other;
-//   1 warp that allocates TMEM and issues the products: S of tile i + 1 before P V of tile i, so
+//   1 warp that brings the codes (bulk copies), 1 that allocates TMEM and issues the products: S of tile i + 1 before P V of tile i, so
 //              that the tensor core works while the softmax of a tile runs.
 // One CTA per SM.  Two groups (head dims up to 128) share each tile's conversion.  Every wait is
 // bounded; one that runs out makes the CTA's rows NaN and counts in qdq_pipeline_timeouts.
@@ -30,7 +30,7 @@ __device__ unsigned int g_attn_tc_timeouts = 0;
 namespace {
 
 constexpr int BN = 64;  // tokens per tile
-constexpr int kSoft = 4, kConv = 8;  // softmax warps per group, converting warps
+constexpr int kSoft = 4, kSet = 4;  // softmax warps per group of rows, warps per converting set
 
 // ---- tcgen05 --------------------------------------------------------------------
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -94,9 +94,7 @@ __device__ __forceinline__ void mma_commit(uint32_t leader, uint64_t *bar) {
       "r"(leader)
       : "memory");
 }
-// Registers per thread of the calling warps' group of four. With two groups of rows the kernel is
-// launched with 96 (17 warps): 8 softmax warps x 128 + 8 converting x 64 + 96 = 17 x 96; all have 96
-// again for the output.
+// Registers per thread of the calling warps' group of four.
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -123,16 +121,33 @@ struct Cfg {
   static constexpr uint32_t kOCol = 2 * BN * G;  // S of group 0 (two), of group 1 (two) | O of group 0, of group 1
   static constexpr uint32_t kCols = kOCol + G * D <= 256 ? 256 : 512;
   static_assert(kOCol + G * D <= 512, "TMEM");
-  static constexpr uint32_t kBytes = 1024 + kRing + kTcSplitBlocks * uint32_t(sizeof(BlockAt));
+  // Codes wait in shared memory as stored, [keys | values, every 8 tokens 16 bytes further so that
+  // the reads of 8 tokens' words meet different banks], brought by bulk copies (the converting
+  // warps' proxy fences wait for a thread's loads in flight, not for these); 256 dims: no
+  // room, plain loads.
+  static constexpr bool kStaged = D <= 192;
+  static constexpr uint32_t kStageV = BN * D, kVStep = 8 * D + 16;
+  static constexpr uint32_t kStage = (kStageV + 8 * kVStep + 127) / 128 * 128;
+  static constexpr uint32_t kFixed = 1024 + kRing + kTcSplitBlocks * uint32_t(sizeof(BlockAt));
+  static constexpr uint32_t kLeft = 225 * 1024 - kFixed;
+  // two sets of converting warps take alternate tiles, unless only one stage fits (two parts:
+  // there the products take twice as long)
+  static constexpr int kSets = kStaged && kLeft < 2 * kStage ? 1 : 2;
+  static constexpr int kSlots = !kStaged ? 0 : kLeft >= 2 * kSets * kStage ? 2 : 1;  // stages per set
+  static constexpr uint32_t kBytes = kFixed + kSets * kSlots * kStage;
   // more than half an SM's shared memory: one CTA per SM, as the columns of TMEM want it
   static constexpr uint32_t kSmem = kBytes > 116 * 1024 ? kBytes : 116 * 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
-  static constexpr int kThreads = 32 * (kSoft * G + kConv + 1);
+  static_assert(kSmem <= 225 * 1024, "shared memory");
+  static constexpr int kConv = kSet * kSets;
+  static constexpr int kThreads = 32 * (kSoft * G + kConv + 2);
+  // 18 warps are launched with 96 registers a thread: 8 softmax warps x 128 + 8 converting x 64
+  // + 2 x 96 = 18 x 96; all have 96 again for the output
+  static constexpr bool kShift = G == 2 && kSets == 2;
 };
 
 template <int G>
 struct Bars {
-  uint64_t kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain;
+  uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain;
   uint32_t tmem;
   int abort, last;
 };
@@ -140,11 +155,12 @@ struct Bars {
 template <int D, int PARTS, int G>
 __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(const AttnArgs a) {
   using C = Cfg<D, PARTS, G>;
-  constexpr int R = kTcRows * G, kThreads = C::kThreads;
+  constexpr int R = kTcRows * G, kThreads = C::kThreads, kConv = C::kConv;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t *kring = smem + PARTS * C::kQPart, *vring = kring + 2 * C::kK;
   BlockAt *s_blk = reinterpret_cast<BlockAt *>(smem + C::kRing);
+  uint8_t *stages = smem + C::kRing + kTcSplitBlocks * sizeof(BlockAt);  // [set][slot]
   __shared__ Bars<G> bars;
   __shared__ float s_qs[R];
   const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
@@ -174,8 +190,12 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.kfull[i], kConv / 2);
-      mbar_init(&bars.vfull[i], kConv / 2);
+      mbar_init(&bars.stage[0][i], 1);
+      mbar_init(&bars.stage[1][i], 1);
+      mbar_init(&bars.sread[0][i], kSet);
+      mbar_init(&bars.sread[1][i], kSet);
+      mbar_init(&bars.kfull[i], kSet);
+      mbar_init(&bars.vfull[i], kSet);
       mbar_init(&bars.kfree[i], 1);
       for (int g = 0; g < G; ++g) {
         mbar_init(&bars.sfull[g][i], 1);
@@ -194,72 +214,81 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // the split's blocks: places and scales (past the last one: zeros, hidden from every row)
-  const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
   const int64_t vplane = int64_t(a.c.page_tokens) * D;
-  for (int i = tid; i < 4 * nt; i += kThreads) {
-    BlockAt e{-1, 0.f, 0.f, 0.f};
-    if (i < cn) {
-      const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
-      const int64_t at = kv_record_of(a.c, s, blk, h, rec);
-      if (at >= 0) {
-        const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
-        const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
-        e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale))};
-      } else {
-        e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
-      }
-    }
-    s_blk[i] = e;
-  }
-
-  // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row
+  // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row.  A lane
+  // copies its 8 dims of all its rows into the tiles' space first (all copies in flight at once,
+  // each read back by the lane that made it) and converts them in a small loop.
   if (warp < kSoft * G + kConv) {
-    constexpr int LR = D / 8 == 24 ? 32 : D / 8, RW = 32 / LR;  // lanes and rows of a warp's load
-    constexpr int kWarps = kSoft * G + kConv, kBatch = 4;
+    constexpr int LR = D / 8 == 24 ? 32 : D / 8, RW = 32 / LR;  // lanes and rows of a warp's copy
+    constexpr int kWarps = kSoft * G + kConv, kStep = kWarps * RW;
+    constexpr int kIter = (R + kStep - 1) / kStep;               // rows per lane
+    constexpr int kRoom = int(2 * (C::kK + C::kV)) / (kWarps * 512 * PARTS);
+    constexpr int kRound = kRoom < kIter ? kRoom : kIter;        // of them at a time
+    static_assert(kRound > 0, "room for the raw queries");
     const int sub = lane / LR, d = lane % LR * 8;
-    for (int rb = warp * RW; rb < R; rb += kWarps * RW * kBatch) {
-      uint4 raw0[kBatch], raw1[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = rb + i * kWarps * RW + sub, row = r0 + r;
-        raw0[i] = raw1[i] = make_uint4(0, 0, 0, 0);
+    const uint32_t mine = smem_u32(kring) + uint32_t(warp * 32 + lane) * (16 * PARTS);  // + iteration * kWarps * 512 * PARTS
+    const bool half = a.type == QDQ_TYPE_F16;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kIter; i0 += kRound) {
+#pragma unroll 1
+      for (int i = 0; i < kRound; ++i) {
+        const int r = (i0 + i) * kStep + warp * RW + sub;
         if (r < nr && d < D) {
-          const int64_t e = int64_t(q0 + row / a.group) * a.q_stride + int64_t(h * a.group + row % a.group) * D + d;
-          if (a.type == QDQ_TYPE_F32) {
-            raw0[i] = ld_u4(static_cast<const float *>(a.q) + e);
-            raw1[i] = ld_u4(static_cast<const float *>(a.q) + e + 4);
-          } else {
-            raw0[i] = ld_u4(static_cast<const uint16_t *>(a.q) + e);
-          }
+          const int qi = int(a.query_of(r0 + r));
+          const int64_t e = int64_t(q0 + qi) * a.q_stride + int64_t(h * a.group + (r0 + r - qi * a.group)) * D + d;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + i * (kWarps * 512 * PARTS) + 16 * p),
+                         "l"(static_cast<const uint8_t *>(a.q) + (PARTS == 2 ? 4 * e + 16 * p : 2 * e))
+                         : "memory");
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+      for (int i = 0; i < kRound; ++i) {
+        const int r = (i0 + i) * kStep + warp * RW + sub;
+        const bool in = r < nr && d < D;
+        uint32_t w[4 * PARTS];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = rb + i * kWarps * RW + sub;
-        float v[8];
-        const uint32_t w0[4] = {raw0[i].x, raw0[i].y, raw0[i].z, raw0[i].w}, w1[4] = {raw1[i].x, raw1[i].y, raw1[i].z, raw1[i].w};
+        for (int p = 0; p < PARTS; ++p) {
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[4 * p]), "=r"(w[4 * p + 1]), "=r"(w[4 * p + 2]), "=r"(w[4 * p + 3])
+                       : "r"(mine + i * (kWarps * 512 * PARTS) + 16 * p)
+                       : "memory");
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a.type == QDQ_TYPE_F32) {
-            v[e] = __uint_as_float(w0[e]);
-            v[4 + e] = __uint_as_float(w1[e]);
-          } else {
-            const float2 f = a.type == QDQ_TYPE_F16 ? unpack2(w0[e], __half{}) : unpack2(w0[e], __nv_bfloat16{});
+          for (int e = 0; e < 4; ++e) w[4 * p + e] = in ? w[4 * p + e] : 0u;
+        }
+        float v[8], mx;  // the elements and the row's largest magnitude (by its bits: NaN is the largest)
+        if constexpr (PARTS == 2) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = __uint_as_float(w[e]);
+            bits = max(bits, w[e] & 0x7FFFFFFFu);
+          }
+#pragma unroll
+          for (int o = LR / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+          mx = __uint_as_float(bits);
+        } else {
+          uint32_t bits = 0;  // two halves
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bits = __vmaxu2(bits, w[e] & 0x7FFF7FFFu);
+#pragma unroll
+          for (int o = LR / 2; o > 0; o >>= 1) bits = __vmaxu2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+          bits = max(bits & 0xFFFFu, bits >> 16);
+          mx = half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = half ? unpack2(w[e], __half{}) : unpack2(w[e], __nv_bfloat16{});
             v[2 * e] = f.x;
             v[2 * e + 1] = f.y;
           }
         }
-        float mx = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx = max_abs_bits(mx, v[e]);
-#pragma unroll
-        for (int o = LR / 2; o > 0; o >>= 1) mx = max_abs_bits(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const bool finite = mx < __int_as_float(0x7f800000);
         int ex = 13 - (int(__float_as_uint(mx) >> 23) - 127);
         ex = max(-120, min(120, ex));
         // the scale's sign goes into the queries, so that a larger product is a larger score
-        float up = finite ? __uint_as_float(uint32_t(ex + 127) << 23) : 0.f;
+        float up = __uint_as_float(uint32_t(ex + 127) << 23);
         if (a.scale < 0.f) up = -up;
         if (d == 0 && r < R) {
           const float q = (finite ? __uint_as_float(uint32_t(127 - ex) << 23) : qnan) * fabsf(a.scale);
@@ -268,19 +297,40 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = finite ? v[2 * e] * up : 0.f, y = finite ? v[2 * e + 1] * up : 0.f;
-          hi[e] = pack2(x, y, __half{});
-          const float2 back = unpack2(hi[e], __half{});
-          lo[e] = pack2(x - back.x, y - back.y, __half{});
+          const float x = v[2 * e] * up, y = v[2 * e + 1] * up;
+          hi[e] = finite ? pack2(x, y, __half{}) : 0u;
+          if constexpr (PARTS == 2) {
+            const float2 back = unpack2(hi[e], __half{});
+            lo[e] = finite ? pack2(x - back.x, y - back.y, __half{}) : 0u;
+          }
         }
         if (r < R && d < D) {
           uint8_t *dst = smem + ((r / kTcRows) * C::kSub + d / 64) * C::kQTile + (r % kTcRows) * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
           *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if constexpr (PARTS == 2) *reinterpret_cast<uint4 *>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  } else {
+    // meanwhile the split's blocks: places and scales (past the last one: zeros, hidden from every row)
+    const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
+#pragma unroll 2
+    for (int i = tid - 32 * (kSoft * G + kConv); i < 4 * nt; i += kThreads - 32 * (kSoft * G + kConv)) {
+      BlockAt e{-1, 0.f, 0.f, 0.f};
+      if (i < cn) {
+        const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
+        const int64_t at = kv_record_of(a.c, s, blk, h, rec);
+        if (at >= 0) {
+          const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
+          const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+          e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale))};
+        } else {
+          e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
+        }
+      }
+      s_blk[i] = e;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -301,13 +351,15 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
   const uint32_t otm = tmem + lanes + C::kOCol + uint32_t(grp * D);  // its O
   if (warp < kSoft * G) {
-    if constexpr (G == 2) reg_inc<128>();
-    const int pos = len - nq + row / a.group;
+    if constexpr (C::kShift) reg_inc<128>();
+    const int qi = int(a.query_of(row));
+    const int pos = len - nq + qi;
     const int lo_pos = a.window > 0 ? pos - a.window + 1 : 0;
     const float qs = s_qs[lr];
-    const float slope = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row % a.group) * kLog2e : 0.f;
+    const float slope = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row - qi * a.group) * kLog2e : 0.f;
     // tokens that every row of the tile sees
     const int all_lo = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0, all_hi = pos_lo + 1;
+    bool ok = true;
     for (int i = 0; i < nt; ++i) {
       const int b = i & 1;
       const uint32_t sp = tmem + lanes + uint32_t((2 * grp + b) * BN);
@@ -343,11 +395,13 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         }
         return true;
       };
-      float2 l2 = f2(0.f, 0.f), l3 = f2(0.f, 0.f);
+      float2 l2, l3;  // sums of a block's probabilities
       // a pair of probabilities (their exponents given) into the sums and, times the value scale, into f16 parts
       auto put = [&](float2 x, float2 vv, int e, uint32_t &hi, uint32_t &lo, bool masked) {
         const float2 p = f2(ex2(x.x), ex2(x.y));
-        if (e & 1)
+        if (e < 2)
+          (e ? l3 : l2) = p;
+        else if (e & 1)
           l3 = __fadd2_rn(l3, p);
         else
           l2 = __fadd2_rn(l2, p);
@@ -362,36 +416,55 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           lo = pack2(pv.x - back.x, pv.y - back.y, __half{});
         }
       };
+      auto block_sum = [&]() { return (l2.x + l2.y) + (l3.x + l3.y); };
       auto store_p = [&](int c, const uint32_t *hi, const uint32_t *lo) {
         tmem_st8(sp + 8 * c, hi);
         if (PARTS == 2) tmem_st8(sp + BN / 2 + 8 * c, lo);
       };
       if (whole && !(a.softcap > 0.f) && !a.slopes) {
-        float f[4], mx = ninf;
+        // With the reference there is: every p * vs of a block is at most the block's sum times
+        // vs, so where those stay below 2^15 (f16 ends at 2^16) no maximum is needed (64 comparisons less per
+        // row and tile: 0.4 of 1.2 us). Else, and for the first tile, the maximum and once more.
+        float f[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float bm = fmaxf(__uint_as_float(r[16 * c]), __uint_as_float(r[16 * c + 1]));
-          float bn = fmaxf(__uint_as_float(r[16 * c + 2]), __uint_as_float(r[16 * c + 3]));
+        for (int c = 0; c < 4; ++c) f[c] = qs * s_blk[4 * i + c].ks;
+        for (bool again = m == ninf;; again = true) {
+          if (__any_sync(0xffffffffu, again)) {
+            float mx = ninf;
 #pragma unroll
-          for (int e = 4; e < 16; e += 4) {
-            bm = fmaxf(fmaxf(bm, __uint_as_float(r[16 * c + e])), __uint_as_float(r[16 * c + e + 1]));
-            bn = fmaxf(fmaxf(bn, __uint_as_float(r[16 * c + e + 2])), __uint_as_float(r[16 * c + e + 3]));
+            for (int c = 0; c < 4; ++c) {
+              float bm = fmaxf(__uint_as_float(r[16 * c]), __uint_as_float(r[16 * c + 1]));
+#pragma unroll
+              for (int e = 2; e < 16; e += 2) bm = fmaxf(fmaxf(bm, __uint_as_float(r[16 * c + e])), __uint_as_float(r[16 * c + e + 1]));
+              mx = fmaxf(mx, fmaf(bm, f[c], s_blk[4 * i + c].lv));
+            }
+            again = true;
+            if (!raise(mx)) {
+              ok = false;
+              break;
+            }
           }
-          f[c] = qs * s_blk[4 * i + c].ks;
-          mx = fmaxf(mx, fmaf(fmaxf(bm, bn), f[c], s_blk[4 * i + c].lv));
-        }
-        if (!raise(mx)) break;
-        const float mref = m == ninf ? 0.f : m;
+          const float mref = m == ninf ? 0.f : m;
+          float sum = 0.f, most = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float vs = s_blk[4 * i + c].vs;
-          uint32_t hi[8], lo[8];
+          for (int c = 0; c < 4; ++c) {
+            const float vs = s_blk[4 * i + c].vs;
+            uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            put(__ffma2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(f[c], f[c]), f2(-mref, -mref)), f2(vs, vs), e,
-                hi[e], lo[e], false);
-          store_p(c, hi, lo);
+            for (int e = 0; e < 8; ++e)
+              put(__ffma2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(f[c], f[c]), f2(-mref, -mref)), f2(vs, vs), e,
+                  hi[e], lo[e], false);
+            store_p(c, hi, lo);
+            const float bs = block_sum();
+            sum += bs;
+            most = fmaxf(most, bs * vs);
+          }
+          if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) {
+            l += sum;
+            break;
+          }
         }
+        if (!ok) break;
       } else {
         float mx = ninf;
 #pragma unroll
@@ -420,47 +493,75 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           for (int e = 0; e < 8; ++e)
             put(__fadd2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(-mref, -mref)), f2(vs, vs), e, hi[e], lo[e], true);
           store_p(c, hi, lo);
+          l += block_sum();
         }
       }
-      l += (l2.x + l2.y) + (l3.x + l3.y);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.pready[grp][b]);
     }
-    if constexpr (G == 2) reg_dec<96>();
+    if constexpr (C::kShift) reg_dec<96>();
   } else if (warp < kSoft * G + kConv) {
     // ---------------- codes to f16 tiles ----------------
-    if constexpr (G == 2) reg_dec<64>();
-    const int set = (warp - kSoft * G) >> 2, w = (warp - kSoft * G) & 3;  // tiles set, set + 2, ...
-    constexpr int KL = D / 32;            // 16-byte loads of keys per thread: tokens 16 w .. 16 w + 15 of the tile
+    if constexpr (C::kShift) reg_dec<64>();
+    const int set = (warp - kSoft * G) / kSet, w = (warp - kSoft * G) % kSet;  // tiles set, set + kSets, ...
+    constexpr int KL = D / 32;            // 16-byte chunks of keys per thread: tokens 16 w .. 16 w + 15 of the tile
     constexpr int VG = (D / 32 + 3) / 4;  // groups of 32 dims of the values per warp
     uint4 kq[KL];
     uint2 vq[VG][8];
-    const int ktok = lane & 7, kch = lane >> 3;  // row and 16-dim chunk of a load
-    const int vtc = lane & 7, vd = lane >> 3;    // 8-token chunk, 8-dim part of the group
-    auto load = [&](int i) {
-      const int64_t at = s_blk[4 * i + w].k;
-      const uint8_t *p = a.c.pages + at + ktok * D + kch * 16;
-#pragma unroll
-      for (int j = 0; j < KL; ++j)  // rows + 8 (j & 1), chunks + 4 (j >> 1)
-        kq[j] = at < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(p + (j & 1) * 8 * D + (j >> 1) * 64);
-      const int64_t av = s_blk[4 * i + vtc / 2].k;
-      const uint8_t *pv = a.c.pages + av + vplane + (vtc & 1) * 8 * D + vd * 8;
-#pragma unroll
-      for (int g = 0; g < VG; ++g)
-        if (w + 4 * g < D / 32) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) vq[g][t] = av < 0 ? make_uint2(0, 0) : ld_u2(pv + t * D + (w + 4 * g) * 32);
-        }
+    const int vtc = lane & 7, vd = lane >> 3;  // 8-token chunk, 8-dim part of the group
+    // chunk j of this thread's keys: row and 16-dim chunk of the warp's 16 tokens
+    auto key_at = [&](int j, int &rr, int &ch) {
+      const int u = lane + 32 * j;
+      rr = u / (D / 16);
+      ch = u % (D / 16);
     };
-    if (set < nt) load(set);
-    uint8_t *kt = kring + set * C::kK, *vt = vring + set * C::kV;
-    for (int i = set; i < nt; i += 2) {
-      if (i >= 2 && !wait(&bars.kfree[set], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
+    uint8_t *my_stages = stages + set * C::kSlots * C::kStage;
+    int n = 0, round = 0;  // slot, and how often it has been used
+    for (int i = set; i < nt; i += C::kSets) {
+      const int b = i & 1;
+      const int64_t ak = s_blk[4 * i + w].k, av = s_blk[4 * i + vtc / 2].k;
+      if constexpr (C::kStaged) {
+        if (!wait(&bars.stage[set][n], round)) break;
+        const uint8_t *st = my_stages + n * C::kStage;
+#pragma unroll
+        for (int j = 0; j < KL; ++j)
+          kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+          if (w + 4 * g < D / 32) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
+          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.sread[set][n]);
+        if (++n == C::kSlots) {
+          n = 0;
+          ++round;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < KL; ++j)
+          kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(a.c.pages + ak + (lane + 32 * j) * 16);
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+          if (w + 4 * g < D / 32) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                : ld_u2(a.c.pages + av + vplane + ((vtc & 1) * 8 + t) * D + (w + 4 * g) * 32 + vd * 8);
+          }
+      }
+      if (i >= 2 && !wait(&bars.kfree[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
+      uint8_t *kt = kring + b * C::kK, *vt = vring + b * C::kV;
 #pragma unroll
       for (int j = 0; j < KL; ++j) {
-        const int rr = 16 * w + 8 * (j & 1) + ktok, ch = kch + 4 * (j >> 1);
+        int rr, ch;
+        key_at(j, rr, ch);
+        rr += 16 * w;
         const uint32_t q[4] = {kq[j].x, kq[j].y, kq[j].z, kq[j].w};
         uint32_t o[8];
 #pragma unroll
@@ -476,8 +577,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.kfull[set]);
-      if (i >= 2 && !wait(&bars.pvdone[G - 1][set], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
+      if (lane == 0) mbar_arrive(&bars.kfull[b]);
+      if (i >= 2 && !wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
 #pragma unroll
       for (int g = 0; g < VG; ++g)
         if (w + 4 * g < D / 32) {
@@ -503,10 +604,46 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.vfull[set]);
-      if (i + 2 < nt) load(i + 2);  // after the fences, which would wait for these loads
+      if (lane == 0) mbar_arrive(&bars.vfull[b]);
     }
-    if constexpr (G == 2) reg_inc<96>();  // waits for the softmax warps' registers
+    if constexpr (C::kShift) reg_inc<96>();  // waits for the softmax warps' registers
+  } else if (warp == kSoft * G + kConv + 1) {
+    // ---------------- copies of the codes ----------------
+    if constexpr (C::kStaged) {
+      if (lane == 0) {
+        int done = 0;  // tiles whose copies have been issued
+        for (int i = 0; i < nt; ++i, ++done) {
+          const int set = i % C::kSets, use = i / C::kSets, n = use % C::kSlots;  // the set's use-th tile
+          if (use >= C::kSlots && !mbar_wait(&bars.sread[set][n], uint32_t(use / C::kSlots - 1) & 1u)) {
+            give_up();
+            break;
+          }
+          uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
+          uint64_t *bar = &bars.stage[set][n];
+          int64_t at[4];
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            at[b] = s_blk[4 * i + b].k;
+            bytes += at[b] >= 0 ? 32 * D : 0;
+          }
+          mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (at[b] < 0) continue;  // no such block: its part of the stage is not read
+            const uint8_t *p = a.c.pages + at[b];
+            bulk_copy_g2s(dst + b * 16 * D, p, 16 * D, bar);
+            bulk_copy_g2s(dst + C::kStageV + (2 * b) * C::kVStep, p + vplane, 8 * D, bar);
+            bulk_copy_g2s(dst + C::kStageV + (2 * b + 1) * C::kVStep, p + vplane + 8 * D, 8 * D, bar);
+          }
+        }
+        // no copy may be in flight when the CTA ends, also after giving up: each stage's last one
+        for (int i = max(0, done - C::kSets * C::kSlots); i < done; ++i)
+          if (!mbar_wait(&bars.stage[i % C::kSets][i / C::kSets % C::kSlots], uint32_t(i / C::kSets / C::kSlots) & 1u))
+            atomicAdd(&g_attn_tc_timeouts, 1u);
+      }
+      __syncwarp();
+    }
   } else {
     // ---------------- products ----------------
     const uint32_t leader = elect_lane();
@@ -626,7 +763,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   __syncthreads();
   if (!bars.last) return;
   __threadfence();
-  constexpr int kShares = kThreads / R;
+  constexpr int kShares = kThreads / R;  // whole ones
   const float *all = a.partial + int64_t(unit) * a.splits * kPart;
   const int jr = tid % R, share = tid / R;
   if (share >= kShares || jr >= nr) return;
