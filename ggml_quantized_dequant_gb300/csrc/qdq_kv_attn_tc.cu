@@ -359,142 +359,129 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     const float slope = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row - qi * a.group) * kLog2e : 0.f;
     // tokens that every row of the tile sees
     const int all_lo = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0, all_hi = pos_lo + 1;
-    bool ok = true;
     for (int i = 0; i < nt; ++i) {
       const int b = i & 1;
       const uint32_t sp = tmem + lanes + uint32_t((2 * grp + b) * BN);
       if (!wait(&bars.sfull[grp][b], i >> 1)) break;
       tc_fence_after();
-      uint32_t r[BN];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld16_async(sp + 16 * c, r + 16 * c);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld16(r + 16 * c);
       const int j0 = (c0 + 4 * i) * kKvBlock;
       const bool whole = j0 >= all_lo && j0 + BN <= all_hi;
-      // the reference is the row's largest score plus log2 of its value scale (see qdq_kv_attn.cu)
-      auto raise = [&](float mx) {
-        const bool grow = mx > m + (m == ninf ? 0.f : kLazy);
-        if (!__any_sync(0xffffffffu, grow)) return true;
-        const float m_new = fmaxf(m, mx);
-        const float corr = m_new > m ? ex2(m - m_new) : 1.f;
-        l *= corr;
-        m = m_new;
-        if (i > 0) {
-          if (!wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1)) return false;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16_async(otm + c, o);
-            tmem_wait_ld16(o);
+      const BlockAt *blk = s_blk + 4 * i;
+      // scores of one block of 16 that need more than a factor: cap, bias, mask (log2 units)
+      auto transform = [&](int c, uint32_t *r) {
+        const float fc = qs * blk[c].ks;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st16(otm + c, o);
-          }
-        }
-        return true;
-      };
-      float2 l2, l3;  // sums of a block's probabilities
-      // a pair of probabilities (their exponents given) into the sums and, times the value scale, into f16 parts
-      auto put = [&](float2 x, float2 vv, int e, uint32_t &hi, uint32_t &lo, bool masked) {
-        const float2 p = f2(ex2(x.x), ex2(x.y));
-        if (e < 2)
-          (e ? l3 : l2) = p;
-        else if (e & 1)
-          l3 = __fadd2_rn(l3, p);
-        else
-          l2 = __fadd2_rn(l2, p);
-        float2 pv = __fmul2_rn(p, vv);
-        if (masked) {  // a hidden token's scale may be NaN
-          if (x.x == ninf) pv.x = 0.f;
-          if (x.y == ninf) pv.y = 0.f;
-        }
-        hi = pack2(pv.x, pv.y, __half{});
-        if (PARTS == 2) {
-          const float2 back = unpack2(hi, __half{});
-          lo = pack2(pv.x - back.x, pv.y - back.y, __half{});
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + 16 * c + e;
+          float x = __uint_as_float(r[e]) * fc;
+          if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x / a.softcap);
+          if (a.slopes) x = fmaf(-slope, float(pos - j), x);
+          if (j > pos || j < lo_pos) x = ninf;
+          r[e] = __float_as_uint(x);
         }
       };
-      auto block_sum = [&]() { return (l2.x + l2.y) + (l3.x + l3.y); };
-      auto store_p = [&](int c, const uint32_t *hi, const uint32_t *lo) {
-        tmem_st8(sp + 8 * c, hi);
-        if (PARTS == 2) tmem_st8(sp + BN / 2 + 8 * c, lo);
-      };
-      if (whole && !(a.softcap > 0.f) && !a.slopes) {
-        // With the reference there is: every p * vs of a block is at most the block's sum times
-        // vs, so where those stay below 2^15 (f16 ends at 2^16) no maximum is needed (64 comparisons less per
-        // row and tile: 0.4 of 1.2 us). Else, and for the first tile, the maximum and once more.
-        float f[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = qs * s_blk[4 * i + c].ks;
-        for (bool again = m == ninf;; again = true) {
-          if (__any_sync(0xffffffffu, again)) {
-            float mx = ninf;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float bm = fmaxf(__uint_as_float(r[16 * c]), __uint_as_float(r[16 * c + 1]));
-#pragma unroll
-              for (int e = 2; e < 16; e += 2) bm = fmaxf(fmaxf(bm, __uint_as_float(r[16 * c + e])), __uint_as_float(r[16 * c + e + 1]));
-              mx = fmaxf(mx, fmaf(bm, f[c], s_blk[4 * i + c].lv));
-            }
-            again = true;
-            if (!raise(mx)) {
-              ok = false;
-              break;
-            }
-          }
-          const float mref = m == ninf ? 0.f : m;
-          float sum = 0.f, most = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float vs = s_blk[4 * i + c].vs;
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              put(__ffma2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(f[c], f[c]), f2(-mref, -mref)), f2(vs, vs), e,
-                  hi[e], lo[e], false);
-            store_p(c, hi, lo);
-            const float bs = block_sum();
-            sum += bs;
-            most = fmaxf(most, bs * vs);
-          }
-          if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) {
-            l += sum;
-            break;
-          }
-        }
-        if (!ok) break;
-      } else {
-        float mx = ninf;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float fc = qs * s_blk[4 * i + c].ks;
-          float bm = ninf;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = j0 + 16 * c + e;
-            float x = __uint_as_float(r[16 * c + e]) * fc;
-            if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x / a.softcap);
-            if (a.slopes) x = fmaf(-slope, float(pos - j), x);
-            if (j > pos || j < lo_pos) x = ninf;
-            bm = fmaxf(bm, x);
-            r[16 * c + e] = __float_as_uint(x);
-          }
-          mx = fmaxf(mx, bm + s_blk[4 * i + c].lv);
-        }
-        if (!raise(mx)) break;
+      uint32_t hi[4][8], lo[4][PARTS == 2 ? 8 : 1];
+      float sum, most;  // of the tile's probabilities; largest sum of a block's times its value scale
+      // the tile's probabilities for the present reference, from S in TMEM, a block of 16 at a time
+      auto probabilities = [&](auto plain) {
+        constexpr bool kPlain = decltype(plain)::value;
         const float mref = m == ninf ? 0.f : m;
+        const float2 mm = f2(-mref, -mref);
+        uint32_t r[2][16];
+        tmem_ld16_async(sp, r[0]);
+        sum = most = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float vs = s_blk[4 * i + c].vs;
-          uint32_t hi[8], lo[8];
+          uint32_t *x = r[c & 1];
+          tmem_wait_ld16(x);
+          if (c < 3) tmem_ld16_async(sp + 16 * (c + 1), r[(c + 1) & 1]);
+          if constexpr (!kPlain) transform(c, x);
+          const float f = kPlain ? qs * blk[c].ks : 1.f, vs = blk[c].vs;
+          float2 l2, l3;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            put(__fadd2_rn(f2_bits(r[16 * c + 2 * e], r[16 * c + 2 * e + 1]), f2(-mref, -mref)), f2(vs, vs), e, hi[e], lo[e], true);
-          store_p(c, hi, lo);
-          l += block_sum();
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = kPlain ? __ffma2_rn(f2_bits(x[2 * e], x[2 * e + 1]), f2(f, f), mm)
+                                    : __fadd2_rn(f2_bits(x[2 * e], x[2 * e + 1]), mm);
+            const float2 p = f2(ex2(y.x), ex2(y.y));
+            if (e == 0) l2 = p;
+            else if (e == 1) l3 = p;
+            else if (e & 1) l3 = __fadd2_rn(l3, p);
+            else l2 = __fadd2_rn(l2, p);
+            float2 pv = __fmul2_rn(p, f2(vs, vs));
+            if constexpr (!kPlain) {  // a hidden token's scale may be NaN
+              if (y.x == ninf) pv.x = 0.f;
+              if (y.y == ninf) pv.y = 0.f;
+            }
+            hi[c][e] = pack2(pv.x, pv.y, __half{});
+            if constexpr (PARTS == 2) {
+              const float2 back = unpack2(hi[c][e], __half{});
+              lo[c][e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
+            }
+          }
+          const float bs = (l2.x + l2.y) + (l3.x + l3.y);
+          sum += bs;
+          most = fmaxf(most, bs * vs);
         }
+      };
+      // the largest score plus log2 of its value scale
+      auto largest = [&](bool plain) {
+        float mx = ninf;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[16];
+          tmem_ld16_async(sp + 16 * c, x);
+          tmem_wait_ld16(x);
+          if (!plain) transform(c, x);
+          float bm = __uint_as_float(x[0]);
+#pragma unroll
+          for (int e = 1; e < 16; ++e) bm = fmaxf(bm, __uint_as_float(x[e]));
+          mx = fmaxf(mx, plain ? fmaf(bm, qs * blk[c].ks, blk[c].lv) : bm + blk[c].lv);
+        }
+        return mx;
+      };
+      // Every p * vs of a block is at most the block's sum of p times vs: where those stay below
+      // 2^15 (f16 ends at 2^16) with the reference there is, no maximum is looked for (64
+      // comparisons less per row and tile).  Else, and for a row's first tile, the maximum moves
+      // the reference and the probabilities are computed once more.
+      const bool plain = whole && !(a.softcap > 0.f) && !a.slopes;
+      bool again = __any_sync(0xffffffffu, m == ninf), ok = true;
+      for (;;) {
+        if (again) {  // the reference: see qdq_kv_attn.cu
+          const float m_new = fmaxf(m, largest(plain));
+          const bool grow = m_new > m + (m == ninf ? 0.f : kLazy);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float corr = m_new > m ? ex2(m - m_new) : 1.f;
+            l *= corr;
+            m = m_new;
+            if (i > 0) {
+              ok = wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16_async(otm + c, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st16(otm + c, o);
+              }
+            }
+          }
+        }
+        if (plain)
+          probabilities(std::true_type{});
+        else
+          probabilities(std::false_type{});
+        if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) break;
+        again = true;
+      }
+      if (!ok) break;
+      l += sum;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // over the block's own columns of S
+        tmem_st8(sp + 16 * c, hi[c]);
+        if constexpr (PARTS == 2) tmem_st8(sp + 16 * c + 8, lo[c]);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -695,7 +682,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
-            mma_ts(leader, tmem + C::kOCol + uint32_t(g * D), tmem + uint32_t((2 * g + b) * BN + part * (BN / 2) + 8 * k),
+            mma_ts(leader, tmem + C::kOCol + uint32_t(g * D), tmem + uint32_t((2 * g + b) * BN + 16 * k + 8 * part),
                    desc_sw128(v_base + b * C::kV + k * 32), idesc_f16(kTcRows, D), (i | part | k) != 0);
         mma_commit(leader, &bars.pvdone[g][b]);
       }
