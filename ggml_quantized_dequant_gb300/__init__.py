@@ -341,6 +341,29 @@ def _type(t) -> int:
 
 
 _of = {}
+_fast = None       # the C marshalling (_fastcall.so), bound to _fast_lib's functions
+_fast_lib = None   # None: not tried yet
+
+
+def _bind_fast():
+    """Bind the C marshalling to the loaded library, once (its build is part of the library's)."""
+    global _fast, _fast_lib
+    import importlib.util
+    import torch
+    if not torch.cuda.is_available():  # nothing can be launched: the Python code checks the arguments
+        _fast_lib = False
+        return
+    _fast_lib = lib()
+    path = os.path.join(_PKG, "_fastcall.so")
+    if not os.path.exists(path):
+        raise RuntimeError("_fastcall.so is not built (%s); run __graft_entry__.build()" % path)
+    spec = importlib.util.spec_from_file_location("_fastcall", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.bind(*[ctypes.cast(getattr(_fast_lib, f), ctypes.c_void_p).value for f in (
+        "qdq_rms_norm", "qdq_kv_append", "qdq_kv_read", "qdq_kv_attention", "qdq_token_logprobs")],
+        torch.float32, torch.float16, torch.bfloat16, torch.int32)
+    _fast = m
 
 
 def _vec(name, t, kind):
@@ -349,6 +372,15 @@ def _vec(name, t, kind):
         return None
     if t.dtype is not _of[kind] or not t.is_contiguous():
         raise TypeError("%s: a contiguous %s tensor expected" % (name, kind))
+    return _cuda(name, t)
+
+
+def _cuda(name, t):
+    """Address of a CUDA tensor, None for None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise TypeError("%s: a CUDA tensor expected" % name)
     return t.data_ptr()
 
 
@@ -359,8 +391,6 @@ def _rows(name, t, width, dtype):
         return None, 0
     if t.dtype is not dtype:
         raise TypeError("%s: %s expected, got %s" % (name, dtype, t.dtype))
-    if t.is_contiguous() and t.numel() == len(t) * width and t.dim() > 1:
-        return t.data_ptr(), width
     shape, st = t.shape, t.stride()
     if len(shape) == 1:
         shape, st = (1, *shape), (width, *st)
@@ -371,19 +401,27 @@ def _rows(name, t, width, dtype):
         w *= shape[d]
     if w != width:
         raise ValueError("%s: rows of %d elements expected, got shape %s" % (name, width, tuple(t.shape)))
-    return t.data_ptr(), st[0] if shape[0] > 1 else width
+    return _cuda(name, t), st[0] if shape[0] > 1 else width
 
 
 def rms_norm(x, weight, out, rows: int, n: int, eps: float = 1e-5, residual=None, sum_out=None, q8_out=None, stream=None):
     """RMS norm of ``x + residual`` per row into ``out`` (x's type) and / or ``q8_out`` (a packed Q8_0 matrix).
 
     ``sum_out`` receives ``x + residual``; it may be ``residual`` or ``x`` itself, and ``out`` may be ``x``."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.rms_norm(x, weight, out, rows, n, eps, residual, sum_out, q8_out, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_rms_norm", status)
     ty, dt = _type(x), x.dtype
     xp, xs = _rows("x", x, n, dt)
     rp, rs = _rows("residual", residual, n, dt)
     sp, ss = _rows("sum_out", sum_out, n, dt)
     op, os_ = _rows("out", out, n, dt)
-    status = lib().qdq_rms_norm(xp, rp, _vec("weight", weight, "float32"), sp, op, _ptr(q8_out), ty, rows, n, xs, rs, ss, os_, eps,
+    status = lib().qdq_rms_norm(xp, rp, _vec("weight", weight, "float32"), sp, op, _cuda("q8_out", q8_out), ty, rows, n, xs, rs, ss, os_, eps,
                                 _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_rms_norm", status)
@@ -409,12 +447,20 @@ def _pool(pages, page_table, page_tokens, n_kv, head_dim):
     if rest or not pages.is_contiguous():
         raise ValueError("pages is not a whole number of packed pages")
     seqs, width = page_table.shape
-    return pages.data_ptr(), n, _vec("page_table", page_table, "int32"), seqs, width
+    return _cuda("pages", pages), n, _vec("page_table", page_table, "int32"), seqs, width
 
 
 def kv_append(pages, page_table, kv_len, k, v, n_kv: int, head_dim: int, page_tokens: int, cu_new=None, max_new: int = 1,
               stream=None):
     """Quantise new tokens (rows of ``k`` and ``v``) into the cache: the last tokens of each sequence's ``kv_len``."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.kv_append(pages, page_table, kv_len, k, v, n_kv, head_dim, page_tokens, cu_new, max_new, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_kv_append", status)
     ty, w = _type(k), n_kv * head_dim
     pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
     kp, ks = _rows("k", k, w, k.dtype)
@@ -427,6 +473,14 @@ def kv_append(pages, page_table, kv_len, k, v, n_kv: int, head_dim: int, page_to
 
 def kv_read(pages, page_table, start, cu, k, v, n_kv: int, head_dim: int, page_tokens: int, max_tokens: int, stream=None):
     """Write the values of cached tokens (``cu[s+1] - cu[s]`` of sequence s from ``start[s]``) to rows of ``k`` and ``v``."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.kv_read(pages, page_table, start, cu, k, v, n_kv, head_dim, page_tokens, max_tokens, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_kv_read", status)
     ty, w = _type(k), n_kv * head_dim
     pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
     kp, ks = _rows("k", k, w, k.dtype)
@@ -452,6 +506,16 @@ def kv_attention(pages, page_table, kv_len, q, out, workspace, n_heads: int, n_k
                  max_kv_len: int, cu_q=None, max_q: int = 1, scale: float | None = None, softcap: float = 0.0,
                  window: int = 0, slopes=None, lse=None, stream=None):
     """Attention of the rows of ``q`` over the cached tokens into ``out`` (``scale`` defaults to head_dim ** -0.5)."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.kv_attention(pages, page_table, kv_len, q, out, workspace, n_heads, n_kv, head_dim, page_tokens,
+                                    max_kv_len, cu_q, max_q, head_dim ** -0.5 if scale is None else scale, softcap, window,
+                                    slopes, lse, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_kv_attention", status)
     ty, w = _type(q), n_heads * head_dim
     pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
     qp, qs = _rows("q", q, w, q.dtype)
@@ -459,7 +523,7 @@ def kv_attention(pages, page_table, kv_len, q, out, workspace, n_heads: int, n_k
     status = lib().qdq_kv_attention(
         pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32"), _vec("cu_q", cu_q, "int32"), seqs,
         max_q, max_kv_len, n_heads, qp, qs, op, os_, _vec("lse", lse, "float32"), _vec("slopes", slopes, "float32"),
-        head_dim ** -0.5 if scale is None else scale, softcap, window, ty, workspace.data_ptr(), workspace.nbytes,
+        head_dim ** -0.5 if scale is None else scale, softcap, window, ty, _cuda("workspace", workspace), workspace.nbytes,
         _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_kv_attention", status)
@@ -478,12 +542,21 @@ def token_logprobs_workspace(rows: int, n: int, k: int, device="cuda"):
 def token_logprobs(logits, tokens, logprob, entropy, rows: int, n: int, workspace, k: int = 0, top_index=None,
                    top_logprob=None, stream=None):
     """Per row: the log probability of ``tokens[r]``, the entropy, and the k best (index, log probability) pairs."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.token_logprobs(logits, tokens, logprob, entropy, rows, n, workspace, k, top_index, top_logprob,
+                                      _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_token_logprobs", status)
     ty = _type(logits)
     xp, xs = _rows("logits", logits, n, logits.dtype)
     status = lib().qdq_token_logprobs(
         xp, xs, ty, _vec("tokens", tokens, "int32"), rows, n, k, _vec("logprob", logprob, "float32"),
         _vec("entropy", entropy, "float32"), _vec("top_index", top_index, "int32"), _vec("top_logprob", top_logprob, "float32"),
-        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+        _cuda("workspace", workspace), workspace.nbytes, _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_token_logprobs", status)
 

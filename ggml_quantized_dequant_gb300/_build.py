@@ -34,6 +34,23 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+FASTCALL_SRC = os.path.join(PKG, "_fastcall.cpp")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
+
+
+def build_fastcall() -> str:
+    """Compile the binding's C argument marshalling (a plain Python extension module, host code only)."""
+    import sysconfig
+    inc = sysconfig.get_paths()["include"]
+    cmd = [_nvcc(), "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", inc,
+           "-o", FASTCALL + ".tmp", FASTCALL_SRC]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("building _fastcall failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(FASTCALL + ".tmp", FASTCALL)
+    return FASTCALL
+
+
 LIB_CHECKED = os.path.join(PKG, "libqdq_checked.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checks")
 
@@ -56,6 +73,9 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None, c
     (qdq_check_status) instead of accessing them.
     """
     bdir, lib = (BUILD_CHECKED, LIB_CHECKED) if checks else (BUILD, LIB)
+    if not checks and (force or not os.path.exists(FASTCALL)
+                       or os.path.getmtime(FASTCALL) < max(os.path.getmtime(f) for f in (FASTCALL_SRC, os.path.join(INCLUDE, "qdq.h")))):
+        build_fastcall()
     os.makedirs(bdir, exist_ok=True)
     srcs = sources()
     objs = [os.path.join(bdir, os.path.basename(s)[:-3] + ".o") for s in srcs]

@@ -169,6 +169,8 @@ def test_binding_refuses_wrong_tensors(qdq):
         qdq.rms_norm(x.t().contiguous().t(), None, torch.zeros(4, 64), 4, 64)
     with pytest.raises(TypeError):
         qdq.token_logprobs(x, torch.zeros(4, dtype=torch.int64), torch.zeros(4), None, 4, 64, torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        qdq.rms_norm(x, None, x.clone(), 4, 64)  # not on the device
     pages = torch.zeros(3, 2176, dtype=torch.uint8)
     table = torch.zeros(1, 2, dtype=torch.int64)
     with pytest.raises(TypeError):
