@@ -4,14 +4,19 @@
 //   lse = log sum_i e^x_i,  logprob = x_t - lse,  entropy = lse - sum_i e^(x_i - lse) x_i
 //   top: the k first of the order of qdq_topk_rows, with their log probabilities
 //
-// A row is cut into segments (one CTA each) of tiles of 4096 logits.  A thread keeps its own
-// running maximum M, l = sum 2^y and u = sum 2^y y with y = (x - M) log2(e) (the difference
-// first: a mask of the type's lowest value must not turn into an infinity), so the
-// tiles need no barrier for the sums; the threads' triples are joined at the end.  The top k:
-// the k-th largest of 64 maxima of the first tile (each over the same number of logits) is a
-// lower bound of the row's k-th best, so only the few logits at or above it become 64-bit keys
-// in shared memory; they are sorted 64 at a time by warps and folded into the best 64 so far,
-// whose k-th then is the bound.  Segments of one row are joined by the CTA that finishes last.
+// A row is cut into segments (one CTA each) of tiles of 4096 logits, the next tile's loads in
+// flight while one is worked on.  A thread keeps its own running maximum M, l = sum 2^y and
+// u = sum 2^y y with y = (x - M) log2(e) (the difference first: a mask of the type's lowest value
+// must not turn into an infinity), so the tiles need no barrier for the sums; the threads'
+// triples are joined at the end.  The top k: the k-th largest of 64 maxima of the first tile (each
+// over the same number of logits) is a lower bound of the row's k-th best, so only the few logits
+// at or above it become 64-bit keys, in a list per warp; a list that fills is cut to its best 64 by
+// the warp.  What the lists hold at the end is ranked by counting the larger keys (all threads
+// at once; sorting networks of one warp took three times as long) or, where they are many, folded
+// by sorting networks.  Segments of one row are joined by the CTA that finishes last: the k-th
+// largest of the segments' first few keys bounds what has to be ranked.
+#include <type_traits>
+
 #include "qdq_types.cuh"
 
 namespace qdq {
@@ -21,8 +26,10 @@ constexpr int kThreads = 256;
 constexpr int kPer = 16;                     // logits per thread and tile
 constexpr int kTile = kThreads * kPer;
 constexpr int kTop = QDQ_MAX_TOPK;
-constexpr int kBuf = kTile + 256;            // candidate keys: a full tile and what waits
 constexpr int kWarps = kThreads / 32;
+constexpr int kList = 64 + 32 * kPer;       // a warp's keys: 64 kept and a tile's share
+constexpr int kBuf = kWarps * kList;
+constexpr int kRank = 256;                  // keys that are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -65,15 +72,22 @@ __device__ __forceinline__ Stat shfl_stat(const Stat &a, int o) {
   return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.l, o), __shfl_xor_sync(0xffffffffu, a.u, o)};
 }
 
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 struct Shared {
-  uint64_t buf[kBuf];
-  uint64_t top[kTop];            // best 64 so far, descending, 0 past the end
+  uint64_t buf[kBuf];            // [warp][kList] while the tiles run
+  uint64_t top[kTop];            // best so far, descending, 0 past the end
   uint64_t list[kWarps / 2][64];
-  float group[64];
+  uint64_t rank[kRank];
+  uint32_t group[64];
   Stat stat[kWarps];
+  int fill[kWarps];              // keys in each warp's list
   int count;
   uint64_t bound;                // keys at or below it are not among the k best
-  float bound_v;                 // its value
   int last;
 };
 
@@ -82,26 +96,40 @@ __device__ __forceinline__ float key_value(uint64_t key) {
   return o == 0xFFFFFFFFu ? __int_as_float(0x7fffffff) : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
-// Folds the `count` keys of sh.buf into sh.top and raises the bound.  All threads call it.
-__device__ void fold_candidates(Shared &sh, int count, int k) {
+// The best of the n <= kRank keys of sh.rank, sorted, into sh.top (0 past the n-th); keys that are
+// not 0 are distinct.  All threads call it; sh.rank is written before a barrier.
+__device__ void rank_keys(Shared &sh, int n) {
+  const int tid = threadIdx.x;
+  int share = 1;  // threads per key
+  while (share < 8 && 2 * share * n <= kThreads) share *= 2;
+  if (tid < kTop) sh.top[tid] = 0;
+  __syncthreads();
+  const int i = tid / share, part = tid % share;
+  const uint64_t mine = i < n ? sh.rank[i] : 0ull;
+  int r = 0;
+  for (int j = part; j < n; j += share) r += sh.rank[j] > mine;
+  for (int o = 1; o < share; o *= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+  if (part == 0 && i < n && mine != 0 && r < kTop) sh.top[r] = mine;
+  __syncthreads();
+}
+
+// The best 64 of `count` keys of sh.buf, sorted, into sh.top.  All threads call it; count is the
+// same for all, the keys are written before a barrier.
+__device__ void sort_keys(Shared &sh, int count) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t a = 0, b = 0;
-  bool any = false;
   for (int base = 64 * warp; base < count; base += 64 * kWarps) {
     uint64_t c = base + lane < count ? sh.buf[base + lane] : 0ull;
     uint64_t d = base + 32 + lane < count ? sh.buf[base + 32 + lane] : 0ull;
     warp_sort64_desc(c, d, lane);
-    if (!any) {
+    if (base == 64 * warp) {
       a = c;
       b = d;
-      any = true;
     } else {
       warp_top64_merge(a, b, c, d, lane);
     }
   }
-  if (warp == 0) warp_top64_merge(a, b, sh.top[lane], sh.top[lane + 32], lane);
   for (int half = kWarps / 2; half >= 1; half >>= 1) {
-    if (count <= 64 * half) continue;  // warps past the keys have nothing
     if (warp >= half && warp < 2 * half) {
       sh.list[warp - half][lane] = a;
       sh.list[warp - half][lane + 32] = b;
@@ -110,27 +138,17 @@ __device__ void fold_candidates(Shared &sh, int count, int k) {
     if (warp < half) warp_top64_merge(a, b, sh.list[warp][lane], sh.list[warp][lane + 32], lane);
     __syncthreads();
   }
-  __syncthreads();
   if (warp == 0) {
     sh.top[lane] = a;
     sh.top[lane + 32] = b;
-    const uint64_t ka = __shfl_sync(0xffffffffu, a, (k - 1) & 31), kb = __shfl_sync(0xffffffffu, b, (k - 1) & 31);
-    const uint64_t kk = k <= 32 ? ka : kb;
-    if (lane == 0) {
-      if (kk > sh.bound) {
-        sh.bound = kk;
-        sh.bound_v = key_value(kk);
-      }
-      sh.count = 0;
-    }
   }
   __syncthreads();
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared &sh = *reinterpret_cast<Shared *>(raw);
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x % a.segs, row = blockIdx.x / a.segs;
   const int k = a.k;
@@ -142,45 +160,60 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
   const int shift = int((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const T *x0 = x - shift;
   const int lo = shift, hi = shift + a.n;  // valid elements of x0
-  if (tid < kTop) sh.top[tid] = 0;
-  if (tid == 0) {
-    sh.count = 0;
-    sh.bound = 0;
-    sh.bound_v = __int_as_float(0xff800000);
-  }
-  __syncthreads();
+  if (tid < kWarps) sh.fill[tid] = 0;
+  if (tid == 0) sh.count = 0;
   const float ninf = __int_as_float(0xff800000);
   Stat st{ninf, 0.f, 0.f};
   const int64_t e0 = int64_t(seg) * a.seg_tiles * kTile;
   const int64_t e1 = min(int64_t(hi), e0 + int64_t(a.seg_tiles) * kTile);
 
-  float v[kPer];
+  // a tile's logits as loaded, -inf outside the row
+  uint4 raw[kPer / V];
   auto load = [&](int64_t base) {
 #pragma unroll
     for (int i = 0; i < kPer / V; ++i) {
       const int64_t e = base + (int64_t(i) * kThreads + tid) * V;
       if (e >= lo && e + V <= hi) {
-        const uint4 w = ld_u4(x0 + e);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        raw[i] = ld_u4(x0 + e);
+      } else {
+        uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if constexpr (sizeof(T) == 4) {
-            v[4 * i + j] = __uint_as_float(ww[j]);
+            w[j] = e + j >= lo && e + j < hi ? ld_u1(x0 + e + j) : 0xff800000u;
           } else {
-            const float2 f = unpack2(ww[j], T{});
-            v[V * i + 2 * j] = f.x;
-            v[V * i + 2 * j + 1] = f.y;
+            const uint32_t pad = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+            const uint32_t p = e + 2 * j >= lo && e + 2 * j < hi ? ld_h1(x0 + e + 2 * j) : pad;
+            const uint32_t q = e + 2 * j + 1 >= lo && e + 2 * j + 1 < hi ? ld_h1(x0 + e + 2 * j + 1) : pad;
+            w[j] = p | (q << 16);
           }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[V * i + j] = e + j >= lo && e + j < hi ? load1(x0 + e + j) : ninf;
+        raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   };
-  bool first = true;
+  uint64_t *list = sh.buf + warp * kList;
+  uint64_t bound = 0;        // this warp's: keys at or below it are not among the k best
+  float bound_v = ninf;
+  if (e0 < e1) load(e0);
+  __syncthreads();
   for (int64_t base = e0; base < e1; base += kTile) {
-    load(base);
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / V; ++i) {
+      const uint32_t ww[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          v[4 * i + j] = __uint_as_float(ww[j]);
+        } else {
+          const float2 f = unpack2(ww[j], T{});
+          v[V * i + 2 * j] = f.x;
+          v[V * i + 2 * j + 1] = f.y;
+        }
+      }
+    }
+    if (base + kTile < e1) load(base + kTile);
     float tm = v[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) tm = max_nan(tm, v[i]);
@@ -192,56 +225,105 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
       st.m = m2;
     }
     const float ref = st.m == ninf ? 0.f : st.m;
+    float2 tl = f2(0.f, 0.f), tu = f2(0.f, 0.f);
+    const float2 nref = f2(-ref, -ref), log2e = f2(kLog2e, kLog2e);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float d = shift_of(v[i], ref);
-      const float e = exp2f(d);
-      st.l += e;
-      st.u = fmaf(e, d, st.u);
+    for (int i = 0; i < kPer; i += 2) {
+      const float2 d = __fmul2_rn(__fadd2_rn(f2(v[i], v[i + 1]), nref), log2e);
+      const float2 e = f2(ex2_approx(d.x), ex2_approx(d.y));
+      tl = __fadd2_rn(tl, e);
+      tu = __ffma2_rn(e, d, tu);
     }
+    float u = tu.x + tu.y;
+    if (u != u) {  // 0 * -inf of a masked logit (or a NaN, which stays one in l): once more, the exponent limited
+      u = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float d = shift_of(v[i], ref);
+        u = fmaf(ex2_approx(d), d, u);
+      }
+    }
+    st.l += tl.x + tl.y;
+    st.u += u;
     if (k > 0) {
-      if (first) {  // a first bound: the k-th largest of 64 groups' maxima
-        first = false;
+      if (base == e0) {  // a first bound: the k-th largest of 64 groups' maxima
         float gm = max_nan(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
         gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-        if ((tid & 3) == 0) sh.group[tid >> 2] = gm;
+        const uint32_t mine = uint32_t(topk_key(gm, 0u) >> 32);  // its order; NaN the largest
+        const int i = tid >> 2, part = tid & 3;
+        if (part == 0) sh.group[i] = mine;
         __syncthreads();
-        if (warp == 0) {
-          // a group of padding alone gives -inf: no bound
-          uint64_t p = topk_key(sh.group[lane], 0xFFFFFFFFu), q = topk_key(sh.group[lane + 32], 0xFFFFFFFFu);
-          warp_sort64_desc(p, q, lane);
-          const uint64_t pk = __shfl_sync(0xffffffffu, p, (k - 1) & 31), qk = __shfl_sync(0xffffffffu, q, (k - 1) & 31);
-          const uint64_t kk = k <= 32 ? pk : qk;
-          const float kv = key_value(kk);
-          if (lane == 0 && kv > ninf) {  // not for NaN: those are few or the row is lost anyway
-            sh.bound = kk;
-            sh.bound_v = kv;
-          }
+        int r = 0;
+#pragma unroll 4
+        for (int j = part; j < 64; j += 4) r += sh.group[j] > mine || (sh.group[j] == mine && j < i);
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if (part == 0 && r == k - 1) sh.bound = uint64_t(mine) << 32;  // below every key of this value
+        __syncthreads();
+        bound = sh.bound;
+        bound_v = key_value(bound);
+        if (!(bound_v > ninf)) {  // padding alone, or NaN: no bound
+          bound = 0;
+          bound_v = ninf;
         }
-        __syncthreads();
       }
-      const float bv = sh.bound_v;
-      const uint64_t bk = sh.bound;
-      if (!(tm < bv)) {
+      if (!(tm < bound_v)) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int64_t e = base + (int64_t(i / V) * kThreads + tid) * V + i % V;
-          if (!(v[i] < bv) && e >= lo && e < hi) {
+          if (!(v[i] < bound_v) && e >= lo && e < hi) {
             const uint64_t key = topk_key(v[i], uint32_t(e - shift));
-            if (key > bk) sh.buf[atomicAdd(&sh.count, 1)] = key;
+            if (key > bound) list[atomicAdd(&sh.fill[warp], 1)] = key;
           }
         }
       }
-      __syncthreads();
-      const int count = sh.count;
-      if (count > kBuf - kTile) fold_candidates(sh, count, k);
-      else __syncthreads();  // nobody adds before everyone has read the count
+      __syncwarp();
+      const int fill = *reinterpret_cast<volatile int *>(&sh.fill[warp]);
+      if (fill > 64) {  // a full tile may not fit behind more: the warp keeps its best 64
+        uint64_t p = list[lane], q = list[lane + 32];
+        warp_sort64_desc(p, q, lane);
+        for (int at = 64; at < fill; at += 64) {
+          uint64_t c = at + lane < fill ? list[at + lane] : 0ull, d = at + 32 + lane < fill ? list[at + 32 + lane] : 0ull;
+          warp_sort64_desc(c, d, lane);
+          warp_top64_merge(p, q, c, d, lane);
+        }
+        __syncwarp();
+        list[lane] = p;
+        list[lane + 32] = q;
+        const uint64_t pk = __shfl_sync(0xffffffffu, p, (k - 1) & 31), qk = __shfl_sync(0xffffffffu, q, (k - 1) & 31);
+        bound = k <= 32 ? pk : qk;
+        bound_v = key_value(bound);
+        if (lane == 0) sh.fill[warp] = k;  // the first k of them
+        __syncwarp();
+      }
     }
   }
-  if (k > 0) {
-    const int count = sh.count;
+  if (k > 0) {  // the warps' lists into one, and its best k
     __syncthreads();
-    if (count > 0) fold_candidates(sh, count, k);
+    int at[kWarps], count = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      at[w] = count;
+      count += sh.fill[w];
+    }
+    if (count <= kRank) {
+      for (int i = lane; i < sh.fill[warp]; i += 32) sh.rank[at[warp] + i] = list[i];
+      __syncthreads();
+      rank_keys(sh, count);
+    } else {  // moved to the front list by list (each at or behind its new place), then sorted
+      for (int w = 1; w < kWarps; ++w) {
+        const int n = sh.fill[w];
+        uint64_t keep[(kList + kThreads - 1) / kThreads];
+#pragma unroll
+        for (int j = 0; j < int(sizeof(keep) / 8); ++j) keep[j] = tid + j * kThreads < n ? sh.buf[w * kList + tid + j * kThreads] : 0ull;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < int(sizeof(keep) / 8); ++j)
+          if (tid + j * kThreads < n) sh.buf[at[w] + tid + j * kThreads] = keep[j];
+        __syncthreads();
+      }
+      sort_keys(sh, count);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) st = join(st, shfl_stat(st, o));
@@ -280,17 +362,44 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t = join(t, shfl_stat(t, o));
     if (lane == 0) sh.stat[warp] = t;
-    if (k > 0) {  // all segments' keys, folded in batches that fit the buffer
-      if (tid < kTop) sh.top[tid] = 0;
-      if (tid == 0) sh.bound = 0;
+    if (k > 0) {
+      auto key_of = [&](int i, int j) {  // j-th key of segment i
+        return __ldcg(reinterpret_cast<const unsigned long long *>(all + size_t(i) * part + 16) + j);
+      };
+      // the k-th largest of every segment's first `few` keys bounds the k-th best of all
+      const int few = (k + a.segs - 1) / a.segs, n0 = few * a.segs;
+      uint64_t low = 0;
+      if (n0 <= kRank) {
+        for (int i = tid; i < n0; i += kThreads) sh.rank[i] = key_of(i / few, i % few);
+        if (tid == 0) sh.count = 0;
+        rank_keys(sh, n0);
+        low = sh.top[k - 1];
+        __syncthreads();
+      }
       const int total = a.segs * k;
-      for (int base = 0; base < total; base += kBuf) {
-        const int m = min(kBuf, total - base);
-        __syncthreads();
-        for (int i = tid; i < m; i += kThreads)
-          sh.buf[i] = __ldcg(reinterpret_cast<const unsigned long long *>(all + size_t((base + i) / k) * part + 16) + (base + i) % k);
-        __syncthreads();
-        fold_candidates(sh, m, k);
+      for (int i = tid; i < total; i += kThreads) {
+        const uint64_t key = key_of(i / k, i % k);
+        if (key >= low && key != 0) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kRank) sh.rank[at] = key;
+        }
+      }
+      __syncthreads();
+      const int count = sh.count;
+      __syncthreads();
+      if (count <= kRank) {
+        rank_keys(sh, count);
+      } else {  // many equal bounds: all keys, as many as fit at a time, with the best of those before
+        int have = 0;
+        for (int base = 0; base < total; base += kBuf - kTop) {
+          const int m = min(kBuf - kTop, total - base);
+          for (int i = tid; i < m; i += kThreads) sh.buf[have + i] = key_of((base + i) / k, (base + i) % k);
+          __syncthreads();
+          sort_keys(sh, have + m);
+          have = kTop;
+          if (tid < kTop) sh.buf[tid] = sh.top[tid];
+          __syncthreads();
+        }
       }
     }
     __syncthreads();
