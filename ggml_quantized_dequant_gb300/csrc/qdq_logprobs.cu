@@ -4,8 +4,9 @@
 //   lse = log sum_i e^x_i,  logprob = x_t - lse,  entropy = lse - sum_i e^(x_i - lse) x_i
 //   top: the k first of the order of qdq_topk_rows, with their log probabilities
 //
-// A row is cut into segments (one CTA each) of tiles of 4096 logits, the next tile's loads in
-// flight while one is worked on.  A thread keeps its own running maximum M, l = sum 2^y and
+// A row is cut into segments (one CTA each) of tiles of 4096 logits.  Each thread brings its own
+// 16 logits of the next tiles by asynchronous copies into shared memory (no barrier: it alone reads
+// them; in registers the compiler moved such loads behind the arithmetic).  A thread keeps its own running maximum M, l = sum 2^y and
 // u = sum 2^y y with y = (x - M) log2(e) (the difference first: a mask of the type's lowest value
 // must not turn into an infinity), so the tiles need no barrier for the sums; the threads'
 // triples are joined at the end.  The top k: the k-th largest of 64 maxima of the first tile (each
@@ -27,10 +28,13 @@ constexpr int kPer = 16;                     // logits per thread and tile
 constexpr int kTile = kThreads * kPer;
 constexpr int kTop = QDQ_MAX_TOPK;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 64 + 32 * kPer;       // a warp's keys: 64 kept and a tile's share
-constexpr int kBuf = kWarps * kList;
+constexpr int kList = 64 + 32;              // a warp's keys: 64 kept and one more of each lane
+constexpr int kStages = 3;                  // tiles in flight or in work
+constexpr int kBuf = 1024;                  // keys sorted at a time, the warps' lists among them
+static_assert(kBuf >= kWarps * kList, "room for the lists");
 constexpr int kRank = 256;                  // keys that are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kBehind = 16.f;             // natural units
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct LpArgs {
@@ -79,6 +83,7 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 
 struct Shared {
+  uint4 tile[kStages][kPer / 4][kThreads];  // (16-bit logits use half)
   uint64_t buf[kBuf];            // [warp][kList] while the tiles run
   uint64_t top[kTop];            // best so far, descending, 0 past the end
   uint64_t list[kWarps / 2][64];
@@ -164,44 +169,63 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
   if (tid == 0) sh.count = 0;
   const float ninf = __int_as_float(0xff800000);
   Stat st{ninf, 0.f, 0.f};
-  const int64_t e0 = int64_t(seg) * a.seg_tiles * kTile;
-  const int64_t e1 = min(int64_t(hi), e0 + int64_t(a.seg_tiles) * kTile);
+  const int e0 = seg * a.seg_tiles * kTile;  // below 2^30 + a tile, as hi is
+  const int e1 = min(hi, e0 + a.seg_tiles * kTile);
 
-  // a tile's logits as loaded, -inf outside the row
-  uint4 raw[kPer / V];
-  auto load = [&](int64_t base) {
+  // this thread's logits of the tile at `base` into stage n, -inf outside the row
+  const uint32_t mine = smem_u32(&sh.tile[0][0][tid]);
+  constexpr uint32_t kStageBytes = sizeof(sh.tile[0]);
+  auto fetch = [&](int base, int n) {
+    if (base < e1) {
+      const T *p = x0 + base + tid * V;
+      const uint32_t dst = mine + uint32_t(n) * kStageBytes;
+      if (base >= lo && base + kTile <= hi) {  // inside the row
 #pragma unroll
-    for (int i = 0; i < kPer / V; ++i) {
-      const int64_t e = base + (int64_t(i) * kThreads + tid) * V;
-      if (e >= lo && e + V <= hi) {
-        raw[i] = ld_u4(x0 + e);
+        for (int i = 0; i < kPer / V; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * (kThreads * 16)), "l"(p + i * (kThreads * V)) : "memory");
       } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (sizeof(T) == 4) {
-            w[j] = e + j >= lo && e + j < hi ? ld_u1(x0 + e + j) : 0xff800000u;
+#pragma unroll 1
+        for (int i = 0; i < kPer / V; ++i) {
+          const int e = base + (i * kThreads + tid) * V;
+          if (e >= lo && e + V <= hi) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * (kThreads * 16)), "l"(x0 + e) : "memory");
           } else {
-            const uint32_t pad = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
-            const uint32_t p = e + 2 * j >= lo && e + 2 * j < hi ? ld_h1(x0 + e + 2 * j) : pad;
-            const uint32_t q = e + 2 * j + 1 >= lo && e + 2 * j + 1 < hi ? ld_h1(x0 + e + 2 * j + 1) : pad;
-            w[j] = p | (q << 16);
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (sizeof(T) == 4) {
+                w[j] = e + j >= lo && e + j < hi ? ld_u1(x0 + e + j) : 0xff800000u;
+              } else {
+                const uint32_t pad = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+                const uint32_t p0 = e + 2 * j >= lo && e + 2 * j < hi ? ld_h1(x0 + e + 2 * j) : pad;
+                const uint32_t p1 = e + 2 * j + 1 >= lo && e + 2 * j + 1 < hi ? ld_h1(x0 + e + 2 * j + 1) : pad;
+                w[j] = p0 | (p1 << 16);
+              }
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + i * (kThreads * 16)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
           }
         }
-        raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   uint64_t *list = sh.buf + warp * kList;
   uint64_t bound = 0;        // this warp's: keys at or below it are not among the k best
   float bound_v = ninf;
-  if (e0 < e1) load(e0);
+#pragma unroll
+  for (int t = 0; t < kStages - 1; ++t) fetch(e0 + t * kTile, t);
   __syncthreads();
-  for (int64_t base = e0; base < e1; base += kTile) {
+  for (int n = 0, base = e0; base < e1; base += kTile) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     float v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer / V; ++i) {
-      const uint32_t ww[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint4 held;
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(held.x), "=r"(held.y), "=r"(held.z), "=r"(held.w)
+                   : "r"(mine + uint32_t(n) * kStageBytes + i * (kThreads * 16))
+                   : "memory");
+      const uint32_t ww[4] = {held.x, held.y, held.z, held.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (sizeof(T) == 4) {
@@ -213,12 +237,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
         }
       }
     }
-    if (base + kTile < e1) load(base + kTile);
+    fetch(base + (kStages - 1) * kTile, n == 0 ? kStages - 1 : n - 1);
+    n = n == kStages - 1 ? 0 : n + 1;
     float tm = v[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) tm = max_nan(tm, v[i]);
-    const float m2 = max_nan(st.m, tm);
-    if (m2 != st.m) {  // also for NaN
+    // the reference moves only when it has fallen kBehind behind (2^(kBehind log2 e) is far from the
+    // largest f32), which is rare; a NaN becomes the reference and stays it
+    if (!(tm <= st.m + kBehind)) {
+      const float m2 = max_nan(st.m, tm);
       const float d = st.l == 0.f ? 0.f : shift_of(st.m, m2), e = exp2f(d);
       st.u = e * fmaf(st.l, d, st.u);
       st.l *= e;
@@ -226,24 +253,32 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     }
     const float ref = st.m == ninf ? 0.f : st.m;
     float2 tl = f2(0.f, 0.f), tu = f2(0.f, 0.f);
-    const float2 nref = f2(-ref, -ref), log2e = f2(kLog2e, kLog2e);
+    const float yref = ref * kLog2e;
+    const float2 nref = f2(-yref, -yref), log2e = f2(kLog2e, kLog2e);
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) {
-      const float2 d = __fmul2_rn(__fadd2_rn(f2(v[i], v[i + 1]), nref), log2e);
+      const float2 d = __ffma2_rn(f2(v[i], v[i + 1]), log2e, nref);
       const float2 e = f2(ex2_approx(d.x), ex2_approx(d.y));
       tl = __fadd2_rn(tl, e);
       tu = __ffma2_rn(e, d, tu);
     }
-    float u = tu.x + tu.y;
-    if (u != u) {  // 0 * -inf of a masked logit (or a NaN, which stays one in l): once more, the exponent limited
-      u = 0.f;
+    float l = tl.x + tl.y, u = tu.x + tu.y;
+    // the exponents above are all too large by rho = ref log2(e) - yref, a rounding: first-order corrections
+    const float rho = fmaf(ref, kLog2e, -yref);
+    u = fmaf(-rho * kLn2, u, fmaf(-rho, l, u));
+    l = fmaf(-rho * kLn2, l, l);
+    // 0 * -inf of a masked logit, a NaN (it stays one in l), or a reference so large that rho is not
+    // small: once more, the difference first and the exponent limited
+    if (u != u || fabsf(ref) > 1024.f) {
+      l = u = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const float d = shift_of(v[i], ref);
-        u = fmaf(ex2_approx(d), d, u);
+        const float d = shift_of(v[i], ref), e = ex2_approx(d);
+        l += e;
+        u = fmaf(e, d, u);
       }
     }
-    st.l += tl.x + tl.y;
+    st.l += l;
     st.u += u;
     if (k > 0) {
       if (base == e0) {  // a first bound: the k-th largest of 64 groups' maxima
@@ -267,33 +302,38 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
           bound_v = ninf;
         }
       }
+      uint32_t which = 0;  // of this thread's logits, those that may be among the best: rarely any
       if (!(tm < bound_v)) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int64_t e = base + (int64_t(i / V) * kThreads + tid) * V + i % V;
-          if (!(v[i] < bound_v) && e >= lo && e < hi) {
-            const uint64_t key = topk_key(v[i], uint32_t(e - shift));
-            if (key > bound) list[atomicAdd(&sh.fill[warp], 1)] = key;
-          }
-        }
+        for (int i = 0; i < kPer; ++i) which |= v[i] < bound_v ? 0u : 1u << i;
       }
-      __syncwarp();
-      const int fill = *reinterpret_cast<volatile int *>(&sh.fill[warp]);
-      if (fill > 64) {  // a full tile may not fit behind more: the warp keeps its best 64
-        uint64_t p = list[lane], q = list[lane + 32];
-        warp_sort64_desc(p, q, lane);
-        for (int at = 64; at < fill; at += 64) {
-          uint64_t c = at + lane < fill ? list[at + lane] : 0ull, d = at + 32 + lane < fill ? list[at + 32 + lane] : 0ull;
-          warp_sort64_desc(c, d, lane);
-          warp_top64_merge(p, q, c, d, lane);
+      while (__any_sync(0xffffffffu, which != 0)) {  // one more of each lane
+        if (which) {
+          const int i = __ffs(which) - 1;
+          which &= which - 1;
+          float x = v[0];
+#pragma unroll
+          for (int j = 1; j < kPer; ++j) x = i == j ? v[j] : x;
+          const int e = base + ((i / V) * kThreads + tid) * V + i % V;
+          const uint64_t key = topk_key(x, uint32_t(e - shift));
+          if (e >= lo && e < hi && key > bound) list[atomicAdd(&sh.fill[warp], 1)] = key;
         }
         __syncwarp();
-        list[lane] = p;
-        list[lane + 32] = q;
-        const uint64_t pk = __shfl_sync(0xffffffffu, p, (k - 1) & 31), qk = __shfl_sync(0xffffffffu, q, (k - 1) & 31);
-        bound = k <= 32 ? pk : qk;
-        bound_v = key_value(bound);
-        if (lane == 0) sh.fill[warp] = k;  // the first k of them
+        const int fill = *reinterpret_cast<volatile int *>(&sh.fill[warp]);
+        if (fill > 64) {  // the next 32 may not fit: the warp keeps its best k
+          uint64_t p = list[lane], q = list[lane + 32];
+          uint64_t c = 64 + lane < fill ? list[64 + lane] : 0ull, d = 0ull;
+          warp_sort64_desc(p, q, lane);
+          warp_sort64_desc(c, d, lane);
+          warp_top64_merge(p, q, c, d, lane);
+          __syncwarp();
+          list[lane] = p;
+          list[lane + 32] = q;
+          const uint64_t pk = __shfl_sync(0xffffffffu, p, (k - 1) & 31), qk = __shfl_sync(0xffffffffu, q, (k - 1) & 31);
+          bound = k <= 32 ? pk : qk;
+          bound_v = key_value(bound);
+          if (lane == 0) sh.fill[warp] = k;
+        }
         __syncwarp();
       }
     }
@@ -310,19 +350,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
       for (int i = lane; i < sh.fill[warp]; i += 32) sh.rank[at[warp] + i] = list[i];
       __syncthreads();
       rank_keys(sh, count);
-    } else {  // moved to the front list by list (each at or behind its new place), then sorted
-      for (int w = 1; w < kWarps; ++w) {
-        const int n = sh.fill[w];
-        uint64_t keep[(kList + kThreads - 1) / kThreads];
-#pragma unroll
-        for (int j = 0; j < int(sizeof(keep) / 8); ++j) keep[j] = tid + j * kThreads < n ? sh.buf[w * kList + tid + j * kThreads] : 0ull;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < int(sizeof(keep) / 8); ++j)
-          if (tid + j * kThreads < n) sh.buf[at[w] + tid + j * kThreads] = keep[j];
-        __syncthreads();
-      }
-      sort_keys(sh, count);
+    } else {  // many: sorted, in the lists' places
+      for (int i = lane; i < kList; i += 32)
+        if (i >= sh.fill[warp]) list[i] = 0;
+      __syncthreads();
+      sort_keys(sh, kWarps * kList);
     }
   }
 #pragma unroll
@@ -436,11 +468,19 @@ struct Plan {
 Plan plan(const DeviceInfo &di, int rows, int n, int k) {
   Plan p{};
   const int tiles = int((int64_t(n) + 7 + kTile - 1) / kTile);  // a row may start up to 7 elements past a boundary
-  const int64_t want = int64_t(di.sm_count) * 8;
-  int64_t segs = (want + rows - 1) / rows;
-  if (segs > tiles) segs = tiles;
-  if (segs < 1) segs = 1;
-  p.seg_tiles = int((tiles + segs - 1) / segs);
+  // the number of segments with the least time by a simple count: waves of resident CTAs (4 per SM)
+  // times a segment's tiles and about 3 tiles' time for its start and end
+  const int64_t slots = int64_t(di.sm_count) * 4;
+  int64_t best = -1;
+  for (int segs = 1; segs <= tiles && segs <= 512; ++segs) {
+    const int per = (tiles + segs - 1) / segs;
+    if (segs > 1 && per == (tiles + segs - 2) / (segs - 1)) continue;  // no shorter than with one segment less
+    const int64_t cost = (int64_t(rows) * segs + slots - 1) / slots * (per + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.seg_tiles = per;
+    }
+  }
   p.segs = (tiles + p.seg_tiles - 1) / p.seg_tiles;
   p.ticket_bytes = (size_t(rows) * 4 + 255) / 256 * 256;
   p.bytes = p.ticket_bytes + (p.segs > 1 ? size_t(rows) * p.segs * part_bytes(k) : 0);
