@@ -30,8 +30,7 @@ constexpr int kTop = QDQ_MAX_TOPK;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 64 + 32;              // a warp's keys: 64 kept and one more of each lane
 constexpr int kStages = 3;                  // tiles in flight or in work
-constexpr int kBuf = 1024;                  // keys sorted at a time, the warps' lists among them
-static_assert(kBuf >= kWarps * kList, "room for the lists");
+constexpr int kBuf = 2048;                  // keys of other segments sorted at a time
 constexpr int kRank = 256;                  // keys that are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBehind = 16.f;             // natural units
@@ -83,11 +82,14 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 
 struct Shared {
-  uint4 tile[kStages][kPer / 4][kThreads];  // (16-bit logits use half)
-  uint64_t buf[kBuf];            // [warp][kList] while the tiles run
-  uint64_t top[kTop];            // best so far, descending, 0 past the end
-  uint64_t list[kWarps / 2][64];
-  uint64_t rank[kRank];
+  union {
+    uint4 tile[kStages][kPer / 4][kThreads];  // (16-bit logits use half)
+    struct {  // after the tiles
+      uint64_t buf[kBuf], rank[kRank], list[kWarps / 2][64];
+    };
+  };
+  uint64_t lists[kWarps][kList];  // the warps' keys
+  uint64_t top[kTop];             // best so far, descending, 0 past the end
   uint32_t group[64];
   Stat stat[kWarps];
   int fill[kWarps];              // keys in each warp's list
@@ -112,20 +114,21 @@ __device__ void rank_keys(Shared &sh, int n) {
   const int i = tid / share, part = tid % share;
   const uint64_t mine = i < n ? sh.rank[i] : 0ull;
   int r = 0;
+#pragma unroll 8
   for (int j = part; j < n; j += share) r += sh.rank[j] > mine;
   for (int o = 1; o < share; o *= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
   if (part == 0 && i < n && mine != 0 && r < kTop) sh.top[r] = mine;
   __syncthreads();
 }
 
-// The best 64 of `count` keys of sh.buf, sorted, into sh.top.  All threads call it; count is the
-// same for all, the keys are written before a barrier.
-__device__ void sort_keys(Shared &sh, int count) {
+// The best 64 of `count` keys (not among sh.list), sorted, into sh.top.  All threads call it; count
+// is the same for all, the keys are written before a barrier.
+__device__ void sort_keys(Shared &sh, const uint64_t *keys, int count) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t a = 0, b = 0;
   for (int base = 64 * warp; base < count; base += 64 * kWarps) {
-    uint64_t c = base + lane < count ? sh.buf[base + lane] : 0ull;
-    uint64_t d = base + 32 + lane < count ? sh.buf[base + 32 + lane] : 0ull;
+    uint64_t c = base + lane < count ? keys[base + lane] : 0ull;
+    uint64_t d = base + 32 + lane < count ? keys[base + 32 + lane] : 0ull;
     warp_sort64_desc(c, d, lane);
     if (base == 64 * warp) {
       a = c;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint64_t *list = sh.buf + warp * kList;
+  uint64_t *list = sh.lists[warp];
   uint64_t bound = 0;        // this warp's: keys at or below it are not among the k best
   float bound_v = ninf;
 #pragma unroll
@@ -338,8 +341,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (k > 0) {  // the warps' lists into one, and its best k
-    __syncthreads();
+    __syncthreads();  // from here the tiles' space is used for keys
     int at[kWarps], count = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
       for (int i = lane; i < kList; i += 32)
         if (i >= sh.fill[warp]) list[i] = 0;
       __syncthreads();
-      sort_keys(sh, kWarps * kList);
+      sort_keys(sh, sh.lists[0], kWarps * kList);
     }
   }
 #pragma unroll
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
           const int m = min(kBuf - kTop, total - base);
           for (int i = tid; i < m; i += kThreads) sh.buf[have + i] = key_of((base + i) / k, (base + i) % k);
           __syncthreads();
-          sort_keys(sh, have + m);
+          sort_keys(sh, sh.buf, have + m);
           have = kTop;
           if (tid < kTop) sh.buf[tid] = sh.top[tid];
           __syncthreads();
@@ -488,6 +492,8 @@ Plan plan(const DeviceInfo &di, int rows, int n, int k) {
 }
 
 }  // namespace
+
+static_assert(sizeof(Shared) <= 57344, "four CTAs per SM");
 
 size_t token_logprobs_workspace_bytes(int rows, int n, int k) {
   DeviceInfo di;
