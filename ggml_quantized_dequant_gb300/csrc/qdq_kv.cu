@@ -94,12 +94,25 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int64_t rec, i
   const int64_t x0 = int64_t(first) + p0 - old;  // row of the block's token 0 (negative part never read)
 
   // the new elements' loads first: they need no page
+  // chunk i of this lane: token i / (D / 128) or (128 / D) i + lane / PT of the block
+  constexpr bool kEven = 32 % PT == 0 || PT % 32 == 0;
+  const T *x_lane = x + x0 * stride + (kEven && PT <= 32 ? (lane / PT) * stride + 4 * (lane % PT) : 4 * lane);
   Quad<T> q[C];
+  if (kEven && held == 0 && end == kKvBlock) {  // a whole block
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = lane + 32 * i, t = ch / PT;
-    q[i].clear();
-    if (t >= held && t < end) q[i].load(x + (x0 + t) * stride + 4 * (ch % PT));
+    for (int i = 0; i < C; ++i) {
+      if constexpr (PT <= 32)
+        q[i].load(x_lane + (i * (32 / PT)) * stride);
+      else
+        q[i].load(x_lane + (i / (PT / 32)) * stride + 128 * (i % (PT / 32)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int ch = lane + 32 * i, t = ch / PT;
+      q[i].clear();
+      if (t >= held && t < end) q[i].load(x + (x0 + t) * stride + 4 * (ch % PT));
+    }
   }
   const int64_t at = kv_record_of(a.c, s, blk, h, rec);
   if (at < 0) return;  // no page for these tokens: they are dropped
@@ -121,7 +134,7 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int64_t rec, i
   const float inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
   if (held && sc != s_old) {  // a larger scale: what the block held, rounded to it
     const float again = sc > 0.f ? __fdiv_rn(s_old, sc) : 0.f;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < C; ++i) {
       const int ch = lane + 32 * i, t = ch / PT;
       if (t < held) {
@@ -148,8 +161,9 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int64_t rec, i
   if (lane == 0 && (held == 0 || sc != s_old)) *scale = sc;
 }
 
+// (fewer registers for more warps: the loads' latency is what a block waits for)
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? (sizeof(T) == 2 ? 8 : 5) : 3) kv_append_kernel(const AppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
