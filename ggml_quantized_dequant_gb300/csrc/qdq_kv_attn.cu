@@ -99,8 +99,8 @@ template <int D, int PARTS, int W>
 constexpr int body_bytes() {
   constexpr int ring = W * Shape<D>::kRing, acc = W * (16 / PARTS) * D * 4;
   constexpr int join = 2 * max_splits(W) * (16 / PARTS) * 4 + W * 32 * 16;
-  static_assert(join <= (ring > acc ? ring : acc), "room for the join");
-  return ring > acc ? ring : acc;
+  constexpr int most = ring > acc ? ring : acc;
+  return most > join ? most : join;
 }
 
 // Place of four dims (quad c) in a row of accumulators in shared memory: exchanged so that the
@@ -173,10 +173,8 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
     }
     copies_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(warp + i * W, i);
-
-  // the queries' loads, then the blocks' scales, all in flight together
+  // the queries' and the scales' loads first, all in flight together: behind the ring's copies
+  // they would come microseconds later
   constexpr int QR = (R + W - 1) / W;  // rows per warp
   float qv[QR][D / 32];
 #pragma unroll
@@ -194,14 +192,26 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
                                             : load1(static_cast<const __nv_bfloat16 *>(a.q) + base + 32 * j);
     }
   }
-  for (int i = threadIdx.x; i < cn; i += kThreads) {
+  auto scales = [&](int i, float &ks, float &vs) {
     const int b = (c0 + i) % (a.c.page_tokens / kKvBlock);  // of its page
     const uint8_t *sc = a.c.pages + (s_blk[i].k - int64_t(b) * S::kPlane + 2 * vplane + 4 * b);
-    const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+    ks = __uint_as_float(ld_u1(sc));
+    vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+  };
+  auto keep = [&](int i, float ks, float vs) {
     const bool none = s_blk[i].ks != 0.f;  // no page: NaN scores
     s_blk[i].lv = log2f(fmaxf(none ? 1.f : vs, kMinScale));  // a NaN scale gives -95 here and stays NaN in vs
     s_blk[i].vs = none ? 1.f : vs * kPScale;
     if (!none) s_blk[i].ks = ks;
+  };
+  float ks0 = 0.f, vs0 = 0.f;
+  if (int(threadIdx.x) < cn) scales(threadIdx.x, ks0, vs0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(warp + i * W, i);
+  if (int(threadIdx.x) < cn) keep(threadIdx.x, ks0, vs0);
+  for (int i = threadIdx.x + kThreads; i < cn; i += kThreads) {
+    scales(i, ks0, vs0);
+    keep(i, ks0, vs0);
   }
   // the tile's queries: scaled by a power of two per row, then f16 parts
 #pragma unroll
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
         p[r][e] = (PARTS == 2 ? sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)] : sc[e >> 1][2 * r + (e & 1)]) * f;
       if (a.softcap > 0.f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[r][e] = a.softcap * kLog2e * tanhf(p[r][e] / a.softcap);
+        for (int e = 0; e < 4; ++e) p[r][e] = a.softcap * kLog2e * tanh_of(p[r][e] * a.inv_cap);
       }
       const int j0 = blk * kKvBlock + 2 * t;
       if (a.slopes) {
@@ -612,7 +622,9 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   // whose starts and ends overlap with their neighbours' work.
   p.warps = p.units <= di.sm_count || blocks > int64_t(max_splits(4)) * max_split_blocks(4) ? resident : 4;
   const int64_t per_wave = int64_t(di.sm_count) * (resident / p.warps);
-  int64_t splits = p.warps == 4 ? 2 * per_wave / p.units : per_wave / (p.units > 0 ? p.units : 1);
+  // small CTAs: four waves of them, so that sequences of different lengths even out (48 sequences
+  // of up to 8K tokens, 24 / 8 heads of 128: 78 us; two waves 87 us, eight 89 us)
+  int64_t splits = p.warps == 4 ? 4 * per_wave / p.units : per_wave / p.units;
   if (splits < 1) splits = 1;
   if (splits > max_splits(p.warps)) splits = max_splits(p.warps);
   // a split costs its join (about 3 us): not below this many blocks per warp
@@ -673,6 +685,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.type = type;
   a.scale = scale;
   a.softcap = softcap;
+  a.inv_cap = softcap > 0.f ? 1.f / softcap : 0.f;
   if (p.tc) {
     e = launch_attn_tc(a, head_dim, p.parts, p.groups, s);
     return e == cudaSuccess ? QDQ_OK : fail_cuda(e);

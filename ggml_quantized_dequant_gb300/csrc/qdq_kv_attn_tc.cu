@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         for (int e = 0; e < 16; ++e) {
           const int j = j0 + 16 * c + e;
           float x = __uint_as_float(r[e]) * fc;
-          if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x / a.softcap);
+          if (a.softcap > 0.f) x = a.softcap * kLog2e * tanh_of(x * a.inv_cap);
           if (a.slopes) x = fmaf(-slope, float(pos - j), x);
           if (j > pos || j < lo_pos) x = ninf;
           r[e] = __float_as_uint(x);
