@@ -573,13 +573,12 @@ int with_dim(int d, F &&f) {
 }
 
 constexpr int kTcMinRows = 64;    // query rows per key/value head from which on the tensor-core kernel runs
-constexpr int kTcMinBlocks = 32;  // blocks of 16 tokens that a split of it has at least
 
 struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
   int parts, groups, warps, tiles, splits, split_blocks;
   int64_t units;
-  size_t ticket_bytes, bytes;
+  size_t ticket_bytes, bytes;  // bytes: for any window
 };
 
 Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, int window,
@@ -596,17 +595,13 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     int64_t tokens = max_kv_len;
     if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
     const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
-    // two waves of CTAs (one per SM) where the tokens are many enough: tiles differ in length
-    int64_t splits = 2 * int64_t(di.sm_count) / p.units;
-    if (splits < 1) splits = 1;
-    int64_t per = ((blocks + splits - 1) / splits + 3) / 4 * 4;  // whole tiles of 64 tokens
-    if (per < kTcMinBlocks) per = kTcMinBlocks;
-    if (per > kTcSplitBlocks) per = kTcSplitBlocks;
-    p.split_blocks = int(per);
-    p.splits = int((blocks + per - 1) / per);
-    if (p.splits < 1) p.splits = 1;
+    // whole waves of CTAs (one per SM), each with at most kTcSplitBlocks of the blocks there can be
+    const int64_t most = p.units * ((blocks + 4) / 4);  // tiles of 64 tokens
+    const int64_t wave = int64_t(di.sm_count) * (kTcSplitBlocks / 4);
+    const int64_t ctas = di.sm_count * ((most + wave - 1) / wave);
+    p.splits = int(ctas < 0x7fffffff ? ctas : 0);
     p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
-    p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * attn_tc_part_bytes(head_dim, p.groups) : 0);
+    p.bytes = p.ticket_bytes + 2 * size_t(ctas) * attn_tc_part_bytes(head_dim, p.groups);
     return p;
   }
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
@@ -617,6 +612,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   int64_t tokens = max_kv_len;
   if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
   const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
+  const int64_t all_blocks = (int64_t(max_kv_len) + kKvBlock - 1) / kKvBlock;  // without a window
   const int resident = head_dim <= 128 ? 16 : 8;  // warps per SM
   // Few tiles: CTAs that fill an SM, so that a tile is cut into few splits; many: small CTAs,
   // whose starts and ends overlap with their neighbours' work.
@@ -635,7 +631,16 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   p.splits = int((blocks + per - 1) / per);
   if (p.splits < 1) p.splits = 1;
   p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
-  p.bytes = p.ticket_bytes + (p.splits > 1 ? size_t(p.units) * p.splits * R * (head_dim + 2) * 4 : 0);
+  // another window can give up to as many splits as either size of CTA aims at or is forced to
+  int64_t most = 1;
+  for (int warps : {4, resident})
+    if (warps == resident || p.units > di.sm_count) {
+      const int64_t aim = (warps == 4 ? 4 : 1) * int64_t(di.sm_count) * (resident / warps) / p.units;
+      const int64_t forced = (all_blocks + max_split_blocks(warps) - 1) / max_split_blocks(warps);
+      for (int64_t n : {aim < max_splits(warps) ? aim : max_splits(warps), forced})
+        if (n > most) most = n;
+    }
+  p.bytes = p.ticket_bytes + (most > 1 ? size_t(p.units) * size_t(most) * R * (head_dim + 2) * 4 : 0);
   return p;
 }
 
@@ -660,7 +665,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
   const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, window, type);
-  if (p.units * p.splits > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
+  if (p.splits < 1 || p.units > 0x7fffffff || (!p.tc && p.units * p.splits > 0x7fffffff)) return QDQ_ERR_UNSUPPORTED;
   AttnArgs a{};
   a.c = c;
   a.kv_len = kv_len;

@@ -88,11 +88,11 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int 
 // The tensor-core kernel (qdq_kv_attn_tc.cu): one or two groups of 128 rows to a tile, head dims that are whole 64s
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
-constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one split, at most
+constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one part, at most
 inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
-// Bytes of one split's partial result.
+// Bytes of one part's result (two per CTA).
 inline size_t attn_tc_part_bytes(int head_dim, int groups) { return size_t(kTcRows) * groups * (head_dim + 2) * 4; }
-// Launches a.tiles * n_kv * n_seqs * a.splits CTAs; parts: f16 parts of the queries and
+// Launches a.splits CTAs, of which each has at most kTcSplitBlocks blocks; parts: f16 parts of the queries and
 // probabilities; groups: of 128 rows to a tile (2 up to head_dim 128).
 cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, int groups, cudaStream_t s);
 int read_attn_tc_timeouts();

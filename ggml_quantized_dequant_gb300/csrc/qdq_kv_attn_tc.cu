@@ -1,8 +1,12 @@
 // Attention of many query rows over the paged 8-bit cache on the 5th-generation tensor cores
 // (prompt chunks; the formulas are those of qdq_kv_attn.cu).
 //
-// A CTA takes one or two groups of 128 rows (query token, head of the group) of one key/value
-// head and walks tiles of 64 tokens of its split:
+// A unit is one or two groups of 128 rows (query token, head of the group) of one key/value head;
+// its work is the tiles of 64 tokens that its rows see.  All units' tiles in one line are cut into
+// equal shares, one per CTA (causal tiles and ragged sequences differ in length; whole units dealt
+// to CTAs took twice as long), so a CTA takes the end of a unit, whole units and the start of
+// another, part by part.  A unit cut by shares is joined from its parts' accumulators by the CTA
+// that finishes last, in order.  For each tile:
 //   S = Q K^T (128 x 64, f32 in TMEM), P = 2^(S - reference) in f16 written over S in TMEM,
 //   O += P V (128 x D, f32 in TMEM).
 // Codes are exact in f16, so K and V tiles are converted in registers, without their scales, into
@@ -30,6 +34,7 @@ __device__ unsigned int g_attn_tc_timeouts = 0;
 namespace {
 
 constexpr int BN = 64;  // tokens per tile
+constexpr int kMinShare = 8;  // tiles: a part costs about as much as 8 tiles besides them
 constexpr int kSoft = 4, kSet = 4;  // softmax warps per group of rows, warps per converting set
 
 // ---- tcgen05 --------------------------------------------------------------------
@@ -95,6 +100,9 @@ __device__ __forceinline__ void mma_commit(uint32_t leader, uint64_t *bar) {
       : "memory");
 }
 // Registers per thread of the calling warps' group of four.
+__device__ __forceinline__ void named_bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -148,8 +156,10 @@ struct Cfg {
 template <int G>
 struct Bars {
   uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain;
+  static constexpr int kBars = 8 + 6 + 6 * G + 1;
+  long long sums[20], first;
   uint32_t tmem;
-  int abort, last;
+  int abort, last, entry;
 };
 
 template <int D, int PARTS, int G>
@@ -165,48 +175,78 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   __shared__ float s_qs[R];
   const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x % a.splits;
-  const int unit = blockIdx.x / a.splits;
-  // tiles of a sequence and head in reverse: with a causal mask the last see the most tokens
-  const int tile = a.tiles - 1 - unit % a.tiles, h = unit / a.tiles % a.c.n_kv, s = unit / a.tiles / a.c.n_kv;
   pdl_launch_dependents();
   pdl_wait();
 
-  const int q0 = a.cu_q ? int(ld_u1(a.cu_q + s)) : s;
-  const int nq = a.cu_q ? int(ld_u1(a.cu_q + s + 1)) - q0 : 1;
-  const int len = int(ld_u1(a.kv_len + s));
-  const int rows = nq * a.group, r0 = tile * R;
-  if (r0 >= rows) return;
-  const int nr = min(R, rows - r0);
-  const bool bad = len < 0 || len > a.max_kv_len || (len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
-  const int pos_lo = len - nq + r0 / a.group, pos_hi = len - nq + (r0 + nr - 1) / a.group;
-  const int b_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) / kKvBlock : 0;
-  const int b_hi = bad ? 0 : (pos_hi + kKvBlock) / kKvBlock;
-  const int nb = max(0, b_hi - b_lo);
-  const int nsplit = max(1, (nb + a.split_blocks - 1) / a.split_blocks);
-  if (split >= nsplit) return;
-  const int c0 = b_lo + split * a.split_blocks, cn = max(0, min(a.split_blocks, b_hi - c0));
-  const int nt = (cn + 3) / 4;  // tiles of 64 tokens
-
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.stage[0][i], 1);
-      mbar_init(&bars.stage[1][i], 1);
-      mbar_init(&bars.sread[0][i], kSet);
-      mbar_init(&bars.sread[1][i], kSet);
-      mbar_init(&bars.kfull[i], kSet);
-      mbar_init(&bars.vfull[i], kSet);
-      mbar_init(&bars.kfree[i], 1);
-      for (int g = 0; g < G; ++g) {
-        mbar_init(&bars.sfull[g][i], 1);
-        mbar_init(&bars.pready[g][i], kSoft);
-        mbar_init(&bars.pvdone[g][i], 1);
-      }
+  // ---- this CTA's share.  Entry e = (sequence, tile of rows); every entry has n_kv units of the same length.
+  struct Entry {
+    int s, q0, len, nq, rows, r0, nr, pos_lo, pos_hi, b_lo, b_hi, tiles;  // tiles: at least 1 where there are rows
+    bool bad;
+  };
+  auto entry = [&](int e) {
+    Entry x;
+    x.s = e / a.tiles;
+    x.r0 = e % a.tiles * R;
+    x.q0 = a.cu_q ? int(ld_u1(a.cu_q + x.s)) : x.s;
+    x.nq = a.cu_q ? int(ld_u1(a.cu_q + x.s + 1)) - x.q0 : 1;
+    x.len = int(ld_u1(a.kv_len + x.s));
+    x.rows = x.nq * a.group;
+    x.nr = min(R, x.rows - x.r0);
+    x.bad = x.len < 0 || x.len > a.max_kv_len || (x.len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
+    x.tiles = 0;
+    if (x.nr <= 0) return x;
+    x.pos_lo = x.len - x.nq + int(a.query_of(x.r0));
+    x.pos_hi = x.len - x.nq + int(a.query_of(x.r0 + x.nr - 1));
+    x.b_lo = a.window > 0 ? max(0, x.pos_lo - a.window + 1) / kKvBlock : 0;
+    x.b_hi = x.bad ? 0 : (x.pos_hi + kKvBlock) / kKvBlock;
+    x.tiles = max(1, (x.b_hi - x.b_lo + 3) / 4);
+    return x;
+  };
+  const int n_entries = a.n_seqs * a.tiles, chunk = (n_entries + kThreads - 1) / kThreads;
+  long long total = 0, g0, g1;  // tiles of all units; this CTA's share of them
+  int shares, e_cur;            // CTAs that have a share; the entry of g0
+  long long e_first;            // and its first tile
+  {
+    long long mine = 0;
+    for (int i = 0; i < chunk; ++i)
+      if (tid * chunk + i < n_entries) mine += entry(tid * chunk + i).tiles;
+    long long up = mine;  // inclusive sums over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
     }
-    mbar_init(&bars.drain, 1);
-    bars.abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (lane == 31) bars.sums[warp] = up;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += bars.sums[w];
+      total += bars.sums[w];
+    }
+    before += up - mine;
+    total *= a.c.n_kv;
+    before *= a.c.n_kv;
+    mine *= a.c.n_kv;
+    shares = int(min((long long)gridDim.x, max(1ll, total / kMinShare)));
+    if (total == 0 || int(blockIdx.x) >= shares) return;
+    g0 = total * blockIdx.x / shares;
+    g1 = total * (blockIdx.x + 1) / shares;
+    if (before <= g0 && g0 < before + mine) {  // one thread has the entry of g0
+      int e = tid * chunk;
+      for (;; ++e) {
+        const long long n = (long long)entry(e).tiles * a.c.n_kv;
+        if (g0 < before + n) break;
+        before += n;
+      }
+      bars.entry = e;
+      bars.first = before;
+    }
+    __syncthreads();
+    e_cur = bars.entry;
+    e_first = bars.first;
   }
+  auto owner = [&](long long g) { return int(((g + 1) * shares - 1) / total); };  // the CTA whose share has tile g
+
   if (warp == kSoft * G + kConv) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)),
                  "r"(C::kCols)
@@ -214,568 +254,631 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  const int64_t vplane = int64_t(a.c.page_tokens) * D;
-  // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row.  A lane
-  // copies its 8 dims of all its rows into the tiles' space first (all copies in flight at once,
-  // each read back by the lane that made it) and converts them in a small loop.
-  if (warp < kSoft * G + kConv) {
-    constexpr int LR = D / 8 == 24 ? 32 : D / 8, RW = 32 / LR;  // lanes and rows of a warp's copy
-    constexpr int kWarps = kSoft * G + kConv, kStep = kWarps * RW;
-    constexpr int kIter = (R + kStep - 1) / kStep;               // rows per lane
-    constexpr int kRoom = int(2 * (C::kK + C::kV)) / (kWarps * 512 * PARTS);
-    constexpr int kRound = kRoom < kIter ? kRoom : kIter;        // of them at a time
-    static_assert(kRound > 0, "room for the raw queries");
-    const int sub = lane / LR, d = lane % LR * 8;
-    const uint32_t mine = smem_u32(kring) + uint32_t(warp * 32 + lane) * (16 * PARTS);  // + iteration * kWarps * 512 * PARTS
-    const bool half = a.type == QDQ_TYPE_F16;
-#pragma unroll 1
-    for (int i0 = 0; i0 < kIter; i0 += kRound) {
-#pragma unroll 1
-      for (int i = 0; i < kRound; ++i) {
-        const int r = (i0 + i) * kStep + warp * RW + sub;
-        if (r < nr && d < D) {
-          const int qi = int(a.query_of(r0 + r));
-          const int64_t e = int64_t(q0 + qi) * a.q_stride + int64_t(h * a.group + (r0 + r - qi * a.group)) * D + d;
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + i * (kWarps * 512 * PARTS) + 16 * p),
-                         "l"(static_cast<const uint8_t *>(a.q) + (PARTS == 2 ? 4 * e + 16 * p : 2 * e))
-                         : "memory");
+  bool started = false;
+  for (; g0 < g1;) {  // part by part
+    const Entry en = entry(e_cur);
+    const int h = int((g0 - e_first) / en.tiles);             // the unit: this entry and head
+    const long long u_first = e_first + (long long)h * en.tiles;
+    const int t0 = int(g0 - u_first), t1 = int(min((long long)en.tiles, g1 - u_first));  // its tiles in this part
+    const int c_lo = owner(u_first), nsplit = owner(u_first + en.tiles - 1) - c_lo + 1;  // parts of the unit
+    const int s = en.s, q0 = en.q0, len = en.len, nq = en.nq, r0 = en.r0, nr = en.nr, pos_lo = en.pos_lo, pos_hi = en.pos_hi;
+    const bool bad = en.bad;
+    const int c0 = en.b_lo + 4 * t0, cn = max(0, min(4 * (t1 - t0), en.b_hi - c0));
+    const int nt = (cn + 3) / 4;
+
+    __syncthreads();  // the part before is done with shared memory
+    if (tid == 0) {
+      if (started)
+        for (int i = 0; i < Bars<G>::kBars; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.stage[0][0] + i)) : "memory");
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.stage[0][i], 1);
+        mbar_init(&bars.stage[1][i], 1);
+        mbar_init(&bars.sread[0][i], kSet);
+        mbar_init(&bars.sread[1][i], kSet);
+        mbar_init(&bars.kfull[i], kSet);
+        mbar_init(&bars.vfull[i], kSet);
+        mbar_init(&bars.kfree[i], 1);
+        for (int g = 0; g < G; ++g) {
+          mbar_init(&bars.sfull[g][i], 1);
+          mbar_init(&bars.pready[g][i], kSoft);
+          mbar_init(&bars.pvdone[g][i], 1);
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      mbar_init(&bars.drain, 1);
+      if (!started) bars.abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    started = true;
+    const int64_t vplane = int64_t(a.c.page_tokens) * D;
+    // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row.  A lane
+    // copies its 8 dims of all its rows into the tiles' space first (all copies in flight at once,
+    // each read back by the lane that made it) and converts them in a small loop.
+    if (warp < kSoft * G + kConv) {
+      constexpr int LR = D / 8 == 24 ? 32 : D / 8, RW = 32 / LR;  // lanes and rows of a warp's copy
+      constexpr int kWarps = kSoft * G + kConv, kStep = kWarps * RW;
+      constexpr int kIter = (R + kStep - 1) / kStep;               // rows per lane
+      constexpr int kRoom = int(2 * (C::kK + C::kV)) / (kWarps * 512 * PARTS);
+      constexpr int kRound = kRoom < kIter ? kRoom : kIter;        // of them at a time
+      static_assert(kRound > 0, "room for the raw queries");
+      const int sub = lane / LR, d = lane % LR * 8;
+      const uint32_t mine = smem_u32(kring) + uint32_t(warp * 32 + lane) * (16 * PARTS);  // + iteration * kWarps * 512 * PARTS
+      const bool half = a.type == QDQ_TYPE_F16;
 #pragma unroll 1
-      for (int i = 0; i < kRound; ++i) {
-        const int r = (i0 + i) * kStep + warp * RW + sub;
-        const bool in = r < nr && d < D;
-        uint32_t w[4 * PARTS];
+      for (int i0 = 0; i0 < kIter; i0 += kRound) {
+#pragma unroll 1
+        for (int i = 0; i < kRound; ++i) {
+          const int r = (i0 + i) * kStep + warp * RW + sub;
+          if (r < nr && d < D) {
+            const int qi = int(a.query_of(r0 + r));
+            const int64_t e = int64_t(q0 + qi) * a.q_stride + int64_t(h * a.group + (r0 + r - qi * a.group)) * D + d;
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[4 * p]), "=r"(w[4 * p + 1]), "=r"(w[4 * p + 2]), "=r"(w[4 * p + 3])
-                       : "r"(mine + i * (kWarps * 512 * PARTS) + 16 * p)
-                       : "memory");
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[4 * p + e] = in ? w[4 * p + e] : 0u;
-        }
-        float v[8], mx;  // the elements and the row's largest magnitude (by its bits: NaN is the largest)
-        if constexpr (PARTS == 2) {
-          uint32_t bits = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = __uint_as_float(w[e]);
-            bits = max(bits, w[e] & 0x7FFFFFFFu);
+            for (int p = 0; p < PARTS; ++p)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + i * (kWarps * 512 * PARTS) + 16 * p),
+                           "l"(static_cast<const uint8_t *>(a.q) + (PARTS == 2 ? 4 * e + 16 * p : 2 * e))
+                           : "memory");
           }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+        for (int i = 0; i < kRound; ++i) {
+          const int r = (i0 + i) * kStep + warp * RW + sub;
+          const bool in = r < nr && d < D;
+          uint32_t w[4 * PARTS];
 #pragma unroll
-          for (int o = LR / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
-          mx = __uint_as_float(bits);
-        } else {
-          uint32_t bits = 0;  // two halves
+          for (int p = 0; p < PARTS; ++p) {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[4 * p]), "=r"(w[4 * p + 1]), "=r"(w[4 * p + 2]), "=r"(w[4 * p + 3])
+                         : "r"(mine + i * (kWarps * 512 * PARTS) + 16 * p)
+                         : "memory");
 #pragma unroll
-          for (int e = 0; e < 4; ++e) bits = __vmaxu2(bits, w[e] & 0x7FFF7FFFu);
+            for (int e = 0; e < 4; ++e) w[4 * p + e] = in ? w[4 * p + e] : 0u;
+          }
+          float v[8], mx;  // the elements and the row's largest magnitude (by its bits: NaN is the largest)
+          if constexpr (PARTS == 2) {
+            uint32_t bits = 0;
 #pragma unroll
-          for (int o = LR / 2; o > 0; o >>= 1) bits = __vmaxu2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
-          bits = max(bits & 0xFFFFu, bits >> 16);
-          mx = half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
+            for (int e = 0; e < 8; ++e) {
+              v[e] = __uint_as_float(w[e]);
+              bits = max(bits, w[e] & 0x7FFFFFFFu);
+            }
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+            mx = __uint_as_float(bits);
+          } else {
+            uint32_t bits = 0;  // two halves
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bits = __vmaxu2(bits, w[e] & 0x7FFF7FFFu);
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1) bits = __vmaxu2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+            bits = max(bits & 0xFFFFu, bits >> 16);
+            mx = half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = half ? unpack2(w[e], __half{}) : unpack2(w[e], __nv_bfloat16{});
+              v[2 * e] = f.x;
+              v[2 * e + 1] = f.y;
+            }
+          }
+          const bool finite = mx < __int_as_float(0x7f800000);
+          int ex = 13 - (int(__float_as_uint(mx) >> 23) - 127);
+          ex = max(-120, min(120, ex));
+          // the scale's sign goes into the queries, so that a larger product is a larger score
+          float up = __uint_as_float(uint32_t(ex + 127) << 23);
+          if (a.scale < 0.f) up = -up;
+          if (d == 0 && r < R) {
+            const float q = (finite ? __uint_as_float(uint32_t(127 - ex) << 23) : qnan) * fabsf(a.scale);
+            s_qs[r] = a.softcap > 0.f ? q : q * kLog2e;
+          }
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = half ? unpack2(w[e], __half{}) : unpack2(w[e], __nv_bfloat16{});
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-          }
-        }
-        const bool finite = mx < __int_as_float(0x7f800000);
-        int ex = 13 - (int(__float_as_uint(mx) >> 23) - 127);
-        ex = max(-120, min(120, ex));
-        // the scale's sign goes into the queries, so that a larger product is a larger score
-        float up = __uint_as_float(uint32_t(ex + 127) << 23);
-        if (a.scale < 0.f) up = -up;
-        if (d == 0 && r < R) {
-          const float q = (finite ? __uint_as_float(uint32_t(127 - ex) << 23) : qnan) * fabsf(a.scale);
-          s_qs[r] = a.softcap > 0.f ? q : q * kLog2e;
-        }
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = v[2 * e] * up, y = v[2 * e + 1] * up;
-          hi[e] = finite ? pack2(x, y, __half{}) : 0u;
-          if constexpr (PARTS == 2) {
-            const float2 back = unpack2(hi[e], __half{});
-            lo[e] = finite ? pack2(x - back.x, y - back.y, __half{}) : 0u;
-          }
-        }
-        if (r < R && d < D) {
-          uint8_t *dst = smem + ((r / kTcRows) * C::kSub + d / 64) * C::kQTile + (r % kTcRows) * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if constexpr (PARTS == 2) *reinterpret_cast<uint4 *>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  } else {
-    // meanwhile the split's blocks: places and scales (past the last one: zeros, hidden from every row)
-    const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
-#pragma unroll 2
-    for (int i = tid - 32 * (kSoft * G + kConv); i < 4 * nt; i += kThreads - 32 * (kSoft * G + kConv)) {
-      BlockAt e{-1, 0.f, 0.f, 0.f};
-      if (i < cn) {
-        const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
-        const int64_t at = kv_record_of(a.c, s, blk, h, rec);
-        if (at >= 0) {
-          const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
-          const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
-          e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale))};
-        } else {
-          e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
-        }
-      }
-      s_blk[i] = e;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars.tmem;
-  auto give_up = [&]() { *reinterpret_cast<volatile int *>(&bars.abort) = 1; };
-  // a whole warp waits; false after the time limit
-  auto wait = [&](uint64_t *bar, int phase) {
-    if (__all_sync(0xffffffffu, mbar_wait(bar, uint32_t(phase) & 1u))) return true;
-    give_up();
-    return false;
-  };
-
-  const int grp = warp / kSoft;        // softmax warps: their group of rows
-  const int lr = tid;                  // and their thread's row of the tile
-  const int row = r0 + lr;
-  float m = ninf, l = 0.f;             // its reference and sum
-  const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-  const uint32_t otm = tmem + lanes + C::kOCol + uint32_t(grp * D);  // its O
-  if (warp < kSoft * G) {
-    if constexpr (C::kShift) reg_inc<128>();
-    const int qi = int(a.query_of(row));
-    const int pos = len - nq + qi;
-    const int lo_pos = a.window > 0 ? pos - a.window + 1 : 0;
-    const float qs = s_qs[lr];
-    const float slope = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row - qi * a.group) * kLog2e : 0.f;
-    // tokens that every row of the tile sees
-    const int all_lo = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0, all_hi = pos_lo + 1;
-    for (int i = 0; i < nt; ++i) {
-      const int b = i & 1;
-      const uint32_t sp = tmem + lanes + uint32_t((2 * grp + b) * BN);
-      if (!wait(&bars.sfull[grp][b], i >> 1)) break;
-      tc_fence_after();
-      const int j0 = (c0 + 4 * i) * kKvBlock;
-      const bool whole = j0 >= all_lo && j0 + BN <= all_hi;
-      const BlockAt *blk = s_blk + 4 * i;
-      // scores of one block of 16 that need more than a factor: cap, bias, mask (log2 units)
-      auto transform = [&](int c, uint32_t *r) {
-        const float fc = qs * blk[c].ks;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = j0 + 16 * c + e;
-          float x = __uint_as_float(r[e]) * fc;
-          if (a.softcap > 0.f) x = a.softcap * kLog2e * tanh_of(x * a.inv_cap);
-          if (a.slopes) x = fmaf(-slope, float(pos - j), x);
-          if (j > pos || j < lo_pos) x = ninf;
-          r[e] = __float_as_uint(x);
-        }
-      };
-      uint32_t hi[4][8], lo[4][PARTS == 2 ? 8 : 1];
-      float sum, most;  // of the tile's probabilities; largest sum of a block's times its value scale
-      // the tile's probabilities for the present reference, from S in TMEM, a block of 16 at a time
-      auto probabilities = [&](auto plain) {
-        constexpr bool kPlain = decltype(plain)::value;
-        const float mref = m == ninf ? 0.f : m;
-        const float2 mm = f2(-mref, -mref);
-        uint32_t r[2][16];
-        tmem_ld16_async(sp, r[0]);
-        sum = most = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t *x = r[c & 1];
-          tmem_wait_ld16(x);
-          if (c < 3) tmem_ld16_async(sp + 16 * (c + 1), r[(c + 1) & 1]);
-          if constexpr (!kPlain) transform(c, x);
-          const float f = kPlain ? qs * blk[c].ks : 1.f, vs = blk[c].vs;
-          float2 l2, l3;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 y = kPlain ? __ffma2_rn(f2_bits(x[2 * e], x[2 * e + 1]), f2(f, f), mm)
-                                    : __fadd2_rn(f2_bits(x[2 * e], x[2 * e + 1]), mm);
-            const float2 p = f2(ex2(y.x), ex2(y.y));
-            if (e == 0) l2 = p;
-            else if (e == 1) l3 = p;
-            else if (e & 1) l3 = __fadd2_rn(l3, p);
-            else l2 = __fadd2_rn(l2, p);
-            float2 pv = __fmul2_rn(p, f2(vs, vs));
-            if constexpr (!kPlain) {  // a hidden token's scale may be NaN
-              if (y.x == ninf) pv.x = 0.f;
-              if (y.y == ninf) pv.y = 0.f;
-            }
-            hi[c][e] = pack2(pv.x, pv.y, __half{});
+            const float x = v[2 * e] * up, y = v[2 * e + 1] * up;
+            hi[e] = finite ? pack2(x, y, __half{}) : 0u;
             if constexpr (PARTS == 2) {
-              const float2 back = unpack2(hi[c][e], __half{});
-              lo[c][e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
+              const float2 back = unpack2(hi[e], __half{});
+              lo[e] = finite ? pack2(x - back.x, y - back.y, __half{}) : 0u;
             }
           }
-          const float bs = (l2.x + l2.y) + (l3.x + l3.y);
-          sum += bs;
-          most = fmaxf(most, bs * vs);
+          if (r < R && d < D) {
+            uint8_t *dst = smem + ((r / kTcRows) * C::kSub + d / 64) * C::kQTile + (r % kTcRows) * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (PARTS == 2) *reinterpret_cast<uint4 *>(dst + C::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
-      };
-      // the largest score plus log2 of its value scale
-      auto largest = [&](bool plain) {
-        float mx = ninf;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[16];
-          tmem_ld16_async(sp + 16 * c, x);
-          tmem_wait_ld16(x);
-          if (!plain) transform(c, x);
-          float bm = __uint_as_float(x[0]);
-#pragma unroll
-          for (int e = 1; e < 16; ++e) bm = fmaxf(bm, __uint_as_float(x[e]));
-          mx = fmaxf(mx, plain ? fmaf(bm, qs * blk[c].ks, blk[c].lv) : bm + blk[c].lv);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    } else {
+      // meanwhile the split's blocks: places and scales (past the last one: zeros, hidden from every row)
+      const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
+#pragma unroll 2
+      for (int i = tid - 32 * (kSoft * G + kConv); i < 4 * nt; i += kThreads - 32 * (kSoft * G + kConv)) {
+        BlockAt e{-1, 0.f, 0.f, 0.f};
+        if (i < cn) {
+          const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
+          const int64_t at = kv_record_of(a.c, s, blk, h, rec);
+          if (at >= 0) {
+            const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
+            const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+            e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale))};
+          } else {
+            e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
+          }
         }
-        return mx;
-      };
-      // Every p * vs of a block is at most the block's sum of p times vs: where those stay below
-      // 2^15 (f16 ends at 2^16) with the reference there is, no maximum is looked for (64
-      // comparisons less per row and tile).  Else, and for a row's first tile, the maximum moves
-      // the reference and the probabilities are computed once more.
-      const bool plain = whole && !(a.softcap > 0.f) && !a.slopes;
-      bool again = __any_sync(0xffffffffu, m == ninf), ok = true;
-      for (;;) {
-        if (again) {  // the reference: see qdq_kv_attn.cu
-          const float m_new = fmaxf(m, largest(plain));
-          const bool grow = m_new > m + (m == ninf ? 0.f : kLazy);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float corr = m_new > m ? ex2(m - m_new) : 1.f;
-            l *= corr;
-            m = m_new;
-            if (i > 0) {
-              ok = wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld16_async(otm + c, o);
-                tmem_wait_ld16(o);
+        s_blk[i] = e;
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    auto give_up = [&]() { *reinterpret_cast<volatile int *>(&bars.abort) = 1; };
+    // a whole warp waits; false after the time limit
+    auto wait = [&](uint64_t *bar, int phase) {
+      if (__all_sync(0xffffffffu, mbar_wait(bar, uint32_t(phase) & 1u))) return true;
+      give_up();
+      return false;
+    };
+
+    const int grp = warp / kSoft;        // softmax warps: their group of rows
+    const int lr = tid;                  // and their thread's row of the tile
+    const int row = r0 + lr;
+    float m = ninf, l = 0.f;             // its reference and sum
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t otm = tmem + lanes + C::kOCol + uint32_t(grp * D);  // its O
+    if (warp < kSoft * G) {
+      if constexpr (C::kShift) reg_inc<128>();
+      const int qi = int(a.query_of(row));
+      const int pos = len - nq + qi;
+      const int lo_pos = a.window > 0 ? pos - a.window + 1 : 0;
+      const float qs = s_qs[lr];
+      const float slope = a.slopes && lr < nr ? __ldg(a.slopes + h * a.group + row - qi * a.group) * kLog2e : 0.f;
+      // tokens that every row of the tile sees
+      const int all_lo = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0, all_hi = pos_lo + 1;
+      for (int i = 0; i < nt; ++i) {
+        const int b = i & 1;
+        const uint32_t sp = tmem + lanes + uint32_t((2 * grp + b) * BN);
+        if (!wait(&bars.sfull[grp][b], i >> 1)) break;
+        tc_fence_after();
+        const int j0 = (c0 + 4 * i) * kKvBlock;
+        const bool whole = j0 >= all_lo && j0 + BN <= all_hi;
+        const BlockAt *blk = s_blk + 4 * i;
+        // scores of one block of 16 that need more than a factor: cap, bias, mask (log2 units)
+        auto transform = [&](int c, uint32_t *r) {
+          const float fc = qs * blk[c].ks;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                tmem_st16(otm + c, o);
+          for (int e = 0; e < 16; ++e) {
+            const int j = j0 + 16 * c + e;
+            float x = __uint_as_float(r[e]) * fc;
+            if (a.softcap > 0.f) x = a.softcap * kLog2e * tanh_of(x * a.inv_cap);
+            if (a.slopes) x = fmaf(-slope, float(pos - j), x);
+            if (j > pos || j < lo_pos) x = ninf;
+            r[e] = __float_as_uint(x);
+          }
+        };
+        uint32_t hi[4][8], lo[4][PARTS == 2 ? 8 : 1];
+        float sum, most;  // of the tile's probabilities; largest sum of a block's times its value scale
+        // the tile's probabilities for the present reference, from S in TMEM, a block of 16 at a time
+        auto probabilities = [&](auto plain) {
+          constexpr bool kPlain = decltype(plain)::value;
+          const float mref = m == ninf ? 0.f : m;
+          const float2 mm = f2(-mref, -mref);
+          uint32_t r[2][16];
+          tmem_ld16_async(sp, r[0]);
+          sum = most = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t *x = r[c & 1];
+            tmem_wait_ld16(x);
+            if (c < 3) tmem_ld16_async(sp + 16 * (c + 1), r[(c + 1) & 1]);
+            if constexpr (!kPlain) transform(c, x);
+            const float f = kPlain ? qs * blk[c].ks : 1.f, vs = blk[c].vs;
+            float2 l2, l3;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = kPlain ? __ffma2_rn(f2_bits(x[2 * e], x[2 * e + 1]), f2(f, f), mm)
+                                      : __fadd2_rn(f2_bits(x[2 * e], x[2 * e + 1]), mm);
+              const float2 p = f2(ex2(y.x), ex2(y.y));
+              if (e == 0) l2 = p;
+              else if (e == 1) l3 = p;
+              else if (e & 1) l3 = __fadd2_rn(l3, p);
+              else l2 = __fadd2_rn(l2, p);
+              float2 pv = __fmul2_rn(p, f2(vs, vs));
+              if constexpr (!kPlain) {  // a hidden token's scale may be NaN
+                if (y.x == ninf) pv.x = 0.f;
+                if (y.y == ninf) pv.y = 0.f;
+              }
+              hi[c][e] = pack2(pv.x, pv.y, __half{});
+              if constexpr (PARTS == 2) {
+                const float2 back = unpack2(hi[c][e], __half{});
+                lo[c][e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
+              }
+            }
+            const float bs = (l2.x + l2.y) + (l3.x + l3.y);
+            sum += bs;
+            most = fmaxf(most, bs * vs);
+          }
+        };
+        // the largest score plus log2 of its value scale
+        auto largest = [&](bool plain) {
+          float mx = ninf;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[16];
+            tmem_ld16_async(sp + 16 * c, x);
+            tmem_wait_ld16(x);
+            if (!plain) transform(c, x);
+            float bm = __uint_as_float(x[0]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) bm = fmaxf(bm, __uint_as_float(x[e]));
+            mx = fmaxf(mx, plain ? fmaf(bm, qs * blk[c].ks, blk[c].lv) : bm + blk[c].lv);
+          }
+          return mx;
+        };
+        // Every p * vs of a block is at most the block's sum of p times vs: where those stay below
+        // 2^15 (f16 ends at 2^16) with the reference there is, no maximum is looked for (64
+        // comparisons less per row and tile).  Else, and for a row's first tile, the maximum moves
+        // the reference and the probabilities are computed once more.
+        const bool plain = whole && !(a.softcap > 0.f) && !a.slopes;
+        bool again = __any_sync(0xffffffffu, m == ninf), ok = true;
+        for (;;) {
+          if (again) {  // the reference: see qdq_kv_attn.cu
+            const float m_new = fmaxf(m, largest(plain));
+            const bool grow = m_new > m + (m == ninf ? 0.f : kLazy);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float corr = m_new > m ? ex2(m - m_new) : 1.f;
+              l *= corr;
+              m = m_new;
+              if (i > 0) {
+                ok = wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16_async(otm + c, o);
+                  tmem_wait_ld16(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                  tmem_st16(otm + c, o);
+                }
               }
             }
           }
+          if (plain)
+            probabilities(std::true_type{});
+          else
+            probabilities(std::false_type{});
+          if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) break;
+          again = true;
         }
-        if (plain)
-          probabilities(std::true_type{});
-        else
-          probabilities(std::false_type{});
-        if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) break;
-        again = true;
-      }
-      if (!ok) break;
-      l += sum;
+        if (!ok) break;
+        l += sum;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // over the block's own columns of S
-        tmem_st8(sp + 16 * c, hi[c]);
-        if constexpr (PARTS == 2) tmem_st8(sp + 16 * c + 8, lo[c]);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.pready[grp][b]);
-    }
-    if constexpr (C::kShift) reg_dec<96>();
-  } else if (warp < kSoft * G + kConv) {
-    // ---------------- codes to f16 tiles ----------------
-    if constexpr (C::kShift) reg_dec<64>();
-    const int set = (warp - kSoft * G) / kSet, w = (warp - kSoft * G) % kSet;  // tiles set, set + kSets, ...
-    constexpr int KL = D / 32;            // 16-byte chunks of keys per thread: tokens 16 w .. 16 w + 15 of the tile
-    constexpr int VG = (D / 32 + 3) / 4;  // groups of 32 dims of the values per warp
-    uint4 kq[KL];
-    uint2 vq[VG][8];
-    const int vtc = lane & 7, vd = lane >> 3;  // 8-token chunk, 8-dim part of the group
-    // chunk j of this thread's keys: row and 16-dim chunk of the warp's 16 tokens
-    auto key_at = [&](int j, int &rr, int &ch) {
-      const int u = lane + 32 * j;
-      rr = u / (D / 16);
-      ch = u % (D / 16);
-    };
-    uint8_t *my_stages = stages + set * C::kSlots * C::kStage;
-    int n = 0, round = 0;  // slot, and how often it has been used
-    for (int i = set; i < nt; i += C::kSets) {
-      const int b = i & 1;
-      const int64_t ak = s_blk[4 * i + w].k, av = s_blk[4 * i + vtc / 2].k;
-      if constexpr (C::kStaged) {
-        if (!wait(&bars.stage[set][n], round)) break;
-        const uint8_t *st = my_stages + n * C::kStage;
-#pragma unroll
-        for (int j = 0; j < KL; ++j)
-          kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
-#pragma unroll
-        for (int g = 0; g < VG; ++g)
-          if (w + 4 * g < D / 32) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-              vq[g][t] = av < 0 ? make_uint2(0, 0)
-                                : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
-          }
+        for (int c = 0; c < 4; ++c) {  // over the block's own columns of S
+          tmem_st8(sp + 16 * c, hi[c]);
+          if constexpr (PARTS == 2) tmem_st8(sp + 16 * c + 8, lo[c]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sread[set][n]);
-        if (++n == C::kSlots) {
-          n = 0;
-          ++round;
-        }
-      } else {
+        if (lane == 0) mbar_arrive(&bars.pready[grp][b]);
+      }
+      if constexpr (C::kShift) {
+        named_bar_sync(1 + grp, 32 * kSoft);  // a group of four warps meets between two changes of its registers
+        reg_dec<96>();
+        named_bar_arrive(3, 32 * (kSoft * G + kConv));
+      }
+    } else if (warp < kSoft * G + kConv) {
+      // ---------------- codes to f16 tiles ----------------
+      if constexpr (C::kShift) reg_dec<64>();
+      const int set = (warp - kSoft * G) / kSet, w = (warp - kSoft * G) % kSet;  // tiles set, set + kSets, ...
+      constexpr int KL = D / 32;            // 16-byte chunks of keys per thread: tokens 16 w .. 16 w + 15 of the tile
+      constexpr int VG = (D / 32 + 3) / 4;  // groups of 32 dims of the values per warp
+      uint4 kq[KL];
+      uint2 vq[VG][8];
+      const int vtc = lane & 7, vd = lane >> 3;  // 8-token chunk, 8-dim part of the group
+      // chunk j of this thread's keys: row and 16-dim chunk of the warp's 16 tokens
+      auto key_at = [&](int j, int &rr, int &ch) {
+        const int u = lane + 32 * j;
+        rr = u / (D / 16);
+        ch = u % (D / 16);
+      };
+      uint8_t *my_stages = stages + set * C::kSlots * C::kStage;
+      int n = 0, round = 0;  // slot, and how often it has been used
+      for (int i = set; i < nt; i += C::kSets) {
+        const int b = i & 1;
+        const int64_t ak = s_blk[4 * i + w].k, av = s_blk[4 * i + vtc / 2].k;
+        if constexpr (C::kStaged) {
+          if (!wait(&bars.stage[set][n], round)) break;
+          const uint8_t *st = my_stages + n * C::kStage;
 #pragma unroll
-        for (int j = 0; j < KL; ++j)
-          kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(a.c.pages + ak + (lane + 32 * j) * 16);
+          for (int j = 0; j < KL; ++j)
+            kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
+#pragma unroll
+          for (int g = 0; g < VG; ++g)
+            if (w + 4 * g < D / 32) {
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+                vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                  : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.sread[set][n]);
+          if (++n == C::kSlots) {
+            n = 0;
+            ++round;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < KL; ++j)
+            kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(a.c.pages + ak + (lane + 32 * j) * 16);
+#pragma unroll
+          for (int g = 0; g < VG; ++g)
+            if (w + 4 * g < D / 32) {
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+                vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                  : ld_u2(a.c.pages + av + vplane + ((vtc & 1) * 8 + t) * D + (w + 4 * g) * 32 + vd * 8);
+            }
+        }
+        if (i >= 2 && !wait(&bars.kfree[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
+        uint8_t *kt = kring + b * C::kK, *vt = vring + b * C::kV;
+#pragma unroll
+        for (int j = 0; j < KL; ++j) {
+          int rr, ch;
+          key_at(j, rr, ch);
+          rr += 16 * w;
+          const uint32_t q[4] = {kq[j].x, kq[j].y, kq[j].z, kq[j].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t u = q[e] ^ 0x80808080u;
+            o[2 * e] = codes_f16<0x4140>(u);
+            o[2 * e + 1] = codes_f16<0x4342>(u);
+          }
+          uint8_t *dst = kt + (ch / 4) * (BN * 128) + rr * 128;
+          const int c = 2 * ch % 8;
+          *reinterpret_cast<uint4 *>(dst + ((c ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.kfull[b]);
+        if (i >= 2 && !wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
 #pragma unroll
         for (int g = 0; g < VG; ++g)
           if (w + 4 * g < D / 32) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-              vq[g][t] = av < 0 ? make_uint2(0, 0)
-                                : ld_u2(a.c.pages + av + vplane + ((vtc & 1) * 8 + t) * D + (w + 4 * g) * 32 + vd * 8);
-          }
-      }
-      if (i >= 2 && !wait(&bars.kfree[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
-      uint8_t *kt = kring + b * C::kK, *vt = vring + b * C::kV;
+            for (int hw = 0; hw < 2; ++hw) {  // four dims
+              uint32_t even[4], odd[4];       // pairs of tokens: dims 0, 1 and dims 2, 3
 #pragma unroll
-      for (int j = 0; j < KL; ++j) {
-        int rr, ch;
-        key_at(j, rr, ch);
-        rr += 16 * w;
-        const uint32_t q[4] = {kq[j].x, kq[j].y, kq[j].z, kq[j].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = q[e] ^ 0x80808080u;
-          o[2 * e] = codes_f16<0x4140>(u);
-          o[2 * e + 1] = codes_f16<0x4342>(u);
-        }
-        uint8_t *dst = kt + (ch / 4) * (BN * 128) + rr * 128;
-        const int c = 2 * ch % 8;
-        *reinterpret_cast<uint4 *>(dst + ((c ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.kfull[b]);
-      if (i >= 2 && !wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
-#pragma unroll
-      for (int g = 0; g < VG; ++g)
-        if (w + 4 * g < D / 32) {
-#pragma unroll
-          for (int hw = 0; hw < 2; ++hw) {  // four dims
-            uint32_t even[4], odd[4];       // pairs of tokens: dims 0, 1 and dims 2, 3
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const uint32_t x = (hw ? vq[g][2 * t].y : vq[g][2 * t].x) ^ 0x80808080u;
-              const uint32_t y = (hw ? vq[g][2 * t + 1].y : vq[g][2 * t + 1].x) ^ 0x80808080u;
-              even[t] = __byte_perm(x, y, 0x5140);
-              odd[t] = __byte_perm(x, y, 0x7362);
+              for (int t = 0; t < 4; ++t) {
+                const uint32_t x = (hw ? vq[g][2 * t].y : vq[g][2 * t].x) ^ 0x80808080u;
+                const uint32_t y = (hw ? vq[g][2 * t + 1].y : vq[g][2 * t + 1].x) ^ 0x80808080u;
+                even[t] = __byte_perm(x, y, 0x5140);
+                odd[t] = __byte_perm(x, y, 0x7362);
+              }
+              const int d = (w + 4 * g) * 32 + vd * 8 + hw * 4;
+              auto put = [&](int dd, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+                *reinterpret_cast<uint4 *>(vt + dd * 128 + ((vtc ^ (dd & 7)) << 4)) = make_uint4(x, y, z, u);
+              };
+              put(d, codes_f16<0x4140>(even[0]), codes_f16<0x4140>(even[1]), codes_f16<0x4140>(even[2]), codes_f16<0x4140>(even[3]));
+              put(d + 1, codes_f16<0x4342>(even[0]), codes_f16<0x4342>(even[1]), codes_f16<0x4342>(even[2]), codes_f16<0x4342>(even[3]));
+              put(d + 2, codes_f16<0x4140>(odd[0]), codes_f16<0x4140>(odd[1]), codes_f16<0x4140>(odd[2]), codes_f16<0x4140>(odd[3]));
+              put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
             }
-            const int d = (w + 4 * g) * 32 + vd * 8 + hw * 4;
-            auto put = [&](int dd, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
-              *reinterpret_cast<uint4 *>(vt + dd * 128 + ((vtc ^ (dd & 7)) << 4)) = make_uint4(x, y, z, u);
-            };
-            put(d, codes_f16<0x4140>(even[0]), codes_f16<0x4140>(even[1]), codes_f16<0x4140>(even[2]), codes_f16<0x4140>(even[3]));
-            put(d + 1, codes_f16<0x4342>(even[0]), codes_f16<0x4342>(even[1]), codes_f16<0x4342>(even[2]), codes_f16<0x4342>(even[3]));
-            put(d + 2, codes_f16<0x4140>(odd[0]), codes_f16<0x4140>(odd[1]), codes_f16<0x4140>(odd[2]), codes_f16<0x4140>(odd[3]));
-            put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
           }
-        }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.vfull[b]);
-    }
-    if constexpr (C::kShift) reg_inc<96>();  // waits for the softmax warps' registers
-  } else if (warp == kSoft * G + kConv + 1) {
-    // ---------------- copies of the codes ----------------
-    if constexpr (C::kStaged) {
-      if (lane == 0) {
-        int done = 0;  // tiles whose copies have been issued
-        for (int i = 0; i < nt; ++i, ++done) {
-          const int set = i % C::kSets, use = i / C::kSets, n = use % C::kSlots;  // the set's use-th tile
-          if (use >= C::kSlots && !mbar_wait(&bars.sread[set][n], uint32_t(use / C::kSlots - 1) & 1u)) {
-            give_up();
-            break;
-          }
-          uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
-          uint64_t *bar = &bars.stage[set][n];
-          int64_t at[4];
-          uint32_t bytes = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            at[b] = s_blk[4 * i + b].k;
-            bytes += at[b] >= 0 ? 32 * D : 0;
-          }
-          mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            if (at[b] < 0) continue;  // no such block: its part of the stage is not read
-            const uint8_t *p = a.c.pages + at[b];
-            bulk_copy_g2s(dst + b * 16 * D, p, 16 * D, bar);
-            bulk_copy_g2s(dst + C::kStageV + (2 * b) * C::kVStep, p + vplane, 8 * D, bar);
-            bulk_copy_g2s(dst + C::kStageV + (2 * b + 1) * C::kVStep, p + vplane + 8 * D, 8 * D, bar);
-          }
-        }
-        // no copy may be in flight when the CTA ends, also after giving up: each stage's last one
-        for (int i = max(0, done - C::kSets * C::kSlots); i < done; ++i)
-          if (!mbar_wait(&bars.stage[i % C::kSets][i / C::kSets % C::kSlots], uint32_t(i / C::kSets / C::kSlots) & 1u))
-            atomicAdd(&g_attn_tc_timeouts, 1u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.vfull[b]);
       }
-      __syncwarp();
-    }
-  } else {
-    // ---------------- products ----------------
-    const uint32_t leader = elect_lane();
-    const uint32_t q_base = smem_u32(smem), k_base = smem_u32(kring), v_base = smem_u32(vring);
-    auto scores = [&](int g, int i) {  // S of tile i
-      const int b = i & 1;
-#pragma unroll
-      for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(leader, tmem + uint32_t((2 * g + b) * BN),
-                 desc_sw128(q_base + part * C::kQPart + (g * C::kSub + k / 4) * C::kQTile + (k % 4) * 32),
-                 desc_sw128(k_base + b * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
-      mma_commit(leader, &bars.sfull[g][b]);
-    };
-    bool ok = true;
-    if (nt > 0) {
-      ok = wait(&bars.kfull[0], 0);
-      if (ok) {
-        tc_fence_after();
-#pragma unroll
-        for (int g = 0; g < G; ++g) scores(g, 0);
-        mma_commit(leader, &bars.kfree[0]);
+      if constexpr (C::kShift) {
+        // not before the softmax warps have given theirs back: a set without a tile would take its
+        // registers again before a softmax group had got them
+        named_bar_sync(3, 32 * (kSoft * G + kConv));
+        reg_inc<96>();
       }
-    }
-    for (int i = 0; i < nt && ok; ++i) {
-      const int b = i & 1;
-      if (i + 1 < nt) {
-        ok = wait(&bars.kfull[b ^ 1], (i + 1) >> 1);
-        // the other S holds the probabilities of tile i - 1 until its products are done
+    } else if (warp == kSoft * G + kConv + 1) {
+      // ---------------- copies of the codes ----------------
+      if constexpr (C::kStaged) {
+        if (lane == 0) {
+          int done = 0;  // tiles whose copies have been issued
+          for (int i = 0; i < nt; ++i, ++done) {
+            const int set = i % C::kSets, use = i / C::kSets, n = use % C::kSlots;  // the set's use-th tile
+            if (use >= C::kSlots && !mbar_wait(&bars.sread[set][n], uint32_t(use / C::kSlots - 1) & 1u)) {
+              give_up();
+              break;
+            }
+            uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
+            uint64_t *bar = &bars.stage[set][n];
+            int64_t at[4];
+            uint32_t bytes = 0;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          if (ok && i >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (i - 1) >> 1);
-          if (ok) {
-            tc_fence_after();
-            scores(g, i + 1);
+            for (int b = 0; b < 4; ++b) {
+              at[b] = s_blk[4 * i + b].k;
+              bytes += at[b] >= 0 ? 32 * D : 0;
+            }
+            mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              if (at[b] < 0) continue;  // no such block: its part of the stage is not read
+              const uint8_t *p = a.c.pages + at[b];
+              bulk_copy_g2s(dst + b * 16 * D, p, 16 * D, bar);
+              bulk_copy_g2s(dst + C::kStageV + (2 * b) * C::kVStep, p + vplane, 8 * D, bar);
+              bulk_copy_g2s(dst + C::kStageV + (2 * b + 1) * C::kVStep, p + vplane + 8 * D, 8 * D, bar);
+            }
           }
+          // no copy may be in flight when the CTA ends, also after giving up: each stage's last one
+          for (int i = max(0, done - C::kSets * C::kSlots); i < done; ++i)
+            if (!mbar_wait(&bars.stage[i % C::kSets][i / C::kSets % C::kSlots], uint32_t(i / C::kSets / C::kSlots) & 1u))
+              atomicAdd(&g_attn_tc_timeouts, 1u);
         }
-        if (!ok) break;
-        mma_commit(leader, &bars.kfree[b ^ 1]);
+        __syncwarp();
       }
-      ok = wait(&bars.vfull[b], i >> 1);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (ok) ok = wait(&bars.pready[g][b], i >> 1);
-        if (!ok) break;
-        tc_fence_after();
+    } else {
+      // ---------------- products ----------------
+      const uint32_t leader = elect_lane();
+      const uint32_t q_base = smem_u32(smem), k_base = smem_u32(kring), v_base = smem_u32(vring);
+      auto scores = [&](int g, int i) {  // S of tile i
+        const int b = i & 1;
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_ts(leader, tmem + C::kOCol + uint32_t(g * D), tmem + uint32_t((2 * g + b) * BN + 16 * k + 8 * part),
-                   desc_sw128(v_base + b * C::kV + k * 32), idesc_f16(kTcRows, D), (i | part | k) != 0);
-        mma_commit(leader, &bars.pvdone[g][b]);
-      }
-    }
-    mma_commit(leader, &bars.drain);
-  }
-
-  // ---------------- output ----------------
-  __syncwarp();
-  // every product has completed before the accumulators are read and TMEM is freed
-  if (!wait(&bars.drain, 0) && lane == 0) atomicAdd(&g_attn_tc_timeouts, 1u);
-  tc_fence_after();
-  __syncthreads();
-  const bool lost = bad || *reinterpret_cast<volatile int *>(&bars.abort) != 0;
-  if (tid == 0 && bars.abort) atomicAdd(&g_attn_tc_timeouts, 1u);
-  constexpr int kPart = R * (D + 2);
-  float *part = a.partial + (int64_t(unit) * a.splits + split) * kPart;  // [dim][row], maxima, sums
-  if (warp < kSoft * G) {
-    if (lost) l = qnan;
-    const float inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
-    const bool in = lr < nr;
-#pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
-      uint32_t o[16];
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(leader, tmem + uint32_t((2 * g + b) * BN),
+                   desc_sw128(q_base + part * C::kQPart + (g * C::kSub + k / 4) * C::kQTile + (k % 4) * 32),
+                   desc_sw128(k_base + b * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
+        mma_commit(leader, &bars.sfull[g][b]);
+      };
+      bool ok = true;
       if (nt > 0) {
-        tmem_ld16_async(otm + c, o);
-        tmem_wait_ld16(o);
-      } else {
+        ok = wait(&bars.kfull[0], 0);
+        if (ok) {
+          tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0;
+          for (int g = 0; g < G; ++g) scores(g, 0);
+          mma_commit(leader, &bars.kfree[0]);
+        }
+      }
+      for (int i = 0; i < nt && ok; ++i) {
+        const int b = i & 1;
+        if (i + 1 < nt) {
+          ok = wait(&bars.kfull[b ^ 1], (i + 1) >> 1);
+          // the other S holds the probabilities of tile i - 1 until its products are done
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            if (ok && i >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (i - 1) >> 1);
+            if (ok) {
+              tc_fence_after();
+              scores(g, i + 1);
+            }
+          }
+          if (!ok) break;
+          mma_commit(leader, &bars.kfree[b ^ 1]);
+        }
+        ok = wait(&bars.vfull[b], i >> 1);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          if (ok) ok = wait(&bars.pready[g][b], i >> 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              mma_ts(leader, tmem + C::kOCol + uint32_t(g * D), tmem + uint32_t((2 * g + b) * BN + 16 * k + 8 * part),
+                     desc_sw128(v_base + b * C::kV + k * 32), idesc_f16(kTcRows, D), (i | part | k) != 0);
+          mma_commit(leader, &bars.pvdone[g][b]);
+        }
+      }
+      mma_commit(leader, &bars.drain);
+    }
+
+    // ---------------- output ----------------
+    __syncwarp();
+    // every product has completed before the accumulators are read and TMEM is freed
+    if (!wait(&bars.drain, 0) && lane == 0) atomicAdd(&g_attn_tc_timeouts, 1u);
+    tc_fence_after();
+    // and every commit's arrival has landed before the barriers are made anew for the next part
+    if (tid == 0 && !*reinterpret_cast<volatile int *>(&bars.abort))
+      for (int b = 0; b < 2 && b < nt; ++b) {
+        const uint32_t last = uint32_t((nt - b + 1) / 2 - 1) & 1u;  // of the (nt - b + 1) / 2 uses
+        bool done = mbar_wait(&bars.kfree[b], last);
+        for (int g = 0; g < G; ++g) done = mbar_wait(&bars.sfull[g][b], last) && mbar_wait(&bars.pvdone[g][b], last) && done;
+        if (!done) give_up();
+      }
+    __syncthreads();
+    const bool lost = bad || *reinterpret_cast<volatile int *>(&bars.abort) != 0;
+    if (tid == 0 && bars.abort) atomicAdd(&g_attn_tc_timeouts, 1u);
+    constexpr int kPart = R * (D + 2);
+    // a CTA keeps up to two parts of cut units: the first of its share, and another, which starts its unit
+    const bool another = u_first != total * c_lo / shares;
+    auto part_of = [&](int k) { return a.partial + (2 * int64_t(c_lo + k) + (k == 0 && another)) * kPart; };  // k-th part
+    float *part = part_of(int(blockIdx.x) - c_lo);  // [dim][row], maxima, sums
+    if (warp < kSoft * G) {
+      if (lost) l = qnan;
+      const float inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
+      const bool in = lr < nr;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        if (nt > 0) {
+          tmem_ld16_async(otm + c, o);
+          tmem_wait_ld16(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0;
+        }
+        if (nsplit == 1) {
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              store_out<D>(a, q0, h, row, c + e,
+                           make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                       __uint_as_float(o[e + 3])),
+                           inv);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[(c + e) * R + lr] = __uint_as_float(o[e]);
+        }
       }
       if (nsplit == 1) {
-        if (in) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            store_out<D>(a, q0, h, row, c + e,
-                         make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                     __uint_as_float(o[e + 3])),
-                         inv);
-        }
+        if (in) store_lse(a, q0, h, row, m, l);
       } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) part[(c + e) * R + lr] = __uint_as_float(o[e]);
+        part[D * R + lr] = m;
+        part[D * R + R + lr] = l;
       }
     }
-    if (nsplit == 1) {
-      if (in) store_lse(a, q0, h, row, m, l);
-    } else {
-      part[D * R + lr] = m;
-      part[D * R + R + lr] = l;
+    tc_fence_before();
+    if (nsplit > 1) {
+      // the CTA that finishes last joins the parts, in order: thread (row, share of the dims)
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) bars.last = atomicInc(a.tickets + int64_t(e_cur) * a.c.n_kv + h, nsplit - 1) == uint32_t(nsplit - 1);
+      __syncthreads();
+      constexpr int kShares = kThreads / R;  // whole ones
+      const int jr = tid % R, share = tid / R;
+      if (bars.last && share < kShares && jr < nr) {
+        __threadfence();
+        float M = ninf, L = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(part_of(k) + D * R + jr));
+        const float ref = M == ninf ? 0.f : M;
+#pragma unroll 4
+        for (int k = 0; k < nsplit; ++k)
+          L = fmaf(__ldcg(part_of(k) + (D + 1) * R + jr), ex2(__ldcg(part_of(k) + D * R + jr) - ref), L);
+        const float inv = L == 0.f ? 0.f : (1.f / kPScale) / L;
+#pragma unroll 1
+        for (int d = share * 16; d < D; d += kShares * 16) {
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          for (int k = 0; k < nsplit; ++k) {
+            const float f = ex2(__ldcg(part_of(k) + D * R + jr) - ref);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = fmaf(__ldcg(part_of(k) + (d + e) * R + jr), f, v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            store_out<D>(a, q0, h, r0 + jr, d + e, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]), inv);
+        }
+        if (share == 0) store_lse(a, q0, h, r0 + jr, M, L);
+      }
+    }
+    g0 = u_first + t1;
+    if (g0 == e_first + (long long)en.tiles * a.c.n_kv) {  // to the next entry that has tiles
+      e_first = g0;
+      if (g0 < g1)
+        do ++e_cur;
+        while (entry(e_cur).tiles == 0);
     }
   }
-  tc_fence_before();
   __syncthreads();
   if (warp == kSoft * G + kConv) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(bars.tmem), "r"(C::kCols) : "memory");
   }
-  if (nsplit == 1) return;
-
-  // the CTA that finishes last joins the splits, in split order: thread (row, share of the dims)
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) bars.last = atomicInc(a.tickets + unit, nsplit - 1) == uint32_t(nsplit - 1);
-  __syncthreads();
-  if (!bars.last) return;
-  __threadfence();
-  constexpr int kShares = kThreads / R;  // whole ones
-  const float *all = a.partial + int64_t(unit) * a.splits * kPart;
-  const int jr = tid % R, share = tid / R;
-  if (share >= kShares || jr >= nr) return;
-  float M = ninf, L = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(all + int64_t(k) * kPart + D * R + jr));
-  const float ref = M == ninf ? 0.f : M;
-#pragma unroll 4
-  for (int k = 0; k < nsplit; ++k)
-    L = fmaf(__ldcg(all + int64_t(k) * kPart + (D + 1) * R + jr), ex2(__ldcg(all + int64_t(k) * kPart + D * R + jr) - ref), L);
-  const float inv = L == 0.f ? 0.f : (1.f / kPScale) / L;
-#pragma unroll 1
-  for (int d = share * 16; d < D; d += kShares * 16) {
-    float v[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    for (int k = 0; k < nsplit; ++k) {
-      const float f = ex2(__ldcg(all + int64_t(k) * kPart + D * R + jr) - ref);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = fmaf(__ldcg(all + int64_t(k) * kPart + (d + e) * R + jr), f, v[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) store_out<D>(a, q0, h, r0 + jr, d + e, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]), inv);
-  }
-  if (share == 0) store_lse(a, q0, h, r0 + jr, M, L);
 }
 
 template <int D, int PARTS, int G>
@@ -784,8 +887,7 @@ cudaError_t run(const AttnArgs &a, cudaStream_t s) {
   const auto kernel = attn_tc_kernel<D, PARTS, G>;
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(C::kSmem));
   if (e != cudaSuccess) return e;
-  const int64_t grid = int64_t(a.n_seqs) * a.c.n_kv * a.tiles * a.splits;
-  return launch(kernel, dim3(unsigned(grid)), dim3(C::kThreads), C::kSmem, s, a);
+  return launch(kernel, dim3(a.splits), dim3(C::kThreads), C::kSmem, s, a);
 }
 template <int D, int PARTS>
 cudaError_t run(const AttnArgs &a, int groups, cudaStream_t s) {

@@ -445,6 +445,42 @@ def test_attention_repeats_bit_for_bit_on_one_workspace(cuda_lib, nq, lens):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n_seqs,nq,heads,n_kv,dim,max_kv", [
+    (1, 1, 8, 8, 128, 161), (1, 1, 4, 2, 64, 40000), (24, 1, 8, 8, 64, 9000), (40, 3, 16, 8, 128, 700), (2, 40, 4, 2, 128, 3000),
+    (2, 65, 2, 2, 64, 5000), (1, 300, 2, 1, 128, 2000)])
+def test_attention_workspace_is_enough_for_any_window(cuda_lib, n_seqs, nq, heads, n_kv, dim, max_kv):
+    # how a call is cut depends on the window; the workspace's size does not: nothing is written past it
+    import torch
+    page = 128
+    lens = [max_kv - 7 * (i % 3) for i in range(n_seqs)]
+    raw = cuda_lib.kv_pages(1, page, n_kv, dim)  # every page the same
+    table = torch.zeros(n_seqs, -(-max_kv // page), dtype=torch.int32, device="cuda")
+    size = cuda_lib.kv_attention_workspace_bytes(n_seqs, nq, max_kv, heads, n_kv, dim)
+    buf = torch.zeros(size + 8192, dtype=torch.uint8, device="cuda")
+    buf[size:] = 0x5A
+    for dtype in ("f32", "bf16"):
+        q = torch.randn(n_seqs * nq, heads, dim, device="cuda").to(_dt(dtype))
+        out = torch.full_like(q, 5.0)
+        for window in (0, 1, 17, 100, max_kv // 3, max_kv // 2, max_kv - 20, 2 * max_kv):
+            cuda_lib.kv_attention(raw, table, _i32(lens), q, out, buf[:size], heads, n_kv, dim, page, max_kv,
+                                  cu_q=_i32(np.arange(n_seqs + 1) * nq), max_q=nq, window=window)
+            assert (out == 0).all() and (buf[size:] == 0x5A).all(), window
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_attention_many_ragged_prompts(cuda_lib, dtype):
+    # prompts whose tiles are dealt out in shares that cut them: empty sequences, single queries, some longer than
+    # others, every one checked
+    rng = np.random.default_rng(11)
+    lens = [0, 700, 65, 1, 1300, 128, 0, 400, 260, 64]
+    nq = [0, 150, 65, 1, 70, 128, 0, 3, 260, 64]
+    raw, table, c = _filled(rng, lens, 32, 2, 64)
+    q = _t(1.5 * rng.standard_normal((sum(nq), 4, 64)).astype(np.float32), _dt(dtype))
+    for window in (0, 100):
+        out, lse = _attend(cuda_lib, raw, table, lens, nq, q, 4, 2, 64, 32, window=window)
+        _check_attention(c, table, lens, nq, q, out, lse, dtype, 0.125, 0, window, None)
+
+
 def test_attention_strided_rows(cuda_lib):
     # q and out inside wider buffers; other elements stay
     import torch
