@@ -157,9 +157,9 @@ template <int G>
 struct Bars {
   uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain;
   static constexpr int kBars = 8 + 6 + 6 * G + 1;
-  long long sums[20], first;
+  long long sums[20], first, g0, g1, total;  // the share's state, kept here while a part runs (registers are short)
   uint32_t tmem;
-  int abort, last, entry;
+  int abort, last, entry, shares;
 };
 
 template <int D, int PARTS, int G>
@@ -204,9 +204,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   };
   const int n_entries = a.n_seqs * a.tiles, chunk = (n_entries + kThreads - 1) / kThreads;
   long long total = 0, g0, g1;  // tiles of all units; this CTA's share of them
-  int shares, e_cur;            // CTAs that have a share; the entry of g0
-  long long e_first;            // and its first tile
-  {
+  int shares;                   // CTAs that have a share
+  {  // bars.entry, bars.first: the entry of tile g0 and its first tile
     long long mine = 0;
     for (int i = 0; i < chunk; ++i)
       if (tid * chunk + i < n_entries) mine += entry(tid * chunk + i).tiles;
@@ -241,12 +240,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       bars.entry = e;
       bars.first = before;
     }
-    __syncthreads();
-    e_cur = bars.entry;
-    e_first = bars.first;
   }
-  auto owner = [&](long long g) { return int(((g + 1) * shares - 1) / total); };  // the CTA whose share has tile g
-
   if (warp == kSoft * G + kConv) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)),
                  "r"(C::kCols)
@@ -254,19 +248,54 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
+  if (tid == 0) {
+    bars.g0 = g0;
+    bars.g1 = g1;
+    bars.total = total;
+    bars.shares = shares;
+  }
+  // (volatile reads: the values are not to live in registers through a part)
+  auto kept = [&](const long long &x) { return *reinterpret_cast<const volatile long long *>(&x); };
   bool started = false;
-  for (; g0 < g1;) {  // part by part
-    const Entry en = entry(e_cur);
-    const int h = int((g0 - e_first) / en.tiles);             // the unit: this entry and head
-    const long long u_first = e_first + (long long)h * en.tiles;
-    const int t0 = int(g0 - u_first), t1 = int(min((long long)en.tiles, g1 - u_first));  // its tiles in this part
-    const int c_lo = owner(u_first), nsplit = owner(u_first + en.tiles - 1) - c_lo + 1;  // parts of the unit
-    const int s = en.s, q0 = en.q0, len = en.len, nq = en.nq, r0 = en.r0, nr = en.nr, pos_lo = en.pos_lo, pos_hi = en.pos_hi;
-    const bool bad = en.bad;
-    const int c0 = en.b_lo + 4 * t0, cn = max(0, min(4 * (t1 - t0), en.b_hi - c0));
+  for (;;) {  // part by part
+    __syncthreads();  // the state is written; the part before is done with shared memory
+    struct Unit {
+      long long first;  // its first tile
+      int h, t0, t1, c_lo, nsplit;  // head, tiles of this part, first CTA with a part of it, parts
+    };
+    auto unit_of = [&](const Entry &en) {
+      const long long at = kept(bars.g0), e0 = kept(bars.first), all = kept(bars.total);
+      const int n = *reinterpret_cast<volatile int *>(&bars.shares);
+      auto owner = [&](long long g) { return int(((g + 1) * n - 1) / all); };  // the CTA whose share has tile g
+      Unit u;
+      u.h = int((at - e0) / en.tiles);
+      u.first = e0 + (long long)u.h * en.tiles;
+      u.t0 = int(at - u.first);
+      u.t1 = int(min((long long)en.tiles, kept(bars.g1) - u.first));
+      u.c_lo = owner(u.first);
+      u.nsplit = owner(u.first + en.tiles - 1) - u.c_lo + 1;
+      return u;
+    };
+    int s, q0, len, nq, r0, nr, pos_lo, pos_hi, c0, cn, h;
+    bool bad;
+    {
+      const Entry en = entry(*reinterpret_cast<volatile int *>(&bars.entry));
+      const Unit u = unit_of(en);
+      s = en.s;
+      q0 = en.q0;
+      len = en.len;
+      nq = en.nq;
+      r0 = en.r0;
+      nr = en.nr;
+      pos_lo = en.pos_lo;
+      pos_hi = en.pos_hi;
+      bad = en.bad;
+      h = u.h;
+      c0 = en.b_lo + 4 * u.t0;
+      cn = max(0, min(4 * (u.t1 - u.t0), en.b_hi - c0));
+    }
     const int nt = (cn + 3) / 4;
 
-    __syncthreads();  // the part before is done with shared memory
     if (tid == 0) {
       if (started)
         for (int i = 0; i < Bars<G>::kBars; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.stage[0][0] + i)) : "memory");
@@ -791,10 +820,14 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     const bool lost = bad || *reinterpret_cast<volatile int *>(&bars.abort) != 0;
     if (tid == 0 && bars.abort) atomicAdd(&g_attn_tc_timeouts, 1u);
     constexpr int kPart = R * (D + 2);
+    const int e_cur = *reinterpret_cast<volatile int *>(&bars.entry);
+    const Entry en = entry(e_cur);
+    const Unit u = unit_of(en);
+    const int nsplit = u.nsplit;
     // a CTA keeps up to two parts of cut units: the first of its share, and another, which starts its unit
-    const bool another = u_first != total * c_lo / shares;
-    auto part_of = [&](int k) { return a.partial + (2 * int64_t(c_lo + k) + (k == 0 && another)) * kPart; };  // k-th part
-    float *part = part_of(int(blockIdx.x) - c_lo);  // [dim][row], maxima, sums
+    const bool another = u.first != kept(bars.total) * u.c_lo / *reinterpret_cast<volatile int *>(&bars.shares);
+    auto part_of = [&](int k) { return a.partial + (2 * int64_t(u.c_lo + k) + (k == 0 && another)) * kPart; };  // k-th part
+    float *part = part_of(int(blockIdx.x) - u.c_lo);  // [row][dim], maxima, sums
     if (warp < kSoft * G) {
       if (lost) l = qnan;
       const float inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
@@ -820,7 +853,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) part[(c + e) * R + lr] = __uint_as_float(o[e]);
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4 *>(part + lr * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (nsplit == 1) {
@@ -832,46 +866,69 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     }
     tc_fence_before();
     if (nsplit > 1) {
-      // the CTA that finishes last joins the parts, in order: thread (row, share of the dims)
+      // the CTA that finishes last joins the parts, in order: four dims of a row per thread and step
       __threadfence();
       __syncthreads();
       if (tid == 0) bars.last = atomicInc(a.tickets + int64_t(e_cur) * a.c.n_kv + h, nsplit - 1) == uint32_t(nsplit - 1);
       __syncthreads();
-      constexpr int kShares = kThreads / R;  // whole ones
-      const int jr = tid % R, share = tid / R;
-      if (bars.last && share < kShares && jr < nr) {
+      if (bars.last) {
         __threadfence();
-        float M = ninf, L = 0.f;
+        float *s_ref = reinterpret_cast<float *>(smem), *s_inv = s_ref + R;
+        for (int r = tid; r < nr; r += kThreads) {
+          float M = ninf, L = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(part_of(k) + D * R + jr));
-        const float ref = M == ninf ? 0.f : M;
+          for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(part_of(k) + D * R + r));
+          const float ref = M == ninf ? 0.f : M;
 #pragma unroll 4
-        for (int k = 0; k < nsplit; ++k)
-          L = fmaf(__ldcg(part_of(k) + (D + 1) * R + jr), ex2(__ldcg(part_of(k) + D * R + jr) - ref), L);
-        const float inv = L == 0.f ? 0.f : (1.f / kPScale) / L;
-#pragma unroll 1
-        for (int d = share * 16; d < D; d += kShares * 16) {
-          float v[16];
+          for (int k = 0; k < nsplit; ++k)
+            L = fmaf(__ldcg(part_of(k) + (D + 1) * R + r), ex2(__ldcg(part_of(k) + D * R + r) - ref), L);
+          s_ref[r] = ref;
+          s_inv[r] = L == 0.f ? 0.f : (1.f / kPScale) / L;
+          store_lse(a, q0, h, r0 + r, M, L);
+        }
+        __syncthreads();
+        constexpr int kAhead = 4;
+        for (int i0 = tid; i0 < nr * (D / 4); i0 += kThreads * kAhead) {
+          float4 v[kAhead];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          for (int j = 0; j < kAhead; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int k = 0; k < nsplit; ++k) {
-            const float f = ex2(__ldcg(part_of(k) + D * R + jr) - ref);
+            const float *p = part_of(k);
+            float4 x[kAhead];
+            float f[kAhead];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = fmaf(__ldcg(part_of(k) + (d + e) * R + jr), f, v[e]);
+            for (int j = 0; j < kAhead; ++j) {
+              const int i = min(i0 + j * kThreads, nr * (D / 4) - 1);
+              x[j] = __ldcg(reinterpret_cast<const float4 *>(p) + i);
+              f[j] = __ldcg(p + D * R + i / (D / 4));
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+              const float w = ex2(f[j] - s_ref[min(i0 + j * kThreads, nr * (D / 4) - 1) / (D / 4)]);
+              v[j] = make_float4(fmaf(x[j].x, w, v[j].x), fmaf(x[j].y, w, v[j].y), fmaf(x[j].z, w, v[j].z), fmaf(x[j].w, w, v[j].w));
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            store_out<D>(a, q0, h, r0 + jr, d + e, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]), inv);
+          for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads, r = i / (D / 4);
+            if (i < nr * (D / 4)) store_out<D>(a, q0, h, r0 + r, i % (D / 4) * 4, v[j], s_inv[r]);
+          }
         }
-        if (share == 0) store_lse(a, q0, h, r0 + jr, M, L);
       }
     }
-    g0 = u_first + t1;
-    if (g0 == e_first + (long long)en.tiles * a.c.n_kv) {  // to the next entry that has tiles
-      e_first = g0;
-      if (g0 < g1)
-        do ++e_cur;
-        while (entry(e_cur).tiles == 0);
+    const long long next = u.first + u.t1, end = kept(bars.first) + (long long)en.tiles * a.c.n_kv;
+    const bool more = next < kept(bars.g1);
+    __syncthreads();  // every thread has read the state
+    if (!more) break;
+    if (tid == 0) {
+      bars.g0 = next;
+      if (next == end) {  // to the next entry that has tiles
+        int e = e_cur;
+        do ++e;
+        while (entry(e).tiles == 0);
+        bars.entry = e;
+        bars.first = next;
+      }
     }
   }
   __syncthreads();
