@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     // a CTA keeps up to two parts of cut units: the first of its share, and another, which starts its unit
     const bool another = u.first != kept(bars.total) * u.c_lo / *reinterpret_cast<volatile int *>(&bars.shares);
     auto part_of = [&](int k) { return a.partial + (2 * int64_t(u.c_lo + k) + (k == 0 && another)) * kPart; };  // k-th part
-    float *part = part_of(int(blockIdx.x) - u.c_lo);  // [row][dim], maxima, sums
+    float *part = part_of(int(blockIdx.x) - u.c_lo);  // [four dims][row][4], maxima, sums
     if (warp < kSoft * G) {
       if (lost) l = qnan;
       const float inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         } else {
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4 *>(part + lr * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            *reinterpret_cast<uint4 *>(part + (c + e) * R + 4 * lr) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (nsplit == 1) {
@@ -866,7 +866,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     }
     tc_fence_before();
     if (nsplit > 1) {
-      // the CTA that finishes last joins the parts, in order: four dims of a row per thread and step
+      // the CTA that finishes last joins the parts, in order: four dims of a row per thread and
+      // step, a warp 16 dims of 8 rows (whole sectors of the parts and of the output)
       __threadfence();
       __syncthreads();
       if (tid == 0) bars.last = atomicInc(a.tickets + int64_t(e_cur) * a.c.n_kv + h, nsplit - 1) == uint32_t(nsplit - 1);
@@ -887,31 +888,42 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           store_lse(a, q0, h, r0 + r, M, L);
         }
         __syncthreads();
-        constexpr int kAhead = 4;
-        for (int i0 = tid; i0 < nr * (D / 4); i0 += kThreads * kAhead) {
+        constexpr int kAhead = 4, kItems = R * D / 4;
+        auto at = [&](int i, int &r, int &d4) {
+          const int block = i / 32, in = i % 32;
+          r = block % (R / 8) * 8 + in % 8;
+          d4 = block / (R / 8) * 4 + in / 8;
+        };
+        for (int i0 = tid; i0 < kItems; i0 += kThreads * kAhead) {
           float4 v[kAhead];
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
           for (int k = 0; k < nsplit; ++k) {
             const float *p = part_of(k);
             float4 x[kAhead];
             float f[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-              const int i = min(i0 + j * kThreads, nr * (D / 4) - 1);
-              x[j] = __ldcg(reinterpret_cast<const float4 *>(p) + i);
-              f[j] = __ldcg(p + D * R + i / (D / 4));
+              int r, d4;
+              at(min(i0 + j * kThreads, kItems - 1), r, d4);
+              x[j] = __ldcg(reinterpret_cast<const float4 *>(p) + d4 * R + r);
+              f[j] = __ldcg(p + D * R + r);
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-              const float w = ex2(f[j] - s_ref[min(i0 + j * kThreads, nr * (D / 4) - 1) / (D / 4)]);
+              int r, d4;
+              at(min(i0 + j * kThreads, kItems - 1), r, d4);
+              const float w = ex2(f[j] - s_ref[r]);
               v[j] = make_float4(fmaf(x[j].x, w, v[j].x), fmaf(x[j].y, w, v[j].y), fmaf(x[j].z, w, v[j].z), fmaf(x[j].w, w, v[j].w));
             }
           }
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j * kThreads, r = i / (D / 4);
-            if (i < nr * (D / 4)) store_out<D>(a, q0, h, r0 + r, i % (D / 4) * 4, v[j], s_inv[r]);
+            const int i = i0 + j * kThreads;
+            int r, d4;
+            at(i, r, d4);
+            if (i < kItems && r < nr) store_out<D>(a, q0, h, r0 + r, 4 * d4, v[j], s_inv[r]);
           }
         }
       }
