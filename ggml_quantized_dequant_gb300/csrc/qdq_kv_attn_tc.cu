@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     }
     const int nt = (cn + 3) / 4;
 
-    if (tid == 0) {
+    if (tid == 32 * (kSoft * G + kConv)) {
       if (started)
         for (int i = 0; i < Bars<G>::kBars; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.stage[0][0] + i)) : "memory");
       for (int i = 0; i < 2; ++i) {
@@ -319,6 +319,31 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     }
     started = true;
     const int64_t vplane = int64_t(a.c.page_tokens) * D;
+    // copies of tile i's codes into its stage
+    auto copy_tile = [&](int i) {
+      if constexpr (C::kStaged) {
+        const int set = i % C::kSets, n = i / C::kSets % C::kSlots;
+        uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
+        uint64_t *bar = &bars.stage[set][n];
+        int64_t at[4];
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          at[b] = s_blk[4 * i + b].k;
+          bytes += at[b] >= 0 ? 32 * D : 0;
+        }
+        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (at[b] < 0) continue;  // no such block: its part of the stage is not read
+          const uint8_t *p = a.c.pages + at[b];
+          bulk_copy_g2s(dst + b * 16 * D, p, 16 * D, bar);
+          bulk_copy_g2s(dst + C::kStageV + (2 * b) * C::kVStep, p + vplane, 8 * D, bar);
+          bulk_copy_g2s(dst + C::kStageV + (2 * b + 1) * C::kVStep, p + vplane + 8 * D, 8 * D, bar);
+        }
+      }
+    };
+    int copied = 0;  // tiles whose copies have been issued (the copying lane's)
     // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row.  A lane
     // copies its 8 dims of all its rows into the tiles' space first (all copies in flight at once,
     // each read back by the lane that made it) and converts them in a small loop.
@@ -434,6 +459,12 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           }
         }
         s_blk[i] = e;
+      }
+      if constexpr (C::kStaged) {  // and the first tiles' copies
+        named_bar_sync(4, 64);
+        if (tid == 32 * (kSoft * G + kConv + 1))
+          for (; copied < min(nt, C::kSets * C::kSlots); ++copied) copy_tile(copied);
+        __syncwarp();
       }
     }
     tc_fence_before();
@@ -711,34 +742,16 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       // ---------------- copies of the codes ----------------
       if constexpr (C::kStaged) {
         if (lane == 0) {
-          int done = 0;  // tiles whose copies have been issued
-          for (int i = 0; i < nt; ++i, ++done) {
-            const int set = i % C::kSets, use = i / C::kSets, n = use % C::kSlots;  // the set's use-th tile
-            if (use >= C::kSlots && !mbar_wait(&bars.sread[set][n], uint32_t(use / C::kSlots - 1) & 1u)) {
+          for (; copied < nt; ++copied) {
+            const int set = copied % C::kSets, use = copied / C::kSets, n = use % C::kSlots;  // the set's use-th tile
+            if (!mbar_wait(&bars.sread[set][n], uint32_t(use / C::kSlots - 1) & 1u)) {
               give_up();
               break;
             }
-            uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
-            uint64_t *bar = &bars.stage[set][n];
-            int64_t at[4];
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              at[b] = s_blk[4 * i + b].k;
-              bytes += at[b] >= 0 ? 32 * D : 0;
-            }
-            mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              if (at[b] < 0) continue;  // no such block: its part of the stage is not read
-              const uint8_t *p = a.c.pages + at[b];
-              bulk_copy_g2s(dst + b * 16 * D, p, 16 * D, bar);
-              bulk_copy_g2s(dst + C::kStageV + (2 * b) * C::kVStep, p + vplane, 8 * D, bar);
-              bulk_copy_g2s(dst + C::kStageV + (2 * b + 1) * C::kVStep, p + vplane + 8 * D, 8 * D, bar);
-            }
+            copy_tile(copied);
           }
           // no copy may be in flight when the CTA ends, also after giving up: each stage's last one
-          for (int i = max(0, done - C::kSets * C::kSlots); i < done; ++i)
+          for (int i = max(0, copied - C::kSets * C::kSlots); i < copied; ++i)
             if (!mbar_wait(&bars.stage[i % C::kSets][i / C::kSets % C::kSlots], uint32_t(i / C::kSets / C::kSlots) & 1u))
               atomicAdd(&g_attn_tc_timeouts, 1u);
         }
