@@ -496,7 +496,7 @@ def kv_attention_workspace_bytes(n_seqs: int, max_q: int, max_kv_len: int, n_hea
 
 
 def kv_attention_workspace(n_seqs: int, max_q: int, max_kv_len: int, n_heads: int, n_kv: int, head_dim: int, device="cuda"):
-    """A zeroed workspace of :func:`kv_attention`; calls on one stream may share it."""
+    """A zeroed workspace of :func:`kv_attention`; calls on one stream may share it, also with :func:`token_logprobs`."""
     import torch
     return torch.zeros(kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim), dtype=torch.uint8,
                        device=device)
@@ -534,7 +534,7 @@ def token_logprobs_workspace_bytes(rows: int, n: int, k: int) -> int:
 
 
 def token_logprobs_workspace(rows: int, n: int, k: int, device="cuda"):
-    """A zeroed workspace of :func:`token_logprobs`; calls on one stream may share it."""
+    """A zeroed workspace of :func:`token_logprobs`; calls on one stream may share it, also with :func:`kv_attention`."""
     import torch
     return torch.zeros(token_logprobs_workspace_bytes(rows, n, k), dtype=torch.uint8, device=device)
 

@@ -162,7 +162,7 @@ int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, 
   if (workspace_bytes < need) return QDQ_ERR_SCRATCH;
   const KvPool c{static_cast<uint8_t *>(const_cast<void *>(pages)), page_table, n_pages, page_tokens, n_kv, table_stride};
   return launch_kv_attention(c, head_dim, kv_len, cu_q, n_seqs, max_q, max_kv_len, n_heads, q, q_stride, out, out_stride, lse,
-                             slopes, scale, softcap, window, type, workspace, stream);
+                             slopes, scale, softcap, window, type, workspace, workspace_bytes, stream);
 }
 
 size_t qdq_token_logprobs_workspace_bytes(int rows, int n, int k) {
@@ -192,7 +192,7 @@ int qdq_token_logprobs(const void *logits, long long row_stride, int type, const
       if (clash(o[i], o[j])) return QDQ_ERR_ALIAS;
   }
   if (workspace_bytes < token_logprobs_workspace_bytes(rows, n, k)) return QDQ_ERR_SCRATCH;
-  return launch_token_logprobs(logits, row_stride, type, tokens, rows, n, k, workspace, logprob, entropy, top_index,
+  return launch_token_logprobs(logits, row_stride, type, tokens, rows, n, k, workspace, workspace_bytes, logprob, entropy, top_index,
                                top_logprob, stream);
 }
 

@@ -578,7 +578,7 @@ struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
   int parts, groups, warps, tiles, splits, split_blocks;
   int64_t units;
-  size_t ticket_bytes, bytes;  // bytes: for any window
+  size_t bytes;  // of the workspace, for any window
 };
 
 Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, int window,
@@ -600,8 +600,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     const int64_t wave = int64_t(di.sm_count) * (kTcSplitBlocks / 4);
     const int64_t ctas = di.sm_count * ((most + wave - 1) / wave);
     p.splits = int(ctas < 0x7fffffff ? ctas : 0);
-    p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
-    p.bytes = p.ticket_bytes + 2 * size_t(ctas) * attn_tc_part_bytes(head_dim, p.groups);
+    p.bytes = workspace_for(size_t(p.units), 2 * size_t(ctas) * attn_tc_part_bytes(head_dim, p.groups));
     return p;
   }
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
@@ -630,7 +629,6 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   p.split_blocks = int(per);
   p.splits = int((blocks + per - 1) / per);
   if (p.splits < 1) p.splits = 1;
-  p.ticket_bytes = (size_t(p.units) * 4 + 255) / 256 * 256;
   // another window can give up to as many splits as either size of CTA aims at or is forced to
   int64_t most = 1;
   for (int warps : {4, resident})
@@ -640,7 +638,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
       for (int64_t n : {aim < max_splits(warps) ? aim : max_splits(warps), forced})
         if (n > most) most = n;
     }
-  p.bytes = p.ticket_bytes + (most > 1 ? size_t(p.units) * size_t(most) * R * (head_dim + 2) * 4 : 0);
+  p.bytes = workspace_for(size_t(p.units), most > 1 ? size_t(p.units) * size_t(most) * R * (head_dim + 2) * 4 : 0);
   return p;
 }
 
@@ -660,7 +658,7 @@ size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n
 int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, int n_seqs, int max_q,
                         int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,
                         float *lse, const float *slopes, float scale, float softcap, int window, int type,
-                        void *workspace, cudaStream_t s) {
+                        void *workspace, size_t workspace_bytes, cudaStream_t s) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
@@ -675,7 +673,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.lse = lse;
   a.slopes = slopes;
   a.tickets = static_cast<uint32_t *>(workspace);
-  a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + p.ticket_bytes);
+  a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes));
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.n_seqs = n_seqs;

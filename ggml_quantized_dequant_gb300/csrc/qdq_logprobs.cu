@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
 
 struct Plan {
   int segs, seg_tiles;
-  size_t ticket_bytes, bytes;
+  size_t bytes;
 };
 Plan plan(const DeviceInfo &di, int rows, int n, int k) {
   Plan p{};
@@ -486,8 +486,7 @@ Plan plan(const DeviceInfo &di, int rows, int n, int k) {
     }
   }
   p.segs = (tiles + p.seg_tiles - 1) / p.seg_tiles;
-  p.ticket_bytes = (size_t(rows) * 4 + 255) / 256 * 256;
-  p.bytes = p.ticket_bytes + (p.segs > 1 ? size_t(rows) * p.segs * part_bytes(k) : 0);
+  p.bytes = workspace_for(size_t(rows), p.segs > 1 ? size_t(rows) * p.segs * part_bytes(k) : 0);
   return p;
 }
 
@@ -502,15 +501,15 @@ size_t token_logprobs_workspace_bytes(int rows, int n, int k) {
 }
 
 int launch_token_logprobs(const void *logits, int64_t stride, int type, const int *tokens, int rows, int n, int k,
-                          void *workspace, float *logprob, float *entropy, int *top_index, float *top_logprob,
-                          cudaStream_t s) {
+                          void *workspace, size_t workspace_bytes, float *logprob, float *entropy, int *top_index,
+                          float *top_logprob, cudaStream_t s) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
   const Plan p = plan(di, rows, n, k);
   if (int64_t(rows) * p.segs > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
   const LpArgs a{logits, stride, tokens, logprob, entropy, top_logprob, top_index, static_cast<uint32_t *>(workspace),
-                 static_cast<uint8_t *>(workspace) + p.ticket_bytes, n, k, p.segs, p.seg_tiles};
+                 static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes), n, k, p.segs, p.seg_tiles};
   e = cudaError_t(with_type(type, [&](auto t) {
     const auto kernel = logprobs_kernel<decltype(t)>;
     const cudaError_t r = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(sizeof(Shared)));

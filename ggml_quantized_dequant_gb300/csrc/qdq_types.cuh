@@ -118,14 +118,22 @@ int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int
                      const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s);
 int launch_kv_read(const KvPool &c, int head_dim, const int *start, const int *cu, int n_seqs, int max_tokens, void *k,
                    void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s);
+// A workspace holds the tickets (zero between calls) in its first eighth and the parts in the rest.  The
+// border follows from the workspace's size alone, so that no call of another shape or operator on the
+// same workspace writes where this one's tickets are.
+inline size_t workspace_tickets(size_t bytes) { return bytes / 8 / 256 * 256; }
+inline size_t workspace_for(size_t tickets, size_t part_bytes) {  // its bytes for that many 4-byte tickets
+  const size_t t = (tickets * 4 + 255) / 256 * 2048, p = (part_bytes + 6) / 7 * 8;
+  return ((t > p ? t : p) + 2047) / 2048 * 2048;
+}
 size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
 int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, int n_seqs, int max_q,
                         int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,
                         float *lse, const float *slopes, float scale, float softcap, int window, int type,
-                        void *workspace, cudaStream_t s);
+                        void *workspace, size_t workspace_bytes, cudaStream_t s);
 size_t token_logprobs_workspace_bytes(int rows, int n, int k);
 int launch_token_logprobs(const void *logits, int64_t stride, int type, const int *tokens, int rows, int n, int k,
-                          void *workspace, float *logprob, float *entropy, int *top_index, float *top_logprob,
-                          cudaStream_t s);
+                          void *workspace, size_t workspace_bytes, float *logprob, float *entropy, int *top_index,
+                          float *top_logprob, cudaStream_t s);
 
 }  // namespace qdq

@@ -375,7 +375,8 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
  * q, out: head_dim elements per head, n_heads heads per row, rows q_stride /
  * out_stride elements apart, 16-byte aligned (strides whole 16 bytes).  out may overlap no other argument.
  * workspace: qdq_kv_attention_workspace_bytes(...) bytes (0 when no device can be queried), 256-byte aligned, ZEROED ONCE by
- * the caller before its first use; a call leaves it ready for the next one on the same stream.
+ * the caller before its first use; a call leaves it ready for the next one on the same stream, also one of
+ * other sizes, types or windows, or of qdq_token_logprobs, that is given the same workspace and workspace_bytes.
  * Results do not depend on the order in which CTAs run.
  */
 #define QDQ_MAX_KV_LEN 4194304   /* the largest max_kv_len */

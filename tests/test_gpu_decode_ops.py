@@ -445,6 +445,39 @@ def test_attention_repeats_bit_for_bit_on_one_workspace(cuda_lib, nq, lens):
             assert torch.equal(a, b)
 
 
+def test_calls_of_other_shapes_share_a_workspace(cuda_lib):
+    # whatever one call keeps in the workspace must not count as another's tickets
+    import torch
+    rng = np.random.default_rng(11)
+    shapes = [  # (lengths, queries of each, heads, cache heads, dims, type, window)
+        ([900, 1400], [200, 300], 6, 2, 64, "bf16", 0), ([700] * 40, [1] * 40, 8, 8, 64, "f32", 0),
+        ([900, 1400], [200, 300], 4, 2, 256, "f32", 0), ([900, 1400], [200, 300], 4, 2, 256, "bf16", 100),
+        ([5000], [1], 6, 2, 128, "f16", 0), ([64] * 500, [1] * 500, 2, 2, 64, "f32", 0)]
+    size = max([cuda_lib.kv_attention_workspace_bytes(len(lens), max(nq), max(lens), h, kv, d) for lens, nq, h, kv, d, _, _ in shapes]
+               + [cuda_lib.token_logprobs_workspace_bytes(r, n, 9) for r, n in ((1, 100000), (700, 300))])
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    calls = []
+    for lens, nq, heads, n_kv, dim, dtype, window in shapes:
+        raw, table, _ = _filled(rng, lens, 32, n_kv, dim)
+        q = _t(rng.standard_normal((sum(nq), heads, dim)).astype(np.float32), _dt(dtype))
+        calls.append(lambda w, raw=raw, table=table, lens=lens, nq=nq, q=q, h=heads, kv=n_kv, d=dim, win=window:
+                     [_np(t) for t in _attend(cuda_lib, raw, table, lens, nq, q, h, kv, d, 32, window=win, workspace=w)])
+    for rows, n in ((1, 100000), (700, 300)):
+        x = _t(rng.standard_normal((rows, n)).astype(np.float32))
+
+        def scores(w, x=x, rows=rows, n=n):
+            out = [torch.full(s, float("nan"), device="cuda") for s in ((rows,), (rows,), (rows, 9))]
+            ids = torch.full((rows, 9), -1, dtype=torch.int32, device="cuda")
+            w = cuda_lib.token_logprobs_workspace(rows, n, 9) if w is None else w
+            cuda_lib.token_logprobs(x, _i32(np.zeros(rows)), out[0], out[1], rows, n, w, 9, ids, out[2])
+            return [_np(t) for t in out + [ids]]
+        calls.append(scores)
+    alone = [c(None) for c in calls]
+    for i in list(range(len(calls))) + list(rng.integers(0, len(calls), 24)):
+        for a, b in zip(calls[i](ws), alone[i]):
+            assert np.array_equal(a, b, equal_nan=True), i
+
+
 @pytest.mark.parametrize("n_seqs,nq,heads,n_kv,dim,max_kv", [
     (1, 1, 8, 8, 128, 161), (1, 1, 4, 2, 64, 40000), (24, 1, 8, 8, 64, 9000), (40, 3, 16, 8, 128, 700), (2, 40, 4, 2, 128, 3000),
     (2, 65, 2, 2, 64, 5000), (1, 300, 2, 1, 128, 2000)])
