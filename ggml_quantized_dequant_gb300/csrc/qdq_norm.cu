@@ -4,10 +4,14 @@
 //   h = x + r,   y = h / sqrt(mean(h^2) + eps) * w
 //   Q8_0: d = f16(max |y| / 127) over 32 consecutive y, code = rint(y * (1 / d)) within +-127
 //
-// One CTA per row.  The row is read once into registers (8 to 32 elements per thread, all
-// loads before the first use), its sum of squares is folded over the warps through shared
-// memory in a fixed order, and every output is written from the registers: x and r are read
-// once and each output written once, which is the floor.  Sums are f32.
+// Bound: memory (4 elements moved per element with residual and sum), for one row latency.  A row
+// is read once into registers (8 to 32 elements per thread, all loads before the first use), its sum of
+// squares is folded over the warps through shared memory in a fixed order, and every output is
+// written from the registers: x and r are read once and each output written once, which is the floor.
+// One CTA per row, or, for many wide or many short rows, CTAs that take row after row through a ring
+// (the rule stands at the launch).  Sums are f32.
+// Measured: one row of 3072 f32 1.8 us; 4096 rows of 8192 bf16 with residual 43 us (6.2 TB/s, 92 % of a
+// plain copy's rate); 1500 rows of 3072 f32 with residual to f32 and Q8_0 14.4 us (5.5 TB/s).
 #include "qdq_types.cuh"
 
 namespace qdq {
@@ -44,6 +48,22 @@ __device__ __forceinline__ void load_v(const T *p, float (&v)[V]) {
     v[0] = load1(p);
   }
 }
+// 16 bytes of shared memory as elements.
+template <typename T, int V>
+__device__ __forceinline__ void load_s(const T *p, float (&v)[V]) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (V == 8) {
+      const float2 f = unpack2(w[i], T{});
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
 template <int V, typename T>
 __device__ __forceinline__ void store_v(T *p, const float (&v)[V]) {
   if constexpr (V == 8) {
@@ -56,8 +76,81 @@ __device__ __forceinline__ void store_v(T *p, const float (&v)[V]) {
   }
 }
 
+template <int V>
+__device__ __forceinline__ void load_weight(const float *p, float (&w)[V]) {
+  if constexpr (V == 8) {
+    const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p)), w1 = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+    w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
+  } else if constexpr (V == 4) {
+    const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p));
+    w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+  } else {
+    w[0] = __ldg(p);
+  }
+}
+
 // V elements per load (16 or 8 bytes, or 1 element where the rows are not aligned), E elements
 // per thread; element (i * blockDim + thread) * V + j of the row is the thread's i-th group.
+
+// The row's norm and outputs from its elements in registers; weight(i, w) gives group i's weights.
+template <typename T, int V, int E, typename W>
+__device__ __forceinline__ void norm_row(const NormArgs &a, int row, const float (&h)[E / V][V], float *part, W &&weight) {
+  constexpr int G = E / V;
+  const int n = a.n;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) s = fmaf(h[i][j], h[i][j], s);
+  s = warp_sum(s);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[warp] = s;
+  __syncthreads();
+  s = warp_sum(lane < int(blockDim.x >> 5) ? part[lane] : 0.f);
+  const float inv = rsqrtf(s / float(n) + a.eps);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+    const bool in = e < n;
+    if (in && a.sum_out) store_v<V>(static_cast<T *>(a.sum_out) + row * a.sum_stride + e, h[i]);
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = h[i][j] * inv;
+    if (in && a.weight) {
+      float w[V];
+      weight(i, w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] *= w[j];
+    }
+    if (in && a.out) store_v<V>(static_cast<T *>(a.out) + row * a.out_stride + e, y);
+    if (a.q8) {  // n % 32 == 0: a block of 32 lies in 32 / V neighbouring lanes, all in or all past the row
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) m = max_abs_bits(m, y[j]);
+#pragma unroll
+      for (int o = 16 / V; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const __half d = __float2half_rn(__fdiv_rn(m, 127.f));
+      const float df = __half2float(d);
+      const float id = df > 0.f ? __frcp_rn(df) : 0.f;
+      if (in) {
+        int8_t q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[j] = int8_t(__float2int_rn(fminf(fmaxf(y[j] * id, -127.f), 127.f)));
+        int8_t *qp = reinterpret_cast<int8_t *>(a.q8) + int64_t(row) * n + e;
+        if constexpr (V == 8)
+          *reinterpret_cast<uint2 *>(qp) = *reinterpret_cast<const uint2 *>(q);
+        else if constexpr (V == 4)
+          *reinterpret_cast<uint32_t *>(qp) = *reinterpret_cast<const uint32_t *>(q);
+        else
+          *qp = q[0];
+        if ((e & 31) == 0)
+          reinterpret_cast<__half *>(a.q8 + int64_t(a.rows) * n)[int64_t(row) * (n / 32) + e / 32] = d;
+      }
+    }
+  }
+}
+
 template <typename T, int V, int E>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
   constexpr int G = E / V;
@@ -94,66 +187,98 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
       }
     }
   }
-  float s = 0.f;
+  if constexpr (E <= 16) {  // the weights' latency beside the sum's
+    float w[G][V];
 #pragma unroll
-  for (int i = 0; i < G; ++i)
+    for (int i = 0; i < G; ++i) {
+      const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+      if (a.weight && e < n) load_weight<V>(a.weight + e, w[i]);
+    }
+    norm_row<T, V, E>(a, row, h, part, [&](int i, float (&v)[V]) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) s = fmaf(h[i][j], h[i][j], s);
-  s = warp_sum(s);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) part[warp] = s;
-  __syncthreads();
-  s = warp_sum(lane < int(blockDim.x >> 5) ? part[lane] : 0.f);
-  const float inv = rsqrtf(s / float(n) + a.eps);
+      for (int j = 0; j < V; ++j) v[j] = w[i][j];
+    });
+  } else {  // no registers for them
+    norm_row<T, V, E>(a, row, h, part, [&](int i, float (&w)[V]) {
+      load_weight<V>(a.weight + (i * int(blockDim.x) + int(threadIdx.x)) * V, w);
+    });
+  }
+}
+
+// Many rows: as many CTAs as fit, each takes every gridDim-th row.  A thread copies its own elements of
+// the next rows into shared memory (no barrier: it alone reads them) while a row is summed and written.
+constexpr int kStages = 3;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <typename T, int E>
+__global__ void __launch_bounds__(1024) rms_norm_rows_kernel(const NormArgs a) {
+  constexpr int V = 16 / sizeof(T), G = E / V;
+  extern __shared__ uint8_t ring[];
+  __shared__ float part[2][32];
+  const int n = a.n, tid = threadIdx.x, threads = blockDim.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint32_t mine = smem_u32(ring) + 16 * tid, group = 16 * threads, slot = (a.residual ? 2 : 1) * G * group;
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) {
+      const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
+      const T *r = static_cast<const T *>(a.residual) + row * a.residual_stride;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int e = (i * threads + tid) * V;
+        if (e < n) {
+          copy16(mine + st * slot + i * group, x + e);
+          if (a.residual) copy16(mine + st * slot + (G + i) * group, r + e);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float w[G][V];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
-    const int e = (i * int(blockDim.x) + int(threadIdx.x)) * V;
-    const bool in = e < n;
-    if (in && a.sum_out) store_v<V>(static_cast<T *>(a.sum_out) + row * a.sum_stride + e, h[i]);
-    float y[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) y[j] = h[i][j] * inv;
-    if (in && a.weight) {
-      float w[V];
-      if constexpr (V == 8) {
-        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + e)), w1 = __ldg(reinterpret_cast<const float4 *>(a.weight + e) + 1);
-        w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-        w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
-      } else if constexpr (V == 4) {
-        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + e));
-        w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-      } else {
-        w[0] = __ldg(a.weight + e);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) y[j] *= w[j];
-    }
-    if (in && a.out) store_v<V>(static_cast<T *>(a.out) + row * a.out_stride + e, y);
-    if (a.q8) {  // n % 32 == 0: a block of 32 lies in 32 / V neighbouring lanes, all in or all past the row
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) m = max_abs_bits(m, y[j]);
-#pragma unroll
-      for (int o = 16 / V; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const __half d = __float2half_rn(__fdiv_rn(m, 127.f));
-      const float df = __half2float(d);
-      const float id = df > 0.f ? __frcp_rn(df) : 0.f;
-      if (in) {
-        int8_t q[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) q[j] = int8_t(__float2int_rn(fminf(fmaxf(y[j] * id, -127.f), 127.f)));
-        int8_t *qp = reinterpret_cast<int8_t *>(a.q8) + int64_t(row) * n + e;
-        if constexpr (V == 8)
-          *reinterpret_cast<uint2 *>(qp) = *reinterpret_cast<const uint2 *>(q);
-        else if constexpr (V == 4)
-          *reinterpret_cast<uint32_t *>(qp) = *reinterpret_cast<const uint32_t *>(q);
-        else
-          *qp = q[0];
-        if ((e & 31) == 0)
-          reinterpret_cast<__half *>(a.q8 + int64_t(a.rows) * n)[int64_t(row) * (n / 32) + e / 32] = d;
-      }
-    }
+    const int e = (i * threads + tid) * V;
+    if (a.weight && e < n) load_weight<V>(a.weight + e, w[i]);
   }
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
+  int st = 0, k = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, k ^= 1) {
+    fetch(row + int64_t(kStages - 1) * gridDim.x, st == 0 ? kStages - 1 : st - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    float h[G][V];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const uint8_t *at = ring + 16 * tid + st * slot + i * group;
+      const bool in = (i * threads + tid) * V < n;
+      if (in) {
+        load_s(reinterpret_cast<const T *>(at), h[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] = 0.f;
+      }
+      if (in && a.residual) {
+        float b[V];
+        load_s(reinterpret_cast<const T *>(at + G * group), b);
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[i][j] += b[j];
+      }
+    }
+    norm_row<T, V, E>(a, int(row), h, part[k], [&](int i, float (&v)[V]) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = w[i][j];
+    });
+    if (++st == kStages) st = 0;
+  }
+}
+
+template <typename T, int E>
+cudaError_t run_rows(const NormArgs &a, int ctas, int threads, cudaStream_t s) {
+  const auto kernel = rms_norm_rows_kernel<T, E>;
+  const int bytes = kStages * (a.residual ? 2 : 1) * E * int(sizeof(T)) * threads;
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes);
+  return e != cudaSuccess ? e : launch(kernel, dim3(ctas), dim3(threads), bytes, s, a);
 }
 
 template <typename T, int V, int E>
@@ -171,6 +296,9 @@ int launch_rms_norm(const void *x, const void *residual, const float *weight, vo
   const NormArgs a{x, residual, weight, sum_out, out, static_cast<uint8_t *>(q8), rows, n, x_stride, residual_stride,
                    sum_stride, out_stride, eps};
   const int eb = type_bytes(type);
+  DeviceInfo di;
+  const cudaError_t de = device_info(&di);
+  if (de != cudaSuccess) return fail_cuda(de);
   // vector loads where every row of every operand starts on a vector boundary
   auto fits = [&](int v) {
     const uintptr_t b = uintptr_t(v) * eb;
@@ -184,8 +312,21 @@ int launch_rms_norm(const void *x, const void *residual, const float *weight, vo
     using T = decltype(t);
     auto pick = [&](auto v) {
       constexpr int V = decltype(v)::value;
-      // the fewest elements per thread that a CTA can hold: at 4096 rows of 8192 (bf16, residual) 8, 16
-      // and 32 per thread took 47.4, 52.8 and 55.2 us, one row of 3072 1.9, 2.1 and 3.6 us
+      // the fewest elements per thread that a CTA can hold: at 4096 rows of 8192 (bf16, residual, a CTA
+      // each) 8, 16 and 32 per thread took 47.4, 52.8 and 55.2 us, one row of 3072 1.9, 2.1 and 3.6 us
+      if constexpr (V * sizeof(T) == 16) {
+        // Rows through a ring where only two CTAs of one row each fit an SM (they wait on barriers and memory
+        // by turns; 4096 rows of 8192 bf16 with residual 47.2 -> 43.0 us, f32 without 48.2 -> 42.9 us) and
+        // shared memory has room for two as well (f32 with residual: one, 78 -> 89 us), or where a row is
+        // moved in less time than a CTA is started (60000 rows of 256 bf16: 60.6 -> 21.3 us, 30000 of 512
+        // 30.6 -> 20.1 us).  Between, small CTAs hide each other's barriers (8192 rows of 4096 bf16: 41.4, ring 44.0 us).
+        const int threads = ((n + 7) / 8 + 31) / 32 * 32, fit = 2048 / threads;
+        if (n <= 8192 && (fit <= 2 || n * eb <= 1536)) {
+          const int smem = kStages * (residual ? 2 : 1) * 8 * eb * threads, room = 220 * 1024 / (smem + 1280);
+          const int most = fit < 32 ? fit : 32, ctas = di.sm_count * (most < room ? most : room);
+          if (room >= 2 && rows > 2 * ctas) return run_rows<T, 8>(a, ctas, threads, s);
+        }
+      }
       if (n <= 8192) return run_norm<T, V, 8>(a, s);
       if (n <= 16384) return run_norm<T, V, 16>(a, s);
       return run_norm<T, V, 32>(a, s);

@@ -119,6 +119,36 @@ def test_norm_to_q8_0(cuda_lib, rows, n, dtype):
     assert (_np(val)[0, :32] == 0).all()
 
 
+@pytest.mark.parametrize("rows,n,dtype,residual,pad", [
+    (650, 8192, "bf16", True, 0), (1251, 7160, "f16", True, 8), (611, 5600, "f32", False, 4), (620, 8192, "f32", True, 0),
+    (9800, 96, "bf16", True, 0), (20001, 8, "f16", False, 8), (9729, 384, "f32", True, 0), (10001, 320, "f16", True, 32)])
+def test_norm_many_rows(cuda_lib, rows, n, dtype, residual, pad):
+    # CTAs that take several rows: strided, in place, with every output
+    import torch
+    rng = np.random.default_rng(rows + n)
+    buf = _t(rng.standard_normal((2, rows * (n + pad))).astype(np.float32), _dt(dtype))
+    x, r = (b.as_strided((rows, n), (n + pad, 1)) for b in buf)
+    w = _t(rng.standard_normal(n).astype(np.float32))
+    y, h = ref.rms_norm(_np(x), _np(r) if residual else None, _np(w), 1e-5)
+    before = buf.clone()
+    q8 = n % 32 == 0
+    packed = torch.full((cuda_lib.q8_0_packed_bytes(rows, n),), 0x55, dtype=torch.uint8, device="cuda") if q8 else None
+    cuda_lib.rms_norm(x, w, x, rows, n, 1e-5, residual=r if residual else None, sum_out=r, q8_out=packed)
+    tiny = 2.0 ** -25 if dtype == "f16" else 0
+    _within(_np(x), y, (64 * U + EPS[dtype]) * np.abs(y) + tiny)
+    _within(_np(r), h, EPS[dtype] * np.abs(h) + tiny)
+    mask = torch.ones_like(buf, dtype=torch.bool)
+    for m in mask:
+        m.as_strided((rows, n), (n + pad, 1)).fill_(False)
+    assert torch.equal(buf[mask], before[mask])
+    if q8:
+        val = torch.empty(rows, n, device="cuda")
+        cuda_lib.q8_0_dequant(packed, val, rows, n)
+        m = np.abs(y.reshape(rows, -1, 32)).max(-1, keepdims=True)
+        step = (m / 127 * (0.5 + 127 * 2.0 ** -11) * (1 + 2.0 ** -10) + 128 * 2.0 ** -25) * np.ones((1, 1, 32))
+        _within(_np(val), y, step.reshape(rows, n) + 64 * U * np.abs(y))
+
+
 def test_norm_rows_that_are_not_finite_or_zero(cuda_lib):
     import torch
     x = torch.randn(4, 64, device="cuda")
