@@ -147,9 +147,9 @@ struct Cfg {
   static constexpr uint32_t kSmem = kBytes > 116 * 1024 ? kBytes : 116 * 1024;
   static_assert(kSmem <= 225 * 1024, "shared memory");
   static constexpr int kConv = kSet * kSets;
-  static constexpr int kThreads = 32 * (kSoft * G + kConv + 2);
-  // 18 warps are launched with 96 registers a thread: 8 softmax warps x 128 + 8 converting x 64
-  // + 2 x 96 = 18 x 96; all have 96 again for the output
+  static constexpr int kThreads = 32 * (kSoft * G + kConv + G + 1);
+  // 19 warps are launched with 96 registers a thread: 8 softmax warps x 128 + 8 converting x 64
+  // + 3 x 96 = 19 x 96; all have 96 again for the output
   static constexpr bool kShift = G == 2 && kSets == 2;
 };
 
@@ -306,14 +306,14 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         mbar_init(&bars.sread[1][i], kSet);
         mbar_init(&bars.kfull[i], kSet);
         mbar_init(&bars.vfull[i], kSet);
-        mbar_init(&bars.kfree[i], 1);
+        mbar_init(&bars.kfree[i], G);
         for (int g = 0; g < G; ++g) {
           mbar_init(&bars.sfull[g][i], 1);
           mbar_init(&bars.pready[g][i], kSoft);
           mbar_init(&bars.pvdone[g][i], 1);
         }
       }
-      mbar_init(&bars.drain, 1);
+      mbar_init(&bars.drain, G);
       if (!started) bars.abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         s_blk[i] = e;
       }
       if constexpr (C::kStaged) {  // and the first tiles' copies
-        named_bar_sync(4, 64);
-        if (tid == 32 * (kSoft * G + kConv + 1))
+        named_bar_sync(4, 32 * (G + 1));
+        if (tid == 32 * (kSoft * G + kConv + G))
           for (; copied < min(nt, C::kSets * C::kSlots); ++copied) copy_tile(copied);
         __syncwarp();
       }
@@ -704,7 +704,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.kfull[b]);
-        if (i >= 2 && !wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)) break;  // P V of tile i - 2: its values' tile is free
+        // P V of tile i - 2: its values' tile is free
+        if (i >= 2 && !(wait(&bars.pvdone[0][b], (i - 2) >> 1) && (G == 1 || wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)))) break;
 #pragma unroll
         for (int g = 0; g < VG; ++g)
           if (w + 4 * g < D / 32) {
@@ -738,7 +739,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         named_bar_sync(3, 32 * (kSoft * G + kConv));
         reg_inc<96>();
       }
-    } else if (warp == kSoft * G + kConv + 1) {
+    } else if (warp == kSoft * G + kConv + G) {
       // ---------------- copies of the codes ----------------
       if constexpr (C::kStaged) {
         if (lane == 0) {
@@ -759,59 +760,47 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       }
     } else {
       // ---------------- products ----------------
+      // a warp per group: one for both spent longer on its waits than the tensor core on the products
+      const int g = warp - (kSoft * G + kConv);
       const uint32_t leader = elect_lane();
-      const uint32_t q_base = smem_u32(smem), k_base = smem_u32(kring), v_base = smem_u32(vring);
-      auto scores = [&](int g, int i) {  // S of tile i
+      const uint32_t q_base = smem_u32(smem) + g * C::kSub * C::kQTile, k_base = smem_u32(kring), v_base = smem_u32(vring);
+      const uint32_t s_col = tmem + uint32_t(2 * g * BN), o_col = tmem + C::kOCol + uint32_t(g * D);
+      auto scores = [&](int i) {  // S of tile i
         const int b = i & 1;
+        tc_fence_after();
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(leader, tmem + uint32_t((2 * g + b) * BN),
-                   desc_sw128(q_base + part * C::kQPart + (g * C::kSub + k / 4) * C::kQTile + (k % 4) * 32),
+            mma_ss(leader, s_col + uint32_t(b * BN), desc_sw128(q_base + part * C::kQPart + (k / 4) * C::kQTile + (k % 4) * 32),
                    desc_sw128(k_base + b * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
         mma_commit(leader, &bars.sfull[g][b]);
+        mma_commit(leader, &bars.kfree[b]);
       };
       bool ok = true;
       if (nt > 0) {
         ok = wait(&bars.kfull[0], 0);
-        if (ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int g = 0; g < G; ++g) scores(g, 0);
-          mma_commit(leader, &bars.kfree[0]);
-        }
+        if (ok) scores(0);
       }
       for (int i = 0; i < nt && ok; ++i) {
         const int b = i & 1;
         if (i + 1 < nt) {
           ok = wait(&bars.kfull[b ^ 1], (i + 1) >> 1);
           // the other S holds the probabilities of tile i - 1 until its products are done
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            if (ok && i >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (i - 1) >> 1);
-            if (ok) {
-              tc_fence_after();
-              scores(g, i + 1);
-            }
-          }
+          if (ok && i >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (i - 1) >> 1);
           if (!ok) break;
-          mma_commit(leader, &bars.kfree[b ^ 1]);
+          scores(i + 1);
         }
-        ok = wait(&bars.vfull[b], i >> 1);
+        ok = wait(&bars.vfull[b], i >> 1) && wait(&bars.pready[g][b], i >> 1);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          if (ok) ok = wait(&bars.pready[g][b], i >> 1);
-          if (!ok) break;
-          tc_fence_after();
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              mma_ts(leader, tmem + C::kOCol + uint32_t(g * D), tmem + uint32_t((2 * g + b) * BN + 16 * k + 8 * part),
-                     desc_sw128(v_base + b * C::kV + k * 32), idesc_f16(kTcRows, D), (i | part | k) != 0);
-          mma_commit(leader, &bars.pvdone[g][b]);
-        }
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(leader, o_col, s_col + uint32_t(b * BN + 16 * k + 8 * part), desc_sw128(v_base + b * C::kV + k * 32),
+                   idesc_f16(kTcRows, D), (i | part | k) != 0);
+        mma_commit(leader, &bars.pvdone[g][b]);
       }
       mma_commit(leader, &bars.drain);
     }
