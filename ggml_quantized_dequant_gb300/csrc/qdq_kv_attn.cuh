@@ -10,6 +10,7 @@ namespace qdq {
 
 constexpr float kLazy = 5.5f;    // accumulators are rescaled once a maximum has grown by 2^kLazy
 constexpr float kPScale = 1024.f;  // probabilities become f16 at this scale: at most 2^15.5 (f16: below 2^16)
+constexpr float kLog2PScale = 10.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinScale = 2.5243549e-29f;  // 2^-95: a smaller value scale counts as this in the reference
 
@@ -62,6 +63,7 @@ struct BlockAt {
   int64_t k;  // byte offset of its first key code
   float ks, vs;
   float lv;   // log2 of the value scale, at least -95 (a block of zeros has scale 0)
+  float inv;  // tensor-core kernel: 1 / vs, 0 where the scale is below 2^-95 or not finite
 };
 
 // Four dims of one row, times inv, in the output's type.

@@ -446,14 +446,15 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
 #pragma unroll 2
       for (int i = tid - 32 * (kSoft * G + kConv); i < 4 * nt; i += kThreads - 32 * (kSoft * G + kConv)) {
-        BlockAt e{-1, 0.f, 0.f, 0.f};
+        BlockAt e{-1, 0.f, 0.f, 0.f, 0.f};
         if (i < cn) {
           const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
           const int64_t at = kv_record_of(a.c, s, blk, h, rec);
           if (at >= 0) {
             const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
             const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
-            e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale))};
+            e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale)), 0.f};
+            if (vs >= kMinScale && vs < __int_as_float(0x7f800000)) e.inv = __frcp_rn(e.vs);
           } else {
             e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
           }
@@ -521,7 +522,6 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         auto probabilities = [&](auto plain) {
           constexpr bool kPlain = decltype(plain)::value;
           const float mref = m == ninf ? 0.f : m;
-          const float2 mm = f2(-mref, -mref);
           uint32_t r[2][16];
           tmem_ld16_async(sp, r[0]);
           sum = most = 0.f;
@@ -531,7 +531,11 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
             tmem_wait_ld16(x);
             if (c < 3) tmem_ld16_async(sp + 16 * (c + 1), r[(c + 1) & 1]);
             if constexpr (!kPlain) transform(c, x);
+            // plain: the value scale goes into the exponent, p * vs = 2^(s - reference + log2 vs), and out of the
+            // block's sum again (a product less per score; the exponent's rounding is within the scores')
             const float f = kPlain ? qs * blk[c].ks : 1.f, vs = blk[c].vs;
+            const float off = kPlain ? blk[c].lv + (kLog2PScale - mref) : -mref;
+            const float2 mm = f2(off, off);
             float2 l2, l3;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -542,8 +546,9 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
               else if (e == 1) l3 = p;
               else if (e & 1) l3 = __fadd2_rn(l3, p);
               else l2 = __fadd2_rn(l2, p);
-              float2 pv = __fmul2_rn(p, f2(vs, vs));
+              float2 pv = p;
               if constexpr (!kPlain) {  // a hidden token's scale may be NaN
+                pv = __fmul2_rn(p, f2(vs, vs));
                 if (y.x == ninf) pv.x = 0.f;
                 if (y.y == ninf) pv.y = 0.f;
               }
@@ -554,8 +559,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
               }
             }
             const float bs = (l2.x + l2.y) + (l3.x + l3.y);
-            sum += bs;
-            most = fmaxf(most, bs * vs);
+            sum = kPlain ? fmaf(bs, blk[c].inv, sum) : sum + bs;
+            most = fmaxf(most, kPlain ? bs : bs * vs);
           }
         };
         // the largest score plus log2 of its value scale
@@ -578,7 +583,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         // 2^15 (f16 ends at 2^16) with the reference there is, no maximum is looked for (64
         // comparisons less per row and tile).  Else, and for a row's first tile, the maximum moves
         // the reference and the probabilities are computed once more.
-        const bool plain = whole && !(a.softcap > 0.f) && !a.slopes;
+        const bool plain = whole && !(a.softcap > 0.f) && !a.slopes &&
+                           fminf(fminf(blk[0].inv, blk[1].inv), fminf(blk[2].inv, blk[3].inv)) > 0.f;
         bool again = __any_sync(0xffffffffu, m == ninf), ok = true;
         for (;;) {
           if (again) {  // the reference: see qdq_kv_attn.cu
