@@ -596,7 +596,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
     const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
     // whole waves of CTAs (one per SM), each with at most kTcSplitBlocks of the blocks there can be
-    const int64_t most = p.units * ((blocks + 4) / 4);  // tiles of 64 tokens
+    const int64_t most = p.units * ((blocks + 4) / 4 + kTcPartCost);  // tiles of 64 tokens and parts' costs
     const int64_t wave = int64_t(di.sm_count) * (kTcSplitBlocks / 4);
     const int64_t ctas = di.sm_count * ((most + wave - 1) / wave);
     p.splits = int(ctas < 0x7fffffff ? ctas : 0);

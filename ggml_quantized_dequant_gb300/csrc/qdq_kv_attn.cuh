@@ -66,11 +66,13 @@ struct BlockAt {
   float inv;  // tensor-core kernel: 1 / vs, 0 where the scale is below 2^-95 or not finite
 };
 
-// Four dims of one row, times inv, in the output's type.
+// Element of dim 0 of a row's output; four dims at element e, times inv, in the output's type.
 template <int D>
-__device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int row, int d, float4 v, float inv) {
+__device__ __forceinline__ int64_t out_at(const AttnArgs &a, int q0, int h, int row) {
   const int qi = int(a.query_of(row));
-  const int64_t e = int64_t(q0 + qi) * a.out_stride + int64_t(h * a.group + row - qi * a.group) * D + d;
+  return int64_t(q0 + qi) * a.out_stride + int64_t(h * a.group + row - qi * a.group) * D;
+}
+__device__ __forceinline__ void store_at(const AttnArgs &a, int64_t e, float4 v, float inv) {
   v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
   if (a.type == QDQ_TYPE_F32)
     store4(static_cast<float *>(a.out) + e, v);
@@ -78,6 +80,10 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int 
     store4(static_cast<__half *>(a.out) + e, v);
   else
     store4(static_cast<__nv_bfloat16 *>(a.out) + e, v);
+}
+template <int D>
+__device__ __forceinline__ void store_out(const AttnArgs &a, int q0, int h, int row, int d, float4 v, float inv) {
+  store_at(a, out_at<D>(a, q0, h, row) + d, v, inv);
 }
 // M: the reference (log2 units), L: the sum of 2^(score - M)
 __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int row, float M, float L) {
@@ -90,6 +96,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int 
 // The tensor-core kernel (qdq_kv_attn_tc.cu): one or two groups of 128 rows to a tile, head dims that are whole 64s
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
+constexpr int kTcPartCost = 9;      // what a part costs besides its tiles of 64 tokens, in tiles (11 us and 1.2 us)
 constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one part, at most
 inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
 // Bytes of one part's result (two per CTA).

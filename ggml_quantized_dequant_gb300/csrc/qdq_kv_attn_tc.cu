@@ -34,7 +34,8 @@ __device__ unsigned int g_attn_tc_timeouts = 0;
 namespace {
 
 constexpr int BN = 64;  // tokens per tile
-constexpr int kMinShare = 8;  // tiles: a part costs about as much as 8 tiles besides them
+constexpr int kMinShare = 8;  // places on the line: a shorter share saves less than its part costs
+constexpr int kJoinSlots = 3;  // for joining parts
 constexpr int kSoft = 4, kSet = 4;  // softmax warps per group of rows, warps per converting set
 
 // ---- tcgen05 --------------------------------------------------------------------
@@ -148,6 +149,10 @@ struct Cfg {
   static_assert(kSmem <= 225 * 1024, "shared memory");
   static constexpr int kConv = kSet * kSets;
   static constexpr int kThreads = 32 * (kSoft * G + kConv + G + 1);
+  // joining parts: columns of 4 dims in a slot, warps that add
+  static constexpr uint32_t join_bytes(int quads) { return 1024 + 2 * kTcRows * G * 4 + kJoinSlots * kTcRows * G * (quads * 16 + 4); }
+  static constexpr int kJoinQuads = join_bytes(16) <= kSmem ? 16 : 8, kJoinWarps = kThreads >= 512 ? 16 : 8;
+  static_assert(join_bytes(kJoinQuads) <= kSmem, "room for the join");
   // 19 warps are launched with 96 registers a thread: 8 softmax warps x 128 + 8 converting x 64
   // + 3 x 96 = 19 x 96; all have 96 again for the output
   static constexpr bool kShift = G == 2 && kSets == 2;
@@ -155,8 +160,8 @@ struct Cfg {
 
 template <int G>
 struct Bars {
-  uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain;
-  static constexpr int kBars = 8 + 6 + 6 * G + 1;
+  uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain, joined[kJoinSlots];
+  static constexpr int kBars = 8 + 6 + 6 * G + 1 + kJoinSlots;
   long long sums[20], first, g0, g1, total;  // the share's state, kept here while a part runs (registers are short)
   uint32_t tmem;
   int abort, last, entry, shares;
@@ -202,13 +207,16 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     x.tiles = max(1, (x.b_hi - x.b_lo + 3) / 4);
     return x;
   };
+  // An entry's unit on the line of all work: a part's cost in tiles, then its tiles, so that a share's end
+  // in a unit's first kTcPartCost leaves the unit to the next CTA.
+  auto line_of = [](const Entry &x) { return x.tiles ? x.tiles + kTcPartCost : 0; };
   const int n_entries = a.n_seqs * a.tiles, chunk = (n_entries + kThreads - 1) / kThreads;
-  long long total = 0, g0, g1;  // tiles of all units; this CTA's share of them
+  long long total = 0, g0, g1;  // the line's length; this CTA's share of it
   int shares;                   // CTAs that have a share
-  {  // bars.entry, bars.first: the entry of tile g0 and its first tile
+  {  // bars.entry, bars.first: the entry at g0 and its place
     long long mine = 0;
     for (int i = 0; i < chunk; ++i)
-      if (tid * chunk + i < n_entries) mine += entry(tid * chunk + i).tiles;
+      if (tid * chunk + i < n_entries) mine += line_of(entry(tid * chunk + i));
     long long up = mine;  // inclusive sums over the threads
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -233,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     if (before <= g0 && g0 < before + mine) {  // one thread has the entry of g0
       int e = tid * chunk;
       for (;; ++e) {
-        const long long n = (long long)entry(e).tiles * a.c.n_kv;
+        const long long n = (long long)line_of(entry(e)) * a.c.n_kv;
         if (g0 < before + n) break;
         before += n;
       }
@@ -260,20 +268,20 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   for (;;) {  // part by part
     __syncthreads();  // the state is written; the part before is done with shared memory
     struct Unit {
-      long long first;  // its first tile
+      long long first;  // its place on the line
       int h, t0, t1, c_lo, nsplit;  // head, tiles of this part, first CTA with a part of it, parts
     };
     auto unit_of = [&](const Entry &en) {
       const long long at = kept(bars.g0), e0 = kept(bars.first), all = kept(bars.total);
       const int n = *reinterpret_cast<volatile int *>(&bars.shares);
-      auto owner = [&](long long g) { return int(((g + 1) * n - 1) / all); };  // the CTA whose share has tile g
+      auto owner = [&](long long g) { return int(((g + 1) * n - 1) / all); };  // the CTA whose share has place g
       Unit u;
-      u.h = int((at - e0) / en.tiles);
-      u.first = e0 + (long long)u.h * en.tiles;
-      u.t0 = int(at - u.first);
-      u.t1 = int(min((long long)en.tiles, kept(bars.g1) - u.first));
-      u.c_lo = owner(u.first);
-      u.nsplit = owner(u.first + en.tiles - 1) - u.c_lo + 1;
+      u.h = int((at - e0) / line_of(en));
+      u.first = e0 + (long long)u.h * line_of(en);
+      u.t0 = int(max(0ll, at - u.first - kTcPartCost));
+      u.t1 = int(min((long long)en.tiles, kept(bars.g1) - u.first - kTcPartCost));
+      u.c_lo = owner(u.first + kTcPartCost);
+      u.nsplit = owner(u.first + kTcPartCost + en.tiles - 1) - u.c_lo + 1;
       return u;
     };
     int s, q0, len, nq, r0, nr, pos_lo, pos_hi, c0, cn, h;
@@ -281,6 +289,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     {
       const Entry en = entry(*reinterpret_cast<volatile int *>(&bars.entry));
       const Unit u = unit_of(en);
+      if (u.t1 <= u.t0) break;  // a share that ends before its first unit's tiles
       s = en.s;
       q0 = en.q0;
       len = en.len;
@@ -314,6 +323,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         }
       }
       mbar_init(&bars.drain, G);
+      for (int i = 0; i < kJoinSlots; ++i) mbar_init(&bars.joined[i], 1);
       if (!started) bars.abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -833,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     const Unit u = unit_of(en);
     const int nsplit = u.nsplit;
     // a CTA keeps up to two parts of cut units: the first of its share, and another, which starts its unit
-    const bool another = u.first != kept(bars.total) * u.c_lo / *reinterpret_cast<volatile int *>(&bars.shares);
+    const bool another = u.first > kept(bars.total) * u.c_lo / *reinterpret_cast<volatile int *>(&bars.shares);
     auto part_of = [&](int k) { return a.partial + (2 * int64_t(u.c_lo + k) + (k == 0 && another)) * kPart; };  // k-th part
     float *part = part_of(int(blockIdx.x) - u.c_lo);  // [four dims][row][4], maxima, sums
     if (warp < kSoft * G) {
@@ -874,70 +884,105 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     }
     tc_fence_before();
     if (nsplit > 1) {
-      // the CTA that finishes last joins the parts, in order: four dims of a row per thread and
-      // step, a warp 16 dims of 8 rows (whole sectors of the parts and of the output)
+      // The CTA that finishes last joins the parts, in order.  Their accumulators (32 or 64 dims of all rows
+      // at a time) and references come through a ring of bulk copies in the space of the tiles; a warp takes
+      // 16 dims of 8 rows at a time, whole sectors of the output.  (Plain loads, 4 of 16 bytes in flight per thread,
+      // took 10 us for two or three parts of 256 rows of 128.)
+      asm volatile("fence.proxy.async;" ::: "memory");
       __threadfence();
       __syncthreads();
       if (tid == 0) bars.last = atomicInc(a.tickets + int64_t(e_cur) * a.c.n_kv + h, nsplit - 1) == uint32_t(nsplit - 1);
       __syncthreads();
       if (bars.last) {
         __threadfence();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        constexpr int kJoinQuads = C::kJoinQuads, kJoinWarps = C::kJoinWarps;
+        constexpr uint32_t kBytes = kJoinQuads * R * 16, kSlot = kBytes + R * 4;
+        constexpr int kRows = R / (8 * kJoinWarps), kQuads = kJoinQuads / 4;  // rows and 4-dim columns per thread
         float *s_ref = reinterpret_cast<float *>(smem), *s_inv = s_ref + R;
+        uint8_t *slots = smem + 2 * R * 4;
+        const int items = D / (4 * kJoinQuads) * nsplit;  // 32 dims of one part each
+        auto bring = [&](int j) {
+          const float *p = part_of(j % nsplit);
+          uint8_t *dst = slots + j % kJoinSlots * kSlot;
+          uint64_t *bar = &bars.joined[j % kJoinSlots];
+          mbar_arrive_expect_tx(bar, kSlot);
+          bulk_copy_g2s(dst, p + int64_t(j / nsplit) * (kJoinQuads * R * 4), kBytes, bar);
+          bulk_copy_g2s(dst + kBytes, p + D * R, R * 4, bar);
+        };
+        if (tid == 0)
+          for (int j = 0; j < min(items, kJoinSlots); ++j) bring(j);
+        __syncwarp();
         for (int r = tid; r < nr; r += kThreads) {
           float M = ninf, L = 0.f;
 #pragma unroll 4
-          for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(part_of(k) + D * R + r));
-          const float ref = M == ninf ? 0.f : M;
-#pragma unroll 4
-          for (int k = 0; k < nsplit; ++k)
-            L = fmaf(__ldcg(part_of(k) + (D + 1) * R + r), ex2(__ldcg(part_of(k) + D * R + r) - ref), L);
-          s_ref[r] = ref;
+          for (int k = 0; k < nsplit; ++k) {
+            const float mk = __ldcg(part_of(k) + D * R + r), lk = __ldcg(part_of(k) + (D + 1) * R + r);
+            const float top = fmaxf(M, mk), ref = top == ninf ? 0.f : top;
+            L = fmaf(lk, ex2(mk - ref), L * ex2(M - ref));
+            M = top;
+          }
+          s_ref[r] = M == ninf ? 0.f : M;
           s_inv[r] = L == 0.f ? 0.f : (1.f / kPScale) / L;
           store_lse(a, q0, h, r0 + r, M, L);
         }
         __syncthreads();
-        constexpr int kAhead = 4, kItems = R * D / 4;
-        auto at = [&](int i, int &r, int &d4) {
-          const int block = i / 32, in = i % 32;
-          r = block % (R / 8) * 8 + in % 8;
-          d4 = block / (R / 8) * 4 + in / 8;
-        };
-        for (int i0 = tid; i0 < kItems; i0 += kThreads * kAhead) {
-          float4 v[kAhead];
+        const int r1 = 8 * warp + (lane & 7), quad = lane >> 3;  // the thread's first row and column
+        float4 v[kRows][kQuads];
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-          for (int k = 0; k < nsplit; ++k) {
-            const float *p = part_of(k);
-            float4 x[kAhead];
-            float f[kAhead];
+        for (int i = 0; i < kRows; ++i)
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-              int r, d4;
-              at(min(i0 + j * kThreads, kItems - 1), r, d4);
-              x[j] = __ldcg(reinterpret_cast<const float4 *>(p) + d4 * R + r);
-              f[j] = __ldcg(p + D * R + r);
-            }
+          for (int c = 0; c < kQuads; ++c) v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int64_t to[kRows];
+        float ref[kRows], inv[kRows];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-              int r, d4;
-              at(min(i0 + j * kThreads, kItems - 1), r, d4);
-              const float w = ex2(f[j] - s_ref[r]);
-              v[j] = make_float4(fmaf(x[j].x, w, v[j].x), fmaf(x[j].y, w, v[j].y), fmaf(x[j].z, w, v[j].z), fmaf(x[j].w, w, v[j].w));
+        for (int i = 0; i < kRows; ++i) {
+          const int r = min(r1 + 8 * kJoinWarps * i, R - 1);
+          to[i] = out_at<D>(a, q0, h, r0 + r) + 4 * quad;
+          ref[i] = s_ref[r];
+          inv[i] = s_inv[r];
+        }
+        int k = 0;
+        for (int j = 0; j < items; ++j) {
+          const bool there = mbar_wait(&bars.joined[j % kJoinSlots], uint32_t(j / kJoinSlots) & 1u);
+          if (!there) give_up();
+          if (warp < kJoinWarps) {
+            const uint8_t *slot = slots + j % kJoinSlots * kSlot;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+              const int r = r1 + 8 * kJoinWarps * i;
+              const float w = there ? ex2(reinterpret_cast<const float *>(slot + kBytes)[r] - ref[i]) : qnan;
+#pragma unroll
+              for (int c = 0; c < kQuads; ++c) {
+                const float4 x = reinterpret_cast<const float4 *>(slot)[(quad + 4 * c) * R + r];
+                float4 &o = v[i][c];
+                o = make_float4(fmaf(x.x, w, o.x), fmaf(x.y, w, o.y), fmaf(x.z, w, o.z), fmaf(x.w, w, o.w));
+              }
             }
           }
+          __syncthreads();  // the slot has been read
+          if (tid == 0 && j + kJoinSlots < items) bring(j + kJoinSlots);
+          if (++k == nsplit) {
+            if (warp < kJoinWarps) {
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j * kThreads;
-            int r, d4;
-            at(i, r, d4);
-            if (i < kItems && r < nr) store_out<D>(a, q0, h, r0 + r, 4 * d4, v[j], s_inv[r]);
+              for (int i = 0; i < kRows; ++i) {
+                const int r = r1 + 8 * kJoinWarps * i;
+#pragma unroll
+                for (int c = 0; c < kQuads; ++c) {
+                  if (r < nr) store_at(a, to[i] + 16 * c, v[i][c], inv[i]);
+                  v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                to[i] += 4 * kJoinQuads;
+              }
+            }
+            k = 0;
           }
         }
       }
     }
-    const long long next = u.first + u.t1, end = kept(bars.first) + (long long)en.tiles * a.c.n_kv;
-    const bool more = next < kept(bars.g1);
+    // the next unit, where the share has tiles of it
+    const long long next = u.first + line_of(en), end = kept(bars.first) + (long long)line_of(en) * a.c.n_kv;
+    const bool more = next + kTcPartCost < kept(bars.g1);
     __syncthreads();  // every thread has read the state
     if (!more) break;
     if (tid == 0) {
