@@ -96,7 +96,9 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int 
 // The tensor-core kernel (qdq_kv_attn_tc.cu): one or two groups of 128 rows to a tile, head dims that are whole 64s
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
-constexpr int kTcPartCost = 9;      // what a part costs besides its tiles of 64 tokens, in tiles (11 us and 1.2 us)
+// What a unit costs besides its tiles of 64 tokens, in tiles: a part costs 11 us, a tile 1.2 us, a join 8 us.  (4
+// sequences of 300 queries over 300 to 2500 tokens, 32 / 8 heads of 128, f16: 9 75.2 us, 12 70.4, 15 70.2, 18 70.6.)
+constexpr int kTcPartCost = 15;
 constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one part, at most
 inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
 // Bytes of one part's result (two per CTA).
