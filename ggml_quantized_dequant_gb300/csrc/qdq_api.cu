@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "qdq_internal.cuh"
+#include "qdq_types.cuh"
 
 namespace qdq {
 
@@ -214,6 +215,9 @@ int qdq_set_option(int key, int value) {
     case QDQ_OPT_BATCH1_KERNEL:
       if (value != 0 && value != 1) return QDQ_ERR_DIMS;
       return g_opt_batch1_kernel.exchange(value);
+    case QDQ_OPT_ATTN_KERNEL:
+      if (value < 0 || value > 2) return QDQ_ERR_DIMS;
+      return qdq::g_opt_attn_kernel.exchange(value);
     default: return QDQ_ERR_DIMS;
   }
 }

@@ -16,12 +16,19 @@
 //   one part (16-bit activations with more than 8 rows per head; a tile is 16 rows): the queries
 //     are exact in f16 but for elements 2^-25 below the row's largest, the
 //     probabilities are rounded to f16 (2^-11 relative, as the output is).
-// The running maximum, the sum and the accumulators are f32.  The four warps of a CTA take every
-// fourth block of their split of the tokens and are joined through shared memory; splits of one
-// tile are joined by the CTA that finishes last, in split order.
+// The running maximum, the sum and the accumulators are f32.  The warps of a CTA (4, or 16 or 8
+// where there are few tiles) take blocks of their split of the tokens in turn and are joined through
+// shared memory; splits of one tile are joined by the CTA that finishes last, in split order.
+// Bound: memory for many or long sequences (a code is read once for all rows of its head); for a short one the
+// chain of a launch, length, page, codes, joins.  Measured (8 heads of 128 in the cache): one sequence of
+// 777 tokens, 24 heads f32 9.0 us; 48 of 1 to 8191 78.5 us (5.2 TB/s, 76 % of a plain copy's rate); one of 131071
+// tokens, 32 heads bf16 50.6 us (5.3 TB/s, 78 %).
 #include "qdq_kv_attn.cuh"
 
 namespace qdq {
+
+std::atomic<int> g_opt_attn_kernel{0};
+
 namespace {
 
 constexpr int kStages = 3;       // blocks in a warp's ring
@@ -572,7 +579,12 @@ int with_dim(int d, F &&f) {
   }
 }
 
-constexpr int kTcMinRows = 64;    // query rows per key/value head from which on the tensor-core kernel runs
+// Query rows per key/value head from which on the tensor-core kernel runs, and the longest context of a CTA
+// up to which this file's kernel is kept all the same where its tiles do not outnumber the SMs (each is then an
+// SM's, split over idle ones).  One sequence of 4000 tokens, 24 / 8 heads of 128, us here and there: 64 queries
+// bf16 28 42, 128 84 45; 43 queries f32 25 46, 64 57 47; 30 queries f32 over 16000 tokens 90 57.  8
+// sequences of up to 6000: 8 queries bf16 39 52, 16 71 52, 64 146 67.  48 of up to 3000: 16 queries bf16 123 157, 22 176 158.
+constexpr int kTcMinRows = 64, kTcMinTokens = 6000;
 
 struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
@@ -585,8 +597,12 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
           int type) {
   Plan p{};
   const int64_t rows = int64_t(max_q) * (n_heads / n_kv);
-  p.parts = type == QDQ_TYPE_F32 ? 2 : 1;
-  p.tc = rows > kTcMinRows && attn_tc_supported(head_dim, p.parts);
+  p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
+  const int64_t small = int64_t(n_seqs) * n_kv * ((rows * p.parts + 15) / 16);  // tiles of the other kernel
+  const bool few = small <= di.sm_count && max_kv_len / (di.sm_count / small) <= kTcMinTokens;
+  const int forced = g_opt_attn_kernel.load(std::memory_order_relaxed);
+  p.tc = (forced == 2 || (forced == 0 && rows > kTcMinRows && !few)) && (type == QDQ_TYPE_F32 || p.parts == 1) &&
+         attn_tc_supported(head_dim, p.parts);
   if (p.tc) {
     p.groups = rows > kTcRows && head_dim <= 128 ? 2 : 1;
     const int R = kTcRows * p.groups;
@@ -603,10 +619,9 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     p.bytes = workspace_for(size_t(p.units), 2 * size_t(ctas) * attn_tc_part_bytes(head_dim, p.groups));
     return p;
   }
-  p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
   const int R = 16 / p.parts;
   p.tiles = int((rows + R - 1) / R);
-  p.units = int64_t(n_seqs) * n_kv * p.tiles;
+  p.units = small;
   // blocks a tile can see: its rows span at most R queries
   int64_t tokens = max_kv_len;
   if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;

@@ -3,6 +3,8 @@
 // int8 cache's page geometry, and the operators' launchers.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "qdq_internal.cuh"
@@ -126,6 +128,7 @@ inline size_t workspace_for(size_t tickets, size_t part_bytes) {  // its bytes f
   const size_t t = (tickets * 4 + 255) / 256 * 2048, p = (part_bytes + 6) / 7 * 8;
   return ((t > p ? t : p) + 2047) / 2048 * 2048;
 }
+extern std::atomic<int> g_opt_attn_kernel;  // QDQ_OPT_ATTN_KERNEL
 size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
 int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, int n_seqs, int max_q,
                         int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,

@@ -463,6 +463,10 @@ int qdq_noop(cudaStream_t stream);
  * kernel's CTA can start streaming beside it).  Same results within the stated bound; the
  * fixed-point arithmetic always runs in the ring kernel. */
 #define QDQ_OPT_BATCH1_KERNEL 7
+/* Kernel of qdq_kv_attention: 0 (default) automatic (by rows per cache head and work); 1 the decode kernel; 2 the
+ * tensor-core kernel wherever it can run (head dims 64, 128, 192, or 256 with 16-bit types; more than 8 rows per
+ * cache head for 16-bit types).  Results within the same bound.  Set it before the workspace is sized. */
+#define QDQ_OPT_ATTN_KERNEL 8
 /* Sets a process-wide option; returns the previous value, or QDQ_ERR_DIMS for a bad key/value. */
 int qdq_set_option(int key, int value);
 

@@ -177,3 +177,10 @@ def test_binding_refuses_wrong_tensors(qdq):
         qdq.kv_append(pages, table, torch.zeros(1, dtype=torch.int32), x, x, 1, 64, 16)
     with pytest.raises(ValueError):
         qdq.kv_append(pages[:, 1:], table.int(), torch.zeros(1, dtype=torch.int32), x, x, 1, 64, 16)
+
+
+def test_attention_kernel_option(qdq):
+    assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 2) == 0
+    assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 3) == qdq.QDQ_ERR_DIMS
+    assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, -1) == qdq.QDQ_ERR_DIMS
+    assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 0) == 2

@@ -289,6 +289,15 @@ def test_tokens_without_a_page(cuda_lib):
 
 # ------------------------------------------------------------------ attention
 
+@pytest.fixture(params=["automatic", "decode", "tensor"])
+def attn_kernel(request, cuda_lib):
+    """The attention tests run with the automatic choice of the kernel and with either one wherever it can run."""
+    old = cuda_lib.set_option(cuda_lib.QDQ_OPT_ATTN_KERNEL, ["automatic", "decode", "tensor"].index(request.param))
+    yield
+    cuda_lib.set_option(cuda_lib.QDQ_OPT_ATTN_KERNEL, old)
+    assert cuda_lib.pipeline_timeouts() == 0
+
+
 def _filled(rng, lens, page, n_kv, dim, n_pages=None, amp=1.0):
     """A pool whose sequences hold random tokens (garbage elsewhere), its table and the oracle's view of it."""
     n_pages = n_pages or sum(-(-max(n, 0) // page) for n in lens) + 3
@@ -379,6 +388,7 @@ ATTN = [
 ]
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("lens,nq,heads,n_kv,dim,page,dtype,softcap,window,bias", ATTN)
 def test_attention(cuda_lib, lens, nq, heads, n_kv, dim, page, dtype, softcap, window, bias):
     rng = np.random.default_rng(sum(lens) + heads + dim)
@@ -389,6 +399,7 @@ def test_attention(cuda_lib, lens, nq, heads, n_kv, dim, page, dtype, softcap, w
     _check_attention(c, table, lens, nq, q, out, lse, dtype, dim ** -0.5, softcap, window, slopes)
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("dtype,nq", [("f32", 1), ("bf16", 1), ("f32", 150), ("bf16", 150)])
 def test_attention_sharp_scores_and_uneven_scales(cuda_lib, dtype, nq):
     # large queries, scales over many orders of magnitude, blocks of zeros (scale 0)
@@ -406,6 +417,7 @@ def test_attention_sharp_scores_and_uneven_scales(cuda_lib, dtype, nq):
     _check_attention(c, table, [n], [nq], q, out, lse, dtype, dim ** -0.5, 0, 0, None)
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("nq", [1, 140])
 def test_attention_rows_that_see_nothing(cuda_lib, nq):
     # more queries than tokens: the first rows stand before the sequence
@@ -418,6 +430,7 @@ def test_attention_rows_that_see_nothing(cuda_lib, nq):
     assert (_np(out)[:nq] == 0).all() and np.isneginf(_np(lse)[:nq]).all()
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("nq", [4, 100])
 def test_attention_nan_stays_in_its_rows(cuda_lib, nq):
     # a NaN block is seen by the rows at or after it (and by none past the window); a NaN or infinite
@@ -441,6 +454,7 @@ def test_attention_nan_stays_in_its_rows(cuda_lib, nq):
     assert np.array_equal(np.isnan(_np(lse)), bad)
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("nq", [1, 70])
 def test_attention_lengths_and_pages_out_of_range(cuda_lib, nq):
     # lengths outside [0, max_kv_len], past the table, a page outside the pool: NaN for that sequence alone
@@ -456,6 +470,7 @@ def test_attention_lengths_and_pages_out_of_range(cuda_lib, nq):
     assert np.isfinite(o[0]).all() and np.isnan(o[1:]).all() and np.isnan(_np(lse).reshape(6, -1)[1:]).all()
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("nq,lens", [(1, [5000, 17, 3000]), (3, [900, 1, 5000]), (129, [600, 300, 129])])
 def test_attention_repeats_bit_for_bit_on_one_workspace(cuda_lib, nq, lens):
     import torch
@@ -475,6 +490,7 @@ def test_attention_repeats_bit_for_bit_on_one_workspace(cuda_lib, nq, lens):
             assert torch.equal(a, b)
 
 
+@pytest.mark.usefixtures("attn_kernel")
 def test_calls_of_other_shapes_share_a_workspace(cuda_lib):
     # whatever one call keeps in the workspace must not count as another's tickets
     import torch
@@ -508,6 +524,7 @@ def test_calls_of_other_shapes_share_a_workspace(cuda_lib):
             assert np.array_equal(a, b, equal_nan=True), i
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("n_seqs,nq,heads,n_kv,dim,max_kv", [
     (1, 1, 8, 8, 128, 161), (1, 1, 4, 2, 64, 40000), (24, 1, 8, 8, 64, 9000), (40, 3, 16, 8, 128, 700), (2, 40, 4, 2, 128, 3000),
     (2, 65, 2, 2, 64, 5000), (1, 300, 2, 1, 128, 2000)])
@@ -530,6 +547,7 @@ def test_attention_workspace_is_enough_for_any_window(cuda_lib, n_seqs, nq, head
             assert (out == 0).all() and (buf[size:] == 0x5A).all(), window
 
 
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_attention_many_ragged_prompts(cuda_lib, dtype):
     # prompts whose tiles are dealt out in shares that cut them: empty sequences, single queries, some longer than
@@ -544,6 +562,7 @@ def test_attention_many_ragged_prompts(cuda_lib, dtype):
         _check_attention(c, table, lens, nq, q, out, lse, dtype, 0.125, 0, window, None)
 
 
+@pytest.mark.usefixtures("attn_kernel")
 def test_attention_strided_rows(cuda_lib):
     # q and out inside wider buffers; other elements stay
     import torch
@@ -561,6 +580,7 @@ def test_attention_strided_rows(cuda_lib):
     _check_attention(c, table, [130, 70], [1, 1], q.contiguous(), plain, lse, "f32", 0.125, 0, 0, None)
 
 
+@pytest.mark.usefixtures("attn_kernel")
 def test_cache_offsets_past_32_bits(cuda_lib):
     # pages beyond 4 GB: append, read and attention reach the same tokens
     import torch
