@@ -181,6 +181,6 @@ def test_binding_refuses_wrong_tensors(qdq):
 
 def test_attention_kernel_option(qdq):
     assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 2) == 0
-    assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 3) == qdq.QDQ_ERR_DIMS
-    assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, -1) == qdq.QDQ_ERR_DIMS
+    assert qdq.lib().qdq_set_option(qdq.QDQ_OPT_ATTN_KERNEL, 3) == qdq.QDQ_ERR_DIMS
+    assert qdq.lib().qdq_set_option(qdq.QDQ_OPT_ATTN_KERNEL, -1) == qdq.QDQ_ERR_DIMS
     assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 0) == 2
