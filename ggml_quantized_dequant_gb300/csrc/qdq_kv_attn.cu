@@ -23,6 +23,8 @@
 // chain of a launch, length, page, codes, joins.  Measured (8 heads of 128 in the cache): one sequence of
 // 777 tokens, 24 heads f32 9.0 us; 48 of 1 to 8191 78.5 us (5.2 TB/s, 76 % of a plain copy's rate); one of 131071
 // tokens, 32 heads bf16 50.6 us (5.3 TB/s, 78 %).
+#include <algorithm>
+
 #include "qdq_kv_attn.cuh"
 
 namespace qdq {
@@ -32,6 +34,13 @@ std::atomic<int> g_opt_attn_kernel{0};
 namespace {
 
 constexpr int kStages = 3;       // blocks in a warp's ring
+constexpr int kMaxEntries = 128;  // sequences times tiles up to which the splits' length is chosen on the device
+// Blocks of 16 tokens in a split from which on its length is chosen on the device: the choice costs 1.6 us (8
+// sequences of 8000 tokens bf16, heads of 64: 20.6 -> 22.2 us), but sequences of different lengths share the SMs evenly (4
+// of 2000 to 20000 f32: 33.9 -> 24.0 us; 8 of 100 to 8000: 29.4 -> 23.6 us).  Small CTAs even out by themselves
+// (48 of 1 to 8191: 79 us, with the choice 94 us).
+constexpr int kEvenBlocks = 192;
+constexpr int kMinBlocks = 4;     // of a split, per warp: a split costs its join (about 3 us)
 // Splits of one tile (the joining CTA keeps their maxima and sums in shared memory), and blocks
 // of 16 tokens in one split.
 constexpr int max_splits(int warps) { return warps > 4 ? 512 : 64; }
@@ -115,8 +124,9 @@ constexpr int body_bytes() {
 // in different banks (unexchanged, a one-token call took 1.5 us longer).
 __device__ __forceinline__ int quad_at(int row, int c) { return c ^ (((c >> 3) & 3) | ((row & 1) << 2)); }
 
-// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.  W warps.
-template <int D, int PARTS, int W>
+// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.  W warps.  EVEN: the splits' length follows the
+// sequences' lengths, else a.split_blocks.
+template <int D, int PARTS, int W, bool EVEN>
 __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kernel(const AttnArgs a) {
   constexpr int kThreads = W * 32;
   using S = Shape<D>;
@@ -133,26 +143,112 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
   const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x % a.splits;
-  const int unit = blockIdx.x / a.splits;  // (sequence, kv head, tile)
-  const int tile = unit % a.tiles, h = unit / a.tiles % a.c.n_kv, s = unit / a.tiles / a.c.n_kv;
   pdl_launch_dependents();
   pdl_wait();
 
-  const int q0 = a.cu_q ? int(ld_u1(a.cu_q + s)) : s;
-  const int nq = a.cu_q ? int(ld_u1(a.cu_q + s + 1)) - q0 : 1;
-  const int len = int(ld_u1(a.kv_len + s));
-  const int rows = nq * a.group, r0 = tile * R;
-  if (r0 >= rows) return;
-  const int nr = min(R, rows - r0);
-  const bool bad = len < 0 || len > a.max_kv_len || (len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
-  const int pos_lo = len - nq + r0 / a.group, pos_hi = len - nq + (r0 + nr - 1) / a.group;
-  const int b_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) / kKvBlock : 0;
-  const int b_hi = bad ? 0 : (pos_hi + kKvBlock) / kKvBlock;  // pos_hi >= -nq: 0 or negative when nothing is visible
-  const int nb = max(0, b_hi - b_lo);
-  const int nsplit = max(1, (nb + a.split_blocks - 1) / a.split_blocks);
-  if (split >= nsplit) return;
-  const int c0 = b_lo + split * a.split_blocks, cn = min(a.split_blocks, b_hi - c0);
+  // rows and blocks of one tile of a sequence
+  struct Tile {
+    int q0, nq, len, nr, b_lo, nb;
+    bool bad;
+  };
+  auto tile_of = [&](int s, int tile) {
+    Tile x;
+    x.q0 = a.cu_q ? int(ld_u1(a.cu_q + s)) : s;
+    x.nq = a.cu_q ? int(ld_u1(a.cu_q + s + 1)) - x.q0 : 1;
+    x.len = int(ld_u1(a.kv_len + s));
+    const int r0 = tile * R, rows = x.nq * a.group;
+    x.nr = min(R, rows - r0);
+    x.bad = x.len < 0 || x.len > a.max_kv_len || (x.len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
+    const int pos_lo = x.len - x.nq + int(a.query_of(r0)), pos_hi = x.len - x.nq + int(a.query_of(r0 + max(x.nr, 1) - 1));
+    x.b_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) / kKvBlock : 0;
+    // pos_hi >= -nq: 0 or negative when nothing is visible
+    x.nb = x.bad ? 0 : max(0, (pos_hi + kKvBlock) / kKvBlock - x.b_lo);
+    return x;
+  };
+  int s, h, tile, split, nsplit, per;  // this CTA's: blocks of a split
+  int64_t first;                       // its unit's first part
+  Tile me;
+  if constexpr (!EVEN) {
+    split = blockIdx.x % a.splits;
+    const int u = blockIdx.x / a.splits;  // (sequence, kv head, tile)
+    tile = u % a.tiles;
+    h = u / a.tiles % a.c.n_kv;
+    s = u / a.tiles / a.c.n_kv;
+    me = tile_of(s, tile);
+    per = a.split_blocks;
+    nsplit = max(1, (me.nb + per - 1) / per);
+    if (me.nr <= 0 || split >= nsplit) return;
+    first = int64_t(u) * a.splits;
+  } else {
+    // Every warp by itself: the shortest splits of which there are no more than CTAs (their length grows by the
+    // excess until that holds), then the entry (sequence, tile) of this CTA, and its head and split.
+    constexpr int kPer = kMaxEntries / 32;
+    int blocks[kPer];  // of entry 32 j + lane; -1: no rows
+    int total = 0, most = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = 32 * j + lane;
+      blocks[j] = -1;
+      if (e < a.entries) {
+        const Tile x = tile_of(e / a.tiles, e % a.tiles);
+        if (x.nr > 0) blocks[j] = x.nb;
+        total += max(blocks[j], 0);
+        most = max(most, blocks[j]);
+      }
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const int ctas = gridDim.x / a.c.n_kv;  // for one head
+    per = max(max(kMinBlocks * W, (most + max_splits(W) - 1) / max_splits(W)), (total + ctas - 1) / ctas);
+    int n[kPer];
+    for (;;) {
+      per = min(per, max_split_blocks(W));
+      int sum = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        n[j] = blocks[j] < 0 ? 0 : max(1, (blocks[j] + per - 1) / per);
+        sum += n[j];
+      }
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (sum <= ctas || per == max_split_blocks(W)) break;
+      per += (per * (sum - ctas) + ctas - 1) / ctas;
+    }
+    int off = 0, found = -1, cnt = 0, at = 0;  // off: parts (of all heads) before entry 32 j
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (32 * j >= a.entries) break;
+      const int mine = n[j] * a.c.n_kv;
+      int up = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += x;
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, int(blockIdx.x) >= off + up - mine && int(blockIdx.x) < off + up);
+      if (who) {
+        const int l = __ffs(who) - 1;
+        found = 32 * j + l;
+        cnt = __shfl_sync(0xffffffffu, n[j], l);
+        at = off + __shfl_sync(0xffffffffu, up - mine, l);
+        break;
+      }
+      off += __shfl_sync(0xffffffffu, up, 31);
+    }
+    if (found < 0) return;  // more CTAs than parts
+    s = found / a.tiles;
+    tile = found % a.tiles;
+    nsplit = cnt;
+    h = (int(blockIdx.x) - at) / cnt;
+    split = (int(blockIdx.x) - at) % cnt;
+    first = at + int64_t(h) * cnt;
+    me = tile_of(s, tile);
+    per = max(1, (me.nb + cnt - 1) / cnt);  // the unit's splits alike
+  }
+  const int unit = (s * a.c.n_kv + h) * a.tiles + tile;
+  const int q0 = me.q0, nq = me.nq, len = me.len, nr = me.nr, r0 = tile * R;
+  const bool bad = me.bad;
+  const int b_lo = me.b_lo, b_hi = me.b_lo + me.nb;
+  const int c0 = b_lo + split * per, cn = max(0, min(per, b_hi - c0));
 
   // where the blocks of this split are
   const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
@@ -277,6 +373,7 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
     l[r] = 0.f;
   }
   // blocks in [full_lo, full_hi) are visible to every row of the tile
+  const int pos_lo = len - nq + int(a.query_of(r0)), pos_hi = len - nq + int(a.query_of(r0 + nr - 1));
   const int full_lo = a.window > 0 ? max(0, pos_hi - a.window + 1 + kKvBlock - 1) / kKvBlock : 0;
   const int full_hi = (pos_lo + 1) / kKvBlock;
 
@@ -472,7 +569,7 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
   }
   __syncthreads();
 
-  float *part = a.partial + (int64_t(unit) * a.splits + split) * (R * (D + 2));
+  float *part = a.partial + (first + split) * (R * (D + 2));
   for (int i = threadIdx.x; i < nr * (D / 4); i += kThreads) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -507,7 +604,7 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
   // maxima and sums into shared memory, weights from them, then the accumulators: thread
   // (k, item) adds every KG-th split's four dims of one row, the KG sums are added in order
   const int step = R * (D + 2);
-  const float *all = a.partial + int64_t(unit) * a.splits * step;
+  const float *all = a.partial + first * step;
   float *w_m = s_acc, *w_l = s_acc + nsplit * R;
   for (int i = threadIdx.x; i < nsplit * R; i += kThreads) {
     const float *p = all + int64_t(i / R) * step + R * D + i % R;
@@ -588,7 +685,7 @@ constexpr int kTcMinRows = 64, kTcMinTokens = 6000;
 
 struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
-  int parts, groups, warps, tiles, splits, split_blocks;
+  int parts, groups, warps, tiles, splits, split_blocks, entries, ctas;
   int64_t units;
   size_t bytes;  // of the workspace, for any window
 };
@@ -637,23 +734,31 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   int64_t splits = p.warps == 4 ? 4 * per_wave / p.units : per_wave / p.units;
   if (splits < 1) splits = 1;
   if (splits > max_splits(p.warps)) splits = max_splits(p.warps);
-  // a split costs its join (about 3 us): not below this many blocks per warp
   int64_t per = (blocks + splits - 1) / splits;
-  if (per < 4 * p.warps) per = 4 * p.warps;
+  if (per < kMinBlocks * p.warps) per = kMinBlocks * p.warps;
   if (per > max_split_blocks(p.warps)) per = max_split_blocks(p.warps);
   p.split_blocks = int(per);
   p.splits = int((blocks + per - 1) / per);
   if (p.splits < 1) p.splits = 1;
-  // another window can give up to as many splits as either size of CTA aims at or is forced to
-  int64_t most = 1;
+  p.ctas = p.units * p.splits <= 0x7fffffff ? int(p.units * p.splits) : 0;
+  // sequences of their own lengths: splits whose length the device chooses (above), as many as CTAs are aimed at
+  const int64_t aim = p.warps == 4 ? 4 * per_wave : per_wave, entries = int64_t(n_seqs) * p.tiles;
+  if (entries <= kMaxEntries && p.warps > 4 && n_seqs > 1 && per >= kEvenBlocks) {
+    const int64_t least = entries * ((blocks + max_split_blocks(p.warps) - 1) / max_split_blocks(p.warps));
+    const int64_t per_head = std::max(std::max(aim / n_kv, entries), least);
+    p.entries = int(entries);
+    p.ctas = per_head * n_kv <= 0x7fffffff ? int(per_head * n_kv) : 0;
+  }
+  // parts there can be, with any window: another one can want either size of CTA
+  int64_t slots = 0;
   for (int warps : {4, resident})
     if (warps == resident || p.units > di.sm_count) {
-      const int64_t aim = (warps == 4 ? 4 : 1) * int64_t(di.sm_count) * (resident / warps) / p.units;
-      const int64_t forced = (all_blocks + max_split_blocks(warps) - 1) / max_split_blocks(warps);
-      for (int64_t n : {aim < max_splits(warps) ? aim : max_splits(warps), forced})
-        if (n > most) most = n;
+      const int64_t to = (warps == 4 ? 4 : 1) * int64_t(di.sm_count) * (resident / warps);
+      const int64_t forced = p.units * ((all_blocks + max_split_blocks(warps) - 1) / max_split_blocks(warps));
+      for (int64_t n : {to, forced})
+        if (n > p.units && n > slots) slots = n;
     }
-  p.bytes = workspace_for(size_t(p.units), most > 1 ? size_t(p.units) * size_t(most) * R * (head_dim + 2) * 4 : 0);
+  p.bytes = workspace_for(size_t(p.units), size_t(slots) * R * (head_dim + 2) * 4);
   return p;
 }
 
@@ -678,7 +783,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
   const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, window, type);
-  if (p.splits < 1 || p.units > 0x7fffffff || (!p.tc && p.units * p.splits > 0x7fffffff)) return QDQ_ERR_UNSUPPORTED;
+  if (p.splits < 1 || p.units > 0x7fffffff || (!p.tc && p.ctas < 1)) return QDQ_ERR_UNSUPPORTED;
   AttnArgs a{};
   a.c = c;
   a.kv_len = kv_len;
@@ -699,6 +804,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.tiles = p.tiles;
   a.splits = p.splits;
   a.split_blocks = p.split_blocks;
+  a.entries = p.entries;
   a.window = window;
   a.type = type;
   a.scale = scale;
@@ -714,11 +820,15 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
     auto run = [&](auto kernel, size_t sm) {
       const cudaError_t r = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(sm));
       if (r != cudaSuccess) return int(r);
-      return int(launch(kernel, dim3(unsigned(p.units * p.splits)), dim3(p.warps * 32), sm, s, a));
+      return int(launch(kernel, dim3(unsigned(p.ctas)), dim3(p.warps * 32), sm, s, a));
     };
     if (p.warps == 4)
-      return p.parts == 2 ? run(kv_attn_kernel<D, 2, 4>, attn_smem<D, 2, 4>()) : run(kv_attn_kernel<D, 1, 4>, attn_smem<D, 1, 4>());
-    return p.parts == 2 ? run(kv_attn_kernel<D, 2, W>, attn_smem<D, 2, W>()) : run(kv_attn_kernel<D, 1, W>, attn_smem<D, 1, W>());
+      return p.parts == 2 ? run(kv_attn_kernel<D, 2, 4, false>, attn_smem<D, 2, 4>()) : run(kv_attn_kernel<D, 1, 4, false>, attn_smem<D, 1, 4>());
+    if (p.entries > 0)
+      return p.parts == 2 ? run(kv_attn_kernel<D, 2, W, true>, attn_smem<D, 2, W>())
+                          : run(kv_attn_kernel<D, 1, W, true>, attn_smem<D, 1, W>());
+    return p.parts == 2 ? run(kv_attn_kernel<D, 2, W, false>, attn_smem<D, 2, W>())
+                        : run(kv_attn_kernel<D, 1, W, false>, attn_smem<D, 1, W>());
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }

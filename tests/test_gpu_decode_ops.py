@@ -562,6 +562,41 @@ def test_attention_many_ragged_prompts(cuda_lib, dtype):
         _check_attention(c, table, lens, nq, q, out, lse, dtype, 0.125, 0, window, None)
 
 
+@pytest.mark.parametrize("lens,nq,heads,n_kv,dim,dtype,window", [
+    ([3000, 17, 0, 900, 1], [1] * 5, 6, 2, 128, "f32", 0),
+    ([5000, 40], [1, 1], 4, 4, 64, "bf16", 0),
+    ([700, 2100, 64], [5, 3, 9], 6, 3, 96, "f16", 0),
+    ([1500, 10, 2600], [1, 0, 4], 8, 2, 256, "bf16", 0),
+    ([130, 4000, 2000, 1999], [1] * 4, 12, 4, 192, "f32", 0),
+    ([9000, 200], [1, 1], 2, 2, 64, "f32", 0),
+    ([2500, 4100, 30], [2, 1, 1], 4, 2, 128, "f32", 3200),
+    ([60] * 19 + [4000], [1] * 20, 7, 7, 64, "f16", 0)])
+def test_attention_splits_follow_the_lengths(cuda_lib, lens, nq, heads, n_kv, dim, dtype, window):
+    # few, uneven sequences with a bound far above their lengths; twice, for the tickets
+    import torch
+    rng = np.random.default_rng(sum(lens))
+    raw, table, c = _filled(rng, lens, 32, n_kv, dim)
+    q = _t((2 * rng.standard_normal((sum(nq), heads, dim))).astype(np.float32), _dt(dtype))
+    ws = cuda_lib.kv_attention_workspace(len(lens), max(nq), 900000, heads, n_kv, dim)
+    first = _attend(cuda_lib, raw, table, lens, nq, q, heads, n_kv, dim, 32, window=window, max_kv=900000, workspace=ws)
+    _check_attention(c, table, lens, nq, q, first[0], first[1], dtype, dim ** -0.5, 0.0, window, None)
+    again = _attend(cuda_lib, raw, table, lens, nq, q, heads, n_kv, dim, 32, window=window, max_kv=900000, workspace=ws)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_attention_splits_with_lengths_out_of_range(cuda_lib):
+    import torch
+    rng = np.random.default_rng(2)
+    lens = [1000, 3000, 2000, 40]
+    raw, table, c = _filled(rng, lens, 32, 2, 64)
+    q = _t(rng.standard_normal((4, 4, 64)).astype(np.float32))
+    told = [1000, 3001 + 32 * 40, -1, 40]  # the second past its table row, the third negative
+    out, lse = _attend(cuda_lib, raw, table, told, [1] * 4, q, 4, 2, 64, 32, max_kv=900000)
+    assert torch.isnan(out[[1, 2]]).all() and torch.isnan(lse[[1, 2]]).all()
+    for s in (0, 3):
+        _check_attention(c, table[s:s + 1], [lens[s]], [1], q[s:s + 1], out[s:s + 1], lse[s:s + 1], "f32", 0.125, 0.0, 0, None)
+
+
 @pytest.mark.usefixtures("attn_kernel")
 def test_attention_strided_rows(cuda_lib):
     # q and out inside wider buffers; other elements stay
