@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
         p[r][e] = (PARTS == 2 ? sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)] : sc[e >> 1][2 * r + (e & 1)]) * f;
       if (a.softcap > 0.f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[r][e] = a.softcap * kLog2e * tanh_of(p[r][e] * a.inv_cap);
+        for (int e = 0; e < 4; ++e) p[r][e] = a.softcap * kLog2e * tanh_of<PARTS == 2>(p[r][e] * a.inv_cap);
       }
       const int j0 = blk * kKvBlock + 2 * t;
       if (a.slopes) {

@@ -48,15 +48,17 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// tanh(x): below 1/4 the Taylor series (its next term is 6e-8 of the value there), else
-// 1 - 2 / (1 + e^2x); both relative to a few 1e-7.  (Half the instructions of tanhf, which took a
-// third of a capped call.)
+// tanh(x) = 1 - 2 / (1 + e^2x), off by 2^-21 at most; with kSmall (f32 activations) also to a few 1e-7
+// relative near 0: below 1/4 the Taylor series (its next term is 6e-8 of the value there).  (tanhf took twice
+// the instructions, a third of a capped call.)
+template <bool kSmall>
 __device__ __forceinline__ float tanh_of(float x) {
-  const float t = x * x;
-  const float small = x * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
   const float e = ex2(x * (2.f * kLog2e));  // 0 or infinity at the ends: -1 and 1
   const float large = 1.f - __fdividef(2.f, 1.f + e);
-  return fabsf(x) < 0.25f ? small : (x > 44.f ? 1.f : large);
+  if constexpr (!kSmall) return large;
+  const float t = x * x;
+  const float small = x * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  return fabsf(x) < 0.25f ? small : large;
 }
 
 // A block of the split.

@@ -25,7 +25,7 @@
 //   1 warp that brings the codes (bulk copies).
 // Bound: the chain of a tile (codes converted, S, softmax, P V: 1.2 us a tile, no unit more than half busy)
 // and what a part costs besides (queries 5 us, output 4 us, a join 8 us).  Measured: 2 prompts of 512 queries
-// over 3500 to 4600 tokens, 24 / 8 heads of 128, bf16: 90 us, 0.5 PFLOP/s; the decode kernel took 278 us.
+// over 3500 to 4600 tokens, 24 / 8 heads of 128, bf16: 85 us, 0.56 PFLOP/s; the decode kernel took 278 us.
 // One CTA per SM.  Two groups (head dims up to 128) share each tile's conversion.  Every wait is
 // bounded; one that runs out makes the CTA's rows NaN and counts in qdq_pipeline_timeouts.
 #include "qdq_kv_attn.cuh"
@@ -170,7 +170,8 @@ struct Bars {
   int abort, last, entry, shares;
 };
 
-template <int D, int PARTS, int G>
+// BENT: the scores have a cap or a bias.
+template <int D, int PARTS, int G, bool BENT>
 __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(const AttnArgs a) {
   using C = Cfg<D, PARTS, G>;
   constexpr int R = kTcRows * G, kThreads = C::kThreads, kConv = C::kConv;
@@ -516,126 +517,199 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         const int j0 = (c0 + 4 * i) * kKvBlock;
         const bool whole = j0 >= all_lo && j0 + BN <= all_hi;
         const BlockAt *blk = s_blk + 4 * i;
-        // scores of one block of 16 that need more than a factor: cap, bias, mask (log2 units)
-        auto transform = [&](int c, uint32_t *r) {
-          const float fc = qs * blk[c].ks;
+        // moves the reference, l and O with it; false after a wait's time limit
+        auto raise = [&](float m_new) {
+          const float corr = m_new > m ? ex2(m - m_new) : 1.f;
+          l *= corr;
+          m = m_new;
+          if (i > 0) {
+            if (!wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16_async(otm + c, o);
+              tmem_wait_ld16(o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = j0 + 16 * c + e;
-            float x = __uint_as_float(r[e]) * fc;
-            if (a.softcap > 0.f) x = a.softcap * kLog2e * tanh_of(x * a.inv_cap);
-            if (a.slopes) x = fmaf(-slope, float(pos - j), x);
-            if (j > pos || j < lo_pos) x = ninf;
-            r[e] = __float_as_uint(x);
-          }
-        };
-        uint32_t hi[4][8], lo[4][PARTS == 2 ? 8 : 1];
-        float sum, most;  // of the tile's probabilities; largest sum of a block's times its value scale
-        // the tile's probabilities for the present reference, from S in TMEM, a block of 16 at a time
-        auto probabilities = [&](auto plain) {
-          constexpr bool kPlain = decltype(plain)::value;
-          const float mref = m == ninf ? 0.f : m;
-          uint32_t r[2][16];
-          tmem_ld16_async(sp, r[0]);
-          sum = most = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t *x = r[c & 1];
-            tmem_wait_ld16(x);
-            if (c < 3) tmem_ld16_async(sp + 16 * (c + 1), r[(c + 1) & 1]);
-            if constexpr (!kPlain) transform(c, x);
-            // plain: the value scale goes into the exponent, p * vs = 2^(s - reference + log2 vs), and out of the
-            // block's sum again (a product less per score; the exponent's rounding is within the scores')
-            const float f = kPlain ? qs * blk[c].ks : 1.f, vs = blk[c].vs;
-            const float off = kPlain ? blk[c].lv + (kLog2PScale - mref) : -mref;
-            const float2 mm = f2(off, off);
-            float2 l2, l3;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 y = kPlain ? __ffma2_rn(f2_bits(x[2 * e], x[2 * e + 1]), f2(f, f), mm)
-                                      : __fadd2_rn(f2_bits(x[2 * e], x[2 * e + 1]), mm);
-              const float2 p = f2(ex2(y.x), ex2(y.y));
-              if (e == 0) l2 = p;
-              else if (e == 1) l3 = p;
-              else if (e & 1) l3 = __fadd2_rn(l3, p);
-              else l2 = __fadd2_rn(l2, p);
-              float2 pv = p;
-              if constexpr (!kPlain) {  // a hidden token's scale may be NaN
-                pv = __fmul2_rn(p, f2(vs, vs));
-                if (y.x == ninf) pv.x = 0.f;
-                if (y.y == ninf) pv.y = 0.f;
-              }
-              hi[c][e] = pack2(pv.x, pv.y, __half{});
-              if constexpr (PARTS == 2) {
-                const float2 back = unpack2(hi[c][e], __half{});
-                lo[c][e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
-              }
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st16(otm + c, o);
             }
-            const float bs = (l2.x + l2.y) + (l3.x + l3.y);
-            sum = kPlain ? fmaf(bs, blk[c].inv, sum) : sum + bs;
-            most = fmaxf(most, kPlain ? bs : bs * vs);
           }
+          return true;
         };
-        // the largest score plus log2 of its value scale
-        auto largest = [&](bool plain) {
-          float mx = ninf;
+        if constexpr (BENT) {
+          // Scores that need more than a factor (cap or bias, and the mask): transformed in their place in TMEM, then the
+          // reference, then the probabilities, a block of 16 at a time in loops (unrolled over the tile this
+          // was 30 KB of code, which eight warps fetched from far: a capped tile took 8 us).
+          float most = ninf;  // the largest score plus log2 of its value scale
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t x[16];
             tmem_ld16_async(sp + 16 * c, x);
             tmem_wait_ld16(x);
-            if (!plain) transform(c, x);
+            const float f = qs * blk[c].ks * (a.softcap > 0.f ? a.inv_cap : 1.f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+            if (a.softcap > 0.f) {
+              const float cap = a.softcap * kLog2e;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(cap * tanh_of<PARTS == 2>(__uint_as_float(x[e])));
+            }
+            if (a.slopes) {
+              const float at = float(pos - (j0 + 16 * c));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(fmaf(-slope, at - float(e), __uint_as_float(x[e])));
+            }
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int j = j0 + 16 * c + e;
+                if (j > pos || j < lo_pos) x[e] = __float_as_uint(ninf);
+              }
+            }
             float bm = __uint_as_float(x[0]);
 #pragma unroll
             for (int e = 1; e < 16; ++e) bm = fmaxf(bm, __uint_as_float(x[e]));
-            mx = fmaxf(mx, plain ? fmaf(bm, qs * blk[c].ks, blk[c].lv) : bm + blk[c].lv);
+            most = fmaxf(most, bm + blk[c].lv);
+            tmem_st16(sp + 16 * c, x);
           }
-          return mx;
-        };
-        // Every p * vs of a block is at most the block's sum of p times vs: where those stay below
-        // 2^15 (f16 ends at 2^16) with the reference there is, no maximum is looked for (64
-        // comparisons less per row and tile).  Else, and for a row's first tile, the maximum moves
-        // the reference and the probabilities are computed once more.
-        const bool plain = whole && !(a.softcap > 0.f) && !a.slopes &&
-                           fminf(fminf(blk[0].inv, blk[1].inv), fminf(blk[2].inv, blk[3].inv)) > 0.f;
-        bool again = __any_sync(0xffffffffu, m == ninf), ok = true;
-        for (;;) {
-          if (again) {  // the reference: see qdq_kv_attn.cu
-            const float m_new = fmaxf(m, largest(plain));
-            const bool grow = m_new > m + (m == ninf ? 0.f : kLazy);
-            if (__any_sync(0xffffffffu, grow)) {
-              const float corr = m_new > m ? ex2(m - m_new) : 1.f;
-              l *= corr;
-              m = m_new;
-              if (i > 0) {
-                ok = wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1);
-                if (!ok) break;
-                tc_fence_after();
+          tmem_wait_st();
+          const float m_new = fmaxf(m, most);
+          if (__any_sync(0xffffffffu, m_new > m + (m == ninf ? 0.f : kLazy))) {
+            if (!raise(m_new)) break;
+          }
+          const float mref = m == ninf ? 0.f : m;
+          const float2 mm = f2(-mref, -mref);
+          float sum = 0.f;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  uint32_t o[16];
-                  tmem_ld16_async(otm + c, o);
-                  tmem_wait_ld16(o);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[16], hi[8], lo[PARTS == 2 ? 8 : 1];
+            tmem_ld16_async(sp + 16 * c, x);
+            tmem_wait_ld16(x);
+            const float vs = blk[c].vs;
+            float2 l2 = f2(0.f, 0.f);
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                  tmem_st16(otm + c, o);
-                }
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = __fadd2_rn(f2_bits(x[2 * e], x[2 * e + 1]), mm), p = f2(ex2(y.x), ex2(y.y));
+              l2 = __fadd2_rn(l2, p);
+              float2 pv = __fmul2_rn(p, f2(vs, vs));
+              if (y.x == ninf) pv.x = 0.f;  // a hidden token's scale may be NaN
+              if (y.y == ninf) pv.y = 0.f;
+              hi[e] = pack2(pv.x, pv.y, __half{});
+              if constexpr (PARTS == 2) {
+                const float2 back = unpack2(hi[e], __half{});
+                lo[e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
               }
             }
+            sum += l2.x + l2.y;
+            tmem_st8(sp + 16 * c, hi);  // over the block's own columns of S
+            if constexpr (PARTS == 2) tmem_st8(sp + 16 * c + 8, lo);
           }
-          if (plain)
-            probabilities(std::true_type{});
-          else
-            probabilities(std::false_type{});
-          if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) break;
-          again = true;
-        }
-        if (!ok) break;
-        l += sum;
+          l += sum;
+        } else {
+          // scores of one block of 16 of which some may be hidden (log2 units)
+          auto transform = [&](int c, uint32_t *r) {
+            const float fc = qs * blk[c].ks;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // over the block's own columns of S
-          tmem_st8(sp + 16 * c, hi[c]);
-          if constexpr (PARTS == 2) tmem_st8(sp + 16 * c + 8, lo[c]);
+            for (int e = 0; e < 16; ++e) {
+              const int j = j0 + 16 * c + e;
+              float x = __uint_as_float(r[e]) * fc;
+              if (j > pos || j < lo_pos) x = ninf;
+              r[e] = __float_as_uint(x);
+            }
+          };
+          uint32_t hi[4][8], lo[4][PARTS == 2 ? 8 : 1];
+          float sum, most;  // of the tile's probabilities; largest sum of a block's times its value scale
+          // the tile's probabilities for the present reference, from S in TMEM, a block of 16 at a time
+          auto probabilities = [&](auto plain) {
+            constexpr bool kPlain = decltype(plain)::value;
+            const float mref = m == ninf ? 0.f : m;
+            uint32_t r[2][16];
+            tmem_ld16_async(sp, r[0]);
+            sum = most = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t *x = r[c & 1];
+              tmem_wait_ld16(x);
+              if (c < 3) tmem_ld16_async(sp + 16 * (c + 1), r[(c + 1) & 1]);
+              if constexpr (!kPlain) transform(c, x);
+              // plain: the value scale goes into the exponent, p * vs = 2^(s - reference + log2 vs), and out of the
+              // block's sum again (a product less per score; the exponent's rounding is within the scores')
+              const float f = kPlain ? qs * blk[c].ks : 1.f, vs = blk[c].vs;
+              const float off = kPlain ? blk[c].lv + (kLog2PScale - mref) : -mref;
+              const float2 mm = f2(off, off);
+              float2 l2, l3;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 y = kPlain ? __ffma2_rn(f2_bits(x[2 * e], x[2 * e + 1]), f2(f, f), mm)
+                                        : __fadd2_rn(f2_bits(x[2 * e], x[2 * e + 1]), mm);
+                const float2 p = f2(ex2(y.x), ex2(y.y));
+                if (e == 0) l2 = p;
+                else if (e == 1) l3 = p;
+                else if (e & 1) l3 = __fadd2_rn(l3, p);
+                else l2 = __fadd2_rn(l2, p);
+                float2 pv = p;
+                if constexpr (!kPlain) {  // a hidden token's scale may be NaN
+                  pv = __fmul2_rn(p, f2(vs, vs));
+                  if (y.x == ninf) pv.x = 0.f;
+                  if (y.y == ninf) pv.y = 0.f;
+                }
+                hi[c][e] = pack2(pv.x, pv.y, __half{});
+                if constexpr (PARTS == 2) {
+                  const float2 back = unpack2(hi[c][e], __half{});
+                  lo[c][e] = pack2(pv.x - back.x, pv.y - back.y, __half{});
+                }
+              }
+              const float bs = (l2.x + l2.y) + (l3.x + l3.y);
+              sum = kPlain ? fmaf(bs, blk[c].inv, sum) : sum + bs;
+              most = fmaxf(most, kPlain ? bs : bs * vs);
+            }
+          };
+          // the largest score plus log2 of its value scale
+          auto largest = [&](bool plain) {
+            float mx = ninf;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[16];
+              tmem_ld16_async(sp + 16 * c, x);
+              tmem_wait_ld16(x);
+              if (!plain) transform(c, x);
+              float bm = __uint_as_float(x[0]);
+#pragma unroll
+              for (int e = 1; e < 16; ++e) bm = fmaxf(bm, __uint_as_float(x[e]));
+              mx = fmaxf(mx, plain ? fmaf(bm, qs * blk[c].ks, blk[c].lv) : bm + blk[c].lv);
+            }
+            return mx;
+          };
+          // Every p * vs of a block is at most the block's sum of p times vs: where those stay below
+          // 2^15 (f16 ends at 2^16) with the reference there is, no maximum is looked for (64
+          // comparisons less per row and tile).  Else, and for a row's first tile, the maximum moves
+          // the reference and the probabilities are computed once more.
+          const bool plain = whole && fminf(fminf(blk[0].inv, blk[1].inv), fminf(blk[2].inv, blk[3].inv)) > 0.f;
+          bool again = __any_sync(0xffffffffu, m == ninf), ok = true;
+          for (;;) {
+            if (again) {  // the reference: see qdq_kv_attn.cu
+              const float m_new = fmaxf(m, largest(plain));
+              const bool grow = m_new > m + (m == ninf ? 0.f : kLazy);
+              if (__any_sync(0xffffffffu, grow)) {
+                ok = raise(m_new);
+                if (!ok) break;
+              }
+            }
+            if (plain)
+              probabilities(std::true_type{});
+            else
+              probabilities(std::false_type{});
+            if (again || !__any_sync(0xffffffffu, most > 32768.f || sum > 1e30f)) break;
+            again = true;
+          }
+          if (!ok) break;
+          l += sum;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // over the block's own columns of S
+            tmem_st8(sp + 16 * c, hi[c]);
+            if constexpr (PARTS == 2) tmem_st8(sp + 16 * c + 8, lo[c]);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1009,7 +1083,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
 template <int D, int PARTS, int G>
 cudaError_t run(const AttnArgs &a, cudaStream_t s) {
   using C = Cfg<D, PARTS, G>;
-  const auto kernel = attn_tc_kernel<D, PARTS, G>;
+  const auto kernel = a.softcap > 0.f || a.slopes ? attn_tc_kernel<D, PARTS, G, true> : attn_tc_kernel<D, PARTS, G, false>;
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(C::kSmem));
   if (e != cudaSuccess) return e;
   return launch(kernel, dim3(a.splits), dim3(C::kThreads), C::kSmem, s, a);
