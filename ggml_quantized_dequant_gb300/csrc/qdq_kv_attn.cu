@@ -676,12 +676,15 @@ int with_dim(int d, F &&f) {
   }
 }
 
-// Query rows per key/value head from which on the tensor-core kernel runs, and the longest context of a CTA
-// up to which this file's kernel is kept all the same where its tiles do not outnumber the SMs (each is then an
-// SM's, split over idle ones).  One sequence of 4000 tokens, 24 / 8 heads of 128, us here and there: 64 queries
-// bf16 28 42, 128 84 45; 43 queries f32 25 46, 64 57 47; 30 queries f32 over 16000 tokens 90 57.  8
-// sequences of up to 6000: 8 queries bf16 39 52, 16 71 52, 64 146 67.  48 of up to 3000: 16 queries bf16 123 157, 22 176 158.
+// Query rows per key/value head from which on the tensor-core kernel runs.  This file's kernel is kept all the same
+// where its tiles do not outnumber the SMs (each is then an SM's, split over idle ones) and a CTA's context is at
+// most kTcMinTokens, and where all rows' tokens times dims are at most kTcMinWork.  Us here and there, 24 / 8 heads
+// of 128: 8 sequences of up to 6000 tokens, 8 queries bf16 39 52, 16 71 52, 64 146 67; 48 of up to 3000, 16
+// queries bf16 123 157, 22 176 158; one of 4000, 64 queries bf16 28 42, 128 84 45, 43 queries f32 25 46; 30 queries
+// f32 over 16000 90 57; a prompt of 100 queries over 1000 f32 31 42, 4 of 64 over 1000 bf16 50 37; 8 / 8 heads,
+// 300 queries over 600 f32 21 43; heads of 64, 512 queries over themselves f32 20 34, bf16 29 30.
 constexpr int kTcMinRows = 64, kTcMinTokens = 6000;
+constexpr int64_t kTcMinWork = 340'000'000;
 
 struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
@@ -697,8 +700,10 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
   const int64_t small = int64_t(n_seqs) * n_kv * ((rows * p.parts + 15) / 16);  // tiles of the other kernel
   const bool few = small <= di.sm_count && max_kv_len / (di.sm_count / small) <= kTcMinTokens;
+  const int64_t tokens_seen = std::max<int64_t>(1, int64_t(max_kv_len) - max_q / 2);
+  const bool light = int64_t(n_seqs) * n_kv * rows * head_dim <= kTcMinWork / tokens_seen;
   const int forced = g_opt_attn_kernel.load(std::memory_order_relaxed);
-  p.tc = (forced == 2 || (forced == 0 && rows > kTcMinRows && !few)) && (type == QDQ_TYPE_F32 || p.parts == 1) &&
+  p.tc = (forced == 2 || (forced == 0 && rows > kTcMinRows && !few && !light)) && (type == QDQ_TYPE_F32 || p.parts == 1) &&
          attn_tc_supported(head_dim, p.parts);
   if (p.tc) {
     p.groups = rows > kTcRows && head_dim <= 128 ? 2 : 1;
