@@ -93,7 +93,7 @@ struct Shared {
   };
   uint64_t lists[kWarps][kList];  // the warps' keys
   uint64_t top[kTop];             // best so far, descending, 0 past the end
-  uint32_t group[64];
+  uint32_t group[128];
   Stat stat[kWarps];
   int fill[kWarps];              // keys in each warp's list
   int count;
@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
   uint64_t bound = 0;        // this warp's: keys at or below it are not among the k best
   float bound_v = ninf, rm = ninf;  // rm: the largest of this thread's logits
   int done = 0;              // tiles
+  const bool many = k > 48;
   // tiles after which no new bound is taken: fewer than about 40 keys would be saved (300 rows of 128256 f32,
   // k = 5: one bound 37.4 us, this 32.9; bf16, k = 40: 68.6 and 46.9; 2000 rows of 32000 bf16, k = 5, always 50.7, this 46.8)
   const int until = max(1, k > 0 ? a.seg_tiles - 40 / k : 0);
@@ -291,21 +292,23 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     st.l += l;
     st.u += u;
     if (k > 0) {
-      // A bound, after 1, 2, 4, ... tiles: the k-th largest of 64 groups' maxima so far.  (With the first
+      // A bound, after 1, 2, 4, ... tiles: the k-th largest of 64 groups' maxima so far (128 from 49 up: of
+      // 64 groups' maxima the 64th lets some 300 logits of a tile by, of 128 some 90: 406 rows of 21944 f32, k = 64, 136
+      // and 31 us; bf16 rows of 128256, k = 40, 47 and 51 us).  (With the first
       // tile's alone every tile has about k logits above it, and half the warps have one.)
       rm = max_nan(rm, tm);
       if (done < until && (done & (done + 1)) == 0) {
         float gm = max_nan(rm, __shfl_xor_sync(0xffffffffu, rm, 1));
-        gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+        if (!many) gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
         const uint32_t mine = uint32_t(topk_key(gm, 0u) >> 32);  // its order; NaN the largest
-        const int i = tid >> 2, part = tid & 3;
+        const int size = many ? 2 : 4, i = tid / size, part = tid % size;
         if (part == 0) sh.group[i] = mine;
         __syncthreads();
         int r = 0;
 #pragma unroll 4
-        for (int j = part; j < 64; j += 4) r += sh.group[j] > mine || (sh.group[j] == mine && j < i);
+        for (int j = part; j < kThreads / size; j += size) r += sh.group[j] > mine || (sh.group[j] == mine && j < i);
         r += __shfl_xor_sync(0xffffffffu, r, 1);
-        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if (!many) r += __shfl_xor_sync(0xffffffffu, r, 2);
         if (part == 0 && r == k - 1) sh.bound = uint64_t(mine) << 32;  // below every key of this value
         __syncthreads();
         const uint64_t b = sh.bound;
@@ -360,9 +363,22 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
       at[w] = count;
       count += sh.fill[w];
     }
-    if (count <= kRank) {
+    if (count > kRank) {  // many: without those that a later bound has passed
+      const uint64_t low = sh.bound;
+      for (int i = lane; i < sh.fill[warp]; i += 32)
+        if (list[i] > low) {
+          const int to = atomicAdd(&sh.count, 1);
+          if (to < kRank) sh.rank[to] = list[i];
+        }
+      __syncthreads();
+      count = sh.count;
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
+    } else {
       for (int i = lane; i < sh.fill[warp]; i += 32) sh.rank[at[warp] + i] = list[i];
       __syncthreads();
+    }
+    if (count <= kRank) {
       rank_keys(sh, count);
     } else {  // many: sorted, in the lists' places
       for (int i = lane; i < kList; i += 32)
