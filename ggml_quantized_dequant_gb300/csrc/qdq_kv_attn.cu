@@ -700,6 +700,8 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
   const int64_t small = int64_t(n_seqs) * n_kv * ((rows * p.parts + 15) / 16);  // tiles of the other kernel
   const bool few = small <= di.sm_count && max_kv_len / (di.sm_count / small) <= kTcMinTokens;
+  // Blocks without a window.  A window's are never more, or its plan could want a larger workspace.
+  const int64_t all_blocks = (int64_t(max_kv_len) + kKvBlock - 1) / kKvBlock;
   const int64_t tokens_seen = std::max<int64_t>(1, int64_t(max_kv_len) - max_q / 2);
   const bool light = int64_t(n_seqs) * n_kv * rows * head_dim <= kTcMinWork / tokens_seen;
   const int forced = g_opt_attn_kernel.load(std::memory_order_relaxed);
@@ -712,7 +714,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     p.units = int64_t(n_seqs) * n_kv * p.tiles;
     int64_t tokens = max_kv_len;
     if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
-    const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
+    const int64_t blocks = std::min(all_blocks, (tokens + kKvBlock - 1) / kKvBlock + (window > 0));
     // whole waves of CTAs (one per SM), each with at most kTcSplitBlocks of the blocks there can be
     const int64_t most = p.units * ((blocks + 4) / 4 + kTcPartCost);  // tiles of 64 tokens and parts' costs
     const int64_t wave = int64_t(di.sm_count) * (kTcSplitBlocks / 4);
@@ -727,8 +729,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   // blocks a tile can see: its rows span at most R queries
   int64_t tokens = max_kv_len;
   if (window > 0 && tokens > int64_t(window) + R) tokens = int64_t(window) + R;
-  const int64_t blocks = (tokens + kKvBlock - 1) / kKvBlock + (window > 0);
-  const int64_t all_blocks = (int64_t(max_kv_len) + kKvBlock - 1) / kKvBlock;  // without a window
+  const int64_t blocks = std::min(all_blocks, (tokens + kKvBlock - 1) / kKvBlock + (window > 0));
   const int resident = head_dim <= 128 ? 16 : 8;  // warps per SM
   // Few tiles: CTAs that fill an SM, so that a tile is cut into few splits; many: small CTAs,
   // whose starts and ends overlap with their neighbours' work.

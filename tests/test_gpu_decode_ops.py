@@ -527,7 +527,7 @@ def test_calls_of_other_shapes_share_a_workspace(cuda_lib):
 @pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("n_seqs,nq,heads,n_kv,dim,max_kv", [
     (1, 1, 8, 8, 128, 161), (1, 1, 4, 2, 64, 40000), (24, 1, 8, 8, 64, 9000), (40, 3, 16, 8, 128, 700), (2, 40, 4, 2, 128, 3000),
-    (2, 65, 2, 2, 64, 5000), (1, 300, 2, 1, 128, 2000)])
+    (2, 65, 2, 2, 64, 5000), (1, 300, 2, 1, 128, 2000), (40, 1, 8, 8, 64, 16384), (11, 3328, 4, 4, 64, 100)])
 def test_attention_workspace_is_enough_for_any_window(cuda_lib, n_seqs, nq, heads, n_kv, dim, max_kv):
     # how a call is cut depends on the window; the workspace's size does not: nothing is written past it
     import torch
