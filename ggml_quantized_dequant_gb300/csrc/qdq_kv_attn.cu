@@ -124,8 +124,8 @@ constexpr int body_bytes() {
 // in different banks (unexchanged, a one-token call took 1.5 us longer).
 __device__ __forceinline__ int quad_at(int row, int c) { return c ^ (((c >> 3) & 3) | ((row & 1) << 2)); }
 
-// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.  W warps.  EVEN: the splits' length follows the
-// sequences' lengths, else a.split_blocks.
+// PARTS = 2: 8 rows per tile in two f16 parts; 1: 16 rows.  W warps.  EVEN: the splits' length follows all
+// sequences' lengths, else it is at most a.split_blocks.
 template <int D, int PARTS, int W, bool EVEN>
 __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kernel(const AttnArgs a) {
   constexpr int kThreads = W * 32;
@@ -175,7 +175,9 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
     h = u / a.tiles % a.c.n_kv;
     s = u / a.tiles / a.c.n_kv;
     me = tile_of(s, tile);
-    per = a.split_blocks;
+    // in large CTAs a sequence far below max_kv_len is cut into as many splits as one at it (one of 4000
+    // tokens under a bound of 131072: 24.0 us in one split)
+    per = W > 4 ? min(a.split_blocks, max(kMinBlocks * W, int(float(me.nb) * a.inv_splits) + 1)) : a.split_blocks;
     nsplit = max(1, (me.nb + per - 1) / per);
     if (me.nr <= 0 || split >= nsplit) return;
     first = int64_t(u) * a.splits;
@@ -810,6 +812,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.tiles = p.tiles;
   a.splits = p.splits;
   a.split_blocks = p.split_blocks;
+  a.inv_splits = 1.f / float(p.splits);
   a.entries = p.entries;
   a.window = window;
   a.type = type;

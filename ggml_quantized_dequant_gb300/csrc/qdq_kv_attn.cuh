@@ -26,7 +26,7 @@ struct AttnArgs {
   int64_t q_stride, out_stride;
   int n_seqs, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
   int entries;  // decode kernel: sequences times tiles where the splits' length is chosen on the device, else 0
-  float scale, softcap, inv_cap;  // inv_cap: 1 / softcap
+  float scale, softcap, inv_cap, inv_splits;  // 1 / softcap, 1 / splits
   uint64_t group_mul;  // ceil(2^40 / group)
   // row / group, exact while row * group < 2^40 (rows are at most 2^30, the group of a row's heads below 2^10)
   __device__ __forceinline__ uint32_t query_of(int row) const { return uint32_t((uint64_t(uint32_t(row)) * group_mul) >> 40); }

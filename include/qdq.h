@@ -370,6 +370,7 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
  * A row that sees no token gives zeros and lse -inf.  A sequence with kv_len outside [0,
  * max_kv_len] or past its table row gives NaN, and so does a row that sees a token
  * with an invalid page or a NaN scale, and a query that is not finite.
+ * max_kv_len, max_q: a call is cut into CTAs by them (and the workspace sized), so bounds near the lengths are faster.
  * max_q: an upper bound of a sequence's queries (rows past it are not written), at most 2^20; a cache head
  * serves at most 1024 heads.
  * q, out: head_dim elements per head, n_heads heads per row, rows q_stride /
