@@ -757,8 +757,10 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     p.entries = int(entries);
     p.ctas = per_head * n_kv <= 0x7fffffff ? int(per_head * n_kv) : 0;
   }
-  // parts there can be, with any window: another one can want either size of CTA
-  int64_t slots = 0;
+  // Parts there can be, with any window: another one can want either size of CTA.  More CTAs than units cut a unit;
+  // as many do where the device chooses the splits, since a sequence without queries leaves its CTAs to the others.
+  const bool chosen = n_seqs > 1 && entries <= kMaxEntries && p.units <= di.sm_count;
+  int64_t slots = chosen ? p.units : 0;
   for (int warps : {4, resident})
     if (warps == resident || p.units > di.sm_count) {
       const int64_t to = (warps == 4 ? 4 : 1) * int64_t(di.sm_count) * (resident / warps);

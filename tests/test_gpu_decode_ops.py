@@ -584,6 +584,41 @@ def test_attention_splits_follow_the_lengths(cuda_lib, lens, nq, heads, n_kv, di
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("n_kv,group,drafts,dim,dtype,bound", [
+    (8, 3, 1, 128, "f32", 8000), (8, 1, 1, 64, "bf16", 3100), (4, 4, 4, 128, "f32", 6000), (2, 8, 1, 192, "f32", 6000),
+    (4, 4, 4, 96, "f16", 4000), (4, 4, 4, 256, "bf16", 8192)])
+def test_attention_workspace_holds_the_parts_of_idle_sequences(cuda_lib, n_kv, group, drafts, dim, dtype, bound):
+    # as many tiles of rows as SMs, a CTA for each: what sequences without queries or with fewer leave goes to the
+    # long ones, which are cut, and their parts need room
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = drafts * group
+    R = 16 if dtype != "f32" and rows > 8 else 8  # rows of a tile
+    n_seqs = sms // (n_kv * -(-rows // R))
+    if n_seqs * n_kv * -(-rows // R) != sms:
+        pytest.skip("no such number of sequences")
+    rng = np.random.default_rng(n_kv + dim)
+    lens = rng.integers(1, 150, n_seqs)
+    nq = rng.integers(0, 2, n_seqs) if drafts == 1 else np.minimum(1, rng.integers(0, 4, n_seqs))
+    long = rng.permutation(n_seqs)[:4]
+    lens[long[:2]], nq[long[:2]] = [bound, bound - 333], [drafts, 1]
+    lens[long[2:]], nq[long[2:]] = 2000, [0, drafts]
+    raw, table, c = _filled(rng, lens, 64, n_kv, dim)
+    q = _t(rng.standard_normal((nq.sum(), n_kv * group, dim)).astype(np.float32), _dt(dtype))
+    size = cuda_lib.kv_attention_workspace_bytes(n_seqs, drafts, bound, n_kv * group, n_kv, dim)
+    assert size - size // 8 // 256 * 256 >= sms * R * (dim + 2) * 4  # a part for each CTA; nothing is launched otherwise
+    buf = torch.zeros(size + (8 << 20), dtype=torch.uint8, device="cuda")
+    buf[size:] = 0x5A
+    first = None
+    for _ in range(2):
+        out, lse = _attend(cuda_lib, raw, table, lens, nq, q, n_kv * group, n_kv, dim, 64, max_kv=bound, workspace=buf[:size],
+                           max_q=drafts)
+        assert (buf[size:] == 0x5A).all()
+        first = first or (out, lse)
+        assert torch.equal(first[0], out) and torch.equal(first[1], lse)
+    _check_attention(c, table, lens, nq, q, out, lse, dtype, dim ** -0.5, 0, 0, None)
+
+
 def test_attention_splits_with_lengths_out_of_range(cuda_lib):
     import torch
     rng = np.random.default_rng(2)
