@@ -28,6 +28,7 @@ struct AppendArgs {
   const void *k, *v;
   int64_t k_stride, v_stride;
   int n_seqs, n_blocks;  // blocks per sequence that the grid covers
+  int max_new;           // tokens of a sequence past it are dropped
 };
 
 // Four elements as loaded: half the registers for the 16-bit types, and a maximum in half the steps
@@ -179,9 +180,9 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? (sizeof(T) == 2 ? 8 : 
     for (int b = blockIdx.y; b < a.n_blocks; b += gridDim.y) {
       const int first = a.cu ? int(ld_u1(a.cu + s)) : s;
       const int n_new = a.cu ? int(ld_u1(a.cu + s + 1)) - first : 1;
-      const int len = int(ld_u1(a.kv_len + s));
-      const int old = len - n_new;
+      const int all = int(ld_u1(a.kv_len + s)), old = all - n_new;
       if (n_new <= 0 || old < 0) break;
+      const int len = n_new > a.max_new ? old + a.max_new : all;
       const int blk = old / kKvBlock + b, p0 = blk * kKvBlock;
       if (p0 >= len) break;
       append_block<T, D>(a, rec, s, h, which, blk, old, len, first, lane);
@@ -193,7 +194,7 @@ struct ReadArgs {
   const int *start, *cu;  // first token of each sequence's range (NULL: 0); range sizes, summed
   void *k, *v;
   int64_t k_stride, v_stride;
-  int n_seqs, n_blocks;
+  int n_seqs, n_blocks, max_tokens;
 };
 
 // One warp per (sequence, block, head, keys or values), as above; a token without a valid page
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) 
   const int64_t stride = which ? a.v_stride : a.k_stride;
   for (int s = blockIdx.z; s < a.n_seqs; s += gridDim.z)
     for (int b = blockIdx.y; b < a.n_blocks; b += gridDim.y) {
-      const int row0 = int(ld_u1(a.cu + s)), n = int(ld_u1(a.cu + s + 1)) - row0;
+      const int row0 = int(ld_u1(a.cu + s)), n = min(int(ld_u1(a.cu + s + 1)) - row0, a.max_tokens);
       const int start = a.start ? int(ld_u1(a.start + s)) : 0;
       if (n <= 0 || start < 0) break;
       const int blk = start / kKvBlock + b, p0 = blk * kKvBlock;
@@ -263,7 +264,7 @@ int blocks_touched(int n) { return n / kKvBlock + (n % kKvBlock > 1 ? 2 : 1); }
 
 int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int *cu, int n_seqs, int max_new,
                      const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s) {
-  const AppendArgs a{c, kv_len, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_new)};
+  const AppendArgs a{c, kv_len, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_new), max_new};
   const dim3 grid = grid_of(c, n_seqs, a.n_blocks);
   const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {
@@ -275,7 +276,7 @@ int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int
 
 int launch_kv_read(const KvPool &c, int head_dim, const int *start, const int *cu, int n_seqs, int max_tokens, void *k,
                    void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s) {
-  const ReadArgs a{c, start, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_tokens)};
+  const ReadArgs a{c, start, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_tokens), max_tokens};
   const dim3 grid = grid_of(c, n_seqs, a.n_blocks);
   const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {

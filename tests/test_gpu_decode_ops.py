@@ -287,6 +287,33 @@ def test_tokens_without_a_page(cuda_lib):
     assert torch.equal(raw, was)
 
 
+def test_tokens_past_the_stated_bounds(cuda_lib):
+    # a sequence with more new (or wanted) tokens than max_new (max_tokens): the first ones are, the others are not
+    import torch
+    page, n_kv, dim = 32, 2, 64
+    raw = _pool(12, page, n_kv, dim)
+    raw[:, :, 2 * page * dim:] = 0  # no NaN scales: the pool's bytes are compared
+    want = ref.Cache(raw.cpu().numpy().copy(), page, n_kv, dim)
+    table = np.array([[5, 1, 7], [2, 0, 3]], np.int32)
+    k, v = torch.randn(90, n_kv, dim, device="cuda"), torch.randn(90, n_kv, dim, device="cuda")
+    for most, lens, new in ((1, [5, 1], [5, 1]), (3, [5 + 12, 3], [12, 2]), (20, [17 + 55, 3 + 15], [55, 15])):
+        cu = np.concatenate([[0], np.cumsum(new)])
+        cuda_lib.kv_append(raw, _i32(table), _i32(lens), k[:cu[-1]], v[:cu[-1]], n_kv, dim, page, cu_new=_i32(cu), max_new=most)
+        for s in range(2):  # the oracle is told of the first ones alone
+            n, at = min(new[s], most), slice(cu[s], cu[s] + min(new[s], most))
+            want.append(table[s:s + 1], [lens[s] - new[s] + n], [0, n], k[at].cpu().numpy(), v[at].cpu().numpy())
+        assert np.array_equal(raw.cpu().numpy().reshape(want.raw.shape), want.raw), most
+    cu, start = [0, 37, 46], [3, 1]
+    for most in (1, 8, 16, 30):
+        ko, vo = torch.full((46, n_kv, dim), 7.0, device="cuda"), torch.full((46, n_kv, dim), 7.0, device="cuda")
+        cuda_lib.kv_read(raw, _i32(table), _i32(start), _i32(cu), ko, vo, n_kv, dim, page, most)
+        for s in range(2):
+            n = min(cu[s + 1] - cu[s], most)
+            for got, val in zip((ko, vo), want.read(table, s, start[s], n)):
+                assert np.array_equal(_np(got[cu[s]:cu[s] + n]), val, equal_nan=True)
+                assert (got[cu[s] + n:cu[s + 1]] == 7).all(), most
+
+
 # ------------------------------------------------------------------ attention
 
 @pytest.fixture(params=["automatic", "decode", "tensor"])
