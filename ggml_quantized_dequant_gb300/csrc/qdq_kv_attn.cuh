@@ -24,7 +24,7 @@ struct AttnArgs {
   uint32_t *tickets;
   float *partial;
   int64_t q_stride, out_stride;
-  int n_seqs, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
+  int n_seqs, max_q, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
   int entries;  // decode kernel: sequences times tiles where the splits' length is chosen on the device, else 0
   float scale, softcap, inv_cap, inv_splits;  // 1 / softcap, 1 / splits
   uint64_t group_mul;  // ceil(2^40 / group)

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     x.q0 = a.cu_q ? int(ld_u1(a.cu_q + x.s)) : x.s;
     x.nq = a.cu_q ? int(ld_u1(a.cu_q + x.s + 1)) - x.q0 : 1;
     x.len = int(ld_u1(a.kv_len + x.s));
-    x.rows = x.nq * a.group;
+    x.rows = min(x.nq, a.max_q) * a.group;
     x.nr = min(R, x.rows - x.r0);
     x.bad = x.len < 0 || x.len > a.max_kv_len || (x.len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
     x.tiles = 0;

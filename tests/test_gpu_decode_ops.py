@@ -660,6 +660,26 @@ def test_attention_splits_with_lengths_out_of_range(cuda_lib):
 
 
 @pytest.mark.usefixtures("attn_kernel")
+@pytest.mark.parametrize("lens,nq,max_q,dtype", [([300, 40], [2, 1], 1, "f32"), ([300, 40], [9, 5], 4, "f16"),
+                                                 ([900, 400, 77], [200, 90, 30], 60, "bf16"), ([900, 400], [200, 150], 101, "f32")])
+def test_attention_of_queries_past_max_q(cuda_lib, lens, nq, max_q, dtype):
+    # a sequence's rows past max_q are not written; the others stand where all of them put them
+    rng = np.random.default_rng(max_q)
+    raw, table, c = _filled(rng, lens, 32, 2, 64)
+    q = _t(rng.standard_normal((sum(nq), 6, 64)).astype(np.float32), _dt(dtype))
+    out, lse = _attend(cuda_lib, raw, table, lens, nq, q, 6, 2, 64, 32, max_q=max_q)
+    full, full_lse = _attend(cuda_lib, raw, table, lens, nq, q, 6, 2, 64, 32)
+    _check_attention(c, table, lens, nq, q, full, full_lse, dtype, 0.125, 0, 0, None)
+    cu = np.concatenate([[0], np.cumsum(nq)])
+    for s in range(len(lens)):
+        n = min(nq[s], max_q)
+        for got, whole in ((out, full), (lse, full_lse)):
+            assert (got[cu[s] + n:cu[s + 1]] == 5).all()
+            got[cu[s] + n:cu[s + 1]] = whole[cu[s] + n:cu[s + 1]]  # for the comparison below
+    _check_attention(c, table, lens, nq, q, out, lse, dtype, 0.125, 0, 0, None)
+
+
+@pytest.mark.usefixtures("attn_kernel")
 def test_attention_strided_rows(cuda_lib):
     # q and out inside wider buffers; other elements stay
     import torch
