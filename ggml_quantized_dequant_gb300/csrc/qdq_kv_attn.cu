@@ -792,6 +792,8 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
+  // a window that hides nothing is none, and a position less a smaller one stays within 32 bits
+  if (window >= max_kv_len) window = 0;
   const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, window, type);
   if (p.splits < 1 || p.units > 0x7fffffff || (!p.tc && p.ctas < 1)) return QDQ_ERR_UNSUPPORTED;
   AttnArgs a{};

@@ -458,6 +458,19 @@ def test_attention_rows_that_see_nothing(cuda_lib, nq):
 
 
 @pytest.mark.usefixtures("attn_kernel")
+@pytest.mark.parametrize("nq", [9, 150])
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 100, 1 << 20, 200, 199])
+def test_attention_widest_windows_of_rows_before_the_sequence(cuda_lib, nq, window):
+    # a window as long as there are numbers for hides nothing, also where the first queries stand before the sequence
+    rng = np.random.default_rng(9)
+    lens, queries = [3, 200], [nq, 1]
+    raw, table, c = _filled(rng, lens, 32, 1, 64)
+    q = _t(rng.standard_normal((nq + 1, 2, 64)).astype(np.float32))
+    out, lse = _attend(cuda_lib, raw, table, lens, queries, q, 2, 1, 64, 32, window=window)
+    _check_attention(c, table, lens, queries, q, out, lse, "f32", 0.125, 0, window, None)
+
+
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("nq", [4, 100])
 def test_attention_nan_stays_in_its_rows(cuda_lib, nq):
     # a NaN block is seen by the rows at or after it (and by none past the window); a NaN or infinite
