@@ -325,7 +325,8 @@ def set_option(key: int, value: int) -> int:
 
 
 # ---------------------------------------------------------------- decode-step operators
-# (the element type and the row strides come from the tensors, whose first dimension is the rows)
+# (the element type and the row strides come from the tensors, whose first dimension is the rows; a tensor
+# with fewer rows or elements than the call reads or writes raises ValueError)
 
 _types = {}  # torch dtype -> QDQ_TYPE_*; filled at the first use, when torch is there
 
@@ -367,12 +368,25 @@ def _bind_fast():
     _fast = m
 
 
-def _vec(name, t, kind):
-    """Address of a contiguous int32 or float32 tensor, None for None (call _type first)."""
+def _vec(name, t, kind, least=0):
+    """Address of a contiguous int32 or float32 tensor of at least so many elements, None for None (call _type first)."""
     if t is None:
         return None
     if t.dtype is not _of[kind] or not t.is_contiguous():
         raise TypeError("%s: a contiguous %s tensor expected" % (name, kind))
+    if t.numel() < least:
+        raise ValueError("%s: %d elements expected, got %d" % (name, least, t.numel()))
+    return _cuda(name, t)
+
+
+def _bytes(name, t, least=0):
+    """Address of a contiguous tensor of at least so many bytes, None for None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("%s: a contiguous tensor expected" % name)
+    if t.nbytes < least:
+        raise ValueError("%s: %d bytes expected, got %d" % (name, least, t.nbytes))
     return _cuda(name, t)
 
 
@@ -385,9 +399,9 @@ def _cuda(name, t):
     return t.data_ptr()
 
 
-def _rows(name, t, width, dtype):
-    """(address, row stride) of a tensor of rows: the first dimension, the others hold ``width`` packed elements
-    (one dimension: one row)."""
+def _rows(name, t, width, dtype, least=0):
+    """(address, row stride) of a tensor of at least ``least`` rows: the first dimension, the others hold ``width`` packed
+    elements (one dimension: one row)."""
     if t is None:
         return None, 0
     if t.dtype is not dtype:
@@ -402,6 +416,8 @@ def _rows(name, t, width, dtype):
         w *= shape[d]
     if w != width:
         raise ValueError("%s: rows of %d elements expected, got shape %s" % (name, width, tuple(t.shape)))
+    if shape[0] < least:
+        raise ValueError("%s: %d rows expected, got %d" % (name, least, shape[0]))
     return _cuda(name, t), st[0] if shape[0] > 1 else width
 
 
@@ -418,12 +434,12 @@ def rms_norm(x, weight, out, rows: int, n: int, eps: float = 1e-5, residual=None
         if status is not None:
             raise QdqError("qdq_rms_norm", status)
     ty, dt = _type(x), x.dtype
-    xp, xs = _rows("x", x, n, dt)
-    rp, rs = _rows("residual", residual, n, dt)
-    sp, ss = _rows("sum_out", sum_out, n, dt)
-    op, os_ = _rows("out", out, n, dt)
-    status = lib().qdq_rms_norm(xp, rp, _vec("weight", weight, "float32"), sp, op, _cuda("q8_out", q8_out), ty, rows, n, xs, rs, ss, os_, eps,
-                                _stream(stream))
+    xp, xs = _rows("x", x, n, dt, rows)
+    rp, rs = _rows("residual", residual, n, dt, rows)
+    sp, ss = _rows("sum_out", sum_out, n, dt, rows)
+    op, os_ = _rows("out", out, n, dt, rows)
+    status = lib().qdq_rms_norm(xp, rp, _vec("weight", weight, "float32", n), sp, op, _bytes("q8_out", q8_out, rows * (n // 32) * 34), ty,
+                                rows, n, xs, rs, ss, os_, eps, _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_rms_norm", status)
 
@@ -464,10 +480,11 @@ def kv_append(pages, page_table, kv_len, k, v, n_kv: int, head_dim: int, page_to
             raise QdqError("qdq_kv_append", status)
     ty, w = _type(k), n_kv * head_dim
     pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
-    kp, ks = _rows("k", k, w, k.dtype)
-    vp, vs = _rows("v", v, w, k.dtype)
-    status = lib().qdq_kv_append(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32"),
-                                 _vec("cu_new", cu_new, "int32"), seqs, max_new, kp, vp, ks, vs, ty, _stream(stream))
+    least = seqs if cu_new is None else 0  # else the device knows how many rows there are
+    kp, ks = _rows("k", k, w, k.dtype, least)
+    vp, vs = _rows("v", v, w, k.dtype, least)
+    status = lib().qdq_kv_append(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32", seqs),
+                                 _vec("cu_new", cu_new, "int32", seqs + 1), seqs, max_new, kp, vp, ks, vs, ty, _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_kv_append", status)
 
@@ -486,8 +503,8 @@ def kv_read(pages, page_table, start, cu, k, v, n_kv: int, head_dim: int, page_t
     pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
     kp, ks = _rows("k", k, w, k.dtype)
     vp, vs = _rows("v", v, w, k.dtype)
-    status = lib().qdq_kv_read(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("start", start, "int32"),
-                               _vec("cu", cu, "int32"), seqs, max_tokens, kp, vp, ks, vs, ty, _stream(stream))
+    status = lib().qdq_kv_read(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("start", start, "int32", seqs),
+                               _vec("cu", cu, "int32", seqs + 1), seqs, max_tokens, kp, vp, ks, vs, ty, _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_kv_read", status)
 
@@ -519,12 +536,14 @@ def kv_attention(pages, page_table, kv_len, q, out, workspace, n_heads: int, n_k
             raise QdqError("qdq_kv_attention", status)
     ty, w = _type(q), n_heads * head_dim
     pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
-    qp, qs = _rows("q", q, w, q.dtype)
-    op, os_ = _rows("out", out, w, q.dtype)
+    least = seqs if cu_q is None else 0  # else the device knows how many rows there are
+    qp, qs = _rows("q", q, w, q.dtype, least)
+    op, os_ = _rows("out", out, w, q.dtype, least)
     status = lib().qdq_kv_attention(
-        pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32"), _vec("cu_q", cu_q, "int32"), seqs,
-        max_q, max_kv_len, n_heads, qp, qs, op, os_, _vec("lse", lse, "float32"), _vec("slopes", slopes, "float32"),
-        head_dim ** -0.5 if scale is None else scale, softcap, window, ty, _cuda("workspace", workspace), workspace.nbytes,
+        pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32", seqs),
+        _vec("cu_q", cu_q, "int32", seqs + 1), seqs, max_q, max_kv_len, n_heads, qp, qs, op, os_,
+        _vec("lse", lse, "float32", least * n_heads), _vec("slopes", slopes, "float32", n_heads),
+        head_dim ** -0.5 if scale is None else scale, softcap, window, ty, _bytes("workspace", workspace), workspace.nbytes,
         _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_kv_attention", status)
@@ -553,11 +572,11 @@ def token_logprobs(logits, tokens, logprob, entropy, rows: int, n: int, workspac
         if status is not None:
             raise QdqError("qdq_token_logprobs", status)
     ty = _type(logits)
-    xp, xs = _rows("logits", logits, n, logits.dtype)
+    xp, xs = _rows("logits", logits, n, logits.dtype, rows)
     status = lib().qdq_token_logprobs(
-        xp, xs, ty, _vec("tokens", tokens, "int32"), rows, n, k, _vec("logprob", logprob, "float32"),
-        _vec("entropy", entropy, "float32"), _vec("top_index", top_index, "int32"), _vec("top_logprob", top_logprob, "float32"),
-        _cuda("workspace", workspace), workspace.nbytes, _stream(stream))
+        xp, xs, ty, _vec("tokens", tokens, "int32", rows), rows, n, k, _vec("logprob", logprob, "float32", rows),
+        _vec("entropy", entropy, "float32", rows), _vec("top_index", top_index, "int32", rows * k),
+        _vec("top_logprob", top_logprob, "float32", rows * k), _bytes("workspace", workspace), workspace.nbytes, _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_token_logprobs", status)
 

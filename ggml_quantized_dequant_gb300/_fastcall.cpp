@@ -1,7 +1,7 @@
 // Argument marshalling of the decode-step operators in C: what the Python binding does for the
 // ordinary case (tensors of the right types, packed), without the interpreter's share of a call
 // (a one-row norm: 8 us through ctypes, of which 2 are the launch).  Anything unusual -- another
-// type, a stride, a wrong shape -- is left to the Python code, which names the error: the
+// type, a stride, a wrong shape, too few elements -- is left to the Python code, which names the error: the
 // functions then return None.  Only the Python C API is used; tensors are read through their
 // Python attributes.
 #define PY_SSIZE_T_CLEAN
@@ -11,7 +11,7 @@
 
 namespace {
 
-PyObject *s_dtype, *s_shape, *s_contig, *s_ptr, *s_nbytes, *s_cuda;
+PyObject *s_dtype, *s_shape, *s_contig, *s_ptr, *s_nbytes, *s_numel, *s_cuda;
 PyObject *g_types[3], *g_int32;  // torch.float32, float16, bfloat16; torch.int32
 decltype(&qdq_rms_norm) f_norm;
 decltype(&qdq_kv_append) f_append;
@@ -80,24 +80,42 @@ struct Reader {
     return t;
   }
   // Address of a packed tensor of one element type; NULL for None.
-  void *vec(PyObject *o, PyObject *dtype) {
+  void *packed(PyObject *o, PyObject *dtype) {
     if (!ok || o == Py_None) return nullptr;
     if (!is(o, s_dtype, dtype)) ok = false;
     contiguous(o);
     return address(o);
   }
-  // ... whose first dimension is rows of `width` elements.
-  void *rows(PyObject *o, long long width, PyObject *dtype, long long *stride) {
+  // ... of at least `least` elements.
+  void *vec(PyObject *o, PyObject *dtype, long long least) {
+    if (!ok || o == Py_None) return nullptr;
+    PyObject *r = PyObject_CallMethodNoArgs(o, s_numel);
+    if (!r || integer(r) < least) ok = false;
+    Py_XDECREF(r);
+    return packed(o, dtype);
+  }
+  // ... whose first dimension is at least `least` rows of `width` elements.
+  void *rows(PyObject *o, long long width, PyObject *dtype, long long *stride, long long least) {
     *stride = 0;
     if (!ok || o == Py_None) return nullptr;
     PyObject *shape = attr(o, s_shape);
     long long w = 1;
     if (!shape || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) < 2) ok = false;
+    if (ok && integer(PyTuple_GET_ITEM(shape, 0)) < least) ok = false;
     for (Py_ssize_t i = 1; ok && i < PyTuple_GET_SIZE(shape); ++i) w *= integer(PyTuple_GET_ITEM(shape, i));
     Py_XDECREF(shape);
     if (w != width) ok = false;
     *stride = width;
-    return vec(o, dtype);
+    return packed(o, dtype);
+  }
+  // Address of a packed tensor of at least `least` bytes; NULL for None.
+  void *bytes(PyObject *o, long long least, size_t *size) {
+    *size = 0;
+    if (!ok || o == Py_None) return nullptr;
+    *size = nbytes(o);
+    if (ok && (long long)*size < least) ok = false;
+    contiguous(o);
+    return address(o);
   }
   size_t nbytes(PyObject *o) {
     PyObject *r = attr(o, s_nbytes);
@@ -127,7 +145,7 @@ struct Pool {
     seqs = r.ok ? r.small(PyTuple_GET_ITEM(shape, 0)) : 0;
     width = r.ok ? r.small(PyTuple_GET_ITEM(shape, 1)) : 0;
     Py_XDECREF(shape);
-    table = static_cast<const int *>(r.vec(t, g_int32));
+    table = static_cast<const int *>(r.packed(t, g_int32));
   }
 };
 
@@ -144,10 +162,11 @@ PyObject *rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const int t = r.type(a[0]), rows = r.small(a[3]), n = r.small(a[4]);
   if (!r.ok) return leave();
   long long xs, rs, ss, os;
-  void *x = r.rows(a[0], n, g_types[t], &xs), *res = r.rows(a[6], n, g_types[t], &rs);
-  void *sum = r.rows(a[7], n, g_types[t], &ss), *out = r.rows(a[2], n, g_types[t], &os);
-  const float *w = static_cast<const float *>(r.vec(a[1], g_types[0]));
-  void *q8 = r.address(a[8]);
+  void *x = r.rows(a[0], n, g_types[t], &xs, rows), *res = r.rows(a[6], n, g_types[t], &rs, rows);
+  void *sum = r.rows(a[7], n, g_types[t], &ss, rows), *out = r.rows(a[2], n, g_types[t], &os, rows);
+  const float *w = static_cast<const float *>(r.vec(a[1], g_types[0], n));
+  size_t qb;
+  void *q8 = r.bytes(a[8], (long long)rows * (n / 32) * 34, &qb);
   const float eps = float(r.real(a[5]));
   const cudaStream_t st = stream_of(r, a[9]);
   if (!r.ok) return leave();
@@ -162,8 +181,9 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const int t = r.type(a[3]);
   if (!r.ok) return leave();
   long long ks, vs;
-  const int *len = static_cast<const int *>(r.vec(a[2], g_int32)), *cu = static_cast<const int *>(r.vec(a[8], g_int32));
-  void *k = r.rows(a[3], (long long)p.n_kv * p.head_dim, g_types[t], &ks), *v = r.rows(a[4], (long long)p.n_kv * p.head_dim, g_types[t], &vs);
+  const int *len = static_cast<const int *>(r.vec(a[2], g_int32, p.seqs)), *cu = static_cast<const int *>(r.vec(a[8], g_int32, p.seqs + 1ll));
+  const long long wide = (long long)p.n_kv * p.head_dim, least = cu ? 0 : p.seqs;
+  void *k = r.rows(a[3], wide, g_types[t], &ks, least), *v = r.rows(a[4], wide, g_types[t], &vs, least);
   const int most = r.small(a[9]);
   const cudaStream_t st = stream_of(r, a[10]);
   if (!r.ok) return leave();
@@ -179,8 +199,9 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const int t = r.type(a[4]);
   if (!r.ok) return leave();
   long long ks, vs;
-  const int *start = static_cast<const int *>(r.vec(a[2], g_int32)), *cu = static_cast<const int *>(r.vec(a[3], g_int32));
-  void *k = r.rows(a[4], (long long)p.n_kv * p.head_dim, g_types[t], &ks), *v = r.rows(a[5], (long long)p.n_kv * p.head_dim, g_types[t], &vs);
+  const int *start = static_cast<const int *>(r.vec(a[2], g_int32, p.seqs)), *cu = static_cast<const int *>(r.vec(a[3], g_int32, p.seqs + 1ll));
+  const long long wide = (long long)p.n_kv * p.head_dim;
+  void *k = r.rows(a[4], wide, g_types[t], &ks, 0), *v = r.rows(a[5], wide, g_types[t], &vs, 0);
   const int most = r.small(a[9]);
   const cudaStream_t st = stream_of(r, a[10]);
   if (!r.ok) return leave();
@@ -197,14 +218,15 @@ PyObject *kv_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const int t = r.type(a[3]), heads = r.small(a[6]);
   if (!r.ok) return leave();
   long long qs, os;
-  const int *len = static_cast<const int *>(r.vec(a[2], g_int32)), *cu = static_cast<const int *>(r.vec(a[11], g_int32));
-  void *q = r.rows(a[3], (long long)heads * p.head_dim, g_types[t], &qs), *out = r.rows(a[4], (long long)heads * p.head_dim, g_types[t], &os);
-  void *ws = r.address(a[5]);
-  const size_t wb = r.nbytes(a[5]);
+  const int *len = static_cast<const int *>(r.vec(a[2], g_int32, p.seqs)), *cu = static_cast<const int *>(r.vec(a[11], g_int32, p.seqs + 1ll));
+  const long long wide = (long long)heads * p.head_dim, least = cu ? 0 : p.seqs;
+  void *q = r.rows(a[3], wide, g_types[t], &qs, least), *out = r.rows(a[4], wide, g_types[t], &os, least);
+  size_t wb;
+  void *ws = r.bytes(a[5], 0, &wb);
   const int most_kv = r.small(a[10]), most_q = r.small(a[12]), window = r.small(a[15]);
   const float scale = float(r.real(a[13])), cap = float(r.real(a[14]));
-  const float *slopes = static_cast<const float *>(r.vec(a[16], g_types[0]));
-  float *lse = static_cast<float *>(r.vec(a[17], g_types[0]));
+  const float *slopes = static_cast<const float *>(r.vec(a[16], g_types[0], heads));
+  float *lse = static_cast<float *>(r.vec(a[17], g_types[0], least * heads));
   const cudaStream_t st = stream_of(r, a[18]);
   if (!r.ok) return leave();
   return PyLong_FromLong(f_attention(p.pages, p.n_pages, p.page_tokens, p.n_kv, p.head_dim, p.table, p.width, len, cu, p.seqs, most_q,
@@ -218,13 +240,13 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const int t = r.type(a[0]), rows = r.small(a[4]), n = r.small(a[5]), k = r.small(a[7]);
   if (!r.ok) return leave();
   long long xs;
-  void *x = r.rows(a[0], n, g_types[t], &xs);
-  const int *tokens = static_cast<const int *>(r.vec(a[1], g_int32));
-  float *lp = static_cast<float *>(r.vec(a[2], g_types[0])), *ent = static_cast<float *>(r.vec(a[3], g_types[0]));
-  int *ti = static_cast<int *>(r.vec(a[8], g_int32));
-  float *tl = static_cast<float *>(r.vec(a[9], g_types[0]));
-  void *ws = r.address(a[6]);
-  const size_t wb = r.nbytes(a[6]);
+  void *x = r.rows(a[0], n, g_types[t], &xs, rows);
+  const int *tokens = static_cast<const int *>(r.vec(a[1], g_int32, rows));
+  float *lp = static_cast<float *>(r.vec(a[2], g_types[0], rows)), *ent = static_cast<float *>(r.vec(a[3], g_types[0], rows));
+  int *ti = static_cast<int *>(r.vec(a[8], g_int32, (long long)rows * k));
+  float *tl = static_cast<float *>(r.vec(a[9], g_types[0], (long long)rows * k));
+  size_t wb;
+  void *ws = r.bytes(a[6], 0, &wb);
   const cudaStream_t st = stream_of(r, a[10]);
   if (!r.ok) return leave();
   return PyLong_FromLong(f_logprobs(x, xs, t, tokens, rows, n, k, lp, ent, ti, tl, ws, wb, st));
@@ -268,6 +290,7 @@ PyMODINIT_FUNC PyInit__fastcall(void) {
   s_contig = PyUnicode_InternFromString("is_contiguous");
   s_ptr = PyUnicode_InternFromString("data_ptr");
   s_nbytes = PyUnicode_InternFromString("nbytes");
+  s_numel = PyUnicode_InternFromString("numel");
   s_cuda = PyUnicode_InternFromString("is_cuda");
   return PyModule_Create(&module);
 }

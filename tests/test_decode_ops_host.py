@@ -179,6 +179,60 @@ def test_binding_refuses_wrong_tensors(qdq):
         qdq.kv_append(pages[:, 1:], table.int(), torch.zeros(1, dtype=torch.int32), x, x, 1, 64, 16)
 
 
+def _short_calls(qdq, device):
+    """Calls whose tensors are right but for one that holds less than the call reads or writes."""
+    import torch
+
+    def f(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype, device=device)
+
+    def i(*shape):
+        return f(*shape, dtype=torch.int32)
+
+    def norm(x=f(4, 64), w=f(64), o=f(4, 64), r=f(4, 64), s=f(4, 64), q=f(4 * 2 * 34, dtype=torch.uint8)):
+        qdq.rms_norm(x, w, o, 4, 64, residual=r, sum_out=s, q8_out=q)
+
+    pages, table, ws = f(3, 2176, dtype=torch.uint8), i(2, 1), f(1 << 22, dtype=torch.uint8)
+
+    def append(n=i(2), k=f(2, 64), v=f(2, 64), cu=None):
+        qdq.kv_append(pages, table, n, k, v, 1, 64, 16, cu_new=cu, max_new=1)
+
+    def read(start=i(2), cu=i(3), k=f(2, 64), v=f(2, 64)):
+        qdq.kv_read(pages, table, start, cu, k, v, 1, 64, 16, 1)
+
+    def attention(n=i(2), q=f(2, 128), o=f(2, 128), cu=None, sl=f(2), lse=f(2, 2), ws=ws):
+        qdq.kv_attention(pages, table, n, q, o, ws, 2, 1, 64, 16, 16, cu_q=cu, slopes=sl, lse=lse)
+
+    def logprobs(x=f(4, 64), t=i(4), lp=f(4), en=f(4), k=3, ti=i(4, 3), tl=f(4, 3), ws=ws):
+        qdq.token_logprobs(x, t, lp, en, 4, 64, ws, k, ti, tl)
+
+    return {norm: dict(x=f(3, 64), w=f(63), o=f(3, 64), r=f(3, 64), s=f(3, 64), q=f(4 * 2 * 34 - 1, dtype=torch.uint8)),
+            append: dict(n=i(1), k=f(1, 64), v=f(1, 64), cu=i(2)), read: dict(start=i(1), cu=i(2)),
+            attention: dict(n=i(1), q=f(1, 128), o=f(1, 128), cu=i(2), sl=f(1), lse=f(1, 2), ws=f(1 << 22, 2, dtype=torch.uint8)[:, 0]),
+            logprobs: dict(x=f(3, 64), t=i(3), lp=f(3), en=f(3), ti=i(3, 3), tl=f(3, 3), ws=f(1 << 22, 2, dtype=torch.uint8)[:, 0])}
+
+
+def test_binding_refuses_short_tensors(qdq, monkeypatch):
+    # (host tensors in the place of the device's: every call is refused before anything is launched)
+    monkeypatch.setattr(qdq, "_cuda", lambda name, t: None if t is None else t.data_ptr())
+    for call, short in _short_calls(qdq, "cpu").items():
+        for name, tensor in short.items():
+            with pytest.raises(ValueError, match="expected"):
+                call(**{name: tensor})
+
+
+@pytest.mark.gpu
+def test_binding_refuses_short_tensors_of_the_device(cuda_lib):
+    # whole tensors run; short ones are refused as on the host, by the ordinary path too
+    import torch
+    for call, short in _short_calls(cuda_lib, "cuda").items():
+        call()
+        for name, tensor in short.items():
+            with pytest.raises(ValueError, match="expected"):
+                call(**{name: tensor})
+    torch.cuda.synchronize()
+
+
 def test_attention_kernel_option(qdq):
     assert qdq.set_option(qdq.QDQ_OPT_ATTN_KERNEL, 2) == 0
     assert qdq.lib().qdq_set_option(qdq.QDQ_OPT_ATTN_KERNEL, 3) == qdq.QDQ_ERR_DIMS
