@@ -344,28 +344,32 @@ def _type(t) -> int:
 
 _of = {}
 _fast = None       # the C marshalling (_fastcall.so), bound to _fast_lib's functions
-_fast_lib = None   # None: not tried yet
+_fast_lib = None   # None: not tried yet; False: every call goes through the Python code
 
 
 def _bind_fast():
-    """Bind the C marshalling to the loaded library, once (its build is part of the library's)."""
+    """Bind the C marshalling to the loaded library, once.  Where it was not built, or for another interpreter, and
+    where nothing can be launched, the Python code makes the calls."""
     global _fast, _fast_lib
     import importlib.util
     import torch
-    if not torch.cuda.is_available():  # nothing can be launched: the Python code checks the arguments
+    path = os.path.join(_PKG, "_fastcall.so")
+    if not torch.cuda.is_available() or not os.path.exists(path):
         _fast_lib = False
         return
-    _fast_lib = lib()
-    path = os.path.join(_PKG, "_fastcall.so")
-    if not os.path.exists(path):
-        raise RuntimeError("_fastcall.so is not built (%s); run __graft_entry__.build()" % path)
-    spec = importlib.util.spec_from_file_location("_fastcall", path)
-    m = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(m)
-    m.bind(*[ctypes.cast(getattr(_fast_lib, f), ctypes.c_void_p).value for f in (
+    handle = lib()
+    try:
+        spec = importlib.util.spec_from_file_location("_fastcall", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+    except ImportError:
+        _fast_lib = False
+        return
+    m.bind(*[ctypes.cast(getattr(handle, f), ctypes.c_void_p).value for f in (
         "qdq_rms_norm", "qdq_kv_append", "qdq_kv_read", "qdq_kv_attention", "qdq_token_logprobs")],
         torch.float32, torch.float16, torch.bfloat16, torch.int32)
-    _fast = m
+    _fast = m  # before _fast_lib, which sends other threads' calls to it
+    _fast_lib = handle
 
 
 def _vec(name, t, kind, least=0):

@@ -38,10 +38,14 @@ FASTCALL_SRC = os.path.join(PKG, "_fastcall.cpp")
 FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 
-def build_fastcall() -> str:
-    """Compile the binding's C argument marshalling (a plain Python extension module, host code only)."""
+def build_fastcall() -> str | None:
+    """Compile the binding's C argument marshalling (a plain Python extension module, host code only).
+
+    None without Python's C headers: the binding's own Python code then makes the calls."""
     import sysconfig
     inc = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(inc, "Python.h")):
+        return None
     cmd = [_nvcc(), "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", inc,
            "-o", FASTCALL + ".tmp", FASTCALL_SRC]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -179,6 +179,33 @@ def test_binding_refuses_wrong_tensors(qdq):
         qdq.kv_append(pages[:, 1:], table.int(), torch.zeros(1, dtype=torch.int32), x, x, 1, 64, 16)
 
 
+def test_binding_without_the_c_marshalling(qdq, monkeypatch, tmp_path):
+    # not built, or not loadable: the Python code makes the calls (and refuses a host tensor)
+    import torch
+    x = torch.zeros(4, 64)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(qdq, "_PKG", str(tmp_path))
+    for content in (None, b"not a library"):
+        if content:
+            (tmp_path / "_fastcall.so").write_bytes(content)
+        monkeypatch.setattr(qdq, "_fast_lib", None)
+        monkeypatch.setattr(qdq, "_fast", None)
+        for _ in range(2):
+            with pytest.raises(TypeError, match="CUDA tensor"):
+                qdq.rms_norm(x, None, x.clone(), 4, 64)
+
+
+def test_build_without_python_headers(qdq, monkeypatch, tmp_path):
+    import sysconfig
+
+    from ggml_quantized_dequant_gb300 import _build
+    paths = dict(sysconfig.get_paths(), include=str(tmp_path))
+    monkeypatch.setattr(sysconfig, "get_paths", lambda: paths)
+    monkeypatch.setattr(_build, "FASTCALL", str(tmp_path / "_fastcall.so"))
+    assert _build.build_fastcall() is None
+    assert _build.build() == _build.LIB and not (tmp_path / "_fastcall.so").exists()
+
+
 def _short_calls(qdq, device):
     """Calls whose tensors are right but for one that holds less than the call reads or writes."""
     import torch
