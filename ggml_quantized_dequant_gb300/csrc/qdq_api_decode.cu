@@ -8,15 +8,27 @@ using namespace qdq;
 
 namespace {
 
-// A byte range; rows of `row` bytes `stride` bytes apart count as the whole span.
+// A byte range, or rows of `row` bytes `stride` bytes apart (stride 0: one range).
 struct Span {
   const void *p;
   size_t n;
+  size_t stride = 0, row = 0;
 };
 Span span(const void *p, int64_t rows, int64_t stride, int64_t row, int eb) {
-  return {p, p && rows > 0 ? size_t((rows - 1) * stride + row) * eb : 0};
+  if (!p || rows <= 0) return {p, 0};
+  return {p, size_t((rows - 1) * stride + row) * eb, rows > 1 ? size_t(stride) * eb : 0, size_t(row) * eb};
 }
-bool clash(const Span &a, const Span &b) { return a.p && b.p && overlaps(a.p, a.n, b.p, b.n); }
+// Rows of one stride (or one row among another's) that lie beside one another, as slices of one wide
+// buffer do, do not clash; rows of different strides whose spans overlap count as if they did.
+bool clash(const Span &a, const Span &b) {
+  if (!a.p || !b.p || !overlaps(a.p, a.n, b.p, b.n)) return false;
+  const size_t s = a.stride ? a.stride : b.stride;
+  if (s == 0 || (a.stride && b.stride && a.stride != b.stride)) return true;
+  const size_t la = a.stride ? a.row : a.n, lb = b.stride ? b.row : b.n;
+  const intptr_t off = (reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % intptr_t(s);
+  const size_t d = size_t(off < 0 ? off + intptr_t(s) : off);  // how far b's rows start behind a's
+  return d < la || d + lb > s;
+}
 
 bool dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 

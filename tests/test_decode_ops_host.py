@@ -48,6 +48,19 @@ def test_rms_norm_refusals(qdq):
     assert call(rows=0, o=x, s=r) == qdq.QDQ_OK                  # in place
 
 
+def test_rows_that_overlap_by_one_element_are_refused(qdq):
+    # slices of one wide buffer that share an element, at either end, and rows of different strides among one another
+    n, st = 256, 512
+    norm = qdq.lib().qdq_rms_norm
+    for off, os in ((n - 1, st), (st - n + 1, st), (-(n - 1), st), (-(st - n + 1), st), (1, st), (n, st + 8)):
+        assert norm(_at(0), None, None, None, _at(0) + 4 * off, None, 0, 4, n, st, 0, 0, os, 1e-5, None) == qdq.QDQ_ERR_ALIAS, off
+    attend = qdq.lib().qdq_kv_attention
+    p, t, ln, q, ws = (_at(i) for i in range(1, 6))
+    for off in (252, 260, -252, -260, 4):  # q and out: 256 of 512 elements
+        assert attend(p, 4, 16, 2, 64, t, 3, ln, None, 2, 1, 48, 4, q, 512, q + 4 * off, 512, None, None, 0.125, 0.0, 0, 0, ws, 0,
+                      None) == qdq.QDQ_ERR_ALIAS, off
+
+
 def test_page_bytes(qdq):
     assert qdq.kv_page_bytes(64, 8, 128) == 8 * 16512             # 16384 codes + 32 bytes of scales, to 128
     assert qdq.kv_page_bytes(16, 1, 64) == 2176

@@ -163,6 +163,23 @@ def test_norm_rows_that_are_not_finite_or_zero(cuda_lib):
         assert np.isfinite(got[[0, 1, 3]]).all() and (got[1] == 0).all() and np.isnan(got[2]).all()
 
 
+def test_norm_between_slices_of_one_buffer(cuda_lib):
+    # x, the residual, the sum and the norm beside one another in wide rows
+    import torch
+    rows, n = 700, 264
+    rng = np.random.default_rng(12)
+    for dtype in ("f32", "bf16"):
+        buf = _t(rng.standard_normal((rows, 4 * n + 8)).astype(np.float32), _dt(dtype))
+        before = buf.clone()
+        x, total, out, r = (buf[:, i:i + n] for i in (0, n, 2 * n, 3 * n + 8))
+        y, h = ref.rms_norm(_np(x), _np(r), None, 1e-5)
+        cuda_lib.rms_norm(x, None, out, rows, n, 1e-5, residual=r, sum_out=total)
+        _within(_np(out), y, (64 * U + EPS[dtype]) * np.abs(y))
+        _within(_np(total), h, EPS[dtype] * np.abs(h))
+        for part in (slice(0, n), slice(3 * n, 4 * n + 8)):
+            assert torch.equal(buf[:, part], before[:, part])
+
+
 # ------------------------------------------------------------------ cache
 
 def _pool(n_pages, page, n_kv, dim, seed=0):
@@ -708,6 +725,23 @@ def test_attention_strided_rows(cuda_lib):
     cuda_lib.kv_attention(raw, _i32(table), _i32([130, 70]), q.contiguous(), plain, ws, 4, 2, 64, 32, 130, lse=lse)
     assert torch.equal(out[:, 1:5], plain) and (out[:, 0] == 3).all() and (out[:, 5:] == 3).all()
     _check_attention(c, table, [130, 70], [1, 1], q.contiguous(), plain, lse, "f32", 0.125, 0, 0, None)
+
+
+def test_attention_between_slices_of_one_buffer(cuda_lib):
+    # the queries and the output beside one another in wide rows
+    import torch
+    rng = np.random.default_rng(13)
+    lens = [130, 70, 5]
+    raw, table, c = _filled(rng, lens, 32, 2, 64)
+    wide = _t(rng.standard_normal((3, 11, 64)).astype(np.float32))
+    before = wide.clone()
+    q, out = wide[:, 1:5], wide[:, 6:10]
+    plain = torch.empty(3, 4, 64, device="cuda")
+    ws = cuda_lib.kv_attention_workspace(3, 1, 130, 4, 2, 64)
+    cuda_lib.kv_attention(raw, _i32(table), _i32(lens), q.contiguous(), plain, ws, 4, 2, 64, 32, 130)
+    cuda_lib.kv_attention(raw, _i32(table), _i32(lens), q, out, ws, 4, 2, 64, 32, 130)
+    assert torch.equal(out, plain)
+    assert torch.equal(wide[:, :6], before[:, :6]) and torch.equal(wide[:, 10], before[:, 10])
 
 
 @pytest.mark.usefixtures("attn_kernel")
