@@ -151,12 +151,18 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int row, const float
   }
 }
 
+// The next kernel on the stream may start early, unless a Q8_0 matrix is written: a projection reads its
+// weights ahead of its wait.
+__device__ __forceinline__ void start_next(const NormArgs &a) {
+  if (!a.q8) pdl_launch_dependents();
+}
+
 template <typename T, int V, int E>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
   constexpr int G = E / V;
   __shared__ float part[32];
   const int row = blockIdx.x, n = a.n;
-  pdl_launch_dependents();
+  start_next(a);
   pdl_wait();
   const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
   const T *r = a.residual ? static_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(1024) rms_norm_rows_kernel(const NormArgs a) {
   extern __shared__ uint8_t ring[];
   __shared__ float part[2][32];
   const int n = a.n, tid = threadIdx.x, threads = blockDim.x;
-  pdl_launch_dependents();
+  start_next(a);
   pdl_wait();
   const uint32_t mine = smem_u32(ring) + 16 * tid, group = 16 * threads, slot = (a.residual ? 2 : 1) * G * group;
   auto fetch = [&](int64_t row, int st) {

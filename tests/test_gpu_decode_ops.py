@@ -149,6 +149,37 @@ def test_norm_many_rows(cuda_lib, rows, n, dtype, residual, pad):
         _within(_np(val), y, step.reshape(rows, n) + 64 * U * np.abs(y))
 
 
+@pytest.mark.parametrize("rows,n,dtype", [(1536, 3072, "f32"), (4096, 8192, "bf16"), (256, 1024, "f16"), (20224, 256, "bf16")])
+def test_norm_to_q8_0_is_the_next_calls_matrix(cuda_lib, rows, n, dtype):
+    # the projections read their weights ahead of the wait for the call before: the norm must have written them by then
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = [torch.randn(rows, n, device="cuda", generator=g).to(_dt(dtype)) for _ in range(4)]
+    v = torch.randn(8, n, device="cuda", generator=g)
+    packed = torch.zeros(cuda_lib.q8_0_packed_bytes(rows, n), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(cuda_lib.gemm_batch_workspace_bytes(8, rows, n), dtype=torch.uint8, device="cuda")
+    outs = {"one": torch.empty(1, rows, device="cuda"), "few": torch.empty(3, rows, device="cuda"),
+            "batch": torch.empty(8, rows, device="cuda")}
+
+    def call(how):
+        if how == "batch":
+            cuda_lib.q8_0_gemm_batch(packed, v, outs[how], ws, rows, n, 8)
+        else:
+            cuda_lib.q8_0_gemv(packed, v, outs[how], rows, n, 1 if how == "one" else 3)
+
+    for how, out in outs.items():
+        want = []
+        for xi in x:
+            cuda_lib.rms_norm(xi, None, None, rows, n, q8_out=packed)
+            torch.cuda.synchronize()
+            call(how)
+            want.append(out.clone())
+        for i in range(24):
+            cuda_lib.rms_norm(x[i % 4], None, None, rows, n, q8_out=packed)
+            call(how)
+            assert torch.equal(out, want[i % 4]), (how, i)
+
+
 def test_norm_rows_that_are_not_finite_or_zero(cuda_lib):
     import torch
     x = torch.randn(4, 64, device="cuda")
