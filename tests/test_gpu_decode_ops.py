@@ -493,6 +493,33 @@ def test_attention_sharp_scores_and_uneven_scales(cuda_lib, dtype, nq):
 
 
 @pytest.mark.usefixtures("attn_kernel")
+@pytest.mark.parametrize("heads,nq", [(8, 1), (2, 4)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attention_of_16_bit_calls_with_few_rows_keeps_both_parts(cuda_lib, dtype, heads, nq):
+    # at most 8 rows per cache head: probabilities in two f16 parts, so no 2^-11 sum p|v| in the bound; values that
+    # nearly cancel, where one part alone would show
+    rng = np.random.default_rng(14)
+    lens, n_kv, dim = [4, 36, 200], 1, 64
+    raw, table, c = _filled(rng, lens, 32, n_kv, dim)
+    for s, n in enumerate(lens):
+        for b in range(-(-n // 16)):
+            pid, t0 = table[s, b * 16 // 32], b * 16 % 32
+            v = c._codes(pid, 0, 1)[t0:t0 + 16]
+            v[1::2] = -v[::2]
+            c._scales(pid, 0, 1)[t0 // 16] = 0.02
+    raw = _t(c.raw)
+    q = _t(0.02 * rng.standard_normal((3 * nq, heads, dim)).astype(np.float32), _dt(dtype))
+    out, lse = _attend(cuda_lib, raw, table, lens, [nq] * 3, q, heads, n_kv, dim, 32)
+    qn, on = _np(q), _np(out)
+    for s, n in enumerate(lens):
+        k, v = _values(c, table, s, n)
+        o, _, av, mag, z = ref.attention(qn[s * nq:(s + 1) * nq], k, v, n - nq + np.arange(nq), 0.125)
+        d = 2.0 ** -18 * mag + 2.0 ** -20
+        _within(on[s * nq:(s + 1) * nq], o, (2 * d + 2.0 ** -17)[..., None] * av + EPS[dtype] * np.abs(o) + 2.0 ** -39 * 127 * n * z[..., None]
+                + (2.0 ** -25 if dtype == "f16" else 0))
+
+
+@pytest.mark.usefixtures("attn_kernel")
 @pytest.mark.parametrize("nq", [1, 140])
 def test_attention_rows_that_see_nothing(cuda_lib, nq):
     # more queries than tokens: the first rows stand before the sequence
