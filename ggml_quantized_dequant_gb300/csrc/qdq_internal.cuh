@@ -180,6 +180,9 @@ int read_checks_xs();
 int read_checks_gemm();
 int read_checks_topk();
 int read_checks_q6k();
+int read_checks_attn();
+int read_checks_attn_tc();
+int read_checks_logprobs();
 
 // A logit and its index as a 64-bit key whose unsigned order is the top-k order: a
 // NaN above every number, then larger values, equal values (+0 = -0) by smaller

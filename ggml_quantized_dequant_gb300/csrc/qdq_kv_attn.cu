@@ -251,6 +251,8 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
   const bool bad = me.bad;
   const int b_lo = me.b_lo, b_hi = me.b_lo + me.nb;
   const int c0 = b_lo + split * per, cn = max(0, min(per, b_hi - c0));
+  if (!QDQ_GUARD(cn <= max_split_blocks(W) && nsplit <= max_splits(W), QDQ_CHECK_SMEM)) return;
+  if (nsplit > 1 && !QDQ_GUARD((first + nsplit) * (R * (D + 2)) <= a.room && unit < a.units, QDQ_CHECK_OUT)) return;
 
   // where the blocks of this split are
   const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
@@ -806,6 +808,8 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.slopes = slopes;
   a.tickets = static_cast<uint32_t *>(workspace);
   a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes));
+  a.room = int64_t((workspace_bytes - workspace_tickets(workspace_bytes)) / 4);
+  a.units = p.units;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.n_seqs = n_seqs;
@@ -846,5 +850,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }
+
+QDQ_CHECK_READER(read_checks_attn)
 
 }  // namespace qdq

@@ -306,6 +306,10 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       h = u.h;
       c0 = en.b_lo + 4 * u.t0;
       cn = max(0, min(4 * (u.t1 - u.t0), en.b_hi - c0));
+      if (!QDQ_GUARD(cn <= kTcSplitBlocks, QDQ_CHECK_SMEM)) break;
+      if (u.nsplit > 1 && !QDQ_GUARD(int64_t(2) * (u.c_lo + u.nsplit) * (R * (D + 2)) <= a.room &&
+                                         int64_t(bars.entry) * a.c.n_kv + h < a.units, QDQ_CHECK_OUT))
+        break;
     }
     const int nt = (cn + 3) / 4;
 
@@ -1106,6 +1110,8 @@ cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, int group
     default: return parts == 1 ? run<256, 1>(a, groups, s) : cudaErrorInvalidValue;
   }
 }
+
+QDQ_CHECK_READER(read_checks_attn_tc)
 
 int read_attn_tc_timeouts() {
   unsigned int v = 0, zero = 0;

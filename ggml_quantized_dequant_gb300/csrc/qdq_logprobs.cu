@@ -48,6 +48,7 @@ struct LpArgs {
   uint32_t *tickets;
   uint8_t *partial;  // [row][segment] { float M, l, u, pad; uint64 keys[k] }
   int n, k, segs, seg_tiles;
+  int64_t room, rows;  // bytes of the workspace's parts, rows (read by the debug build's guards)
 };
 
 // Bytes of a segment's partial result, a multiple of 16.
@@ -332,7 +333,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
           for (int j = 1; j < kPer; ++j) x = i == j ? v[j] : x;
           const int e = base + ((i / V) * kThreads + tid) * V + i % V;
           const uint64_t key = topk_key(x, uint32_t(e - shift));
-          if (e >= lo && e < hi && key > bound) list[atomicAdd(&sh.fill[warp], 1)] = key;
+          if (e >= lo && e < hi && key > bound) {
+            const int at = atomicAdd(&sh.fill[warp], 1);
+            if (QDQ_GUARD(at < kList, QDQ_CHECK_SMEM)) list[at] = key;
+          }
         }
         __syncwarp();
         const int fill = *reinterpret_cast<volatile int *>(&sh.fill[warp]);
@@ -401,6 +405,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
 
   if (a.segs > 1) {
     const size_t part = part_bytes(k);
+    if (!QDQ_GUARD(int64_t((size_t(row) + 1) * a.segs * part) <= a.room && row < a.rows, QDQ_CHECK_OUT)) return;
     uint8_t *mine = a.partial + (size_t(row) * a.segs + seg) * part;
     if (tid == 0) {
       float *f = reinterpret_cast<float *>(mine);
@@ -535,7 +540,8 @@ int launch_token_logprobs(const void *logits, int64_t stride, int type, const in
   const Plan p = plan(di, rows, n, k);
   if (int64_t(rows) * p.segs > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
   const LpArgs a{logits, stride, tokens, logprob, entropy, top_logprob, top_index, static_cast<uint32_t *>(workspace),
-                 static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes), n, k, p.segs, p.seg_tiles};
+                 static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes), n, k, p.segs, p.seg_tiles,
+                 int64_t(workspace_bytes - workspace_tickets(workspace_bytes)), rows};
   e = cudaError_t(with_type(type, [&](auto t) {
     const auto kernel = logprobs_kernel<decltype(t)>;
     const cudaError_t r = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(sizeof(Shared)));
@@ -544,5 +550,7 @@ int launch_token_logprobs(const void *logits, int64_t stride, int type, const in
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }
+
+QDQ_CHECK_READER(read_checks_logprobs)
 
 }  // namespace qdq
