@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(W * 32, (D <= 128 ? 16 : 8) / W) kv_attn_kerne
     x.q0 = a.cu_q ? int(ld_u1(a.cu_q + s)) : s;
     x.nq = a.cu_q ? int(ld_u1(a.cu_q + s + 1)) - x.q0 : 1;
     x.len = int(ld_u1(a.kv_len + s));
-    const int r0 = tile * R, rows = min(x.nq, a.max_q) * a.group;
-    x.nr = min(R, rows - r0);
+    const int r0 = tile * R, rows = x.nq * a.group;
+    x.nr = min(min(R, a.max_rows - r0), rows - r0);
     x.bad = x.len < 0 || x.len > a.max_kv_len || (x.len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride;
     const int pos_lo = x.len - x.nq + int(a.query_of(r0)), pos_hi = x.len - x.nq + int(a.query_of(r0 + max(x.nr, 1) - 1));
     x.b_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) / kKvBlock : 0;
@@ -814,6 +814,7 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   a.out_stride = out_stride;
   a.n_seqs = n_seqs;
   a.max_q = max_q;
+  a.max_rows = max_q * (n_heads / c.n_kv);
   a.max_kv_len = max_kv_len;
   a.n_heads = n_heads;
   a.group = n_heads / c.n_kv;

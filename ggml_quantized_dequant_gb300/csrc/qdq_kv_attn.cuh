@@ -25,7 +25,8 @@ struct AttnArgs {
   float *partial;
   int64_t q_stride, out_stride;
   int64_t room, units;  // floats of the workspace's parts, tickets that are used (read by the debug build's guards)
-  int n_seqs, max_q, max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
+  int n_seqs, max_q, max_rows;  // max_rows: the rows of max_q queries of one cache head
+  int max_kv_len, n_heads, group, tiles, splits, split_blocks, window, type;
   int entries;  // decode kernel: sequences times tiles where the splits' length is chosen on the device, else 0
   float scale, softcap, inv_cap, inv_splits;  // 1 / softcap, 1 / splits
   uint64_t group_mul;  // ceil(2^40 / group)
