@@ -8,6 +8,8 @@ using namespace qdq;
 
 namespace {
 
+// A NULL pointer is refused only where the call has something to do: an empty tensor's is NULL.
+
 // A byte range, or rows of `row` bytes `stride` bytes apart (stride 0: one range).
 struct Span {
   const void *p;
@@ -33,8 +35,8 @@ bool clash(const Span &a, const Span &b) {
 bool dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 
 int check_pool(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *table,
-               int table_stride, int n_seqs) {
-  if (!pages || !table) return QDQ_ERR_NULL;
+               int table_stride, int n_seqs, bool nothing) {
+  if (!nothing && (!pages || !table)) return QDQ_ERR_NULL;
   if (n_pages < 1 || page_tokens < QDQ_KV_BLOCK || page_tokens % QDQ_KV_BLOCK || n_kv < 1 || head_dim < 1 ||
       table_stride < 1 || n_seqs < 0)
     return QDQ_ERR_DIMS;
@@ -58,7 +60,7 @@ extern "C" {
 int qdq_rms_norm(const void *x, const void *residual, const float *weight, void *sum_out, void *out, void *q8_out,
                  int type, int rows, int n, long long x_stride, long long residual_stride, long long sum_stride,
                  long long out_stride, float eps, cudaStream_t stream) {
-  if (!x || (!out && !q8_out)) return QDQ_ERR_NULL;
+  if (rows != 0 && (!x || (!out && !q8_out))) return QDQ_ERR_NULL;
   if (!type_ok(type) || rows < 0 || n < 1 || !(eps >= 0.f) || (q8_out && n % 32)) return QDQ_ERR_DIMS;
   if (x_stride < n || (residual && residual_stride < n) || (sum_out && sum_stride < n) || (out && out_stride < n))
     return QDQ_ERR_DIMS;
@@ -93,14 +95,15 @@ size_t qdq_kv_page_bytes(int page_tokens, int n_kv, int head_dim) {
 int qdq_kv_append(void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
                   int table_stride, const int *kv_len, const int *cu_new, int n_seqs, int max_new, const void *k,
                   const void *v, long long k_stride, long long v_stride, int type, cudaStream_t stream) {
-  if (!kv_len || !k || !v) return QDQ_ERR_NULL;
-  int rc = check_pool(pages, n_pages, page_tokens, n_kv, head_dim, page_table, table_stride, n_seqs);
+  const bool nothing = n_seqs == 0 || max_new == 0;
+  if (!nothing && (!kv_len || !k || !v)) return QDQ_ERR_NULL;
+  int rc = check_pool(pages, n_pages, page_tokens, n_kv, head_dim, page_table, table_stride, n_seqs, nothing);
   if (rc != QDQ_OK) return rc;
   if (!type_ok(type) || max_new < 0 || (!cu_new && max_new != 1)) return QDQ_ERR_DIMS;
   if (!aligned(kv_len, 4) || !aligned(cu_new, 4)) return QDQ_ERR_ALIGN;
   const int64_t width = int64_t(n_kv) * head_dim;
   if ((rc = check_rows(k, k_stride, width, type)) != QDQ_OK || (rc = check_rows(v, v_stride, width, type)) != QDQ_OK) return rc;
-  if (n_seqs == 0 || max_new == 0) return QDQ_OK;
+  if (nothing) return QDQ_OK;
   const Span sp{pages, size_t(n_pages) * page_bytes(page_tokens, n_kv, head_dim)};
   const int eb = type_bytes(type);  // at least one row of k and v per call is known to the host
   if (clash(sp, span(k, cu_new ? 1 : n_seqs, k_stride, width, eb)) || clash(sp, span(v, cu_new ? 1 : n_seqs, v_stride, width, eb)) ||
@@ -114,14 +117,15 @@ int qdq_kv_append(void *pages, int n_pages, int page_tokens, int n_kv, int head_
 int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
                 int table_stride, const int *start, const int *cu, int n_seqs, int max_tokens, void *k, void *v,
                 long long k_stride, long long v_stride, int type, cudaStream_t stream) {
-  if (!cu || !k || !v) return QDQ_ERR_NULL;
-  int rc = check_pool(pages, n_pages, page_tokens, n_kv, head_dim, page_table, table_stride, n_seqs);
+  const bool nothing = n_seqs == 0 || max_tokens == 0;
+  if (!nothing && (!cu || !k || !v)) return QDQ_ERR_NULL;
+  int rc = check_pool(pages, n_pages, page_tokens, n_kv, head_dim, page_table, table_stride, n_seqs, nothing);
   if (rc != QDQ_OK) return rc;
   if (!type_ok(type) || max_tokens < 0) return QDQ_ERR_DIMS;
   if (!aligned(start, 4) || !aligned(cu, 4)) return QDQ_ERR_ALIGN;
   const int64_t width = int64_t(n_kv) * head_dim;
   if ((rc = check_rows(k, k_stride, width, type)) != QDQ_OK || (rc = check_rows(v, v_stride, width, type)) != QDQ_OK) return rc;
-  if (n_seqs == 0 || max_tokens == 0) return QDQ_OK;
+  if (nothing) return QDQ_OK;
   const Span sp{pages, size_t(n_pages) * page_bytes(page_tokens, n_kv, head_dim)};
   const int eb = type_bytes(type);
   const Span sk = span(k, 1, k_stride, width, eb), sv = span(v, 1, v_stride, width, eb);
@@ -145,8 +149,9 @@ int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, 
                      int n_heads, const void *q, long long q_stride, void *out, long long out_stride, float *lse,
                      const float *slopes, float scale, float softcap, int window, int type, void *workspace,
                      size_t workspace_bytes, cudaStream_t stream) {
-  if (!kv_len || !q || !out || !workspace) return QDQ_ERR_NULL;
-  int rc = check_pool(pages, n_pages, page_tokens, n_kv, head_dim, page_table, table_stride, n_seqs);
+  const bool nothing = n_seqs == 0 || max_q == 0;
+  if (!nothing && (!kv_len || !q || !out || !workspace)) return QDQ_ERR_NULL;
+  int rc = check_pool(pages, n_pages, page_tokens, n_kv, head_dim, page_table, table_stride, n_seqs, nothing);
   if (rc != QDQ_OK) return rc;
   if (!type_ok(type) || max_q < 0 || (!cu_q && max_q != 1) || max_kv_len < 0 || n_heads < 1 || n_heads % n_kv || window < 0 ||
       !std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
@@ -156,7 +161,7 @@ int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, 
     return QDQ_ERR_ALIGN;
   const int64_t width = int64_t(n_heads) * head_dim;
   if ((rc = check_rows(q, q_stride, width, type)) != QDQ_OK || (rc = check_rows(out, out_stride, width, type)) != QDQ_OK) return rc;
-  if (n_seqs == 0 || max_q == 0) return QDQ_OK;
+  if (nothing) return QDQ_OK;
   const int64_t known = cu_q ? 1 : n_seqs;  // query rows the host can count on
   const int eb = type_bytes(type);
   const Span so = span(out, known, out_stride, width, eb), sl = span(lse, known, n_heads, n_heads, 4);
@@ -185,7 +190,7 @@ size_t qdq_token_logprobs_workspace_bytes(int rows, int n, int k) {
 int qdq_token_logprobs(const void *logits, long long row_stride, int type, const int *tokens, int rows, int n, int k,
                        float *logprob, float *entropy, int *top_index, float *top_logprob, void *workspace,
                        size_t workspace_bytes, cudaStream_t stream) {
-  if (!logits || !workspace || !tokens != !logprob || (k > 0 && (!top_index || !top_logprob))) return QDQ_ERR_NULL;
+  if (rows != 0 && (!logits || !workspace || !tokens != !logprob || (k > 0 && (!top_index || !top_logprob)))) return QDQ_ERR_NULL;
   if (!type_ok(type) || rows < 0 || n < 1 || k < 0 || k > n || row_stride < n) return QDQ_ERR_DIMS;
   if (k > QDQ_MAX_TOPK || n > (1 << 30)) return QDQ_ERR_UNSUPPORTED;
   const int eb = type_bytes(type);

@@ -61,6 +61,24 @@ def test_rows_that_overlap_by_one_element_are_refused(qdq):
                       None) == qdq.QDQ_ERR_ALIAS, off
 
 
+def test_nothing_to_do_needs_no_pointers(qdq):
+    # no rows, sequences, tokens or queries: OK whatever the (empty) tensors' addresses; other arguments are still checked
+    lib, ok = qdq.lib(), qdq.QDQ_OK
+    assert lib.qdq_rms_norm(None, None, None, None, None, None, 0, 0, 64, 64, 0, 0, 0, 1e-5, None) == ok
+    assert lib.qdq_rms_norm(None, None, None, None, None, None, 3, 0, 64, 64, 0, 0, 0, 1e-5, None) == qdq.QDQ_ERR_DIMS
+    for seqs, most in ((0, 5), (2, 0)):
+        for f in (lib.qdq_kv_append, lib.qdq_kv_read):
+            assert f(_at(0), 4, 16, 2, 64, _at(1), 3, None, _at(2), seqs, most, None, None, 128, 128, 0, None) == ok
+            assert f(None, 4, 16, 2, 64, None, 3, None, _at(2), seqs, most, None, None, 128, 128, 0, None) == ok
+            assert f(None, 4, 24, 2, 64, None, 3, None, _at(2), seqs, most, None, None, 128, 128, 0, None) == qdq.QDQ_ERR_DIMS
+        assert lib.qdq_kv_attention(None, 4, 16, 2, 64, None, 3, None, _at(2), seqs, most, 48, 4, None, 256, None, 256, None, None,
+                                    0.125, 0.0, 0, 0, None, 0, None) == ok
+        assert lib.qdq_kv_attention(None, 4, 16, 2, 64, None, 3, None, _at(2), seqs, most, 48, 3, None, 256, None, 256, None, None,
+                                    0.125, 0.0, 0, 0, None, 0, None) == qdq.QDQ_ERR_DIMS
+    assert lib.qdq_token_logprobs(None, 1000, 0, _at(0), 0, 1000, 5, None, None, None, None, None, 0, None) == ok
+    assert lib.qdq_token_logprobs(None, 1000, 0, _at(0), 0, 1000, 1001, None, None, None, None, None, 0, None) == qdq.QDQ_ERR_DIMS
+
+
 def test_page_bytes(qdq):
     assert qdq.kv_page_bytes(64, 8, 128) == 8 * 16512             # 16384 codes + 32 bytes of scales, to 128
     assert qdq.kv_page_bytes(16, 1, 64) == 2176

@@ -925,6 +925,29 @@ def test_logprobs_rows_past_32_bits(cuda_lib):
 
 # ------------------------------------------------------------------ together
 
+def test_empty_tensors(cuda_lib):
+    # no rows, no sequences, no queries: nothing to do, and nothing to refuse
+    import torch
+
+    def f(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+
+    none, table, pages = f(0, 128), f(2, 3, dtype=torch.int32), cuda_lib.kv_pages(4, 16, 2, 64)
+    cuda_lib.rms_norm(none, None, f(0, 128), 0, 128, residual=f(0, 128), sum_out=f(0, 128))
+    cuda_lib.rms_norm(none, f(128), None, 0, 128, q8_out=f(0, dtype=torch.uint8))
+    before = pages.clone()
+    for tab, lens, most in ((table, _i32([0, 0]), 0), (table[:0], _i32([]), 1)):
+        cu = _i32([0] * (len(tab) + 1))
+        cuda_lib.kv_append(pages, tab, lens, none, none, 2, 64, 16, cu_new=cu, max_new=most)
+        cuda_lib.kv_read(pages, tab, None, cu, f(0, 128), f(0, 128), 2, 64, 16, most)
+        ws = cuda_lib.kv_attention_workspace(len(tab), most, 48, 2, 2, 64)
+        cuda_lib.kv_attention(pages, tab, lens, none, f(0, 128), ws, 2, 2, 64, 16, 48, cu_q=cu, max_q=most, lse=f(0, 2))
+    cuda_lib.token_logprobs(f(0, 500), _i32([]), f(0), f(0), 0, 500, cuda_lib.token_logprobs_workspace(0, 500, 3), 3,
+                            f(0, 3, dtype=torch.int32), f(0, 3))
+    torch.cuda.synchronize()
+    assert torch.equal(pages, before)
+
+
 def test_operators_on_a_stream_of_their_own_in_a_graph(cuda_lib):
     # the decode chain captured into a CUDA graph on a side stream gives what the calls give
     import torch
