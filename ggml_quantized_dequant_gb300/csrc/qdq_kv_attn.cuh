@@ -51,7 +51,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // tanh(x) = 1 - 2 / (1 + e^2x), off by 2^-21 at most; with kSmall (f32 activations) also to a few 1e-7
-// relative near 0: below 1/4 the Taylor series (its next term is 6e-8 of the value there).  (tanhf took twice
+// relative near 0: below 1/4 the Taylor series (its next term is 1e-8 of the value there).  (tanhf took twice
 // the instructions, a third of a capped call.)
 template <bool kSmall>
 __device__ __forceinline__ float tanh_of(float x) {

@@ -11,7 +11,9 @@
 // One CTA per row, or, for many wide or many short rows, CTAs that take row after row through a ring
 // (the rule stands at the launch).  Sums are f32.
 // Measured: one row of 3072 f32 1.8 us; 4096 rows of 8192 bf16 with residual 43 us (6.2 TB/s, 92 % of a
-// plain copy's rate); 1500 rows of 3072 f32 with residual to f32 and Q8_0 14.4 us (5.5 TB/s).
+// plain copy's rate); 1500 rows of 3072 f32 with residual to f32 and Q8_0 14.7 us (5.3 TB/s, its inputs partly in L2), to Q8_0
+// alone 12.8 us (4.7 TB/s: by their 41 registers three of the CTAs of 384 threads fit an SM, and 1500 rows are 3.3 rounds
+// of them).  Rows that are not aligned go element by element (4096 rows of 8193 bf16 273 us, above 8192 elements with spills).
 #include "qdq_types.cuh"
 
 namespace qdq {
@@ -322,8 +324,9 @@ int launch_rms_norm(const void *x, const void *residual, const float *weight, vo
       // the fewest elements per thread that a CTA can hold: at 4096 rows of 8192 (bf16, residual, a CTA
       // each) 8, 16 and 32 per thread took 47.4, 52.8 and 55.2 us, one row of 3072 1.9, 2.1 and 3.6 us
       if constexpr (V * sizeof(T) == 16) {
-        // Rows through a ring where only two CTAs of one row each fit an SM (they wait on barriers and memory
-        // by turns; 4096 rows of 8192 bf16 with residual 47.2 -> 43.0 us, f32 without 48.2 -> 42.9 us) and
+        // Rows through a ring where by their threads only two CTAs of one row each fit an SM (they wait on barriers and
+        // memory by turns; 4096 rows of 8192 bf16 with residual 47.2 -> 43.0 us, f32 without 48.2 -> 42.9 us; of the
+        // ring's CTAs of 1024 threads at 50 to 57 registers one is on an SM at a time, so they come in two rounds) and
         // shared memory has room for two as well (f32 with residual: one, 78 -> 89 us), or where a row is
         // moved in less time than a CTA is started (60000 rows of 256 bf16: 60.6 -> 21.3 us, 30000 of 512
         // 30.6 -> 20.1 us).  Between, small CTAs hide each other's barriers (8192 rows of 4096 bf16: 41.4, ring 44.0 us).

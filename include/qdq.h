@@ -87,7 +87,7 @@ extern "C" {
 #define QDQ_ERR_UNSUPPORTED -4  /* valid arguments this build does not handle (e.g. n_in too large) */
 #define QDQ_ERR_CUDA        -5  /* a CUDA runtime call failed; see qdq_last_cuda_error() */
 #define QDQ_ERR_ALIAS       -6  /* an output overlaps an input it may not overlap */
-#define QDQ_ERR_SCRATCH     -7  /* the request does not fit the library's fixed scratch array */
+#define QDQ_ERR_SCRATCH     -7  /* the request does not fit the library's fixed scratch array, or the workspace's bytes */
 
 /* Human-readable name of a status code (static string). */
 const char *qdq_status_string(int status);
@@ -298,8 +298,11 @@ int qdq_q4k_swiglu_batch(const void *Wg, const void *Wu, const float *X, float *
  * No counterpart on the reference pages (their attention, cache and norm live in another
  * engine): the operators that a model's layer needs between the projections above.
  * Activations are f32, f16 or bf16 (QDQ_TYPE_*); all sums, maxima and softmax
- * statistics are f32, and an output is rounded once to its type.  Strides count
- * elements between consecutive rows (tokens).
+ * statistics are f32, and an output is rounded once to its type (attention rounds more for 16-bit types: below).
+ * Strides count elements between consecutive rows (tokens).  Rows of one stride may lie beside one another, as slices of
+ * one wide buffer do; of operands with different strides the whole spans may not overlap.  Where an int array on the
+ * device (cu_new, cu, cu_q) says how many rows there are, the host compares the first row alone.
+ * Norm weights and slopes count as weights: a kernel may read them while an earlier call of this library still runs.
  */
 #define QDQ_TYPE_F32  0
 #define QDQ_TYPE_F16  1
@@ -313,7 +316,8 @@ int qdq_q4k_swiglu_batch(const void *Wg, const void *Wu, const float *X, float *
  * out (may be NULL): y in the type.  q8_out (may be NULL; n % 32 == 0, 16-byte aligned):
  * y as a packed Q8_0 matrix of rows x n (qdq_q8_0_packed_bytes(rows, n) bytes, layout
  * above): d = f16(max |y| / 127) over each 32, code = rint(y * (1 / d)) within
- * +-127, 0 where d is 0; a block with a NaN has d = NaN.  out or q8_out is given.
+ * +-127, 0 where d is 0; a block with a NaN has d = NaN.  (The rounded d is divided by, so a code can differ by one
+ * from a quantiser that divides by the unrounded one.)  The next call may take q8_out as its W.  out or q8_out is given.
  * x, residual, sum_out and out are aligned to their elements and weight to 4 bytes (16-byte
  * aligned rows are faster); strides are at least n.  sum_out may be exactly residual or x, and out exactly x
  * or residual (with its stride); outputs may overlap nothing else.
@@ -367,7 +371,12 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
  *   slopes (n_heads f32, may be NULL): x[j] -= slopes[h] * (pos - j);
  *   visible: j <= pos, and pos - j < window when window > 0;
  *   out = sum_j softmax(x)[j] v[j],  lse (n_heads f32 per query row, may be NULL) = log sum_j e^x[j].
- * A row that sees no token gives zeros and lse -inf.  A sequence with kv_len outside [0,
+ * Rounding: with f32 activations, and with 16-bit ones where max_q * (n_heads / n_kv) <= 8, the probabilities times
+ * their value scales keep 2^-22 (two f16 parts); with 16-bit ones and more rows they are rounded to f16 once (2^-11, as an f16
+ * output), and query elements 2^-25 below their row's largest count as 0.  So a token's result moves within that when
+ * it is computed with others instead of alone.  With 16-bit activations the cap's tanh is off by up to 2^-21, times softcap.
+ * A row that sees no token gives zeros and lse -inf.  A value scale of 2^118 and more (values from 4e37) gives NaN.
+ * A sequence with kv_len outside [0,
  * max_kv_len] or past its table row gives NaN, and so does a row that sees a token
  * with an invalid page or a NaN scale, and a query that is not finite.
  * max_kv_len, max_q: a call is cut into CTAs by them (and the workspace sized), so bounds near the lengths are faster.
@@ -378,7 +387,8 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
  * workspace: qdq_kv_attention_workspace_bytes(...) bytes (0 when no device can be queried), 256-byte aligned, ZEROED ONCE by
  * the caller before its first use; a call leaves it ready for the next one on the same stream, also one of
  * other sizes, types or windows, or of qdq_token_logprobs, that is given the same workspace and workspace_bytes.
- * Results do not depend on the order in which CTAs run.
+ * Results do not depend on the order in which CTAs run; the last bits of a row do on the lengths of all sequences of
+ * the call, which decide where its sums are cut.
  */
 #define QDQ_MAX_KV_LEN 4194304   /* the largest max_kv_len */
 size_t qdq_kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
@@ -413,8 +423,8 @@ int qdq_pipeline_timeouts(void);
 
 /* ---- debug build: device-side guards ----------------------------------------
  * A library built with -DQDQ_CHECKS (ggml_quantized_dequant_gb300._build.build(checks=True),
- * libqdq_checked.so) guards its shared-memory row buffers, weight-row and
- * activation indices, output indices and bulk-copy alignment inside the kernels:
+ * libqdq_checked.so) guards its shared-memory row buffers, blocks and lists, weight-row and
+ * activation indices, output and workspace indices and bulk-copy alignment inside the kernels:
  * an index out of bounds skips that access and sets a bit of a device status word
  * (QDQ_CHECK_* in the library's internal header: 1 shared memory, 2 weight row,
  * 4 output, 8 copy alignment) instead of trapping.  qdq_check_status waits for the
