@@ -372,9 +372,10 @@ int qdq_kv_read(const void *pages, int n_pages, int page_tokens, int n_kv, int h
  *   visible: j <= pos, and pos - j < window when window > 0;
  *   out = sum_j softmax(x)[j] v[j],  lse (n_heads f32 per query row, may be NULL) = log sum_j e^x[j].
  * Rounding: with f32 activations, and with 16-bit ones where max_q * (n_heads / n_kv) <= 8, the probabilities times
- * their value scales keep 2^-22 (two f16 parts); with 16-bit ones and more rows they are rounded to f16 once (2^-11, as an f16
- * output), and query elements 2^-25 below their row's largest count as 0.  So a token's result moves within that when
- * it is computed with others instead of alone.  With 16-bit activations the cap's tanh is off by up to 2^-21, times softcap.
+ * their value scales keep 2^-22 (two f16 parts, which end 2^-35 below the row's largest).  With 16-bit ones and more rows
+ * they are rounded to f16 once (2^-11, as an f16 output), and query elements 2^-25 below their row's largest count
+ * as 0; so a token's result moves within that when it is computed with others instead of alone.  With 16-bit
+ * activations the cap's tanh is off by up to 2^-21, times softcap.
  * A row that sees no token gives zeros and lse -inf.  A value scale of 2^118 and more (values from 4e37) gives NaN.
  * A sequence with kv_len outside [0,
  * max_kv_len] or past its table row gives NaN, and so does a row that sees a token
