@@ -30,6 +30,7 @@ QDQ_MAX_GEMV_N_IN = 32768
 QDQ_MAX_NORM_N = 32768
 QDQ_KV_BLOCK = 16
 QDQ_MAX_KV_LEN = 4194304
+QDQ_MAX_TREE = 64
 QDQ_TYPE_F32 = 0
 QDQ_TYPE_F16 = 1
 QDQ_TYPE_BF16 = 2
@@ -92,6 +93,15 @@ SIGNATURES = {
                             _c_vp]),
     "qdq_token_logprobs_workspace_bytes": (_c_size, [_c_int] * 3),
     "qdq_token_logprobs": (_c_int, [_c_vp, _c_ll, _c_int, _c_vp, _c_int, _c_int, _c_int] + [_c_vp] * 5 + [_c_size, _c_vp]),
+    "qdq_kv_append_rope": (_c_int, [_c_vp] + [_c_int] * 4 + [_c_vp, _c_int] + [_c_vp] * 3 + [_c_int] * 3 + [_c_vp, _c_ll] * 4
+                           + [_c_vp, _c_vp, _c_float, _c_vp] + [_c_int] * 3 + [_c_vp]),
+    "qdq_kv_tree_attention": (_c_int, [_c_vp] + [_c_int] * 4 + [_c_vp, _c_int] + [_c_vp] * 3 + [_c_int] * 4
+                              + [_c_vp, _c_ll, _c_vp, _c_ll, _c_vp, _c_vp, _c_float, _c_float, _c_int, _c_int, _c_vp, _c_size,
+                                 _c_vp]),
+    "qdq_verify_drafts_workspace_bytes": (_c_size, [_c_int] * 3),
+    "qdq_verify_drafts": (_c_int, [_c_vp, _c_ll, _c_int] + [_c_vp] * 3 + [_c_int] * 3 + [_c_vp, _c_ll, _c_vp, _c_float]
+                          + [_c_vp] * 4 + [_c_size, _c_vp]),
+    "qdq_kv_keep": (_c_int, [_c_vp] + [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp]),
     "qdq_pipeline_timeouts": (_c_int, []),
     "qdq_noop": (_c_int, [_c_vp]),
     "qdq_check_status": (_c_int, []),
@@ -331,11 +341,15 @@ def set_option(key: int, value: int) -> int:
 _types = {}  # torch dtype -> QDQ_TYPE_*; filled at the first use, when torch is there
 
 
-def _type(t) -> int:
+def _type_names():
     if not _types:
         import torch
-        _types.update({torch.float32: QDQ_TYPE_F32, torch.float16: QDQ_TYPE_F16, torch.bfloat16: QDQ_TYPE_BF16})
         _of["int32"], _of["float32"] = torch.int32, torch.float32
+        _types.update({torch.float32: QDQ_TYPE_F32, torch.float16: QDQ_TYPE_F16, torch.bfloat16: QDQ_TYPE_BF16})
+
+
+def _type(t) -> int:
+    _type_names()
     v = _types.get(t.dtype)
     if v is None:
         raise TypeError("float32, float16 or bfloat16 expected, got %s" % t.dtype)
@@ -366,7 +380,8 @@ def _bind_fast():
         _fast_lib = False
         return
     m.bind(*[ctypes.cast(getattr(handle, f), ctypes.c_void_p).value for f in (
-        "qdq_rms_norm", "qdq_kv_append", "qdq_kv_read", "qdq_kv_attention", "qdq_token_logprobs")],
+        "qdq_rms_norm", "qdq_kv_append", "qdq_kv_read", "qdq_kv_attention", "qdq_token_logprobs", "qdq_kv_append_rope",
+        "qdq_kv_tree_attention", "qdq_verify_drafts", "qdq_kv_keep")],
         torch.float32, torch.float16, torch.bfloat16, torch.int32)
     _fast = m  # before _fast_lib, which sends other threads' calls to it
     _fast_lib = handle
@@ -583,6 +598,133 @@ def token_logprobs(logits, tokens, logprob, entropy, rows: int, n: int, workspac
         _vec("top_logprob", top_logprob, "float32", rows * k), _bytes("workspace", workspace), workspace.nbytes, _stream(stream))
     if status != QDQ_OK:
         raise QdqError("qdq_token_logprobs", status)
+
+
+# ---------------------------------------------------------------- drafted tokens
+# (several tokens of a sequence in one step; a tree is each row's parent, an earlier row of its sequence or -1)
+
+def kv_append_rope(pages, page_table, kv_len, q, q_out, k, v, n_heads: int, n_kv: int, head_dim: int, page_tokens: int, freqs=None,
+                   interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6, cu_new=None, max_new: int = 1,
+                   parent=None, stream=None):
+    """Norm (where weights are given) and turn new tokens' queries into ``q_out`` and keys, and append keys and values to
+    the cache as :func:`kv_append` does.
+
+    ``freqs`` (radians per position and pair) turns the first ``2 * len(freqs)`` elements of a head, pairs
+    ``(i, i + len(freqs))`` or, ``interleaved``, ``(2i, 2i + 1)``; ``parent`` gives drafted tokens their positions in a tree."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.kv_append_rope(pages, page_table, kv_len, q, q_out, k, v, n_heads, n_kv, head_dim, page_tokens, freqs,
+                                      interleaved, q_weight, k_weight, eps, cu_new, max_new, parent, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_kv_append_rope", status)
+    ty, w = _type(k), n_kv * head_dim
+    pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
+    least = seqs if cu_new is None else 0  # else the device knows how many rows there are
+    qp, qs = _rows("q", q, n_heads * head_dim, k.dtype, least)
+    op, os_ = _rows("q_out", q_out, n_heads * head_dim, k.dtype, least)
+    kp, ks = _rows("k", k, w, k.dtype, least)
+    vp, vs = _rows("v", v, w, k.dtype, least)
+    fp = _vec("freqs", freqs, "float32")
+    status = lib().qdq_kv_append_rope(
+        pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32", seqs),
+        _vec("cu_new", cu_new, "int32", seqs + 1), _vec("parent", parent, "int32", least), seqs, max_new, n_heads, qp, qs, op, os_,
+        kp, ks, vp, vs, _vec("q_weight", q_weight, "float32", head_dim), _vec("k_weight", k_weight, "float32", head_dim), eps, fp,
+        0 if freqs is None else 2 * freqs.numel(), int(bool(interleaved)), ty, _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_kv_append_rope", status)
+
+
+def kv_tree_attention(pages, page_table, kv_len, q, out, workspace, n_heads: int, n_kv: int, head_dim: int, page_tokens: int,
+                      max_kv_len: int, cu_q, max_q: int, parent, scale: float | None = None, softcap: float = 0.0,
+                      window: int = 0, slopes=None, lse=None, stream=None):
+    """Attention of each sequence's tree of drafted tokens: a row sees the tokens cached before the tree, its ancestors
+    and itself.  ``workspace`` and the other arguments are those of :func:`kv_attention`."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.kv_tree_attention(pages, page_table, kv_len, q, out, workspace, n_heads, n_kv, head_dim, page_tokens,
+                                         max_kv_len, cu_q, max_q, head_dim ** -0.5 if scale is None else scale, softcap, window,
+                                         slopes, lse, parent, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_kv_tree_attention", status)
+    ty, w = _type(q), n_heads * head_dim
+    pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
+    qp, qs = _rows("q", q, w, q.dtype)
+    op, os_ = _rows("out", out, w, q.dtype)
+    status = lib().qdq_kv_tree_attention(
+        pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32", seqs),
+        _vec("cu_q", cu_q, "int32", seqs + 1), _vec("parent", parent, "int32"), seqs, max_q, max_kv_len, n_heads, qp, qs, op, os_,
+        _vec("lse", lse, "float32"), _vec("slopes", slopes, "float32", n_heads), head_dim ** -0.5 if scale is None else scale,
+        softcap, window, ty, _bytes("workspace", workspace), workspace.nbytes, _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_kv_tree_attention", status)
+
+
+def verify_drafts_workspace_bytes(n_seqs: int, max_rows: int, n: int) -> int:
+    return int(lib().qdq_verify_drafts_workspace_bytes(n_seqs, max_rows, n))
+
+
+def verify_drafts_workspace(n_seqs: int, max_rows: int, n: int, device="cuda"):
+    """A zeroed workspace of :func:`verify_drafts`; calls on one stream may share it, also with :func:`kv_attention`."""
+    import torch
+    return torch.zeros(verify_drafts_workspace_bytes(n_seqs, max_rows, n), dtype=torch.uint8, device=device)
+
+
+def verify_drafts(logits, tokens, uniform, accepted, path, next_token, n: int, workspace, cu=None, max_rows: int = 1, parent=None,
+                  draft_probs=None, temperature: float = 1.0, stream=None):
+    """Accept or reject each sequence's drafted tokens by the target's ``logits`` and given random numbers, and draw the
+    next token: ``accepted`` (drafts), ``path`` (row 0 and the accepted ones, -1 past them) and ``next_token``.
+
+    ``draft_probs`` are the probabilities that the children of each row's node were drawn from (None: drafts without
+    probabilities); at temperature 0 the largest logit decides.  Without ``cu`` each sequence has one row and no drafts."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.verify_drafts(logits, tokens, uniform, accepted, path, next_token, n, workspace, cu, max_rows, parent,
+                                     draft_probs, temperature, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_verify_drafts", status)
+    import torch
+    ty, seqs = _type(logits), accepted.numel()
+    least = seqs if cu is None else 0  # else the device knows how many rows there are
+    xp, xs = _rows("logits", logits, n, logits.dtype, least)
+    dp, ds = _rows("draft_probs", draft_probs, n, torch.float32, least)
+    status = lib().qdq_verify_drafts(
+        xp, xs, ty, _vec("tokens", tokens, "int32", least), _vec("cu", cu, "int32", seqs + 1), _vec("parent", parent, "int32", least),
+        seqs, max_rows, n, dp, ds, _vec("uniform", uniform, "float32", least), temperature, _vec("accepted", accepted, "int32"),
+        _vec("path", path, "int32", seqs * max_rows), _vec("next_token", next_token, "int32", seqs), _bytes("workspace", workspace),
+        workspace.nbytes, _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_verify_drafts", status)
+
+
+def kv_keep(pages, page_table, kv_len, cu, path, accepted, n_kv: int, head_dim: int, page_tokens: int, stream=None):
+    """Move the cached tokens of each sequence's accepted path (``path`` and ``accepted`` of :func:`verify_drafts`) to the
+    places behind the tokens cached before the drafts; the caller then shortens ``kv_len``."""
+    if _fast_lib is None:
+        _bind_fast()
+    if _lib is _fast_lib:  # the ordinary case; None: something is unusual, and the code below says what
+        status = _fast.kv_keep(pages, page_table, kv_len, cu, path, accepted, n_kv, head_dim, page_tokens, _stream(stream))
+        if status == 0:
+            return
+        if status is not None:
+            raise QdqError("qdq_kv_keep", status)
+    _type_names()
+    pp, n, tp, seqs, width = _pool(pages, page_table, page_tokens, n_kv, head_dim)
+    if path.dim() != 2 or path.shape[0] < seqs:
+        raise ValueError("path: %d rows expected, got shape %s" % (seqs, tuple(path.shape)))
+    status = lib().qdq_kv_keep(pp, n, page_tokens, n_kv, head_dim, tp, width, _vec("kv_len", kv_len, "int32", seqs),
+                               _vec("cu", cu, "int32", seqs + 1), seqs, _vec("path", path, "int32"), path.shape[1],
+                               _vec("accepted", accepted, "int32", seqs), _stream(stream))
+    if status != QDQ_OK:
+        raise QdqError("qdq_kv_keep", status)
 
 
 # ---------------------------------------------------------------- upload helpers

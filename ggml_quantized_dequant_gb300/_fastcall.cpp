@@ -18,6 +18,10 @@ decltype(&qdq_kv_append) f_append;
 decltype(&qdq_kv_read) f_read;
 decltype(&qdq_kv_attention) f_attention;
 decltype(&qdq_token_logprobs) f_logprobs;
+decltype(&qdq_kv_append_rope) f_rope;
+decltype(&qdq_kv_tree_attention) f_tree;
+decltype(&qdq_verify_drafts) f_verify;
+decltype(&qdq_kv_keep) f_keep;
 
 // Reads arguments; `ok` falls to false at the first one that is not ordinary.
 struct Reader {
@@ -252,14 +256,120 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   return PyLong_FromLong(f_logprobs(x, xs, t, tokens, rows, n, k, lp, ent, ti, tl, ws, wb, st));
 }
 
-// Addresses of the five functions in the loaded library, then torch.float32, float16, bfloat16, int32.
+// pages, table, kv_len, q, q_out, k, v, n_heads, n_kv, head_dim, page_tokens, freqs, interleaved, q_weight, k_weight, eps, cu_new,
+// max_new, parent, stream
+PyObject *kv_append_rope(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  Reader r;
+  if (n_args != 20 || !f_rope) return leave();
+  const Pool p(r, a[0], a[1], a[8], a[9], a[10]);
+  const int t = r.type(a[5]), heads = r.small(a[7]);
+  if (!r.ok) return leave();
+  long long qs, os, ks, vs;
+  const int *len = static_cast<const int *>(r.vec(a[2], g_int32, p.seqs)), *cu = static_cast<const int *>(r.vec(a[16], g_int32, p.seqs + 1ll));
+  const long long wide = (long long)p.n_kv * p.head_dim, q_wide = (long long)heads * p.head_dim, least = cu ? 0 : p.seqs;
+  void *q = r.rows(a[3], q_wide, g_types[t], &qs, least), *o = r.rows(a[4], q_wide, g_types[t], &os, least);
+  void *k = r.rows(a[5], wide, g_types[t], &ks, least), *v = r.rows(a[6], wide, g_types[t], &vs, least);
+  int n_rot = 0;
+  if (r.ok && a[11] != Py_None) {
+    PyObject *n = PyObject_CallMethodNoArgs(a[11], s_numel);
+    if (n) {
+      n_rot = 2 * r.small(n);
+      Py_DECREF(n);
+    } else {
+      r.ok = false;
+    }
+  }
+  const float *freqs = static_cast<const float *>(r.vec(a[11], g_types[0], 0));
+  const int pairs = r.ok ? PyObject_IsTrue(a[12]) : 0, most = r.small(a[17]);
+  if (pairs < 0) r.ok = false;
+  const float *qw = static_cast<const float *>(r.vec(a[13], g_types[0], p.head_dim)), *kw = static_cast<const float *>(r.vec(a[14], g_types[0], p.head_dim));
+  const float eps = float(r.real(a[15]));
+  const int *parent = static_cast<const int *>(r.vec(a[18], g_int32, least));
+  const cudaStream_t st = stream_of(r, a[19]);
+  if (!r.ok) return leave();
+  return PyLong_FromLong(f_rope(p.pages, p.n_pages, p.page_tokens, p.n_kv, p.head_dim, p.table, p.width, len, cu, parent, p.seqs, most, heads,
+                                q, qs, o, os, k, ks, v, vs, qw, kw, eps, freqs, n_rot, pairs, t, st));
+}
+
+// pages, table, kv_len, q, out, workspace, n_heads, n_kv, head_dim, page_tokens, max_kv_len, cu_q, max_q, scale, softcap,
+// window, slopes, lse, parent, stream
+PyObject *kv_tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  Reader r;
+  if (n_args != 20 || !f_tree) return leave();
+  const Pool p(r, a[0], a[1], a[7], a[8], a[9]);
+  const int t = r.type(a[3]), heads = r.small(a[6]);
+  if (!r.ok) return leave();
+  long long qs, os;
+  const int *len = static_cast<const int *>(r.vec(a[2], g_int32, p.seqs)), *cu = static_cast<const int *>(r.vec(a[11], g_int32, p.seqs + 1ll));
+  const long long wide = (long long)heads * p.head_dim;
+  void *q = r.rows(a[3], wide, g_types[t], &qs, 0), *out = r.rows(a[4], wide, g_types[t], &os, 0);
+  size_t wb;
+  void *ws = r.bytes(a[5], 0, &wb);
+  const int most_kv = r.small(a[10]), most_q = r.small(a[12]), window = r.small(a[15]);
+  const float scale = float(r.real(a[13])), cap = float(r.real(a[14]));
+  const float *slopes = static_cast<const float *>(r.vec(a[16], g_types[0], heads));
+  float *lse = static_cast<float *>(r.vec(a[17], g_types[0], 0));
+  const int *parent = static_cast<const int *>(r.vec(a[18], g_int32, 0));
+  const cudaStream_t st = stream_of(r, a[19]);
+  if (!r.ok) return leave();
+  return PyLong_FromLong(f_tree(p.pages, p.n_pages, p.page_tokens, p.n_kv, p.head_dim, p.table, p.width, len, cu, parent, p.seqs, most_q,
+                                most_kv, heads, q, qs, out, os, lse, slopes, scale, cap, window, t, ws, wb, st));
+}
+
+// logits, tokens, uniform, accepted, path, next_token, n, workspace, cu, max_rows, parent, draft_probs, temperature, stream
+PyObject *verify_drafts(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  Reader r;
+  if (n_args != 14 || !f_verify) return leave();
+  const int t = r.type(a[0]), n = r.small(a[6]), rows = r.small(a[9]);
+  PyObject *count = r.ok ? PyObject_CallMethodNoArgs(a[3], s_numel) : nullptr;
+  const int seqs = count ? r.small(count) : 0;
+  Py_XDECREF(count);
+  if (!r.ok || !count) return leave();
+  const int *cu = static_cast<const int *>(r.vec(a[8], g_int32, seqs + 1ll));
+  const long long least = cu ? 0 : seqs;
+  long long xs, ds;
+  void *x = r.rows(a[0], n, g_types[t], &xs, least);
+  const float *probs = static_cast<const float *>(r.rows(a[11], n, g_types[0], &ds, least));
+  const int *tokens = static_cast<const int *>(r.vec(a[1], g_int32, least)), *parent = static_cast<const int *>(r.vec(a[10], g_int32, least));
+  const float *uniform = static_cast<const float *>(r.vec(a[2], g_types[0], least));
+  int *accepted = static_cast<int *>(r.vec(a[3], g_int32, 0)), *path = static_cast<int *>(r.vec(a[4], g_int32, (long long)seqs * rows));
+  int *next = static_cast<int *>(r.vec(a[5], g_int32, seqs));
+  size_t wb;
+  void *ws = r.bytes(a[7], 0, &wb);
+  const float temperature = float(r.real(a[12]));
+  const cudaStream_t st = stream_of(r, a[13]);
+  if (!r.ok) return leave();
+  return PyLong_FromLong(f_verify(x, xs, t, tokens, cu, parent, seqs, rows, n, probs, ds, uniform, temperature, accepted, path, next, ws, wb,
+                                  st));
+}
+
+// pages, table, kv_len, cu, path, accepted, n_kv, head_dim, page_tokens, stream
+PyObject *kv_keep(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  Reader r;
+  if (n_args != 10 || !f_keep) return leave();
+  const Pool p(r, a[0], a[1], a[6], a[7], a[8]);
+  if (!r.ok) return leave();
+  const int *len = static_cast<const int *>(r.vec(a[2], g_int32, p.seqs)), *cu = static_cast<const int *>(r.vec(a[3], g_int32, p.seqs + 1ll));
+  PyObject *shape = r.attr(a[4], s_shape);
+  if (!shape || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != 2 || r.integer(PyTuple_GET_ITEM(shape, 0)) < p.seqs) r.ok = false;
+  const int width = r.ok ? r.small(PyTuple_GET_ITEM(shape, 1)) : 0;
+  Py_XDECREF(shape);
+  const int *path = static_cast<const int *>(r.vec(a[4], g_int32, 0)), *accepted = static_cast<const int *>(r.vec(a[5], g_int32, p.seqs));
+  const cudaStream_t st = stream_of(r, a[9]);
+  if (!r.ok) return leave();
+  return PyLong_FromLong(f_keep(p.pages, p.n_pages, p.page_tokens, p.n_kv, p.head_dim, p.table, p.width, len, cu, p.seqs, path, width, accepted,
+                                st));
+}
+
+// Addresses of the nine functions in the loaded library, then torch.float32, float16, bfloat16, int32.
+constexpr int kFunctions = 9;
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  if (n_args != 9) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 9 arguments");
+  if (n_args != kFunctions + 4) {
+    PyErr_SetString(PyExc_TypeError, "bind takes 13 arguments");
     return nullptr;
   }
-  void *f[5];
-  for (int i = 0; i < 5; ++i) {
+  void *f[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -268,18 +378,23 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   f_read = reinterpret_cast<decltype(f_read)>(f[2]);
   f_attention = reinterpret_cast<decltype(f_attention)>(f[3]);
   f_logprobs = reinterpret_cast<decltype(f_logprobs)>(f[4]);
+  f_rope = reinterpret_cast<decltype(f_rope)>(f[5]);
+  f_tree = reinterpret_cast<decltype(f_tree)>(f[6]);
+  f_verify = reinterpret_cast<decltype(f_verify)>(f[7]);
+  f_keep = reinterpret_cast<decltype(f_keep)>(f[8]);
   for (int i = 0; i < 3; ++i) {
-    Py_INCREF(a[5 + i]);
-    Py_XSETREF(g_types[i], a[5 + i]);
+    Py_INCREF(a[kFunctions + i]);
+    Py_XSETREF(g_types[i], a[kFunctions + i]);
   }
-  Py_INCREF(a[8]);
-  Py_XSETREF(g_int32, a[8]);
+  Py_INCREF(a[kFunctions + 3]);
+  Py_XSETREF(g_int32, a[kFunctions + 3]);
   Py_RETURN_NONE;
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),         FAST(rms_norm),       FAST(kv_append), FAST(kv_read),
-                         FAST(kv_attention), FAST(token_logprobs), {nullptr, nullptr, 0, nullptr}};
+                         FAST(kv_attention), FAST(token_logprobs), FAST(kv_append_rope), FAST(kv_tree_attention),
+                         FAST(verify_drafts), FAST(kv_keep), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -241,6 +241,94 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) 
     }
 }
 
+struct KeepArgs {
+  KvPool c;
+  const int *kv_len, *cu, *path, *accepted;  // path: path_stride per sequence, of which accepted + 1 count
+  int n_seqs, path_stride;
+};
+
+// The tokens of an accepted path, moved to the places behind the old ones.  One warp per (sequence, head, keys or
+// values) goes over the blocks that change, in order: a token only moves to an earlier place, so
+// a block's sources lie in it or behind it, where nothing has been written yet.  Block by block: lanes 0-15 find their
+// tokens' sources and scales, then all codes are loaded before any is written.
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_keep_kernel(const KeepArgs a) {
+  constexpr int PT = D / 4, CPT = (PT + 31) / 32;  // words of a token, words per lane
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int hw = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (hw >= 2 * a.c.n_kv) return;
+  const int h = hw >> 1, which = hw & 1;
+  const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
+  const int64_t plane = int64_t(which) * a.c.page_tokens * D;
+  const float qnan = __int_as_float(0x7fffffff);
+  for (int s = blockIdx.y; s < a.n_seqs; s += gridDim.y) {
+    const int n = int(ld_u1(a.cu + s + 1)) - int(ld_u1(a.cu + s)), old = int(ld_u1(a.kv_len + s)) - n;
+    const int most = int(ld_u1(a.accepted + s));
+    if (n <= 0 || old < 0 || most < 0) continue;
+    const int m = min(min(most, a.path_stride - 1), n - 1) + 1;
+    int last = -1;  // the node before this block's first
+    for (int p0 = old / kKvBlock * kKvBlock; p0 < old + m; p0 += kKvBlock) {
+      // lane t (and t + 16): the block's token t
+      const int t = lane & 15, i = p0 + t - old;
+      const int node = i >= 0 && i < m ? int(ld_u1(a.path + int64_t(s) * a.path_stride + i)) : -1;
+      int before = __shfl_up_sync(0xffffffffu, node, 1, 16);
+      if (t == 0 || i == 0) before = last;
+      // nodes in ever larger numbers: at the first that is not one the path ends
+      const uint32_t wrong = __ballot_sync(0xffffffffu, i >= 0 && i < m && (node <= before || node >= n)) & 0xFFFFu;
+      const int cut = wrong ? __ffs(wrong) - 1 : kKvBlock;
+      const bool mine = i < m && t < cut;
+      const int src = !mine ? p0 : i < 0 ? p0 + t : old + node;
+      if (__any_sync(0xffffffffu, mine && src != p0 + t)) {
+        const int64_t to = kv_record_of(a.c, s, p0 / kKvBlock, h, rec);
+        const int64_t from = mine ? kv_record_of(a.c, s, src / kKvBlock, h, rec) : -1;
+        const int sb = src % a.c.page_tokens;
+        float sc = 0.f;
+        if (mine)
+          sc = from < 0 ? qnan  // a token without a page
+                        : __uint_as_float(ld_u1(a.c.pages + from + int64_t(2) * a.c.page_tokens * D +
+                                                4 * (which * (a.c.page_tokens / kKvBlock) + sb / kKvBlock)));
+        float top = sc;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max_abs_bits(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float ratio = top > 0.f ? __fdiv_rn(sc, top) : 0.f;
+        const int64_t off = (from < 0 ? 0 : from) + plane + int64_t(sb) * D;  // without a page: any valid place
+        uint32_t w[kKvBlock][CPT];
+#pragma unroll
+        for (int j = 0; j < kKvBlock; ++j) {
+          const int64_t at = __shfl_sync(0xffffffffu, (long long)off, j);
+#pragma unroll
+          for (int c = 0; c < CPT; ++c)
+            if (lane + 32 * c < PT) w[j][c] = ld_u1(a.c.pages + at + 4 * (lane + 32 * c));
+        }
+        if (to >= 0) {
+          uint8_t *codes = a.c.pages + to + plane + int64_t(p0 % a.c.page_tokens) * D;
+#pragma unroll
+          for (int j = 0; j < kKvBlock; ++j) {
+            const float r = __shfl_sync(0xffffffffu, ratio, j);
+            const bool moved = __shfl_sync(0xffffffffu, int(mine && (src != p0 + t || r != 1.f)), j);
+            if (!moved) continue;
+#pragma unroll
+            for (int c = 0; c < CPT; ++c)
+              if (lane + 32 * c < PT) {
+                uint32_t v = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v |= uint32_t(__float2int_rn(float(int8_t(w[j][c] >> (8 * e))) * r) & 0xFF) << (8 * e);
+                *reinterpret_cast<uint32_t *>(codes + j * D + 4 * (lane + 32 * c)) = v;
+              }
+          }
+          if (lane == 0)
+            *reinterpret_cast<float *>(a.c.pages + to + int64_t(2) * a.c.page_tokens * D +
+                                       4 * (which * (a.c.page_tokens / kKvBlock) + p0 % a.c.page_tokens / kKvBlock)) = top;
+        }
+      }
+      if (wrong) break;
+      last = __shfl_sync(0xffffffffu, node, 15);
+    }
+  }
+}
+
 template <typename F>
 int with_dim(int d, F &&f) {
   switch (d) {
@@ -257,14 +345,11 @@ dim3 grid_of(const KvPool &c, int n_seqs, int n_blocks) {
   return dim3((2 * c.n_kv + kWarps - 1) / kWarps, n_blocks < 65535 ? n_blocks : 65535, n_seqs < 65535 ? n_seqs : 65535);
 }
 
-// Blocks of 16 that n consecutive tokens can touch.
-int blocks_touched(int n) { return n / kKvBlock + (n % kKvBlock > 1 ? 2 : 1); }
-
 }  // namespace
 
 int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int *cu, int n_seqs, int max_new,
                      const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s) {
-  const AppendArgs a{c, kv_len, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_new), max_new};
+  const AppendArgs a{c, kv_len, cu, k, v, k_stride, v_stride, n_seqs, kv_blocks_touched(max_new), max_new};
   const dim3 grid = grid_of(c, n_seqs, a.n_blocks);
   const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {
@@ -276,13 +361,22 @@ int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int
 
 int launch_kv_read(const KvPool &c, int head_dim, const int *start, const int *cu, int n_seqs, int max_tokens, void *k,
                    void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s) {
-  const ReadArgs a{c, start, cu, k, v, k_stride, v_stride, n_seqs, blocks_touched(max_tokens), max_tokens};
+  const ReadArgs a{c, start, cu, k, v, k_stride, v_stride, n_seqs, kv_blocks_touched(max_tokens), max_tokens};
   const dim3 grid = grid_of(c, n_seqs, a.n_blocks);
   const cudaError_t e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {
       return int(launch(kv_read_kernel<decltype(t), decltype(d)::value>, grid, dim3(kWarps * 32), 0, s, a));
     });
   }));
+  return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
+}
+
+int launch_kv_keep(const KvPool &c, int head_dim, const int *kv_len, const int *cu, int n_seqs, const int *path, int path_stride,
+                   const int *accepted, cudaStream_t s) {
+  const KeepArgs a{c, kv_len, cu, path, accepted, n_seqs, path_stride};
+  const dim3 grid((2 * c.n_kv + kWarps - 1) / kWarps, n_seqs < 65535 ? n_seqs : 65535);
+  const cudaError_t e = cudaError_t(
+      with_dim(head_dim, [&](auto d) { return int(launch(kv_keep_kernel<decltype(d)::value>, grid, dim3(kWarps * 32), 0, s, a)); }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }
 

@@ -17,6 +17,7 @@ constexpr float kMinScale = 2.5243549e-29f;  // 2^-95: a smaller value scale cou
 struct AttnArgs {
   KvPool c;
   const int *kv_len, *cu_q;
+  const int *parent;  // of each query row in its sequence's tree (the tree kernels)
   const void *q;
   void *out;
   float *lse;
@@ -98,6 +99,52 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int q0, int h, int 
         L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// A sequence's tree of drafted tokens in shared memory: each node's depth, and itself and its ancestors as bits.  Node i is
+// the i-th of the sequence's last tokens; its position is that of the first of them plus its depth.
+template <bool TREE>
+struct TreeNodes {  // no tree: nothing of it is called
+  __device__ __forceinline__ int depth_of(int) const { return 0; }
+  __device__ __forceinline__ bool wrong(int) const { return false; }
+};
+template <>
+struct TreeNodes<true> {
+  uint64_t seen[QDQ_MAX_TREE];
+  int parent[QDQ_MAX_TREE], depth[QDQ_MAX_TREE];
+  // threads 0, 1, ... of a block; a barrier between the two, and one behind them
+  __device__ __forceinline__ void load(const int *p, int n, int tid) {
+    if (tid < n) parent[tid] = int(ld_u1(p + tid));
+  }
+  __device__ __forceinline__ void walk(int n, int window, int tid) {
+    if (tid >= n) return;
+    uint64_t bits = 0;
+    int steps = 0;
+    for (int node = tid;;) {  // up to the root (to ever smaller numbers, so it ends)
+      if (window <= 0 || steps < window) bits |= uint64_t(1) << node;
+      const int up = parent[node];
+      if (up == -1) break;
+      if (up < 0 || up >= node) {  // no tree: the row is NaN
+        steps = -1;
+        break;
+      }
+      node = up;
+      ++steps;
+    }
+    seen[tid] = bits;
+    depth[tid] = steps;
+  }
+  // (rows and keys past the nodes: any node's, they are hidden or not written)
+  __device__ __forceinline__ int depth_of(int node) const { return depth[min(node, QDQ_MAX_TREE - 1)]; }
+  __device__ __forceinline__ uint64_t seen_of(int node) const { return seen[min(node, QDQ_MAX_TREE - 1)]; }
+  __device__ __forceinline__ bool wrong(int node) const { return depth_of(node) < 0; }
+};
+// Bit e: whether a row sees token at + e, e < 16: tokens from lo up to base, and of those from base on the ones in `seen`.
+__device__ __forceinline__ uint32_t tree_sees(uint64_t seen, int base, int lo, int at) {
+  const int old = min(max(base - at, 0), 16), skip = min(max(lo - at, 0), 16), off = at - base;
+  const uint32_t cached = ((1u << old) - 1u) & ~((1u << skip) - 1u);
+  const uint32_t drafted = off >= 0 ? (off < 64 ? uint32_t(seen >> off) : 0u) : (off > -16 ? uint32_t(seen) << -off : 0u);
+  return (cached | drafted) & 0xFFFFu;
+}
+
 // The tensor-core kernel (qdq_kv_attn_tc.cu): one or two groups of 128 rows to a tile, head dims that are whole 64s
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
@@ -112,5 +159,10 @@ inline size_t attn_tc_part_bytes(int head_dim, int groups) { return size_t(kTcRo
 // probabilities; groups: of 128 rows to a tile (2 up to head_dim 128).
 cudaError_t launch_attn_tc(const AttnArgs &a, int head_dim, int parts, int groups, cudaStream_t s);
 int read_attn_tc_timeouts();
+
+// The same two kernels for trees of drafted tokens (qdq_kv_tree.cu, qdq_kv_tree_tc.cu).
+cudaError_t launch_attn_tree(const AttnArgs &a, int head_dim, int parts, int warps, int ctas, cudaStream_t s);
+cudaError_t launch_attn_tree_tc(const AttnArgs &a, int head_dim, int parts, int groups, cudaStream_t s);
+int read_attn_tree_tc_timeouts();
 
 }  // namespace qdq

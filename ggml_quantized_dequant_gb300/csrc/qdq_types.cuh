@@ -112,6 +112,9 @@ __device__ __forceinline__ int64_t kv_record_of(const KvPool &c, int s, int blk,
   return (int64_t(id) * c.n_kv + h) * rec;
 }
 
+// Blocks of 16 that n consecutive tokens can touch.
+inline int kv_blocks_touched(int n) { return n / kKvBlock + (n % kKvBlock > 1 ? 2 : 1); }
+
 // Decode-step operators (qdq_norm.cu, qdq_kv.cu, qdq_kv_attn.cu, qdq_logprobs.cu); arguments as in qdq.h.
 int launch_rms_norm(const void *x, const void *residual, const float *weight, void *sum_out, void *out, void *q8,
                     int type, int rows, int n, int64_t x_stride, int64_t residual_stride, int64_t sum_stride,
@@ -120,6 +123,21 @@ int launch_kv_append(const KvPool &c, int head_dim, const int *kv_len, const int
                      const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s);
 int launch_kv_read(const KvPool &c, int head_dim, const int *start, const int *cu, int n_seqs, int max_tokens, void *k,
                    void *v, int64_t k_stride, int64_t v_stride, int type, cudaStream_t s);
+// Drafted tokens (qdq_kv_rope.cu, qdq_kv.cu, qdq_kv_tree.cu, qdq_verify.cu)
+int launch_kv_append_rope(const KvPool &c, int head_dim, const int *kv_len, const int *cu, const int *parent, int n_seqs,
+                          int max_new, int n_heads, const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                          const void *k, int64_t k_stride, const void *v, int64_t v_stride, const float *q_weight,
+                          const float *k_weight, float eps, const float *freqs, int n_rot, int adjacent, int type, cudaStream_t s);
+int launch_kv_keep(const KvPool &c, int head_dim, const int *kv_len, const int *cu, int n_seqs, const int *path, int path_stride,
+                   const int *accepted, cudaStream_t s);
+size_t verify_drafts_workspace_bytes(int n_seqs, int max_rows, int n);
+int launch_verify_drafts(const void *logits, int64_t stride, int type, const int *tokens, const int *cu, const int *parent,
+                         int n_seqs, int max_rows, int n, const float *draft_probs, int64_t draft_stride, const float *uniform,
+                         float temperature, int *accepted, int *path, int *next_token, void *workspace,
+                         size_t workspace_bytes, cudaStream_t s);
+int read_checks_tree();
+int read_checks_tree_tc();
+int read_checks_verify();
 // A workspace holds the tickets (zero between calls) in its first eighth and the parts in the rest.  The
 // border follows from the workspace's size alone, so that no call of another shape or operator on the
 // same workspace writes where this one's tickets are.
@@ -130,8 +148,9 @@ inline size_t workspace_for(size_t tickets, size_t part_bytes) {  // its bytes f
 }
 extern std::atomic<int> g_opt_attn_kernel;  // QDQ_OPT_ATTN_KERNEL
 size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
-int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, int n_seqs, int max_q,
-                        int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,
+// parent: NULL, or a tree of queries for each sequence
+int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, const int *parent, int n_seqs,
+                        int max_q, int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,
                         float *lse, const float *slopes, float scale, float softcap, int window, int type,
                         void *workspace, size_t workspace_bytes, cudaStream_t s);
 size_t token_logprobs_workspace_bytes(int rows, int n, int k);

@@ -414,6 +414,78 @@ int qdq_token_logprobs(const void *logits, long long row_stride, int type, const
                        float *logprob, float *entropy, int *top_index, float *top_logprob, void *workspace,
                        size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- drafted tokens ---------------------------------------------------------------------
+ * Several tokens of a sequence run in one step: guesses of what follows, verified by the model's own
+ * probabilities.  They are a tree: node i of n is row cu[s] + i, and the i-th of the sequence's last n
+ * cached tokens; parent[row] is an earlier node's number (0 <= parent < i), or -1.  A node's depth is the number of its
+ * ancestors, its position kv_len[s] - n + depth.  A step is
+ *   qdq_kv_append_rope -> qdq_kv_tree_attention (every layer), qdq_verify_drafts, qdq_kv_keep (every layer's cache),
+ * and then kv_len[s] -= n - 1 - accepted[s].  A tree has at most QDQ_MAX_TREE nodes; a node whose parent is
+ * neither -1 nor earlier gives NaN (and its cache blocks do), or is not accepted.
+ *
+ * qdq_kv_append_rope norms and turns new tokens' queries and keys, and appends keys and values to the cache:
+ *   q_weight, k_weight (head_dim f32 each, may be NULL: no norm): per head y = x / sqrt(mean(x^2) + eps) * weight;
+ *   freqs (n_rot / 2 f32, radians per position; NULL: nothing is turned): pair i of a head's first n_rot elements,
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t) with t = position * freqs[i]; the pair is elements
+ *     (2i, 2i + 1) where interleaved is 1, else (i, i + n_rot / 2).  n_rot: a multiple of 8, at most head_dim.
+ *     For freqs up to 1 the angle is off by at most 2^-30 before cos and sin, at every position.
+ *   q_out: the queries in the type (may be exactly q with its stride); keys go into the cache in f32, values as they are,
+ *   by the definition of qdq_kv_append, whose other arguments, refusals and dropped tokens hold here.
+ *   parent NULL: tokens one after the other (position = place in the cache).  q and q_out NULL with n_heads 0: keys and values alone.
+ *   Where a sequence has more new tokens than kv_len, nothing is appended and its rows of q_out are NaN.
+ *   Weights and freqs count as weights (above); they are 16-byte and 4-byte aligned.
+ *
+ * qdq_kv_tree_attention is qdq_kv_attention with cu_q and parent: node i sees the tokens before
+ *   kv_len[s] - n, its ancestors and itself, of which the window hides those at positions too far before its own; bias by
+ *   positions.  Same workspace (qdq_kv_attention_workspace_bytes), rounding and other rules.
+ *   max_q: at most QDQ_MAX_TREE; a sequence with more rows gives NaN in its first max_q.
+ *
+ * qdq_verify_drafts accepts drafts of each sequence and draws its next token.  logits: n per row (type, row_stride
+ *   elements apart), the target's after the row's token; cu NULL: one row per sequence (the next token alone).
+ *   Row 0 is the sequence's last token, rows i > 0 are drafts tokens[row] under their parents (parent
+ *   NULL: i - 1).  p = softmax(logits / temperature).  At the present node, first 0, with w = p: its children x in order
+ *     accepted when uniform[row of x] * q(x) < w(x): the present node then, and w its p;
+ *     else w = max(w - q, 0) / sum (as it was where the sum is 0).
+ *   q = draft_probs (n f32 per row, draft_stride apart: what the children of the row's node were drawn from,
+ *   independently); draft_probs NULL: 1 at x, so that w loses x.  Then, where no child is left:
+ *     next_token[s] = the first i with w_0 + .. + w_i > uniform[row 0] * sum w,
+ *     accepted[s] = the number of accepted drafts, path[s * max_rows ..] = 0, the accepted nodes, then -1.
+ *   temperature 0: a child is accepted when it is the row's largest logit (the first of equals), which is next_token
+ *   too; draft_probs and uniform are not read.  Else temperature is between 1e-6 and 1e6.
+ *   A drafted token outside [0, n) is not accepted.  Numbers outside [0, 1) count as the nearest inside.  At a node
+ *   whose row has a NaN or +inf, or nothing above -inf, no child is accepted and next_token is -1.  A sequence without
+ *   rows gets accepted -1, next_token -1 and a path of -1.  max_rows: at most QDQ_MAX_TREE; rows past it do not count.
+ *   p is computed in f32 relative to 2^-20, sums in f64: a number that lies that near a border may fall to either side.
+ *   workspace: qdq_verify_drafts_workspace_bytes(...) bytes, 256-byte aligned; it may be shared as those above.
+ *
+ * qdq_kv_keep moves the cached tokens of the accepted paths: of sequence s's last n = cu[s + 1] - cu[s] tokens, node
+ *   path[s * path_stride + i], i <= accepted[s], goes to place kv_len[s] - n + i (kv_len is not changed).  Per block
+ *   that gets a token from elsewhere: its scale becomes the largest scale of its tokens' blocks, s, and
+ *   every code rint(code * (s_of_its_block / s)); tokens that stay lose nothing where their scale is the largest.  A path's
+ *   nodes are in growing order (as qdq_verify_drafts writes them); it ends before the first that is not, or is not below n.
+ *   accepted below 0, or n above kv_len: nothing.  A token without a page counts as one of scale NaN.
+ */
+#define QDQ_MAX_TREE 64
+int qdq_kv_append_rope(void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
+                       int table_stride, const int *kv_len, const int *cu_new, const int *parent, int n_seqs, int max_new,
+                       int n_heads, const void *q, long long q_stride, void *q_out, long long q_out_stride, const void *k,
+                       long long k_stride, const void *v, long long v_stride, const float *q_weight,
+                       const float *k_weight, float eps, const float *freqs, int n_rot, int interleaved, int type,
+                       cudaStream_t stream);
+int qdq_kv_tree_attention(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,
+                          int table_stride, const int *kv_len, const int *cu_q, const int *parent, int n_seqs, int max_q,
+                          int max_kv_len, int n_heads, const void *q, long long q_stride, void *out, long long out_stride,
+                          float *lse, const float *slopes, float scale, float softcap, int window, int type,
+                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t qdq_verify_drafts_workspace_bytes(int n_seqs, int max_rows, int n);
+int qdq_verify_drafts(const void *logits, long long row_stride, int type, const int *tokens, const int *cu, const int *parent,
+                      int n_seqs, int max_rows, int n, const float *draft_probs, long long draft_stride,
+                      const float *uniform, float temperature, int *accepted, int *path, int *next_token, void *workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+int qdq_kv_keep(void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table, int table_stride,
+                const int *kv_len, const int *cu, int n_seqs, const int *path, int path_stride, const int *accepted,
+                cudaStream_t stream);
+
 /* ---- pipeline health -------------------------------------------------------
  * Every wait inside the tensor-core pipeline is bounded (2 s wall clock); a
  * wait that runs out makes its CTA stop early instead of hanging, and counts
