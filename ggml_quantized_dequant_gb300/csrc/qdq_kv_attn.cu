@@ -50,10 +50,12 @@ struct Plan {
   size_t bytes;  // of the workspace, for any window
 };
 
-// span: queries that a tile's tokens lie apart by besides its rows (a tree's nodes, in any order), for a window.
+// tree: a sequence's queries are one.  For a window, span: how much further apart a tile's tokens may lie than its
+// rows (a tree's nodes come in any order).
 Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, int window,
-          int type, int span = 0) {
+          int type, bool tree = false) {
   Plan p{};
+  const int span = tree ? max_q : 0;
   const int64_t rows = int64_t(max_q) * (n_heads / n_kv);
   p.parts = type != QDQ_TYPE_F32 && rows > 8 ? 1 : 2;
   const int64_t small = int64_t(n_seqs) * n_kv * ((rows * p.parts + 15) / 16);  // tiles of the other kernel
@@ -66,7 +68,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   p.tc = (forced == 2 || (forced == 0 && rows > kTcMinRows && !few && !light)) && (type == QDQ_TYPE_F32 || p.parts == 1) &&
          attn_tc_supported(head_dim, p.parts);
   if (p.tc) {
-    p.groups = rows > kTcRows && head_dim <= 128 ? 2 : 1;
+    p.groups = rows > kTcRows && head_dim <= 128 && !tree ? 2 : 1;
     const int R = kTcRows * p.groups;
     p.tiles = int((rows + R - 1) / R);
     p.units = int64_t(n_seqs) * n_kv * p.tiles;
@@ -75,7 +77,7 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
     const int64_t blocks = std::min(all_blocks, (tokens + kKvBlock - 1) / kKvBlock + (window > 0));
     // whole waves of CTAs (one per SM), each with at most kTcSplitBlocks of the blocks there can be
     const int64_t most = p.units * ((blocks + 4) / 4 + kTcPartCost);  // tiles of 64 tokens and parts' costs
-    const int64_t wave = int64_t(di.sm_count) * (kTcSplitBlocks / 4);
+    const int64_t wave = int64_t(di.sm_count) * ((tree && head_dim <= 128 ? kTcTreeBlocks : kTcSplitBlocks) / 4);
     const int64_t ctas = di.sm_count * ((most + wave - 1) / wave);
     p.splits = int(ctas < 0x7fffffff ? ctas : 0);
     p.bytes = workspace_for(size_t(p.units), 2 * size_t(ctas) * attn_tc_part_bytes(head_dim, p.groups));
@@ -151,8 +153,8 @@ int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const 
   // a window that hides nothing is none, and a position less a smaller one stays within 32 bits
   if (window >= max_kv_len) window = 0;
   const bool tree = parent != nullptr;
-  const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, window, type, tree ? max_q : 0);
-  if (p.splits < 1 || p.units > 0x7fffffff || (!p.tc && p.ctas < 1)) return QDQ_ERR_UNSUPPORTED;
+  const Plan p = plan(di, n_seqs, max_q, max_kv_len, n_heads, c.n_kv, head_dim, window, type, tree);
+  if (p.splits < 1 || p.units > 0x7fffffff / (tree ? 16 : 1) || (!p.tc && p.ctas < 1)) return QDQ_ERR_UNSUPPORTED;
   AttnArgs a{};
   a.c = c;
   a.kv_len = kv_len;

@@ -152,6 +152,7 @@ constexpr int kTcRows = 128;
 // sequences of 300 queries over 300 to 2500 tokens, 32 / 8 heads of 128, f16: 9 75.2 us, 12 70.4, 15 70.2, 18 70.6.)
 constexpr int kTcPartCost = 15;
 constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one part, at most
+constexpr int kTcTreeBlocks = 768;  // ... of a tree's
 inline bool attn_tc_supported(int head_dim, int parts) { return head_dim % 64 == 0 && head_dim * parts <= 384; }
 // Bytes of one part's result (two per CTA).
 inline size_t attn_tc_part_bytes(int head_dim, int groups) { return size_t(kTcRows) * groups * (head_dim + 2) * 4; }

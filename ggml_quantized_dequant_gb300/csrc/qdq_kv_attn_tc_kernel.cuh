@@ -14,6 +14,7 @@ namespace {
 constexpr int BN = 64;  // tokens per tile
 constexpr int kMinShare = 8;  // places on the line: a shorter share saves less than its part costs
 constexpr int kJoinSlots = 3;  // for joining parts
+constexpr int kSplitSlots = 4;  // stages of keys and of values where the converting sets take one each
 constexpr int kSoft = 4, kSet = 4;  // softmax warps per group of rows, warps per converting set
 
 // ---- tcgen05 --------------------------------------------------------------------
@@ -98,13 +99,18 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
 // kind::f16 with f16 operands (format 0), f32 accumulator, both K-major.
 constexpr uint32_t idesc_f16(int m, int n) { return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24); }
 
-template <int D, int PARTS, int G>
+// SPLIT: the two groups take alternate tiles of the same 128 rows, each with a tile of keys and one of values of its
+// own, and are joined at the end of a part; one converting set takes the keys of every tile, the other the values.
+template <int D, int PARTS, int G, bool SPLIT>
 struct Cfg {
   static constexpr int kSub = D / 64;                    // 64-dim sub-tiles
   static constexpr uint32_t kQTile = kTcRows * 128;      // bytes of 128 rows of a sub-tile
-  static constexpr uint32_t kQPart = G * kSub * kQTile;  // [group][sub-tile]
+  static constexpr int kRows = SPLIT ? 1 : G;            // groups of rows
+  static constexpr uint32_t kQPart = kRows * kSub * kQTile;  // [group][sub-tile]
   static constexpr uint32_t kK = kSub * BN * 128, kV = D * 128;
-  static constexpr uint32_t kRing = PARTS * kQPart + 2 * (kK + kV);
+  // tiles of keys: two for each group of SPLIT where they fit (two parts of queries leave no room)
+  static constexpr int kKeys = SPLIT && PARTS == 1 ? 4 : 2;
+  static constexpr uint32_t kRing = PARTS * kQPart + kKeys * kK + 2 * kV;
   static constexpr uint32_t kOCol = 2 * BN * G;  // S of group 0 (two), of group 1 (two) | O of group 0, of group 1
   static constexpr uint32_t kCols = kOCol + G * D <= 256 ? 256 : 512;
   static_assert(kOCol + G * D <= 512, "TMEM");
@@ -115,20 +121,23 @@ struct Cfg {
   static constexpr bool kStaged = D <= 192;
   static constexpr uint32_t kStageV = BN * D, kVStep = 8 * D + 16;
   static constexpr uint32_t kStage = (kStageV + 8 * kVStep + 127) / 128 * 128;
-  static constexpr uint32_t kFixed = 1024 + kRing + kTcSplitBlocks * uint32_t(sizeof(BlockAt));
+  static constexpr int kMaxBlocks = SPLIT ? kTcTreeBlocks : kTcSplitBlocks;  // of one part
+  static constexpr uint32_t kFixed = 1024 + kRing + kMaxBlocks * uint32_t(sizeof(BlockAt));
   static constexpr uint32_t kLeft = 225 * 1024 - kFixed;
   // two sets of converting warps take alternate tiles, unless only one stage fits (two parts:
   // there the products take twice as long)
   static constexpr int kSets = kStaged && kLeft < 2 * kStage ? 1 : 2;
+  static_assert(!SPLIT || (kStaged && kSets == 2 && G == 2), "a converting set for the keys and one for the values");
   static constexpr int kSlots = !kStaged ? 0 : kLeft >= 2 * kSets * kStage ? 2 : 1;  // stages per set
   static constexpr uint32_t kBytes = kFixed + kSets * kSlots * kStage;
   // more than half an SM's shared memory: one CTA per SM, as the columns of TMEM want it
   static constexpr uint32_t kSmem = kBytes > 116 * 1024 ? kBytes : 116 * 1024;
   static_assert(kSmem <= 225 * 1024, "shared memory");
+  static_assert(!SPLIT || kSets * kSlots == kSplitSlots, "stages");
   static constexpr int kConv = kSet * kSets;
   static constexpr int kThreads = 32 * (kSoft * G + kConv + G + 1);
   // joining parts: columns of 4 dims in a slot, warps that add
-  static constexpr uint32_t join_bytes(int quads) { return 1024 + 2 * kTcRows * G * 4 + kJoinSlots * kTcRows * G * (quads * 16 + 4); }
+  static constexpr uint32_t join_bytes(int quads) { return 1024 + 2 * kTcRows * kRows * 4 + kJoinSlots * kTcRows * kRows * (quads * 16 + 4); }
   static constexpr int kJoinQuads = join_bytes(16) <= kSmem ? 16 : 8, kJoinWarps = kThreads >= 512 ? 16 : 8;
   static_assert(join_bytes(kJoinQuads) <= kSmem, "room for the join");
   // 19 warps are launched with 96 registers a thread: 8 softmax warps x 128 + 8 converting x 64
@@ -136,26 +145,62 @@ struct Cfg {
   static constexpr bool kShift = G == 2 && kSets == 2;
 };
 
-template <int G>
-struct Bars {
+template <int N>
+struct MoreBars {
+  uint64_t vstage[N], vread[N], kfull4[N], kfree4[N];
+};
+template <>
+struct MoreBars<0> {};
+// (SPLIT: stage and sread are of the keys, vstage and vread of the values)
+template <int G, bool SPLIT>
+struct Bars : MoreBars<SPLIT ? kSplitSlots : 0> {
   uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain, joined[kJoinSlots];
-  static constexpr int kBars = 8 + 6 + 6 * G + 1 + kJoinSlots;
+  static constexpr int kBars = 8 + 6 + 6 * G + 1 + kJoinSlots + (SPLIT ? 4 * kSplitSlots : 0);
   long long sums[20], first, g0, g1, total;  // the share's state, kept here while a part runs (registers are short)
   uint32_t tmem;
   int abort, last, entry, shares;
 };
 
+// Entry e = (sequence, tile of R rows).
+struct TcEntry {
+  int s, q0, len, nq, rows, r0, nr, pos_lo, pos_hi, b_lo, b_hi, tiles;  // tiles: at least 1 where there are rows
+  bool bad;
+};
+template <bool TREE>
+__device__ __forceinline__ TcEntry tc_entry(const AttnArgs &a, int e, int R) {
+  TcEntry x;
+  x.s = e / a.tiles;
+  x.r0 = e % a.tiles * R;
+  x.q0 = a.cu_q ? int(ld_u1(a.cu_q + x.s)) : x.s;
+  x.nq = a.cu_q ? int(ld_u1(a.cu_q + x.s + 1)) - x.q0 : 1;
+  x.len = int(ld_u1(a.kv_len + x.s));
+  x.rows = min(x.nq, a.max_q) * a.group;
+  x.nr = min(R, x.rows - x.r0);
+  x.bad = x.len < 0 || x.len > a.max_kv_len || (x.len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride ||
+          (TREE && x.nq > a.max_q);
+  x.tiles = 0;
+  if (x.nr <= 0) return x;
+  // (a tree's nodes stand anywhere from its root's position on, and their keys are the last ones)
+  x.pos_lo = x.len - x.nq + (TREE ? 0 : int(a.query_of(x.r0)));
+  x.pos_hi = TREE ? x.len - 1 : x.len - x.nq + int(a.query_of(x.r0 + x.nr - 1));
+  x.b_lo = a.window > 0 ? max(0, x.pos_lo - a.window + 1) / kKvBlock : 0;
+  x.b_hi = x.bad ? 0 : (x.pos_hi + kKvBlock) / kKvBlock;
+  x.tiles = max(1, (x.b_hi - x.b_lo + 3) / 4);
+  return x;
+}
+
 // BENT: the scores have a cap or a bias.  TREE: a sequence's queries are a tree of drafted tokens.
 template <int D, int PARTS, int G, bool BENT, bool TREE>
-__global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(const AttnArgs a) {
-  using C = Cfg<D, PARTS, G>;
-  constexpr int R = kTcRows * G, kThreads = C::kThreads, kConv = C::kConv;
+__global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1) attn_tc_kernel(const AttnArgs a) {
+  constexpr bool SPLIT = TREE && G == 2;  // a tree rarely has more than 128 rows
+  using C = Cfg<D, PARTS, G, SPLIT>;
+  constexpr int R = kTcRows * C::kRows, kThreads = C::kThreads, kConv = C::kConv;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *kring = smem + PARTS * C::kQPart, *vring = kring + 2 * C::kK;
+  uint8_t *kring = smem + PARTS * C::kQPart, *vring = kring + C::kKeys * C::kK;
   BlockAt *s_blk = reinterpret_cast<BlockAt *>(smem + C::kRing);
-  uint8_t *stages = smem + C::kRing + kTcSplitBlocks * sizeof(BlockAt);  // [set][slot]
-  __shared__ Bars<G> bars;
+  uint8_t *stages = smem + C::kRing + C::kMaxBlocks * sizeof(BlockAt);  // [set][slot]
+  __shared__ Bars<G, SPLIT> bars;
   __shared__ float s_qs[R];
   __shared__ TreeNodes<TREE> s_tree;
   const float ninf = __int_as_float(0xff800000), qnan = __int_as_float(0x7fffffff);
@@ -164,31 +209,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   pdl_wait();
 
   // ---- this CTA's share.  Entry e = (sequence, tile of rows); every entry has n_kv units of the same length.
-  struct Entry {
-    int s, q0, len, nq, rows, r0, nr, pos_lo, pos_hi, b_lo, b_hi, tiles;  // tiles: at least 1 where there are rows
-    bool bad;
-  };
-  auto entry = [&](int e) {
-    Entry x;
-    x.s = e / a.tiles;
-    x.r0 = e % a.tiles * R;
-    x.q0 = a.cu_q ? int(ld_u1(a.cu_q + x.s)) : x.s;
-    x.nq = a.cu_q ? int(ld_u1(a.cu_q + x.s + 1)) - x.q0 : 1;
-    x.len = int(ld_u1(a.kv_len + x.s));
-    x.rows = min(x.nq, a.max_q) * a.group;
-    x.nr = min(R, x.rows - x.r0);
-    x.bad = x.len < 0 || x.len > a.max_kv_len || (x.len + a.c.page_tokens - 1) / a.c.page_tokens > a.c.table_stride ||
-            (TREE && x.nq > a.max_q);
-    x.tiles = 0;
-    if (x.nr <= 0) return x;
-    // (a tree's nodes stand anywhere from its root's position on, and their keys are the last ones)
-    x.pos_lo = x.len - x.nq + (TREE ? 0 : int(a.query_of(x.r0)));
-    x.pos_hi = TREE ? x.len - 1 : x.len - x.nq + int(a.query_of(x.r0 + x.nr - 1));
-    x.b_lo = a.window > 0 ? max(0, x.pos_lo - a.window + 1) / kKvBlock : 0;
-    x.b_hi = x.bad ? 0 : (x.pos_hi + kKvBlock) / kKvBlock;
-    x.tiles = max(1, (x.b_hi - x.b_lo + 3) / 4);
-    return x;
-  };
+  using Entry = TcEntry;
+  auto entry = [&](int e) { return tc_entry<TREE>(a, e, R); };
   // An entry's unit on the line of all work: a part's cost in tiles, then its tiles, so that a share's end
   // in a unit's first kTcPartCost leaves the unit to the next CTA.
   auto line_of = [](const Entry &x) { return x.tiles ? x.tiles + kTcPartCost : 0; };
@@ -284,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       h = u.h;
       c0 = en.b_lo + 4 * u.t0;
       cn = max(0, min(4 * (u.t1 - u.t0), en.b_hi - c0));
-      if (!QDQ_GUARD(cn <= kTcSplitBlocks, QDQ_CHECK_SMEM)) break;
+      if (!QDQ_GUARD(cn <= C::kMaxBlocks, QDQ_CHECK_SMEM)) break;
       if (u.nsplit > 1 && !QDQ_GUARD(int64_t(2) * (u.c_lo + u.nsplit) * (R * (D + 2)) <= a.room &&
                                          int64_t(bars.entry) * a.c.n_kv + h < a.units, QDQ_CHECK_OUT))
         break;
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
 
     if (tid == 32 * (kSoft * G + kConv)) {
       if (started)
-        for (int i = 0; i < Bars<G>::kBars; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.stage[0][0] + i)) : "memory");
+        for (int i = 0; i < Bars<G, SPLIT>::kBars; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars) + 8 * i) : "memory");
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bars.stage[0][i], 1);
         mbar_init(&bars.stage[1][i], 1);
@@ -301,13 +323,20 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         mbar_init(&bars.sread[1][i], kSet);
         mbar_init(&bars.kfull[i], kSet);
         mbar_init(&bars.vfull[i], kSet);
-        mbar_init(&bars.kfree[i], G);
+        mbar_init(&bars.kfree[i], SPLIT ? 1 : G);
         for (int g = 0; g < G; ++g) {
           mbar_init(&bars.sfull[g][i], 1);
           mbar_init(&bars.pready[g][i], kSoft);
           mbar_init(&bars.pvdone[g][i], 1);
         }
       }
+      if constexpr (SPLIT)
+        for (int i = 0; i < kSplitSlots; ++i) {
+          mbar_init(&bars.vstage[i], 1);
+          mbar_init(&bars.vread[i], kSet);
+          mbar_init(&bars.kfull4[i], kSet);
+          mbar_init(&bars.kfree4[i], 1);
+        }
       mbar_init(&bars.drain, G);
       for (int i = 0; i < kJoinSlots; ++i) mbar_init(&bars.joined[i], 1);
       if (!started) bars.abort = 0;
@@ -315,9 +344,49 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     }
     started = true;
     const int64_t vplane = int64_t(a.c.page_tokens) * D;
+    // block i of the part: its place and scales
+    auto block_at = [&](int i) {
+      BlockAt e{-1, 0.f, 0.f, 0.f, 0.f};
+      if (i < cn) {
+        const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
+        const int64_t at = kv_record_of(a.c, s, blk, h, kv_record_bytes(a.c.page_tokens, D));
+        if (at >= 0) {
+          const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
+          const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
+          e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale)), 0.f};
+          if (vs >= kMinScale && vs < __int_as_float(0x7f800000)) e.inv = __frcp_rn(e.vs);
+        } else {
+          e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
+        }
+      }
+      return e;
+    };
+    // copies of tile i's keys or values into their stage (SPLIT), by a whole warp: a lane for each (one lane after the other
+    // took 0.4 us a tile)
+    auto copy_keys = [&](int i, bool values) {
+      if constexpr (SPLIT) {
+        const int n = i % kSplitSlots, piece = values ? lane >> 1 : lane;  // of the tile's four blocks
+        uint8_t *dst = stages + n * C::kStage;
+        uint64_t *bar = values ? &bars.vstage[n] : &bars.stage[0][0] + n;
+        const int64_t at = piece < 4 ? s_blk[4 * i + piece].k : -1;  // no such block: its part of the stage is not read
+        const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(__popc(have)) * (values ? 8 : 16) * D);
+        __syncwarp();
+        if (at >= 0) {
+          if (values)
+            bulk_copy_g2s(dst + C::kStageV + lane * C::kVStep, a.c.pages + at + vplane + (lane & 1) * 8 * D, 8 * D, bar);
+          else
+            bulk_copy_g2s(dst + lane * 16 * D, a.c.pages + at, 16 * D, bar);
+        }
+        __syncwarp();
+      }
+    };
     // copies of tile i's codes into its stage
     auto copy_tile = [&](int i) {
-      if constexpr (C::kStaged) {
+      if constexpr (SPLIT) {
+        copy_keys(i, false);
+        copy_keys(i, true);
+      } else if constexpr (C::kStaged) {
         const int set = i % C::kSets, n = i / C::kSets % C::kSlots;
         uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
         uint64_t *bar = &bars.stage[set][n];
@@ -439,25 +508,17 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     } else {
       // meanwhile the split's blocks: places and scales (past the last one: zeros, hidden from every row)
-      const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
 #pragma unroll 2
-      for (int i = tid - 32 * (kSoft * G + kConv); i < 4 * nt; i += kThreads - 32 * (kSoft * G + kConv)) {
-        BlockAt e{-1, 0.f, 0.f, 0.f, 0.f};
-        if (i < cn) {
-          const int blk = c0 + i, b = blk % (a.c.page_tokens / kKvBlock);
-          const int64_t at = kv_record_of(a.c, s, blk, h, rec);
-          if (at >= 0) {
-            const uint8_t *sc = a.c.pages + at + 2 * vplane + 4 * b;
-            const float ks = __uint_as_float(ld_u1(sc)), vs = __uint_as_float(ld_u1(sc + 4 * (a.c.page_tokens / kKvBlock)));
-            e = BlockAt{at + int64_t(b) * kKvBlock * D, ks, vs * kPScale, log2f(fmaxf(vs, kMinScale)), 0.f};
-            if (vs >= kMinScale && vs < __int_as_float(0x7f800000)) e.inv = __frcp_rn(e.vs);
-          } else {
-            e.ks = qnan;  // no page: its codes count as 0, its scores are NaN
-          }
+      for (int i = tid - 32 * (kSoft * G + kConv); !SPLIT && i < 4 * nt; i += kThreads - 32 * (kSoft * G + kConv)) s_blk[i] = block_at(i);
+      if constexpr (SPLIT) {  // the first of them (the others follow before their copies), and the first tiles' copies
+        if (warp == kSoft * G + kConv + G) {
+          if (lane < 4 * nt) s_blk[lane] = block_at(lane);
+          __syncwarp();
         }
-        s_blk[i] = e;
-      }
-      if constexpr (C::kStaged) {  // and the first tiles' copies
+        named_bar_sync(4, 32 * (G + 1));
+        if (warp == kSoft * G + kConv + G)
+          for (; copied < min(nt, kSplitSlots); ++copied) copy_tile(copied);
+      } else if constexpr (C::kStaged) {  // and the first tiles' copies
         named_bar_sync(4, 32 * (G + 1));
         if (tid == 32 * (kSoft * G + kConv + G))
           for (; copied < min(nt, C::kSets * C::kSlots); ++copied) copy_tile(copied);
@@ -488,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     };
 
     const int grp = warp / kSoft;        // softmax warps: their group of rows
-    const int lr = tid;                  // and their thread's row of the tile
+    const int lr = SPLIT ? tid % kTcRows : tid;  // and their thread's row of the tile
     const int row = r0 + lr;
     float m = ninf, l = 0.f;             // its reference and sum
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -506,10 +567,11 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       // tokens that every row of the tile sees
       const int all_lo = a.window > 0 ? max(0, (TREE ? base + min(nq, QDQ_MAX_TREE) - 1 : pos_hi) - a.window + 1) : 0;
       const int all_hi = TREE ? base : pos_lo + 1;
-      for (int i = 0; i < nt; ++i) {
-        const int b = i & 1;
+      // the group's t-th tile is i
+      for (int i = SPLIT ? grp : 0, t = 0; i < nt; i += SPLIT ? 2 : 1, ++t) {
+        const int b = t & 1;
         const uint32_t sp = tmem + lanes + uint32_t((2 * grp + b) * BN);
-        if (!wait(&bars.sfull[grp][b], i >> 1)) break;
+        if (!wait(&bars.sfull[grp][b], t >> 1)) break;
         tc_fence_after();
         const int j0 = (c0 + 4 * i) * kKvBlock;
         const bool whole = j0 >= all_lo && j0 + BN <= all_hi;
@@ -519,8 +581,8 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
           const float corr = m_new > m ? ex2(m - m_new) : 1.f;
           l *= corr;
           m = m_new;
-          if (i > 0) {
-            if (!wait(&bars.pvdone[grp][(i - 1) & 1], (i - 1) >> 1)) return false;
+          if (t > 0) {
+            if (!wait(&bars.pvdone[grp][(t - 1) & 1], (t - 1) >> 1)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -748,6 +810,92 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         rr = u / (D / 16);
         ch = u % (D / 16);
       };
+      // the registers' codes into a tile of keys, and into one of values
+      auto put_keys = [&](uint8_t *kt) {
+#pragma unroll
+        for (int j = 0; j < KL; ++j) {
+          int rr, ch;
+          key_at(j, rr, ch);
+          rr += 16 * w;
+          const uint32_t q[4] = {kq[j].x, kq[j].y, kq[j].z, kq[j].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t u = q[e] ^ 0x80808080u;
+            o[2 * e] = codes_f16<0x4140>(u);
+            o[2 * e + 1] = codes_f16<0x4342>(u);
+          }
+          uint8_t *dst = kt + (ch / 4) * (BN * 128) + rr * 128;
+          const int c = 2 * ch % 8;
+          *reinterpret_cast<uint4 *>(dst + ((c ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      };
+      auto put_values = [&](uint8_t *vt) {
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+          if (w + 4 * g < D / 32) {
+#pragma unroll
+            for (int hw = 0; hw < 2; ++hw) {  // four dims
+              uint32_t even[4], odd[4];       // pairs of tokens: dims 0, 1 and dims 2, 3
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint32_t x = (hw ? vq[g][2 * t].y : vq[g][2 * t].x) ^ 0x80808080u;
+                const uint32_t y = (hw ? vq[g][2 * t + 1].y : vq[g][2 * t + 1].x) ^ 0x80808080u;
+                even[t] = __byte_perm(x, y, 0x5140);
+                odd[t] = __byte_perm(x, y, 0x7362);
+              }
+              const int d = (w + 4 * g) * 32 + vd * 8 + hw * 4;
+              auto put = [&](int dd, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+                *reinterpret_cast<uint4 *>(vt + dd * 128 + ((vtc ^ (dd & 7)) << 4)) = make_uint4(x, y, z, u);
+              };
+              put(d, codes_f16<0x4140>(even[0]), codes_f16<0x4140>(even[1]), codes_f16<0x4140>(even[2]), codes_f16<0x4140>(even[3]));
+              put(d + 1, codes_f16<0x4342>(even[0]), codes_f16<0x4342>(even[1]), codes_f16<0x4342>(even[2]), codes_f16<0x4342>(even[3]));
+              put(d + 2, codes_f16<0x4140>(odd[0]), codes_f16<0x4140>(odd[1]), codes_f16<0x4140>(odd[2]), codes_f16<0x4140>(odd[3]));
+              put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
+            }
+          }
+      };
+      if constexpr (SPLIT) {
+        for (int i = 0; i < nt; ++i) {
+          const int n = i % kSplitSlots, round = i / kSplitSlots, b = i & 1;
+          const uint8_t *st = stages + n * C::kStage;
+          if (set == 0) {
+            if (!wait(&bars.stage[0][0] + n, round)) break;
+            const int64_t ak = s_blk[4 * i + w].k;
+#pragma unroll
+            for (int j = 0; j < KL; ++j)
+              kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sread[0][0] + n);
+            const int k = i % C::kKeys;
+            if (i >= C::kKeys && !wait(&bars.kfree4[k], i / C::kKeys - 1)) break;  // S of the tile that was there is done
+            put_keys(kring + k * C::kK);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.kfull4[k]);
+          } else {
+            if (!wait(&bars.vstage[n], round)) break;
+            const int64_t av = s_blk[4 * i + vtc / 2].k;
+#pragma unroll
+            for (int g = 0; g < VG; ++g)
+              if (w + 4 * g < D / 32) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                  vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                    : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
+              }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.vread[n]);
+            const int t = (i >> 1) - 1;  // P V of tile i - 2, the group's t-th
+            if (i >= 2 && !wait(&bars.pvdone[b][t & 1], t >> 1)) break;
+            put_values(vring + b * C::kV);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.vfull[b]);
+          }
+        }
+      } else {
       uint8_t *my_stages = stages + set * C::kSlots * C::kStage;
       int n = 0, round = 0;  // slot, and how often it has been used
       for (int i = set; i < nt; i += C::kSets) {
@@ -788,55 +936,17 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
         }
         if (i >= 2 && !wait(&bars.kfree[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
         uint8_t *kt = kring + b * C::kK, *vt = vring + b * C::kV;
-#pragma unroll
-        for (int j = 0; j < KL; ++j) {
-          int rr, ch;
-          key_at(j, rr, ch);
-          rr += 16 * w;
-          const uint32_t q[4] = {kq[j].x, kq[j].y, kq[j].z, kq[j].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t u = q[e] ^ 0x80808080u;
-            o[2 * e] = codes_f16<0x4140>(u);
-            o[2 * e + 1] = codes_f16<0x4342>(u);
-          }
-          uint8_t *dst = kt + (ch / 4) * (BN * 128) + rr * 128;
-          const int c = 2 * ch % 8;
-          *reinterpret_cast<uint4 *>(dst + ((c ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
+        put_keys(kt);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.kfull[b]);
         // P V of tile i - 2: its values' tile is free
         if (i >= 2 && !(wait(&bars.pvdone[0][b], (i - 2) >> 1) && (G == 1 || wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)))) break;
-#pragma unroll
-        for (int g = 0; g < VG; ++g)
-          if (w + 4 * g < D / 32) {
-#pragma unroll
-            for (int hw = 0; hw < 2; ++hw) {  // four dims
-              uint32_t even[4], odd[4];       // pairs of tokens: dims 0, 1 and dims 2, 3
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const uint32_t x = (hw ? vq[g][2 * t].y : vq[g][2 * t].x) ^ 0x80808080u;
-                const uint32_t y = (hw ? vq[g][2 * t + 1].y : vq[g][2 * t + 1].x) ^ 0x80808080u;
-                even[t] = __byte_perm(x, y, 0x5140);
-                odd[t] = __byte_perm(x, y, 0x7362);
-              }
-              const int d = (w + 4 * g) * 32 + vd * 8 + hw * 4;
-              auto put = [&](int dd, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
-                *reinterpret_cast<uint4 *>(vt + dd * 128 + ((vtc ^ (dd & 7)) << 4)) = make_uint4(x, y, z, u);
-              };
-              put(d, codes_f16<0x4140>(even[0]), codes_f16<0x4140>(even[1]), codes_f16<0x4140>(even[2]), codes_f16<0x4140>(even[3]));
-              put(d + 1, codes_f16<0x4342>(even[0]), codes_f16<0x4342>(even[1]), codes_f16<0x4342>(even[2]), codes_f16<0x4342>(even[3]));
-              put(d + 2, codes_f16<0x4140>(odd[0]), codes_f16<0x4140>(odd[1]), codes_f16<0x4140>(odd[2]), codes_f16<0x4140>(odd[3]));
-              put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
-            }
-          }
+        put_values(vt);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.vfull[b]);
+      }
       }
       if constexpr (C::kShift) {
         // not before the softmax warps have given theirs back: a set without a tile would take its
@@ -846,7 +956,37 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       }
     } else if (warp == kSoft * G + kConv + G) {
       // ---------------- copies of the codes ----------------
-      if constexpr (C::kStaged) {
+      if constexpr (SPLIT) {
+        // tile by tile, and the places of the next eight tiles' blocks, one to a lane, before those tiles' copies
+        int keys = copied, values = copied;  // tiles whose copies have been issued
+        bool ok = true;
+        for (int batch = 0; 8 * batch < nt && ok; ++batch) {
+          const int next = 32 * (batch + 1) + lane;
+          BlockAt e{};
+          if (next < 4 * nt) e = block_at(next);
+          while (values < min(nt, 8 * (batch + 1)) && ok) {
+            const int n = values % kSplitSlots, round = values / kSplitSlots - 1;
+            ok = wait(&bars.sread[0][0] + n, round);
+            if (!ok) break;
+            copy_keys(keys++, false);
+            ok = wait(&bars.vread[n], round);
+            if (!ok) break;
+            copy_keys(values++, true);
+          }
+          if (next < 4 * nt) s_blk[next] = e;
+          __syncwarp();
+        }
+        // no copy may be in flight when the CTA ends, also after giving up: each stage's last one
+        if (lane == 0) {
+          bool done = true;
+          for (int i = max(0, keys - kSplitSlots); i < keys; ++i)
+            done = mbar_wait(&bars.stage[0][0] + i % kSplitSlots, uint32_t(i / kSplitSlots) & 1u) && done;
+          for (int i = max(0, values - kSplitSlots); i < values; ++i)
+            done = mbar_wait(&bars.vstage[i % kSplitSlots], uint32_t(i / kSplitSlots) & 1u) && done;
+          if (!done) atomicAdd(&g_attn_tc_timeouts, 1u);
+        }
+        __syncwarp();
+      } else if constexpr (C::kStaged) {
         if (lane == 0) {
           for (; copied < nt; ++copied) {
             const int set = copied % C::kSets, use = copied / C::kSets, n = use % C::kSlots;  // the set's use-th tile
@@ -868,43 +1008,55 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
       // a warp per group: one for both spent longer on its waits than the tensor core on the products
       const int g = warp - (kSoft * G + kConv);
       const uint32_t leader = elect_lane();
-      const uint32_t q_base = smem_u32(smem) + g * C::kSub * C::kQTile, k_base = smem_u32(kring), v_base = smem_u32(vring);
+      const uint32_t q_base = smem_u32(smem) + (SPLIT ? 0 : g * C::kSub * C::kQTile), k_base = smem_u32(kring), v_base = smem_u32(vring);
       const uint32_t s_col = tmem + uint32_t(2 * g * BN), o_col = tmem + C::kOCol + uint32_t(g * D);
-      auto scores = [&](int i) {  // S of tile i
-        const int b = i & 1;
+      const int mine = SPLIT ? (nt - g + 1) / 2 : nt;  // the group's tiles
+      // where the keys and values of the group's t-th tile are, and which use of that place they are
+      auto slot = [&](int t) { return SPLIT ? g : t & 1; };
+      auto use = [&](int t) { return SPLIT ? t : t >> 1; };
+      auto k_slot = [&](int t) { return SPLIT ? (2 * t + g) % C::kKeys : t & 1; };
+      auto keys_there = [&](int t) {
+        if constexpr (SPLIT) return wait(&bars.kfull4[k_slot(t)], (2 * t + g) / C::kKeys);
+        return wait(&bars.kfull[t & 1], t >> 1);
+      };
+      auto scores = [&](int t) {  // S of the t-th tile
+        const int b = t & 1;
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ss(leader, s_col + uint32_t(b * BN), desc_sw128(q_base + part * C::kQPart + (k / 4) * C::kQTile + (k % 4) * 32),
-                   desc_sw128(k_base + b * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
+                   desc_sw128(k_base + k_slot(t) * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
         mma_commit(leader, &bars.sfull[g][b]);
-        mma_commit(leader, &bars.kfree[b]);
+        if constexpr (SPLIT)
+          mma_commit(leader, &bars.kfree4[k_slot(t)]);
+        else
+          mma_commit(leader, &bars.kfree[t & 1]);
       };
       bool ok = true;
-      if (nt > 0) {
-        ok = wait(&bars.kfull[0], 0);
+      if (mine > 0) {
+        ok = keys_there(0);
         if (ok) scores(0);
       }
-      for (int i = 0; i < nt && ok; ++i) {
-        const int b = i & 1;
-        if (i + 1 < nt) {
-          ok = wait(&bars.kfull[b ^ 1], (i + 1) >> 1);
-          // the other S holds the probabilities of tile i - 1 until its products are done
-          if (ok && i >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (i - 1) >> 1);
+      for (int t = 0; t < mine && ok; ++t) {
+        const int b = t & 1;
+        if (t + 1 < mine) {
+          ok = keys_there(t + 1);
+          // the other S holds the probabilities of tile t - 1 until its products are done
+          if (ok && t >= 1) ok = wait(&bars.pvdone[g][b ^ 1], (t - 1) >> 1);
           if (!ok) break;
-          scores(i + 1);
+          scores(t + 1);
         }
-        ok = wait(&bars.vfull[b], i >> 1) && wait(&bars.pready[g][b], i >> 1);
+        ok = wait(&bars.vfull[slot(t)], use(t)) && wait(&bars.pready[g][b], t >> 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
-            mma_ts(leader, o_col, s_col + uint32_t(b * BN + 16 * k + 8 * part), desc_sw128(v_base + b * C::kV + k * 32),
-                   idesc_f16(kTcRows, D), (i | part | k) != 0);
+            mma_ts(leader, o_col, s_col + uint32_t(b * BN + 16 * k + 8 * part), desc_sw128(v_base + slot(t) * C::kV + k * 32),
+                   idesc_f16(kTcRows, D), (t | part | k) != 0);
         mma_commit(leader, &bars.pvdone[g][b]);
       }
       mma_commit(leader, &bars.drain);
@@ -916,13 +1068,24 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     if (!wait(&bars.drain, 0) && lane == 0) atomicAdd(&g_attn_tc_timeouts, 1u);
     tc_fence_after();
     // and every commit's arrival has landed before the barriers are made anew for the next part
-    if (tid == 0 && !*reinterpret_cast<volatile int *>(&bars.abort))
-      for (int b = 0; b < 2 && b < nt; ++b) {
-        const uint32_t last = uint32_t((nt - b + 1) / 2 - 1) & 1u;  // of the (nt - b + 1) / 2 uses
-        bool done = mbar_wait(&bars.kfree[b], last);
-        for (int g = 0; g < G; ++g) done = mbar_wait(&bars.sfull[g][b], last) && mbar_wait(&bars.pvdone[g][b], last) && done;
-        if (!done) give_up();
+    if (tid == 0 && !*reinterpret_cast<volatile int *>(&bars.abort)) {
+      bool done = true;
+      if constexpr (SPLIT) {
+        for (int k = 0; k < C::kKeys && k < nt; ++k) done = mbar_wait(&bars.kfree4[k], uint32_t((nt - 1 - k) / C::kKeys) & 1u) && done;
+        for (int g = 0; g < G; ++g)
+          for (int b = 0; b < 2 && 2 * b + g < nt; ++b) {
+            const uint32_t last = uint32_t(((nt - g + 1) / 2 - 1 - b) / 2) & 1u;  // of the group's tiles
+            done = mbar_wait(&bars.sfull[g][b], last) && mbar_wait(&bars.pvdone[g][b], last) && done;
+          }
+      } else {
+        for (int b = 0; b < 2 && b < nt; ++b) {
+          const uint32_t last = uint32_t((nt - b + 1) / 2 - 1) & 1u;  // of the (nt - b + 1) / 2 uses
+          done = mbar_wait(&bars.kfree[b], last) && done;
+          for (int g = 0; g < G; ++g) done = mbar_wait(&bars.sfull[g][b], last) && mbar_wait(&bars.pvdone[g][b], last) && done;
+        }
       }
+      if (!done) give_up();
+    }
     __syncthreads();
     const bool lost = bad || *reinterpret_cast<volatile int *>(&bars.abort) != 0;
     if (tid == 0 && bars.abort) atomicAdd(&g_attn_tc_timeouts, 1u);
@@ -935,13 +1098,85 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
     const bool another = u.first > kept(bars.total) * u.c_lo / *reinterpret_cast<volatile int *>(&bars.shares);
     auto part_of = [&](int k) { return a.partial + (2 * int64_t(u.c_lo + k) + (k == 0 && another)) * kPart; };  // k-th part
     float *part = part_of(int(blockIdx.x) - u.c_lo);  // [four dims][row][4], maxima, sums
-    if (warp < kSoft * G) {
+    const bool in = lr < nr;
+    float inv = 0.f;
+    // 16 dims of the row from dim c: to the output, or into the part
+    auto emit = [&](int c, const float (&o)[16]) {
+      if (nsplit == 1) {
+        if (in) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) store_out<D>(a, q0, h, row, c + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), inv);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(part + (c + e) * R + 4 * lr) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+    };
+    auto finish = [&]() {
+      if (nsplit == 1) {
+        if (in) store_lse(a, q0, h, row, m, l);
+      } else {
+        part[D * R + lr] = m;
+        part[D * R + R + lr] = l;
+      }
+    };
+    if constexpr (SPLIT) {
+      // The groups are joined: each gives the other half its dims through shared memory, in the place of the tiles, and
+      // writes the other half.  (The second has no tile where the part has one.)
+      __shared__ float s_ml[2][2][kTcRows];
+      float4 *other = reinterpret_cast<float4 *>(kring);  // [four dims][row]
+      const bool some = nt > grp, others = nt > 1 - grp;
+      if (warp < kSoft * G) {
+        if (some) {
+#pragma unroll 1
+          for (int c = (1 - grp) * (D / 2); c < (2 - grp) * (D / 2); c += 16) {
+            uint32_t o[16];
+            tmem_ld16_async(otm + c, o);
+            tmem_wait_ld16(o);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              other[(c + e) / 4 * kTcRows + lr] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                                              __uint_as_float(o[e + 3]));
+          }
+        }
+        s_ml[grp][0][lr] = m;
+        s_ml[grp][1][lr] = l;
+      }
+      __syncthreads();
+      if (warp < kSoft * G) {
+        const float m0 = s_ml[0][0][lr], m1 = s_ml[1][0][lr], top = fmaxf(m0, m1), ref = top == ninf ? 0.f : top;
+        const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+        const float f_own = grp == 0 ? f0 : f1, f_other = grp == 0 ? f1 : f0;
+        l = lost ? qnan : fmaf(s_ml[0][1][lr], f0, s_ml[1][1][lr] * f1);
+        m = top;
+        inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
+#pragma unroll 1
+        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 16) {
+          uint32_t o[16];
+          float v[16];
+          if (some) {
+            tmem_ld16_async(otm + c, o);
+            tmem_wait_ld16(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 x = others ? other[(c + e) / 4 * kTcRows + lr] : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[e] = fmaf(some ? __uint_as_float(o[e]) : 0.f, f_own, x.x * f_other);
+            v[e + 1] = fmaf(some ? __uint_as_float(o[e + 1]) : 0.f, f_own, x.y * f_other);
+            v[e + 2] = fmaf(some ? __uint_as_float(o[e + 2]) : 0.f, f_own, x.z * f_other);
+            v[e + 3] = fmaf(some ? __uint_as_float(o[e + 3]) : 0.f, f_own, x.w * f_other);
+          }
+          emit(c, v);
+        }
+        if (grp == 0) finish();
+      }
+    } else if (warp < kSoft * G) {
       if (lost) l = qnan;
-      const float inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
-      const bool in = lr < nr;
+      inv = l == 0.f ? 0.f : (1.f / kPScale) / l;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
+        float v[16];
         if (nt > 0) {
           tmem_ld16_async(otm + c, o);
           tmem_wait_ld16(o);
@@ -949,30 +1184,15 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = 0;
         }
-        if (nsplit == 1) {
-          if (in) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              store_out<D>(a, q0, h, row, c + e,
-                           make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                       __uint_as_float(o[e + 3])),
-                           inv);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4 *>(part + (c + e) * R + 4 * lr) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
+        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]);
+        emit(c, v);
       }
-      if (nsplit == 1) {
-        if (in) store_lse(a, q0, h, row, m, l);
-      } else {
-        part[D * R + lr] = m;
-        part[D * R + R + lr] = l;
-      }
+      finish();
     }
     tc_fence_before();
-    if (nsplit > 1) {
+    // (a tree's parts are joined by another kernel)
+    if (!TREE && nsplit > 1) {
       // The CTA that finishes last joins the parts, in order.  Their accumulators (32 or 64 dims of all rows
       // at a time) and references come through a ring of bulk copies in the space of the tiles; a warp takes
       // 16 dims of 8 rows at a time, whole sectors of the output.  (Plain loads, 4 of 16 bytes in flight per thread,
@@ -1092,20 +1312,103 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G>::kThreads, 1) attn_tc_kernel(
   }
 }
 
+// A tree's parts, joined in order: a CTA takes 16 dims of a unit's rows (one CTA for all of them took 50 us for 38 parts
+// of 128 rows of 128).  The line of work is found as the CTAs of the attention found it.
+template <int D>
+__global__ void __launch_bounds__(kTcRows) attn_tree_join_kernel(const AttnArgs a) {
+  __shared__ long long s_sum[2][kTcRows / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kSlices = D / 16, kPart = kTcRows * (D + 2);
+  const float ninf = __int_as_float(0xff800000);
+  const int slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices, h = unit % a.c.n_kv, e = unit / a.c.n_kv;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n_entries = a.n_seqs * a.tiles;
+  long long before = 0, total = 0;
+  for (int i = tid; i < n_entries; i += kTcRows) {
+    const int tiles = tc_entry<true>(a, i, kTcRows).tiles;
+    const int line = tiles ? tiles + kTcPartCost : 0;
+    total += line;
+    if (i < e) before += line;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    s_sum[0][warp] = before;
+    s_sum[1][warp] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < kTcRows / 32; ++w) {
+    before += s_sum[0][w];
+    total += s_sum[1][w];
+  }
+  before *= a.c.n_kv;
+  total *= a.c.n_kv;
+  const TcEntry en = tc_entry<true>(a, e, kTcRows);
+  if (en.tiles == 0) return;
+  const int shares = int(min((long long)a.splits, max(1ll, total / kMinShare)));
+  auto owner = [&](long long g) { return int(((g + 1) * shares - 1) / total); };
+  const long long first = before + (long long)h * (en.tiles + kTcPartCost);
+  const int c_lo = owner(first + kTcPartCost), nsplit = owner(first + kTcPartCost + en.tiles - 1) - c_lo + 1;
+  if (nsplit == 1 || tid >= en.nr) return;
+  const bool another = first > total * c_lo / shares;
+  const float4 *p = reinterpret_cast<const float4 *>(a.partial + 2 * int64_t(c_lo) * kPart) + (4 * slice) * kTcRows + tid;
+  const float *q = a.partial + 2 * int64_t(c_lo) * kPart + D * kTcRows + tid;
+  if (another) {  // the unit's first part is its CTA's second
+    p += kPart / 4;
+    q += kPart;
+  }
+  float M = ninf, L = 0.f;
+  float4 v[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < nsplit; ++k) {
+    const float mk = __ldcg(q), lk = __ldcg(q + kTcRows);
+    float4 x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = __ldcg(p + c * kTcRows);
+    const int64_t step = 2 * int64_t(kPart) - (k == 0 && another ? kPart : 0);
+    p += step / 4;
+    q += step;
+    const float top = fmaxf(M, mk), ref = top == ninf ? 0.f : top, f = ex2(M - ref), w = ex2(mk - ref);
+    M = top;
+    L = fmaf(lk, w, L * f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      v[c] = make_float4(fmaf(x[c].x, w, v[c].x * f), fmaf(x[c].y, w, v[c].y * f), fmaf(x[c].z, w, v[c].z * f), fmaf(x[c].w, w, v[c].w * f));
+  }
+  const float inv = L == 0.f ? 0.f : (1.f / kPScale) / L;
+  const int64_t to = out_at<D>(a, en.q0, h, en.r0 + tid) + 16 * slice;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) store_at(a, to + 4 * c, v[c], inv);
+  if (slice == 0) store_lse(a, en.q0, h, en.r0 + tid, M, L);
+}
+
 template <bool TREE, int D, int PARTS, int G>
 cudaError_t run(const AttnArgs &a, cudaStream_t s) {
-  using C = Cfg<D, PARTS, G>;
+  using C = Cfg<D, PARTS, G, TREE && G == 2>;
   const auto kernel = a.softcap > 0.f || a.slopes ? attn_tc_kernel<D, PARTS, G, true, TREE> : attn_tc_kernel<D, PARTS, G, false, TREE>;
-  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(C::kSmem));
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), int(C::kSmem));
   if (e != cudaSuccess) return e;
-  return launch(kernel, dim3(a.splits), dim3(C::kThreads), C::kSmem, s, a);
+  e = launch(kernel, dim3(a.splits), dim3(C::kThreads), C::kSmem, s, a);
+  if constexpr (TREE) {
+    if (e == cudaSuccess) e = launch(attn_tree_join_kernel<D>, dim3(unsigned(a.units * (D / 16))), dim3(kTcRows), 0, s, a);
+  }
+  return e;
 }
 template <bool TREE, int D, int PARTS>
 cudaError_t run(const AttnArgs &a, int groups, cudaStream_t s) {
-  if constexpr (D <= 128) {
-    if (groups == 2) return run<TREE, D, PARTS, 2>(a, s);
+  if constexpr (TREE) return run<true, D, PARTS, D <= 128 ? 2 : 1>(a, s);
+  if constexpr (!TREE && D <= 128) {
+    if (groups == 2) return run<false, D, PARTS, 2>(a, s);
   }
-  return run<TREE, D, PARTS, 1>(a, s);
+  if constexpr (!TREE) return run<false, D, PARTS, 1>(a, s);
 }
 template <bool TREE>
 cudaError_t run_attn_tc(const AttnArgs &a, int head_dim, int parts, int groups, cudaStream_t s) {
