@@ -14,7 +14,7 @@ namespace {
 constexpr int BN = 64;  // tokens per tile
 constexpr int kMinShare = 8;  // places on the line: a shorter share saves less than its part costs
 constexpr int kJoinSlots = 3;  // for joining parts
-constexpr int kSplitSlots = 4;  // stages of keys and of values where the converting sets take one each
+constexpr int kPairs = 2;  // pairs of tiles whose codes are on the way or waiting (SPLIT)
 constexpr int kSoft = 4, kSet = 4;  // softmax warps per group of rows, warps per converting set
 
 // ---- tcgen05 --------------------------------------------------------------------
@@ -100,7 +100,7 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
 constexpr uint32_t idesc_f16(int m, int n) { return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24); }
 
 // SPLIT: the two groups take alternate tiles of the same 128 rows, each with a tile of keys and one of values of its
-// own, and are joined at the end of a part; one converting set takes the keys of every tile, the other the values.
+// own, and are joined at the end of a part; one converting set takes the keys of the groups' tiles, the other the values.
 template <int D, int PARTS, int G, bool SPLIT>
 struct Cfg {
   static constexpr int kSub = D / 64;                    // 64-dim sub-tiles
@@ -108,7 +108,7 @@ struct Cfg {
   static constexpr int kRows = SPLIT ? 1 : G;            // groups of rows
   static constexpr uint32_t kQPart = kRows * kSub * kQTile;  // [group][sub-tile]
   static constexpr uint32_t kK = kSub * BN * 128, kV = D * 128;
-  // tiles of keys: two for each group of SPLIT where they fit (two parts of queries leave no room)
+  // tiles of keys: two pairs for SPLIT where they fit (two parts of queries leave no room)
   static constexpr int kKeys = SPLIT && PARTS == 1 ? 4 : 2;
   static constexpr uint32_t kRing = PARTS * kQPart + kKeys * kK + 2 * kV;
   static constexpr uint32_t kOCol = 2 * BN * G;  // S of group 0 (two), of group 1 (two) | O of group 0, of group 1
@@ -119,7 +119,9 @@ struct Cfg {
   // warps' proxy fences wait for a thread's loads in flight, not for these); 256 dims: no
   // room, plain loads.
   static constexpr bool kStaged = D <= 192;
-  static constexpr uint32_t kStageV = BN * D, kVStep = 8 * D + 16;
+  // (SPLIT: a pair of tiles' keys, then their values, unpadded, so that blocks that lie behind one another in a page come in
+  // one copy; the lanes that read 8 tokens' words take different dims of them there)
+  static constexpr uint32_t kStageV = BN * D, kVStep = 8 * D + (SPLIT ? 0 : 16);
   static constexpr uint32_t kStage = (kStageV + 8 * kVStep + 127) / 128 * 128;
   static constexpr int kMaxBlocks = SPLIT ? kTcTreeBlocks : kTcSplitBlocks;  // of one part
   static constexpr uint32_t kFixed = 1024 + kRing + kMaxBlocks * uint32_t(sizeof(BlockAt));
@@ -133,7 +135,7 @@ struct Cfg {
   // more than half an SM's shared memory: one CTA per SM, as the columns of TMEM want it
   static constexpr uint32_t kSmem = kBytes > 116 * 1024 ? kBytes : 116 * 1024;
   static_assert(kSmem <= 225 * 1024, "shared memory");
-  static_assert(!SPLIT || kSets * kSlots == kSplitSlots, "stages");
+  static_assert(!SPLIT || kSets * kSlots == 2 * kPairs, "stages");
   static constexpr int kConv = kSet * kSets;
   static constexpr int kThreads = 32 * (kSoft * G + kConv + G + 1);
   // joining parts: columns of 4 dims in a slot, warps that add
@@ -147,15 +149,15 @@ struct Cfg {
 
 template <int N>
 struct MoreBars {
-  uint64_t vstage[N], vread[N], kfull4[N], kfree4[N];
+  uint64_t kstage[N], kread[N], vstage[N], vread[N], kfull2[N], kfree2[N];
 };
 template <>
 struct MoreBars<0> {};
-// (SPLIT: stage and sread are of the keys, vstage and vread of the values)
+// (SPLIT: those of a pair of tiles, one for each group; stage, sread, kfull and kfree stay unused, of vfull one is used)
 template <int G, bool SPLIT>
-struct Bars : MoreBars<SPLIT ? kSplitSlots : 0> {
+struct Bars : MoreBars<SPLIT ? kPairs : 0> {
   uint64_t stage[2][2], sread[2][2], kfull[2], vfull[2], kfree[2], sfull[G][2], pready[G][2], pvdone[G][2], drain, joined[kJoinSlots];
-  static constexpr int kBars = 8 + 6 + 6 * G + 1 + kJoinSlots + (SPLIT ? 4 * kSplitSlots : 0);
+  static constexpr int kBars = 8 + 6 + 6 * G + 1 + kJoinSlots + (SPLIT ? 6 * kPairs : 0);
   long long sums[20], first, g0, g1, total;  // the share's state, kept here while a part runs (registers are short)
   uint32_t tmem;
   int abort, last, entry, shares;
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
         mbar_init(&bars.sread[1][i], kSet);
         mbar_init(&bars.kfull[i], kSet);
         mbar_init(&bars.vfull[i], kSet);
-        mbar_init(&bars.kfree[i], SPLIT ? 1 : G);
+        mbar_init(&bars.kfree[i], G);
         for (int g = 0; g < G; ++g) {
           mbar_init(&bars.sfull[g][i], 1);
           mbar_init(&bars.pready[g][i], kSoft);
@@ -331,11 +333,13 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
         }
       }
       if constexpr (SPLIT)
-        for (int i = 0; i < kSplitSlots; ++i) {
+        for (int i = 0; i < kPairs; ++i) {
+          mbar_init(&bars.kstage[i], 1);
+          mbar_init(&bars.kread[i], kSet);
           mbar_init(&bars.vstage[i], 1);
           mbar_init(&bars.vread[i], kSet);
-          mbar_init(&bars.kfull4[i], kSet);
-          mbar_init(&bars.kfree4[i], 1);
+          mbar_init(&bars.kfull2[i], kSet);
+          mbar_init(&bars.kfree2[i], G);
         }
       mbar_init(&bars.drain, G);
       for (int i = 0; i < kJoinSlots; ++i) mbar_init(&bars.joined[i], 1);
@@ -361,32 +365,29 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
       }
       return e;
     };
-    // copies of tile i's keys or values into their stage (SPLIT), by a whole warp: a lane for each (one lane after the other
-    // took 0.4 us a tile)
-    auto copy_keys = [&](int i, bool values) {
+    // copies of the p-th pair of tiles' keys or values into their stage (SPLIT), by a whole warp: a lane for each run of blocks
+    // that lie behind one another.  (Bulk copies cost by their number: 24 of 1 and 2 KB a pair set the pace at 0.8 us a tile.)
+    auto copy_pair = [&](int p, bool values) {
       if constexpr (SPLIT) {
-        const int n = i % kSplitSlots, piece = values ? lane >> 1 : lane;  // of the tile's four blocks
-        uint8_t *dst = stages + n * C::kStage;
-        uint64_t *bar = values ? &bars.vstage[n] : &bars.stage[0][0] + n;
-        const int64_t at = piece < 4 ? s_blk[4 * i + piece].k : -1;  // no such block: its part of the stage is not read
-        const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(__popc(have)) * (values ? 8 : 16) * D);
+        const int n = p % kPairs;
+        uint64_t *bar = values ? &bars.vstage[n] : &bars.kstage[n];
+        const int64_t at = lane < 8 && 8 * p + lane < 4 * nt ? s_blk[8 * p + lane].k : -1;  // no such block: not read
+        const int64_t prev = __shfl_up_sync(0xffffffffu, (long long)at, 1);
+        const bool first = at >= 0 && (lane == 0 || prev < 0 || at != prev + 16 * D);
+        const uint32_t have = __ballot_sync(0xffffffffu, at >= 0), ends = __ballot_sync(0xffffffffu, first) | ~have;
+        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(__popc(have)) * 16 * D);
         __syncwarp();
-        if (at >= 0) {
-          if (values)
-            bulk_copy_g2s(dst + C::kStageV + lane * C::kVStep, a.c.pages + at + vplane + (lane & 1) * 8 * D, 8 * D, bar);
-          else
-            bulk_copy_g2s(dst + lane * 16 * D, a.c.pages + at, 16 * D, bar);
+        if (first) {
+          const uint32_t bytes = uint32_t(__ffs(int(ends >> (lane + 1)))) * 16 * D;
+          bulk_copy_g2s(stages + 2 * n * C::kStage + (values ? 2 * C::kStageV : 0) + lane * 16 * D,
+                        a.c.pages + at + (values ? vplane : 0), bytes, bar);
         }
         __syncwarp();
       }
     };
     // copies of tile i's codes into its stage
     auto copy_tile = [&](int i) {
-      if constexpr (SPLIT) {
-        copy_keys(i, false);
-        copy_keys(i, true);
-      } else if constexpr (C::kStaged) {
+      if constexpr (C::kStaged) {
         const int set = i % C::kSets, n = i / C::kSets % C::kSlots;
         uint8_t *dst = stages + (set * C::kSlots + n) * C::kStage;
         uint64_t *bar = &bars.stage[set][n];
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
         }
       }
     };
-    int copied = 0;  // tiles whose copies have been issued (the copying lane's)
+    int copied = 0;  // tiles (SPLIT: pairs) whose copies have been issued (the copying lane's, or warp's)
     // the queries, scaled by a power of two per row, into f16 parts: D / 8 lanes to a row.  A lane
     // copies its 8 dims of all its rows into the tiles' space first (all copies in flight at once,
     // each read back by the lane that made it) and converts them in a small loop.
@@ -517,7 +518,10 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
         }
         named_bar_sync(4, 32 * (G + 1));
         if (warp == kSoft * G + kConv + G)
-          for (; copied < min(nt, kSplitSlots); ++copied) copy_tile(copied);
+          for (; 2 * copied < nt && copied < kPairs; ++copied) {
+            copy_pair(copied, false);
+            copy_pair(copied, true);
+          }
       } else if constexpr (C::kStaged) {  // and the first tiles' copies
         named_bar_sync(4, 32 * (G + 1));
         if (tid == 32 * (kSoft * G + kConv + G))
@@ -831,68 +835,73 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
           *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
       };
-      auto put_values = [&](uint8_t *vt) {
+      // (8 tokens, chunk vc, of 8 dims from d0)
+      auto put_values = [&](uint8_t *vt, const uint2 (&v)[8], int d0, int vc) {
 #pragma unroll
-        for (int g = 0; g < VG; ++g)
-          if (w + 4 * g < D / 32) {
+        for (int hw = 0; hw < 2; ++hw) {  // four dims
+          uint32_t even[4], odd[4];       // pairs of tokens: dims 0, 1 and dims 2, 3
 #pragma unroll
-            for (int hw = 0; hw < 2; ++hw) {  // four dims
-              uint32_t even[4], odd[4];       // pairs of tokens: dims 0, 1 and dims 2, 3
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const uint32_t x = (hw ? vq[g][2 * t].y : vq[g][2 * t].x) ^ 0x80808080u;
-                const uint32_t y = (hw ? vq[g][2 * t + 1].y : vq[g][2 * t + 1].x) ^ 0x80808080u;
-                even[t] = __byte_perm(x, y, 0x5140);
-                odd[t] = __byte_perm(x, y, 0x7362);
-              }
-              const int d = (w + 4 * g) * 32 + vd * 8 + hw * 4;
-              auto put = [&](int dd, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
-                *reinterpret_cast<uint4 *>(vt + dd * 128 + ((vtc ^ (dd & 7)) << 4)) = make_uint4(x, y, z, u);
-              };
-              put(d, codes_f16<0x4140>(even[0]), codes_f16<0x4140>(even[1]), codes_f16<0x4140>(even[2]), codes_f16<0x4140>(even[3]));
-              put(d + 1, codes_f16<0x4342>(even[0]), codes_f16<0x4342>(even[1]), codes_f16<0x4342>(even[2]), codes_f16<0x4342>(even[3]));
-              put(d + 2, codes_f16<0x4140>(odd[0]), codes_f16<0x4140>(odd[1]), codes_f16<0x4140>(odd[2]), codes_f16<0x4140>(odd[3]));
-              put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
-            }
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t x = (hw ? v[2 * t].y : v[2 * t].x) ^ 0x80808080u;
+            const uint32_t y = (hw ? v[2 * t + 1].y : v[2 * t + 1].x) ^ 0x80808080u;
+            even[t] = __byte_perm(x, y, 0x5140);
+            odd[t] = __byte_perm(x, y, 0x7362);
           }
+          const int d = d0 + hw * 4;
+          auto put = [&](int dd, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+            *reinterpret_cast<uint4 *>(vt + dd * 128 + ((vc ^ (dd & 7)) << 4)) = make_uint4(x, y, z, u);
+          };
+          put(d, codes_f16<0x4140>(even[0]), codes_f16<0x4140>(even[1]), codes_f16<0x4140>(even[2]), codes_f16<0x4140>(even[3]));
+          put(d + 1, codes_f16<0x4342>(even[0]), codes_f16<0x4342>(even[1]), codes_f16<0x4342>(even[2]), codes_f16<0x4342>(even[3]));
+          put(d + 2, codes_f16<0x4140>(odd[0]), codes_f16<0x4140>(odd[1]), codes_f16<0x4140>(odd[2]), codes_f16<0x4140>(odd[3]));
+          put(d + 3, codes_f16<0x4342>(odd[0]), codes_f16<0x4342>(odd[1]), codes_f16<0x4342>(odd[2]), codes_f16<0x4342>(odd[3]));
+        }
       };
       if constexpr (SPLIT) {
-        for (int i = 0; i < nt; ++i) {
-          const int n = i % kSplitSlots, round = i / kSplitSlots, b = i & 1;
-          const uint8_t *st = stages + n * C::kStage;
+        // a pair of tiles at a time: waits, fence and arrivals cost as much as the conversion of one
+        constexpr int kKeyPairs = C::kKeys / 2;
+        for (int p = 0; 2 * p < nt; ++p) {
+          const int n = p % kPairs, tiles = min(2, nt - 2 * p);
           if (set == 0) {
-            if (!wait(&bars.stage[0][0] + n, round)) break;
-            const int64_t ak = s_blk[4 * i + w].k;
+            const int k = p % kKeyPairs;
+            if (!wait(&bars.kstage[n], p / kPairs)) break;
+            if (p >= kKeyPairs && !wait(&bars.kfree2[k], p / kKeyPairs - 1)) break;  // S of the tiles that were there is done
+            for (int x = 0; x < tiles; ++x) {
+              const uint8_t *st = stages + 2 * n * C::kStage + x * C::kStageV;
+              const int64_t ak = s_blk[8 * p + 4 * x + w].k;
 #pragma unroll
-            for (int j = 0; j < KL; ++j)
-              kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.sread[0][0] + n);
-            const int k = i % C::kKeys;
-            if (i >= C::kKeys && !wait(&bars.kfree4[k], i / C::kKeys - 1)) break;  // S of the tile that was there is done
-            put_keys(kring + k * C::kK);
+              for (int j = 0; j < KL; ++j)
+                kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
+              put_keys(kring + (2 * k + x) * C::kK);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.kfull4[k]);
+            if (lane == 0) {
+              mbar_arrive(&bars.kread[n]);
+              mbar_arrive(&bars.kfull2[k]);
+            }
           } else {
-            if (!wait(&bars.vstage[n], round)) break;
-            const int64_t av = s_blk[4 * i + vtc / 2].k;
+            if (!wait(&bars.vstage[n], p / kPairs)) break;
+            // P V of the pair before
+            if (p >= 1 && !(wait(&bars.pvdone[0][(p - 1) & 1], (p - 1) >> 1) && wait(&bars.pvdone[1][(p - 1) & 1], (p - 1) >> 1))) break;
+            for (int x = 0; x < tiles; ++x) {
+              // A thread's 8 tokens and 8 dims: 16 lanes take 16 different dims (8 of them twice, heads of 64) of their
+              // tokens, 8 lanes 8 different chunks of tokens, so that neither the reads nor the stores meet in one bank.
+              if (D == 64 && w / 2 != x) continue;
+              const int q = lane & 15, k = 2 * (D == 64 ? w & 1 : w) + (lane >> 4), vc = q & 7;
+              const int d0 = D == 64 ? ((q + k + (q >> 3) * 4) & 7) * 8 : ((q + k) & 15) * 8;
+              const uint8_t *st = stages + 2 * n * C::kStage + 2 * C::kStageV + x * C::kStageV + vc * 8 * D + d0;
+              const int64_t av = s_blk[8 * p + 4 * x + vc / 2].k;
 #pragma unroll
-            for (int g = 0; g < VG; ++g)
-              if (w + 4 * g < D / 32) {
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                  vq[g][t] = av < 0 ? make_uint2(0, 0)
-                                    : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
-              }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.vread[n]);
-            const int t = (i >> 1) - 1;  // P V of tile i - 2, the group's t-th
-            if (i >= 2 && !wait(&bars.pvdone[b][t & 1], t >> 1)) break;
-            put_values(vring + b * C::kV);
+              for (int t = 0; t < 8; ++t) vq[0][t] = av < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(st + t * D);
+              put_values(vring + x * C::kV, vq[0], d0, vc);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.vfull[b]);
+            if (lane == 0) {
+              mbar_arrive(&bars.vread[n]);
+              mbar_arrive(&bars.vfull[0]);
+            }
           }
         }
       } else {
@@ -942,7 +951,9 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars.kfull[b]);
         // P V of tile i - 2: its values' tile is free
         if (i >= 2 && !(wait(&bars.pvdone[0][b], (i - 2) >> 1) && (G == 1 || wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)))) break;
-        put_values(vt);
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+          if (w + 4 * g < D / 32) put_values(vt, vq[g], (w + 4 * g) * 32 + vd * 8, vtc);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.vfull[b]);
@@ -958,20 +969,20 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
       // ---------------- copies of the codes ----------------
       if constexpr (SPLIT) {
         // tile by tile, and the places of the next eight tiles' blocks, one to a lane, before those tiles' copies
-        int keys = copied, values = copied;  // tiles whose copies have been issued
+        int keys = copied, values = copied;  // pairs whose copies have been issued
         bool ok = true;
         for (int batch = 0; 8 * batch < nt && ok; ++batch) {
           const int next = 32 * (batch + 1) + lane;
           BlockAt e{};
           if (next < 4 * nt) e = block_at(next);
-          while (values < min(nt, 8 * (batch + 1)) && ok) {
-            const int n = values % kSplitSlots, round = values / kSplitSlots - 1;
-            ok = wait(&bars.sread[0][0] + n, round);
+          while (2 * values < min(nt, 8 * (batch + 1))) {
+            const int n = values % kPairs, round = values / kPairs - 1;
+            ok = wait(&bars.kread[n], round);
             if (!ok) break;
-            copy_keys(keys++, false);
+            copy_pair(keys++, false);
             ok = wait(&bars.vread[n], round);
             if (!ok) break;
-            copy_keys(values++, true);
+            copy_pair(values++, true);
           }
           if (next < 4 * nt) s_blk[next] = e;
           __syncwarp();
@@ -979,10 +990,9 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
         // no copy may be in flight when the CTA ends, also after giving up: each stage's last one
         if (lane == 0) {
           bool done = true;
-          for (int i = max(0, keys - kSplitSlots); i < keys; ++i)
-            done = mbar_wait(&bars.stage[0][0] + i % kSplitSlots, uint32_t(i / kSplitSlots) & 1u) && done;
-          for (int i = max(0, values - kSplitSlots); i < values; ++i)
-            done = mbar_wait(&bars.vstage[i % kSplitSlots], uint32_t(i / kSplitSlots) & 1u) && done;
+          for (int i = max(0, keys - kPairs); i < keys; ++i) done = mbar_wait(&bars.kstage[i % kPairs], uint32_t(i / kPairs) & 1u) && done;
+          for (int i = max(0, values - kPairs); i < values; ++i)
+            done = mbar_wait(&bars.vstage[i % kPairs], uint32_t(i / kPairs) & 1u) && done;
           if (!done) atomicAdd(&g_attn_tc_timeouts, 1u);
         }
         __syncwarp();
@@ -1011,13 +1021,17 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
       const uint32_t q_base = smem_u32(smem) + (SPLIT ? 0 : g * C::kSub * C::kQTile), k_base = smem_u32(kring), v_base = smem_u32(vring);
       const uint32_t s_col = tmem + uint32_t(2 * g * BN), o_col = tmem + C::kOCol + uint32_t(g * D);
       const int mine = SPLIT ? (nt - g + 1) / 2 : nt;  // the group's tiles
-      // where the keys and values of the group's t-th tile are, and which use of that place they are
-      auto slot = [&](int t) { return SPLIT ? g : t & 1; };
-      auto use = [&](int t) { return SPLIT ? t : t >> 1; };
-      auto k_slot = [&](int t) { return SPLIT ? (2 * t + g) % C::kKeys : t & 1; };
+      // where the keys and values of the group's t-th tile are, and whether they are there
+      constexpr int kKeyPairs = C::kKeys / 2;
+      auto k_slot = [&](int t) { return SPLIT ? t % kKeyPairs * 2 + g : t & 1; };
+      auto v_slot = [&](int t) { return SPLIT ? g : t & 1; };
       auto keys_there = [&](int t) {
-        if constexpr (SPLIT) return wait(&bars.kfull4[k_slot(t)], (2 * t + g) / C::kKeys);
+        if constexpr (SPLIT) return wait(&bars.kfull2[t % kKeyPairs], t / kKeyPairs);
         return wait(&bars.kfull[t & 1], t >> 1);
+      };
+      auto values_there = [&](int t) {
+        if constexpr (SPLIT) return wait(&bars.vfull[0], t);
+        return wait(&bars.vfull[t & 1], t >> 1);
       };
       auto scores = [&](int t) {  // S of the t-th tile
         const int b = t & 1;
@@ -1030,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
                    desc_sw128(k_base + k_slot(t) * C::kK + (k / 4) * (BN * 128) + (k % 4) * 32), idesc_f16(kTcRows, BN), (part | k) != 0);
         mma_commit(leader, &bars.sfull[g][b]);
         if constexpr (SPLIT)
-          mma_commit(leader, &bars.kfree4[k_slot(t)]);
+          mma_commit(leader, &bars.kfree2[t % kKeyPairs]);
         else
           mma_commit(leader, &bars.kfree[t & 1]);
       };
@@ -1048,16 +1062,21 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
           if (!ok) break;
           scores(t + 1);
         }
-        ok = wait(&bars.vfull[slot(t)], use(t)) && wait(&bars.pready[g][b], t >> 1);
+        ok = values_there(t) && wait(&bars.pready[g][b], t >> 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
-            mma_ts(leader, o_col, s_col + uint32_t(b * BN + 16 * k + 8 * part), desc_sw128(v_base + slot(t) * C::kV + k * 32),
+            mma_ts(leader, o_col, s_col + uint32_t(b * BN + 16 * k + 8 * part), desc_sw128(v_base + v_slot(t) * C::kV + k * 32),
                    idesc_f16(kTcRows, D), (t | part | k) != 0);
         mma_commit(leader, &bars.pvdone[g][b]);
+      }
+      if constexpr (SPLIT) {
+        // a last pair of one tile: its keys' place is free of the second group, too (not before the pair is there: the
+        // first group may still have to free the pair before)
+        if (g == 1 && (nt & 1) && ok && keys_there(nt >> 1)) mma_commit(leader, &bars.kfree2[(nt >> 1) % kKeyPairs]);
       }
       mma_commit(leader, &bars.drain);
     }
@@ -1071,7 +1090,9 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
     if (tid == 0 && !*reinterpret_cast<volatile int *>(&bars.abort)) {
       bool done = true;
       if constexpr (SPLIT) {
-        for (int k = 0; k < C::kKeys && k < nt; ++k) done = mbar_wait(&bars.kfree4[k], uint32_t((nt - 1 - k) / C::kKeys) & 1u) && done;
+        const int pairs = (nt + 1) / 2;
+        for (int k = 0; k < C::kKeys / 2 && k < pairs; ++k)
+          done = mbar_wait(&bars.kfree2[k], uint32_t((pairs - 1 - k) / (C::kKeys / 2)) & 1u) && done;
         for (int g = 0; g < G; ++g)
           for (int b = 0; b < 2 && 2 * b + g < nt; ++b) {
             const uint32_t last = uint32_t(((nt - g + 1) / 2 - 1 - b) / 2) & 1u;  // of the group's tiles
