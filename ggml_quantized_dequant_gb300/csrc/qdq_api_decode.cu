@@ -85,7 +85,7 @@ int attention(const void *pages, int n_pages, int page_tokens, int n_kv, int hea
   for (const Span &i : in)
     if (clash(i, so) || clash(i, sl) || clash(i, sws)) return QDQ_ERR_ALIAS;
   if (clash(so, sl) || clash(so, sws) || clash(sl, sws)) return QDQ_ERR_ALIAS;
-  const size_t need = kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim);
+  const size_t need = kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, parent != nullptr);
   if (workspace_bytes < need) return QDQ_ERR_SCRATCH;
   const KvPool c{static_cast<uint8_t *>(const_cast<void *>(pages)), page_table, n_pages, page_tokens, n_kv, table_stride};
   return launch_kv_attention(c, head_dim, kv_len, cu_q, parent, n_seqs, max_q, max_kv_len, n_heads, q, q_stride, out, out_stride, lse,
@@ -180,7 +180,9 @@ size_t qdq_kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, i
   if (n_seqs < 1 || max_q < 1 || max_kv_len < 0 || max_kv_len > QDQ_MAX_KV_LEN || n_kv < 1 || n_heads < 1 || n_heads % n_kv || !dim_ok(head_dim) ||
       max_q > (1 << 20) || n_heads / n_kv > 1024)
     return 0;
-  return kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim);
+  const size_t b = kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, false);
+  const size_t tree = max_q <= QDQ_MAX_TREE ? kv_attention_workspace_bytes(n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, true) : 0;
+  return b > tree ? b : tree;
 }
 
 int qdq_kv_attention(const void *pages, int n_pages, int page_tokens, int n_kv, int head_dim, const int *page_table,

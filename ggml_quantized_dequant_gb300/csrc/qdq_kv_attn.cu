@@ -42,6 +42,12 @@ namespace {
 // 300 queries over 600 f32 21 43; heads of 64, 512 queries over themselves f32 20 34, bf16 29 30.
 constexpr int kTcMinRows = 64, kTcMinTokens = 6000;
 constexpr int64_t kTcMinWork = 340'000'000;
+// The same for trees, whose tensor-core kernel is another one (qdq_kv_tree_tc.cu).  Us there and here, 24 / 8 heads of 128
+// bf16: one sequence of 131071 tokens, 18 rows 132 112, 39 rows 131 165, 96 rows 131 323; 16 of 300 to 6000, 18 rows 74
+// 80, 39 rows 75 104, 96 rows 77 171; 48 of 300 to 3000, 18 rows 119 105, 39 rows 122 142; 9 of 200 to 6001 f16, heads of 64,
+// 248 rows, cap, bias and a window of 1500 35 32.
+constexpr int kTreeMinRows = 32;
+constexpr int64_t kTreeMinWork = 600'000'000;
 
 struct Plan {
   bool tc;  // the tensor-core kernel of qdq_kv_attn_tc.cu
@@ -62,10 +68,11 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
   const bool few = small <= di.sm_count && max_kv_len / (di.sm_count / small) <= kTcMinTokens;
   // Blocks without a window.  A window's are never more, or its plan could want a larger workspace.
   const int64_t all_blocks = (int64_t(max_kv_len) + kKvBlock - 1) / kKvBlock;
-  const int64_t tokens_seen = std::max<int64_t>(1, int64_t(max_kv_len) - max_q / 2);
-  const bool light = int64_t(n_seqs) * n_kv * rows * head_dim <= kTcMinWork / tokens_seen;
+  const int64_t far = tree && window > 0 ? std::min<int64_t>(max_kv_len, int64_t(window) + max_q) : max_kv_len;
+  const int64_t tokens_seen = std::max<int64_t>(1, far - max_q / 2);
+  const bool light = int64_t(n_seqs) * n_kv * rows * head_dim <= (tree ? kTreeMinWork : kTcMinWork) / tokens_seen;
   const int forced = g_opt_attn_kernel.load(std::memory_order_relaxed);
-  p.tc = (forced == 2 || (forced == 0 && rows > kTcMinRows && !few && !light)) && (type == QDQ_TYPE_F32 || p.parts == 1) &&
+  p.tc = (forced == 2 || (forced == 0 && rows > (tree ? kTreeMinRows : kTcMinRows) && !few && !light)) && (type == QDQ_TYPE_F32 || p.parts == 1) &&
          attn_tc_supported(head_dim, p.parts);
   if (p.tc) {
     p.groups = rows > kTcRows && head_dim <= 128 && !tree ? 2 : 1;
@@ -132,12 +139,12 @@ Plan plan(const DeviceInfo &di, int n_seqs, int max_q, int max_kv_len, int n_hea
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim) {
+size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, bool tree) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return 0;
   size_t most = 0;  // enough for every element type
   for (int type : {QDQ_TYPE_F32, QDQ_TYPE_BF16}) {
-    const size_t b = plan(di, n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, 0, type).bytes;
+    const size_t b = plan(di, n_seqs, max_q, max_kv_len, n_heads, n_kv, head_dim, 0, type, tree).bytes;
     if (b > most) most = b;
   }
   return most;

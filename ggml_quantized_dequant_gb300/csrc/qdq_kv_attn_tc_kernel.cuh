@@ -143,8 +143,10 @@ struct Cfg {
   static constexpr int kJoinQuads = join_bytes(16) <= kSmem ? 16 : 8, kJoinWarps = kThreads >= 512 ? 16 : 8;
   static_assert(join_bytes(kJoinQuads) <= kSmem, "room for the join");
   // 19 warps are launched with 96 registers a thread: 8 softmax warps x 128 + 8 converting x 64
-  // + 3 x 96 = 19 x 96; all have 96 again for the output
+  // + 3 x 96 = 19 x 96; all have 96 again for the output.  (SPLIT: what spills less: 131071 tokens bf16 136 us with
+  // 128 and 64, 130 with 112 and 80, f32 164 and, with 120 and 72, 160.)
   static constexpr bool kShift = G == 2 && kSets == 2;
+  static constexpr int kSoftRegs = !SPLIT ? 128 : PARTS == 1 ? 112 : 120, kConvRegs = 192 - kSoftRegs;
 };
 
 template <int N>
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t otm = tmem + lanes + C::kOCol + uint32_t(grp * D);  // its O
     if (warp < kSoft * G) {
-      if constexpr (C::kShift) reg_inc<128>();
+      if constexpr (C::kShift) reg_inc<C::kSoftRegs>();
       const int qi = int(a.query_of(row));
       const int base = len - nq;  // a tree's first key
       const int pos = base + (TREE ? s_tree.depth_of(qi) : qi);
@@ -801,7 +803,7 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
       }
     } else if (warp < kSoft * G + kConv) {
       // ---------------- codes to f16 tiles ----------------
-      if constexpr (C::kShift) reg_dec<64>();
+      if constexpr (C::kShift) reg_dec<C::kConvRegs>();
       const int set = (warp - kSoft * G) / kSet, w = (warp - kSoft * G) % kSet;  // tiles set, set + kSets, ...
       constexpr int KL = D / 32;            // 16-byte chunks of keys per thread: tokens 16 w .. 16 w + 15 of the tile
       constexpr int VG = (D / 32 + 3) / 4;  // groups of 32 dims of the values per warp

@@ -147,7 +147,7 @@ inline size_t workspace_for(size_t tickets, size_t part_bytes) {  // its bytes f
   return ((t > p ? t : p) + 2047) / 2048 * 2048;
 }
 extern std::atomic<int> g_opt_attn_kernel;  // QDQ_OPT_ATTN_KERNEL
-size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim);
+size_t kv_attention_workspace_bytes(int n_seqs, int max_q, int max_kv_len, int n_heads, int n_kv, int head_dim, bool tree);
 // parent: NULL, or a tree of queries for each sequence
 int launch_kv_attention(const KvPool &c, int head_dim, const int *kv_len, const int *cu_q, const int *parent, int n_seqs,
                         int max_q, int max_kv_len, int n_heads, const void *q, int64_t q_stride, void *out, int64_t out_stride,
