@@ -9,17 +9,19 @@
 // 2 pi): no digits are lost at far positions (in f32 the angle of position 4,000,000 is off by a tenth of
 // a radian), and cos and sin get the fraction between -1/2 and 1/2.
 //
-// A CTA takes the new tokens of one block of 16 (which share a key scale) and a share of the heads: their cosines
-// and sines once into shared memory, then a warp at a time one head's 16 tokens: all loads before the first use, a token's
-// elements in 16 or 32 lanes (its sum of squares is folded by shuffles, the other element of a pair lies in another
-// lane or in the same four elements), a key block's maximum from registers.  Every input is read once, every output written once.
-// Bound: memory for prompts, for single tokens the chain of launch, length, page and scale.
+// A CTA takes the new tokens of one block of 16 (which share a key scale) and a share of the heads.  Its threads compute
+// the tokens' cosines and sines once into shared memory, while the first loads are on their way; then 4 to 8 lanes
+// take a token's head, in couples of four elements and the four that they are paired with, so that a rotation needs no other
+// lane and the sum of squares two or three shuffles (32 lanes to a head: 9 shuffles each, 136 us for the prompts below).  A
+// warp holds a head's 16 keys (a block's maximum comes from its registers), or 16 queries of any heads and tokens.  Every
+// input is read once, every output written once.
+// Bound: memory for prompts, with the arithmetic close behind; for single tokens the chain of launch, length, page and scale.
 #include "qdq_types.cuh"
 
 namespace qdq {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct RopeArgs {
   KvPool c;
@@ -29,13 +31,16 @@ struct RopeArgs {
   const float *q_weight, *k_weight, *freqs;
   int64_t q_stride, q_out_stride, k_stride, v_stride;
   int n_seqs, n_blocks, max_new, n_heads, n_rot, adjacent;
+  int q_iters;  // of GT queries in a warp's item
   float eps;
 };
 
-// Where a lane's elements lie: LPT lanes to a token, TPI tokens at a time, CPT times four elements 128 apart.
+// LPT lanes to a token's head, GT heads at a time, C couples of four elements and four others per lane; NI times GT
+// tokens are a block's.
 template <int D>
 struct Lanes {
-  static constexpr int LPT = D == 64 ? 16 : 32, TPI = 32 / LPT, NI = kKvBlock / TPI, CPT = (D + 127) / 128;
+  static constexpr int C = D == 64 ? 1 : D == 128 ? 2 : D == 256 ? 4 : 3;
+  static constexpr int LPT = D / 8 / C, GT = 32 / LPT, NI = kKvBlock / GT;
 };
 
 // Four elements as loaded.
@@ -55,7 +60,11 @@ struct Raw {
       w[1] = v.y;
     }
   }
-  __device__ __forceinline__ void values(float (&x)[4]) const {
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (uint32_t &x : w) x = 0;
+  }
+  __device__ __forceinline__ void values(float *x) const {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
@@ -69,123 +78,68 @@ struct Raw {
   }
 };
 
-// One head's new tokens of a block: tokens lo to hi - 1 of the 16; x: element 0 of token 0's head.
-template <typename T, int D>
-__device__ __forceinline__ void load_head(const T *x, int64_t stride, int lo, int hi, int lane,
-                                          float (&f)[Lanes<D>::NI][Lanes<D>::CPT][4]) {
-  using L = Lanes<D>;
-  Raw<T> r[L::NI][L::CPT];
-  const int sub = lane % L::LPT;
-#pragma unroll
-  for (int i = 0; i < L::NI; ++i) {
-    const int t = i * L::TPI + lane / L::LPT;
-#pragma unroll
-    for (int c = 0; c < L::CPT; ++c) {
-      const int d = 4 * sub + 128 * c;
-#pragma unroll
-      for (uint32_t &w : r[i][c].w) w = 0;
-      if (t >= lo && t < hi && d < D) r[i][c].load(x + t * stride + d);
-    }
+// First element of a couple's two quads: of pairs that lie n_rot / 2 apart, or beside one another.
+struct Couple {
+  int a, b;
+  bool turned;
+  __device__ __forceinline__ Couple(const RopeArgs &r, int j) {
+    turned = j < r.n_rot / 8;
+    const bool apart = turned && !r.adjacent;
+    a = apart ? 4 * j : 8 * j;
+    b = apart ? 4 * j + r.n_rot / 2 : 8 * j + 4;
   }
-#pragma unroll
-  for (int i = 0; i < L::NI; ++i)
-#pragma unroll
-    for (int c = 0; c < L::CPT; ++c) r[i][c].values(f[i][c]);
-}
+};
 
-// Norm and rotation of iteration i's tokens.
+// Norm (weight: of the lane's elements) and rotation of a token's head.
 template <int D>
-__device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>::CPT][4], const float *weight, const float *cs,
-                                          const float *sn, int lane) {
+__device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>::C][8], bool norm, const float (&weight)[Lanes<D>::C][8],
+                                          const float *cs, const float *sn, int sub) {
   using L = Lanes<D>;
-  const int sub = lane % L::LPT;
-  if (weight) {
+  if (norm) {
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < L::CPT; ++c)
+    for (int c = 0; c < L::C; ++c)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(x[c][e], x[c][e], s);
+      for (int e = 0; e < 8; ++e) s = fmaf(x[c][e], x[c][e], s);
 #pragma unroll
     for (int o = L::LPT / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float inv = rsqrtf(s * (1.f / D) + a.eps);
 #pragma unroll
-    for (int c = 0; c < L::CPT; ++c) {
-      const int d = 4 * sub + 128 * c;
-      const float4 w = d < D ? __ldg(reinterpret_cast<const float4 *>(weight + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[c][0] *= inv * w.x;
-      x[c][1] *= inv * w.y;
-      x[c][2] *= inv * w.z;
-      x[c][3] *= inv * w.w;
-    }
-  }
-  if (a.n_rot == 0) return;
-  if (a.adjacent) {
+    for (int c = 0; c < L::C; ++c)
 #pragma unroll
-    for (int c = 0; c < L::CPT; ++c) {
-      const int d = 4 * sub + 128 * c;
-      if (d < a.n_rot) {
-        const float2 co = *reinterpret_cast<const float2 *>(cs + d / 2), si = *reinterpret_cast<const float2 *>(sn + d / 2);
-        const float x0 = x[c][0], x2 = x[c][2];
-        x[c][0] = x0 * co.x - x[c][1] * si.x;
-        x[c][1] = x[c][1] * co.x + x0 * si.x;
-        x[c][2] = x2 * co.y - x[c][3] * si.y;
-        x[c][3] = x[c][3] * co.y + x2 * si.y;
+      for (int e = 0; e < 8; ++e) x[c][e] *= inv * weight[c][e];
+  }
+#pragma unroll
+  for (int c = 0; c < L::C; ++c) {
+    const int j = sub + L::LPT * c;
+    if (j < a.n_rot / 8) {
+      const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * j), si = *reinterpret_cast<const float4 *>(sn + 4 * j);
+      const float cw[4] = {co.x, co.y, co.z, co.w}, sw[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float &u = a.adjacent ? x[c][2 * e] : x[c][e], &v = a.adjacent ? x[c][2 * e + 1] : x[c][4 + e];
+        const float p = u, q = v;
+        u = p * cw[e] - q * sw[e];
+        v = q * cw[e] + p * sw[e];
       }
     }
-    return;
   }
-  const int h = a.n_rot / 2;
-  float y[L::CPT][4];
-#pragma unroll
-  for (int c = 0; c < L::CPT; ++c) {
-    const int d = 4 * sub + 128 * c;
-    const bool turned = d < a.n_rot, low = d < h;
-    const int other = turned ? (low ? d + h : d - h) : d;  // where the other elements of the pairs are
-    const int from = lane / L::LPT * L::LPT + other / 4 % L::LPT;
-    float p[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      p[e] = __shfl_sync(0xffffffffu, x[0][e], from);
-      if constexpr (L::CPT == 2) {
-        const float far = __shfl_sync(0xffffffffu, x[1][e], from);
-        p[e] = other >= 128 ? far : p[e];
-      }
-    }
-    if (turned) {
-      const int i = low ? d : d - h;
-      const float4 co = *reinterpret_cast<const float4 *>(cs + i), si = *reinterpret_cast<const float4 *>(sn + i);
-      const float g = low ? -1.f : 1.f;
-      y[c][0] = x[c][0] * co.x + g * p[0] * si.x;
-      y[c][1] = x[c][1] * co.y + g * p[1] * si.y;
-      y[c][2] = x[c][2] * co.z + g * p[2] * si.z;
-      y[c][3] = x[c][3] * co.w + g * p[3] * si.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[c][e] = x[c][e];
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < L::CPT; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[c][e] = y[c][e];
 }
 
-// The block's codes and scale from its new tokens held..end - 1 in x (definition in qdq_kv.cu).
+// The block's codes and scale from its new tokens held .. end - 1 in x, 0 elsewhere (definition in qdq_kv.cu).
 template <int D>
-__device__ __forceinline__ void quantise(uint8_t *record, int page_tokens, int which, int t0, int held, int end,
-                                         const float (&x)[Lanes<D>::NI][Lanes<D>::CPT][4], int lane) {
+__device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int which, int t0, int held, int end, float s_old,
+                                         const float (&x)[Lanes<D>::NI][Lanes<D>::C][8], int lane) {
   using L = Lanes<D>;
-  const int sub = lane % L::LPT;
+  const int sub = lane % L::LPT, page_tokens = a.c.page_tokens;
   int8_t *codes = reinterpret_cast<int8_t *>(record) + (int64_t(which) * page_tokens + t0) * D;
-  float *scale = reinterpret_cast<float *>(record + int64_t(2) * page_tokens * D) + which * (page_tokens / kKvBlock) + t0 / kKvBlock;
-  const float s_old = held ? __uint_as_float(ld_u1(scale)) : 0.f;
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < L::NI; ++i)
 #pragma unroll
-    for (int c = 0; c < L::CPT; ++c)
+    for (int c = 0; c < L::C; ++c)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m = max_abs_bits(m, x[i][c][e]);  // 0 where there is no new token
+      for (int e = 0; e < 8; ++e) m = max_abs_bits(m, x[i][c][e]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
   float s_new = __fdiv_rn(m, 127.f);
@@ -197,46 +151,50 @@ __device__ __forceinline__ void quantise(uint8_t *record, int page_tokens, int w
   const float again = grown && sc > 0.f ? __fdiv_rn(s_old, sc) : 0.f;
 #pragma unroll
   for (int i = 0; i < L::NI; ++i) {
-    const int t = i * L::TPI + lane / L::LPT;
+    const int t = i * L::GT + lane / L::LPT;
 #pragma unroll
-    for (int c = 0; c < L::CPT; ++c) {
-      const int d = 4 * sub + 128 * c;
-      if (d >= D) continue;
-      uint32_t *p = reinterpret_cast<uint32_t *>(codes + t * D + d);
-      if (grown && t < held) {  // a larger scale: what the block held, rounded to it
-        const uint32_t w = ld_u1(p);
-        uint32_t r = 0;
+    for (int c = 0; c < L::C; ++c) {
+      const Couple at(a, sub + L::LPT * c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r |= uint32_t(__float2int_rn(float(int8_t(w >> (8 * j))) * again) & 0xFF) << (8 * j);
-        *p = r;
-      }
-      if (t >= held && t < end) {
-        auto code = [&](float f) { return uint32_t(__float2int_rn(fminf(fmaxf(f * inv, -127.f), 127.f)) & 0xFF); };
-        *p = code(x[i][c][0]) | (code(x[i][c][1]) << 8) | (code(x[i][c][2]) << 16) | (code(x[i][c][3]) << 24);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t *p = reinterpret_cast<uint32_t *>(codes + t * D + (which ? 8 * (sub + L::LPT * c) + 4 * q : q ? at.b : at.a));
+        if (grown && t < held) {  // a larger scale: what the block held, rounded to it
+          const uint32_t w = ld_u1(p);
+          uint32_t r = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r |= uint32_t(__float2int_rn(float(int8_t(w >> (8 * j))) * again) & 0xFF) << (8 * j);
+          *p = r;
+        }
+        if (t >= held && t < end) {
+          auto code = [&](float f) { return uint32_t(__float2int_rn(fminf(fmaxf(f * inv, -127.f), 127.f)) & 0xFF); };
+          const float *v = &x[i][c][4 * q];
+          *p = code(v[0]) | (code(v[1]) << 8) | (code(v[2]) << 16) | (code(v[3]) << 24);
+        }
       }
     }
   }
-  if (lane == 0 && (held == 0 || sc != s_old)) *scale = sc;
+  if (lane == 0 && (held == 0 || sc != s_old))
+    *(reinterpret_cast<float *>(record + int64_t(2) * page_tokens * D) + which * (page_tokens / kKvBlock) + t0 / kKvBlock) = sc;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 2 : 1) kv_append_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_kernel(const RopeArgs a) {
   using L = Lanes<D>;
   constexpr int kThreads = kWarps * 32;
   __shared__ unsigned long long s_turn[D / 2];  // 2^64 frac(freq / 2 pi)
   __shared__ __align__(16) float s_cos[kKvBlock][D / 2], s_sin[kKvBlock][D / 2];
   __shared__ int s_parent[QDQ_MAX_TREE], s_pos[kKvBlock];
   __shared__ bool s_bad[kKvBlock];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % L::LPT, grp = lane / L::LPT;
   const float qnan = __int_as_float(0x7fffffff);
   pdl_launch_dependents();
   const int pairs = a.n_rot / 2;
   for (int i = tid; i < pairs; i += kThreads) {  // (frequencies and weights count as weights: read ahead of the wait)
-    const double turns = double(__ldg(a.freqs + i)) * 0.15915494309189533577;  // 1 / (2 pi)
-    s_turn[i] = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
+    const float f = __ldg(a.freqs + i);
+    const double turns = double(f) * 0.15915494309189533577;  // 1 / (2 pi)
+    s_turn[i] = isfinite(f) ? (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0) : 0ull;
   }
   pdl_wait();
-  const int items = 2 * a.c.n_kv + a.n_heads;
   const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
   for (int s = blockIdx.z; s < a.n_seqs; s += gridDim.z)
     for (int b = blockIdx.y; b < a.n_blocks; b += gridDim.y) {
@@ -248,10 +206,54 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 2 : 1) kv_append_rope_
       const int old = bad ? 0 : all - n_new, n = min(n_new, a.max_new), len = old + n;
       const int blk = old / kKvBlock + b, p0 = blk * kKvBlock;
       if (p0 >= len) break;
-      const int held = max(old - p0, 0), end = min(len - p0, kKvBlock);
-      __syncthreads();  // the tables of the block before have been read
-      if (a.parent && tid < min(n, QDQ_MAX_TREE)) s_parent[tid] = int(ld_u1(a.parent + first + tid));
-      __syncthreads();
+      const int held = max(old - p0, 0), end = min(len - p0, kKvBlock), fresh = end - held;
+      const int64_t row0 = int64_t(first) + p0 - old;  // the row of the block's token 0 (a negative part is never read)
+      // items: keys and values of a head, then q_iters times GT queries (head, token) one after the other
+      const uint32_t by_fresh = uint32_t(((uint64_t(1) << 32) + fresh - 1) / fresh);  // (2^32 for 1 is 0)
+      auto head_of = [&](int u) { return fresh == 1 ? u : int(__umulhi(uint32_t(u), by_fresh)); };  // u / fresh: u is below 2^28
+      const int q_all = a.n_heads * fresh, q_item = a.q_iters * L::GT, items = 2 * a.c.n_kv + (q_all + q_item - 1) / q_item;
+      Raw<T> raw[L::NI][L::C][2];
+      int64_t at = -1;   // of a key or value item: its record
+      float s_old = 0.f;
+      auto load = [&](int item) {
+        const bool kv = item < 2 * a.c.n_kv;
+        const int which = item & 1, h = item >> 1;
+        const T *x = kv ? static_cast<const T *>(which ? a.v : a.k) + row0 * (which ? a.v_stride : a.k_stride) + h * D
+                        : static_cast<const T *>(a.q) + row0 * a.q_stride;
+        const int64_t stride = !kv ? a.q_stride : which ? a.v_stride : a.k_stride;
+#pragma unroll
+        for (int i = 0; i < L::NI; ++i) {
+          const int u = (item - 2 * a.c.n_kv) * q_item + i * L::GT + grp, hq = kv ? 0 : head_of(u);  // the query, its head
+          const int t = kv ? i * L::GT + grp : held + u - hq * fresh;
+          const bool in = kv ? t >= held && t < end && !bad : i < a.q_iters && u < q_all;
+          const T *p = x + t * stride + hq * D;
+#pragma unroll
+          for (int c = 0; c < L::C; ++c) {
+            const int j = sub + L::LPT * c;
+            const Couple cp(a, j);
+            raw[i][c][0].clear();
+            raw[i][c][1].clear();
+            if (in) {
+              raw[i][c][0].load(p + (kv && which ? 8 * j : cp.a));
+              raw[i][c][1].load(p + (kv && which ? 8 * j + 4 : cp.b));
+            }
+          }
+        }
+        if (kv && !bad) {
+          at = kv_record_of(a.c, s, blk, h, rec);
+          const int t0 = p0 % a.c.page_tokens;
+          s_old = held && at >= 0 ? __uint_as_float(ld_u1(a.c.pages + at + int64_t(2) * a.c.page_tokens * D +
+                                                           4 * (which * (a.c.page_tokens / kKvBlock) + t0 / kKvBlock)))
+                                  : 0.f;
+        }
+      };
+      int item = blockIdx.x * kWarps + warp;
+      if (item < items) load(item);  // in flight beside the tables
+      __syncthreads();               // the tables of the block before have been read
+      if (a.parent) {
+        if (tid < min(n, QDQ_MAX_TREE)) s_parent[tid] = int(ld_u1(a.parent + first + tid));
+        __syncthreads();
+      }
       if (tid < kKvBlock) {
         const int i = p0 + tid - old;  // the token among the new ones
         int pos = p0 + tid;
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 2 : 1) kv_append_rope_
         s_bad[tid] = wrong;
       }
       __syncthreads();
-      for (int i = tid; i < (end - held) * pairs; i += kThreads) {
+      for (int i = tid; i < fresh * pairs; i += kThreads) {
         const int t = held + i / pairs, p = i % pairs;
         const long long turn = (long long)((unsigned long long)(long long)s_pos[t] * s_turn[p]);
         float sn, cs;
@@ -280,57 +282,81 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 2 : 1) kv_append_rope_
         s_sin[t][p] = wrong ? qnan : sn;
       }
       __syncthreads();
-      for (int item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
-        float x[L::NI][L::CPT][4];
-        const int64_t row0 = int64_t(first) + p0 - old;  // the row of the block's token 0 (a negative part is never read)
-        if (item < 2 * a.c.n_kv) {
-          const int h = item >> 1, which = item & 1;
-          if (bad) continue;
-          const T *p = static_cast<const T *>(which ? a.v : a.k) + row0 * (which ? a.v_stride : a.k_stride) + h * D;
-          load_head<T, D>(p, which ? a.v_stride : a.k_stride, held, end, lane, x);
-          const int64_t at = kv_record_of(a.c, s, blk, h, rec);
-          if (at < 0) continue;  // no page for these tokens: they are dropped
-          if (which == 0) {
+      while (item < items) {
+        const bool kv = item < 2 * a.c.n_kv;
+        const int which = item & 1;
+        const float *wp = kv ? (which ? nullptr : a.k_weight) : a.q_weight;
+        float w[L::C][8];
+        if (wp) {
+#pragma unroll
+          for (int c = 0; c < L::C; ++c) {
+            const Couple cp(a, sub + L::LPT * c);
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(wp + cp.a)), v = __ldg(reinterpret_cast<const float4 *>(wp + cp.b));
+            w[c][0] = u.x;
+            w[c][1] = u.y;
+            w[c][2] = u.z;
+            w[c][3] = u.w;
+            w[c][4] = v.x;
+            w[c][5] = v.y;
+            w[c][6] = v.z;
+            w[c][7] = v.w;
+          }
+        }
+        if (kv) {
+          if (!bad && at >= 0) {  // (no page for these tokens: they are dropped)
+            float x[L::NI][L::C][8];
 #pragma unroll
             for (int i = 0; i < L::NI; ++i) {
-              const int t = i * L::TPI + lane / L::LPT;
-              if (i * L::TPI + L::TPI > held && i * L::TPI < end) {
-                const int at_t = min(max(t, held), end - 1);  // (a lane whose token is no new one: zeros by any angle)
-                norm_turn<D>(a, x[i], a.k_weight, s_cos[at_t], s_sin[at_t], lane);
-                if (t < held || t >= end) {
+              const int t = i * L::GT + grp;
 #pragma unroll
-                  for (int c = 0; c < L::CPT; ++c)
+              for (int c = 0; c < L::C; ++c) {
+                raw[i][c][0].values(x[i][c]);
+                raw[i][c][1].values(x[i][c] + 4);
+              }
+              if (which == 0 && (i + 1) * L::GT > held && i * L::GT < end) {
+                const int tt = min(max(t, held), end - 1);  // (a lane whose token is no new one: zeros by any angle)
+                norm_turn<D>(a, x[i], wp != nullptr, w, s_cos[tt], s_sin[tt], sub);
+                const bool in = t >= held && t < end, wrong = s_bad[tt];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][c][e] = 0.f;
-                } else if (s_bad[t]) {  // also where nothing is turned
+                for (int c = 0; c < L::C; ++c)
 #pragma unroll
-                  for (int c = 0; c < L::CPT; ++c) x[i][c][0] = qnan;
+                  for (int e = 0; e < 8; ++e) x[i][c][e] = !in ? 0.f : wrong ? qnan : x[i][c][e];
+              }
+            }
+            quantise<D>(a, a.c.pages + at, which, p0 % a.c.page_tokens, held, end, s_old, x, lane);
+          }
+        } else {
+          const int u0 = (item - 2 * a.c.n_kv) * q_item;
+#pragma unroll
+          for (int i = 0; i < L::NI; ++i) {
+            if (i < a.q_iters && u0 + i * L::GT < q_all) {
+              // (past the last query: any token's angles)
+              const int u = u0 + i * L::GT + grp, hq = head_of(u), t = held + u - hq * fresh;
+              float x[L::C][8];
+#pragma unroll
+              for (int c = 0; c < L::C; ++c) {
+                raw[i][c][0].values(x[c]);
+                raw[i][c][1].values(x[c] + 4);
+              }
+              norm_turn<D>(a, x, wp != nullptr, w, s_cos[t], s_sin[t], sub);
+              T *o = static_cast<T *>(a.q_out) + (row0 + t) * a.q_out_stride + hq * D;
+              const bool wrong = s_bad[t];
+              if (u < q_all) {
+#pragma unroll
+                for (int c = 0; c < L::C; ++c) {
+                  const Couple cp(a, sub + L::LPT * c);
+                  if (wrong)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[c][e] = qnan;
+                  store4(o + cp.a, make_float4(x[c][0], x[c][1], x[c][2], x[c][3]));
+                  store4(o + cp.b, make_float4(x[c][4], x[c][5], x[c][6], x[c][7]));
                 }
               }
             }
           }
-          quantise<D>(a.c.pages + at, a.c.page_tokens, which, p0 % a.c.page_tokens, held, end, x, lane);
-        } else {
-          const int h = item - 2 * a.c.n_kv;
-          load_head<T, D>(static_cast<const T *>(a.q) + row0 * a.q_stride + h * D, a.q_stride, held, end, lane, x);
-          T *o = static_cast<T *>(a.q_out) + row0 * a.q_out_stride + h * D;
-#pragma unroll
-          for (int i = 0; i < L::NI; ++i) {
-            const int t = i * L::TPI + lane / L::LPT;
-            if (i * L::TPI + L::TPI > held && i * L::TPI < end) {
-              const int at_t = min(max(t, held), end - 1);
-              norm_turn<D>(a, x[i], a.q_weight, s_cos[at_t], s_sin[at_t], lane);
-              const bool wrong = s_bad[at_t];
-#pragma unroll
-              for (int c = 0; c < L::CPT; ++c) {
-                const int d = 4 * (lane % L::LPT) + 128 * c;
-                if (t >= held && t < end && d < D)
-                  store4(o + t * a.q_out_stride + d, wrong ? make_float4(qnan, qnan, qnan, qnan)
-                                                            : make_float4(x[i][c][0], x[i][c][1], x[i][c][2], x[i][c][3]));
-              }
-            }
-          }
         }
+        item += gridDim.x * kWarps;
+        if (item < items) load(item);
       }
     }
 }
@@ -355,12 +381,16 @@ int launch_kv_append_rope(const KvPool &c, int head_dim, const int *kv_len, cons
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
-  const RopeArgs a{c, kv_len, cu, parent, q, k, v, q_out, q_weight, k_weight, freqs, q_stride, q_out_stride, k_stride, v_stride,
-                   n_seqs, kv_blocks_touched(max_new), max_new, n_heads, freqs ? n_rot : 0, adjacent, eps};
-  const int groups = (2 * c.n_kv + n_heads + kWarps - 1) / kWarps;
-  const int64_t blocks = int64_t(a.n_blocks) * n_seqs;
-  const int want = int(blocks < 4 * di.sm_count ? (4 * di.sm_count + blocks - 1) / blocks : 1);
-  const dim3 grid(groups < want ? groups : want, a.n_blocks < 65535 ? a.n_blocks : 65535, n_seqs < 65535 ? n_seqs : 65535);
+  RopeArgs a{c, kv_len, cu, parent, q, k, v, q_out, q_weight, k_weight, freqs, q_stride, q_out_stride, k_stride, v_stride,
+             n_seqs, kv_blocks_touched(max_new), max_new, n_heads, freqs ? n_rot : 0, adjacent, 1, eps};
+  const int gt = with_dim(head_dim, [](auto d) { return Lanes<decltype(d)::value>::GT; });
+  const int tokens = max_new < kKvBlock ? max_new : kKvBlock;  // of a block
+  const int64_t blocks = int64_t(a.n_blocks) * n_seqs, queries = int64_t(n_heads) * tokens;
+  // few queries: a warp for every GT of them; many: 16 to a warp, whose loads are in flight together
+  a.q_iters = queries * blocks > 64 * int64_t(di.sm_count) * gt ? kKvBlock / gt : 1;
+  const int64_t items = 2 * c.n_kv + (queries + a.q_iters * gt - 1) / (a.q_iters * gt), groups = (items + kWarps - 1) / kWarps;
+  const int64_t want = blocks < 4 * di.sm_count ? (4 * di.sm_count + blocks - 1) / blocks : 1;
+  const dim3 grid(unsigned(groups < want ? groups : want), a.n_blocks < 65535 ? a.n_blocks : 65535, n_seqs < 65535 ? n_seqs : 65535);
   e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {
       return int(launch(kv_append_rope_kernel<decltype(t), decltype(d)::value>, grid, dim3(kWarps * 32), 0, s, a));
