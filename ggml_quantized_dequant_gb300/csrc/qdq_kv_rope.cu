@@ -30,7 +30,7 @@ struct RopeArgs {
   void *q_out;
   const float *q_weight, *k_weight, *freqs;
   int64_t q_stride, q_out_stride, k_stride, v_stride;
-  int n_seqs, n_blocks, max_new, n_heads, n_rot, adjacent;
+  int n_seqs, n_blocks, max_new, n_heads, n_rot;
   int q_iters;  // of GT queries in a warp's item
   float eps;
 };
@@ -79,19 +79,18 @@ struct Raw {
 };
 
 // First element of a couple's two quads: of pairs that lie n_rot / 2 apart, or beside one another.
+template <bool ADJACENT>
 struct Couple {
   int a, b;
-  bool turned;
   __device__ __forceinline__ Couple(const RopeArgs &r, int j) {
-    turned = j < r.n_rot / 8;
-    const bool apart = turned && !r.adjacent;
+    const bool apart = !ADJACENT && j < r.n_rot / 8;
     a = apart ? 4 * j : 8 * j;
     b = apart ? 4 * j + r.n_rot / 2 : 8 * j + 4;
   }
 };
 
 // Norm (weight: of the lane's elements) and rotation of a token's head.
-template <int D>
+template <int D, bool ADJACENT>
 __device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>::C][8], bool norm, const float (&weight)[Lanes<D>::C][8],
                                           const float *cs, const float *sn, int sub) {
   using L = Lanes<D>;
@@ -117,7 +116,7 @@ __device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>
       const float cw[4] = {co.x, co.y, co.z, co.w}, sw[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float &u = a.adjacent ? x[c][2 * e] : x[c][e], &v = a.adjacent ? x[c][2 * e + 1] : x[c][4 + e];
+        float &u = x[c][ADJACENT ? 2 * e : e], &v = x[c][ADJACENT ? 2 * e + 1 : 4 + e];
         const float p = u, q = v;
         u = p * cw[e] - q * sw[e];
         v = q * cw[e] + p * sw[e];
@@ -126,22 +125,21 @@ __device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>
   }
 }
 
-// The block's codes and scale from its new tokens held .. end - 1 in x, 0 elsewhere (definition in qdq_kv.cu).
-template <int D>
-__device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int which, int t0, int held, int end, float s_old,
+// The larger magnitude; NaN wins.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// The block's codes and scale from its new tokens held .. end - 1 in x, whose largest magnitude is m (definition in qdq_kv.cu).
+// A product with 1 / s is at most 127 and some roundings, so that 1.5 2^23 added and its bits' low byte are rint and its code.
+template <int D, bool ADJACENT>
+__device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int which, int t0, int held, int end, float s_old, float m,
                                          const float (&x)[Lanes<D>::NI][Lanes<D>::C][8], int lane) {
   using L = Lanes<D>;
   const int sub = lane % L::LPT, page_tokens = a.c.page_tokens;
   int8_t *codes = reinterpret_cast<int8_t *>(record) + (int64_t(which) * page_tokens + t0) * D;
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < L::NI; ++i)
-#pragma unroll
-    for (int c = 0; c < L::C; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_abs_bits(m, x[i][c][e]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_abs_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
   float s_new = __fdiv_rn(m, 127.f);
   if (s_new < 1.17549435e-38f) s_new = 0.f;
   if (!(m < __int_as_float(0x7f800000))) s_new = __int_as_float(0x7fffffff);
@@ -154,7 +152,7 @@ __device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int
     const int t = i * L::GT + lane / L::LPT;
 #pragma unroll
     for (int c = 0; c < L::C; ++c) {
-      const Couple at(a, sub + L::LPT * c);
+      const Couple<ADJACENT> at(a, sub + L::LPT * c);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t *p = reinterpret_cast<uint32_t *>(codes + t * D + (which ? 8 * (sub + L::LPT * c) + 4 * q : q ? at.b : at.a));
@@ -166,9 +164,12 @@ __device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int
           *p = r;
         }
         if (t >= held && t < end) {
-          auto code = [&](float f) { return uint32_t(__float2int_rn(fminf(fmaxf(f * inv, -127.f), 127.f)) & 0xFF); };
           const float *v = &x[i][c][4 * q];
-          *p = code(v[0]) | (code(v[1]) << 8) | (code(v[2]) << 16) | (code(v[3]) << 24);
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[e], inv), 12582912.f));
+          const uint32_t r = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+          *p = sc == sc ? r : 0u;
         }
       }
     }
@@ -177,7 +178,7 @@ __device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int
     *(reinterpret_cast<float *>(record + int64_t(2) * page_tokens * D) + which * (page_tokens / kKvBlock) + t0 / kKvBlock) = sc;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool ADJACENT>
 __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_kernel(const RopeArgs a) {
   using L = Lanes<D>;
   constexpr int kThreads = kWarps * 32;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
 #pragma unroll
           for (int c = 0; c < L::C; ++c) {
             const int j = sub + L::LPT * c;
-            const Couple cp(a, j);
+            const Couple<ADJACENT> cp(a, j);
             raw[i][c][0].clear();
             raw[i][c][1].clear();
             if (in) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
         if (wp) {
 #pragma unroll
           for (int c = 0; c < L::C; ++c) {
-            const Couple cp(a, sub + L::LPT * c);
+            const Couple<ADJACENT> cp(a, sub + L::LPT * c);
             const float4 u = __ldg(reinterpret_cast<const float4 *>(wp + cp.a)), v = __ldg(reinterpret_cast<const float4 *>(wp + cp.b));
             w[c][0] = u.x;
             w[c][1] = u.y;
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
         }
         if (kv) {
           if (!bad && at >= 0) {  // (no page for these tokens: they are dropped)
-            float x[L::NI][L::C][8];
+            float x[L::NI][L::C][8], m = 0.f;
 #pragma unroll
             for (int i = 0; i < L::NI; ++i) {
               const int t = i * L::GT + grp;
@@ -315,15 +316,19 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
               }
               if (which == 0 && (i + 1) * L::GT > held && i * L::GT < end) {
                 const int tt = min(max(t, held), end - 1);  // (a lane whose token is no new one: zeros by any angle)
-                norm_turn<D>(a, x[i], wp != nullptr, w, s_cos[tt], s_sin[tt], sub);
-                const bool in = t >= held && t < end, wrong = s_bad[tt];
+                norm_turn<D, ADJACENT>(a, x[i], wp != nullptr, w, s_cos[tt], s_sin[tt], sub);
+                if (t == tt && s_bad[tt]) m = qnan;
+              }
+              // (tokens that are not new: their zeros stay zeros, unless an angle is NaN)
+              if (t >= held && t < end)
 #pragma unroll
                 for (int c = 0; c < L::C; ++c)
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) x[i][c][e] = !in ? 0.f : wrong ? qnan : x[i][c][e];
-              }
+                  for (int e = 0; e < 8; ++e) m = max_abs(m, x[i][c][e]);
             }
-            quantise<D>(a, a.c.pages + at, which, p0 % a.c.page_tokens, held, end, s_old, x, lane);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+            quantise<D, ADJACENT>(a, a.c.pages + at, which, p0 % a.c.page_tokens, held, end, s_old, m, x, lane);
           }
         } else {
           const int u0 = (item - 2 * a.c.n_kv) * q_item;
@@ -338,13 +343,13 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
                 raw[i][c][0].values(x[c]);
                 raw[i][c][1].values(x[c] + 4);
               }
-              norm_turn<D>(a, x, wp != nullptr, w, s_cos[t], s_sin[t], sub);
+              norm_turn<D, ADJACENT>(a, x, wp != nullptr, w, s_cos[t], s_sin[t], sub);
               T *o = static_cast<T *>(a.q_out) + (row0 + t) * a.q_out_stride + hq * D;
               const bool wrong = s_bad[t];
               if (u < q_all) {
 #pragma unroll
                 for (int c = 0; c < L::C; ++c) {
-                  const Couple cp(a, sub + L::LPT * c);
+                  const Couple<ADJACENT> cp(a, sub + L::LPT * c);
                   if (wrong)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[c][e] = qnan;
@@ -382,7 +387,7 @@ int launch_kv_append_rope(const KvPool &c, int head_dim, const int *kv_len, cons
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return fail_cuda(e);
   RopeArgs a{c, kv_len, cu, parent, q, k, v, q_out, q_weight, k_weight, freqs, q_stride, q_out_stride, k_stride, v_stride,
-             n_seqs, kv_blocks_touched(max_new), max_new, n_heads, freqs ? n_rot : 0, adjacent, 1, eps};
+             n_seqs, kv_blocks_touched(max_new), max_new, n_heads, freqs ? n_rot : 0, 1, eps};
   const int gt = with_dim(head_dim, [](auto d) { return Lanes<decltype(d)::value>::GT; });
   const int tokens = max_new < kKvBlock ? max_new : kKvBlock;  // of a block
   const int64_t blocks = int64_t(a.n_blocks) * n_seqs, queries = int64_t(n_heads) * tokens;
@@ -393,7 +398,9 @@ int launch_kv_append_rope(const KvPool &c, int head_dim, const int *kv_len, cons
   const dim3 grid(unsigned(groups < want ? groups : want), a.n_blocks < 65535 ? a.n_blocks : 65535, n_seqs < 65535 ? n_seqs : 65535);
   e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {
-      return int(launch(kv_append_rope_kernel<decltype(t), decltype(d)::value>, grid, dim3(kWarps * 32), 0, s, a));
+      constexpr int D = decltype(d)::value;
+      return int(adjacent ? launch(kv_append_rope_kernel<decltype(t), D, true>, grid, dim3(kWarps * 32), 0, s, a)
+                          : launch(kv_append_rope_kernel<decltype(t), D, false>, grid, dim3(kWarps * 32), 0, s, a));
     });
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
