@@ -9,13 +9,18 @@
 // 2 pi): no digits are lost at far positions (in f32 the angle of position 4,000,000 is off by a tenth of
 // a radian), and cos and sin get the fraction between -1/2 and 1/2.
 //
-// A CTA takes the new tokens of one block of 16 (which share a key scale) and a share of the heads.  Its threads compute
-// the tokens' cosines and sines once into shared memory, while the first loads are on their way; then 4 to 8 lanes
-// take a token's head, in couples of four elements and the four that they are paired with, so that a rotation needs no other
-// lane and the sum of squares two or three shuffles (32 lanes to a head: 9 shuffles each, 136 us for the prompts below).  A
-// warp holds a head's 16 keys (a block's maximum comes from its registers), or 16 queries of any heads and tokens.  Every
-// input is read once, every output written once.
-// Bound: memory for prompts, with the arithmetic close behind; for single tokens the chain of launch, length, page and scale.
+// A CTA takes the new tokens of one block of 16 (which share a key scale) and a share of the heads.  4 to 8 lanes take a
+// token's head, in couples of four elements and the four that they are paired with, so that a rotation needs no other
+// lane and the sum of squares two or three shuffles (32 lanes to a head: 9 shuffles each, 136 us for the prompts below).
+// Every input is read once, every output written once.  Two kernels:
+//   items (few new tokens): the CTA's threads compute the tokens' cosines and sines once into shared memory, while the first
+//   loads are on their way; a warp holds a head's 16 keys (a block's maximum comes from its registers), or 16 queries of any
+//   heads and tokens, so that a single token's heads spread over all warps.
+//   rows (many): a warp keeps 4 or 8 tokens and goes through the heads with them.
+// Measured (alone, in a graph): one token, 24 / 8 heads of 128, f32 5.3 us; 48 trees of 5 to 26 tokens, 32 / 8 heads of 128,
+// bf16 10.3 us (items 13.9); 6 prompts of 900 to 3000 tokens, 24 / 8 heads of 128, bf16 58 us, 5.2 TB/s (items 85).
+// Bound: for prompts memory and the instructions' issue (half its rate) together; for single tokens the chain of launch,
+// length, page and scale.
 #include "qdq_types.cuh"
 
 namespace qdq {
@@ -89,10 +94,24 @@ struct Couple {
   }
 };
 
-// Norm (weight: of the lane's elements) and rotation of a token's head.
-template <int D, bool ADJACENT>
+template <typename Couple>
+__device__ __forceinline__ void load_weight(const float *p, const Couple &cp, float (&w)[8]) {
+  const float4 u = __ldg(reinterpret_cast<const float4 *>(p + cp.a)), v = __ldg(reinterpret_cast<const float4 *>(p + cp.b));
+  w[0] = u.x;
+  w[1] = u.y;
+  w[2] = u.z;
+  w[3] = u.w;
+  w[4] = v.x;
+  w[5] = v.y;
+  w[6] = v.z;
+  w[7] = v.w;
+}
+
+// Norm (weight: of the lane's elements) and rotation of a token's head; cosines and sines by couples, the lane's or the
+// token's.
+template <int D, bool ADJACENT, bool IN_LANE>
 __device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>::C][8], bool norm, const float (&weight)[Lanes<D>::C][8],
-                                          const float *cs, const float *sn, int sub) {
+                                          const float4 *cs, const float4 *sn, int sub) {
   using L = Lanes<D>;
   if (norm) {
     float s = 0.f;
@@ -112,7 +131,7 @@ __device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>
   for (int c = 0; c < L::C; ++c) {
     const int j = sub + L::LPT * c;
     if (j < a.n_rot / 8) {
-      const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * j), si = *reinterpret_cast<const float4 *>(sn + 4 * j);
+      const float4 co = cs[IN_LANE ? c : j], si = sn[IN_LANE ? c : j];
       const float cw[4] = {co.x, co.y, co.z, co.w}, sw[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -132,57 +151,91 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   return r;
 }
 
-// The block's codes and scale from its new tokens held .. end - 1 in x, whose largest magnitude is m (definition in qdq_kv.cu).
-// A product with 1 / s is at most 127 and some roundings, so that 1.5 2^23 added and its bits' low byte are rint and its code.
+// What a block's codes are made by (definition in qdq_kv.cu).
+struct Scale {
+  float old, now, inv, again;
+  __device__ __forceinline__ Scale(float s_old, float m) : old(s_old) {  // m: the new tokens' largest magnitude
+    float s_new = __fdiv_rn(m, 127.f);
+    if (s_new < 1.17549435e-38f) s_new = 0.f;
+    if (!(m < __int_as_float(0x7f800000))) s_new = __int_as_float(0x7fffffff);
+    now = max_abs_bits(s_old, s_new);  // NaN wins
+    inv = now > 0.f ? __frcp_rn(now) : 0.f;
+    again = now > 0.f ? __fdiv_rn(s_old, now) : 0.f;
+  }
+};
+// Four new codes.  A product with 1 / s is at most 127 and some roundings, so that 1.5 2^23 added and its bits' low byte
+// are rint and its code.
+__device__ __forceinline__ uint32_t new_codes(const float *v, const Scale &sc) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[e], sc.inv), 12582912.f));
+  const uint32_t r = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  return sc.now == sc.now ? r : 0u;
+}
+// Four codes that a block held, rounded to a larger scale.
+__device__ __forceinline__ void old_codes(uint32_t *p, const Scale &sc) {
+  const uint32_t w = ld_u1(p);
+  uint32_t r = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r |= uint32_t(__float2int_rn(float(int8_t(w >> (8 * j))) * sc.again) & 0xFF) << (8 * j);
+  *p = r;
+}
+
+// The block's codes and scale from its new tokens held .. end - 1 in x, whose largest magnitude is m.
 template <int D, bool ADJACENT>
 __device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int which, int t0, int held, int end, float s_old, float m,
                                          const float (&x)[Lanes<D>::NI][Lanes<D>::C][8], int lane) {
   using L = Lanes<D>;
   const int sub = lane % L::LPT, page_tokens = a.c.page_tokens;
   int8_t *codes = reinterpret_cast<int8_t *>(record) + (int64_t(which) * page_tokens + t0) * D;
-  float s_new = __fdiv_rn(m, 127.f);
-  if (s_new < 1.17549435e-38f) s_new = 0.f;
-  if (!(m < __int_as_float(0x7f800000))) s_new = __int_as_float(0x7fffffff);
-  const float sc = max_abs_bits(s_old, s_new);  // NaN wins
-  const float inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
-  const bool grown = held && sc != s_old;
-  const float again = grown && sc > 0.f ? __fdiv_rn(s_old, sc) : 0.f;
+  const Scale sc(s_old, m);
+  const bool grown = held && sc.now != sc.old;
 #pragma unroll
   for (int i = 0; i < L::NI; ++i) {
     const int t = i * L::GT + lane / L::LPT;
 #pragma unroll
     for (int c = 0; c < L::C; ++c) {
-      const Couple<ADJACENT> at(a, sub + L::LPT * c);
+      const int j = sub + L::LPT * c;
+      const Couple<ADJACENT> at(a, j);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t *p = reinterpret_cast<uint32_t *>(codes + t * D + (which ? 8 * (sub + L::LPT * c) + 4 * q : q ? at.b : at.a));
-        if (grown && t < held) {  // a larger scale: what the block held, rounded to it
-          const uint32_t w = ld_u1(p);
-          uint32_t r = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) r |= uint32_t(__float2int_rn(float(int8_t(w >> (8 * j))) * again) & 0xFF) << (8 * j);
-          *p = r;
-        }
-        if (t >= held && t < end) {
-          const float *v = &x[i][c][4 * q];
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[e], inv), 12582912.f));
-          const uint32_t r = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
-          *p = sc == sc ? r : 0u;
-        }
+        uint32_t *p = reinterpret_cast<uint32_t *>(codes + t * D + (which ? 8 * j + 4 * q : q ? at.b : at.a));
+        if (grown && t < held) old_codes(p, sc);
+        if (t >= held && t < end) *p = new_codes(&x[i][c][4 * q], sc);
       }
     }
   }
-  if (lane == 0 && (held == 0 || sc != s_old))
-    *(reinterpret_cast<float *>(record + int64_t(2) * page_tokens * D) + which * (page_tokens / kKvBlock) + t0 / kKvBlock) = sc;
+  if (lane == 0 && (held == 0 || grown))
+    *(reinterpret_cast<float *>(record + int64_t(2) * page_tokens * D) + which * (page_tokens / kKvBlock) + t0 / kKvBlock) = sc.now;
+}
+
+// 2^64 frac(freq / 2 pi), a turn's fraction per position
+__device__ __forceinline__ unsigned long long turn_of(float f) {
+  const double turns = double(f) * 0.15915494309189533577;  // 1 / (2 pi)
+  return isfinite(f) ? (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0) : 0ull;
+}
+__device__ __forceinline__ void angle(int pos, unsigned long long turn, float *sn, float *cs) {
+  // the product's upper 32 bits: a turn to 2^-32, where an angle's f32 has 2^-25
+  const int half = int(((unsigned long long)(long long)pos * turn + 0x80000000ull) >> 32);
+  sincospif(float(half) * 4.656612873077393e-10f, sn, cs);  // 2^-31: half turns
+}
+// Position of node i of a tree whose first node is at `old`; `wrong` where it or an ancestor has no valid parent.
+__device__ __forceinline__ int tree_position(const int *parent, int i, int old, bool &wrong) {
+  int pos = old;
+  for (int node = i;;) {  // up to the root (to ever smaller numbers, so it ends)
+    const int up = parent[node];
+    wrong |= up < -1 || up >= node;
+    if (up < 0 || up >= node) return pos;
+    node = up;
+    ++pos;
+  }
 }
 
 template <typename T, int D, bool ADJACENT>
 __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_kernel(const RopeArgs a) {
   using L = Lanes<D>;
   constexpr int kThreads = kWarps * 32;
-  __shared__ unsigned long long s_turn[D / 2];  // 2^64 frac(freq / 2 pi)
+  __shared__ unsigned long long s_turn[D / 2];
   __shared__ __align__(16) float s_cos[kKvBlock][D / 2], s_sin[kKvBlock][D / 2];
   __shared__ int s_parent[QDQ_MAX_TREE], s_pos[kKvBlock];
   __shared__ bool s_bad[kKvBlock];
@@ -191,9 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
   pdl_launch_dependents();
   const int pairs = a.n_rot / 2;
   for (int i = tid; i < pairs; i += kThreads) {  // (frequencies and weights count as weights: read ahead of the wait)
-    const float f = __ldg(a.freqs + i);
-    const double turns = double(f) * 0.15915494309189533577;  // 1 / (2 pi)
-    s_turn[i] = isfinite(f) ? (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0) : 0ull;
+    s_turn[i] = turn_of(__ldg(a.freqs + i));
   }
   pdl_wait();
   const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
@@ -259,25 +310,15 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
         const int i = p0 + tid - old;  // the token among the new ones
         int pos = p0 + tid;
         bool wrong = bad;
-        if (a.parent && i >= 0 && i < n) {
-          pos = old;
-          for (int node = i;;) {  // up to the root (to ever smaller numbers, so it ends)
-            const int up = s_parent[node];
-            wrong |= up < -1 || up >= node;
-            if (up < 0 || up >= node) break;
-            node = up;
-            ++pos;
-          }
-        }
+        if (a.parent && i >= 0 && i < n) pos = tree_position(s_parent, i, old, wrong);
         s_pos[tid] = pos;
         s_bad[tid] = wrong;
       }
       __syncthreads();
       for (int i = tid; i < fresh * pairs; i += kThreads) {
         const int t = held + i / pairs, p = i % pairs;
-        const long long turn = (long long)((unsigned long long)(long long)s_pos[t] * s_turn[p]);
         float sn, cs;
-        sincospif(float(turn) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63: half turns
+        angle(s_pos[t], s_turn[p], &sn, &cs);
         const bool wrong = s_bad[t] || !isfinite(__ldg(a.freqs + p));
         s_cos[t][p] = wrong ? qnan : cs;
         s_sin[t][p] = wrong ? qnan : sn;
@@ -290,18 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
         float w[L::C][8];
         if (wp) {
 #pragma unroll
-          for (int c = 0; c < L::C; ++c) {
-            const Couple<ADJACENT> cp(a, sub + L::LPT * c);
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(wp + cp.a)), v = __ldg(reinterpret_cast<const float4 *>(wp + cp.b));
-            w[c][0] = u.x;
-            w[c][1] = u.y;
-            w[c][2] = u.z;
-            w[c][3] = u.w;
-            w[c][4] = v.x;
-            w[c][5] = v.y;
-            w[c][6] = v.z;
-            w[c][7] = v.w;
-          }
+          for (int c = 0; c < L::C; ++c) load_weight(wp, Couple<ADJACENT>(a, sub + L::LPT * c), w[c]);
         }
         if (kv) {
           if (!bad && at >= 0) {  // (no page for these tokens: they are dropped)
@@ -316,7 +346,8 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
               }
               if (which == 0 && (i + 1) * L::GT > held && i * L::GT < end) {
                 const int tt = min(max(t, held), end - 1);  // (a lane whose token is no new one: zeros by any angle)
-                norm_turn<D, ADJACENT>(a, x[i], wp != nullptr, w, s_cos[tt], s_sin[tt], sub);
+                norm_turn<D, ADJACENT, false>(a, x[i], wp != nullptr, w, reinterpret_cast<const float4 *>(s_cos[tt]),
+                                              reinterpret_cast<const float4 *>(s_sin[tt]), sub);
                 if (t == tt && s_bad[tt]) m = qnan;
               }
               // (tokens that are not new: their zeros stay zeros, unless an angle is NaN)
@@ -343,7 +374,8 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
                 raw[i][c][0].values(x[c]);
                 raw[i][c][1].values(x[c] + 4);
               }
-              norm_turn<D, ADJACENT>(a, x, wp != nullptr, w, s_cos[t], s_sin[t], sub);
+              norm_turn<D, ADJACENT, false>(a, x, wp != nullptr, w, reinterpret_cast<const float4 *>(s_cos[t]),
+                                            reinterpret_cast<const float4 *>(s_sin[t]), sub);
               T *o = static_cast<T *>(a.q_out) + (row0 + t) * a.q_out_stride + hq * D;
               const bool wrong = s_bad[t];
               if (u < q_all) {
@@ -362,6 +394,209 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
         }
         item += gridDim.x * kWarps;
         if (item < items) load(item);
+      }
+    }
+}
+
+template <typename T, int D>
+constexpr int kRowsCtas = D == 64 ? 5 - (sizeof(T) == 4) : D == 128 ? (sizeof(T) == 2 ? 4 : 3) : 2;  // resident per SM
+// Prompts: a warp keeps GT tokens of the block and goes through the heads with them, their cosines and sines in
+// registers (no tables, and a quarter of the registers that a whole block's keys take).  The NI warps that share a block
+// exchange the largest magnitudes of a head's keys and values; the next head's elements are on the way meanwhile.
+// A CTA for 8 heads: for 4 the prompts take 70 us, for 8 58, for 12 59, for all 74.
+template <typename T, int D, bool ADJACENT>
+__global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_rows_kernel(const RopeArgs a) {
+  using L = Lanes<D>;
+  constexpr int kThreads = kWarps * 32, kGroups = kWarps / L::NI;  // groups of warps, each with heads of its own
+  __shared__ unsigned long long s_turn[D / 2];
+  __shared__ float s_max[2][kWarps][2];
+  __shared__ int s_parent[QDQ_MAX_TREE];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % L::LPT, grp = lane / L::LPT;
+  const int slice = warp % L::NI, group = warp / L::NI;
+  const float qnan = __int_as_float(0x7fffffff);
+  pdl_launch_dependents();
+  const int pairs = a.n_rot / 2;
+  for (int i = tid; i < pairs; i += kThreads) s_turn[i] = turn_of(__ldg(a.freqs + i));
+  pdl_wait();
+  const int64_t rec = kv_record_bytes(a.c.page_tokens, D);
+  for (int s = blockIdx.z; s < a.n_seqs; s += gridDim.z)
+    for (int b = blockIdx.y; b < a.n_blocks; b += gridDim.y) {
+      const int first = a.cu ? int(ld_u1(a.cu + s)) : s;
+      const int n_new = a.cu ? int(ld_u1(a.cu + s + 1)) - first : 1;
+      const int all = int(ld_u1(a.kv_len + s));
+      if (n_new <= 0) break;
+      const bool bad = all < n_new;  // more new tokens than there are: nothing is appended, their queries are NaN
+      const int old = bad ? 0 : all - n_new, n = min(n_new, a.max_new), len = old + n;
+      const int blk = old / kKvBlock + b, p0 = blk * kKvBlock, t0 = p0 % a.c.page_tokens;
+      if (p0 >= len) break;
+      const int held = max(old - p0, 0), end = min(len - p0, kKvBlock);
+      const int t = slice * L::GT + grp, i = p0 + t - old;  // the lane's token in the block, and among the new ones
+      const bool in = t >= held && t < end;
+      const int64_t row = int64_t(first) + (in ? i : 0);
+      const int stride = gridDim.x * kGroups, h0 = blockIdx.x * kGroups + group;
+      __syncthreads();  // (s_turn is written; the block before is done with s_parent and s_max)
+      if (a.parent) {
+        if (tid < min(n, QDQ_MAX_TREE)) s_parent[tid] = int(ld_u1(a.parent + first + tid));
+        __syncthreads();
+      }
+      int pos = p0 + t;
+      bool wrong = bad;
+      if (a.parent && in) pos = tree_position(s_parent, i, old, wrong);
+      float4 cs[L::C], sn[L::C];
+#pragma unroll
+      for (int c = 0; c < L::C; ++c) {
+        const int j = sub + L::LPT * c;
+        float x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = 1.f;
+          y[e] = 0.f;
+          if (j < a.n_rot / 8) {
+            angle(pos, s_turn[4 * j + e], &y[e], &x[e]);
+            if (wrong || !isfinite(__ldg(a.freqs + 4 * j + e))) x[e] = y[e] = qnan;
+          }
+        }
+        cs[c] = make_float4(x[0], x[1], x[2], x[3]);
+        sn[c] = make_float4(y[0], y[1], y[2], y[3]);
+      }
+      // (lanes without a token read the first one's elements and write nothing)
+      auto load = [&](Raw<T> (&r)[L::C][2], const T *p, bool plain) {
+#pragma unroll
+        for (int c = 0; c < L::C; ++c) {
+          const int j = sub + L::LPT * c;
+          const Couple<ADJACENT> cp(a, j);
+          r[c][0].load(p + (plain ? 8 * j : cp.a));
+          r[c][1].load(p + (plain ? 8 * j + 4 : cp.b));
+        }
+      };
+      // keys and values, head by head (every warp of the CTA goes through the same number of them)
+      if (!bad) {
+        const T *kp = static_cast<const T *>(a.k) + row * a.k_stride, *vp = static_cast<const T *>(a.v) + row * a.v_stride;
+        const int rounds = (a.c.n_kv - int(blockIdx.x) * kGroups + stride - 1) / stride;
+        float w[L::C][8];
+        if (a.k_weight)
+#pragma unroll
+          for (int c = 0; c < L::C; ++c) load_weight(a.k_weight, Couple<ADJACENT>(a, sub + L::LPT * c), w[c]);
+        Raw<T> rk[L::C][2], rv[L::C][2];
+        load(rk, kp + min(h0, a.c.n_kv - 1) * D, false);
+        load(rv, vp + min(h0, a.c.n_kv - 1) * D, true);
+        const int64_t at0 = kv_record_of(a.c, s, blk, 0, rec);  // without a page the tokens are dropped
+        uint8_t *const records = a.c.pages + (at0 < 0 ? 0 : at0);
+        for (int r = 0; r < rounds; ++r) {
+          const int h = h0 + r * stride;
+          const bool there = at0 >= 0 && h < a.c.n_kv;
+          int8_t *const record = reinterpret_cast<int8_t *>(records + (there ? h * rec : 0));
+          float *scales = reinterpret_cast<float *>(record + 2 * a.c.page_tokens * D) + t0 / kKvBlock, *v_scale = scales + a.c.page_tokens / kKvBlock;
+          float k_old = 0.f, v_old = 0.f;
+          if (held && there) {
+            k_old = __uint_as_float(ld_u1(scales));
+            v_old = __uint_as_float(ld_u1(v_scale));
+          }
+          float xk[L::C][8], xv[L::C][8], mk = 0.f, mv = 0.f;
+#pragma unroll
+          for (int c = 0; c < L::C; ++c) {
+            rk[c][0].values(xk[c]);
+            rk[c][1].values(xk[c] + 4);
+            rv[c][0].values(xv[c]);
+            rv[c][1].values(xv[c] + 4);
+          }
+          if (h + stride < a.c.n_kv) {
+            load(rk, kp + (h + stride) * D, false);
+            load(rv, vp + (h + stride) * D, true);
+          }
+          norm_turn<D, ADJACENT, true>(a, xk, a.k_weight != nullptr, w, cs, sn, sub);
+          if (in) {
+#pragma unroll
+            for (int c = 0; c < L::C; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                mk = max_abs(mk, xk[c][e]);
+                mv = max_abs(mv, xv[c][e]);
+              }
+            if (wrong) mk = qnan;
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            mk = max_abs(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = max_abs(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+          }
+          if (lane == 0) {
+            s_max[r & 1][warp][0] = mk;
+            s_max[r & 1][warp][1] = mv;
+          }
+          __syncthreads();
+          if (!there) continue;
+#pragma unroll
+          for (int y = 0; y < L::NI; ++y) {
+            mk = max_abs(mk, s_max[r & 1][group * L::NI + y][0]);
+            mv = max_abs(mv, s_max[r & 1][group * L::NI + y][1]);
+          }
+          const Scale sk(k_old, mk), sv(v_old, mv);
+          int8_t *codes = record + (t0 + t) * D, *v_codes = codes + a.c.page_tokens * D;
+#pragma unroll
+          for (int c = 0; c < L::C; ++c) {
+            const int j = sub + L::LPT * c;
+            const Couple<ADJACENT> cp(a, j);
+            if (in) {
+              *reinterpret_cast<uint32_t *>(codes + cp.a) = new_codes(xk[c], sk);
+              *reinterpret_cast<uint32_t *>(codes + cp.b) = new_codes(xk[c] + 4, sk);
+              *reinterpret_cast<uint2 *>(v_codes + 8 * j) = make_uint2(new_codes(xv[c], sv), new_codes(xv[c] + 4, sv));
+            } else if (t < held) {  // a larger scale: what the block held, rounded to it
+              if (sk.now != sk.old) {
+                old_codes(reinterpret_cast<uint32_t *>(codes + cp.a), sk);
+                old_codes(reinterpret_cast<uint32_t *>(codes + cp.b), sk);
+              }
+              if (sv.now != sv.old) {
+                old_codes(reinterpret_cast<uint32_t *>(v_codes + 8 * j), sv);
+                old_codes(reinterpret_cast<uint32_t *>(v_codes + 8 * j + 4), sv);
+              }
+            }
+          }
+          if (lane == 0 && slice == 0) {
+            if (held == 0 || sk.now != sk.old) *scales = sk.now;
+            if (held == 0 || sv.now != sv.old) *v_scale = sv.now;
+          }
+        }
+      }
+      // queries
+      if (a.n_heads > 0) {
+        const T *qp = static_cast<const T *>(a.q) + row * a.q_stride;
+        T *op = static_cast<T *>(a.q_out) + row * a.q_out_stride;
+        float w[L::C][8];
+        if (a.q_weight)
+#pragma unroll
+          for (int c = 0; c < L::C; ++c) load_weight(a.q_weight, Couple<ADJACENT>(a, sub + L::LPT * c), w[c]);
+        constexpr int kAhead = 2;  // heads whose elements are on the way
+        Raw<T> r[kAhead][L::C][2];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y)
+          load(r[y], qp + min(h0 + y * stride, a.n_heads - 1) * D, false);
+        for (int h = h0; h < a.n_heads; h += kAhead * stride) {
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            const int hh = h + y * stride;
+            if (hh >= a.n_heads) break;
+            float x[L::C][8];
+#pragma unroll
+            for (int c = 0; c < L::C; ++c) {
+              r[y][c][0].values(x[c]);
+              r[y][c][1].values(x[c] + 4);
+            }
+            if (hh + kAhead * stride < a.n_heads) load(r[y], qp + (hh + kAhead * stride) * D, false);
+            norm_turn<D, ADJACENT, true>(a, x, a.q_weight != nullptr, w, cs, sn, sub);
+            if (in) {
+#pragma unroll
+              for (int c = 0; c < L::C; ++c) {
+                const Couple<ADJACENT> cp(a, sub + L::LPT * c);
+                if (wrong)
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) x[c][e] = qnan;
+                store4(op + hh * D + cp.a, make_float4(x[c][0], x[c][1], x[c][2], x[c][3]));
+                store4(op + hh * D + cp.b, make_float4(x[c][4], x[c][5], x[c][6], x[c][7]));
+              }
+            }
+          }
+        }
       }
     }
 }
@@ -393,12 +628,21 @@ int launch_kv_append_rope(const KvPool &c, int head_dim, const int *kv_len, cons
   const int64_t blocks = int64_t(a.n_blocks) * n_seqs, queries = int64_t(n_heads) * tokens;
   // few queries: a warp for every GT of them; many: 16 to a warp, whose loads are in flight together
   a.q_iters = queries * blocks > 64 * int64_t(di.sm_count) * gt ? kKvBlock / gt : 1;
-  const int64_t items = 2 * c.n_kv + (queries + a.q_iters * gt - 1) / (a.q_iters * gt), groups = (items + kWarps - 1) / kWarps;
-  const int64_t want = blocks < 4 * di.sm_count ? (4 * di.sm_count + blocks - 1) / blocks : 1;
+  // A warp that keeps its tokens pays for their angles by itself and takes an idle share of a block with few of them:
+  // 1 sequence of 5 tokens, 32 / 8 heads of 128, bf16: 5.5 us items, 7.6 rows; 64 of 5: 10.7, 11.2; 64 of 8: 13.4, 11.4;
+  // 16 of 8: 8.3, 8.7; 16 of 12: 9.7, 8.7; 1 of 64: 7.6, 8.2; 1 of 4096: 39.8, 27.5.
+  const bool rows = max_new >= 6 && int64_t(n_seqs) * max_new >= 160;
+  const int64_t items = 2 * c.n_kv + (queries + a.q_iters * gt - 1) / (a.q_iters * gt);
+  const int64_t heads = n_heads > c.n_kv ? n_heads : c.n_kv;
+  const int64_t groups = rows ? (heads + 7) / 8 : (items + kWarps - 1) / kWarps;
+  const int64_t want = rows ? groups : blocks < 4 * di.sm_count ? (4 * di.sm_count + blocks - 1) / blocks : 1;
   const dim3 grid(unsigned(groups < want ? groups : want), a.n_blocks < 65535 ? a.n_blocks : 65535, n_seqs < 65535 ? n_seqs : 65535);
   e = cudaError_t(with_type(type, [&](auto t) {
     return with_dim(head_dim, [&](auto d) {
       constexpr int D = decltype(d)::value;
+      if (rows)
+        return int(adjacent ? launch(kv_append_rope_rows_kernel<decltype(t), D, true>, grid, dim3(kWarps * 32), 0, s, a)
+                            : launch(kv_append_rope_rows_kernel<decltype(t), D, false>, grid, dim3(kWarps * 32), 0, s, a));
       return int(adjacent ? launch(kv_append_rope_kernel<decltype(t), D, true>, grid, dim3(kWarps * 32), 0, s, a)
                           : launch(kv_append_rope_kernel<decltype(t), D, false>, grid, dim3(kWarps * 32), 0, s, a));
     });
