@@ -10,24 +10,31 @@
 // drawn with certainty (q = 1 at the child): w loses the child.  Temperature 0: a child is accepted when it is the
 // target's best token (the smallest of equals), which is also the next one.
 //
-// w is always max(a p - b q, 0) with two numbers a and b: a rejection turns them into a / Z and (b + 1) / Z, Z the sum
-// of max(a p - (b + 1) q, 0).  So a rejection is one pass over a row of logits and a row of q, and nothing is stored.
+// w is always max(p - b q, 0) / S with two numbers b and S, first 0 and 1: a rejection adds S to b, and S is then the sum of
+// max(p - b q, 0).  So a rejection is one pass over a row of logits and a row of q, nothing is stored or divided, and
+// the comparison is u q S < max(p - b q, 0).
 //
-// First kernel: every row of logits, in chunks of 1024, one warp each: the largest logit and the sum of exponentials relative
-// to it (at temperature 0 the best key).  Second kernel, one CTA or cluster per sequence: the rows' sums from their
-// chunks, every child's p and q at once, then the walk; a rejection's pass is shared by the CTAs of the cluster, its
-// chunks' sums go through the workspace; the drawn token's chunk is found from the chunks' sums, and the token in it by
-// a warp.  Sums over chunks, a, b and Z are f64, within a chunk f32.
-// Bound: memory in the first kernel, the chain of loads and joins in the second.
+// A row's softmax comes from its chunks of 1024, one warp each: the largest logit and the sum of exponentials relative to it
+// (at temperature 0 the best key).  Either a kernel of its own reads every row, and the walk, one CTA or cluster
+// per sequence, joins their chunks (few rows: all of them at once are sooner there than one after the other); or the
+// walk's cluster reads each node's row when it gets there (many rows: those of drafts that are not reached are not
+// read), its warps' sums exchanged through one another's shared memory.  Then every child's p and q at once, and the
+// comparisons; a rejection's pass is shared by the cluster, too.  The drawn token's chunk is found from the
+// chunks' sums, and the token in it by a warp.
+// Sums within a chunk are f32, over chunks pairs of f32 (48 bits; f64 adds have a 64th of f32's rate here and were most
+// of the walk's time), p, b and S f32.
+// Bound: memory for many rows, the chain of loads and joins for few.
 #include "qdq_types.cuh"
 
 namespace qdq {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the first kernel
+constexpr int kWalk = 512, kWalkWarps = kWalk / 32;    // of the walk
 constexpr int kPer = 32;             // logits per lane
 constexpr int kChunk = 32 * kPer;    // ... and warp
 constexpr int kCluster = 8;          // CTAs that share a rejection's pass
+constexpr int64_t kLazyBytes = int64_t(128) << 20;  // of logits, from which on the walk reads the rows
 constexpr float kFar = -1e30f;       // stands for -inf, whose product with 0 would be NaN
 
 struct VerifyArgs {
@@ -39,6 +46,7 @@ struct VerifyArgs {
   float2 *stats;  // [sequence][row][chunk]: largest logit, sum of 2^((x - largest) c); temperature 0: a 64-bit key
   float *sums;    // [sequence][chunk]: of a rejection's pass
   int n_seqs, max_rows, n, chunks, groups;  // chunks: of a row, at most
+  bool ahead;                               // draft probabilities that may be needed are brought into the L2
   float c_hi, c_lo;                         // log2(e) / temperature in two parts
 };
 
@@ -72,46 +80,46 @@ struct Row {
   __device__ __forceinline__ int chunks() const { return (hi + kChunk - 1) / kChunk; }
 };
 
-// Element of this lane's value i of a chunk: neighbouring lanes' vectors beside one another, or each lane's values.
-template <typename T, bool OWN>
+// This lane's value i of a run of 32 N elements (neighbouring lanes' vectors beside one another): its place in the run.
+template <typename T>
 __device__ __forceinline__ int element(int i, int lane) {
-  constexpr int V = 16 / int(sizeof(T)), G = kPer / V;
-  return ((OWN ? lane * G + i / V : i / V * 32 + lane)) * V + i % V;
+  constexpr int V = 16 / int(sizeof(T));
+  return (i / V * 32 + lane) * V + i % V;
 }
 
-// A chunk's logits, -inf outside the row.
-template <typename T, bool OWN>
-__device__ __forceinline__ void load_chunk(const Row<T> &r, int base, int lane, float (&x)[kPer]) {
-  constexpr int V = 16 / int(sizeof(T)), G = kPer / V;
-  if (base >= r.lo && base + kChunk <= r.hi) {
-    uint4 u[G];
+// A run's logits, -inf outside the row.
+template <typename T, int N>
+__device__ __forceinline__ void load_run(const Row<T> &r, int base, int lane, float (&x)[N]) {
+  constexpr int V = 16 / int(sizeof(T));
+  if (base >= r.lo && base + 32 * N <= r.hi) {
+    uint4 u[N / V];
 #pragma unroll
-    for (int j = 0; j < G; ++j) u[j] = ld_u4(r.x + base + element<T, OWN>(j * V, lane));
+    for (int j = 0; j < N / V; ++j) u[j] = ld_u4(r.x + base + element<T>(j * V, lane));
 #pragma unroll
-    for (int j = 0; j < G; ++j) unpack<T>(u[j], x + j * V);
+    for (int j = 0; j < N / V; ++j) unpack<T>(u[j], x + j * V);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = base + element<T, OWN>(i, lane);
+    for (int i = 0; i < N; ++i) {
+      const int e = base + element<T>(i, lane);
       x[i] = e >= r.lo && e < r.hi ? load1(r.x + e) : __int_as_float(0xff800000);
     }
   }
 }
 
 // The same elements of a row of draft probabilities (0 outside the row).
-template <typename T, bool OWN>
-__device__ __forceinline__ void load_draft(const float *q, const Row<T> &r, int base, int lane, float (&x)[kPer]) {
+template <typename T, int N>
+__device__ __forceinline__ void load_draft(const float *q, const Row<T> &r, int base, int lane, float (&x)[N]) {
   const float *p = q - r.lo;  // element e of the row's count is p[e]
-  if (base >= r.lo && base + kChunk <= r.hi && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    uint4 u[kPer / 4];
+  if (base >= r.lo && base + 32 * N <= r.hi && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    uint4 u[N / 4];
 #pragma unroll
-    for (int j = 0; j < kPer / 4; ++j) u[j] = ld_u4(p + base + element<T, OWN>(4 * j, lane));
+    for (int j = 0; j < N / 4; ++j) u[j] = ld_u4(p + base + element<T>(4 * j, lane));
 #pragma unroll
-    for (int j = 0; j < kPer / 4; ++j) unpack<float>(u[j], x + 4 * j);
+    for (int j = 0; j < N / 4; ++j) unpack<float>(u[j], x + 4 * j);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = base + element<T, OWN>(i, lane);
+    for (int i = 0; i < N; ++i) {
+      const int e = base + element<T>(i, lane);
       x[i] = e >= r.lo && e < r.hi ? load1(p + e) : 0.f;
     }
   }
@@ -132,10 +140,81 @@ __device__ __forceinline__ float weight(const VerifyArgs &a, float x, float m) {
   const float y = fmaxf(x - m, kFar);
   return ex2(fmaf(y, a.c_hi, y * a.c_lo));
 }
-__device__ __forceinline__ double warp_sum_f64(double v) {
+
+// A sum as hi + lo, with the roundings of hi in lo.
+struct Pair {
+  float hi, lo;
+  __device__ __forceinline__ float value() const { return hi + lo; }
+};
+__device__ __forceinline__ Pair operator+(const Pair &a, const Pair &b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return {s, a.lo + b.lo + ((a.hi - (s - t)) + (b.hi - t))};
+}
+__device__ __forceinline__ Pair operator*(float f, const Pair &a) {
+  const float h = f * a.hi;
+  return {h, fmaf(f, a.lo, fmaf(f, a.hi, -h))};
+}
+__device__ __forceinline__ float operator-(const Pair &a, const Pair &b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+__device__ __forceinline__ Pair warp_sum_pair(Pair v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) v = v + Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
   return v;
+}
+// The sum of this lane's and lower lanes' (the warp's all in lane 31).
+__device__ __forceinline__ Pair warp_scan(Pair v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair u = {__shfl_up_sync(0xffffffffu, v.hi, o), __shfl_up_sync(0xffffffffu, v.lo, o)};
+    if (lane >= o) v = u + v;
+  }
+  return v;
+}
+__device__ __forceinline__ float warp_max_nan(float m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t key) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t other = shfl_xor_key(key, o);
+    key = other > key ? other : key;
+  }
+  return key;
+}
+// A chunk of 1024 elements of size B at p, less what the row does not have, into the L2.
+__device__ __forceinline__ void prefetch(const void *p, int bytes, int lane) {
+  for (int o = lane * 128; o < bytes; o += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + o));
+}
+
+// What is kept of a chunk: its largest logit and the sum of exponentials relative to it, or its best key.
+template <typename T, bool GREEDY>
+__device__ __forceinline__ uint2 chunk_stats(const VerifyArgs &a, const Row<T> &r, int c, int lane, const float (&x)[kPer]) {
+  if constexpr (GREEDY) {
+    // (outside the row -inf: no better than a row's elements, and behind them)
+    uint32_t best = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) best = max(best, uint32_t(topk_key(x[k], 0u) >> 32));
+    best = __reduce_max_sync(0xffffffffu, best);
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int k = kPer - 1; k >= 0; --k) {
+      const int e = c * kChunk + element<T>(k, lane);
+      if (uint32_t(topk_key(x[k], 0u) >> 32) == best && e >= r.lo && e < r.hi) at = e;
+    }
+    at = __reduce_min_sync(0xffffffffu, at);
+    return make_uint2(~uint32_t(at - r.lo), best);
+  } else {
+    float m = x[0];
+#pragma unroll
+    for (int k = 1; k < kPer; ++k) m = max_nan(m, x[k]);
+    m = warp_max_nan(m);
+    const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
+    float l[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) l[k & 3] += weight(a, x[k], ref);
+    return make_uint2(__float_as_uint(m), __float_as_uint(warp_sum((l[0] + l[1]) + (l[2] + l[3]))));
+  }
 }
 
 template <typename T, bool GREEDY>
@@ -150,35 +229,9 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyArgs
   const int chunks = r.chunks();
   for (int c = g * kWarps + warp; c < chunks; c += a.groups * kWarps) {
     float x[kPer];
-    load_chunk<T, false>(r, c * kChunk, lane, x);
-    float2 *to = a.stats + int64_t(at) * a.chunks + c;
-    if constexpr (GREEDY) {
-      uint64_t key = 0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int e = c * kChunk + element<T, false>(k, lane);
-        const uint64_t mine = e >= r.lo && e < r.hi ? topk_key(x[k], uint32_t(e - r.lo)) : 0;
-        key = mine > key ? mine : key;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t other = shfl_xor_key(key, o);
-        key = other > key ? other : key;
-      }
-      if (lane == 0) *reinterpret_cast<uint64_t *>(to) = key;
-    } else {
-      float m = x[0];
-#pragma unroll
-      for (int k = 1; k < kPer; ++k) m = max_nan(m, x[k]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
-      float l[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) l[k & 3] += weight(a, x[k], ref);
-      const float sum = warp_sum((l[0] + l[1]) + (l[2] + l[3]));
-      if (lane == 0) *to = make_float2(m, sum);
-    }
+    load_run<T>(r, c * kChunk, lane, x);
+    const uint2 v = chunk_stats<T, GREEDY>(a, r, c, lane, x);
+    if (lane == 0) *reinterpret_cast<uint2 *>(a.stats + int64_t(at) * a.chunks + c) = v;
   }
 }
 
@@ -192,142 +245,251 @@ __device__ __forceinline__ void all_ctas() {  // barrier, with global writes bef
 }
 
 struct WalkShared {
-  double z[QDQ_MAX_TREE];            // a row's sum of weights relative to its largest logit
-  float m[QDQ_MAX_TREE];             // its largest logit
-  int best[QDQ_MAX_TREE];            // temperature 0: its best token
-  int bad[QDQ_MAX_TREE];             // a NaN or +inf, or nothing above -inf
+  uint2 parts[2][kCluster * kWalkWarps];  // every warp's part of a sum or a maximum, of the cluster; two exchanges in turn
+  float z[QDQ_MAX_TREE];              // a row's sum of weights relative to its largest logit
+  float m[QDQ_MAX_TREE];              // its largest logit
+  int best[QDQ_MAX_TREE];             // temperature 0: its best token
+  int bad[QDQ_MAX_TREE];              // a NaN or +inf, or nothing above -inf
   int parent[QDQ_MAX_TREE], token[QDQ_MAX_TREE], path[QDQ_MAX_TREE];
   float p[QDQ_MAX_TREE], q[QDQ_MAX_TREE], u[QDQ_MAX_TREE];  // of a child: its probabilities at its parent, its number
-  int lost[QDQ_MAX_TREE];            // rejected drafts without probabilities, at the present node
-  float rest[QDQ_MAX_TREE];          // their chunks' sums without them
-  double part[kWarps], left;
-  int chunk;
+  int lost[QDQ_MAX_TREE];             // rejected drafts without probabilities, at the present node
+  float rest[QDQ_MAX_TREE];           // their chunks' sums without them
+  uint32_t mask[kWalkWarps][kChunk / 32];  // a chunk's lost tokens
+  Pair part[kWalkWarps];
+  float left;
+  int chunk, next;
 };
 
-template <typename T, bool GREEDY, int CTAS>
-__global__ void __launch_bounds__(kThreads) verify_walk_kernel(const VerifyArgs a) {
+// Every warp's part to every CTA of the cluster; what the warps wrote to global memory before is visible behind it.
+template <int CTAS>
+__device__ __forceinline__ void exchange(WalkShared &sh, int turn, uint2 mine, int rank, int warp, int lane) {
+  uint2 *to = &sh.parts[turn][rank * kWalkWarps + warp];
+  if constexpr (CTAS == 1) {
+    if (lane == 0) *to = mine;
+    __syncthreads();
+  } else {
+    if (lane < CTAS) {
+      uint32_t at = uint32_t(__cvta_generic_to_shared(to));
+      asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(lane));
+      asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(mine.x), "r"(mine.y) : "memory");
+    }
+    __syncwarp();
+    all_ctas<CTAS>();
+  }
+}
+
+template <typename T, bool GREEDY, int CTAS, bool LAZY>
+__global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(const VerifyArgs a) {
   __shared__ WalkShared sh;
+  constexpr int kParts = CTAS * kWalkWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / CTAS, rank = blockIdx.x % CTAS;
   const float ninf = __int_as_float(0xff800000);
   pdl_launch_dependents();
+  if constexpr (CTAS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   const int first = a.cu ? int(ld_u1(a.cu + s)) : s;
   const int n = min(a.cu ? int(ld_u1(a.cu + s + 1)) - first : 1, a.max_rows);
   int *path = a.path + int64_t(s) * a.max_rows;
+  if constexpr (CTAS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs
   if (n <= 0) {  // (the whole cluster leaves)
     if (rank == 0) {
-      for (int i = tid; i < a.max_rows; i += kThreads) path[i] = -1;
+      for (int i = tid; i < a.max_rows; i += kWalk) path[i] = -1;
       if (tid == 0) a.accepted[s] = a.next[s] = -1;
     }
     return;
   }
-  const float2 *stats = a.stats + int64_t(s) * a.max_rows * a.chunks;
-  // every row's sums; a child's token, parent and number
-  for (int i = warp; i < n; i += kWarps) {
-    const Row<T> r(a, int64_t(first) + i);
-    const int chunks = r.chunks();
-    const float2 *st = stats + int64_t(i) * a.chunks;
-    if constexpr (GREEDY) {
-      uint64_t key = 0;
-      for (int c = lane; c < chunks; c += 32) {
-        const uint2 k = ld_u2(st + c);
-        const uint64_t mine = (uint64_t(k.y) << 32) | k.x;
-        key = mine > key ? mine : key;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t other = shfl_xor_key(key, o);
-        key = other > key ? other : key;
-      }
-      if (lane == 0) {
-        const uint32_t hi = uint32_t(key >> 32);  // +inf and NaN from 0xFF800000 on, -inf 0x007FFFFF
-        sh.bad[i] = hi >= 0xFF800000u || hi <= 0x007FFFFFu;
-        sh.best[i] = int(~uint32_t(key));
-      }
-    } else {
-      float m = ninf;
-      for (int c = lane; c < chunks; c += 32) m = max_nan(m, __uint_as_float(ld_u1(&st[c].x)));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const bool bad = !(m > ninf && m < -ninf);
-      double z = 0.0;
-      if (!bad)
-        for (int c = lane; c < chunks; c += 32) {
-          const uint2 v = ld_u2(st + c);
-          z += double(__uint_as_float(v.y) * weight(a, __uint_as_float(v.x), m));
-        }
-      z = warp_sum_f64(z);
-      if (lane == 0) {
-        sh.bad[i] = bad;
-        sh.m[i] = m;
-        sh.z[i] = z;
-      }
-    }
-  }
+  float2 *stats = a.stats + int64_t(s) * a.max_rows * a.chunks;
+  int turn = 0;
+  // a warp's share of a row's chunks, into the L2
+  auto row_ahead = [&](int node) {
+    const Row<T> r(a, int64_t(first) + node);
+    for (int c = rank * kWalkWarps + warp; c < r.chunks(); c += kParts) prefetch(r.x + c * kChunk, min(kChunk, r.hi - c * kChunk) * int(sizeof(T)), lane);
+  };
+  if constexpr (LAZY) row_ahead(0);
+  float cx = ninf, cq = 1.f;  // of a thread's row, as a child: its logit at its parent, its draft probability
   if (tid < n) {
     const int up = tid == 0 ? -1 : a.parent ? int(ld_u1(a.parent + first + tid)) : tid - 1;
     sh.parent[tid] = up >= 0 && up < tid ? up : -1;  // without a parent: never reached
-    sh.token[tid] = tid == 0 ? -1 : int(ld_u1(a.tokens + first + tid));
+    const int x = tid == 0 ? -1 : int(ld_u1(a.tokens + first + tid));
+    sh.token[tid] = x;
     // (numbers outside [0, 1) count as the nearest inside)
-    if constexpr (!GREEDY) sh.u[tid] = fminf(fmaxf(__uint_as_float(ld_u1(a.uniform + first + tid)), 0.f), 0.99999994f);
+    if constexpr (!GREEDY) {
+      sh.u[tid] = fminf(fmaxf(__uint_as_float(ld_u1(a.uniform + first + tid)), 0.f), 0.99999994f);
+      if (up >= 0 && up < tid && x >= 0 && x < a.n) {
+        const int64_t row = int64_t(first) + up;
+        cx = load1(static_cast<const T *>(a.logits) + row * a.stride + x);
+        if (a.draft) cq = load1(a.draft + row * a.draft_stride + x);
+      }
+    }
+  }
+  auto row_key = [&](int i, uint64_t key) {
+    const uint32_t hi = uint32_t(key >> 32);  // +inf and NaN from 0xFF800000 on, -inf 0x007FFFFF
+    sh.bad[i] = hi >= 0xFF800000u || hi <= 0x007FFFFFu;
+    sh.best[i] = int(~uint32_t(key));
+  };
+  // a row's largest logit and sum, from lanes' largest ones and sums relative to them
+  auto row_sum = [&](int i, float m, Pair z) {
+    const float most = warp_max_nan(m);
+    const bool bad = !(most > ninf && most < -ninf);
+    z = warp_sum_pair((bad || m == ninf ? 0.f : weight(a, m, most)) * z);
+    if (lane == 0) {
+      sh.bad[i] = bad;
+      sh.m[i] = most;
+      sh.z[i] = z.value();
+    }
+  };
+  auto chunk_of = [&](int node, int c) { return ld_u2(stats + int64_t(node) * a.chunks + c); };
+  if constexpr (!LAZY) {
+    // every row's sums
+    for (int i = warp; i < n; i += kWalkWarps) {
+      const Row<T> r(a, int64_t(first) + i);
+      const int chunks = r.chunks();
+      if constexpr (GREEDY) {
+        uint64_t key = 0;
+        for (int c = lane; c < chunks; c += 32) {
+          const uint2 k = chunk_of(i, c);
+          const uint64_t mine = (uint64_t(k.y) << 32) | k.x;
+          key = mine > key ? mine : key;
+        }
+        key = warp_max_key(key);
+        if (lane == 0) row_key(i, key);
+      } else {
+        float m = ninf;
+        Pair z = {0.f, 0.f};
+        for (int c0 = lane; c0 < chunks; c0 += 4 * 32) {
+          uint2 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = c0 + 32 * k < chunks ? chunk_of(i, c0 + 32 * k) : make_uint2(0xff800000u, 0);
+          float most = m;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) most = max_nan(most, __uint_as_float(v[k].x));
+          if (most > ninf) {  // (NaN and +inf: bad, whatever the sum)
+            z = weight(a, m, most) * z;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z = z + Pair{__uint_as_float(v[k].y) * weight(a, __uint_as_float(v[k].x), most), 0.f};
+          }
+          m = most;
+        }
+        row_sum(i, m, z);
+      }
+    }
   }
   __syncthreads();
-  if constexpr (!GREEDY) {
+  if constexpr (!LAZY && !GREEDY) {
     if (tid < n && sh.parent[tid] >= 0) {
-      const int up = sh.parent[tid], x = sh.token[tid];
-      float p = 0.f, q = 1.f;
-      if (x >= 0 && x < a.n && !sh.bad[up]) {
-        const int64_t row = int64_t(first) + up;
-        p = float(double(weight(a, load1(static_cast<const T *>(a.logits) + row * a.stride + x), sh.m[up])) / sh.z[up]);
-        if (a.draft) q = load1(a.draft + row * a.draft_stride + x);
-      }
-      sh.p[tid] = p;
-      sh.q[tid] = q;
+      const int up = sh.parent[tid];
+      sh.p[tid] = sh.bad[up] ? 0.f : weight(a, cx, sh.m[up]) / sh.z[up];
+      sh.q[tid] = cq;
     }
     __syncthreads();
   }
 
   int cur = 0, count = 0, lost = 0;
-  double wa = 1.0, wb = 0.0, gone = 0.0;  // w = max(wa p - wb q, 0); what rejected drafts without probabilities had
-  double sa = 1.0, sb = 0.0;              // a.sums holds the chunks' sums of max(sa p - sb q, 0), a multiple of w
-  bool summed = false;                    // ... where this is set
-  // the chunks' sums of max(ka p - kb q, 0) at the present node, and their sum
-  auto pass = [&](double ka, double kb) {
+  float wb = 0.f, ws = 1.f;   // w = max(p - wb q, 0) / ws
+  float kept = 1.f;           // what rejected drafts without probabilities have left
+  float summed = 0.f;         // a.sums holds the chunks' sums of max(p - summed q, 0), where this is not 0
+  // the chunks' sums of max(p - b q, 0) at the present node, and their sum
+  auto pass = [&](float b) {
     const Row<T> r(a, int64_t(first) + cur);
     const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
-    const float fa = float(ka / sh.z[cur]), fb = float(kb), m = sh.m[cur];
+    const float inv = 1.f / sh.z[cur], m = sh.m[cur];
     const int chunks = r.chunks();
     float *sums = a.sums + int64_t(s) * a.chunks;
-    for (int c = rank * kWarps + warp; c < chunks; c += CTAS * kWarps) {
-      float x[kPer], y[kPer];
-      load_chunk<T, false>(r, c * kChunk, lane, x);
-      load_draft<T, false>(q, r, c * kChunk, lane, y);
-      float l[4] = {0.f, 0.f, 0.f, 0.f};
+    Pair z = {0.f, 0.f};
+    for (int c = rank * kWalkWarps + warp; c < chunks; c += kParts) {
+      float l[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float x[kPer / 2], y[kPer / 2];
+        load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
+        load_draft<T>(q, r, c * kChunk + h * (kChunk / 2), lane, y);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) l[k & 3] += fmaxf(fmaf(fa, weight(a, x[k], m), -fb * y[k]), 0.f);
-      const float sum = warp_sum((l[0] + l[1]) + (l[2] + l[3]));
+        for (int k = 0; k < kPer / 2; ++k) l[k & 1] += fmaxf(fmaf(inv, weight(a, x[k], m), -b * y[k]), 0.f);
+      }
+      const float sum = warp_sum(l[0] + l[1]);
       if (lane == 0) sums[c] = sum;
+      z = z + Pair{sum, 0.f};
     }
-    __syncwarp();
-    all_ctas<CTAS>();
-    double z = 0.0;
-    for (int c = tid; c < chunks; c += kThreads) z += double(__ldcg(sums + c));
-    z = warp_sum_f64(z);
-    if (lane == 0) sh.part[warp] = z;
-    __syncthreads();
-    z = 0.0;
+    exchange<CTAS>(sh, turn, make_uint2(__float_as_uint(z.hi), __float_as_uint(z.lo)), rank, warp, lane);
+    z = {0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) z += sh.part[w];
-    all_ctas<CTAS>();  // everyone has read the sums (and the parts) before the next pass writes them
-    return z;
+    for (int k = 0; k < (kParts + 31) / 32; ++k) {
+      const uint2 v = lane + 32 * k < kParts ? sh.parts[turn][lane + 32 * k] : make_uint2(0, 0);
+      z = z + Pair{__uint_as_float(v.x), __uint_as_float(v.y)};
+    }
+    turn ^= 1;
+    return warp_sum_pair(z).value();
   };
 
   for (;;) {  // at the present node (every thread of every CTA alike)
     // its children, in order, as bits
     const uint64_t low = __ballot_sync(0xffffffffu, lane < n && sh.parent[lane] == cur);
     const uint64_t high = __ballot_sync(0xffffffffu, lane + 32 < n && sh.parent[lane + 32] == cur);
-    uint64_t children = sh.bad[cur] ? 0 : low | (high << 32);
+    uint64_t children = low | (high << 32);
+    if constexpr (LAZY) {
+      const Row<T> r(a, int64_t(first) + cur);
+      const int chunks = r.chunks();
+      float m = ninf, l = 0.f;
+      uint64_t key = 0;
+      for (int c = rank * kWalkWarps + warp; c < chunks; c += kParts) {
+        float x[kPer];
+        load_run<T>(r, c * kChunk, lane, x);
+        if (c < kParts && children) row_ahead(__ffsll((long long)children) - 1);  // the likeliest to come next
+        const uint2 v = chunk_stats<T, GREEDY>(a, r, c, lane, x);
+        if constexpr (GREEDY) {
+          const uint64_t mine = (uint64_t(v.y) << 32) | v.x;
+          key = mine > key ? mine : key;
+        } else {
+          if (lane == 0) *reinterpret_cast<uint2 *>(stats + int64_t(cur) * a.chunks + c) = v;
+          const float mine = __uint_as_float(v.x), most = max_nan(m, mine);
+          if (most > ninf) l = l * weight(a, m, most) + __uint_as_float(v.y) * weight(a, mine, most);
+          m = most;
+        }
+      }
+      exchange<CTAS>(sh, turn, GREEDY ? make_uint2(uint32_t(key), uint32_t(key >> 32)) : make_uint2(__float_as_uint(m), __float_as_uint(l)), rank, warp, lane);
+      if (warp == 0) {
+        if constexpr (GREEDY) {
+          key = 0;
+#pragma unroll
+          for (int k = 0; k < (kParts + 31) / 32; ++k) {
+            const uint2 v = sh.parts[turn][lane + 32 * k];
+            const uint64_t mine = (uint64_t(v.y) << 32) | v.x;
+            key = mine > key ? mine : key;
+          }
+          key = warp_max_key(key);
+          if (lane == 0) row_key(cur, key);
+        } else {
+          float most = ninf;
+#pragma unroll
+          for (int k = 0; k < kParts / 32; ++k) most = max_nan(most, __uint_as_float(sh.parts[turn][lane + 32 * k].x));
+          Pair z = {0.f, 0.f};
+          if (most > ninf)
+#pragma unroll
+            for (int k = 0; k < kParts / 32; ++k) {
+              const uint2 v = sh.parts[turn][lane + 32 * k];
+              z = z + Pair{__uint_as_float(v.y) * weight(a, __uint_as_float(v.x), most), 0.f};
+            }
+          row_sum(cur, most, z);
+        }
+      }
+      turn ^= 1;
+      __syncthreads();
+    }
+    if (sh.bad[cur]) children = 0;
+    if constexpr (!GREEDY) {
+      if (LAZY && children) {
+        if (tid < n && sh.parent[tid] == cur) {
+          sh.p[tid] = weight(a, cx, sh.m[cur]) / sh.z[cur];
+          sh.q[tid] = cq;
+        }
+        __syncthreads();
+      }
+      if (a.ahead && a.draft && children) {
+        const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
+        for (int c = rank * kWalkWarps + warp; c * kChunk < a.n; c += kParts) prefetch(q + c * kChunk, min(kChunk, a.n - c * kChunk) * 4, lane);
+      }
+    }
     int went = -1;
     while (children) {
       const int i = __ffsll((long long)children) - 1;
@@ -335,28 +497,27 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const VerifyArgs 
       const int x = sh.token[i];
       if constexpr (GREEDY) {
         if (x == sh.best[cur]) went = i;
+      } else if (x < 0 || x >= a.n) {
+        continue;
       } else if (a.draft) {
-        const double w = fmax(wa * double(sh.p[i]) - wb * double(sh.q[i]), 0.0);
-        if (double(sh.u[i]) * double(sh.q[i]) < w) {
+        if (sh.u[i] * sh.q[i] * ws < fmaf(-wb, sh.q[i], sh.p[i])) {
           went = i;
-        } else if (x >= 0 && x < a.n) {
-          const double z = pass(wa, wb + 1.0);
-          summed = z > 0.0;
-          if (summed) {
-            sa = wa;
-            sb = wb + 1.0;
-            wa = sa / z;
-            wb = sb / z;
+        } else {
+          const float z = pass(wb + ws);
+          summed = z > 0.f ? wb + ws : 0.f;
+          if (z > 0.f) {
+            wb += ws;
+            ws = z;
           }
         }
       } else {
-        bool again = x < 0 || x >= a.n;  // no token, or one that is lost already
+        bool again = false;  // lost already
         for (int k = 0; k < lost; ++k) again |= sh.lost[k] == x;
         if (!again) {
-          if (double(sh.u[i]) * fmax(1.0 - gone, 0.0) < double(sh.p[i])) {
+          if (sh.u[i] * kept < sh.p[i]) {
             went = i;
           } else {
-            gone += double(sh.p[i]);
+            kept = fmaxf(kept - sh.p[i], 0.f);
             __syncthreads();
             if (tid == 0) sh.lost[lost] = x;
             ++lost;
@@ -370,23 +531,18 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const VerifyArgs 
     cur = went;
     if (tid == 0) sh.path[count] = went;
     ++count;
-    wa = 1.0;
-    wb = gone = 0.0;
+    wb = summed = 0.f;
+    ws = kept = 1.f;
     lost = 0;
-    summed = false;
   }
   // w as the last pass summed it, where a later one found nothing left
   if constexpr (!GREEDY) {
-    if (a.draft && wb > 0.0 && !summed) {
-      sa = wa;
-      sb = wb;
-      pass(sa, sb);
-    }
+    if (a.draft && wb > 0.f && summed == 0.f) pass(wb);
   }
   if (rank != 0) return;
   __syncthreads();
   if (tid == 0) a.accepted[s] = count;
-  for (int i = tid; i < a.max_rows; i += kThreads) path[i] = i == 0 ? 0 : i <= count ? sh.path[i - 1] : -1;
+  for (int i = tid; i < a.max_rows; i += kWalk) path[i] = i == 0 ? 0 : i <= count ? sh.path[i - 1] : -1;
   if constexpr (GREEDY) {
     if (tid == 0) a.next[s] = sh.bad[cur] ? -1 : sh.best[cur];
     return;
@@ -399,129 +555,155 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const VerifyArgs 
   // the next token, drawn from w
   const Row<T> r(a, int64_t(first) + cur);
   const int chunks = r.chunks();
-  const float2 *st = stats + int64_t(cur) * a.chunks;
   const float *sums = a.sums + int64_t(s) * a.chunks;
-  const bool left = a.draft && wb > 0.0;  // w from the pass's sums, else the target's without the lost tokens
+  const bool left = a.draft && wb > 0.f;  // w from the pass's sums, else the target's without the lost tokens
   const float m = sh.m[cur];
-  for (int k = warp; k < lost; k += kWarps) {  // sums of the chunks that hold lost tokens
-    const int c = (sh.lost[k] + r.lo) / kChunk;
-    float x[kPer];
-    load_chunk<T, false>(r, c * kChunk, lane, x);
-    const float ref = __uint_as_float(ld_u1(&st[c].x));
-    float l = 0.f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = c * kChunk + element<T, false>(j, lane) - r.lo;
-      bool out = !(ref > ninf);
-      for (int o = 0; o < lost; ++o) out |= sh.lost[o] == e;
-      l += out ? 0.f : weight(a, x[j], ref);
+  // the lost tokens of a chunk as bits
+  auto mask_of = [&](uint32_t *mask, int c, int from, int step) {
+    for (int o = from; o < lost; o += step) {
+      const int at = sh.lost[o] + r.lo - c * kChunk;
+      if (at >= 0 && at < kChunk) atomicOr(mask + at / 32, 1u << (at % 32));
     }
-    l = warp_sum(l);
-    if (lane == 0) sh.rest[k] = l;
-  }
-  __syncthreads();
+  };
+  if (!left)
+    for (int k = warp; k < lost; k += kWalkWarps) {  // sums of the chunks that hold lost tokens
+      const int c = (sh.lost[k] + r.lo) / kChunk;
+      uint32_t *mask = sh.mask[warp];
+      __syncwarp();
+      mask[lane] = 0;
+      __syncwarp();
+      mask_of(mask, c, lane, 32);
+      __syncwarp();
+      const float ref = __uint_as_float(chunk_of(cur, c).x);
+      float l = 0.f;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float x[kPer / 2];
+        load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+          const int at = h * (kChunk / 2) + element<T>(j, lane);
+          l += (mask[at / 32] >> (at % 32)) & 1 || !(ref > ninf) ? 0.f : weight(a, x[j], ref);
+        }
+      }
+      l = warp_sum(l);
+      if (lane == 0) sh.rest[k] = l;
+    }
+  if (lost) __syncthreads();
   bool with_lost = false;  // nothing else is left: the lost tokens count again
   auto chunk_sum = [&](int c) {
-    if (left) return double(__ldcg(sums + c));
-    const uint2 v = ld_u2(st + c);
+    if (left) return __ldcg(sums + c);
+    const uint2 v = chunk_of(cur, c);
     float l = __uint_as_float(v.y);
     if (!with_lost)
       for (int k = 0; k < lost; ++k)
         if ((sh.lost[k] + r.lo) / kChunk == c) l = sh.rest[k];
-    return double(l * weight(a, __uint_as_float(v.x), m));
+    return l * weight(a, __uint_as_float(v.x), m);
   };
   // each thread's chunks one after the other; where the sums pass the drawn number
-  const int per = (chunks + kThreads - 1) / kThreads, c0 = min(chunks, tid * per), c1 = min(chunks, c0 + per);
-  double mine = 0.0, before = 0.0, all = 0.0;
-  for (int turn = 0; turn < 2; ++turn) {
-    mine = 0.0;
-    for (int c = c0; c < c1; ++c) mine += chunk_sum(c);
-    double up = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += v;
+  const int per = (chunks + kWalk - 1) / kWalk, c0 = min(chunks, tid * per), c1 = min(chunks, c0 + per);
+  Pair before, all;
+  float v0 = 0.f;  // the first chunk's
+  for (int again = 0; again < 2; ++again) {
+    Pair mine = {0.f, 0.f};
+    for (int c = c0; c < c1; ++c) {
+      const float v = chunk_sum(c);
+      if (c == c0) v0 = v;
+      mine = mine + Pair{v, 0.f};
     }
-    __syncthreads();
+    const Pair up = warp_scan(mine, lane);
     if (lane == 31) sh.part[warp] = up;
     if (tid == 0) sh.chunk = -1;
     __syncthreads();
-    before = up - mine;
-    all = 0.0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sh.part[w];
-      all += sh.part[w];
+    before = up + Pair{-mine.hi, -mine.lo};
+    all = {0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWalkWarps; ++w) {
+      const Pair v = sh.part[w];
+      if (w < warp) before = v + before;
+      all = all + v;
     }
-    if (all > 0.0 || lost == 0) break;
+    if (all.value() > 0.f || lost == 0) break;
     with_lost = true;
+    __syncthreads();
   }
-  const double drawn = double(sh.u[0]) * all;
+  const Pair drawn = sh.u[0] * all;
   {
     // the last chunk with a sum above 0 whose tokens begin at or below the drawn number
-    double at = before;
+    Pair at = before;
     int found = -1;
-    double rest = 0.0;
+    float rest = 0.f;
     for (int c = c0; c < c1; ++c) {
-      const double v = chunk_sum(c);
-      if (v > 0.0 && at <= drawn) {
+      const float v = c == c0 ? v0 : chunk_sum(c);
+      const float over = drawn - at;
+      if (v > 0.f && over >= 0.f) {
         found = c;
-        rest = drawn - at;
+        rest = over;
       }
-      at += v;
+      at = at + Pair{v, 0.f};
     }
     if (found >= 0) atomicMax(&sh.chunk, found);
     __syncthreads();
     if (found >= 0 && sh.chunk == found) sh.left = rest;
     __syncthreads();
   }
-  if (warp != 0) return;
+  // the last token of that chunk with a weight whose range begins at or below the drawn number, each thread's beside one another
   const int c = sh.chunk;
   if (c < 0) {  // no sum above 0: draft probabilities that are no numbers
-    if (lane == 0) a.next[s] = -1;
+    if (tid == 0) a.next[s] = -1;
     return;
   }
-  float x[kPer], y[kPer];
-  load_chunk<T, true>(r, c * kChunk, lane, x);
-  double to = sh.left;
-  const float ref = left ? m : __uint_as_float(ld_u1(&st[c].x));
-  if (left) {
-    load_draft<T, true>(a.draft + (int64_t(first) + cur) * a.draft_stride, r, c * kChunk, lane, y);
-  } else {
-    to /= double(weight(a, ref, m));  // in the chunk's own units
-  }
-  const float fa = float(sa / sh.z[cur]), fb = float(sb);
-  double own = 0.0;
+  if (tid < kChunk / 32) sh.mask[0][tid] = 0;
+  if (tid == 0) sh.next = -1;
+  __syncthreads();
+  if (!with_lost) mask_of(sh.mask[0], c, tid, kWalk);
+  constexpr int kOwn = kChunk / kWalk;
+  float x[kOwn], y[kOwn];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int e = c * kChunk + element<T, true>(k, lane) - r.lo;
-    float w;
-    if (left) {
-      w = fmaxf(fmaf(fa, weight(a, x[k], m), -fb * y[k]), 0.f);
-    } else {
-      bool out = !(x[k] > ninf);
-      if (!with_lost)
-        for (int o = 0; o < lost; ++o) out |= sh.lost[o] == e;
-      w = out ? 0.f : weight(a, x[k], ref);
-    }
-    x[k] = w;
-    own += double(w);
+  for (int k = 0; k < kOwn; ++k) {
+    const int e = c * kChunk + tid * kOwn + k;
+    const bool in = e >= r.lo && e < r.hi;
+    x[k] = in ? load1(r.x + e) : ninf;
+    y[k] = in && left ? load1(a.draft + (int64_t(first) + cur) * a.draft_stride + e - r.lo) : 0.f;
   }
-  double up = own;
+  const float ref = left ? m : __uint_as_float(chunk_of(cur, c).x), inv = 1.f / sh.z[cur];
+  float to = sh.left;
+  if (!left) to /= weight(a, ref, m);  // in the chunk's own units
+  __syncthreads();
+  float own = 0.f;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int at = tid * kOwn + k;
+    if (left) {
+      x[k] = fmaxf(fmaf(inv, weight(a, x[k], m), -wb * y[k]), 0.f);
+    } else {
+      x[k] = (sh.mask[0][at / 32] >> (at % 32)) & 1 || !(x[k] > ninf) ? 0.f : weight(a, x[k], ref);
+    }
+    own += x[k];
+  }
+  float up = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double v = __shfl_up_sync(0xffffffffu, up, o);
+    const float v = __shfl_up_sync(0xffffffffu, up, o);
     if (lane >= o) up += v;
   }
-  // the last token with a weight whose range begins at or below the drawn number
-  double at = up - own;
+  if (lane == 31) sh.part[warp].hi = up;
+  __syncthreads();
+  float at = __shfl_up_sync(0xffffffffu, up, 1);
+  if (lane == 0) at = 0.f;
+  float below = 0.f;
+  for (int w = 0; w < warp; ++w) below += sh.part[w].hi;
+  at += below;
   int token = -1;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (x[k] > 0.f && at <= to) token = c * kChunk + element<T, true>(k, lane) - r.lo;
-    at += double(x[k]);
+  for (int k = 0; k < kOwn; ++k) {
+    if (x[k] > 0.f && at <= to) token = c * kChunk + tid * kOwn + k - r.lo;
+    at += x[k];
   }
   token = __reduce_max_sync(0xffffffffu, token);
-  if (lane == 0) a.next[s] = token;
+  if (lane == 0 && token >= 0) atomicMax(&sh.next, token);
+  __syncthreads();
+  if (tid == 0) a.next[s] = sh.next;
 }
 
 // Chunks of a row, whatever its alignment.
@@ -531,7 +713,7 @@ template <int CTAS, typename Kernel>
 cudaError_t launch_walk(Kernel kernel, const VerifyArgs &a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.n_seqs) * CTAS);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kWalk);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -584,15 +766,20 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
   const int most = (a.chunks + kWarps - 1) / kWarps;  // CTAs of a row with a chunk for each warp
   a.groups = rows * most <= 8 * di.sm_count ? most : (most + 3) / 4;
   if (rows * a.groups > 0x7fffffff || int64_t(n_seqs) * kCluster > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
+  a.ahead = n_seqs <= 8;
+  const bool wide = a.chunks > 2 * kWarps;
   e = cudaError_t(with_type(type, [&](auto t) {
     using T = decltype(t);
+    if (wide && max_rows > 1 && rows * n * int64_t(sizeof(T)) > kLazyBytes)
+      return int(greedy ? launch_walk<kCluster>(verify_walk_kernel<T, true, kCluster, true>, a, s)
+                        : launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, true>, a, s));
     const dim3 grid(unsigned(rows * a.groups));
     const cudaError_t r = greedy ? launch(verify_stats_kernel<T, true>, grid, dim3(kThreads), 0, s, a)
                                  : launch(verify_stats_kernel<T, false>, grid, dim3(kThreads), 0, s, a);
     if (r != cudaSuccess) return int(r);
-    if (greedy) return int(launch_walk<1>(verify_walk_kernel<T, true, 1>, a, s));
-    if (a.draft && a.chunks > 2 * kWarps) return int(launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster>, a, s));
-    return int(launch_walk<1>(verify_walk_kernel<T, false, 1>, a, s));
+    if (greedy) return int(launch_walk<1>(verify_walk_kernel<T, true, 1, false>, a, s));
+    if (a.draft && wide) return int(launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, false>, a, s));
+    return int(launch_walk<1>(verify_walk_kernel<T, false, 1, false>, a, s));
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }
