@@ -23,6 +23,10 @@
 // chunks' sums, and the token in it by a warp.
 // Sums within a chunk are f32, over chunks pairs of f32 (48 bits; f64 adds have a 64th of f32's rate here and were most
 // of the walk's time), p, b and S f32.
+// A kernel's code runs once here, so that its length is time too (fetched from the L2): the draw is two tokens to a thread, not
+// 32 to a lane of one warp, which took 4 us more.
+// Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 9.9 us; 48 chains of 2
+// to 8, bf16 29 us; 16 trees of 9 to 40, f32, without probabilities 19 us; one row 6.3 us.
 // Bound: memory for many rows, the chain of loads and joins for few.
 #include "qdq_types.cuh"
 
@@ -33,8 +37,11 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the first kernel
 constexpr int kWalk = 512, kWalkWarps = kWalk / 32;    // of the walk
 constexpr int kPer = 32;             // logits per lane
 constexpr int kChunk = 32 * kPer;    // ... and warp
-constexpr int kCluster = 8;          // CTAs that share a rejection's pass
-constexpr int64_t kLazyBytes = int64_t(128) << 20;  // of logits, from which on the walk reads the rows
+constexpr int kCluster = 8;          // CTAs of a sequence at most
+// Of logits, from which on the walk reads the rows it reaches (its steps take 2 to 3 us each): 16 trees of 9 to 40 of 128256,
+// f32 (328 MB at most) 19 us, by all rows 44; 48 chains of 2 to 8, bf16 (98 MB) 41 against 33; 48 trees of 6, f32 (148) 39
+// against 41.
+constexpr int64_t kLazyBytes = int64_t(128) << 20;
 constexpr float kFar = -1e30f;       // stands for -inf, whose product with 0 would be NaN
 
 struct VerifyArgs {
@@ -190,29 +197,24 @@ __device__ __forceinline__ void prefetch(const void *p, int bytes, int lane) {
 // What is kept of a chunk: its largest logit and the sum of exponentials relative to it, or its best key.
 template <typename T, bool GREEDY>
 __device__ __forceinline__ uint2 chunk_stats(const VerifyArgs &a, const Row<T> &r, int c, int lane, const float (&x)[kPer]) {
-  if constexpr (GREEDY) {
-    // (outside the row -inf: no better than a row's elements, and behind them)
-    uint32_t best = 0;
+  float m = x[0];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) best = max(best, uint32_t(topk_key(x[k], 0u) >> 32));
-    best = __reduce_max_sync(0xffffffffu, best);
+  for (int k = 1; k < kPer; ++k) m = max_nan(m, x[k]);
+  m = warp_max_nan(m);
+  if constexpr (GREEDY) {
+    // the first that equals it (a row whose largest is NaN or -inf has no best token, so that any will do there)
     int at = 0x7fffffff;
 #pragma unroll
-    for (int k = kPer - 1; k >= 0; --k) {
-      const int e = c * kChunk + element<T>(k, lane);
-      if (uint32_t(topk_key(x[k], 0u) >> 32) == best && e >= r.lo && e < r.hi) at = e;
-    }
+    for (int k = kPer - 1; k >= 0; --k)
+      if (x[k] == m) at = c * kChunk + element<T>(k, lane);
     at = __reduce_min_sync(0xffffffffu, at);
-    return make_uint2(~uint32_t(at - r.lo), best);
+    const uint64_t key = topk_key(m, uint32_t(at - r.lo));
+    return make_uint2(uint32_t(key), uint32_t(key >> 32));
   } else {
-    float m = x[0];
-#pragma unroll
-    for (int k = 1; k < kPer; ++k) m = max_nan(m, x[k]);
-    m = warp_max_nan(m);
     const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
     float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) l[k & 3] += weight(a, x[k], ref);
+    for (int k = 0; k < kPer; ++k) l[k & 3] += ex2((x[k] - ref) * a.c_hi);  // (c_lo: a share of the sum below 2^-25)
     return make_uint2(__float_as_uint(m), __float_as_uint(warp_sum((l[0] + l[1]) + (l[2] + l[3]))));
   }
 }
@@ -766,19 +768,24 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
   const int most = (a.chunks + kWarps - 1) / kWarps;  // CTAs of a row with a chunk for each warp
   a.groups = rows * most <= 8 * di.sm_count ? most : (most + 3) / 4;
   if (rows * a.groups > 0x7fffffff || int64_t(n_seqs) * kCluster > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
-  a.ahead = n_seqs <= 8;
-  const bool wide = a.chunks > 2 * kWarps;
+  a.ahead = n_seqs <= 8;  // (where it costs no bandwidth that other sequences need)
+  // 8 CTAs to a sequence while all are resident together, else 4: 48 chains of 128256 29.3 us, with 8 32.6; 1 chain 11.4, with 8 9.9
+  const bool wide = a.chunks > 2 * kWarps, few = int64_t(n_seqs) * kCluster <= 2 * di.sm_count;
   e = cudaError_t(with_type(type, [&](auto t) {
     using T = decltype(t);
     if (wide && max_rows > 1 && rows * n * int64_t(sizeof(T)) > kLazyBytes)
-      return int(greedy ? launch_walk<kCluster>(verify_walk_kernel<T, true, kCluster, true>, a, s)
-                        : launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, true>, a, s));
+      return int(greedy  ? few ? launch_walk<kCluster>(verify_walk_kernel<T, true, kCluster, true>, a, s)
+                               : launch_walk<kCluster / 2>(verify_walk_kernel<T, true, kCluster / 2, true>, a, s)
+                 : few ? launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, true>, a, s)
+                       : launch_walk<kCluster / 2>(verify_walk_kernel<T, false, kCluster / 2, true>, a, s));
     const dim3 grid(unsigned(rows * a.groups));
     const cudaError_t r = greedy ? launch(verify_stats_kernel<T, true>, grid, dim3(kThreads), 0, s, a)
                                  : launch(verify_stats_kernel<T, false>, grid, dim3(kThreads), 0, s, a);
     if (r != cudaSuccess) return int(r);
     if (greedy) return int(launch_walk<1>(verify_walk_kernel<T, true, 1, false>, a, s));
-    if (a.draft && wide) return int(launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, false>, a, s));
+    if (a.draft && wide)
+      return int(few ? launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, false>, a, s)
+                     : launch_walk<kCluster / 2>(verify_walk_kernel<T, false, kCluster / 2, false>, a, s));
     return int(launch_walk<1>(verify_walk_kernel<T, false, 1, false>, a, s));
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
