@@ -494,7 +494,8 @@ int qdq_check_status(void) {
   if (qdq_checks_enabled() && cudaDeviceSynchronize() != cudaSuccess) return -1;
   const int r[] = {read_checks_dl(), read_checks_xs(), read_checks_gemm(), read_checks_topk(), read_checks_q6k(),
                    read_checks_attn(), read_checks_attn_tc(), read_checks_logprobs(), read_checks_tree(),
-                   read_checks_tree_tc(), read_checks_verify()};
+                   read_checks_tree_tc(), read_checks_verify(),
+                   read_checks_rope()};
   int v = 0;
   for (int x : r) {
     if (x < 0) return -1;

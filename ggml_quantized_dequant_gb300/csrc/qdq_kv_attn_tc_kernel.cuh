@@ -1379,6 +1379,7 @@ __global__ void __launch_bounds__(kTcRows) attn_tree_join_kernel(const AttnArgs 
   const long long first = before + (long long)h * (en.tiles + kTcPartCost);
   const int c_lo = owner(first + kTcPartCost), nsplit = owner(first + kTcPartCost + en.tiles - 1) - c_lo + 1;
   if (nsplit == 1 || tid >= en.nr) return;
+  if (!QDQ_GUARD(2 * (int64_t(c_lo) + nsplit) * kPart <= a.room, QDQ_CHECK_OUT)) return;
   const bool another = first > total * c_lo / shares;
   const float4 *p = reinterpret_cast<const float4 *>(a.partial + 2 * int64_t(c_lo) * kPart) + (4 * slice) * kTcRows + tid;
   const float *q = a.partial + 2 * int64_t(c_lo) * kPart + D * kTcRows + tid;

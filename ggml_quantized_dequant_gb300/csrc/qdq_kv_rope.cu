@@ -187,6 +187,10 @@ __device__ __forceinline__ void quantise(const RopeArgs &a, uint8_t *record, int
                                          const float (&x)[Lanes<D>::NI][Lanes<D>::C][8], int lane) {
   using L = Lanes<D>;
   const int sub = lane % L::LPT, page_tokens = a.c.page_tokens;
+  if (!QDQ_GUARD(t0 + kKvBlock <= page_tokens && record >= a.c.pages &&
+                     record + kv_record_bytes(page_tokens, D) <= a.c.pages + int64_t(a.c.n_pages) * a.c.n_kv * kv_record_bytes(page_tokens, D),
+                 QDQ_CHECK_OUT))
+    return;
   int8_t *codes = reinterpret_cast<int8_t *>(record) + (int64_t(which) * page_tokens + t0) * D;
   const Scale sc(s_old, m);
   const bool grown = held && sc.now != sc.old;
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_r
             s_max[r & 1][warp][1] = mv;
           }
           __syncthreads();
-          if (!there) continue;
+          if (!there || !QDQ_GUARD(t0 + kKvBlock <= a.c.page_tokens && at0 + (h + 1) * rec <= int64_t(a.c.n_pages) * a.c.n_kv * rec, QDQ_CHECK_OUT)) continue;
 #pragma unroll
           for (int y = 0; y < L::NI; ++y) {
             mk = max_abs(mk, s_max[r & 1][group * L::NI + y][0]);
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_r
             }
             if (hh + kAhead * stride < a.n_heads) load(r[y], qp + (hh + kAhead * stride) * D, false);
             norm_turn<D, ADJACENT, true>(a, x, a.q_weight != nullptr, w, cs, sn, sub);
-            if (in) {
+            if (in && QDQ_GUARD(i >= 0 && i < n && hh < a.n_heads, QDQ_CHECK_OUT)) {
 #pragma unroll
               for (int c = 0; c < L::C; ++c) {
                 const Couple<ADJACENT> cp(a, sub + L::LPT * c);
@@ -649,5 +653,7 @@ int launch_kv_append_rope(const KvPool &c, int head_dim, const int *kv_len, cons
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }
+
+QDQ_CHECK_READER(read_checks_rope)
 
 }  // namespace qdq

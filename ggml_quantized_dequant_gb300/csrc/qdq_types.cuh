@@ -138,6 +138,7 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
 int read_checks_tree();
 int read_checks_tree_tc();
 int read_checks_verify();
+int read_checks_rope();
 // A workspace holds the tickets (zero between calls) in its first eighth and the parts in the rest.  The
 // border follows from the workspace's size alone, so that no call of another shape or operator on the
 // same workspace writes where this one's tickets are.

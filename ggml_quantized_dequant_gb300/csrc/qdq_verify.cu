@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyArgs
     float x[kPer];
     load_run<T>(r, c * kChunk, lane, x);
     const uint2 v = chunk_stats<T, GREEDY>(a, r, c, lane, x);
-    if (lane == 0) *reinterpret_cast<uint2 *>(a.stats + int64_t(at) * a.chunks + c) = v;
+    if (lane == 0 && QDQ_GUARD(c < a.chunks, QDQ_CHECK_OUT)) *reinterpret_cast<uint2 *>(a.stats + int64_t(at) * a.chunks + c) = v;
   }
 }
 
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         for (int k = 0; k < kPer / 2; ++k) l[k & 1] += fmaxf(fmaf(inv, weight(a, x[k], m), -b * y[k]), 0.f);
       }
       const float sum = warp_sum(l[0] + l[1]);
-      if (lane == 0) sums[c] = sum;
+      if (lane == 0 && QDQ_GUARD(c < a.chunks, QDQ_CHECK_OUT)) sums[c] = sum;
       z = z + Pair{sum, 0.f};
     }
     exchange<CTAS>(sh, turn, make_uint2(__float_as_uint(z.hi), __float_as_uint(z.lo)), rank, warp, lane);
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
           const uint64_t mine = (uint64_t(v.y) << 32) | v.x;
           key = mine > key ? mine : key;
         } else {
-          if (lane == 0) *reinterpret_cast<uint2 *>(stats + int64_t(cur) * a.chunks + c) = v;
+          if (lane == 0 && QDQ_GUARD(c < a.chunks && cur < a.max_rows, QDQ_CHECK_OUT)) *reinterpret_cast<uint2 *>(stats + int64_t(cur) * a.chunks + c) = v;
           const float mine = __uint_as_float(v.x), most = max_nan(m, mine);
           if (most > ninf) l = l * weight(a, m, most) + __uint_as_float(v.y) * weight(a, mine, most);
           m = most;
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
           } else {
             kept = fmaxf(kept - sh.p[i], 0.f);
             __syncthreads();
-            if (tid == 0) sh.lost[lost] = x;
+            if (tid == 0 && QDQ_GUARD(lost < QDQ_MAX_TREE, QDQ_CHECK_SMEM)) sh.lost[lost] = x;
             ++lost;
             __syncthreads();
           }
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     }
     if (went < 0) break;
     cur = went;
-    if (tid == 0) sh.path[count] = went;
+    if (tid == 0 && QDQ_GUARD(count < QDQ_MAX_TREE, QDQ_CHECK_SMEM)) sh.path[count] = went;
     ++count;
     wb = summed = 0.f;
     ws = kept = 1.f;

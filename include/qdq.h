@@ -428,7 +428,7 @@ int qdq_token_logprobs(const void *logits, long long row_stride, int type, const
  *   freqs (n_rot / 2 f32, radians per position; NULL: nothing is turned): pair i of a head's first n_rot elements,
  *     (a, b) -> (a cos t - b sin t, b cos t + a sin t) with t = position * freqs[i]; the pair is elements
  *     (2i, 2i + 1) where interleaved is 1, else (i, i + n_rot / 2).  n_rot: a multiple of 8, at most head_dim.
- *     For freqs up to 1 the angle is off by at most 2^-30 before cos and sin, at every position.
+ *     For freqs up to 1 the angle is off by at most 2^-29 + position * 2^-52, and an f32's rounding, before cos and sin.
  *   q_out: the queries in the type (may be exactly q with its stride); keys go into the cache in f32, values as they are,
  *   by the definition of qdq_kv_append, whose other arguments, refusals and dropped tokens hold here.
  *   parent NULL: tokens one after the other (position = place in the cache).  q and q_out NULL with n_heads 0: keys and values alone.
@@ -455,7 +455,7 @@ int qdq_token_logprobs(const void *logits, long long row_stride, int type, const
  *   A drafted token outside [0, n) is not accepted.  Numbers outside [0, 1) count as the nearest inside.  At a node
  *   whose row has a NaN or +inf, or nothing above -inf, no child is accepted and next_token is -1.  A sequence without
  *   rows gets accepted -1, next_token -1 and a path of -1.  max_rows: at most QDQ_MAX_TREE; rows past it do not count.
- *   p is computed in f32 relative to 2^-20, sums in f64: a number that lies that near a border may fall to either side.
+ *   p and w are computed in f32 relative to 2^-20: a number that lies that near a border may fall to either side.
  *   workspace: qdq_verify_drafts_workspace_bytes(...) bytes, 256-byte aligned; it may be shared as those above.
  *
  * qdq_kv_keep moves the cached tokens of the accepted paths: of sequence s's last n = cu[s + 1] - cu[s] tokens, node

@@ -737,6 +737,131 @@ def test_keep_scales_that_are_zero_or_nan(cuda_lib):
     _same_cache(raw, c)
 
 
+# ------------------------------------------------------------------ many tokens, many rows: the kernels that large calls take
+
+# A warp keeps its tokens from 6 new tokens of a sequence and 160 of the batch on.
+ROPE_MANY = [
+    ([0, 3, 17, 40], [64, 9, 33, 50], 5, 3, 64, 16, "f32", 64, False, True, "tree"),
+    ([0, 3, 17, 40], [64, 0, 33, 1], 9, 2, 96, 48, "bf16", 96, True, True, "forest"),
+    ([7, 3, 15], [60, 64, 64], 17, 1, 128, 16, "f16", 56, False, True, "star"),
+    ([100, 31, 0], [64, 64, 40], 2, 9, 192, 64, "f32", 8, True, False, "tree"),
+    ([100, 31, 0], [64, 64, 40], 8, 2, 256, 32, "bf16", 256, False, True, "chain"),
+    ([1, 2, 3, 4, 5] * 8, [6, 1, 0, 5, 3] * 8, 24, 8, 128, 64, "f32", 128, False, True, None),
+    ([160, 2], [161, 1], 0, 2, 64, 16, "bf16", 64, False, True, None),
+    ([15], [162], 1, 1, 64, 16, "f16", 0, False, False, None),
+]
+
+
+@pytest.mark.parametrize("old,new,heads,n_kv,dim,page,dtype,turned,interleaved,norm,kind", ROPE_MANY)
+def test_append_rope_of_many_tokens(cuda_lib, old, new, heads, n_kv, dim, page, dtype, turned, interleaved, norm, kind):
+    rng = np.random.default_rng(sum(old) + dim + heads)
+    if heads == 0:  # keys and values alone: as with one head of queries
+        r = [_append_rope(cuda_lib, np.random.default_rng(5), old, new, h, n_kv, dim, page, dtype, turned, interleaved, norm, kind)
+             for h in (1,)][0]
+        raw, _, _ = _filled(np.random.default_rng(5), old, page, n_kv, dim, n_pages=r["raw"].shape[0])
+        cuda_lib.kv_append_rope(raw, _i32(r["table"]), _i32(r["lens"]), None, None, r["k"], r["v"], 0, n_kv, dim, page, _t(r["freqs"]),
+                                interleaved, None, _t(r["kw"]), 1e-6, cu_new=_i32(r["cu"]), max_new=max(new))
+        assert np.array_equal(raw.cpu().numpy(), r["raw"].cpu().numpy())
+        return
+    r = _append_rope(cuda_lib, rng, old, new, heads, n_kv, dim, page, dtype, turned, interleaved, norm, kind)
+    _check_rope(r, old, new, n_kv, dim, page, dtype, interleaved)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_append_rope_of_many_tokens_is_that_of_few(cuda_lib, dim):
+    # one batch at once, and its sequences one by one (other kernels): the cache bit for bit, missing pages, a sequence that has
+    # more new tokens than tokens and nodes without a parent among them
+    import torch
+    rng = np.random.default_rng(dim)
+    heads, n_kv, page, seqs, m = 6, 2, 16, 8, 24
+    old = [int(x) for x in rng.integers(0, 60, seqs)]
+    lens = [x + m for x in old]
+    raw, table, c = _filled(rng, lens, page, n_kv, dim)
+    lens[3] = m - 1
+    table[4, (old[4] + m - 1) // page] = -1
+    parents = np.concatenate([_parents(rng, m) for _ in range(seqs)]).astype(np.int32)
+    parents[5 * m + 10] = 12
+    parents[6 * m + 3] = -2
+    q, k, v = (_t(rng.standard_normal((seqs * m, h, dim)).astype(np.float32)) for h in (heads, n_kv, n_kv))
+    freqs, w = _t((10000.0 ** (-np.arange(dim // 2) * 2 / dim)).astype(np.float32)), _t(rng.uniform(0.5, 1.5, dim).astype(np.float32))
+    whole, single = raw.clone(), raw.clone()
+    outs = [torch.full_like(q, 5.0) for _ in range(2)]
+    cuda_lib.kv_append_rope(whole, _i32(table), _i32(lens), q, outs[0], k, v, heads, n_kv, dim, page, freqs, q_weight=w, k_weight=w,
+                            cu_new=_i32(np.arange(seqs + 1) * m), max_new=m, parent=_i32(parents))
+    for s in range(seqs):
+        at = slice(s * m, s * m + m)
+        cuda_lib.kv_append_rope(single, _i32(table[s:s + 1]), _i32(lens[s:s + 1]), q[at], outs[1][at], k[at], v[at], heads, n_kv, dim, page,
+                                freqs, q_weight=w, k_weight=w, cu_new=_i32([0, m]), max_new=m, parent=_i32(parents[at]))
+    assert torch.isnan(outs[0][3 * m:4 * m]).all() and torch.isnan(outs[0][5 * m + 10]).all() and torch.isnan(outs[0][6 * m + 3]).all()
+    assert torch.equal(torch.isnan(outs[0]), torch.isnan(outs[1])) and torch.equal(outs[0].nan_to_num(), outs[1].nan_to_num())
+    _same_cache(whole, ref.Cache(single.cpu().numpy(), page, n_kv, dim))
+
+
+# The walk reads the rows that it reaches where 128 MiB of logits could be rows (a bound by max_rows); more than two CTAs to
+# an SM at 8 to a sequence make it 4.
+VERIFY_MANY = [
+    ([5, 9, 64, 1, 0, 6, 20, 3, 2, 7, 4, 30], 60001, "tree", True, 1.0, "f32"),
+    ([5, 9, 64, 1, 0, 6, 20, 3, 2, 7, 4, 30], 120003, "tree", False, 0.8, "bf16"),
+    ([40, 9, 33, 1, 0, 6, 20, 3, 2, 7, 4, 30], 120000, "star", True, 1.0, "f16"),
+    ([40, 9, 33, 1, 0, 6, 20, 3, 2, 7, 4, 30], 90000, "star", False, 1.0, "f32"),
+    ([5, 9, 64, 1, 0, 6, 20, 3, 2, 7, 4, 30], 100001, "tree", True, 0.0, "bf16"),
+    ([3, 1, 2, 0, 5] * 9 + [40], 30001, "chain", True, 1.0, "f32"),
+    ([3, 1, 2, 0, 5] * 9 + [40], 40001, "tree", False, 1.0, "f16"),
+    ([3, 1, 2, 0, 5] * 9 + [40], 30007, "tree", False, 0.0, "f32"),
+    ([3, 1, 2, 0, 5] * 9, 20001, "chain", True, 1.0, "f32"),
+    ([3, 1, 2, 0, 5] * 9, 18001, "tree", True, 1.2, "bf16"),
+]
+
+
+@pytest.mark.parametrize("nodes,n,kind,drafts,temperature,dtype", VERIFY_MANY)
+def test_verify_many_rows(cuda_lib, nodes, n, kind, drafts, temperature, dtype):
+    rng = np.random.default_rng(n)
+    w = _problem(rng, nodes, n, kind, drafts, temperature, dtype)
+    _check_verify(w, _verify(cuda_lib, w))
+
+
+@pytest.mark.parametrize("temperature", [0.0, 1.0])
+def test_verify_many_rows_that_are_not_finite(cuda_lib, temperature):
+    # a NaN, +inf or a row of -inf at the root, at a draft that is reached and at one that is not
+    import torch
+    rng = np.random.default_rng(3)
+    seqs, m, n = 40, 21, 45000
+    x = torch.randn(seqs * m, n, device="cuda")
+    tokens = rng.integers(0, n, seqs * m)
+    for s in range(seqs):
+        x[s * m, tokens[s * m + 1]] = 60.0  # the first draft is accepted
+    x[0, 44999] = float("nan")
+    x[m, 0] = float("inf")
+    x[2 * m] = float("-inf")
+    x[3 * m + 1, 30000] = float("nan")
+    x[4 * m + 1] = float("-inf")
+    x[5 * m + 2] = float("nan")
+    parents = np.tile(np.concatenate([[-1, 0], np.zeros(m - 2, int)]), (seqs, 1))
+    w = dict(x=x, tokens=tokens, parents=list(parents), u=rng.random(seqs * m).astype(np.float32), probs=None, cu=_cu([m] * seqs),
+             nodes=[m] * seqs, n=n, temperature=temperature, kind="tree")
+    acc, path, nxt = _verify(cuda_lib, w)
+    assert acc.tolist() == [0, 0, 0] + [1] * (seqs - 3)
+    assert (nxt[:5] == -1).all() and (nxt[5:] >= 0).all() and (nxt < n).all()
+    assert (path[:3, 1:] == -1).all() and (path[3:, 1] == 1).all()
+
+
+def test_verify_many_rows_by_either_way(cuda_lib):
+    # rows past the sequences' own make the bound large: the same problem read at once and row by row, with masked logits
+    import torch
+    rng = np.random.default_rng(9)
+    w = _problem(rng, [6, 3, 9, 12, 1, 7], 50000, "tree", True, 1.0, "f32")
+    w["x"][:, rng.choice(50000, 20000, replace=False)] = torch.finfo(torch.float32).min
+    w["x"][:, 7::11] = float("-inf")
+    few, many = _verify(cuda_lib, w), _verify(cuda_lib, w, max_rows=64)
+    assert 6 * 64 * 50000 * 4 <= 128 << 20 < 12 * 64 * 50000 * 4
+    w2 = dict(w, nodes=w["nodes"] * 2, parents=w["parents"] * 2, cu=_cu(w["nodes"] * 2), tokens=np.tile(w["tokens"], 2), u=np.tile(w["u"], 2),
+              x=w["x"].repeat(2, 1), probs=np.tile(w["probs"], (2, 1)))
+    lazy = _verify(cuda_lib, w2, max_rows=64)
+    for a, b in ((few[0], many[0]), (few[2], many[2]), (np.tile(few[0], 2), lazy[0]), (np.tile(few[2], 2), lazy[2]),
+                 (np.tile(many[1], (2, 1)), lazy[1])):
+        assert np.array_equal(a, b)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
