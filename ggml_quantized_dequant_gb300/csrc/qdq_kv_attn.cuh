@@ -149,7 +149,8 @@ __device__ __forceinline__ uint32_t tree_sees(uint64_t seen, int base, int lo, i
 // (256 in two parts does not fit shared memory).
 constexpr int kTcRows = 128;
 // What a unit costs besides its tiles of 64 tokens, in tiles: a part costs 11 us, a tile 1.2 us, a join 8 us.  (4
-// sequences of 300 queries over 300 to 2500 tokens, 32 / 8 heads of 128, f16: 9 75.2 us, 12 70.4, 15 70.2, 18 70.6.)
+// sequences of 300 queries over 300 to 2500 tokens, 32 / 8 heads of 128, f16: 9 75.2 us, 12 70.4, 15 70.2, 18 70.6; 48 trees of 22
+// nodes behind 300 to 3000: 8 127, 11 121, 15 118, 20 123.)
 constexpr int kTcPartCost = 15;
 constexpr int kTcSplitBlocks = 256;  // blocks of 16 tokens in one part, at most
 constexpr int kTcTreeBlocks = 768;  // ... of a tree's

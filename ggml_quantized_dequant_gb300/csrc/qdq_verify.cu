@@ -766,7 +766,8 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
   a.stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes));
   a.sums = reinterpret_cast<float *>(a.stats + rows * a.chunks);
   const int most = (a.chunks + kWarps - 1) / kWarps;  // CTAs of a row with a chunk for each warp
-  a.groups = rows * most <= 8 * di.sm_count ? most : (most + 3) / 4;
+  // many rows: two chunks for each warp (48 chains 28.6 us, with four 29.3, with one 30.5)
+  a.groups = rows * most <= 8 * di.sm_count ? most : (most + 1) / 2;
   if (rows * a.groups > 0x7fffffff || int64_t(n_seqs) * kCluster > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
   a.ahead = n_seqs <= 8;  // (where it costs no bandwidth that other sequences need)
   // 8 CTAs to a sequence while all are resident together, else 4: 48 chains of 128256 29.3 us, with 8 32.6; 1 chain 11.4, with 8 9.9

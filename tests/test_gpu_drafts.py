@@ -862,6 +862,47 @@ def test_verify_many_rows_by_either_way(cuda_lib):
         assert np.array_equal(a, b)
 
 
+def test_verify_replayed_graphs_share_a_workspace(cuda_lib):
+    # clusters and all rows at once, captured into graphs with one workspace, replayed in turns with other inputs
+    import torch
+    rng = np.random.default_rng(77)
+    shapes = [([6, 3, 9, 12], 40000, True, 12), ([6, 3, 9, 12, 1, 7] * 2, 50000, False, 64), ([5] * 40, 20001, True, 5), ([4, 7], 3001, True, 7)]
+    first, second = ([_problem(rng, nodes, n, "tree", drafts, 1.0, "f32") for nodes, n, drafts, _ in shapes] for _ in range(2))
+    ws = torch.zeros(max(cuda_lib.verify_drafts_workspace_bytes(len(x[0]), x[3], x[1]) for x in shapes), dtype=torch.uint8, device="cuda")
+    runs = []
+    for w, x in zip(first, shapes):
+        seqs = len(x[0])
+        acc, path, nxt = (torch.full(shape, -9, dtype=torch.int32, device="cuda") for shape in ((seqs,), (seqs, x[3]), (seqs,)))
+        ins = dict(x=w["x"].clone(), tokens=_i32(w["tokens"]), u=_t(w["u"]), parent=_i32(np.concatenate(w["parents"])),
+                   probs=None if w["probs"] is None else _t(w["probs"]))
+
+        def call(ins=ins, acc=acc, path=path, nxt=nxt, w=w, x=x, cu=_i32(w["cu"])):
+            cuda_lib.verify_drafts(ins["x"], ins["tokens"], ins["u"], acc, path, nxt, x[1], ws, cu=cu, max_rows=x[3], parent=ins["parent"],
+                                   draft_probs=ins["probs"])
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, ins, (acc, path, nxt), call))  # (the call holds cu)
+    for problems in (second, first):
+        for (_, ins, outs, _), w in zip(runs, problems):
+            ins["x"].copy_(w["x"])
+            ins["tokens"].copy_(_i32(w["tokens"]))
+            ins["u"].copy_(_t(w["u"]))
+            ins["parent"].copy_(_i32(np.concatenate(w["parents"])))
+            if ins["probs"] is not None:
+                ins["probs"].copy_(_t(w["probs"]))
+            for t in outs:
+                t.fill_(-9)
+        for graph, _, _, _ in runs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, outs, _), w in zip(runs, problems):
+            _check_verify(w, tuple(_np(t) for t in outs))
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
