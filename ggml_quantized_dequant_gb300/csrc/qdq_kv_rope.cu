@@ -18,9 +18,9 @@
 //   heads and tokens, so that a single token's heads spread over all warps.
 //   rows (many): a warp keeps 4 or 8 tokens and goes through the heads with them.
 // Measured (alone, in a graph): one token, 24 / 8 heads of 128, f32 5.3 us; 48 trees of 5 to 26 tokens, 32 / 8 heads of 128,
-// bf16 10.3 us (items 13.9); 6 prompts of 900 to 3000 tokens, 24 / 8 heads of 128, bf16 58 us, 5.2 TB/s (items 85).
-// Bound: for prompts memory and the instructions' issue (half its rate) together; for single tokens the chain of launch,
-// length, page and scale.
+// bf16 9.7 us (items 13.9); 6 prompts of 900 to 3000 tokens, 24 / 8 heads of 128, bf16 53 us, 4.2 TB/s (items 85).
+// Bound: for prompts the loads that 16 warps to an SM have in flight and the instructions' issue (half its rate) together; for
+// single tokens the chain of launch, length, page and scale.
 #include "qdq_types.cuh"
 
 namespace qdq {
@@ -107,40 +107,74 @@ __device__ __forceinline__ void load_weight(const float *p, const Couple &cp, fl
   w[7] = v.w;
 }
 
-// Norm (weight: of the lane's elements) and rotation of a token's head; cosines and sines by couples, the lane's or the
-// token's.
+// Two f32 in one register pair: an instruction for both.
+struct Two {
+  unsigned long long v;
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Two(unsigned long long x) : v(x) {}
+  __device__ __forceinline__ void to(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(const Two &a, const Two &b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return Two(r);
+}
+__device__ __forceinline__ Two fma(const Two &a, const Two &b, const Two &c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return Two(r);
+}
+
+// Norm (weight: of the lane's elements) and rotation of a token's head, all times `factor`; cosines and sines by couples, the
+// lane's or the token's.  Each product and sum is rounded by itself in either kernel and kind of pairs, so that they agree:
+// ((a w_a) cos - (b w_b) sin) / rms, ((b w_b) cos + [(a w_a) sin]) / rms, with one rounding for what is in brackets.
 template <int D, bool ADJACENT, bool IN_LANE>
 __device__ __forceinline__ void norm_turn(const RopeArgs &a, float (&x)[Lanes<D>::C][8], bool norm, const float (&weight)[Lanes<D>::C][8],
-                                          const float4 *cs, const float4 *sn, int sub) {
+                                          const float4 *cs, const float4 *sn, int sub, float factor) {
   using L = Lanes<D>;
   if (norm) {
-    float s = 0.f;
+    Two s(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < L::C; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(x[c][e], x[c][e], s);
+      for (int e = 0; e < 8; e += 2) {
+        const Two v(x[c][e], x[c][e + 1]);
+        s = fma(v, v, s);
+        (v * Two(weight[c][e], weight[c][e + 1])).to(x[c][e], x[c][e + 1]);
+      }
+    float s0, s1;
+    s.to(s0, s1);
+    s0 += s1;
 #pragma unroll
-    for (int o = L::LPT / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float inv = rsqrtf(s * (1.f / D) + a.eps);
-#pragma unroll
-    for (int c = 0; c < L::C; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[c][e] *= inv * weight[c][e];
+    for (int o = L::LPT / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    factor *= rsqrtf(s0 * (1.f / D) + a.eps);
   }
+  const Two minus(-1.f, -1.f), times(factor, factor);
 #pragma unroll
   for (int c = 0; c < L::C; ++c) {
     const int j = sub + L::LPT * c;
     if (j < a.n_rot / 8) {
       const float4 co = cs[IN_LANE ? c : j], si = sn[IN_LANE ? c : j];
-      const float cw[4] = {co.x, co.y, co.z, co.w}, sw[4] = {si.x, si.y, si.z, si.w};
+      if constexpr (ADJACENT) {
+        const float cw[4] = {co.x, co.y, co.z, co.w}, sw[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float &u = x[c][ADJACENT ? 2 * e : e], &v = x[c][ADJACENT ? 2 * e + 1 : 4 + e];
-        const float p = u, q = v;
-        u = p * cw[e] - q * sw[e];
-        v = q * cw[e] + p * sw[e];
+        for (int e = 0; e < 4; ++e) {
+          const float p = x[c][2 * e], q = x[c][2 * e + 1];
+          x[c][2 * e] = __fmaf_rn(__fmul_rn(q, sw[e]), -1.f, __fmul_rn(p, cw[e]));
+          x[c][2 * e + 1] = __fmaf_rn(p, sw[e], __fmul_rn(q, cw[e]));
+        }
+      } else {
+        const Two cw[2] = {Two(co.x, co.y), Two(co.z, co.w)}, sw[2] = {Two(si.x, si.y), Two(si.z, si.w)};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Two p(x[c][2 * e], x[c][2 * e + 1]), q(x[c][4 + 2 * e], x[c][5 + 2 * e]);
+          fma(q * sw[e], minus, p * cw[e]).to(x[c][2 * e], x[c][2 * e + 1]);
+          fma(p, sw[e], q * cw[e]).to(x[c][4 + 2 * e], x[c][5 + 2 * e]);
+        }
       }
     }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) (Two(x[c][e], x[c][e + 1]) * times).to(x[c][e], x[c][e + 1]);
   }
 }
 
@@ -166,7 +200,7 @@ struct Scale {
 // Four new codes.  A product with 1 / s is at most 127 and some roundings, so that 1.5 2^23 added and its bits' low byte
 // are rint and its code.
 __device__ __forceinline__ uint32_t new_codes(const float *v, const Scale &sc) {
-  uint32_t w[4];
+  uint32_t w[4];  // (a product and a sum of two f32 at once come out as one rounding here, which is not the definition)
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[e], sc.inv), 12582912.f));
   const uint32_t r = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
@@ -351,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
               if (which == 0 && (i + 1) * L::GT > held && i * L::GT < end) {
                 const int tt = min(max(t, held), end - 1);  // (a lane whose token is no new one: zeros by any angle)
                 norm_turn<D, ADJACENT, false>(a, x[i], wp != nullptr, w, reinterpret_cast<const float4 *>(s_cos[tt]),
-                                              reinterpret_cast<const float4 *>(s_sin[tt]), sub);
+                                              reinterpret_cast<const float4 *>(s_sin[tt]), sub, 1.f);
                 if (t == tt && s_bad[tt]) m = qnan;
               }
               // (tokens that are not new: their zeros stay zeros, unless an angle is NaN)
@@ -379,16 +413,12 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 3 : 2) kv_append_rope_
                 raw[i][c][1].values(x[c] + 4);
               }
               norm_turn<D, ADJACENT, false>(a, x, wp != nullptr, w, reinterpret_cast<const float4 *>(s_cos[t]),
-                                            reinterpret_cast<const float4 *>(s_sin[t]), sub);
+                                            reinterpret_cast<const float4 *>(s_sin[t]), sub, s_bad[t] ? qnan : 1.f);
               T *o = static_cast<T *>(a.q_out) + (row0 + t) * a.q_out_stride + hq * D;
-              const bool wrong = s_bad[t];
               if (u < q_all) {
 #pragma unroll
                 for (int c = 0; c < L::C; ++c) {
                   const Couple<ADJACENT> cp(a, sub + L::LPT * c);
-                  if (wrong)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[c][e] = qnan;
                   store4(o + cp.a, make_float4(x[c][0], x[c][1], x[c][2], x[c][3]));
                   store4(o + cp.b, make_float4(x[c][4], x[c][5], x[c][6], x[c][7]));
                 }
@@ -407,7 +437,8 @@ constexpr int kRowsCtas = D == 64 ? 5 - (sizeof(T) == 4) : D == 128 ? (sizeof(T)
 // Prompts: a warp keeps GT tokens of the block and goes through the heads with them, their cosines and sines in
 // registers (no tables, and a quarter of the registers that a whole block's keys take).  The NI warps that share a block
 // exchange the largest magnitudes of a head's keys and values; the next head's elements are on the way meanwhile.
-// A CTA for 8 heads: for 4 the prompts take 70 us, for 8 58, for 12 59, for all 74.
+// A CTA for 8 heads: for 6 the prompts take 61 us, for 8 53, for 12 54; three heads of queries on their way: with two 56, with
+// four 52.5, but heads of 256 in f32 38 instead of 37.
 template <typename T, int D, bool ADJACENT>
 __global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_rows_kernel(const RopeArgs a) {
   using L = Lanes<D>;
@@ -508,7 +539,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_r
             load(rk, kp + (h + stride) * D, false);
             load(rv, vp + (h + stride) * D, true);
           }
-          norm_turn<D, ADJACENT, true>(a, xk, a.k_weight != nullptr, w, cs, sn, sub);
+          norm_turn<D, ADJACENT, true>(a, xk, a.k_weight != nullptr, w, cs, sn, sub, 1.f);
           if (in) {
 #pragma unroll
             for (int c = 0; c < L::C; ++c)
@@ -570,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_r
         if (a.q_weight)
 #pragma unroll
           for (int c = 0; c < L::C; ++c) load_weight(a.q_weight, Couple<ADJACENT>(a, sub + L::LPT * c), w[c]);
-        constexpr int kAhead = 2;  // heads whose elements are on the way
+        constexpr int kAhead = 3;  // heads whose elements are on the way
         Raw<T> r[kAhead][L::C][2];
 #pragma unroll
         for (int y = 0; y < kAhead; ++y)
@@ -587,14 +618,11 @@ __global__ void __launch_bounds__(kWarps * 32, kRowsCtas<T, D>) kv_append_rope_r
               r[y][c][1].values(x[c] + 4);
             }
             if (hh + kAhead * stride < a.n_heads) load(r[y], qp + (hh + kAhead * stride) * D, false);
-            norm_turn<D, ADJACENT, true>(a, x, a.q_weight != nullptr, w, cs, sn, sub);
+            norm_turn<D, ADJACENT, true>(a, x, a.q_weight != nullptr, w, cs, sn, sub, wrong ? qnan : 1.f);
             if (in && QDQ_GUARD(i >= 0 && i < n && hh < a.n_heads, QDQ_CHECK_OUT)) {
 #pragma unroll
               for (int c = 0; c < L::C; ++c) {
                 const Couple<ADJACENT> cp(a, sub + L::LPT * c);
-                if (wrong)
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) x[c][e] = qnan;
                 store4(op + hh * D + cp.a, make_float4(x[c][0], x[c][1], x[c][2], x[c][3]));
                 store4(op + hh * D + cp.b, make_float4(x[c][4], x[c][5], x[c][6], x[c][7]));
               }
