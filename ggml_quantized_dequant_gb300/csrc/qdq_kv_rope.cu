@@ -107,24 +107,6 @@ __device__ __forceinline__ void load_weight(const float *p, const Couple &cp, fl
   w[7] = v.w;
 }
 
-// Two f32 in one register pair: an instruction for both.
-struct Two {
-  unsigned long long v;
-  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ explicit Two(unsigned long long x) : v(x) {}
-  __device__ __forceinline__ void to(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ Two operator*(const Two &a, const Two &b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-  return Two(r);
-}
-__device__ __forceinline__ Two fma(const Two &a, const Two &b, const Two &c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return Two(r);
-}
-
 // Norm (weight: of the lane's elements) and rotation of a token's head, all times `factor`; cosines and sines by couples, the
 // lane's or the token's.  Each product and sum is rounded by itself in either kernel and kind of pairs, so that they agree:
 // ((a w_a) cos - (b w_b) sin) / rms, ((b w_b) cos + [(a w_a) sin]) / rms, with one rounding for what is in brackets.

@@ -83,6 +83,29 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v.x, v.y, T{}), pack2(v.z, v.w, T{}));
 }
 
+// Two f32 in one register pair: an instruction for both.
+struct Two {
+  unsigned long long v;
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Two(unsigned long long x) : v(x) {}
+  __device__ __forceinline__ void to(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(const Two &a, const Two &b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return Two(r);
+}
+__device__ __forceinline__ Two operator+(const Two &a, const Two &b) {  // (of products: may come out as one rounding)
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return Two(r);
+}
+__device__ __forceinline__ Two fma(const Two &a, const Two &b, const Two &c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return Two(r);
+}
+
 // Larger of two non-negative floats with a NaN counted as the largest (the order of their bits).
 __device__ __forceinline__ float max_abs_bits(float a, float b) {
   const uint32_t x = __float_as_uint(a) & 0x7FFFFFFFu, y = __float_as_uint(b) & 0x7FFFFFFFu;

@@ -26,7 +26,7 @@
 // A kernel's code runs once here, so that its length is time too (fetched from the L2): the draw is two tokens to a thread, not
 // 32 to a lane of one warp, which took 4 us more.
 // Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 9.9 us; 48 chains of 2
-// to 8, bf16 29 us; 16 trees of 9 to 40, f32, without probabilities 19 us; one row 6.3 us.
+// to 8, bf16 28 us; 16 trees of 9 to 40, f32, without probabilities 19 us; one row 6.3 us.
 // Bound: memory for many rows, the chain of loads and joins for few.
 #include "qdq_types.cuh"
 
@@ -212,10 +212,17 @@ __device__ __forceinline__ uint2 chunk_stats(const VerifyArgs &a, const Row<T> &
     return make_uint2(uint32_t(key), uint32_t(key >> 32));
   } else {
     const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
-    float l[4] = {0.f, 0.f, 0.f, 0.f};
+    const Two off(-ref, -ref), factor(a.c_hi, a.c_hi);  // (c_lo: a share of the sum below 2^-25)
+    Two l[2] = {Two(0.f, 0.f), Two(0.f, 0.f)};
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) l[k & 3] += ex2((x[k] - ref) * a.c_hi);  // (c_lo: a share of the sum below 2^-25)
-    return make_uint2(__float_as_uint(m), __float_as_uint(warp_sum((l[0] + l[1]) + (l[2] + l[3]))));
+    for (int k = 0; k < kPer; k += 2) {
+      float u, v;
+      ((Two(x[k], x[k + 1]) + off) * factor).to(u, v);
+      l[k / 2 % 2] = l[k / 2 % 2] + Two(ex2(u), ex2(v));
+    }
+    float u, v;
+    (l[0] + l[1]).to(u, v);
+    return make_uint2(__float_as_uint(m), __float_as_uint(warp_sum(u + v)));
   }
 }
 
