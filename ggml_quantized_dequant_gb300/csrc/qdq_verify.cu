@@ -21,13 +21,16 @@
 // read), its warps' sums exchanged through one another's shared memory.  Then every child's p and q at once, and the
 // comparisons; a rejection's pass is shared by the cluster, too.  The drawn token's chunk is found from the
 // chunks' sums, and the token in it by a warp.
-// Sums within a chunk are f32, over chunks pairs of f32 (48 bits; f64 adds have a 64th of f32's rate here and were most
-// of the walk's time), p, b and S f32.
+// Sums within a chunk are f32, without its likeliest token, which is taken as a pair of f32 like the sums over chunks (48 bits; f64
+// adds have a 64th of f32's rate here and were most of the walk's time); p, b and S are f32 in the comparisons.
 // A kernel's code runs once here, so that its length is time too (fetched from the L2): the draw is two tokens to a thread, not
 // 32 to a lane of one warp, which took 4 us more.
-// Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 9.9 us; 48 chains of 2
-// to 8, bf16 28 us; 16 trees of 9 to 40, f32, without probabilities 19 us; one row 6.3 us.
+// Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 12.9 us; 48 chains of 2
+// to 8, bf16 37 us; 16 trees of 9 to 40, f32, without probabilities 25 us; one row 7.6 us.  (All in f32: 9.9, 28, 19 and 6.3, but of
+// 9600 drawn tokens 8 were a neighbour of the exact one, now 1.)
 // Bound: memory for many rows, the chain of loads and joins for few.
+#include <cmath>
+
 #include "qdq_types.cuh"
 
 namespace qdq {
@@ -38,10 +41,11 @@ constexpr int kWalk = 512, kWalkWarps = kWalk / 32;    // of the walk
 constexpr int kPer = 32;             // logits per lane
 constexpr int kChunk = 32 * kPer;    // ... and warp
 constexpr int kCluster = 8;          // CTAs of a sequence at most
-// Of logits, from which on the walk reads the rows it reaches (its steps take 2 to 3 us each): 16 trees of 9 to 40 of 128256,
-// f32 (328 MB at most) 19 us, by all rows 44; 48 chains of 2 to 8, bf16 (98 MB) 41 against 33; 48 trees of 6, f32 (148) 39
-// against 41.
+// Of logits, from which on the walk reads the rows it reaches (its steps take 3 to 4 us each).  Measured before sums were pairs: 16
+// trees of 9 to 40 of 128256, f32 (328 MB at most) 19 us, by all rows 44; 48 chains of 2 to 8, bf16 (98 MB) 41 against 33; 48 trees
+// of 6, f32 (148) 39 against 41.
 constexpr int64_t kLazyBytes = int64_t(128) << 20;
+constexpr float kBig = 1.f / 512.f;  // a probability from which on a token's weight is taken as a pair where the next token is drawn
 constexpr float kFar = -1e30f;       // stands for -inf, whose product with 0 would be NaN
 
 struct VerifyArgs {
@@ -50,8 +54,8 @@ struct VerifyArgs {
   const int *tokens, *cu, *parent;
   const float *draft, *uniform;
   int *accepted, *path, *next;
-  float2 *stats;  // [sequence][row][chunk]: largest logit, sum of 2^((x - largest) c); temperature 0: a 64-bit key
-  float *sums;    // [sequence][chunk]: of a rejection's pass
+  float2 *stats;  // [sequence][row][chunk]: largest logit, the others' sum of 2^((x - largest) c); temperature 0: a 64-bit key
+  float2 *sums;   // [sequence][chunk]: of a rejection's pass, as pairs
   int n_seqs, max_rows, n, chunks, groups;  // chunks: of a row, at most
   bool ahead;                               // draft probabilities that may be needed are brought into the L2
   float c_hi, c_lo;                         // log2(e) / temperature in two parts
@@ -189,12 +193,45 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t key) {
   }
   return key;
 }
+__device__ __forceinline__ Pair operator*(const Pair &a, const Pair &b) {
+  const float h = a.hi * b.hi;
+  return {h, fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi)};
+}
+// weight() to 2^-30: the difference and its product with the factor as pairs, 2^i times the series of e^g, |g| <= ln(2) / 2.
+__device__ __forceinline__ Pair weight_pair(const VerifyArgs &a, float x, float m) {
+  const float y = x - m, back = y - x, rest = (x - (y - back)) - (m + back);
+  const float h = y * a.c_hi;
+  if (!(h > -100.f)) return {0.f, 0.f};
+  const float i = rintf(h), f = h - i, l = fmaf(y, a.c_hi, -h) + fmaf(y, a.c_lo, rest * a.c_hi);
+  const float g = f * 0.693147182464599609375f;  // ln 2 and what is left of it
+  const Pair e = {g, fmaf(f, 0.693147182464599609375f, -g) + fmaf(f, -1.904654323148236e-9f, l * 0.693147182464599609375f)};
+  float r = 1.f / 362880.f;
+  r = fmaf(r, g, 1.f / 40320.f);
+  r = fmaf(r, g, 1.f / 5040.f);
+  r = fmaf(r, g, 1.f / 720.f);
+  r = fmaf(r, g, 1.f / 120.f);
+  r = fmaf(r, g, 1.f / 24.f);
+  r = fmaf(r, g, 1.f / 6.f);
+  const Pair v = Pair{1.f, 0.f} + e + 0.5f * (e * e) + Pair{r * g * g * g, 0.f};
+  return __int_as_float((127 + int(i)) << 23) * v;
+}
+__device__ __forceinline__ Pair reciprocal(const Pair &z) {
+  const float i = 1.f / z.value();
+  return {i, i * (fmaf(-i, z.hi, 1.f) - i * z.lo)};
+}
+// What max(p - b q, 0) is of a logit x, as a pair.
+__device__ __forceinline__ Pair share(const VerifyArgs &a, const Pair &inverse, float x, float m, float b, float q) {
+  const float t = b * q;
+  const Pair w = inverse * weight_pair(a, x, m) + Pair{-t, -fmaf(b, q, -t)};
+  return w.value() > 0.f ? w : Pair{0.f, 0.f};
+}
 // A chunk of 1024 elements of size B at p, less what the row does not have, into the L2.
 __device__ __forceinline__ void prefetch(const void *p, int bytes, int lane) {
   for (int o = lane * 128; o < bytes; o += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + o));
 }
 
-// What is kept of a chunk: its largest logit and the sum of exponentials relative to it, or its best key.
+// What is kept of a chunk: its largest logit and the sum of the others' exponentials relative to it, or its best key.  (The largest is
+// 1 by itself: beside it the others would lose what lies below its last place.)
 template <typename T, bool GREEDY>
 __device__ __forceinline__ uint2 chunk_stats(const VerifyArgs &a, const Row<T> &r, int c, int lane, const float (&x)[kPer]) {
   float m = x[0];
@@ -212,22 +249,28 @@ __device__ __forceinline__ uint2 chunk_stats(const VerifyArgs &a, const Row<T> &
     return make_uint2(uint32_t(key), uint32_t(key >> 32));
   } else {
     const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
-    const Two off(-ref, -ref), factor(a.c_hi, a.c_hi);  // (c_lo: a share of the sum below 2^-25)
-    Two l[2] = {Two(0.f, 0.f), Two(0.f, 0.f)};
+    const Two off(-ref, -ref), hi(a.c_hi, a.c_hi), lo(a.c_lo, a.c_lo);
+    Two l(0.f, 0.f), ones(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kPer; k += 2) {
-      float u, v;
-      ((Two(x[k], x[k + 1]) + off) * factor).to(u, v);
-      l[k / 2 % 2] = l[k / 2 % 2] + Two(ex2(u), ex2(v));
+      float u, v, p, q;
+      const Two y = Two(x[k], x[k + 1]) + off;
+      y.to(p, q);
+      const Two one(p == 0.f ? -1.f : 0.f, q == 0.f ? -1.f : 0.f);
+      fma(y, hi, y * lo).to(u, v);
+      l = l + (Two(ex2(u), ex2(v)) + one);
+      ones = ones + one;
     }
-    float u, v;
-    (l[0] + l[1]).to(u, v);
-    return make_uint2(__float_as_uint(m), __float_as_uint(warp_sum(u + v)));
+    float u, v, p, q;
+    l.to(u, v);
+    ones.to(p, q);
+    const float more = __reduce_add_sync(0xffffffffu, int(-(p + q))) - 1;  // of equal largest ones
+    return make_uint2(__float_as_uint(m), __float_as_uint(warp_sum(u + v) + (m == ref ? more : 0.f)));
   }
 }
 
 template <typename T, bool GREEDY>
-__global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) verify_stats_kernel(const VerifyArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.x % a.groups, at = blockIdx.x / a.groups, s = at / a.max_rows, i = at % a.max_rows;
   pdl_launch_dependents();
@@ -254,25 +297,25 @@ __device__ __forceinline__ void all_ctas() {  // barrier, with global writes bef
 }
 
 struct WalkShared {
-  uint2 parts[2][kCluster * kWalkWarps];  // every warp's part of a sum or a maximum, of the cluster; two exchanges in turn
-  float z[QDQ_MAX_TREE];              // a row's sum of weights relative to its largest logit
+  uint4 parts[2][kCluster * kWalkWarps];  // every warp's part of a sum or a maximum, of the cluster; two exchanges in turn
+  Pair z[QDQ_MAX_TREE];               // a row's sum of weights relative to its largest logit
   float m[QDQ_MAX_TREE];              // its largest logit
   int best[QDQ_MAX_TREE];             // temperature 0: its best token
   int bad[QDQ_MAX_TREE];              // a NaN or +inf, or nothing above -inf
   int parent[QDQ_MAX_TREE], token[QDQ_MAX_TREE], path[QDQ_MAX_TREE];
   float p[QDQ_MAX_TREE], q[QDQ_MAX_TREE], u[QDQ_MAX_TREE];  // of a child: its probabilities at its parent, its number
   int lost[QDQ_MAX_TREE];             // rejected drafts without probabilities, at the present node
-  float rest[QDQ_MAX_TREE];           // their chunks' sums without them
+  Pair rest[QDQ_MAX_TREE];            // their chunks' sums without them
   uint32_t mask[kWalkWarps][kChunk / 32];  // a chunk's lost tokens
   Pair part[kWalkWarps];
-  float left;
+  Pair left;
   int chunk, next;
 };
 
 // Every warp's part to every CTA of the cluster; what the warps wrote to global memory before is visible behind it.
 template <int CTAS>
-__device__ __forceinline__ void exchange(WalkShared &sh, int turn, uint2 mine, int rank, int warp, int lane) {
-  uint2 *to = &sh.parts[turn][rank * kWalkWarps + warp];
+__device__ __forceinline__ void exchange(WalkShared &sh, int turn, uint4 mine, int rank, int warp, int lane) {
+  uint4 *to = &sh.parts[turn][rank * kWalkWarps + warp];
   if constexpr (CTAS == 1) {
     if (lane == 0) *to = mine;
     __syncthreads();
@@ -280,7 +323,7 @@ __device__ __forceinline__ void exchange(WalkShared &sh, int turn, uint2 mine, i
     if (lane < CTAS) {
       uint32_t at = uint32_t(__cvta_generic_to_shared(to));
       asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(lane));
-      asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(mine.x), "r"(mine.y) : "memory");
+      asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(mine.x), "r"(mine.y), "r"(mine.z), "r"(mine.w) : "memory");
     }
     __syncwarp();
     all_ctas<CTAS>();
@@ -337,16 +380,18 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     sh.bad[i] = hi >= 0xFF800000u || hi <= 0x007FFFFFu;
     sh.best[i] = int(~uint32_t(key));
   };
-  // a row's largest logit and sum, from lanes' largest ones and sums relative to them
-  auto row_sum = [&](int i, float m, Pair z) {
-    const float most = warp_max_nan(m);
-    const bool bad = !(most > ninf && most < -ninf);
-    z = warp_sum_pair((bad || m == ninf ? 0.f : weight(a, m, most)) * z);
+  // a row's largest logit, and its sum from lanes' sums relative to it
+  auto row_sum = [&](int i, float most, Pair z) {
+    z = warp_sum_pair(z);
     if (lane == 0) {
-      sh.bad[i] = bad;
+      sh.bad[i] = !(most > ninf && most < -ninf);
       sh.m[i] = most;
-      sh.z[i] = z.value();
+      sh.z[i] = z;
     }
+  };
+  // a chunk's sum relative to a row's largest logit
+  auto chunk_part = [&](const uint2 &v, float most) {
+    return weight_pair(a, __uint_as_float(v.x), most) * (Pair{1.f, 0.f} + Pair{__uint_as_float(v.y), 0.f});
   };
   auto chunk_of = [&](int node, int c) { return ld_u2(stats + int64_t(node) * a.chunks + c); };
   if constexpr (!LAZY) {
@@ -364,22 +409,18 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         key = warp_max_key(key);
         if (lane == 0) row_key(i, key);
       } else {
+        uint2 v[4];  // (all at up to 128 chunks)
         float m = ninf;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < chunks ? chunk_of(i, lane + 32 * k) : make_uint2(0xff800000u, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max_nan(m, __uint_as_float(v[k].x));
+        for (int c = lane + 128; c < chunks; c += 32) m = max_nan(m, __uint_as_float(chunk_of(i, c).x));
+        m = warp_max_nan(m);
         Pair z = {0.f, 0.f};
-        for (int c0 = lane; c0 < chunks; c0 += 4 * 32) {
-          uint2 v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = c0 + 32 * k < chunks ? chunk_of(i, c0 + 32 * k) : make_uint2(0xff800000u, 0);
-          float most = m;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) most = max_nan(most, __uint_as_float(v[k].x));
-          if (most > ninf) {  // (NaN and +inf: bad, whatever the sum)
-            z = weight(a, m, most) * z;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z = z + Pair{__uint_as_float(v[k].y) * weight(a, __uint_as_float(v[k].x), most), 0.f};
-          }
-          m = most;
-        }
+        for (int k = 0; k < 4; ++k) z = z + chunk_part(v[k], m);
+        for (int c = lane + 128; c < chunks; c += 32) z = z + chunk_part(chunk_of(i, c), m);
         row_sum(i, m, z);
       }
     }
@@ -388,7 +429,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   if constexpr (!LAZY && !GREEDY) {
     if (tid < n && sh.parent[tid] >= 0) {
       const int up = sh.parent[tid];
-      sh.p[tid] = sh.bad[up] ? 0.f : weight(a, cx, sh.m[up]) / sh.z[up];
+      sh.p[tid] = sh.bad[up] ? 0.f : weight(a, cx, sh.m[up]) / sh.z[up].value();
       sh.q[tid] = cq;
     }
     __syncthreads();
@@ -402,29 +443,45 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   auto pass = [&](float b) {
     const Row<T> r(a, int64_t(first) + cur);
     const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
-    const float inv = 1.f / sh.z[cur], m = sh.m[cur];
+    const float m = sh.m[cur];
+    const Pair inverse = reciprocal(sh.z[cur]);
+    const float inv = inverse.hi, big = kBig * sh.z[cur].value(), nan = __int_as_float(0x7fffffff);
     const int chunks = r.chunks();
-    float *sums = a.sums + int64_t(s) * a.chunks;
+    float2 *sums = a.sums + int64_t(s) * a.chunks;
     Pair z = {0.f, 0.f};
     for (int c = rank * kWalkWarps + warp; c < chunks; c += kParts) {
+      float top = __uint_as_float(chunk_of(cur, c).x);  // where it is likely: its tokens' shares as pairs, the others' in f32
+      if (!(weight(a, top, m) > big)) top = nan;
       float l[2] = {0.f, 0.f};
+      uint32_t tops = 0;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float x[kPer / 2], y[kPer / 2];
         load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
         load_draft<T>(q, r, c * kChunk + h * (kChunk / 2), lane, y);
 #pragma unroll
-        for (int k = 0; k < kPer / 2; ++k) l[k & 1] += fmaxf(fmaf(inv, weight(a, x[k], m), -b * y[k]), 0.f);
+        for (int k = 0; k < kPer / 2; ++k) {
+          if (x[k] == top)
+            tops |= 1u << (h * (kPer / 2) + k);
+          else
+            l[k & 1] += fmaxf(fmaf(inv, weight(a, x[k], m), -b * y[k]), 0.f);
+        }
       }
-      const float sum = warp_sum(l[0] + l[1]);
-      if (lane == 0 && QDQ_GUARD(c < a.chunks, QDQ_CHECK_OUT)) sums[c] = sum;
-      z = z + Pair{sum, 0.f};
+      Pair sum = {l[0] + l[1], 0.f};
+      for (; tops; tops &= tops - 1) {
+        const int j = __ffs(tops) - 1, e = c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane);
+        sum = sum + share(a, inverse, top, m, b, load1(q + e - r.lo));
+      }
+      __syncwarp();
+      sum = warp_sum_pair(sum);
+      if (lane == 0 && QDQ_GUARD(c < a.chunks, QDQ_CHECK_OUT)) sums[c] = make_float2(sum.hi, sum.lo);
+      z = z + sum;
     }
-    exchange<CTAS>(sh, turn, make_uint2(__float_as_uint(z.hi), __float_as_uint(z.lo)), rank, warp, lane);
+    exchange<CTAS>(sh, turn, make_uint4(__float_as_uint(z.hi), __float_as_uint(z.lo), 0, 0), rank, warp, lane);
     z = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < (kParts + 31) / 32; ++k) {
-      const uint2 v = lane + 32 * k < kParts ? sh.parts[turn][lane + 32 * k] : make_uint2(0, 0);
+      const uint4 v = lane + 32 * k < kParts ? sh.parts[turn][lane + 32 * k] : make_uint4(0, 0, 0, 0);
       z = z + Pair{__uint_as_float(v.x), __uint_as_float(v.y)};
     }
     turn ^= 1;
@@ -439,7 +496,8 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     if constexpr (LAZY) {
       const Row<T> r(a, int64_t(first) + cur);
       const int chunks = r.chunks();
-      float m = ninf, l = 0.f;
+      float m = ninf;
+      Pair l = {0.f, 0.f};
       uint64_t key = 0;
       for (int c = rank * kWalkWarps + warp; c < chunks; c += kParts) {
         float x[kPer];
@@ -452,17 +510,22 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         } else {
           if (lane == 0 && QDQ_GUARD(c < a.chunks && cur < a.max_rows, QDQ_CHECK_OUT)) *reinterpret_cast<uint2 *>(stats + int64_t(cur) * a.chunks + c) = v;
           const float mine = __uint_as_float(v.x), most = max_nan(m, mine);
-          if (most > ninf) l = l * weight(a, m, most) + __uint_as_float(v.y) * weight(a, mine, most);
+          const Pair part = Pair{1.f, 0.f} + Pair{__uint_as_float(v.y), 0.f};
+          if (m == ninf)
+            l = part;
+          else if (most > ninf)
+            l = weight_pair(a, m, most) * l + weight_pair(a, mine, most) * part;
           m = most;
         }
       }
-      exchange<CTAS>(sh, turn, GREEDY ? make_uint2(uint32_t(key), uint32_t(key >> 32)) : make_uint2(__float_as_uint(m), __float_as_uint(l)), rank, warp, lane);
+      exchange<CTAS>(sh, turn, GREEDY ? make_uint4(uint32_t(key), uint32_t(key >> 32), 0, 0)
+                                        : make_uint4(__float_as_uint(m), __float_as_uint(l.hi), __float_as_uint(l.lo), 0), rank, warp, lane);
       if (warp == 0) {
         if constexpr (GREEDY) {
           key = 0;
 #pragma unroll
           for (int k = 0; k < (kParts + 31) / 32; ++k) {
-            const uint2 v = sh.parts[turn][lane + 32 * k];
+            const uint4 v = sh.parts[turn][lane + 32 * k];
             const uint64_t mine = (uint64_t(v.y) << 32) | v.x;
             key = mine > key ? mine : key;
           }
@@ -472,13 +535,13 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
           float most = ninf;
 #pragma unroll
           for (int k = 0; k < kParts / 32; ++k) most = max_nan(most, __uint_as_float(sh.parts[turn][lane + 32 * k].x));
+          most = warp_max_nan(most);
           Pair z = {0.f, 0.f};
-          if (most > ninf)
 #pragma unroll
-            for (int k = 0; k < kParts / 32; ++k) {
-              const uint2 v = sh.parts[turn][lane + 32 * k];
-              z = z + Pair{__uint_as_float(v.y) * weight(a, __uint_as_float(v.x), most), 0.f};
-            }
+          for (int k = 0; k < kParts / 32; ++k) {
+            const uint4 v = sh.parts[turn][lane + 32 * k];
+            z = z + weight_pair(a, __uint_as_float(v.x), most) * Pair{__uint_as_float(v.y), __uint_as_float(v.z)};
+          }
           row_sum(cur, most, z);
         }
       }
@@ -489,7 +552,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     if constexpr (!GREEDY) {
       if (LAZY && children) {
         if (tid < n && sh.parent[tid] == cur) {
-          sh.p[tid] = weight(a, cx, sh.m[cur]) / sh.z[cur];
+          sh.p[tid] = weight(a, cx, sh.m[cur]) / sh.z[cur].value();
           sh.q[tid] = cq;
         }
         __syncthreads();
@@ -561,12 +624,18 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     return;
   }
 
-  // the next token, drawn from w
+  // The next token, drawn from w.  A drawn number is often next to the border of two tokens where most of the vocabulary
+  // shares little of the probability (128256 tokens with 1 %: 8e-8 each), so what lies before it is summed with likely tokens
+  // by weight_pair, and the others, whose roundings are a share of little, in f32.
   const Row<T> r(a, int64_t(first) + cur);
   const int chunks = r.chunks();
-  const float *sums = a.sums + int64_t(s) * a.chunks;
-  const bool left = a.draft && wb > 0.f;  // w from the pass's sums, else the target's without the lost tokens
-  const float m = sh.m[cur];
+  const float2 *sums = a.sums + int64_t(s) * a.chunks;
+  const float *q = a.draft ? a.draft + (int64_t(first) + cur) * a.draft_stride : nullptr;
+  const bool left = a.draft && wb > 0.f;  // w by the pass's sums, else the target's without the lost tokens
+  const float m = sh.m[cur], big = kBig * sh.z[cur].value();
+  const Pair inverse = reciprocal(sh.z[cur]);
+  const float inv = inverse.hi;
+  bool with_lost = false;  // nothing else is left: the lost tokens count again
   // the lost tokens of a chunk as bits
   auto mask_of = [&](uint32_t *mask, int c, int from, int step) {
     for (int o = from; o < lost; o += step) {
@@ -574,87 +643,96 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
       if (at >= 0 && at < kChunk) atomicOr(mask + at / 32, 1u << (at % 32));
     }
   };
-  if (!left)
-    for (int k = warp; k < lost; k += kWalkWarps) {  // sums of the chunks that hold lost tokens
-      const int c = (sh.lost[k] + r.lo) / kChunk;
-      uint32_t *mask = sh.mask[warp];
-      __syncwarp();
-      mask[lane] = 0;
-      __syncwarp();
-      mask_of(mask, c, lane, 32);
-      __syncwarp();
-      const float ref = __uint_as_float(chunk_of(cur, c).x);
-      float l = 0.f;
+  // sums of the chunks that hold lost tokens
+  for (int k = warp; k < lost; k += kWalkWarps) {
+    const int c = (sh.lost[k] + r.lo) / kChunk;
+    uint32_t *mask = sh.mask[warp];
+    __syncwarp();
+    mask[lane] = 0;
+    __syncwarp();
+    mask_of(mask, c, lane, 32);
+    __syncwarp();
+    uint32_t likes = 0;  // this lane's likely tokens
+    float l = 0.f;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float x[kPer / 2];
-        load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
+    for (int h = 0; h < 2; ++h) {
+      float x[kPer / 2];
+      load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
 #pragma unroll
-        for (int j = 0; j < kPer / 2; ++j) {
-          const int at = h * (kChunk / 2) + element<T>(j, lane);
-          l += (mask[at / 32] >> (at % 32)) & 1 || !(ref > ninf) ? 0.f : weight(a, x[j], ref);
-        }
+      for (int j = 0; j < kPer / 2; ++j) {
+        const int at = h * (kChunk / 2) + element<T>(j, lane);
+        const float w = x[j] > ninf && !((mask[at / 32] >> (at % 32)) & 1) ? weight(a, x[j], m) : 0.f;
+        if (w > big)
+          likes |= 1u << (h * (kPer / 2) + j);
+        else
+          l += w;
       }
-      l = warp_sum(l);
-      if (lane == 0) sh.rest[k] = l;
     }
+    Pair sum = {l, 0.f};
+    for (; likes; likes &= likes - 1) {
+      const int j = __ffs(likes) - 1;
+      sum = sum + weight_pair(a, load1(r.x + c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane)), m);
+    }
+    __syncwarp();
+    sum = warp_sum_pair(sum);
+    if (lane == 0) sh.rest[k] = sum;
+  }
   if (lost) __syncthreads();
-  bool with_lost = false;  // nothing else is left: the lost tokens count again
   auto chunk_sum = [&](int c) {
-    if (left) return __ldcg(sums + c);
-    const uint2 v = chunk_of(cur, c);
-    float l = __uint_as_float(v.y);
+    if (c >= chunks) return Pair{0.f, 0.f};
+    if (left) {
+      const float2 v = __ldcg(sums + c);
+      return Pair{v.x, v.y};
+    }
     if (!with_lost)
       for (int k = 0; k < lost; ++k)
-        if ((sh.lost[k] + r.lo) / kChunk == c) l = sh.rest[k];
-    return l * weight(a, __uint_as_float(v.x), m);
+        if ((sh.lost[k] + r.lo) / kChunk == c) return sh.rest[k];
+    return chunk_part(chunk_of(cur, c), m);
   };
   // each thread's chunks one after the other; where the sums pass the drawn number
-  const int per = (chunks + kWalk - 1) / kWalk, c0 = min(chunks, tid * per), c1 = min(chunks, c0 + per);
-  Pair before, all;
-  float v0 = 0.f;  // the first chunk's
+  const int per = (chunks + kWalk - 1) / kWalk, c0 = tid * per;
+  Pair before, all, v0;
   for (int again = 0; again < 2; ++again) {
     Pair mine = {0.f, 0.f};
-    for (int c = c0; c < c1; ++c) {
-      const float v = chunk_sum(c);
-      if (c == c0) v0 = v;
-      mine = mine + Pair{v, 0.f};
+    for (int k = 0; k < per; ++k) {
+      const Pair v = chunk_sum(c0 + k);
+      if (k == 0) v0 = v;
+      mine = mine + v;
     }
     const Pair up = warp_scan(mine, lane);
     if (lane == 31) sh.part[warp] = up;
-    if (tid == 0) sh.chunk = -1;
+    if (tid == 0) sh.chunk = sh.next = -1;
     __syncthreads();
     before = up + Pair{-mine.hi, -mine.lo};
     all = {0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kWalkWarps; ++w) {
       const Pair v = sh.part[w];
       if (w < warp) before = v + before;
       all = all + v;
     }
+    __syncthreads();
     if (all.value() > 0.f || lost == 0) break;
     with_lost = true;
-    __syncthreads();
   }
   const Pair drawn = sh.u[0] * all;
   {
     // the last chunk with a sum above 0 whose tokens begin at or below the drawn number
     Pair at = before;
     int found = -1;
-    float rest = 0.f;
-    for (int c = c0; c < c1; ++c) {
-      const float v = c == c0 ? v0 : chunk_sum(c);
-      const float over = drawn - at;
-      if (v > 0.f && over >= 0.f) {
-        found = c;
+    Pair rest = {0.f, 0.f};
+    for (int k = 0; k < per; ++k) {
+      const Pair v = k == 0 ? v0 : chunk_sum(c0 + k);
+      const Pair over = drawn + Pair{-at.hi, -at.lo};
+      if (v.value() > 0.f && over.value() >= 0.f) {
+        found = c0 + k;
         rest = over;
       }
-      at = at + Pair{v, 0.f};
+      at = at + v;
     }
     if (found >= 0) atomicMax(&sh.chunk, found);
     __syncthreads();
     if (found >= 0 && sh.chunk == found) sh.left = rest;
-    __syncthreads();
   }
   // the last token of that chunk with a weight whose range begins at or below the drawn number, each thread's beside one another
   const int c = sh.chunk;
@@ -663,51 +741,38 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     return;
   }
   if (tid < kChunk / 32) sh.mask[0][tid] = 0;
-  if (tid == 0) sh.next = -1;
   __syncthreads();
   if (!with_lost) mask_of(sh.mask[0], c, tid, kWalk);
+  __syncthreads();
   constexpr int kOwn = kChunk / kWalk;
-  float x[kOwn], y[kOwn];
+  Pair mine[kOwn], own = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) {
-    const int e = c * kChunk + tid * kOwn + k;
-    const bool in = e >= r.lo && e < r.hi;
-    x[k] = in ? load1(r.x + e) : ninf;
-    y[k] = in && left ? load1(a.draft + (int64_t(first) + cur) * a.draft_stride + e - r.lo) : 0.f;
+    const int at = tid * kOwn + k, e = c * kChunk + at;
+    const bool in = e >= r.lo && e < r.hi && !((sh.mask[0][at / 32] >> (at % 32)) & 1);
+    const float x = in ? load1(r.x + e) : ninf, prob = in && left ? load1(q + e - r.lo) : 0.f;
+    const float w = x > ninf ? weight(a, x, m) : 0.f;
+    if (w > big)
+      mine[k] = left ? share(a, inverse, x, m, wb, prob) : weight_pair(a, x, m);
+    else
+      mine[k] = Pair{left ? fmaxf(fmaf(inv, w, -wb * prob), 0.f) : w, 0.f};
+    own = own + mine[k];
   }
-  const float ref = left ? m : __uint_as_float(chunk_of(cur, c).x), inv = 1.f / sh.z[cur];
-  float to = sh.left;
-  if (!left) to /= weight(a, ref, m);  // in the chunk's own units
+  const Pair up = warp_scan(own, lane);
+  if (lane == 31) sh.part[warp] = up;
   __syncthreads();
-  float own = 0.f;
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) {
-    const int at = tid * kOwn + k;
-    if (left) {
-      x[k] = fmaxf(fmaf(inv, weight(a, x[k], m), -wb * y[k]), 0.f);
-    } else {
-      x[k] = (sh.mask[0][at / 32] >> (at % 32)) & 1 || !(x[k] > ninf) ? 0.f : weight(a, x[k], ref);
-    }
-    own += x[k];
-  }
-  float up = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float v = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += v;
-  }
-  if (lane == 31) sh.part[warp].hi = up;
-  __syncthreads();
-  float at = __shfl_up_sync(0xffffffffu, up, 1);
-  if (lane == 0) at = 0.f;
-  float below = 0.f;
-  for (int w = 0; w < warp; ++w) below += sh.part[w].hi;
-  at += below;
+  Pair at = {__shfl_up_sync(0xffffffffu, up.hi, 1), __shfl_up_sync(0xffffffffu, up.lo, 1)};
+  if (lane == 0) at = {0.f, 0.f};
+  Pair below = {0.f, 0.f};
+#pragma unroll 1
+  for (int w = 0; w < warp; ++w) below = below + sh.part[w];
+  at = below + at;
+  const Pair to = sh.left;
   int token = -1;
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) {
-    if (x[k] > 0.f && at <= to) token = c * kChunk + tid * kOwn + k - r.lo;
-    at += x[k];
+    if (mine[k].value() > 0.f && to - at >= 0.f) token = c * kChunk + tid * kOwn + k - r.lo;
+    at = at + mine[k];
   }
   token = __reduce_max_sync(0xffffffffu, token);
   if (lane == 0 && token >= 0) atomicMax(&sh.next, token);
@@ -739,7 +804,7 @@ cudaError_t launch_walk(Kernel kernel, const VerifyArgs &a, cudaStream_t s) {
 
 size_t verify_drafts_workspace_bytes(int n_seqs, int max_rows, int n) {
   const size_t chunks = size_t(row_chunks(n));
-  return workspace_for(0, size_t(n_seqs) * chunks * (size_t(max_rows) * 8 + 4));
+  return workspace_for(0, size_t(n_seqs) * chunks * (size_t(max_rows) * 8 + 8));
 }
 
 int launch_verify_drafts(const void *logits, int64_t stride, int type, const int *tokens, const int *cu, const int *parent,
@@ -768,10 +833,11 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
   a.chunks = int(row_chunks(n));
   const double c = greedy ? 0.0 : 1.4426950408889634074 / double(temperature);
   a.c_hi = float(c);
-  a.c_lo = float(c - double(a.c_hi));
+  if (!greedy && double(a.c_hi) >= c) a.c_hi = std::nextafterf(a.c_hi, 0.f);
+  a.c_lo = float(c - double(a.c_hi));  // above 0, so that -inf times both is -inf
   const int64_t rows = int64_t(n_seqs) * max_rows;
   a.stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes));
-  a.sums = reinterpret_cast<float *>(a.stats + rows * a.chunks);
+  a.sums = a.stats + rows * a.chunks;
   const int most = (a.chunks + kWarps - 1) / kWarps;  // CTAs of a row with a chunk for each warp
   // many rows: two chunks for each warp (48 chains 28.6 us, with four 29.3, with one 30.5)
   a.groups = rows * most <= 8 * di.sm_count ? most : (most + 1) / 2;
