@@ -110,12 +110,18 @@ template <>
 struct TreeNodes<true> {
   uint64_t seen[QDQ_MAX_TREE];
   int parent[QDQ_MAX_TREE], depth[QDQ_MAX_TREE];
-  // threads 0, 1, ... of a block; a barrier between the two, and one behind them
+  // threads 0, 1, ... (64 at least) of a block; a barrier between the two, and one behind them
   __device__ __forceinline__ void load(const int *p, int n, int tid) {
     if (tid < n) parent[tid] = int(ld_u1(p + tid));
   }
   __device__ __forceinline__ void walk(int n, int window, int tid) {
-    if (tid >= n) return;
+    if (tid >= n) {  // rows past the tree's last are computed, and share votes with its rows: the same ones in every call
+      if (tid < QDQ_MAX_TREE) {
+        seen[tid] = 0;
+        depth[tid] = 0;
+      }
+      return;
+    }
     uint64_t bits = 0;
     int steps = 0;
     for (int node = tid;;) {  // up to the root (to ever smaller numbers, so it ends)
@@ -132,7 +138,7 @@ struct TreeNodes<true> {
     seen[tid] = bits;
     depth[tid] = steps;
   }
-  // (rows and keys past the nodes: any node's, they are hidden or not written)
+  // (rows and keys past 64: the last node's, they are hidden or not written)
   __device__ __forceinline__ int depth_of(int node) const { return depth[min(node, QDQ_MAX_TREE - 1)]; }
   __device__ __forceinline__ uint64_t seen_of(int node) const { return seen[min(node, QDQ_MAX_TREE - 1)]; }
   __device__ __forceinline__ bool wrong(int node) const { return depth_of(node) < 0; }
