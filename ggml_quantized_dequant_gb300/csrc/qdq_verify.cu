@@ -445,15 +445,15 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
     const float m = sh.m[cur];
     const Pair inverse = reciprocal(sh.z[cur]);
-    const float inv = inverse.hi, big = kBig * sh.z[cur].value(), nan = __int_as_float(0x7fffffff);
+    const float inv = inverse.hi, big = kBig * sh.z[cur].value();
     const int chunks = r.chunks();
     float2 *sums = a.sums + int64_t(s) * a.chunks;
     Pair z = {0.f, 0.f};
     for (int c = rank * kWalkWarps + warp; c < chunks; c += kParts) {
-      float top = __uint_as_float(chunk_of(cur, c).x);  // where it is likely: its tokens' shares as pairs, the others' in f32
-      if (!(weight(a, top, m) > big)) top = nan;
+      // likely tokens' shares as pairs, the others' in f32: token for token what the draw takes, or a chunk whose sum is above 0
+      // could have no token there
+      uint32_t likes = 0;
       float l[2] = {0.f, 0.f};
-      uint32_t tops = 0;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float x[kPer / 2], y[kPer / 2];
@@ -461,16 +461,17 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         load_draft<T>(q, r, c * kChunk + h * (kChunk / 2), lane, y);
 #pragma unroll
         for (int k = 0; k < kPer / 2; ++k) {
-          if (x[k] == top)
-            tops |= 1u << (h * (kPer / 2) + k);
+          const float w = weight(a, x[k], m);
+          if (w > big)
+            likes |= 1u << (h * (kPer / 2) + k);
           else
-            l[k & 1] += fmaxf(fmaf(inv, weight(a, x[k], m), -b * y[k]), 0.f);
+            l[k & 1] += fmaxf(fmaf(inv, w, -b * y[k]), 0.f);
         }
       }
       Pair sum = {l[0] + l[1], 0.f};
-      for (; tops; tops &= tops - 1) {
-        const int j = __ffs(tops) - 1, e = c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane);
-        sum = sum + share(a, inverse, top, m, b, load1(q + e - r.lo));
+      for (; likes; likes &= likes - 1) {
+        const int j = __ffs(likes) - 1, e = c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane);
+        sum = sum + share(a, inverse, load1(r.x + e), m, b, load1(q + e - r.lo));
       }
       __syncwarp();
       sum = warp_sum_pair(sum);
