@@ -215,6 +215,11 @@ __device__ __forceinline__ Pair weight_pair(const VerifyArgs &a, float x, float 
   const Pair v = Pair{1.f, 0.f} + e + 0.5f * (e * e) + Pair{r * g * g * g, 0.f};
   return __int_as_float((127 + int(i)) << 23) * v;
 }
+// As weight_pair, which is 0 below 2^-100; to 2^-16 there.
+__device__ __forceinline__ Pair weight_any(const VerifyArgs &a, float x, float m) {
+  const Pair v = weight_pair(a, x, m);
+  return v.hi > 0.f ? v : Pair{weight(a, x, m), 0.f};
+}
 __device__ __forceinline__ Pair reciprocal(const Pair &z) {
   const float i = 1.f / z.value();
   return {i, i * (fmaf(-i, z.hi, 1.f) - i * z.lo)};
@@ -303,7 +308,8 @@ struct WalkShared {
   int best[QDQ_MAX_TREE];             // temperature 0: its best token
   int bad[QDQ_MAX_TREE];              // a NaN or +inf, or nothing above -inf
   int parent[QDQ_MAX_TREE], token[QDQ_MAX_TREE], path[QDQ_MAX_TREE];
-  float p[QDQ_MAX_TREE], q[QDQ_MAX_TREE], u[QDQ_MAX_TREE];  // of a child: its probabilities at its parent, its number
+  Pair e[QDQ_MAX_TREE];               // of a child: its weight at its parent, relative to the largest logit there
+  float q[QDQ_MAX_TREE], u[QDQ_MAX_TREE];  // ... its draft probability, its number
   int lost[QDQ_MAX_TREE];             // rejected drafts without probabilities, at the present node
   Pair rest[QDQ_MAX_TREE];            // their chunks' sums without them
   uint32_t mask[kWalkWarps][kChunk / 32];  // a chunk's lost tokens
@@ -330,8 +336,13 @@ __device__ __forceinline__ void exchange(WalkShared &sh, int turn, uint4 mine, i
   }
 }
 
-template <typename T, bool GREEDY, int CTAS, bool LAZY>
+// What decides over a draft: whether it is the row's best token, its probability alone, or that and its draft probability.  A kernel
+// for each: one for the last two spilled registers (one chain 13.3 us, 16 trees 29, apart 11.9 and 25.5).
+enum Kind { kBest, kCertain, kDrawn };
+
+template <typename T, Kind KIND, int CTAS, bool LAZY>
 __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(const VerifyArgs a) {
+  constexpr bool GREEDY = KIND == kBest, DRAFT = KIND == kDrawn;
   __shared__ WalkShared sh;
   constexpr int kParts = CTAS * kWalkWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -371,7 +382,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
       if (up >= 0 && up < tid && x >= 0 && x < a.n) {
         const int64_t row = int64_t(first) + up;
         cx = load1(static_cast<const T *>(a.logits) + row * a.stride + x);
-        if (a.draft) cq = load1(a.draft + row * a.draft_stride + x);
+        if constexpr (DRAFT) cq = load1(a.draft + row * a.draft_stride + x);
       }
     }
   }
@@ -429,7 +440,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   if constexpr (!LAZY && !GREEDY) {
     if (tid < n && sh.parent[tid] >= 0) {
       const int up = sh.parent[tid];
-      sh.p[tid] = sh.bad[up] ? 0.f : weight(a, cx, sh.m[up]) / sh.z[up].value();
+      sh.e[tid] = weight_any(a, cx, sh.m[up]);
       sh.q[tid] = cq;
     }
     __syncthreads();
@@ -437,7 +448,8 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
 
   int cur = 0, count = 0, lost = 0;
   float wb = 0.f, ws = 1.f;   // w = max(p - wb q, 0) / ws
-  float kept = 1.f;           // what rejected drafts without probabilities have left
+  Pair kept = {0.f, 0.f};     // what rejected drafts without probabilities have left, relative to the largest logit
+  float known = 0.f;          // ... when it was summed last
   float summed = 0.f;         // a.sums holds the chunks' sums of max(p - summed q, 0), where this is not 0
   // the chunks' sums of max(p - b q, 0) at the present node, and their sum
   auto pass = [&](float b) {
@@ -487,6 +499,57 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     }
     turn ^= 1;
     return warp_sum_pair(z).value();
+  };
+  // the lost tokens of a chunk as bits
+  auto mask_of = [&](const Row<T> &r, uint32_t *mask, int c, int from, int step) {
+    for (int o = from; o < lost; o += step) {
+      const int at = sh.lost[o] + r.lo - c * kChunk;
+      if (at >= 0 && at < kChunk) atomicOr(mask + at / 32, 1u << (at % 32));
+    }
+  };
+  // the sums of the chunks that hold lost tokens, without these
+  auto rests = [&](const Row<T> &r) {
+    const float m = sh.m[cur], big = kBig * sh.z[cur].value();
+    for (int k = warp; k < lost; k += kWalkWarps) {
+      const int c = (sh.lost[k] + r.lo) / kChunk;
+      uint32_t *mask = sh.mask[warp];
+      __syncwarp();
+      mask[lane] = 0;
+      __syncwarp();
+      mask_of(r, mask, c, lane, 32);
+      __syncwarp();
+      uint32_t likes = 0;  // this lane's likely tokens
+      float l[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float x[kPer / 2];
+        load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+          const int at = h * (kChunk / 2) + element<T>(j, lane);
+          const float w = x[j] > ninf && !((mask[at / 32] >> (at % 32)) & 1) ? weight(a, x[j], m) : 0.f;
+          if (w > big)
+            likes |= 1u << (h * (kPer / 2) + j);
+          else
+            l[j & 1] += w;
+        }
+      }
+      Pair sum = {l[0] + l[1], 0.f};
+      for (; likes; likes &= likes - 1) {
+        const int j = __ffs(likes) - 1;
+        sum = sum + weight_pair(a, load1(r.x + c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane)), m);
+      }
+      __syncwarp();
+      sum = warp_sum_pair(sum);
+      if (lane == 0) sh.rest[k] = sum;
+    }
+    __syncthreads();
+  };
+  // a chunk's sum without lost tokens, whose chunks have been summed by rests()
+  auto chunk_left = [&](const Row<T> &r, int c) {
+    for (int k = 0; k < lost; ++k)
+      if ((sh.lost[k] + r.lo) / kChunk == c) return sh.rest[k];
+    return chunk_part(chunk_of(cur, c), sh.m[cur]);
   };
 
   for (;;) {  // at the present node (every thread of every CTA alike)
@@ -553,17 +616,21 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     if constexpr (!GREEDY) {
       if (LAZY && children) {
         if (tid < n && sh.parent[tid] == cur) {
-          sh.p[tid] = weight(a, cx, sh.m[cur]) / sh.z[cur].value();
+          sh.e[tid] = weight_any(a, cx, sh.m[cur]);
           sh.q[tid] = cq;
         }
         __syncthreads();
       }
-      if (a.ahead && a.draft && children) {
+      if (DRAFT && a.ahead && children) {
         const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
         for (int c = rank * kWalkWarps + warp; c * kChunk < a.n; c += kParts) prefetch(q + c * kChunk, min(kChunk, a.n - c * kChunk) * 4, lane);
       }
     }
     int went = -1;
+    if constexpr (!GREEDY) {
+      kept = sh.z[cur];
+      known = kept.value();
+    }
     while (children) {
       const int i = __ffsll((long long)children) - 1;
       children &= children - 1;
@@ -572,8 +639,8 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         if (x == sh.best[cur]) went = i;
       } else if (x < 0 || x >= a.n) {
         continue;
-      } else if (a.draft) {
-        if (sh.u[i] * sh.q[i] * ws < fmaf(-wb, sh.q[i], sh.p[i])) {
+      } else if constexpr (DRAFT) {
+        if (sh.u[i] * sh.q[i] * ws < fmaf(-wb, sh.q[i], sh.e[i].value() / sh.z[cur].value())) {
           went = i;
         } else {
           const float z = pass(wb + ws);
@@ -587,14 +654,30 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         bool again = false;  // lost already
         for (int k = 0; k < lost; ++k) again |= sh.lost[k] == x;
         if (!again) {
-          if (sh.u[i] * kept < sh.p[i]) {
+          const Pair e = sh.e[i];
+          if (sh.u[i] * kept - e < 0.f) {
             went = i;
           } else {
-            kept = fmaxf(kept - sh.p[i], 0.f);
+            kept = kept + Pair{-e.hi, -e.lo};
             __syncthreads();
             if (tid == 0 && QDQ_GUARD(lost < QDQ_MAX_TREE, QDQ_CHECK_SMEM)) sh.lost[lost] = x;
             ++lost;
             __syncthreads();
+            // Less than half of what was summed: that sum's error is now twice as large a share, so the tokens that are left are
+            // summed by themselves (by every CTA for itself; a likely token that is refused is rare).
+            if (!(kept.value() >= 0.5f * known)) {
+              const Row<T> r(a, int64_t(first) + cur);
+              rests(r);
+              Pair z = {0.f, 0.f};
+              for (int c = tid; c < r.chunks(); c += kWalk) z = z + chunk_left(r, c);
+              z = warp_sum_pair(z);
+              if (lane == 0) sh.part[warp] = z;
+              __syncthreads();
+              kept = {0.f, 0.f};
+#pragma unroll 1
+              for (int w = 0; w < kWalkWarps; ++w) kept = kept + sh.part[w];
+              known = kept.value();
+            }
           }
         }
       }
@@ -605,12 +688,12 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     if (tid == 0 && QDQ_GUARD(count < QDQ_MAX_TREE, QDQ_CHECK_SMEM)) sh.path[count] = went;
     ++count;
     wb = summed = 0.f;
-    ws = kept = 1.f;
+    ws = 1.f;
     lost = 0;
   }
   // w as the last pass summed it, where a later one found nothing left
-  if constexpr (!GREEDY) {
-    if (a.draft && wb > 0.f && summed == 0.f) pass(wb);
+  if constexpr (DRAFT) {
+    if (wb > 0.f && summed == 0.f) pass(wb);
   }
   if (rank != 0) return;
   __syncthreads();
@@ -631,64 +714,20 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   const Row<T> r(a, int64_t(first) + cur);
   const int chunks = r.chunks();
   const float2 *sums = a.sums + int64_t(s) * a.chunks;
-  const float *q = a.draft ? a.draft + (int64_t(first) + cur) * a.draft_stride : nullptr;
-  const bool left = a.draft && wb > 0.f;  // w by the pass's sums, else the target's without the lost tokens
+  const float *q = DRAFT ? a.draft + (int64_t(first) + cur) * a.draft_stride : nullptr;
+  const bool left = DRAFT && wb > 0.f;  // w by the pass's sums, else the target's without the lost tokens
   const float m = sh.m[cur], big = kBig * sh.z[cur].value();
   const Pair inverse = reciprocal(sh.z[cur]);
   const float inv = inverse.hi;
   bool with_lost = false;  // nothing else is left: the lost tokens count again
-  // the lost tokens of a chunk as bits
-  auto mask_of = [&](uint32_t *mask, int c, int from, int step) {
-    for (int o = from; o < lost; o += step) {
-      const int at = sh.lost[o] + r.lo - c * kChunk;
-      if (at >= 0 && at < kChunk) atomicOr(mask + at / 32, 1u << (at % 32));
-    }
-  };
-  // sums of the chunks that hold lost tokens
-  for (int k = warp; k < lost; k += kWalkWarps) {
-    const int c = (sh.lost[k] + r.lo) / kChunk;
-    uint32_t *mask = sh.mask[warp];
-    __syncwarp();
-    mask[lane] = 0;
-    __syncwarp();
-    mask_of(mask, c, lane, 32);
-    __syncwarp();
-    uint32_t likes = 0;  // this lane's likely tokens
-    float l = 0.f;
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float x[kPer / 2];
-      load_run<T>(r, c * kChunk + h * (kChunk / 2), lane, x);
-#pragma unroll
-      for (int j = 0; j < kPer / 2; ++j) {
-        const int at = h * (kChunk / 2) + element<T>(j, lane);
-        const float w = x[j] > ninf && !((mask[at / 32] >> (at % 32)) & 1) ? weight(a, x[j], m) : 0.f;
-        if (w > big)
-          likes |= 1u << (h * (kPer / 2) + j);
-        else
-          l += w;
-      }
-    }
-    Pair sum = {l, 0.f};
-    for (; likes; likes &= likes - 1) {
-      const int j = __ffs(likes) - 1;
-      sum = sum + weight_pair(a, load1(r.x + c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane)), m);
-    }
-    __syncwarp();
-    sum = warp_sum_pair(sum);
-    if (lane == 0) sh.rest[k] = sum;
-  }
-  if (lost) __syncthreads();
+  if (lost) rests(r);
   auto chunk_sum = [&](int c) {
     if (c >= chunks) return Pair{0.f, 0.f};
     if (left) {
       const float2 v = __ldcg(sums + c);
       return Pair{v.x, v.y};
     }
-    if (!with_lost)
-      for (int k = 0; k < lost; ++k)
-        if ((sh.lost[k] + r.lo) / kChunk == c) return sh.rest[k];
-    return chunk_part(chunk_of(cur, c), m);
+    return with_lost ? chunk_part(chunk_of(cur, c), m) : chunk_left(r, c);
   };
   // each thread's chunks one after the other; where the sums pass the drawn number
   const int per = (chunks + kWalk - 1) / kWalk, c0 = tid * per;
@@ -743,7 +782,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   }
   if (tid < kChunk / 32) sh.mask[0][tid] = 0;
   __syncthreads();
-  if (!with_lost) mask_of(sh.mask[0], c, tid, kWalk);
+  if (!with_lost) mask_of(r, sh.mask[0], c, tid, kWalk);
   __syncthreads();
   constexpr int kOwn = kChunk / kWalk;
   Pair mine[kOwn], own = {0.f, 0.f};
@@ -848,20 +887,24 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
   const bool wide = a.chunks > 2 * kWarps, few = int64_t(n_seqs) * kCluster <= 2 * di.sm_count;
   e = cudaError_t(with_type(type, [&](auto t) {
     using T = decltype(t);
-    if (wide && max_rows > 1 && rows * n * int64_t(sizeof(T)) > kLazyBytes)
-      return int(greedy  ? few ? launch_walk<kCluster>(verify_walk_kernel<T, true, kCluster, true>, a, s)
-                               : launch_walk<kCluster / 2>(verify_walk_kernel<T, true, kCluster / 2, true>, a, s)
-                 : few ? launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, true>, a, s)
-                       : launch_walk<kCluster / 2>(verify_walk_kernel<T, false, kCluster / 2, true>, a, s));
+    auto lazy = [&](auto kind) {
+      constexpr Kind K = decltype(kind)::value;
+      return int(few ? launch_walk<kCluster>(verify_walk_kernel<T, K, kCluster, true>, a, s)
+                     : launch_walk<kCluster / 2>(verify_walk_kernel<T, K, kCluster / 2, true>, a, s));
+    };
+    constexpr std::integral_constant<Kind, kBest> best{};
+    constexpr std::integral_constant<Kind, kCertain> certain{};
+    constexpr std::integral_constant<Kind, kDrawn> drawn{};
+    if (wide && max_rows > 1 && rows * n * int64_t(sizeof(T)) > kLazyBytes) return greedy ? lazy(best) : a.draft ? lazy(drawn) : lazy(certain);
     const dim3 grid(unsigned(rows * a.groups));
     const cudaError_t r = greedy ? launch(verify_stats_kernel<T, true>, grid, dim3(kThreads), 0, s, a)
                                  : launch(verify_stats_kernel<T, false>, grid, dim3(kThreads), 0, s, a);
     if (r != cudaSuccess) return int(r);
-    if (greedy) return int(launch_walk<1>(verify_walk_kernel<T, true, 1, false>, a, s));
-    if (a.draft && wide)
-      return int(few ? launch_walk<kCluster>(verify_walk_kernel<T, false, kCluster, false>, a, s)
-                     : launch_walk<kCluster / 2>(verify_walk_kernel<T, false, kCluster / 2, false>, a, s));
-    return int(launch_walk<1>(verify_walk_kernel<T, false, 1, false>, a, s));
+    if (greedy) return int(launch_walk<1>(verify_walk_kernel<T, kBest, 1, false>, a, s));
+    if (!a.draft) return int(launch_walk<1>(verify_walk_kernel<T, kCertain, 1, false>, a, s));
+    if (!wide) return int(launch_walk<1>(verify_walk_kernel<T, kDrawn, 1, false>, a, s));
+    return int(few ? launch_walk<kCluster>(verify_walk_kernel<T, kDrawn, kCluster, false>, a, s)
+                   : launch_walk<kCluster / 2>(verify_walk_kernel<T, kDrawn, kCluster / 2, false>, a, s));
   }));
   return e == cudaSuccess ? QDQ_OK : fail_cuda(e);
 }

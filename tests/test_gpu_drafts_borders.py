@@ -1,8 +1,17 @@
-"""Drafted tokens next to borders: results that no other call and no rounding may change."""
+"""Drafted tokens next to borders: results that no other call and no rounding may change.
+
+Bounds (u = 2^-24), beside those of test_gpu_drafts.py.  A row's sum of weights Z holds each chunk's likeliest token and the joins
+of chunks as pairs of f32; the other tokens' weights are f32: an exponent h (in bits) is off by |h| 2^-23, which is |h| ln 2 2^-23
+of the weight, exp2 by 2^-22, and a chunk's sum by 22 u: 2^-18 of what those tokens have, where |h| is at most 20.
+* what rejected drafts without probabilities leave is summed from the tokens that are left wherever less than half of the last
+  such sum remains, likely tokens as pairs, the others as above with |h| up to 42 (a draft that leaves less than 2^-24 is never
+  rejected): 2 (22 u + 2^-22 + 42 ln 2 2^-23) < 2^-16 of itself; 2^-15 below.
+"""
 import numpy as np
 import pytest
 
-from test_gpu_decode_ops import _dt, _filled, _t, attn_kernel  # noqa: F401
+from oracle import draft_oracle as dref
+from test_gpu_decode_ops import _dt, _filled, _np, _t, attn_kernel  # noqa: F401
 from test_gpu_drafts import _cu, _parents, _tree, _verify
 
 pytestmark = pytest.mark.gpu
@@ -60,6 +69,44 @@ def _stars(x, tokens, u, probs=None, max_rows=None):
         q = q.reshape(-1, n)
     return dict(x=_t(rows.reshape(-1, n)), tokens=tokens.reshape(-1), parents=[np.array([-1] + [0] * (m - 1))] * seqs,
                 u=u.astype(np.float32).reshape(-1), probs=q, cu=_cu([m] * seqs), nodes=[m] * seqs, n=n, temperature=1.0, kind="star")
+
+
+def _accepted(w):
+    """What the oracle accepts, by sequence."""
+    x, m = _np(w["x"]), w["nodes"][0]
+    return [dref.verify(x[s * m:s * m + m], w["tokens"][s * m:s * m + m], list(w["parents"][s]), w["u"][s * m:s * m + m].astype(np.float64),
+                        None if w["probs"] is None else w["probs"][s * m:s * m + m], 1.0)[0][1:] for s in range(len(w["nodes"]))]
+
+
+@pytest.mark.parametrize("n,at,max_rows", [(3000, [5, 9, 1500, 2999, 7], None), (3000, [0, 1030, 2050, 1, 2], None),
+                                           (30001, [5, 9, 15000, 30000, 7], None), (30001, [5, 9, 15000, 30000, 7], 64)])
+def test_what_rejected_likely_drafts_leave(cuda_lib, n, at, max_rows):
+    # Drafts without probabilities: the likeliest tokens in order, all but the last refused, which is 2^-15 from its border.  The
+    # first has up to 1 - 10^-6 of the probability.  (64 rows: the bound from which on rows are read when they are reached.)
+    rng = np.random.default_rng(n + at[1])
+    x, tokens, u, want = [], [], [], []
+    for gap in (2.0, 5.0, 8.0, 11.0, 14.0):
+        for last in range(5):
+            for side in (-1, 1):
+                for _ in range(1 if n > 3000 else 4):
+                    row = (-gap - np.log(n) - 1 + 0.5 * rng.standard_normal(n)).astype(np.float32)
+                    row[at] = (np.array([0.0] + [-gap] * 4) + 0.3 * rng.standard_normal(5)).astype(np.float32)
+                    e = np.exp(row.astype(np.float64))
+                    numbers = np.full(6, 0.5)
+                    for i in range(last + 1):
+                        w = e[at[i]] / e.sum()
+                        numbers[1 + i] = w + 0.5 * (1 - w) if i < last else min(w * (1 + side * 2.0 ** -15), 1 - 2.0 ** -24)
+                        e[at[i]] = 0
+                    x.append(row)
+                    tokens.append([0] + at[:last + 1] + [-1] * (4 - last))
+                    u.append(numbers)
+                    want.append([] if side > 0 and numbers[1 + last] > w else [last + 1])
+    w = _stars(np.array(x), np.array(tokens), np.array(u))
+    assert _accepted(w) == want
+    assert max_rows is None or len(x) * max_rows * n * 4 > 128 << 20
+    acc, path, nxt = _verify(cuda_lib, w, max_rows=max_rows)
+    assert [p[1:a + 1].tolist() for p, a in zip(path, acc)] == want
+    assert (nxt >= 0).all()
 
 
 def test_a_row_that_is_finite_gives_a_token(cuda_lib):
