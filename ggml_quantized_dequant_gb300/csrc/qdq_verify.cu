@@ -22,7 +22,8 @@
 // comparisons; a rejection's pass is shared by the cluster, too.  The drawn token's chunk is found from the
 // chunks' sums, and the token in it by a warp.
 // Sums within a chunk are f32, without its likeliest token, which is taken as a pair of f32 like the sums over chunks (48 bits; f64
-// adds have a 64th of f32's rate here and were most of the walk's time); p, b and S are f32 in the comparisons.
+// adds have a 64th of f32's rate here and were most of the walk's time).  A child's p, b, S and what lost tokens leave are pairs,
+// too: they are compared with near numbers where a draft has nearly all of the probability, or nearly the target's.
 // A kernel's code runs once here, so that its length is time too (fetched from the L2): the draw is two tokens to a thread, not
 // 32 to a lane of one warp, which took 4 us more.
 // Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 12.9 us; 48 chains of 2
@@ -224,10 +225,10 @@ __device__ __forceinline__ Pair reciprocal(const Pair &z) {
   const float i = 1.f / z.value();
   return {i, i * (fmaf(-i, z.hi, 1.f) - i * z.lo)};
 }
-// What max(p - b q, 0) is of a logit x, as a pair.
-__device__ __forceinline__ Pair share(const VerifyArgs &a, const Pair &inverse, float x, float m, float b, float q) {
-  const float t = b * q;
-  const Pair w = inverse * weight_pair(a, x, m) + Pair{-t, -fmaf(b, q, -t)};
+// max(p - b q, 0) of a weight e (1 / inverse: the row's sum), as a pair.
+__device__ __forceinline__ Pair share(const Pair &inverse, const Pair &e, const Pair &b, float q) {
+  const float t = b.hi * q;
+  const Pair w = inverse * e + Pair{-t, -fmaf(b.lo, q, fmaf(b.hi, q, -t))};
   return w.value() > 0.f ? w : Pair{0.f, 0.f};
 }
 // A chunk of 1024 elements of size B at p, less what the row does not have, into the L2.
@@ -447,12 +448,12 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   }
 
   int cur = 0, count = 0, lost = 0;
-  float wb = 0.f, ws = 1.f;   // w = max(p - wb q, 0) / ws
+  Pair wb = {0.f, 0.f}, ws = {1.f, 0.f};  // w = max(p - wb q, 0) / ws
   Pair kept = {0.f, 0.f};     // what rejected drafts without probabilities have left, relative to the largest logit
   float known = 0.f;          // ... when it was summed last
-  float summed = 0.f;         // a.sums holds the chunks' sums of max(p - summed q, 0), where this is not 0
+  bool summed = false;        // a.sums holds the chunks' sums of max(p - wb q, 0)
   // the chunks' sums of max(p - b q, 0) at the present node, and their sum
-  auto pass = [&](float b) {
+  auto pass = [&](const Pair &b) {
     const Row<T> r(a, int64_t(first) + cur);
     const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
     const float m = sh.m[cur];
@@ -477,13 +478,13 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
           if (w > big)
             likes |= 1u << (h * (kPer / 2) + k);
           else
-            l[k & 1] += fmaxf(fmaf(inv, w, -b * y[k]), 0.f);
+            l[k & 1] += fmaxf(fmaf(inv, w, -b.hi * y[k]), 0.f);
         }
       }
       Pair sum = {l[0] + l[1], 0.f};
       for (; likes; likes &= likes - 1) {
         const int j = __ffs(likes) - 1, e = c * kChunk + j / (kPer / 2) * (kChunk / 2) + element<T>(j % (kPer / 2), lane);
-        sum = sum + share(a, inverse, load1(r.x + e), m, b, load1(q + e - r.lo));
+        sum = sum + share(inverse, weight_pair(a, load1(r.x + e), m), b, load1(q + e - r.lo));
       }
       __syncwarp();
       sum = warp_sum_pair(sum);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
       z = z + Pair{__uint_as_float(v.x), __uint_as_float(v.y)};
     }
     turn ^= 1;
-    return warp_sum_pair(z).value();
+    return warp_sum_pair(z);
   };
   // the lost tokens of a chunk as bits
   auto mask_of = [&](const Row<T> &r, uint32_t *mask, int c, int from, int step) {
@@ -640,13 +641,14 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
       } else if (x < 0 || x >= a.n) {
         continue;
       } else if constexpr (DRAFT) {
-        if (sh.u[i] * sh.q[i] * ws < fmaf(-wb, sh.q[i], sh.e[i].value() / sh.z[cur].value())) {
+        // (near numbers where the draft's probabilities are nearly the target's)
+        if (sh.u[i] * sh.q[i] * ws - share(reciprocal(sh.z[cur]), sh.e[i], wb, sh.q[i]) < 0.f) {
           went = i;
         } else {
-          const float z = pass(wb + ws);
-          summed = z > 0.f ? wb + ws : 0.f;
-          if (z > 0.f) {
-            wb += ws;
+          const Pair b = wb + ws, z = pass(b);
+          summed = z.value() > 0.f;
+          if (summed) {
+            wb = b;
             ws = z;
           }
         }
@@ -687,13 +689,14 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     cur = went;
     if (tid == 0 && QDQ_GUARD(count < QDQ_MAX_TREE, QDQ_CHECK_SMEM)) sh.path[count] = went;
     ++count;
-    wb = summed = 0.f;
-    ws = 1.f;
+    wb = {0.f, 0.f};
+    ws = {1.f, 0.f};
+    summed = false;
     lost = 0;
   }
   // w as the last pass summed it, where a later one found nothing left
   if constexpr (DRAFT) {
-    if (wb > 0.f && summed == 0.f) pass(wb);
+    if (wb.hi > 0.f && !summed) pass(wb);
   }
   if (rank != 0) return;
   __syncthreads();
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
   const int chunks = r.chunks();
   const float2 *sums = a.sums + int64_t(s) * a.chunks;
   const float *q = DRAFT ? a.draft + (int64_t(first) + cur) * a.draft_stride : nullptr;
-  const bool left = DRAFT && wb > 0.f;  // w by the pass's sums, else the target's without the lost tokens
+  const bool left = DRAFT && wb.hi > 0.f;  // w by the pass's sums, else the target's without the lost tokens
   const float m = sh.m[cur], big = kBig * sh.z[cur].value();
   const Pair inverse = reciprocal(sh.z[cur]);
   const float inv = inverse.hi;
@@ -793,9 +796,9 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
     const float x = in ? load1(r.x + e) : ninf, prob = in && left ? load1(q + e - r.lo) : 0.f;
     const float w = x > ninf ? weight(a, x, m) : 0.f;
     if (w > big)
-      mine[k] = left ? share(a, inverse, x, m, wb, prob) : weight_pair(a, x, m);
+      mine[k] = left ? share(inverse, weight_pair(a, x, m), wb, prob) : weight_pair(a, x, m);
     else
-      mine[k] = Pair{left ? fmaxf(fmaf(inv, w, -wb * prob), 0.f) : w, 0.f};
+      mine[k] = Pair{left ? fmaxf(fmaf(inv, w, -wb.hi * prob), 0.f) : w, 0.f};
     own = own + mine[k];
   }
   const Pair up = warp_scan(own, lane);

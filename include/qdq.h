@@ -455,7 +455,10 @@ int qdq_token_logprobs(const void *logits, long long row_stride, int type, const
  *   A drafted token outside [0, n) is not accepted.  Numbers outside [0, 1) count as the nearest inside.  At a node
  *   whose row has a NaN or +inf, or nothing above -inf, no child is accepted and next_token is -1.  A sequence without
  *   rows gets accepted -1, next_token -1 and a path of -1.  max_rows: at most QDQ_MAX_TREE; rows past it do not count.
- *   p and w are computed in f32 relative to 2^-20: a number that lies that near a border may fall to either side.
+ *   A number may fall to either side of a border that lies as near as what decides is off: p by 2^-17 of itself (below 2^-126
+ *   of the row's largest it counts as 0); after rejections, without draft_probs, w by 2^-16 of itself; with draft_probs
+ *   w = max(p - b q, 0) / S, where b is the sum of the S before (first 0 and 1), max(p - b q, 0) by 2^-16 of p + b q for each
+ *   rejection at the node, and S by what that is for all its tokens; the drawn token's sum by the same share of it.
  *   workspace: qdq_verify_drafts_workspace_bytes(...) bytes, 256-byte aligned; it may be shared as those above.
  *
  * qdq_kv_keep moves the cached tokens of the accepted paths: of sequence s's last n = cu[s + 1] - cu[s] tokens, node

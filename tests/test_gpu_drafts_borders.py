@@ -6,6 +6,8 @@ of the weight, exp2 by 2^-22, and a chunk's sum by 22 u: 2^-18 of what those tok
 * what rejected drafts without probabilities leave is summed from the tokens that are left wherever less than half of the last
   such sum remains, likely tokens as pairs, the others as above with |h| up to 42 (a draft that leaves less than 2^-24 is never
   rejected): 2 (22 u + 2^-22 + 42 ln 2 2^-23) < 2^-16 of itself; 2^-15 below.
+* a child's p is a pair: its weight to 2^-30, Z as above.  Where all tokens but the likeliest of their chunks share less
+  than 2^-9.9, p is within 2^-27.9 of itself, and so is p - b q of p + b q.
 """
 import numpy as np
 import pytest
@@ -107,6 +109,64 @@ def test_what_rejected_likely_drafts_leave(cuda_lib, n, at, max_rows):
     acc, path, nxt = _verify(cuda_lib, w, max_rows=max_rows)
     assert [p[1:a + 1].tolist() for p, a in zip(path, acc)] == want
     assert (nxt >= 0).all()
+
+
+@pytest.mark.parametrize("n,max_rows", [(5000, None), (30001, None), (30001, 64)])
+def test_drafts_that_the_target_nearly_has(cuda_lib, n, max_rows):
+    # Probabilities that are the target's but for 2 * 10^-4 to 2 * 10^-3 of themselves.  The first draft is refused; the second
+    # is 2^-13 from its border, or refused and the third is.  p - b q is 6 * 10^-5 there and S 2.7 * 10^-4: both are off by 2^-14
+    # of themselves together.
+    rng = np.random.default_rng(n)
+    at = [10, 1500, 2600, 3700]
+    x, probs, tokens, u, want = [], [], [], [], []
+    for k in range(40):
+        row = (np.log(1e-3 / n) - 0.3 + 0.5 * rng.standard_normal(n)).astype(np.float32)
+        row[at] = np.log([0.3, 0.3, 0.25, 0.15]) + 0.02 * rng.standard_normal(4)
+        p = np.exp(row.astype(np.float64))
+        p /= p.sum()
+        assert p.sum() - p[at].sum() < 2.0 ** -9.9
+        q = 1.01 * p
+        q[at] = p[at] * [1.5, 1 - 2e-4, 1 - 8e-4, 1 - 2e-3]
+        q = q.astype(np.float32)
+        side, last, w, numbers = (-1, 1)[k % 2], 1 + k // 2 % 2, p, np.full(4, 0.5)
+        for i in range(last + 1):
+            border = w[at[i]] / float(q[at[i]])
+            numbers[1 + i] = border + 0.5 * (1 - border) if i < last else border * (1 + side * 2.0 ** -13)
+            w = np.maximum(w - q, 0)
+            w /= w.sum()
+        x.append(row)
+        probs.append(q)
+        tokens.append([0] + at[:last + 1] + [-1] * (2 - last))
+        u.append(numbers)
+        want.append([] if side > 0 else [last + 1])
+    w = _stars(np.array(x), np.array(tokens), np.array(u), np.array(probs))
+    assert (np.array(u) < 1).all() and _accepted(w) == want
+    assert max_rows is None or len(x) * max_rows * n * 4 > 128 << 20
+    acc, path, nxt = _verify(cuda_lib, w, max_rows=max_rows)
+    assert [p[1:a + 1].tolist() for p, a in zip(path, acc)] == want
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+def test_a_draft_far_below_the_likeliest(cuda_lib, drafts):
+    # p of 10^-20 to 10^-29: its number is 2^-21 from the border
+    rng = np.random.default_rng(8)
+    n, seqs = 3000, 60
+    x = np.full((seqs, n), -90.0, np.float32)
+    x[:, 1234] = rng.standard_normal(seqs)
+    x[:, 77] = x[:, 1234] - rng.uniform(45, 66, seqs)
+    p = np.exp(x.astype(np.float64) - x.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    side = np.where(np.arange(seqs) % 2 == 0, -1, 1)
+    probs = None
+    if drafts:
+        probs = np.full((seqs, n), 1 / n, np.float32)
+        probs[:, 77] = 2.0 ** -10
+    u = np.stack([np.full(seqs, 0.5), p[:, 77] / (2.0 ** -10 if drafts else 1) * (1 + side * 2.0 ** -21)], 1)
+    w = _stars(x, np.tile([0, 77], (seqs, 1)), u, probs)
+    want = [[1] if s < 0 else [] for s in side]
+    assert _accepted(w) == want
+    acc, path, nxt = _verify(cuda_lib, w)
+    assert [q[1:a + 1].tolist() for q, a in zip(path, acc)] == want
 
 
 def test_a_row_that_is_finite_gives_a_token(cuda_lib):
