@@ -266,12 +266,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv_keep_kernel(const KeepArgs a) 
   const int64_t plane = int64_t(which) * a.c.page_tokens * D;
   const float qnan = __int_as_float(0x7fffffff);
   for (int s = blockIdx.y; s < a.n_seqs; s += gridDim.y) {
-    const int n = int(ld_u1(a.cu + s + 1)) - int(ld_u1(a.cu + s)), old = int(ld_u1(a.kv_len + s)) - n;
+    const int n = int(ld_u1(a.cu + s + 1)) - int(ld_u1(a.cu + s)), len = int(ld_u1(a.kv_len + s));
     const int most = int(ld_u1(a.accepted + s));
-    if (n <= 0 || old < 0 || most < 0) continue;
+    if (n <= 0 || len < n || most < 0) continue;
+    const int old = len - n;
     const int m = min(min(most, a.path_stride - 1), n - 1) + 1;
     int last = -1;  // the node before this block's first
-    for (int p0 = old / kKvBlock * kKvBlock; p0 < old + m; p0 += kKvBlock) {
+    for (int blk = old / kKvBlock; blk <= (old + m - 1) / kKvBlock; ++blk) {  // (a count of places would pass 32 bits near 2^31)
+      const int p0 = blk * kKvBlock;
       // lane t (and t + 16): the block's token t
       const int t = lane & 15, i = p0 + t - old;
       const int node = i >= 0 && i < m ? int(ld_u1(a.path + int64_t(s) * a.path_stride + i)) : -1;
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_keep_kernel(const KeepArgs a) 
       const bool mine = i < m && t < cut;
       const int src = !mine ? p0 : i < 0 ? p0 + t : old + node;
       if (__any_sync(0xffffffffu, mine && src != p0 + t)) {
-        const int64_t to = kv_record_of(a.c, s, p0 / kKvBlock, h, rec);
+        const int64_t to = kv_record_of(a.c, s, blk, h, rec);
         const int64_t from = mine ? kv_record_of(a.c, s, src / kKvBlock, h, rec) : -1;
         const int sb = src % a.c.page_tokens;
         float sc = 0.f;

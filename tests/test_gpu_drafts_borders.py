@@ -13,7 +13,7 @@ import numpy as np
 import pytest
 
 from oracle import draft_oracle as dref
-from test_gpu_decode_ops import _dt, _filled, _np, _t, attn_kernel  # noqa: F401
+from test_gpu_decode_ops import _dt, _filled, _i32, _np, _t, attn_kernel  # noqa: F401
 from test_gpu_drafts import _cu, _parents, _tree, _verify
 
 pytestmark = pytest.mark.gpu
@@ -189,3 +189,19 @@ def test_a_row_that_is_finite_gives_a_token(cuda_lib):
     acc, path, nxt = _verify(cuda_lib, w)
     assert (acc == 0).all()
     assert np.isin(nxt, [3, 40]).all()
+
+
+@pytest.mark.parametrize("far", [2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 17, 2 ** 30, -2 ** 31])
+def test_keep_of_a_length_far_past_the_pages(cuda_lib, far):
+    # such a sequence's tokens have no pages: nothing of it is written, and the others' paths are kept
+    import torch
+    rng = np.random.default_rng(1)
+    page, n_kv, dim = 16, 2, 64
+    lens, nodes = [40, 40, 50], [10, 9, 12]
+    raw, table, c = _filled(rng, lens, page, n_kv, dim)
+    paths, acc = [[0, 3, 5, 9], [0, 2, 4, 8], [0, 1, 7, 11]], [3, 3, 3]
+    want = raw.clone()
+    cuda_lib.kv_keep(want, _i32(table), _i32(lens), _i32(_cu(nodes)), _i32(paths), _i32([3, -1, 3]), n_kv, dim, page)
+    lens[1] = far
+    cuda_lib.kv_keep(raw, _i32(table), _i32(lens), _i32(_cu(nodes)), _i32(paths), _i32(acc), n_kv, dim, page)
+    assert torch.equal(raw, want)
