@@ -26,9 +26,10 @@
 // too: they are compared with near numbers where a draft has nearly all of the probability, or nearly the target's.
 // A kernel's code runs once here, so that its length is time too (fetched from the L2): the draw is two tokens to a thread, not
 // 32 to a lane of one warp, which took 4 us more.
-// Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 12.9 us; 48 chains of 2
-// to 8, bf16 37 us; 16 trees of 9 to 40, f32, without probabilities 25 us; one row 7.6 us.  (All in f32: 9.9, 28, 19 and 6.3, but of
-// 9600 drawn tokens 8 were a neighbour of the exact one, now 1.)
+// Measured (in a graph, with the results read back): one chain of 6, 128256 tokens, f32, with probabilities 11.8 us; 48 chains of 2
+// to 8, bf16 36.5 us; 16 trees of 9 to 40, f32, without probabilities 25.4 us; one row 7.4 us.  (All in f32: 9.9, 28, 19 and 6.3, but of
+// 9600 drawn tokens 8 were a neighbour of the exact one, now 1.)  Draft probabilities brought into the L2 before they are needed
+// cost more than they save: one chain 12.8 us, 8 chains 18.4 (17.2 without), 48 chains 39.5.
 // Bound: memory for many rows, the chain of loads and joins for few.
 #include <cmath>
 
@@ -42,9 +43,9 @@ constexpr int kWalk = 512, kWalkWarps = kWalk / 32;    // of the walk
 constexpr int kPer = 32;             // logits per lane
 constexpr int kChunk = 32 * kPer;    // ... and warp
 constexpr int kCluster = 8;          // CTAs of a sequence at most
-// Of logits, from which on the walk reads the rows it reaches (its steps take 3 to 4 us each).  Measured before sums were pairs: 16
-// trees of 9 to 40 of 128256, f32 (328 MB at most) 19 us, by all rows 44; 48 chains of 2 to 8, bf16 (98 MB) 41 against 33; 48 trees
-// of 6, f32 (148) 39 against 41.
+// Of logits, from which on the walk reads the rows it reaches (its steps take 3 to 4 us each).  Measured, of 128256 tokens:
+// 16 trees of 9 to 40, f32 (328 MB at most) 25 us, by all rows 53; 100 of 9 to 40, bf16 (1026 MB) 61, 162; 48 chains of 2 to 8, bf16
+// (98 MB) 60, 36.5; near the bound 48 trees of 6 with probabilities, f32 (148 MB) 54, 50; 200 of 4 of 50000, bf16 (80 MB) 50, 44.
 constexpr int64_t kLazyBytes = int64_t(128) << 20;
 constexpr float kBig = 1.f / 512.f;  // a probability from which on a token's weight is taken as a pair where the next token is drawn
 constexpr float kFar = -1e30f;       // stands for -inf, whose product with 0 would be NaN
@@ -58,7 +59,6 @@ struct VerifyArgs {
   float2 *stats;  // [sequence][row][chunk]: largest logit, the others' sum of 2^((x - largest) c); temperature 0: a 64-bit key
   float2 *sums;   // [sequence][chunk]: of a rejection's pass, as pairs
   int n_seqs, max_rows, n, chunks, groups;  // chunks: of a row, at most
-  bool ahead;                               // draft probabilities that may be needed are brought into the L2
   float c_hi, c_lo;                         // log2(e) / temperature in two parts
 };
 
@@ -622,10 +622,6 @@ __global__ void __launch_bounds__(kWalk, CTAS > 1 ? 2 : 1) verify_walk_kernel(co
         }
         __syncthreads();
       }
-      if (DRAFT && a.ahead && children) {
-        const float *q = a.draft + (int64_t(first) + cur) * a.draft_stride;
-        for (int c = rank * kWalkWarps + warp; c * kChunk < a.n; c += kParts) prefetch(q + c * kChunk, min(kChunk, a.n - c * kChunk) * 4, lane);
-      }
     }
     int went = -1;
     if constexpr (!GREEDY) {
@@ -882,11 +878,10 @@ int launch_verify_drafts(const void *logits, int64_t stride, int type, const int
   a.stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + workspace_tickets(workspace_bytes));
   a.sums = a.stats + rows * a.chunks;
   const int most = (a.chunks + kWarps - 1) / kWarps;  // CTAs of a row with a chunk for each warp
-  // many rows: two chunks for each warp (48 chains 28.6 us, with four 29.3, with one 30.5)
+  // many rows: two chunks for each warp (48 chains 36.5 us, with four 37.2, with one 38.2); few: one (one chain 11.8 us, with two 12.5)
   a.groups = rows * most <= 8 * di.sm_count ? most : (most + 1) / 2;
   if (rows * a.groups > 0x7fffffff || int64_t(n_seqs) * kCluster > 0x7fffffff) return QDQ_ERR_UNSUPPORTED;
-  a.ahead = n_seqs <= 8;  // (where it costs no bandwidth that other sequences need)
-  // 8 CTAs to a sequence while all are resident together, else 4: 48 chains of 128256 29.3 us, with 8 32.6; 1 chain 11.4, with 8 9.9
+  // 8 CTAs to a sequence while all are resident together, else 4: 48 chains of 128256 36.5 us, with 8 39.3; 8 chains 21.5, with 8 18.4
   const bool wide = a.chunks > 2 * kWarps, few = int64_t(n_seqs) * kCluster <= 2 * di.sm_count;
   e = cudaError_t(with_type(type, [&](auto t) {
     using T = decltype(t);
