@@ -907,59 +907,59 @@ __global__ void __launch_bounds__(Cfg<D, PARTS, G, TREE && G == 2>::kThreads, 1)
           }
         }
       } else {
-      uint8_t *my_stages = stages + set * C::kSlots * C::kStage;
-      int n = 0, round = 0;  // slot, and how often it has been used
-      for (int i = set; i < nt; i += C::kSets) {
-        const int b = i & 1;
-        const int64_t ak = s_blk[4 * i + w].k, av = s_blk[4 * i + vtc / 2].k;
-        if constexpr (C::kStaged) {
-          if (!wait(&bars.stage[set][n], round)) break;
-          const uint8_t *st = my_stages + n * C::kStage;
+        uint8_t *my_stages = stages + set * C::kSlots * C::kStage;
+        int n = 0, round = 0;  // slot, and how often it has been used
+        for (int i = set; i < nt; i += C::kSets) {
+          const int b = i & 1;
+          const int64_t ak = s_blk[4 * i + w].k, av = s_blk[4 * i + vtc / 2].k;
+          if constexpr (C::kStaged) {
+            if (!wait(&bars.stage[set][n], round)) break;
+            const uint8_t *st = my_stages + n * C::kStage;
 #pragma unroll
-          for (int j = 0; j < KL; ++j)
-            kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
+            for (int j = 0; j < KL; ++j)
+              kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(st + w * 16 * D + (lane + 32 * j) * 16);
 #pragma unroll
-          for (int g = 0; g < VG; ++g)
-            if (w + 4 * g < D / 32) {
+            for (int g = 0; g < VG; ++g)
+              if (w + 4 * g < D / 32) {
 #pragma unroll
-              for (int t = 0; t < 8; ++t)
-                vq[g][t] = av < 0 ? make_uint2(0, 0)
-                                  : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
+                for (int t = 0; t < 8; ++t)
+                  vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                    : *reinterpret_cast<const uint2 *>(st + C::kStageV + vtc * C::kVStep + t * D + (w + 4 * g) * 32 + vd * 8);
+              }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sread[set][n]);
+            if (++n == C::kSlots) {
+              n = 0;
+              ++round;
             }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.sread[set][n]);
-          if (++n == C::kSlots) {
-            n = 0;
-            ++round;
+          } else {
+#pragma unroll
+            for (int j = 0; j < KL; ++j)
+              kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(a.c.pages + ak + (lane + 32 * j) * 16);
+#pragma unroll
+            for (int g = 0; g < VG; ++g)
+              if (w + 4 * g < D / 32) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                  vq[g][t] = av < 0 ? make_uint2(0, 0)
+                                    : ld_u2(a.c.pages + av + vplane + ((vtc & 1) * 8 + t) * D + (w + 4 * g) * 32 + vd * 8);
+              }
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < KL; ++j)
-            kq[j] = ak < 0 ? make_uint4(0, 0, 0, 0) : ld_u4(a.c.pages + ak + (lane + 32 * j) * 16);
+          if (i >= 2 && !wait(&bars.kfree[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
+          uint8_t *kt = kring + b * C::kK, *vt = vring + b * C::kV;
+          put_keys(kt);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.kfull[b]);
+          // P V of tile i - 2: its values' tile is free
+          if (i >= 2 && !(wait(&bars.pvdone[0][b], (i - 2) >> 1) && (G == 1 || wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)))) break;
 #pragma unroll
           for (int g = 0; g < VG; ++g)
-            if (w + 4 * g < D / 32) {
-#pragma unroll
-              for (int t = 0; t < 8; ++t)
-                vq[g][t] = av < 0 ? make_uint2(0, 0)
-                                  : ld_u2(a.c.pages + av + vplane + ((vtc & 1) * 8 + t) * D + (w + 4 * g) * 32 + vd * 8);
-            }
+            if (w + 4 * g < D / 32) put_values(vt, vq[g], (w + 4 * g) * 32 + vd * 8, vtc);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.vfull[b]);
         }
-        if (i >= 2 && !wait(&bars.kfree[b], (i - 2) >> 1)) break;  // S of tile i - 2 is done: its keys' tile is free
-        uint8_t *kt = kring + b * C::kK, *vt = vring + b * C::kV;
-        put_keys(kt);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.kfull[b]);
-        // P V of tile i - 2: its values' tile is free
-        if (i >= 2 && !(wait(&bars.pvdone[0][b], (i - 2) >> 1) && (G == 1 || wait(&bars.pvdone[G - 1][b], (i - 2) >> 1)))) break;
-#pragma unroll
-        for (int g = 0; g < VG; ++g)
-          if (w + 4 * g < D / 32) put_values(vt, vq[g], (w + 4 * g) * 32 + vd * 8, vtc);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.vfull[b]);
-      }
       }
       if constexpr (C::kShift) {
         // not before the softmax warps have given theirs back: a set without a tile would take its
